@@ -22,6 +22,8 @@ __all__ = [
     "draft_topk_softmax_workspace", "spec_get_status", "spec_uniforms",
     "spec_profile_row_pass", "spec_profile_pending", "spec_rheo_expand", "spec_rheo_expand_workspace",
     "spec_set_fused_limit", "SpecError", "use_checked_library", "spec_check_selftest",
+    "SPEC_ADAMW_BLOCK", "SpecAdamwTable", "spec_process_logits", "spec_process_logits_workspace",
+    "spec_distill_loss", "spec_distill_loss_workspace", "spec_adamw_table", "spec_adamw_step",
 ]
 
 SPEC_OK = 0
@@ -46,6 +48,7 @@ LIB_PATH = Path(__file__).resolve().parent / "libspecverify.so"
 # SPEC_ERR_BOUNDS); a test build.
 CHECKED_LIB_PATH = Path(__file__).resolve().parent / "libspecverify_checked.so"
 HEADER = Path(__file__).resolve().parent.parent / "include" / "specverify.h"
+DRAFT_HEADER = HEADER.parent / "specdraft.h"   # the operators around a draft head (draft.py)
 
 _lib = None
 _lib_path = LIB_PATH
@@ -115,7 +118,7 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"{_lib_path.name} is not built; run "
                                "`python -c 'import __graft_entry__ as g; g.build()'`")
         L = ctypes.CDLL(str(_lib_path))
-        for name, (res, args) in _SIGS.items():
+        for name, (res, args) in {**_SIGS, **_DRAFT_SIGS}.items():
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
@@ -123,9 +126,9 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
-def header_functions() -> list[str]:
-    """Names of the functions include/specverify.h declares."""
-    text = HEADER.read_text()
+def header_functions(header=HEADER) -> list[str]:
+    """Names of the functions a header (include/specverify.h) declares."""
+    text = header.read_text()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return re.findall(r"^\s*(?:const\s+)?\w+\s*\**\s*(\w+)\s*\(", text, flags=re.M)
 
@@ -432,3 +435,10 @@ def spec_profile_pending() -> bool:
     """True while events registered with spec_profile_row_pass have not been
     taken by a call: after a call, whether that call recorded them."""
     return bool(lib().spec_profile_pending())
+
+
+# the operators around a draft head
+from .draft import (  # noqa: E402
+    SIGS as _DRAFT_SIGS, SPEC_ADAMW_BLOCK, SpecAdamwTable, spec_adamw_step, spec_adamw_table,
+    spec_distill_loss, spec_distill_loss_workspace, spec_process_logits,
+    spec_process_logits_workspace)

@@ -1,0 +1,476 @@
+// Penalties, biases and grammar masks on the rows of a verification batch
+// (spec_process_logits of specdraft.h), one launch.
+//
+// Almost every token of a row keeps its bits, so the kernel is a copy that
+// knows where it must not be one. A CTA owns a range of the vocabulary (CH
+// tokens) of one request for a segment of its rows. It first builds, in
+// shared memory, the range's table: for every token the count of its
+// generated occurrences and whether the prompt holds it, from one scan of the
+// request's history (the scan is re-read from L2 by the other ranges), and
+// the request's biases. Each thread owns the same P tokens of the range in
+// every row and keeps one bit per token ("a rule touches it") in a register,
+// so the rows then stream through registers with one compare per 16 bytes,
+// and only flagged tokens look at the table. Draft tokens between two rows
+// are added by the thread that owns them, without a barrier; a tree row's
+// path is added before the row and taken out after it.
+//
+// Bound by HBM: each logit is read once and written once. A 16-byte vector
+// whose tokens are all masked is not read at all: the mask of row i+1 is in
+// registers while row i is processed, and the row's loads go by it.
+#include "draft.cuh"
+
+#include <algorithm>
+
+namespace sv {
+namespace {
+
+constexpr int RU_THREADS = 256;
+constexpr int RU_MAX_SEG = 16;             // rows of one CTA
+constexpr int RU_SEEN = (int)0x80000000u;  // table: the prompt holds the token
+constexpr uint32_t RU_FULL = 0xffffffffu;
+
+struct RulesArgs {
+  const void *in;
+  void *out;
+  const int32_t *cu_rows;
+  int R, V, B, max_rows, nch, seg, inplace;
+  spec_logits_rules r;
+  WsHeader *hdr;
+};
+
+// Shared memory: [CH] counts, [CH] bias indexes (if any), the segment's mask
+// rows and new tokens, and the trees' path tokens inside this range.
+template <int CH>
+struct RulesSmem {
+  static size_t bytes(bool bias, bool tree) {
+    return sizeof(int) * ((size_t)CH * (bias ? 2 : 1) + 2 * RU_MAX_SEG +
+                          (tree ? RU_MAX_SEG * (1 + SPEC_MAX_TREE_DEPTH) : 0));
+  }
+};
+
+template <typename E> struct Elem;
+template <> struct Elem<uint16_t> {
+  static constexpr uint32_t NEG_INF = 0xff80u;
+  __device__ static float to_f32(uint32_t b) { return bf16_bits_to_f32(b); }
+  __device__ static uint32_t from_f32(float v) { return f32_to_bf16_bits(v); }
+};
+template <> struct Elem<uint32_t> {
+  static constexpr uint32_t NEG_INF = 0xff800000u;
+  __device__ static float to_f32(uint32_t b) { return __uint_as_float(b); }
+  __device__ static uint32_t from_f32(float v) { return __float_as_uint(v); }
+};
+
+// A thread's unit of access: 16 bytes, or one element where rows are not
+// 16-byte aligned.
+template <typename E, int VEC> struct Unit { using T = uint4; };
+template <> struct Unit<uint16_t, 1> { using T = uint16_t; };
+template <> struct Unit<uint32_t, 1> { using T = uint32_t; };
+
+// E: the element's bits; VEC elements per access; P tokens per thread.
+template <typename E, int VEC, int P>
+__global__ void __launch_bounds__(RU_THREADS) k_rules(RulesArgs a) {
+  using U = typename Unit<E, VEC>::T;
+  constexpr int CH = RU_THREADS * P;
+  constexpr int NV = P / VEC;                    // accesses of a thread per row
+  constexpr uint32_t VFULL = VEC == 1 ? 1u : (1u << VEC) - 1;
+  constexpr int NRAW = VEC == 1 ? 1 : NV;        // mask words of a thread per row
+  extern __shared__ __align__(16) int sm[];
+  const bool has_bias = a.r.bias_ids != nullptr;
+  const bool tree = a.r.parent != nullptr;
+  int *cnt = sm;
+  int *bidx = cnt + CH;
+  int *s_mrow = bidx + (has_bias ? CH : 0);
+  int *s_tok = s_mrow + RU_MAX_SEG;
+  int *s_pn = s_tok + RU_MAX_SEG;                // trees: path tokens in range, per row
+  int *s_path = s_pn + RU_MAX_SEG;
+
+  const int t = threadIdx.x, lane = t & 31;
+  const int c = blockIdx.x % a.nch;
+  const int b = (blockIdx.x / a.nch) % a.B;
+  const int i0 = (blockIdx.x / a.nch) / a.B * a.seg;
+  const int c0 = c * CH;
+  const int lo = GLD(a.cu_rows + b), hi = GLD(a.cu_rows + b + 1);
+  if (lo < 0 || hi < lo || hi > a.R || hi - lo > a.max_rows || (b == 0 && lo != 0) ||
+      (b == a.B - 1 && hi != a.R)) {
+    if (t == 0) set_status(a.hdr, SPEC_ERR_INVALID_ARG, b);
+    return;
+  }
+  const int n = min(a.seg, hi - lo - i0);        // rows of this CTA
+  if (n <= 0) return;
+
+  // the request's parameters
+  const float rho = a.r.repetition ? GLD(a.r.repetition + b) : 1.f;
+  const float fr = a.r.frequency ? GLD(a.r.frequency + b) : 0.f;
+  const float pr = a.r.presence ? GLD(a.r.presence + b) : 0.f;
+  int h0 = 0, h1 = 0, hp = 0, b0 = 0, b1 = 0, k0 = 0, K = 0;
+  bool bad = !(rho > 0.f) || !isfinite(rho) || !isfinite(fr) || !isfinite(pr);
+  if (a.r.history != nullptr) {
+    h0 = GLD(a.r.cu_history + b), h1 = GLD(a.r.cu_history + b + 1);
+    if (h0 < 0 || h1 < h0) bad = true, h1 = h0 = 0;
+    hp = a.r.prompt_len ? GLD(a.r.prompt_len + b) : 0;
+  }
+  if (has_bias) {
+    b0 = GLD(a.r.cu_bias + b), b1 = GLD(a.r.cu_bias + b + 1);
+    if (b0 < 0 || b1 < b0) bad = true, b1 = b0 = 0;
+  }
+  if (a.r.tokens != nullptr && !tree) {
+    k0 = GLD(a.r.cu_tokens + b), K = GLD(a.r.cu_tokens + b + 1) - k0;
+    if (k0 < 0 || K < 0) bad = true, K = 0;
+  }
+
+  for (int i = t; i < CH / 4; i += RU_THREADS) {
+    reinterpret_cast<int4 *>(cnt)[i] = make_int4(0, 0, 0, 0);
+    if (has_bias) reinterpret_cast<int4 *>(bidx)[i] = make_int4(0, 0, 0, 0);
+  }
+  if (t < n) {
+    int mrow = -1;
+    if (a.r.mask != nullptr) {
+      mrow = a.r.mask_rows ? GLD(a.r.mask_rows + lo + i0 + t) : lo + i0 + t;
+      if (mrow < -1 || mrow >= a.r.n_mask) bad = true, mrow = -1;
+    }
+    s_mrow[t] = mrow;
+    // the draft that row t sees and row t-1 does not (row 0's are in the table)
+    const int j = i0 + t - 1;
+    int tok = -1;
+    if (!tree && t > 0 && j < K) {
+      tok = GLD(a.r.tokens + k0 + j);
+      if (tok < 0 || tok >= a.V) bad = true, tok = -1;
+    }
+    s_tok[t] = tok;
+    if (tree) {   // this row's path, the tokens of this range only
+      int m = 0, v = i0 + t, steps = 0;
+      while (v > 0) {
+        const int tk = GLD(a.r.tokens + lo + v);
+        if (tk < 0 || tk >= a.V) {
+          bad = true;
+        } else if (tk >= c0 && tk < c0 + CH) {
+          s_path[t * SPEC_MAX_TREE_DEPTH + m++] = tk - c0;
+        }
+        const int up = GLD(a.r.parent + lo + v);
+        if (up < 0 || up >= v || ++steps >= SPEC_MAX_TREE_DEPTH) {
+          if (up != 0) bad = true;
+          break;
+        }
+        v = up;
+      }
+      s_pn[t] = m;
+    }
+  }
+  __syncthreads();
+
+  // tokens of this thread that exist (rows of 16-byte vectors hold whole ones)
+  uint32_t valid = 0;
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+    if (c0 + (v * RU_THREADS + t) * VEC < a.V) valid |= VFULL << (v * VEC);
+  if (P < 32) valid &= (1u << (P & 31)) - 1;
+
+  const int W = (a.V + 31) >> 5;
+  uint32_t raw[NRAW];
+  auto load_mask = [&](int i) {
+    const int mrow = s_mrow[i];
+#pragma unroll
+    for (int q = 0; q < NRAW; ++q) raw[q] = RU_FULL;
+    if (mrow < 0) return;
+    const uint32_t *words = a.r.mask + (long long)mrow * W;
+    if (VEC == 1) {   // lane v holds the warp's 32 bits of access v
+      const int w = (c0 + lane * RU_THREADS + (t & ~31)) >> 5;
+      if (lane < NV && w < W) raw[0] = GLD(words + w);
+    } else {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int e = c0 + (v * RU_THREADS + t) * VEC;
+        if (e < a.V) raw[v % NRAW] = GLD(reinterpret_cast<const uint8_t *>(words) + (e >> 3));
+      }
+    }
+  };
+  auto allowed_bits = [&]() -> uint32_t {
+    uint32_t A = 0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if (VEC == 1) {
+        A |= ((__shfl_sync(RU_FULL, raw[0], v) >> lane) & 1u) << v;
+      } else if (VEC == 8) {
+        A |= (raw[v % NRAW] & 0xffu) << (v * VEC % 32);
+      } else {
+        A |= ((raw[v % NRAW] >> ((t & 1) * 4)) & 0xfu) << (v * VEC % 32);
+      }
+    }
+    return A & valid;
+  };
+
+  U cur[NV], nxt[NV];
+  auto row_ptr = [&](const void *base, int i) {
+    return reinterpret_cast<const U *>(static_cast<const E *>(base) +
+                                       (long long)(lo + i0 + i) * a.V + c0);
+  };
+  // in place, a vector that neither the mask nor a rule touches stays
+  auto untouched = [&](uint32_t av, uint32_t fv, uint32_t vv) { return av == vv && fv == 0; };
+  auto load_row = [&](U *dst, int i, uint32_t A, uint32_t F) {
+    const U *p = row_ptr(a.in, i);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const uint32_t av = (A >> (v * VEC)) & VFULL, fv = (F >> (v * VEC)) & VFULL,
+                     vv = (valid >> (v * VEC)) & VFULL;
+      if (av != 0 && !(a.inplace && untouched(av, fv, vv))) dst[v] = GLD(p + v * RU_THREADS + t);
+    }
+  };
+  auto own_bit = [&](int e) -> uint32_t {   // this thread's bit for token c0 + e, or 0
+    if (e < 0 || e >= CH || (e / VEC) % RU_THREADS != t) return 0;
+    return 1u << ((e / VEC / RU_THREADS) * VEC + e % VEC);
+  };
+  auto new_bits = [&](int i) -> uint32_t {
+    if (!tree) return s_tok[i] < 0 ? 0 : own_bit(s_tok[i] - c0);
+    uint32_t f = 0;
+    for (int m = 0; m < s_pn[i]; ++m) f |= own_bit(s_path[i * SPEC_MAX_TREE_DEPTH + m]);
+    return f;
+  };
+
+  load_mask(0);
+  uint32_t A = allowed_bits();
+  if (!a.inplace) load_row(cur, 0, A, 0);
+  if (n > 1) load_mask(1);
+
+  // ---- the range's table: one scan of the history, the drafts before this
+  // segment, the biases
+  for (int j = h0 + t; j < h1; j += RU_THREADS) {
+    const int tok = GLD(a.r.history + j);
+    if (tok < 0 || tok >= a.V) bad = true;
+    const int e = tok - c0;
+    if (e >= 0 && e < CH) {
+      if (j - h0 < hp) atomicOr(cnt + e, RU_SEEN);
+      else atomicAdd(cnt + e, 1);
+    }
+  }
+  if (!tree) {
+    for (int j = t; j < min(i0, K); j += RU_THREADS) {
+      const int tok = GLD(a.r.tokens + k0 + j);
+      if (tok < 0 || tok >= a.V) bad = true;
+      const int e = tok - c0;
+      if (e >= 0 && e < CH) atomicAdd(cnt + e, 1);
+    }
+  }
+  for (int j = b0 + t; j < b1; j += RU_THREADS) {
+    const int id = GLD(a.r.bias_ids + j);
+    const float bv = GLD(a.r.bias_values + j);
+    if (id < 0 || id >= a.V || isnan(bv) || bv == INFINITY) bad = true;
+    const int e = id - c0;
+    if (e >= 0 && e < CH) atomicMax(bidx + e, j - b0 + 1);   // the last entry holds
+  }
+  if (bad) set_status(a.hdr, SPEC_ERR_INVALID_ARG, b);
+  __syncthreads();
+
+  uint32_t F = 0;   // tokens of this thread that a rule touches
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const int e = (v * RU_THREADS + t) * VEC + j;
+      if (cnt[e] != 0 || (has_bias && bidx[e] != 0)) F |= 1u << (v * VEC + j);
+    }
+  }
+  if (a.inplace) load_row(cur, 0, A, F | new_bits(0));
+
+  for (int i = 0; i < n; ++i) {
+    uint32_t A1 = 0;
+    if (i + 1 < n) {
+      A1 = allowed_bits();
+      load_row(nxt, i + 1, A1, a.inplace ? (F | new_bits(i) | new_bits(i + 1)) : 0);
+      if (i + 2 < n) load_mask(i + 2);
+    }
+    // the tokens that come in with this row
+    uint32_t Fi = F;
+    if (!tree) {
+      if (s_tok[i] >= 0) {
+        const uint32_t f = own_bit(s_tok[i] - c0);
+        if (f) ++cnt[s_tok[i] - c0];
+        F |= f;
+        Fi = F;
+      }
+    } else {
+      for (int m = 0; m < s_pn[i]; ++m) {
+        const int e = s_path[i * SPEC_MAX_TREE_DEPTH + m];
+        const uint32_t f = own_bit(e);
+        if (f) ++cnt[e];
+        Fi |= f;
+      }
+    }
+    U *o = const_cast<U *>(row_ptr(a.out, i));
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const uint32_t av = (A >> (v * VEC)) & VFULL, fv = (Fi >> (v * VEC)) & VFULL,
+                     vv = (valid >> (v * VEC)) & VFULL;
+      if (vv == 0 || (a.inplace && untouched(av, fv, vv))) continue;
+      U x = cur[v];
+      if (av != VFULL || fv != 0) {
+        E w[VEC];
+        memcpy(w, &x, sizeof(x));
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          if (!((av >> j) & 1)) {
+            w[j] = (E)Elem<E>::NEG_INF;
+          } else if ((fv >> j) & 1) {
+            const int e = (v * RU_THREADS + t) * VEC + j;
+            const int ent = cnt[e];
+            float z = Elem<E>::to_f32(w[j]);
+            if (has_bias) {
+              const int k = bidx[e];
+              if (k != 0) z += GLD(a.r.bias_values + b0 + k - 1);
+            }
+            if (ent != 0) {
+              z = z > 0.f ? z / rho : z * rho;
+              const int m = ent & ~RU_SEEN;
+              if (m != 0) z = z - fr * (float)m - pr;
+            }
+            w[j] = (E)Elem<E>::from_f32(z);
+          }
+        }
+        memcpy(&x, w, sizeof(x));
+      }
+      GST(o + v * RU_THREADS + t, x);
+    }
+    if (tree) {
+      for (int m = 0; m < s_pn[i]; ++m) {
+        const int e = s_path[i * SPEC_MAX_TREE_DEPTH + m];
+        if (own_bit(e)) --cnt[e];
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) cur[v] = nxt[v];
+    A = A1;
+  }
+}
+
+template <typename E, int VEC, int P>
+int launch_rules(const RulesArgs &a, long long ctas, bool bias, bool tree, cudaStream_t st) {
+  const size_t smem = RulesSmem<RU_THREADS * P>::bytes(bias, tree);
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(k_rules<E, VEC, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)smem) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  k_rules<E, VEC, P><<<(unsigned)ctas, RU_THREADS, smem, st>>>(a);
+  return launched();
+}
+
+}  // namespace
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" size_t spec_process_logits_workspace(void) { return sizeof(WsHeader); }
+
+extern "C" int spec_process_logits(const void *logits, int dt, int R, int V,
+                                   const int32_t *cu_rows, int B, int max_rows,
+                                   const spec_logits_rules *rules, void *out, void *workspace,
+                                   size_t ws_bytes, spec_stream_t stream) {
+  if (R < 0 || B < 0 || V <= 0 || V > SPEC_MAX_V) return SPEC_ERR_INVALID_ARG;
+  if (dt != SPEC_F32 && dt != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
+  if (max_rows < 1 || max_rows > SPEC_MAX_TREE_NODES) return SPEC_ERR_INVALID_ARG;
+  if (cu_rows == nullptr || !aligned(cu_rows, 4)) return SPEC_ERR_INVALID_ARG;
+  if (R > 0 && (logits == nullptr || out == nullptr || B == 0)) return SPEC_ERR_INVALID_ARG;
+  if (!aligned(logits, 16) || !aligned(out, 16)) return SPEC_ERR_INVALID_ARG;
+  const long long es = dt == SPEC_BF16 ? 2 : 4;
+  const uintptr_t in0 = (uintptr_t)logits, out0 = (uintptr_t)out;
+  const uintptr_t bytes = (uintptr_t)((long long)R * V * es);
+  if (in0 != out0 && in0 < out0 + bytes && out0 < in0 + bytes) return SPEC_ERR_INVALID_ARG;
+  RulesArgs a{};
+  if (rules != nullptr) a.r = *rules;
+  const spec_logits_rules &r = a.r;
+  if ((r.history == nullptr) != (r.cu_history == nullptr)) return SPEC_ERR_INVALID_ARG;
+  if (r.prompt_len != nullptr && r.history == nullptr) return SPEC_ERR_INVALID_ARG;
+  if (r.parent != nullptr ? (r.tokens == nullptr || r.cu_tokens != nullptr)
+                          : (r.tokens == nullptr) != (r.cu_tokens == nullptr))
+    return SPEC_ERR_INVALID_ARG;
+  if ((r.bias_ids == nullptr) != (r.bias_values == nullptr) ||
+      (r.bias_ids == nullptr) != (r.cu_bias == nullptr))
+    return SPEC_ERR_INVALID_ARG;
+  if (r.mask == nullptr ? r.mask_rows != nullptr
+                        : (r.n_mask < 0 || (r.mask_rows == nullptr && r.n_mask < R)))
+    return SPEC_ERR_INVALID_ARG;
+  const void *words[] = {r.history, r.cu_history, r.prompt_len, r.tokens,   r.cu_tokens,
+                         r.parent,  r.repetition, r.frequency,  r.presence, r.bias_ids,
+                         r.bias_values, r.cu_bias, r.mask,      r.mask_rows};
+  for (const void *p : words)
+    if (!aligned(p, 4)) return SPEC_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned(workspace, 256) || ws_bytes < sizeof(WsHeader))
+    return SPEC_ERR_WORKSPACE;
+
+  a.in = logits;
+  a.out = out;
+  a.cu_rows = cu_rows;
+  a.R = R;
+  a.V = V;
+  a.B = B;
+  a.max_rows = max_rows;
+  a.inplace = logits == out;
+  a.hdr = static_cast<WsHeader *>(workspace);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+
+#ifdef SPEC_CHECKED
+  check_begin(a.hdr);
+  check_add(workspace, sizeof(WsHeader));
+  check_add(logits, bytes);
+  if (!a.inplace) check_add(out, bytes);
+  check_add(cu_rows, (B + 1) * 4ull);
+  int total = 0;
+  if (r.history != nullptr) {
+    if (check_read_int(r.cu_history + B, st, &total) != SPEC_OK) return SPEC_ERR_CUDA;
+    check_add(r.history, (unsigned long long)std::max(total, 0) * 4);
+    check_add(r.cu_history, (B + 1) * 4ull);
+    check_add(r.prompt_len, B * 4ull);
+  }
+  if (r.tokens != nullptr) {
+    total = R;
+    if (r.cu_tokens != nullptr) {
+      if (check_read_int(r.cu_tokens + B, st, &total) != SPEC_OK) return SPEC_ERR_CUDA;
+      check_add(r.cu_tokens, (B + 1) * 4ull);
+    }
+    check_add(r.tokens, (unsigned long long)std::max(total, 0) * 4);
+    check_add(r.parent, R * 4ull);
+  }
+  check_add(r.repetition, B * 4ull);
+  check_add(r.frequency, B * 4ull);
+  check_add(r.presence, B * 4ull);
+  if (r.bias_ids != nullptr) {
+    if (check_read_int(r.cu_bias + B, st, &total) != SPEC_OK) return SPEC_ERR_CUDA;
+    check_add(r.bias_ids, (unsigned long long)std::max(total, 0) * 4);
+    check_add(r.bias_values, (unsigned long long)std::max(total, 0) * 4);
+    check_add(r.cu_bias, (B + 1) * 4ull);
+  }
+  check_add(r.mask, (unsigned long long)r.n_mask * ((V + 31) / 32) * 4);
+  check_add(r.mask_rows, R * 4ull);
+#endif
+  if (reset_header(workspace, st) != SPEC_OK) return SPEC_ERR_CUDA;
+  if (R == 0) return SPEC_OK;
+  if (check_upload(st) != SPEC_OK) return SPEC_ERR_CUDA;
+
+  const bool bias = r.bias_ids != nullptr, tree = r.parent != nullptr;
+  const int vec = (V * es) % 16 == 0 ? (int)(16 / es) : 1;
+  // Long calls: wide ranges and segments of many rows, so that a table serves
+  // many rows. Calls that would not fill the SMs: shorter segments, then
+  // narrow ranges.
+  int P = 32;
+  int seg = std::min(max_rows, RU_MAX_SEG);
+  auto ctas = [&](int p, int s) {
+    return (long long)((V + RU_THREADS * p - 1) / (RU_THREADS * p)) * B * ((max_rows + s - 1) / s);
+  };
+  const long long want = 4ll * num_sms();
+  while (seg > 1 && ctas(P, seg) < want) seg = (seg + 1) / 2;
+  if (ctas(P, seg) < want) P = 8;
+  a.seg = seg;
+  a.nch = (V + RU_THREADS * P - 1) / (RU_THREADS * P);
+  const long long n = ctas(P, seg);
+  if (n > 0x7fffffffll) return SPEC_ERR_UNSUPPORTED;
+  if (dt == SPEC_BF16) {
+    if (vec == 8)
+      return P == 32 ? launch_rules<uint16_t, 8, 32>(a, n, bias, tree, st)
+                     : launch_rules<uint16_t, 8, 8>(a, n, bias, tree, st);
+    return P == 32 ? launch_rules<uint16_t, 1, 32>(a, n, bias, tree, st)
+                   : launch_rules<uint16_t, 1, 8>(a, n, bias, tree, st);
+  }
+  if (vec == 4)
+    return P == 32 ? launch_rules<uint32_t, 4, 32>(a, n, bias, tree, st)
+                   : launch_rules<uint32_t, 4, 8>(a, n, bias, tree, st);
+  return P == 32 ? launch_rules<uint32_t, 1, 32>(a, n, bias, tree, st)
+                 : launch_rules<uint32_t, 1, 8>(a, n, bias, tree, st);
+}
