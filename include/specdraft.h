@@ -255,6 +255,54 @@ int spec_adamw_step(const void *table, int64_t n_items, int state_bits,
                     const spec_adamw_hyper *hyper, void *workspace,
                     size_t ws_bytes, spec_stream_t stream);
 
+/* Activations of a head's product. */
+typedef enum {
+  SPEC_ACT_NONE = 0,
+  SPEC_ACT_SILU = 1, /* z / (1 + e^-z)                                       */
+  SPEC_ACT_GELU = 2  /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2      */
+} spec_act;
+
+/* Bytes of workspace the head's calls need (0 on invalid sizes). */
+size_t spec_head_forward_workspace(int M, int N, int K);
+size_t spec_head_backward_workspace(int M, int N, int K);
+
+/*
+ * y = act(x W^T + bias) + residual for M rows: a draft head's residual block,
+ * or its projection to the vocabulary (logits for the verifier). All
+ * matrices are bf16, contiguous and 16-byte aligned (any K and N; rows of x
+ * and W that are no multiple of 8 elements are first copied to padded ones
+ * in the workspace). Products and sums are held in 32 bits, y is rounded
+ * once.
+ *
+ *   x         [M, K]; weight [N, K]; bias [N] or NULL; residual [M, N] or
+ *             NULL; 0 <= M <= 2^24, 1 <= N, K <= 2^24.
+ *   y         [M, N]. May be `residual` itself, not another input.
+ *   pre       [M, N] or NULL: x W^T + bias, rounded to bf16, for the
+ *             backward pass.
+ */
+int spec_head_forward(const void *x, const void *weight, const void *bias,
+                      const void *residual, int M, int N, int K, int act,
+                      void *y, void *pre, void *workspace, size_t ws_bytes,
+                      spec_stream_t stream);
+
+/*
+ * The gradients of spec_head_forward given dy = dL/dy:
+ *
+ *   dz = dy act'(pre)     dx = dz W     dw = dz^T x     db = sum over rows of dz
+ *
+ * (the residual's gradient is dy itself). dz is rounded to bf16 as the two
+ * products' operand, db sums it unrounded. Sums in 32 bits, dx and dw
+ * rounded once.
+ *
+ *   dy, pre   [M, N]; pre may be NULL with SPEC_ACT_NONE.
+ *   dx        [M, K] or NULL; dw [N, K] or NULL; db [N] f32 or NULL. None may
+ *             overlap an input. With M = 0, dw and db become zero.
+ */
+int spec_head_backward(const void *dy, const void *x, const void *weight,
+                       const void *pre, int M, int N, int K, int act,
+                       void *dx, void *dw, float *db, void *workspace,
+                       size_t ws_bytes, spec_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

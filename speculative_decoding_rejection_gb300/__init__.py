@@ -24,6 +24,8 @@ __all__ = [
     "spec_set_fused_limit", "SpecError", "use_checked_library", "spec_check_selftest",
     "SPEC_ADAMW_BLOCK", "SpecAdamwTable", "spec_process_logits", "spec_process_logits_workspace",
     "spec_distill_loss", "spec_distill_loss_workspace", "spec_adamw_table", "spec_adamw_step",
+    "SPEC_ACT_NONE", "SPEC_ACT_SILU", "SPEC_ACT_GELU", "spec_head_forward",
+    "spec_head_forward_workspace", "spec_head_backward", "spec_head_backward_workspace",
 ]
 
 SPEC_OK = 0
@@ -439,6 +441,8 @@ def spec_profile_pending() -> bool:
 
 # the operators around a draft head
 from .draft import (  # noqa: E402
-    SIGS as _DRAFT_SIGS, SPEC_ADAMW_BLOCK, SpecAdamwTable, spec_adamw_step, spec_adamw_table,
-    spec_distill_loss, spec_distill_loss_workspace, spec_process_logits,
+    SIGS as _DRAFT_SIGS, SPEC_ACT_GELU, SPEC_ACT_NONE, SPEC_ACT_SILU, SPEC_ADAMW_BLOCK,
+    SpecAdamwTable, spec_adamw_step, spec_adamw_table, spec_distill_loss,
+    spec_distill_loss_workspace, spec_head_backward, spec_head_backward_workspace,
+    spec_head_forward, spec_head_forward_workspace, spec_process_logits,
     spec_process_logits_workspace)

@@ -21,7 +21,8 @@ BUILD = ROOT / "_build"
 LIB = PKG / "libspecverify.so"
 CHECKED_LIB = PKG / "libspecverify_checked.so"
 SOURCES = ["rowpass.cu", "linear.cu", "stream.cu", "resident.cu", "small.cu", "topk.cu", "tree.cu",
-           "rheo.cu", "api.cu", "noalloc.cu", "rules.cu", "distill.cu", "adamw.cu"]
+           "rheo.cu", "api.cu", "noalloc.cu", "rules.cu", "distill.cu", "adamw.cu",
+           "head.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          f"-I{INCLUDE}", f"-I{CSRC}"]

@@ -10,6 +10,7 @@ import ctypes
 import speculative_decoding_rejection_gb300 as _sv
 
 SPEC_ADAMW_BLOCK = 256
+SPEC_ACT_NONE, SPEC_ACT_SILU, SPEC_ACT_GELU = 0, 1, 2
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
 
@@ -46,6 +47,11 @@ SIGS = {
     "spec_adamw_table_bytes": (_sz, [ctypes.POINTER(SpecAdamwTensor), _i32, _i32]),
     "spec_adamw_table": (_i32, [ctypes.POINTER(SpecAdamwTensor), _i32, _i32, _vp, _sz,
                                 ctypes.POINTER(_i64)]),
+    "spec_head_forward_workspace": (_sz, [_i32, _i32, _i32]),
+    "spec_head_forward": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "spec_head_backward_workspace": (_sz, [_i32, _i32, _i32]),
+    "spec_head_backward": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _sz,
+                                  _vp]),
     "spec_adamw_step": (_i32, [_vp, _i64, _i32, ctypes.POINTER(SpecAdamwHyper), _vp, _sz, _vp]),
 }
 
@@ -192,6 +198,101 @@ def spec_distill_loss(target, draft, cu_draft, temperature=None, weight=None, *,
             _sv._stream(s))
     _sv._check(code, "spec_distill_loss")
     return loss, grad, ws
+
+
+# --------------------------------------------------------- a head's products
+def spec_head_forward_workspace(M: int, N: int, K: int) -> int:
+    return int(_sv.lib().spec_head_forward_workspace(M, N, K))
+
+
+def spec_head_backward_workspace(M: int, N: int, K: int) -> int:
+    return int(_sv.lib().spec_head_backward_workspace(M, N, K))
+
+
+def _head_sizes(x, weight):
+    torch = _sv._torch()
+    M, K = x.shape
+    N = weight.shape[0]
+    if weight.shape[1] != K:
+        raise ValueError(f"weight must be [N, {K}]")
+    _want("x", x, torch.bfloat16)
+    _want("weight", weight, torch.bfloat16, None, x.device)
+    return M, N, K
+
+
+def _head_workspace(size, where, device, workspace):
+    if workspace is not None:
+        return workspace
+    if size == 0:
+        raise _sv.SpecError(_sv.SPEC_ERR_INVALID_ARG, where)
+    return _sv._workspace(size, device)
+
+
+def spec_head_forward(x, weight, bias=None, residual=None, *, act: int = SPEC_ACT_NONE,
+                      want_pre=False, workspace=None, out=None, stream=None):
+    """y = act(x weight^T + bias) + residual in bf16, x [M, K], weight [N, K].
+    With `want_pre` the pre-activation is returned too, for
+    spec_head_backward. See include/specdraft.h.
+
+    Returns (y [M, N], pre [M, N] or None, workspace).
+    """
+    torch = _sv._torch()
+    M, N, K = _head_sizes(x, weight)
+    dev, bf = x.device, torch.bfloat16
+    _want("bias", bias, bf, N, dev)
+    _want("residual", residual, bf, M * N, dev)
+    y, pre = (None, None) if out is None else out
+    _want("y", y, bf, M * N, dev)
+    _want("pre", pre, bf, M * N, dev)
+    ptr = _sv._ptr
+    s, ctx = _begin(dev, stream, (x, weight, bias, residual, y, pre, workspace))
+    with ctx:
+        ws = _head_workspace(0 if workspace is not None else spec_head_forward_workspace(M, N, K),
+                             "spec_head_forward_workspace", dev, workspace)
+        if out is None:
+            y = torch.empty(M, N, dtype=bf, device=dev)
+            pre = torch.empty_like(y) if want_pre else None
+        code = _sv.lib().spec_head_forward(
+            ptr(x), ptr(weight), ptr(bias), ptr(residual), M, N, K, act, ptr(y), ptr(pre), ptr(ws),
+            _bytes(ws), _sv._stream(s))
+    _sv._check(code, "spec_head_forward")
+    return y, pre, ws
+
+
+def spec_head_backward(dy, x, weight, pre=None, *, act: int = SPEC_ACT_NONE, want_dx=True,
+                       want_dw=True, want_db=False, workspace=None, out=None, stream=None):
+    """The gradients of spec_head_forward given dy [M, N]; `pre` is the
+    pre-activation it returned (not needed without an activation). See
+    include/specdraft.h.
+
+    Returns (dx [M, K], dw [N, K], db [N] f32, workspace), None for what is
+    not wanted.
+    """
+    torch = _sv._torch()
+    M, N, K = _head_sizes(x, weight)
+    dev, bf = x.device, torch.bfloat16
+    if tuple(dy.shape) != (M, N):
+        raise ValueError(f"dy must be [{M}, {N}]")
+    _want("dy", dy, bf, M * N, dev)
+    _want("pre", pre, bf, M * N, dev)
+    dx, dw, db = (None, None, None) if out is None else out
+    _want("dx", dx, bf, M * K, dev)
+    _want("dw", dw, bf, N * K, dev)
+    _want("db", db, torch.float32, N, dev)
+    ptr = _sv._ptr
+    s, ctx = _begin(dev, stream, (dy, x, weight, pre, dx, dw, db, workspace))
+    with ctx:
+        ws = _head_workspace(0 if workspace is not None else spec_head_backward_workspace(M, N, K),
+                             "spec_head_backward_workspace", dev, workspace)
+        if out is None:
+            dx = torch.empty(M, K, dtype=bf, device=dev) if want_dx else None
+            dw = torch.empty(N, K, dtype=bf, device=dev) if want_dw else None
+            db = torch.empty(N, dtype=torch.float32, device=dev) if want_db else None
+        code = _sv.lib().spec_head_backward(
+            ptr(dy), ptr(x), ptr(weight), ptr(pre), M, N, K, act, ptr(dx), ptr(dw), ptr(db), ptr(ws),
+            _bytes(ws), _sv._stream(s))
+    _sv._check(code, "spec_head_backward")
+    return dx, dw, db, ws
 
 
 # ------------------------------------------------------------------- AdamW

@@ -186,3 +186,35 @@ def test_reference_activation_slopes(name):
     h = 1e-6
     diff = (O.act(z + h, name) - O.act(z - h, name)) / (2 * h)
     assert np.max(np.abs(diff - O.act_slope(z, name))) < 1e-8
+
+
+# -------------------------------------------------------------------- head
+FORWARD_OK = dict(x=FAKE, w=FAKE, bias=None, residual=None, M=4, N=64, K=64, act=0, y=FAKE, pre=None,
+                  ws=FAKE, ws_bytes=1 << 30, stream=None)
+BACKWARD_OK = dict(dy=FAKE, x=FAKE, w=FAKE, pre=FAKE, M=4, N=64, K=64, act=1, dx=FAKE, dw=FAKE, db=FAKE,
+                   ws=FAKE, ws_bytes=1 << 30, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(M=-1), INV), (dict(N=0), INV), (dict(K=0), INV), (dict(K=(1 << 24) + 1), INV),
+    (dict(act=3), INV), (dict(act=-1), INV), (dict(x=None), INV), (dict(w=None), INV), (dict(y=None), INV),
+    (dict(x=FAKE + 8), INV), (dict(w=FAKE + 2), INV), (dict(y=FAKE + 4), INV), (dict(bias=FAKE + 1), INV),
+    (dict(ws=None), WS), (dict(ws=FAKE + 64), WS), (dict(ws_bytes=128), WS)])
+def test_head_forward_refuses_bad_arguments(L, kw, code):
+    assert L.spec_head_forward(*{**FORWARD_OK, **kw}.values()) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(M=-1), INV), (dict(N=0), INV), (dict(act=9), INV), (dict(dy=None), INV), (dict(pre=None), INV),
+    (dict(w=None), INV), (dict(x=None), INV), (dict(dx=FAKE + 8), INV), (dict(dw=FAKE + 2), INV),
+    (dict(db=FAKE + 2), INV), (dict(ws=None), WS), (dict(ws_bytes=256), WS)])
+def test_head_backward_refuses_bad_arguments(L, kw, code):
+    assert L.spec_head_backward(*{**BACKWARD_OK, **kw}.values()) == code
+
+
+def test_head_workspaces():
+    for f in (sv.spec_head_forward_workspace, sv.spec_head_backward_workspace):
+        assert f(1, 32000, 4096) >= 256 and f(0, 10, 10) >= 256
+        assert f(-1, 10, 10) == 0 and f(1, 0, 10) == 0 and f(1, 10, 0) == 0
+    # padded copies of odd operands are part of it
+    assert sv.spec_head_forward_workspace(4, 64, 63) >= 2 * 64 * (64 + 4)
