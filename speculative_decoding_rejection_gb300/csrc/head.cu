@@ -17,8 +17,10 @@
 // A persistent CTA per SM: one warp feeds a ring of TMA stages (64 of r each),
 // one issues tcgen05.mma, four run the epilogue from the other of two
 // accumulators. Where the tiles alone would not fill the SMs, r is split: the
-// parts leave f32 partials, and whichever part of a tile comes last adds them
-// up in the order of r, so the result does not depend on who came last.
+// parts leave f32 partials, and a second launch over all SMs adds them up in
+// the order of r and runs the epilogue (joining inside the product, by the last
+// part of a tile, left one SM per tile reading the parts: 197 rows of 2880 x
+// 2880 took 96 us that way, 31 us this way).
 #include <cuda.h>   // tensor map types; the encoder is resolved at run time
 
 #include "draft.cuh"
@@ -33,7 +35,9 @@ constexpr int HD_I = 128;         // rows of a tile (TMEM lanes)
 constexpr int HD_R = 64;          // reduction elements of a stage (128 bytes)
 constexpr int HD_MAX_J = 256;     // columns of a tile
 constexpr int HD_MAX_STAGES = 12;
-constexpr int HD_SMEM = 222 * 1024;   // ring
+constexpr int HD_STAGE_LD = 36;       // floats between columns of a warp's staging (no bank conflicts)
+constexpr int HD_STAGING = 4 * 32 * HD_STAGE_LD * 4;   // four warps, 32 columns of 32 lanes
+constexpr int HD_SMEM = 226 * 1024 - HD_STAGING - 1024;   // ring
 constexpr int HD_PLAN_SMS = 152;      // SMs the split is planned for
 constexpr int HD_MAX_SPLIT = 32;
 constexpr int HD_A_BYTES = HD_I * HD_R * 2;
@@ -46,7 +50,8 @@ struct HeadArgs {
   __nv_bfloat16 *out, *pre;
   int act;
   float *part;         // [units][nt][128] partials of a split
-  unsigned *count;     // [tiles] parts that have arrived
+  int reset;           // this launch starts the call: the status is set to OK
+  int vec;             // rows of the result and of its residual suit 16-byte accesses
   WsHeader *hdr;
 };
 
@@ -55,7 +60,6 @@ struct HeadSmem {
   uint64_t acc_full[2], acc_empty[2];
   uint32_t tmem;
   int abort;
-  int last;
 };
 
 __device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
@@ -89,19 +93,22 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
       : "memory");
 }
-// 16 accumulator columns of this thread's lane.
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, float *v) {
-  uint32_t r[16];
+// 32 accumulator columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float *v) {
+  uint32_t r[32];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-      "%13, %14, %15}, [%16];"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+      "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
+      "[%32];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-        "=r"(r[15])
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 __device__ __forceinline__ float act_value(float z, int act) {
@@ -123,21 +130,52 @@ __device__ __forceinline__ float act_slope(float z, int act) {
   return 1.f;
 }
 
-// 16 columns of lane i: bias, activation, residual, one rounding to bf16.
-__device__ __forceinline__ void finish16(const HeadArgs &a, float *v, int i, int j) {
-  if (i >= a.I) return;
-  const float bias = a.bias ? __bfloat162float(a.bias[i]) : 0.f;
+__device__ __forceinline__ float bf16_at(const __nv_bfloat16 *p, long long i) {
+  return bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(p)[i]);
+}
+__device__ __forceinline__ void bf16_to(__nv_bfloat16 *p, long long i, float v) {
+  reinterpret_cast<uint16_t *>(p)[i] = (uint16_t)f32_to_bf16_bits(v);
+}
+__device__ __forceinline__ void unpack8(const uint4 &w, float *x) {
+  x[0] = bf16lo(w.x), x[1] = bf16hi(w.x), x[2] = bf16lo(w.y), x[3] = bf16hi(w.y);
+  x[4] = bf16lo(w.z), x[5] = bf16hi(w.z), x[6] = bf16lo(w.w), x[7] = bf16hi(w.w);
+}
+__device__ __forceinline__ uint4 pack8(const float *x) {
+  return make_uint4(f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3]),
+                    f32x2_to_bf16x2(x[4], x[5]), f32x2_to_bf16x2(x[6], x[7]));
+}
+
+// The epilogue of 8 elements i .. i+7 of column j: bias, activation,
+// residual, one rounding to bf16.
+__device__ __forceinline__ void finish8(const HeadArgs &a, float *z, int i, int j) {
+  if (j >= a.J || i >= a.I) return;
   const long long at = (long long)j * a.ldo + i;
-  float res[16];
+  if (a.vec) {   // I is a multiple of 8 then
+    float x[8];
+    if (a.bias) {
+      unpack8(*reinterpret_cast<const uint4 *>(a.bias + i), x);
 #pragma unroll
-  for (int q = 0; q < 16; ++q)
-    res[q] = a.residual && j + q < a.J ? __bfloat162float(a.residual[at + q * a.ldo]) : 0.f;
+      for (int q = 0; q < 8; ++q) z[q] += x[q];
+    }
+    if (a.pre) *reinterpret_cast<uint4 *>(a.pre + at) = pack8(z);
+    if (a.act != SPEC_ACT_NONE) {
 #pragma unroll
-  for (int q = 0; q < 16; ++q) {
-    if (j + q >= a.J) break;
-    const float z = v[q] + bias;
-    if (a.pre) a.pre[at + q * a.ldo] = __float2bfloat16_rn(z);
-    a.out[at + q * a.ldo] = __float2bfloat16_rn(act_value(z, a.act) + res[q]);
+      for (int q = 0; q < 8; ++q) z[q] = act_value(z[q], a.act);
+    }
+    if (a.residual) {
+      unpack8(*reinterpret_cast<const uint4 *>(a.residual + at), x);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) z[q] += x[q];
+    }
+    *reinterpret_cast<uint4 *>(a.out + at) = pack8(z);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      if (i + q >= a.I) break;
+      const float v = z[q] + (a.bias ? bf16_at(a.bias, i + q) : 0.f);
+      if (a.pre) bf16_to(a.pre, at + q, v);
+      bf16_to(a.out, at + q, act_value(v, a.act) + (a.residual ? bf16_at(a.residual, at + q) : 0.f));
+    }
   }
 }
 
@@ -148,13 +186,16 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
   extern __shared__ uint8_t dyn[];
   __shared__ HeadSmem sh;
   uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)dyn + 1023) & ~(uintptr_t)1023);
+  float *staging = reinterpret_cast<float *>(ring + a.stages * (HD_A_BYTES + a.nt * HD_R * 2));
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int stage_bytes = HD_A_BYTES + a.nt * HD_R * 2;
   uint32_t cols = 32;   // TMEM columns: two accumulators, a power of two
-  while (cols < 2u * a.nt) cols <<= 1;
+  while (cols < 2u * ((a.nt + 31) & ~31)) cols <<= 1;
   volatile int *abort = &sh.abort;
 
   if (t == 0) {
+    // the only error is a wait that runs out, seconds after this
+    if (blockIdx.x == 0 && a.reset) a.hdr->status = SPEC_OK, a.hdr->detail = -1;
     sh.abort = 0;
     for (int s = 0; s < a.stages; ++s) mbar_init(&sh.full[s], 1), mbar_init(&sh.empty[s], 1);
     for (int s = 0; s < 2; ++s) mbar_init(&sh.acc_full[s], 1), mbar_init(&sh.acc_empty[s], 4);
@@ -254,56 +295,51 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
     int n = 0;
     for (int u = blockIdx.x; u < a.units; u += gridDim.x, ++n) {
       const int tile = u % tiles, buf = n & 1;
-      const int i = tile / a.tiles_j * HD_I + t, j0 = tile % a.tiles_j * a.nt;
-      const bool got = mbar_wait_bounded(&sh.acc_full[buf], (n >> 1) & 1, abort);
-      // one verdict for the four warps, which meet at barriers below
-      int alive;
-      asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
-                   "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
-                   : "=r"(alive)
-                   : "r"((int)got)
-                   : "memory");
-      if (!alive) {
+      const int i0 = tile / a.tiles_j * HD_I, j0 = tile % a.tiles_j * a.nt;
+      // one verdict for the warp, which loads from TMEM together
+      if (!__all_sync(~0u, mbar_wait_bounded(&sh.acc_full[buf], (n >> 1) & 1, abort))) {
         *abort = 1;
-        set_status(a.hdr, SPEC_ERR_TIMEOUT, 0);
+        if (lane == 0) set_status(a.hdr, SPEC_ERR_TIMEOUT, 0);
         break;
       }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t d = tmem + buf * (cols / 2) + ((uint32_t)(warp * 32) << 16);
-      float *mine = a.part + (long long)u * a.nt * HD_I + t;
-      for (int c = 0; c < a.nt; c += 16) {
-        float v[16];
-        tmem_ld16(d + c, v);
-        if (a.S == 1) {
-          finish16(a, v, i, j0 + c);
-        } else {
+      if (a.S > 1) {   // 128 bytes per warp and column
+        float *mine = a.part + (long long)u * a.nt * HD_I + t;
+        for (int c = 0; c < a.nt; c += 32) {
+          float v[32];
+          tmem_ld32(d + c, v);
 #pragma unroll
-          for (int q = 0; q < 16; ++q)
-            if (j0 + c + q < a.J) mine[(c + q) * HD_I] = v[q];
+          for (int q = 0; q < 32; ++q)
+            if (c + q < a.nt && j0 + c + q < a.J) mine[(c + q) * HD_I] = v[q];
+        }
+      } else {
+        // turned through shared memory, 32 columns of the warp's 32 lanes at a
+        // time, so that the result leaves in 16-byte stores of 64 bytes a row
+        float *st = staging + warp * 32 * HD_STAGE_LD;
+        for (int c = 0; c < a.nt; c += 32) {
+          float v[32];
+          tmem_ld32(d + c, v);
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 32; ++q) st[q * HD_STAGE_LD + lane] = v[q];
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int col = q * 8 + lane / 4;
+            float z[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float4 w = *reinterpret_cast<const float4 *>(st + col * HD_STAGE_LD + lane % 4 * 8 + h * 4);
+              z[4 * h] = w.x, z[4 * h + 1] = w.y, z[4 * h + 2] = w.z, z[4 * h + 3] = w.w;
+            }
+            if (c + col < a.nt) finish8(a, z, i0 + warp * 32 + lane % 4 * 8, j0 + c + col);
+          }
         }
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
-      if (a.S > 1) {
-        __threadfence();
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (t == 0) sh.last = atomicAdd(a.count + tile, 1u) == (unsigned)a.S - 1;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (sh.last) {
-          __threadfence();
-          for (int c = 0; c < a.nt && j0 + c < a.J; c += 16) {
-            float v[16] = {};
-            for (int s = 0; s < a.S; ++s) {
-              const float *p = a.part + ((long long)s * tiles + tile) * a.nt * HD_I + t;
-#pragma unroll
-              for (int q = 0; q < 16; ++q)
-                if (j0 + c + q < a.J) v[q] += __ldcg(p + (c + q) * HD_I);
-            }
-            finish16(a, v, i, j0 + c);
-          }
-        }
-      }
     }
   }
   __syncthreads();
@@ -311,6 +347,31 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
     __syncwarp();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
+  }
+}
+
+// The parts of a split added up in the order of r, and the epilogue: a thread
+// takes 8 elements of i of one column.
+__global__ void __launch_bounds__(256) k_head_join(const HeadArgs a) {
+  const int tiles = a.tiles_i * a.tiles_j;
+  const long long n = (long long)tiles * a.nt * (HD_I / 8);
+  for (long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x; e < n;
+       e += (long long)gridDim.x * blockDim.x) {
+    const int iv = (int)(e % (HD_I / 8)), col = (int)(e / (HD_I / 8) % a.nt);
+    const int tile = (int)(e / (HD_I / 8) / a.nt);
+    const int i = tile / a.tiles_j * HD_I + iv * 8, j = tile % a.tiles_j * a.nt + col;
+    if (j >= a.J || i >= a.I) continue;
+    const float *p = a.part + ((long long)tile * a.nt + col) * HD_I + iv * 8;
+    const long long step = (long long)tiles * a.nt * HD_I;
+    float z[8] = {};
+#pragma unroll 4
+    for (int s = 0; s < a.S; ++s) {
+      const float4 x = __ldcs(reinterpret_cast<const float4 *>(p + s * step));
+      const float4 y = __ldcs(reinterpret_cast<const float4 *>(p + s * step) + 1);
+      z[0] += x.x, z[1] += x.y, z[2] += x.z, z[3] += x.w;
+      z[4] += y.x, z[5] += y.y, z[6] += y.z, z[7] += y.w;
+    }
+    finish8(a, z, i, j);
   }
 }
 
@@ -431,7 +492,7 @@ int make_map(CUtensorMap *m, const void *p, long long rows, long long inner, lon
 struct Plan {
   int tiles_i, tiles_j, nt, KB, S;
   long long units;
-  size_t count_bytes, part_bytes;
+  size_t part_bytes;
 };
 
 Plan make_plan(long long I, long long J, long long R, bool b_mn) {
@@ -442,19 +503,20 @@ Plan make_plan(long long I, long long J, long long R, bool b_mn) {
   p.nt = (int)((each + step - 1) / step * step);
   p.KB = (int)((R + HD_R - 1) / HD_R);
   const long long tiles = (long long)p.tiles_i * p.tiles_j;
-  // rounds of units per SM times the stages of a unit; a split adds the
-  // partials' way out and back, worth about six stages at nt = 256
+  // rounds of units per SM times the stages of a unit (a stage of nt = 256 takes
+  // 0.27 us); a split adds the partials' way out, and the join's launch and
+  // its reads
   double best = 0;
   p.S = 1;
   for (int S = 1; S <= HD_MAX_SPLIT && S <= p.KB; ++S) {
     const long long units = tiles * S, rounds = (units + HD_PLAN_SMS - 1) / HD_PLAN_SMS;
     if (S > 1 && (units * p.nt * HD_I * 4 > (128ll << 20))) break;
-    const double cost = (double)rounds * ((p.KB + S - 1) / S + 2.0 + (S > 1 ? 6.0 * p.nt / 256 : 0)) +
-                        (S > 1 ? 0.5 * S * p.nt / 256 + 2 : 0);
+    const double stage = 0.25 + 0.75 * p.nt / 256;   // of a full stage: A's copy counts too
+    const double cost = (double)rounds * (((p.KB + S - 1) / S + 2.0) * stage + (S > 1 ? 4.0 * p.nt / 256 : 0)) +
+                        (S > 1 ? 10.0 + 0.1 * units * p.nt / 256 : 0);
     if (S == 1 || cost < best) best = cost, p.S = S;
   }
   p.units = tiles * p.S;
-  p.count_bytes = p.S > 1 ? align256((size_t)tiles * 4) : 0;
   p.part_bytes = p.S > 1 ? align256((size_t)p.units * p.nt * HD_I * 4) : 0;
   return p;
 }
@@ -465,14 +527,21 @@ int launch_head(const Plan &p, const CUtensorMap &ma, const CUtensorMap &mb, Hea
   a.units = (int)p.units;
   const int stage = HD_A_BYTES + p.nt * HD_R * 2;
   a.stages = std::min(HD_MAX_STAGES, HD_SMEM / stage);
-  const int smem = a.stages * stage + 1024;
+  const int smem = a.stages * stage + HD_STAGING + 1024;
+  a.vec = a.I % 8 == 0 && a.ldo % 8 == 0 && aligned(a.bias, 16) && aligned(a.residual, 16);
   const int sms = num_sms();
   if (sms <= 0) return SPEC_ERR_CUDA;
   if (cudaFuncSetAttribute(k_head<A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
       cudaSuccess)
     return SPEC_ERR_CUDA;
   k_head<A_MN, B_MN><<<(unsigned)std::min<long long>(p.units, sms), HD_THREADS, smem, st>>>(ma, mb, a);
-  return launched();
+  int rc = launched();
+  if (rc == SPEC_OK && p.S > 1) {
+    const long long n = (long long)p.tiles_i * p.tiles_j * p.nt * (HD_I / 8);
+    k_head_join<<<(unsigned)std::min<long long>((n + 255) / 256, 8ll * sms), 256, 0, st>>>(a);
+    rc = launched();
+  }
+  return rc;
 }
 
 inline long long round8(long long x) { return (x + 7) / 8 * 8; }
@@ -498,7 +567,7 @@ bool sizes_ok(int M, int N, int K) {
 
 size_t forward_bytes(int M, int N, int K) {
   const Plan p = make_plan(N, std::max(M, 1), K, false);
-  return sizeof(WsHeader) + p.count_bytes + p.part_bytes + padded_bytes(M, K) + padded_bytes(N, K);
+  return sizeof(WsHeader) + p.part_bytes + padded_bytes(M, K) + padded_bytes(N, K);
 }
 
 inline int dz_segments(int M) { return (M + HD_DZ_ROWS - 1) / HD_DZ_ROWS; }
@@ -506,7 +575,7 @@ inline int dz_segments(int M) { return (M + HD_DZ_ROWS - 1) / HD_DZ_ROWS; }
 size_t backward_bytes(int M, int N, int K) {
   const int m = std::max(M, 1);
   const Plan px = make_plan(K, m, N, false), pw = make_plan(K, N, m, true);
-  return sizeof(WsHeader) + px.count_bytes + pw.count_bytes + std::max(px.part_bytes, pw.part_bytes) +
+  return sizeof(WsHeader) + std::max(px.part_bytes, pw.part_bytes) +
          padded_bytes(M, K) + padded_bytes(N, K) + align256((size_t)m * round8(N) * 2) +
          align256((size_t)dz_segments(m) * N * 4);
 }
@@ -535,20 +604,18 @@ extern "C" int spec_head_forward(const void *x, const void *weight, const void *
   if (p.units > 0x7fffffffll) return SPEC_ERR_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char *ws = static_cast<char *>(workspace);
-  // the status and the split's arrival counts start at zero
-  if (cudaMemsetAsync(ws, 0, sizeof(WsHeader) + p.count_bytes, st) != cudaSuccess) return SPEC_ERR_CUDA;
-  if (M == 0) return SPEC_OK;
+  if (M == 0) return reset_header(ws, st);
   HeadArgs a{};
   a.hdr = reinterpret_cast<WsHeader *>(ws);
-  a.count = reinterpret_cast<unsigned *>(ws + sizeof(WsHeader));
-  a.part = reinterpret_cast<float *>(ws + sizeof(WsHeader) + p.count_bytes);
-  ws += sizeof(WsHeader) + p.count_bytes + p.part_bytes;
+  a.part = reinterpret_cast<float *>(ws + sizeof(WsHeader));
+  ws += sizeof(WsHeader) + p.part_bytes;
   a.I = N, a.J = M, a.ldo = N;
   a.bias = static_cast<const __nv_bfloat16 *>(bias);
   a.residual = static_cast<const __nv_bfloat16 *>(residual);
   a.out = static_cast<__nv_bfloat16 *>(y);
   a.pre = static_cast<__nv_bfloat16 *>(pre);
   a.act = act;
+  a.reset = 1;
   int rc;
   if ((rc = operand(&x, M, K, &ws, st)) != SPEC_OK || (rc = operand(&weight, N, K, &ws, st)) != SPEC_OK)
     return rc;
@@ -583,11 +650,8 @@ extern "C" int spec_head_backward(const void *dy, const void *x, const void *wei
   char *ws = static_cast<char *>(workspace);
   HeadArgs a{};
   a.hdr = reinterpret_cast<WsHeader *>(ws);
-  unsigned *count_x = reinterpret_cast<unsigned *>(ws + sizeof(WsHeader));
-  unsigned *count_w = reinterpret_cast<unsigned *>(ws + sizeof(WsHeader) + px.count_bytes);
-  if (cudaMemsetAsync(ws, 0, sizeof(WsHeader) + px.count_bytes + pw.count_bytes, st) != cudaSuccess)
-    return SPEC_ERR_CUDA;
-  ws += sizeof(WsHeader) + px.count_bytes + pw.count_bytes;
+  if (reset_header(ws, st) != SPEC_OK) return SPEC_ERR_CUDA;
+  ws += sizeof(WsHeader);
   a.part = reinterpret_cast<float *>(ws);
   ws += std::max(px.part_bytes, pw.part_bytes);
   if (M == 0) {   // no rows: the weights' gradients are zero
@@ -627,7 +691,6 @@ extern "C" int spec_head_backward(const void *dy, const void *x, const void *wei
     if ((rc = make_map(&ma, weight, N, K, ldk, 64)) != SPEC_OK ||
         (rc = make_map(&mb, gz, M, N, ldz, px.nt)) != SPEC_OK)
       return rc;
-    a.count = count_x;
     a.I = K, a.J = M, a.ldo = K;
     a.out = static_cast<__nv_bfloat16 *>(dx);
     if ((rc = launch_head<true, false>(px, ma, mb, a, st)) != SPEC_OK) return rc;
@@ -637,7 +700,6 @@ extern "C" int spec_head_backward(const void *dy, const void *x, const void *wei
     if ((rc = make_map(&ma, x, M, K, ldk, 64)) != SPEC_OK ||
         (rc = make_map(&mb, gz, M, N, ldz, 64)) != SPEC_OK)
       return rc;
-    a.count = count_w;
     a.I = K, a.J = N, a.ldo = K;
     a.out = static_cast<__nv_bfloat16 *>(dw);
     if ((rc = launch_head<true, true>(pw, ma, mb, a, st)) != SPEC_OK) return rc;
