@@ -3,16 +3,18 @@
 //
 // Almost every token of a row keeps its bits, so the kernel is a copy that
 // knows where it must not be one. A CTA owns a range of the vocabulary (CH
-// tokens) of one request for a segment of its rows. It first builds, in
-// shared memory, the range's table: for every token the count of its
-// generated occurrences and whether the prompt holds it, from one scan of the
-// request's history (the scan is re-read from L2 by the other ranges), and
-// the request's biases. Each thread owns the same P tokens of the range in
-// every row and keeps one bit per token ("a rule touches it") in a register,
-// so the rows then stream through registers with one compare per 16 bytes,
-// and only flagged tokens look at the table. Draft tokens between two rows
-// are added by the thread that owns them, without a barrier; a tree row's
-// path is added before the row and taken out after it.
+// tokens) of one request for a segment of its rows, and each thread the same P
+// tokens of the range in every row. Two scans of the request's history (the
+// second mostly from registers) build, in shared memory, a bit per touched
+// token and its count of generated occurrences; counts of untouched tokens are
+// never initialised. A thread keeps its P bits in a register. The rows then
+// stream through registers in 16-byte vectors, and the thread goes back for
+// its few touched tokens one by one, from L1, after the row's vectors are out:
+// with hundreds of touched tokens per request nearly every warp has one, and
+// taking them inside the vector code made the whole kernel issue-bound (2.5
+// times the time). Draft tokens between two rows are added by the thread that
+// owns them, without a barrier; a tree row's path is added before the row and
+// taken out after it.
 //
 // Bound by HBM: each logit is read once and written once. A 16-byte vector
 // whose tokens are all masked is not read at all: the mask of row i+1 is in
@@ -26,8 +28,9 @@ namespace {
 
 constexpr int RU_THREADS = 256;
 constexpr int RU_MAX_SEG = 16;             // rows of one CTA
+constexpr int RU_BIASES = 256;             // biases of a range listed in shared memory
+constexpr int RU_HELD = 4;                 // history tokens a thread keeps between the scans
 constexpr int RU_SEEN = (int)0x80000000u;  // table: the prompt holds the token
-constexpr uint32_t RU_FULL = 0xffffffffu;
 
 struct RulesArgs {
   const void *in;
@@ -38,14 +41,18 @@ struct RulesArgs {
   WsHeader *hdr;
 };
 
-// Shared memory: [CH] counts, [CH] bias indexes (if any), the segment's mask
-// rows and new tokens, and the trees' path tokens inside this range.
+// Shared memory of a CTA. The counts' space first holds a tree's parents and
+// tokens, where they fit.
 template <int CH>
 struct RulesSmem {
-  static size_t bytes(bool bias, bool tree) {
-    return sizeof(int) * ((size_t)CH * (bias ? 2 : 1) + 2 * RU_MAX_SEG +
-                          (tree ? RU_MAX_SEG * (1 + SPEC_MAX_TREE_DEPTH) : 0));
-  }
+  int cnt[CH];                  // generated occurrences, RU_SEEN for the prompt's
+  uint32_t bits[CH / 32];       // tokens that the history or a bias touches
+  int n_bias;
+  int2 bias[RU_BIASES];         // (token - c0, entry of the request's list)
+  int mrow[RU_MAX_SEG];
+  int tok[RU_MAX_SEG];          // the draft that a row sees and the row before does not
+  int pn[RU_MAX_SEG];           // trees: path tokens inside this range, per row
+  int path[RU_MAX_SEG][SPEC_MAX_TREE_DEPTH];
 };
 
 template <typename E> struct Elem;
@@ -74,17 +81,11 @@ __global__ void __launch_bounds__(RU_THREADS) k_rules(RulesArgs a) {
   constexpr int NV = P / VEC;                    // accesses of a thread per row
   constexpr uint32_t VFULL = VEC == 1 ? 1u : (1u << VEC) - 1;
   constexpr int NRAW = VEC == 1 ? 1 : NV;        // mask words of a thread per row
-  extern __shared__ __align__(16) int sm[];
-  const bool has_bias = a.r.bias_ids != nullptr;
+  extern __shared__ __align__(16) unsigned char dyn[];
+  RulesSmem<CH> &sm = *reinterpret_cast<RulesSmem<CH> *>(dyn);
   const bool tree = a.r.parent != nullptr;
-  int *cnt = sm;
-  int *bidx = cnt + CH;
-  int *s_mrow = bidx + (has_bias ? CH : 0);
-  int *s_tok = s_mrow + RU_MAX_SEG;
-  int *s_pn = s_tok + RU_MAX_SEG;                // trees: path tokens in range, per row
-  int *s_path = s_pn + RU_MAX_SEG;
 
-  const int t = threadIdx.x, lane = t & 31;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int c = blockIdx.x % a.nch;
   const int b = (blockIdx.x / a.nch) % a.B;
   const int i0 = (blockIdx.x / a.nch) / a.B * a.seg;
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(RU_THREADS) k_rules(RulesArgs a) {
     if (h0 < 0 || h1 < h0) bad = true, h1 = h0 = 0;
     hp = a.r.prompt_len ? GLD(a.r.prompt_len + b) : 0;
   }
-  if (has_bias) {
+  if (a.r.bias_ids != nullptr) {
     b0 = GLD(a.r.cu_bias + b), b1 = GLD(a.r.cu_bias + b + 1);
     if (b0 < 0 || b1 < b0) bad = true, b1 = b0 = 0;
   }
@@ -117,43 +118,37 @@ __global__ void __launch_bounds__(RU_THREADS) k_rules(RulesArgs a) {
     k0 = GLD(a.r.cu_tokens + b), K = GLD(a.r.cu_tokens + b + 1) - k0;
     if (k0 < 0 || K < 0) bad = true, K = 0;
   }
-
-  for (int i = t; i < CH / 4; i += RU_THREADS) {
-    reinterpret_cast<int4 *>(cnt)[i] = make_int4(0, 0, 0, 0);
-    if (has_bias) reinterpret_cast<int4 *>(bidx)[i] = make_int4(0, 0, 0, 0);
+  int held[RU_HELD];   // this thread's first history tokens, on their way early
+#pragma unroll
+  for (int q = 0; q < RU_HELD; ++q) {
+    const int j = h0 + q * RU_THREADS + t;
+    held[q] = j < h1 ? GLD(a.r.history + j) : -1;
+    if (j < h1 && (held[q] < 0 || held[q] >= a.V)) bad = true, held[q] = -1;
   }
+
+  if (t < CH / 32) sm.bits[t] = 0;
+  if (t == 0) sm.n_bias = 0;
   if (t < n) {
     int mrow = -1;
     if (a.r.mask != nullptr) {
       mrow = a.r.mask_rows ? GLD(a.r.mask_rows + lo + i0 + t) : lo + i0 + t;
       if (mrow < -1 || mrow >= a.r.n_mask) bad = true, mrow = -1;
     }
-    s_mrow[t] = mrow;
-    // the draft that row t sees and row t-1 does not (row 0's are in the table)
-    const int j = i0 + t - 1;
+    sm.mrow[t] = mrow;
+    const int j = i0 + t - 1;   // row 0's drafts are in the table
     int tok = -1;
     if (!tree && t > 0 && j < K) {
       tok = GLD(a.r.tokens + k0 + j);
       if (tok < 0 || tok >= a.V) bad = true, tok = -1;
     }
-    s_tok[t] = tok;
-    if (tree) {   // this row's path, the tokens of this range only
-      int m = 0, v = i0 + t, steps = 0;
-      while (v > 0) {
-        const int tk = GLD(a.r.tokens + lo + v);
-        if (tk < 0 || tk >= a.V) {
-          bad = true;
-        } else if (tk >= c0 && tk < c0 + CH) {
-          s_path[t * SPEC_MAX_TREE_DEPTH + m++] = tk - c0;
-        }
-        const int up = GLD(a.r.parent + lo + v);
-        if (up < 0 || up >= v || ++steps >= SPEC_MAX_TREE_DEPTH) {
-          if (up != 0) bad = true;
-          break;
-        }
-        v = up;
-      }
-      s_pn[t] = m;
+    sm.tok[t] = tok;
+    sm.pn[t] = 0;
+  }
+  const bool staged = i0 + n <= CH / 2;
+  if (tree && staged) {   // the tree up to this segment's last row
+    for (int v = t; v < i0 + n; v += RU_THREADS) {
+      sm.cnt[v] = GLD(a.r.parent + lo + v);
+      sm.cnt[CH / 2 + v] = GLD(a.r.tokens + lo + v);
     }
   }
   __syncthreads();
@@ -163,14 +158,13 @@ __global__ void __launch_bounds__(RU_THREADS) k_rules(RulesArgs a) {
 #pragma unroll
   for (int v = 0; v < NV; ++v)
     if (c0 + (v * RU_THREADS + t) * VEC < a.V) valid |= VFULL << (v * VEC);
-  if (P < 32) valid &= (1u << (P & 31)) - 1;
 
   const int W = (a.V + 31) >> 5;
   uint32_t raw[NRAW];
   auto load_mask = [&](int i) {
-    const int mrow = s_mrow[i];
+    const int mrow = sm.mrow[i];
 #pragma unroll
-    for (int q = 0; q < NRAW; ++q) raw[q] = RU_FULL;
+    for (int q = 0; q < NRAW; ++q) raw[q] = ~0u;
     if (mrow < 0) return;
     const uint32_t *words = a.r.mask + (long long)mrow * W;
     if (VEC == 1) {   // lane v holds the warp's 32 bits of access v
@@ -189,7 +183,7 @@ __global__ void __launch_bounds__(RU_THREADS) k_rules(RulesArgs a) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       if (VEC == 1) {
-        A |= ((__shfl_sync(RU_FULL, raw[0], v) >> lane) & 1u) << v;
+        A |= ((__shfl_sync(~0u, raw[0], v) >> lane) & 1u) << v;
       } else if (VEC == 8) {
         A |= (raw[v % NRAW] & 0xffu) << (v * VEC % 32);
       } else {
@@ -198,142 +192,201 @@ __global__ void __launch_bounds__(RU_THREADS) k_rules(RulesArgs a) {
     }
     return A & valid;
   };
+  auto bits_of = [&](uint32_t m, int v) -> uint32_t { return (m >> (v * VEC)) & VFULL; };
 
   U cur[NV], nxt[NV];
-  auto row_ptr = [&](const void *base, int i) {
-    return reinterpret_cast<const U *>(static_cast<const E *>(base) +
-                                       (long long)(lo + i0 + i) * a.V + c0);
-  };
-  // in place, a vector that neither the mask nor a rule touches stays
-  auto untouched = [&](uint32_t av, uint32_t fv, uint32_t vv) { return av == vv && fv == 0; };
-  auto load_row = [&](U *dst, int i, uint32_t A, uint32_t F) {
-    const U *p = row_ptr(a.in, i);
+  auto row_at = [&](int i) { return (long long)(lo + i0 + i) * a.V + c0; };
+  // vectors with an allowed token; in place, only those that the mask cuts
+  auto load_row = [&](U *dst, int i, uint32_t A) {
+    const U *p = reinterpret_cast<const U *>(static_cast<const E *>(a.in) + row_at(i));
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const uint32_t av = (A >> (v * VEC)) & VFULL, fv = (F >> (v * VEC)) & VFULL,
-                     vv = (valid >> (v * VEC)) & VFULL;
-      if (av != 0 && !(a.inplace && untouched(av, fv, vv))) dst[v] = GLD(p + v * RU_THREADS + t);
+      const uint32_t av = bits_of(A, v);
+      if (av != 0 && !(a.inplace && av == bits_of(valid, v))) dst[v] = GLD(p + v * RU_THREADS + t);
     }
   };
   auto own_bit = [&](int e) -> uint32_t {   // this thread's bit for token c0 + e, or 0
     if (e < 0 || e >= CH || (e / VEC) % RU_THREADS != t) return 0;
     return 1u << ((e / VEC / RU_THREADS) * VEC + e % VEC);
   };
-  auto new_bits = [&](int i) -> uint32_t {
-    if (!tree) return s_tok[i] < 0 ? 0 : own_bit(s_tok[i] - c0);
-    uint32_t f = 0;
-    for (int m = 0; m < s_pn[i]; ++m) f |= own_bit(s_path[i * SPEC_MAX_TREE_DEPTH + m]);
-    return f;
-  };
 
   load_mask(0);
   uint32_t A = allowed_bits();
-  if (!a.inplace) load_row(cur, 0, A, 0);
+  load_row(cur, 0, A);
   if (n > 1) load_mask(1);
 
-  // ---- the range's table: one scan of the history, the drafts before this
-  // segment, the biases
-  for (int j = h0 + t; j < h1; j += RU_THREADS) {
-    const int tok = GLD(a.r.history + j);
-    if (tok < 0 || tok >= a.V) bad = true;
+  if (tree) {
+    if (t < n) {   // this row's path, the tokens of this range only
+      int m = 0, v = i0 + t, steps = 0;
+      while (v > 0) {
+        const int tk = staged ? sm.cnt[CH / 2 + v] : GLD(a.r.tokens + lo + v);
+        if (tk < 0 || tk >= a.V) {
+          bad = true;
+        } else if (tk >= c0 && tk < c0 + CH) {
+          sm.path[t][m++] = tk - c0;
+        }
+        const int up = staged ? sm.cnt[v] : GLD(a.r.parent + lo + v);
+        if (up < 0 || up >= v || ++steps >= SPEC_MAX_TREE_DEPTH) {
+          if (up != 0) bad = true;
+          break;
+        }
+        v = up;
+      }
+      sm.pn[t] = m;
+    }
+    __syncthreads();
+  }
+
+  // ---- first scan: the touched tokens, whose counts start at zero (any
+  // number of threads may store that zero)
+  auto touch = [&](int tok) {
     const int e = tok - c0;
     if (e >= 0 && e < CH) {
-      if (j - h0 < hp) atomicOr(cnt + e, RU_SEEN);
-      else atomicAdd(cnt + e, 1);
+      sm.cnt[e] = 0;
+      atomicOr(&sm.bits[e >> 5], 1u << (e & 31));
     }
+  };
+#pragma unroll
+  for (int q = 0; q < RU_HELD; ++q)
+    if (held[q] >= 0) touch(held[q]);
+  for (int j = h0 + RU_HELD * RU_THREADS + t; j < h1; j += RU_THREADS) {
+    const int tok = GLD(a.r.history + j);
+    if (tok < 0 || tok >= a.V) bad = true;
+    else touch(tok);
   }
   if (!tree) {
     for (int j = t; j < min(i0, K); j += RU_THREADS) {
       const int tok = GLD(a.r.tokens + k0 + j);
       if (tok < 0 || tok >= a.V) bad = true;
-      const int e = tok - c0;
-      if (e >= 0 && e < CH) atomicAdd(cnt + e, 1);
+      else touch(tok);
     }
   }
   for (int j = b0 + t; j < b1; j += RU_THREADS) {
     const int id = GLD(a.r.bias_ids + j);
     const float bv = GLD(a.r.bias_values + j);
-    if (id < 0 || id >= a.V || isnan(bv) || bv == INFINITY) bad = true;
-    const int e = id - c0;
-    if (e >= 0 && e < CH) atomicMax(bidx + e, j - b0 + 1);   // the last entry holds
+    if (id < 0 || id >= a.V || isnan(bv) || bv == INFINITY) {
+      bad = true;
+    } else if (id >= c0 && id < c0 + CH) {
+      touch(id);
+      const int k = atomicAdd(&sm.n_bias, 1);
+      if (k < RU_BIASES) sm.bias[k] = make_int2(id - c0, j);
+    }
+  }
+  if (t < n) {   // what comes in with the rows: a count, no bit yet
+    const int e = sm.tok[t] - c0;
+    if (sm.tok[t] >= 0 && e >= 0 && e < CH) sm.cnt[e] = 0;
+    for (int m = 0; m < sm.pn[t]; ++m) sm.cnt[sm.path[t][m]] = 0;
   }
   if (bad) set_status(a.hdr, SPEC_ERR_INVALID_ARG, b);
   __syncthreads();
 
-  uint32_t F = 0;   // tokens of this thread that a rule touches
+  // ---- second scan: the counts
+  auto count = [&](int tok, bool prompt) {
+    const int e = tok - c0;
+    if (e >= 0 && e < CH) {
+      if (prompt) atomicOr(&sm.cnt[e], RU_SEEN);
+      else atomicAdd(&sm.cnt[e], 1);
+    }
+  };
+#pragma unroll
+  for (int q = 0; q < RU_HELD; ++q)
+    if (held[q] >= 0) count(held[q], q * RU_THREADS + t < hp);
+  for (int j = h0 + RU_HELD * RU_THREADS + t; j < h1; j += RU_THREADS)
+    count(GLD(a.r.history + j), j - h0 < hp);
+  if (!tree)
+    for (int j = t; j < min(i0, K); j += RU_THREADS) count(GLD(a.r.tokens + k0 + j), false);
+  __syncthreads();
+
+  uint32_t F = 0;   // tokens of this thread that the history or a bias touches
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const int e = (v * RU_THREADS + t) * VEC + j;
-      if (cnt[e] != 0 || (has_bias && bidx[e] != 0)) F |= 1u << (v * VEC + j);
-    }
+    if (VEC == 8)
+      F |= (uint32_t)reinterpret_cast<const uint8_t *>(sm.bits)[v * RU_THREADS + t] << (v * VEC % 32);
+    else if (VEC == 4)
+      F |= ((reinterpret_cast<const uint8_t *>(sm.bits)[(v * RU_THREADS + t) >> 1] >> ((t & 1) * 4)) & 0xfu)
+           << (v * VEC % 32);
+    else
+      F |= ((sm.bits[v * (RU_THREADS / 32) + warp] >> lane) & 1u) << v;
   }
-  if (a.inplace) load_row(cur, 0, A, F | new_bits(0));
 
+  const float inv_rho = 1.f / rho;
+  const int n_bias = sm.n_bias;
   for (int i = 0; i < n; ++i) {
     uint32_t A1 = 0;
     if (i + 1 < n) {
       A1 = allowed_bits();
-      load_row(nxt, i + 1, A1, a.inplace ? (F | new_bits(i) | new_bits(i + 1)) : 0);
+      load_row(nxt, i + 1, A1);
       if (i + 2 < n) load_mask(i + 2);
     }
     // the tokens that come in with this row
     uint32_t Fi = F;
     if (!tree) {
-      if (s_tok[i] >= 0) {
-        const uint32_t f = own_bit(s_tok[i] - c0);
-        if (f) ++cnt[s_tok[i] - c0];
+      if (sm.tok[i] >= 0) {
+        const uint32_t f = own_bit(sm.tok[i] - c0);
+        if (f) ++sm.cnt[sm.tok[i] - c0];
         F |= f;
         Fi = F;
       }
     } else {
-      for (int m = 0; m < s_pn[i]; ++m) {
-        const int e = s_path[i * SPEC_MAX_TREE_DEPTH + m];
+      for (int m = 0; m < sm.pn[i]; ++m) {
+        const int e = sm.path[i][m];
         const uint32_t f = own_bit(e);
-        if (f) ++cnt[e];
+        if (f) ++sm.cnt[e];
         Fi |= f;
       }
     }
-    U *o = const_cast<U *>(row_ptr(a.out, i));
+    const E *in = static_cast<const E *>(a.in) + row_at(i);
+    E *out = static_cast<E *>(a.out) + row_at(i);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const uint32_t av = (A >> (v * VEC)) & VFULL, fv = (Fi >> (v * VEC)) & VFULL,
-                     vv = (valid >> (v * VEC)) & VFULL;
-      if (vv == 0 || (a.inplace && untouched(av, fv, vv))) continue;
-      U x = cur[v];
-      if (av != VFULL || fv != 0) {
-        E w[VEC];
-        memcpy(w, &x, sizeof(x));
+      const uint32_t av = bits_of(A, v), vv = bits_of(valid, v);
+      if (vv == 0 || (a.inplace && av == vv)) continue;
+      if (VEC == 1) {
+        GST(out + v * RU_THREADS + t, av ? *reinterpret_cast<const E *>(&cur[v]) : (E)Elem<E>::NEG_INF);
+      } else {
+        uint4 x = *reinterpret_cast<const uint4 *>(&cur[v]);
+        if (av != VFULL) {
+          uint32_t *w = &x.x;
+          if (VEC == 8) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          if (!((av >> j) & 1)) {
-            w[j] = (E)Elem<E>::NEG_INF;
-          } else if ((fv >> j) & 1) {
-            const int e = (v * RU_THREADS + t) * VEC + j;
-            const int ent = cnt[e];
-            float z = Elem<E>::to_f32(w[j]);
-            if (has_bias) {
-              const int k = bidx[e];
-              if (k != 0) z += GLD(a.r.bias_values + b0 + k - 1);
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t keep = ((av >> (2 * q)) & 1u) * 0xffffu | ((av >> (2 * q + 1)) & 1u) * 0xffff0000u;
+              w[q] = (w[q] & keep) | (0xff80ff80u & ~keep);
             }
-            if (ent != 0) {
-              z = z > 0.f ? z / rho : z * rho;
-              const int m = ent & ~RU_SEEN;
-              if (m != 0) z = z - fr * (float)m - pr;
-            }
-            w[j] = (E)Elem<E>::from_f32(z);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[q] = (av >> q) & 1u ? w[q] : 0xff800000u;
           }
         }
-        memcpy(&x, w, sizeof(x));
+        GST(reinterpret_cast<uint4 *>(out) + v * RU_THREADS + t, x);
       }
-      GST(o + v * RU_THREADS + t, x);
+    }
+    for (uint32_t todo = Fi & A; todo != 0; todo &= todo - 1) {
+      const int k = __ffs(todo) - 1;
+      const int e = (k / VEC * RU_THREADS + t) * VEC + k % VEC;
+      float z = Elem<E>::to_f32(GLD(in + e));
+      if (n_bias != 0) {   // of an id listed twice the last entry holds
+        int last = -1;
+        if (n_bias <= RU_BIASES) {
+          for (int m = 0; m < n_bias; ++m)
+            if (sm.bias[m].x == e) last = max(last, sm.bias[m].y);
+        } else {
+          for (int m = b1 - 1; m >= b0 && last < 0; --m)
+            if (GLD(a.r.bias_ids + m) == c0 + e) last = m;
+        }
+        if (last >= 0) z += GLD(a.r.bias_values + last);
+      }
+      const int ent = sm.cnt[e];
+      if (ent != 0) {
+        z *= z > 0.f ? inv_rho : rho;
+        const int m = ent & ~RU_SEEN;
+        if (m != 0) z = z - fr * (float)m - pr;
+      }
+      GST(out + e, (E)Elem<E>::from_f32(z));
     }
     if (tree) {
-      for (int m = 0; m < s_pn[i]; ++m) {
-        const int e = s_path[i * SPEC_MAX_TREE_DEPTH + m];
-        if (own_bit(e)) --cnt[e];
-      }
+      for (int m = 0; m < sm.pn[i]; ++m)
+        if (own_bit(sm.path[i][m])) --sm.cnt[sm.path[i][m]];
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) cur[v] = nxt[v];
@@ -342,8 +395,8 @@ __global__ void __launch_bounds__(RU_THREADS) k_rules(RulesArgs a) {
 }
 
 template <typename E, int VEC, int P>
-int launch_rules(const RulesArgs &a, long long ctas, bool bias, bool tree, cudaStream_t st) {
-  const size_t smem = RulesSmem<RU_THREADS * P>::bytes(bias, tree);
+int launch_rules(const RulesArgs &a, long long ctas, cudaStream_t st) {
+  const size_t smem = sizeof(RulesSmem<RU_THREADS * P>);
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(k_rules<E, VEC, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)smem) != cudaSuccess)
@@ -444,12 +497,14 @@ extern "C" int spec_process_logits(const void *logits, int dt, int R, int V,
   if (R == 0) return SPEC_OK;
   if (check_upload(st) != SPEC_OK) return SPEC_ERR_CUDA;
 
-  const bool bias = r.bias_ids != nullptr, tree = r.parent != nullptr;
   const int vec = (V * es) % 16 == 0 ? (int)(16 / es) : 1;
   // Long calls: wide ranges and segments of many rows, so that a table serves
   // many rows. Calls that would not fill the SMs: shorter segments, then
   // narrow ranges.
-  int P = 32;
+  // A thread's row is 64 bytes in registers (16 elements where rows are not
+  // 16-byte aligned).
+  const int wide = dt == SPEC_BF16 && vec == 8 ? 32 : 16;
+  int P = wide;
   int seg = std::min(max_rows, RU_MAX_SEG);
   auto ctas = [&](int p, int s) {
     return (long long)((V + RU_THREADS * p - 1) / (RU_THREADS * p)) * B * ((max_rows + s - 1) / s);
@@ -463,14 +518,10 @@ extern "C" int spec_process_logits(const void *logits, int dt, int R, int V,
   if (n > 0x7fffffffll) return SPEC_ERR_UNSUPPORTED;
   if (dt == SPEC_BF16) {
     if (vec == 8)
-      return P == 32 ? launch_rules<uint16_t, 8, 32>(a, n, bias, tree, st)
-                     : launch_rules<uint16_t, 8, 8>(a, n, bias, tree, st);
-    return P == 32 ? launch_rules<uint16_t, 1, 32>(a, n, bias, tree, st)
-                   : launch_rules<uint16_t, 1, 8>(a, n, bias, tree, st);
+      return P == 32 ? launch_rules<uint16_t, 8, 32>(a, n, st) : launch_rules<uint16_t, 8, 8>(a, n, st);
+    return P == 16 ? launch_rules<uint16_t, 1, 16>(a, n, st) : launch_rules<uint16_t, 1, 8>(a, n, st);
   }
   if (vec == 4)
-    return P == 32 ? launch_rules<uint32_t, 4, 32>(a, n, bias, tree, st)
-                   : launch_rules<uint32_t, 4, 8>(a, n, bias, tree, st);
-  return P == 32 ? launch_rules<uint32_t, 1, 32>(a, n, bias, tree, st)
-                 : launch_rules<uint32_t, 1, 8>(a, n, bias, tree, st);
+    return P == 16 ? launch_rules<uint32_t, 4, 16>(a, n, st) : launch_rules<uint32_t, 4, 8>(a, n, st);
+  return P == 16 ? launch_rules<uint32_t, 1, 16>(a, n, st) : launch_rules<uint32_t, 1, 8>(a, n, st);
 }

@@ -6,8 +6,14 @@ on a non-zero return code; the kernels of libspecverify.so do the work.
 from __future__ import annotations
 
 import ctypes
+import struct
+
+import torch
 
 import speculative_decoding_rejection_gb300 as _sv
+
+# the current stream's handle without a Stream object (less host time per call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 SPEC_ADAMW_BLOCK = 256
 SPEC_ACT_NONE, SPEC_ACT_SILU, SPEC_ACT_GELU = 0, 1, 2
@@ -37,10 +43,17 @@ class SpecAdamwHyper(ctypes.Structure):
         ("step_dev", ctypes.c_void_p)]
 
 
+# the two records as they lie in memory, for calls (less host time than a
+# Structure's fields)
+_RULES = struct.Struct("@14Pi4x")
+_HYPER = struct.Struct("@5dq3P")
+assert _RULES.size == ctypes.sizeof(SpecLogitsRules)
+assert _HYPER.size == ctypes.sizeof(SpecAdamwHyper)
+
 SIGS = {
     "spec_process_logits_workspace": (_sz, []),
     "spec_process_logits": (_i32, [_vp, _i32, _i32, _i32, _vp, _i32, _i32,
-                                   ctypes.POINTER(SpecLogitsRules), _vp, _vp, _sz, _vp]),
+                                   _vp, _vp, _vp, _sz, _vp]),
     "spec_distill_loss_workspace": (_sz, [_i32, _i32]),
     "spec_distill_loss": (_i32, [_vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp,
                                  _sz, _vp]),
@@ -52,39 +65,79 @@ SIGS = {
     "spec_head_backward_workspace": (_sz, [_i32, _i32, _i32]),
     "spec_head_backward": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _sz,
                                   _vp]),
-    "spec_adamw_step": (_i32, [_vp, _i64, _i32, ctypes.POINTER(SpecAdamwHyper), _vp, _sz, _vp]),
+    "spec_adamw_step": (_i32, [_vp, _i64, _i32, _vp, _vp, _sz, _vp]),
 }
 
 
-def _want(name, t, dtype, numel=None, device=None):
-    """A tensor of the dtype and size that the call reads; None passes."""
+def _arg(name, t, dtype, numel, dev):
+    """The address of a tensor the call reads or writes (None passes): of the
+    dtype, at least that many elements, contiguous, on device `dev`."""
     if t is None:
-        return
-    if t.dtype != dtype:
+        return None
+    if t.dtype is dtype and t.get_device() == dev and t.numel() >= numel and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if numel is not None and t.numel() < numel:
-        raise ValueError(f"{name} has {t.numel()} elements, {numel} are needed")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
+    _sv._ptr(t)   # raises for a host tensor and for one that is not contiguous
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{dev}")
+    raise ValueError(f"{name} has {t.numel()} elements, {numel} are needed")
 
 
-def _begin(device, stream, tensors):
-    """The stream of the call and a context in which its buffers are
-    allocated. Where that is not torch's current stream, the tensors the
-    caller made elsewhere are marked as in use there, so that their memory is
-    not handed out before the call's work is done."""
-    torch = _sv._torch()
-    cur = torch.cuda.current_stream(device)
-    s = cur if stream is None else stream
-    if s != cur:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(s)
-    return s, torch.cuda.stream(s)
+def _device(name, t):
+    """The CUDA device index of the call's first tensor."""
+    dev = t.get_device()
+    if dev < 0:
+        _sv._ptr(t)   # raises
+        raise ValueError(f"{name} must live on a CUDA device")
+    return dev
 
 
-def _bytes(t):
-    return ctypes.c_size_t(t.numel() * t.element_size())
+class _Call:
+    """The stream of a call, as a context in which its buffers are allocated.
+    Where that is not torch's current stream, the tensors the caller made
+    elsewhere are marked as in use there, so that their memory is not handed
+    out before the call's work is done."""
+
+    __slots__ = ("raw", "ctx")
+
+    def __init__(self, dev, stream, tensors):
+        self.ctx = None
+        if stream is None:
+            self.raw = torch.cuda.current_stream(dev).cuda_stream if _raw_stream is None \
+                else _raw_stream(dev)
+            return
+        self.raw = stream.cuda_stream
+        if stream != torch.cuda.current_stream(dev):
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+        self.ctx = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self
+
+    def __exit__(self, *e):
+        if self.ctx is not None:
+            self.ctx.__exit__(*e)
+
+
+def _scratch(size, dev, workspace):
+    """(workspace, address, bytes); one of `size` bytes where the caller has none."""
+    if workspace is None:
+        workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=f"cuda:{dev}")
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        _sv._ptr(workspace)
+        raise ValueError("the workspace is on another device")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _f32_or_bf16(t):
+    d = t.dtype
+    return _sv.SPEC_BF16 if d is torch.bfloat16 else _sv.SPEC_F32 if d is torch.float32 \
+        else _sv._dtype_code(t)
 
 
 # ------------------------------------------------------- rules on the logits
@@ -104,55 +157,50 @@ def spec_process_logits(logits, cu_rows, *, max_rows: int, history=None, cu_hist
 
     Returns (out [R, V], workspace).
     """
-    torch = _sv._torch()
     R, V = logits.shape
     B = cu_rows.numel() - 1
-    dev = logits.device
+    dev = _device("logits", logits)
     i32, f32 = torch.int32, torch.float32
-    _want("cu_rows", cu_rows, i32, 1, dev)
-    _want("history", history, i32, None, dev)
-    _want("cu_history", cu_history, i32, B + 1, dev)
-    _want("prompt_len", prompt_len, i32, B, dev)
-    _want("tokens", tokens, i32, R if parent is not None else None, dev)
-    _want("cu_tokens", cu_tokens, i32, B + 1, dev)
-    _want("parent", parent, i32, R, dev)
-    _want("repetition", repetition, f32, B, dev)
-    _want("frequency", frequency, f32, B, dev)
-    _want("presence", presence, f32, B, dev)
-    _want("bias_ids", bias_ids, i32, None, dev)
-    _want("bias_values", bias_values, f32, bias_ids.numel() if bias_ids is not None else None, dev)
-    _want("cu_bias", cu_bias, i32, B + 1, dev)
-    _want("mask_rows", mask_rows, i32, R, dev)
-    _want("out", out, logits.dtype, R * V, dev)
+    n_mask = 0
     if mask is not None:
-        _want("mask", mask, i32, None, dev)
-        if mask.dim() != 2 or mask.shape[1] != (V + 31) // 32:
+        n_mask, words = mask.shape
+        if words != (V + 31) // 32:
             raise ValueError(f"mask must be [n, {(V + 31) // 32}] int32 words")
-    ptr = _sv._ptr
-    rules = SpecLogitsRules(
-        ptr(history), ptr(cu_history), ptr(prompt_len), ptr(tokens), ptr(cu_tokens), ptr(parent),
-        ptr(repetition), ptr(frequency), ptr(presence), ptr(bias_ids), ptr(bias_values),
-        ptr(cu_bias), ptr(mask), ptr(mask_rows), 0 if mask is None else mask.shape[0])
+        if n_mask == 0 and mask_rows is not None:   # no row goes by a mask
+            mask = mask_rows = None
     # an empty list has no address: without entries the step is left out
-    for names in (("history", "cu_history", "prompt_len"), ("tokens", "cu_tokens", "parent"),
-                  ("bias_ids", "bias_values", "cu_bias")):
-        first = dict(history=history, tokens=tokens, bias_ids=bias_ids)[names[0]]
-        if first is not None and first.numel() == 0:
-            for n in names:
-                setattr(rules, n, None)
-    if mask is not None and mask.numel() == 0 and mask_rows is not None:
-        rules.mask = rules.mask_rows = None
-        rules.n_mask = 0
-    s, ctx = _begin(dev, stream, (logits, cu_rows, history, cu_history, prompt_len, tokens,
-                                  cu_tokens, parent, repetition, frequency, presence, bias_ids,
-                                  bias_values, cu_bias, mask, mask_rows, workspace, out))
-    with ctx:
-        ws = _sv._workspace(256, dev, workspace)
+    if history is not None and history.numel() == 0:
+        history = cu_history = prompt_len = None
+    if tokens is not None and tokens.numel() == 0:
+        tokens = cu_tokens = parent = None
+    if bias_ids is not None and bias_ids.numel() == 0:
+        bias_ids = bias_values = cu_bias = None
+    n_tokens = R if parent is not None else 0
+    n_bias = bias_ids.numel() if bias_ids is not None else 0
+    rules = _RULES.pack(
+        _arg("history", history, i32, 0, dev) or 0,
+        _arg("cu_history", cu_history, i32, B + 1, dev) or 0,
+        _arg("prompt_len", prompt_len, i32, B, dev) or 0,
+        _arg("tokens", tokens, i32, n_tokens, dev) or 0,
+        _arg("cu_tokens", cu_tokens, i32, B + 1, dev) or 0,
+        _arg("parent", parent, i32, R, dev) or 0,
+        _arg("repetition", repetition, f32, B, dev) or 0,
+        _arg("frequency", frequency, f32, B, dev) or 0,
+        _arg("presence", presence, f32, B, dev) or 0,
+        _arg("bias_ids", bias_ids, i32, 0, dev) or 0,
+        _arg("bias_values", bias_values, f32, n_bias, dev) or 0,
+        _arg("cu_bias", cu_bias, i32, B + 1, dev) or 0,
+        _arg("mask", mask, i32, 0, dev) or 0, _arg("mask_rows", mask_rows, i32, R, dev) or 0, n_mask)
+    with _Call(dev, stream, (logits, cu_rows, history, cu_history, prompt_len, tokens, cu_tokens,
+                             parent, repetition, frequency, presence, bias_ids, bias_values,
+                             cu_bias, mask, mask_rows, workspace, out)) as call:
+        ws, ws_at, ws_bytes = _scratch(256, dev, workspace)
         if out is None:
-            out = torch.empty_like(logits)
+            out = torch.empty_like(logits, memory_format=torch.contiguous_format)
         code = _sv.lib().spec_process_logits(
-            ptr(logits), _sv._dtype_code(logits), R, V, ptr(cu_rows), B, int(max_rows),
-            ctypes.byref(rules), ptr(out), ptr(ws), _bytes(ws), _sv._stream(s))
+            _arg("logits", logits, logits.dtype, 0, dev), _f32_or_bf16(logits), R, V,
+            _arg("cu_rows", cu_rows, i32, 1, dev), B, max_rows, rules,
+            _arg("out", out, logits.dtype, R * V, dev), ws_at, ws_bytes, call.raw)
     _sv._check(code, "spec_process_logits")
     return out, ws
 
@@ -169,33 +217,26 @@ def spec_distill_loss(target, draft, cu_draft, temperature=None, weight=None, *,
 
     Returns (loss [R_d] f32, grad [R_d, V] or None, workspace).
     """
-    torch = _sv._torch()
     R, V = draft.shape
     B = cu_draft.numel() - 1
-    dev = draft.device
-    if target.dtype != draft.dtype:
+    dev, dt, f32 = _device("draft", draft), draft.dtype, torch.float32
+    if target.dtype is not dt:
         raise TypeError("target and draft logits must have the same type")
     if target.shape[1] != V or target.shape[0] < R + B:
         raise ValueError(f"target must be [{R + B}, {V}] logits")
-    _want("target", target, draft.dtype, None, dev)
-    _want("cu_draft", cu_draft, torch.int32, 1, dev)
-    _want("temperature", temperature, torch.float32, B, dev)
-    _want("weight", weight, torch.float32, R, dev)
     loss, grad = (None, None) if out is None else out
-    _want("loss", loss, torch.float32, R, dev)
-    _want("grad", grad, draft.dtype, R * V, dev)
-    ptr = _sv._ptr
-    s, ctx = _begin(dev, stream, (target, draft, cu_draft, temperature, weight, workspace, loss,
-                                  grad))
-    with ctx:
-        ws = _sv._workspace(256, dev, workspace)
+    with _Call(dev, stream, (target, draft, cu_draft, temperature, weight, workspace, loss,
+                             grad)) as call:
+        ws, ws_at, ws_bytes = _scratch(256, dev, workspace)
         if out is None:
-            loss = torch.empty(R, dtype=torch.float32, device=dev)
-            grad = torch.empty_like(draft) if want_grad else None
+            loss = torch.empty(R, dtype=f32, device=draft.device)
+            grad = torch.empty_like(draft, memory_format=torch.contiguous_format) if want_grad else None
         code = _sv.lib().spec_distill_loss(
-            ptr(target), ptr(draft), _sv._dtype_code(draft), R, V, ptr(cu_draft), B,
-            ptr(temperature), ptr(weight), ptr(loss), ptr(grad), ptr(ws), _bytes(ws),
-            _sv._stream(s))
+            _arg("target", target, dt, 0, dev), _arg("draft", draft, dt, 0, dev),
+            _f32_or_bf16(draft), R, V, _arg("cu_draft", cu_draft, torch.int32, 1, dev), B,
+            _arg("temperature", temperature, f32, B, dev), _arg("weight", weight, f32, R, dev),
+            _arg("loss", loss, f32, R, dev), _arg("grad", grad, dt, R * V, dev), ws_at, ws_bytes,
+            call.raw)
     _sv._check(code, "spec_distill_loss")
     return loss, grad, ws
 
@@ -210,22 +251,21 @@ def spec_head_backward_workspace(M: int, N: int, K: int) -> int:
 
 
 def _head_sizes(x, weight):
-    torch = _sv._torch()
     M, K = x.shape
     N = weight.shape[0]
     if weight.shape[1] != K:
         raise ValueError(f"weight must be [N, {K}]")
-    _want("x", x, torch.bfloat16)
-    _want("weight", weight, torch.bfloat16, None, x.device)
     return M, N, K
 
 
-def _head_workspace(size, where, device, workspace):
+def _head_workspace(query, M, N, K, workspace):
+    """What a call without a workspace of its own has to allocate."""
     if workspace is not None:
-        return workspace
+        return 0
+    size = query(M, N, K)
     if size == 0:
-        raise _sv.SpecError(_sv.SPEC_ERR_INVALID_ARG, where)
-    return _sv._workspace(size, device)
+        raise _sv.SpecError(_sv.SPEC_ERR_INVALID_ARG, query.__name__)
+    return size
 
 
 def spec_head_forward(x, weight, bias=None, residual=None, *, act: int = SPEC_ACT_NONE,
@@ -236,25 +276,20 @@ def spec_head_forward(x, weight, bias=None, residual=None, *, act: int = SPEC_AC
 
     Returns (y [M, N], pre [M, N] or None, workspace).
     """
-    torch = _sv._torch()
     M, N, K = _head_sizes(x, weight)
-    dev, bf = x.device, torch.bfloat16
-    _want("bias", bias, bf, N, dev)
-    _want("residual", residual, bf, M * N, dev)
+    dev, bf = _device("x", x), torch.bfloat16
     y, pre = (None, None) if out is None else out
-    _want("y", y, bf, M * N, dev)
-    _want("pre", pre, bf, M * N, dev)
-    ptr = _sv._ptr
-    s, ctx = _begin(dev, stream, (x, weight, bias, residual, y, pre, workspace))
-    with ctx:
-        ws = _head_workspace(0 if workspace is not None else spec_head_forward_workspace(M, N, K),
-                             "spec_head_forward_workspace", dev, workspace)
+    with _Call(dev, stream, (x, weight, bias, residual, y, pre, workspace)) as call:
+        ws, ws_at, ws_bytes = _scratch(
+            _head_workspace(spec_head_forward_workspace, M, N, K, workspace), dev, workspace)
         if out is None:
-            y = torch.empty(M, N, dtype=bf, device=dev)
+            y = torch.empty(M, N, dtype=bf, device=x.device)
             pre = torch.empty_like(y) if want_pre else None
         code = _sv.lib().spec_head_forward(
-            ptr(x), ptr(weight), ptr(bias), ptr(residual), M, N, K, act, ptr(y), ptr(pre), ptr(ws),
-            _bytes(ws), _sv._stream(s))
+            _arg("x", x, bf, 0, dev), _arg("weight", weight, bf, 0, dev),
+            _arg("bias", bias, bf, N, dev), _arg("residual", residual, bf, M * N, dev), M, N, K,
+            act, _arg("y", y, bf, M * N, dev), _arg("pre", pre, bf, M * N, dev), ws_at, ws_bytes,
+            call.raw)
     _sv._check(code, "spec_head_forward")
     return y, pre, ws
 
@@ -268,29 +303,23 @@ def spec_head_backward(dy, x, weight, pre=None, *, act: int = SPEC_ACT_NONE, wan
     Returns (dx [M, K], dw [N, K], db [N] f32, workspace), None for what is
     not wanted.
     """
-    torch = _sv._torch()
     M, N, K = _head_sizes(x, weight)
-    dev, bf = x.device, torch.bfloat16
+    dev, bf = _device("x", x), torch.bfloat16
     if tuple(dy.shape) != (M, N):
         raise ValueError(f"dy must be [{M}, {N}]")
-    _want("dy", dy, bf, M * N, dev)
-    _want("pre", pre, bf, M * N, dev)
     dx, dw, db = (None, None, None) if out is None else out
-    _want("dx", dx, bf, M * K, dev)
-    _want("dw", dw, bf, N * K, dev)
-    _want("db", db, torch.float32, N, dev)
-    ptr = _sv._ptr
-    s, ctx = _begin(dev, stream, (dy, x, weight, pre, dx, dw, db, workspace))
-    with ctx:
-        ws = _head_workspace(0 if workspace is not None else spec_head_backward_workspace(M, N, K),
-                             "spec_head_backward_workspace", dev, workspace)
+    with _Call(dev, stream, (dy, x, weight, pre, dx, dw, db, workspace)) as call:
+        ws, ws_at, ws_bytes = _scratch(
+            _head_workspace(spec_head_backward_workspace, M, N, K, workspace), dev, workspace)
         if out is None:
-            dx = torch.empty(M, K, dtype=bf, device=dev) if want_dx else None
-            dw = torch.empty(N, K, dtype=bf, device=dev) if want_dw else None
-            db = torch.empty(N, dtype=torch.float32, device=dev) if want_db else None
+            dx = torch.empty(M, K, dtype=bf, device=x.device) if want_dx else None
+            dw = torch.empty(N, K, dtype=bf, device=x.device) if want_dw else None
+            db = torch.empty(N, dtype=torch.float32, device=x.device) if want_db else None
         code = _sv.lib().spec_head_backward(
-            ptr(dy), ptr(x), ptr(weight), ptr(pre), M, N, K, act, ptr(dx), ptr(dw), ptr(db), ptr(ws),
-            _bytes(ws), _sv._stream(s))
+            _arg("dy", dy, bf, M * N, dev), _arg("x", x, bf, 0, dev),
+            _arg("weight", weight, bf, 0, dev), _arg("pre", pre, bf, M * N, dev), M, N, K, act,
+            _arg("dx", dx, bf, M * K, dev), _arg("dw", dw, bf, N * K, dev),
+            _arg("db", db, torch.float32, N, dev), ws_at, ws_bytes, call.raw)
     _sv._check(code, "spec_head_backward")
     return dx, dw, db, ws
 
@@ -311,7 +340,6 @@ def spec_adamw_table(params, grads, exp_avg, exp_avg_sq, *, exp_avg_scale=None,
     scales, one per SPEC_ADAMW_BLOCK elements. `master` lists f32 copies of
     bf16 weights (entries may be None). The tensors' addresses must stay as
     they are while the table is used."""
-    torch = _sv._torch()
     n = len(params)
     if not (len(grads) == len(exp_avg) == len(exp_avg_sq) == n):
         raise ValueError("params, grads and states must be lists of the same length")
@@ -321,26 +349,28 @@ def spec_adamw_table(params, grads, exp_avg, exp_avg_sq, *, exp_avg_scale=None,
             raise ValueError(f"{name} must be a list of the same length")
     if n == 0:
         raise ValueError("no tensors")
-    dev = params[0].device
+    dev = _device("params[0]", params[0])
+    f32 = torch.float32
     codes = (torch.float8_e4m3fn, torch.uint8)
     bits = 8 if exp_avg[0].dtype in codes else 32
-    pick = lambda xs, i: None if xs is None else xs[i]   # noqa: E731
     rows = (SpecAdamwTensor * n)()
     for i in range(n):
-        p, g, m, v = params[i], grads[i], exp_avg[i], exp_avg_sq[i]
-        ms, vs, w = pick(exp_avg_scale, i), pick(exp_avg_sq_scale, i), pick(master, i)
+        p, m, v = params[i], exp_avg[i], exp_avg_sq[i]
+        ms = exp_avg_scale[i] if exp_avg_scale is not None else None
+        vs = exp_avg_sq_scale[i] if exp_avg_sq_scale is not None else None
+        w = master[i] if master is not None else None
         size = p.numel()
         blocks = -(-size // SPEC_ADAMW_BLOCK)
-        _want(f"grads[{i}]", g, p.dtype, size, dev)
         for name, s in (("exp_avg", m), ("exp_avg_sq", v)):
-            if s.dtype not in (codes if bits == 8 else (torch.float32,)):
+            if s.dtype not in (codes if bits == 8 else (f32,)):
                 raise TypeError(f"{name}[{i}] must hold states of {bits} bits, got {s.dtype}")
-            _want(f"{name}[{i}]", s, s.dtype, size, dev)
-        _want(f"exp_avg_scale[{i}]", ms, torch.float32, blocks, dev)
-        _want(f"exp_avg_sq_scale[{i}]", vs, torch.float32, blocks, dev)
-        _want(f"master[{i}]", w, torch.float32, size, dev)
-        rows[i] = SpecAdamwTensor(*(x if x is None else x.value for x in map(
-            _sv._ptr, (p, g, m, v, ms, vs, w))), size, _sv._dtype_code(p))
+        rows[i] = SpecAdamwTensor(
+            _arg(f"params[{i}]", p, p.dtype, 0, dev), _arg(f"grads[{i}]", grads[i], p.dtype, size, dev),
+            _arg(f"exp_avg[{i}]", m, m.dtype, size, dev),
+            _arg(f"exp_avg_sq[{i}]", v, v.dtype, size, dev),
+            _arg(f"exp_avg_scale[{i}]", ms, f32, blocks, dev),
+            _arg(f"exp_avg_sq_scale[{i}]", vs, f32, blocks, dev),
+            _arg(f"master[{i}]", w, f32, size, dev), size, _f32_or_bf16(p))
     L = _sv.lib()
     nbytes = L.spec_adamw_table_bytes(rows, n, bits)
     if nbytes == 0:
@@ -351,7 +381,7 @@ def spec_adamw_table(params, grads, exp_avg, exp_avg_sq, *, exp_avg_scale=None,
                "spec_adamw_table")
     keep = (list(params), list(grads), list(exp_avg), list(exp_avg_sq), exp_avg_scale,
             exp_avg_sq_scale, master)
-    return SpecAdamwTable(host.to(dev), items.value, bits, keep)
+    return SpecAdamwTable(host.to(params[0].device), items.value, bits, keep)
 
 
 def spec_adamw_step(table, step: int = 1, *, lr: float, beta1: float = 0.9, beta2: float = 0.999,
@@ -361,22 +391,17 @@ def spec_adamw_step(table, step: int = 1, *, lr: float, beta1: float = 0.9, beta
     `lr_dev` (f32) and `step_dev` (int32) are one-element device tensors read
     when the kernel runs. See include/specdraft.h for the semantics. Returns
     the workspace."""
-    torch = _sv._torch()
-    dev = table.data.device
-    _want("grad_scale", grad_scale, torch.float32, 1, dev)
-    _want("lr_dev", lr_dev, torch.float32, 1, dev)
-    _want("step_dev", step_dev, torch.int32, 1, dev)
-    ptr = _sv._ptr
-    hyper = SpecAdamwHyper(lr, beta1, beta2, eps, weight_decay, int(step), ptr(grad_scale),
-                           ptr(lr_dev), ptr(step_dev))
-    used = [table.data, grad_scale, lr_dev, step_dev, workspace]
-    if stream is not None:
-        used += [t for group in table.tensors if group is not None for t in group]
-    s, ctx = _begin(dev, stream, used)
-    with ctx:
-        ws = _sv._workspace(256, dev, workspace)
-        code = _sv.lib().spec_adamw_step(
-            ptr(table.data), table.n_items, table.state_bits, ctypes.byref(hyper), ptr(ws),
-            _bytes(ws), _sv._stream(s))
+    dev, f32 = table.data.get_device(), torch.float32
+    hyper = _HYPER.pack(lr, beta1, beta2, eps, weight_decay, step,
+                        _arg("grad_scale", grad_scale, f32, 1, dev) or 0,
+                        _arg("lr_dev", lr_dev, f32, 1, dev) or 0,
+                        _arg("step_dev", step_dev, torch.int32, 1, dev) or 0)
+    used = () if stream is None else (
+        table.data, grad_scale, lr_dev, step_dev, workspace,
+        *(t for group in table.tensors if group is not None for t in group))
+    with _Call(dev, stream, used) as call:
+        ws, ws_at, ws_bytes = _scratch(256, dev, workspace)
+        code = _sv.lib().spec_adamw_step(table.data.data_ptr(), table.n_items, table.state_bits,
+                                         hyper, ws_at, ws_bytes, call.raw)
     _sv._check(code, "spec_adamw_step")
     return ws
