@@ -1,14 +1,31 @@
 // The distillation loss of draft positions and its gradient
-// (spec_distill_loss of specdraft.h), one launch.
+// (spec_distill_loss of specdraft.h).
 //
-// A cluster of CTAs takes a position: its target row and its draft row,
-// each CTA one slice of both. The first pass keeps, per thread and with a
-// running maximum, S_t = sum 2^((z_t - m_t) c), S_d likewise and
-// A = sum 2^((z_t - m_t) c) (z_t - z_d), c = log2(e) / T. The CTAs exchange
-// those five numbers through distributed shared memory, and with them
+// Two passes over a position's target row and draft row. The first keeps, per
+// thread and with running maxima, S_t = sum 2^((z_t - m_t) c), S_d likewise and
+// A = sum 2^((z_t - m_t) c) (z_t - z_d), c = log2(e) / T. Merged over the row,
 //   KL = ln 2 (A c / S_t - (m_t - m_d) c - log2 S_t + log2 S_d)
-// and the second pass writes (w / T) (q - p). It reads the slices again, from
-// L2: a position's two rows are far smaller than it.
+// and the second pass writes (w / T) (q - p).
+//
+// Resident schedule (k_distill_setup, k_distill_resident), for calls that fill
+// the SMs: a persistent cluster takes one position after another, each CTA a
+// slice of both rows. A producer lane feeds a ring of pieces by bulk copies; the
+// consumer warps take a row's pieces for the first pass, leave them in shared
+// memory, and come back to them for the second, which frees them. Between the
+// two they work on the first pieces of the next row, while one warp merges the
+// statistics and exchanges them with the other CTAs through distributed shared
+// memory (in every consumer warp that cost a third of the instructions), and HBM
+// and L2 see each logit once. Issue slots bound it: 17 to 20 per pair of logits.
+//
+// Other calls (few positions, rows that bulk copies cannot address or a cluster
+// cannot hold) run as one launch with a cluster per position (k_distill): each
+// CTA passes over its slice twice, the second time from L2.
+//
+// Measured at 4096 positions of 201088 bf16 logits, 3/4 of them weighted: 0.81 ms
+// (5.1 TB/s of the bytes that have to move); a cluster per position 1.06 ms (1.18 ms with its slices in shared memory but no
+// overlap of positions); persistent CTAs whose second-pass units follow the
+// first-pass units of later rows 1.04 to 1.8 ms, as L2 does not hold the rows
+// between the two.
 #include "draft.cuh"
 
 #include <cooperative_groups.h>
@@ -22,6 +39,17 @@ namespace cg = cooperative_groups;
 
 constexpr int DI_THREADS = 256;
 constexpr int DI_MAX_CLUSTER = 8;
+// resident schedule
+constexpr int DR_WARPS = 16;               // consumer warps of a CTA, after a producer and a merging warp
+constexpr int DR_THREADS = 32 * (2 + DR_WARPS);
+constexpr int DR_VECS = 2;                 // 16-byte vectors of a piece per consumer thread and row
+constexpr int DR_PV = 32 * DR_WARPS * DR_VECS;
+constexpr int DR_PIECE = DR_PV * 16;       // bytes of each row in a ring slot
+constexpr int DR_SLOTS = 6;                // 192 KB
+constexpr int DR_AHEAD = 1;                // pieces of the next row between a row's two passes, at least
+constexpr int DR_MAX_CLUSTER = 8;
+// calls whose rows hold less than this run as a cluster per position
+constexpr long long DR_MIN_BYTES = 32ll << 20;
 
 struct DistillArgs {
   const void *target, *draft;
@@ -34,63 +62,193 @@ struct DistillArgs {
 };
 
 // Statistics of part of a row pair.
-struct PairStat {
+struct __align__(16) PairStat {
   float mt, St, A, md, Sd;
 };
 
-__device__ __forceinline__ void merge_pair(PairStat &x, const PairStat &y, float c) {
-  const float M = fmaxf(x.mt, y.mt), D = fmaxf(x.md, y.md);
-  const float f1 = ex2((x.mt - M) * c), f2 = ex2((y.mt - M) * c);
-  const float g1 = ex2((x.md - D) * c), g2 = ex2((y.md - D) * c);
-  // an infinite A (a draft probability of 0) stays infinite
-  const float a1 = isinf(x.A) ? x.A : x.A * f1, a2 = isinf(y.A) ? y.A : y.A * f2;
-  x.St = x.St * f1 + y.St * f2;
-  x.A = a1 + a2;
-  x.Sd = x.Sd * g1 + y.Sd * g2;
-  x.mt = M;
-  x.md = D;
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
+__device__ __forceinline__ f32x2 ex2_2(f32x2 x) { return pk2(ex2(lo2(x)), ex2(hi2(x))); }
 
-__device__ __forceinline__ PairStat shfl_pair(const PairStat &x, int o) {
-  return PairStat{__shfl_xor_sync(~0u, x.mt, o), __shfl_xor_sync(~0u, x.St, o),
-                  __shfl_xor_sync(~0u, x.A, o), __shfl_xor_sync(~0u, x.md, o),
-                  __shfl_xor_sync(~0u, x.Sd, o)};
-}
-
-// VEC elements of a row as f32: 16 bytes, or one element.
-template <bool BF16, int VEC>
-__device__ __forceinline__ void load_vec(const char *row, int i, float *z) {
-  if (VEC == 8) {
-    const uint4 w = GLD(reinterpret_cast<const uint4 *>(row) + i);
-    z[0] = bf16lo(w.x); z[1 % VEC] = bf16hi(w.x);
-    z[2 % VEC] = bf16lo(w.y); z[3 % VEC] = bf16hi(w.y);
-    z[4 % VEC] = bf16lo(w.z); z[5 % VEC] = bf16hi(w.z);
-    z[6 % VEC] = bf16lo(w.w); z[7 % VEC] = bf16hi(w.w);
-  } else if (VEC == 4) {
-    const uint4 w = GLD(reinterpret_cast<const uint4 *>(row) + i);
-    z[0] = __uint_as_float(w.x); z[1 % VEC] = __uint_as_float(w.y);
-    z[2 % VEC] = __uint_as_float(w.z); z[3 % VEC] = __uint_as_float(w.w);
-  } else if (BF16) {
-    z[0] = bf16_bits_to_f32(GLD(reinterpret_cast<const uint16_t *>(row) + i));
+// 16 bytes of a row less m, as packed f32 pairs: 8 bf16 (the subtraction widens
+// them) or 4 f32.
+template <bool BF16>
+__device__ __forceinline__ void minus16(const uint4 &w, float m, f32x2 *x) {
+  if (BF16) {
+    x[0] = bsub2(w.x, m), x[1] = bsub2(w.y, m), x[2] = bsub2(w.z, m), x[3] = bsub2(w.w, m);
   } else {
-    z[0] = GLD(reinterpret_cast<const float *>(row) + i);
+    const f32x2 n = pk2(-m, -m);
+    x[0] = add2(pk2(__uint_as_float(w.x), __uint_as_float(w.y)), n);
+    x[1] = add2(pk2(__uint_as_float(w.z), __uint_as_float(w.w)), n);
+  }
+}
+// The largest of K vectors of a row.
+template <bool BF16, int K>
+__device__ __forceinline__ float max16(const uint4 *w) {
+  if (BF16) {
+    uint32_t m = bmax2(bmax2(w[0].x, w[0].y), bmax2(w[0].z, w[0].w));
+#pragma unroll
+    for (int k = 1; k < K; ++k) m = bmax2(m, bmax2(bmax2(w[k].x, w[k].y), bmax2(w[k].z, w[k].w)));
+    return fmaxf(bf16lo(m), bf16hi(m));
+  }
+  float m = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(w[k].x), __uint_as_float(w[k].y)),
+                       fmaxf(__uint_as_float(w[k].z), __uint_as_float(w[k].w))));
+  return m;
+}
+template <bool BF16>
+__device__ __forceinline__ uint4 pack16(const f32x2 *g) {
+  if (BF16)
+    return make_uint4(f32x2_to_bf16x2(lo2(g[0]), hi2(g[0])), f32x2_to_bf16x2(lo2(g[1]), hi2(g[1])),
+                      f32x2_to_bf16x2(lo2(g[2]), hi2(g[2])), f32x2_to_bf16x2(lo2(g[3]), hi2(g[3])));
+  return make_uint4(__float_as_uint(lo2(g[0])), __float_as_uint(hi2(g[0])), __float_as_uint(lo2(g[1])),
+                    __float_as_uint(hi2(g[1])));
+}
+template <bool BF16>
+__device__ __forceinline__ float load1(const char *row, int i) {
+  return BF16 ? bf16_bits_to_f32(GLD(reinterpret_cast<const uint16_t *>(row) + i))
+              : GLD(reinterpret_cast<const float *>(row) + i);
+}
+template <bool BF16>
+__device__ __forceinline__ void store1(char *row, int i, float g) {
+  if (BF16) GST(reinterpret_cast<uint16_t *>(row) + i, (uint16_t)f32_to_bf16_bits(g));
+  else GST(reinterpret_cast<float *>(row) + i, g);
+}
+
+// 2 N elements of both rows, DI_THREADS apart; -inf behind the row's end.
+template <bool BF16, int N>
+__device__ __forceinline__ void load_scalars(const char *trow, const char *drow, int i0, int end, f32x2 *zt,
+                                             f32x2 *zd) {
+  float xt[2 * N], xd[2 * N];
+#pragma unroll
+  for (int j = 0; j < 2 * N; ++j) {
+    const int i = i0 + j * DI_THREADS;
+    xt[j] = i < end ? load1<BF16>(trow, i) : -INFINITY;
+    xd[j] = i < end ? load1<BF16>(drow, i) : -INFINITY;
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) zt[j] = pk2(xt[2 * j], xt[2 * j + 1]), zd[j] = pk2(xd[2 * j], xd[2 * j + 1]);
+}
+
+// The thread's maxima become at least mt and md. s.A is kept as the sum of
+// e_t ((z_t - m_t) - (z_d - m_d)) at the thread's own maxima.
+__device__ __forceinline__ void raise(PairStat &s, float mt, float md, float c) {
+  if (mt > s.mt || md > s.md) {
+    const float Mt = fmaxf(mt, s.mt), Md = fmaxf(md, s.md);
+    const float f = ex2((s.mt - Mt) * c);
+    // an infinite A (a draft probability of 0) stays infinite
+    if (!isinf(s.A)) s.A = f * (s.A + s.St * ((Md - s.md) - (Mt - s.mt)));
+    s.St *= f;
+    s.Sd *= ex2((s.md - Md) * c);
+    s.mt = Mt, s.md = Md;
   }
 }
 
-template <bool BF16, int VEC>
-__device__ __forceinline__ void store_vec(char *row, int i, const float *g) {
-  if (VEC == 8) {
-    GST(reinterpret_cast<uint4 *>(row) + i,
-        make_uint4(f32x2_to_bf16x2(g[0], g[1 % VEC]), f32x2_to_bf16x2(g[2 % VEC], g[3 % VEC]),
-                   f32x2_to_bf16x2(g[4 % VEC], g[5 % VEC]), f32x2_to_bf16x2(g[6 % VEC], g[7 % VEC])));
-  } else if (VEC == 4) {
-    GST(reinterpret_cast<float4 *>(row) + i,
-        make_float4(g[0], g[1 % VEC], g[2 % VEC], g[3 % VEC]));
-  } else if (BF16) {
-    GST(reinterpret_cast<uint16_t *>(row) + i, (uint16_t)f32_to_bf16_bits(g[0]));
-  } else {
-    GST(reinterpret_cast<float *>(row) + i, g[0]);
+// 2 N elements, less the maxima, into the sums.
+template <int N>
+__device__ __forceinline__ void add_pairs(PairStat &s, const f32x2 *xt, const f32x2 *xd, float c) {
+  const f32x2 cc = pk2(c, c), minus = pk2(-1.f, -1.f);
+  f32x2 St = 0, Sd = 0, A = 0;   // pairs of +0
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const f32x2 et = ex2_2(mul2(xt[j], cc)), ed = ex2_2(mul2(xd[j], cc));
+    St = add2(St, et);
+    Sd = add2(Sd, ed);
+    A = fma2(et, fma2(xd[j], minus, xt[j]), A);
   }
+  s.St += lo2(St) + hi2(St);
+  s.Sd += lo2(Sd) + hi2(Sd);
+  float a = lo2(A) + hi2(A);
+  if (isnan(a)) {   // tokens that are -inf take no part where 2^(z_t) is 0
+    a = 0.f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const f32x2 et = ex2_2(mul2(xt[j], cc));
+      if (lo2(et) > 0.f) a += lo2(et) * (lo2(xt[j]) - lo2(xd[j]));
+      if (hi2(et) > 0.f) a += hi2(et) * (hi2(xt[j]) - hi2(xd[j]));
+    }
+  }
+  s.A += a;
+}
+
+// K vectors of both rows into a thread's statistics.
+template <bool BF16, int K>
+__device__ __forceinline__ void add_stats(PairStat &s, const uint4 *wt, const uint4 *wd, float c) {
+  constexpr int N = BF16 ? 4 : 2;
+  raise(s, max16<BF16, K>(wt), max16<BF16, K>(wd), c);
+  f32x2 xt[N * K], xd[N * K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) minus16<BF16>(wt[k], s.mt, xt + N * k), minus16<BF16>(wd[k], s.md, xd + N * k);
+  add_pairs<N * K>(s, xt, xd, c);
+}
+// 2 N elements of both rows.
+template <int N>
+__device__ __forceinline__ void add_stats(PairStat &s, const f32x2 *zt, const f32x2 *zd, float c) {
+  float mt = fmaxf(lo2(zt[0]), hi2(zt[0])), md = fmaxf(lo2(zd[0]), hi2(zd[0]));
+#pragma unroll
+  for (int j = 1; j < N; ++j) {
+    mt = fmaxf(mt, fmaxf(lo2(zt[j]), hi2(zt[j])));
+    md = fmaxf(md, fmaxf(lo2(zd[j]), hi2(zd[j])));
+  }
+  raise(s, mt, md, c);
+  const f32x2 nt = pk2(-s.mt, -s.mt), nd = pk2(-s.md, -s.md);
+  f32x2 xt[N], xd[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) xt[j] = add2(zt[j], nt), xd[j] = add2(zd[j], nd);
+  add_pairs<N>(s, xt, xd, c);
+}
+
+// The gradient's scalars: g = kd 2^((z_d - m_d) c) - kt 2^((z_t - m_t) c), kd = w / (T S_d)
+// and kt = w / (T S_t).
+struct GradK {
+  float mt, md;
+  f32x2 c, kt, kd;   // kt with its sign turned
+};
+__device__ __forceinline__ GradK grad_of(const PairStat &s, float c, float k) {
+  const float kt = -k / s.St, kd = k / s.Sd;
+  return GradK{s.mt, s.md, pk2(c, c), pk2(kt, kt), pk2(kd, kd)};
+}
+template <int N>
+__device__ __forceinline__ void gradient(const GradK &g, const f32x2 *xt, const f32x2 *xd, f32x2 *out) {
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    out[j] = fma2(ex2_2(mul2(xt[j], g.c)), g.kt, mul2(ex2_2(mul2(xd[j], g.c)), g.kd));
+}
+
+// The warp's statistics in every lane: sums at the warp's maxima, added in a
+// butterfly.
+__device__ __forceinline__ void warp_merge(PairStat &s, float c) {
+  float M = s.mt, D = s.md;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+    D = fmaxf(D, __shfl_xor_sync(~0u, D, o));
+  }
+  const float f = ex2((s.mt - M) * c);
+  s.St *= f;
+  if (!isinf(s.A)) s.A *= f;
+  s.Sd *= ex2((s.md - D) * c);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s.St += __shfl_xor_sync(~0u, s.St, o);
+    s.A += __shfl_xor_sync(~0u, s.A, o);
+    s.Sd += __shfl_xor_sync(~0u, s.Sd, o);
+  }
+  s.mt = M;
+  s.md = D;
+}
+
+__device__ __forceinline__ float loss_of(const PairStat &s, float c, float w) {
+  // in 64 bits: the terms are larger than their sum
+  const double kl = 0.693147180559945309 *
+                    ((double)s.A / (double)s.St * c - ((double)s.mt - (double)s.md) * c -
+                     (double)log2f(s.St) + (double)log2f(s.Sd));
+  return (float)((double)w * kl);
 }
 
 // The request of position r: cu[b] <= r < cu[b + 1], found by the block in
@@ -117,7 +275,8 @@ __device__ int find_request(const int32_t *cu, int B, int r, int *slot) {
   return -1;
 }
 
-template <bool BF16, int VEC>
+// A cluster per position. VEC: the rows are 16-byte aligned.
+template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(DI_THREADS) k_distill(DistillArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -126,7 +285,7 @@ __global__ void __launch_bounds__(DI_THREADS) k_distill(DistillArgs a) {
   __shared__ PairStat s_cta;     // this CTA's statistics, read by its peers
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int r = blockIdx.x / C;
-  constexpr int ES = BF16 ? 2 : 4;
+  constexpr int ES = BF16 ? 2 : 4, PER = 16 / ES, N = PER / 2;
 
   if (blockIdx.x == 0) {   // the offsets and temperatures, once per call
     bool bad = false;
@@ -140,97 +299,421 @@ __global__ void __launch_bounds__(DI_THREADS) k_distill(DistillArgs a) {
     }
     if (bad) set_status(a.hdr, SPEC_ERR_INVALID_ARG, 0);
   }
-  const int b = find_request(a.cu, a.B, r, &s_slot);
   float w = a.weight ? GLD(a.weight + r) : 1.f;
-  float T = a.temp && b >= 0 ? GLD(a.temp + b) : 1.f;
-  if (b < 0 || !isfinite(w) || !(T >= 0.f) || !isfinite(T)) {
+  // this CTA's part of the row, in units of 16 bytes or of elements
+  const int units = VEC ? a.V / PER : a.V;
+  const int u0 = (int)((long long)units * rank / C), u1 = (int)((long long)units * (rank + 1) / C);
+  char *grow = a.grad ? static_cast<char *>(a.grad) + (long long)r * a.V * ES : nullptr;
+  const int b = w != 0.f ? find_request(a.cu, a.B, r, &s_slot) : 0;
+  const float T0 = a.temp && b >= 0 && w != 0.f ? GLD(a.temp + b) : 1.f;
+  if (b < 0 || !isfinite(w) || !(T0 >= 0.f) || !isfinite(T0)) {
     if (t == 0) set_status(a.hdr, SPEC_ERR_INVALID_ARG, r);
     w = 0.f;
   }
-  if (T < SPEC_GREEDY_T) T = 1.f;
-  const int nvec = a.V / VEC;   // VEC > 1 only where V is a multiple of it
-  const int v0 = (int)((long long)nvec * rank / C), v1 = (int)((long long)nvec * (rank + 1) / C);
-  char *grow = a.grad ? static_cast<char *>(a.grad) + (long long)r * a.V * ES : nullptr;
   if (w == 0.f) {   // the whole cluster leaves: nobody waits for its statistics
     if (rank == 0 && t == 0) GST(a.loss + r, 0.f);
     if (grow != nullptr) {
-      float z[VEC] = {};
-      for (int i = v0 + t; i < v1; i += DI_THREADS) store_vec<BF16, VEC>(grow, i, z);
+      for (int i = u0 + t; i < u1; i += DI_THREADS) {
+        if (VEC) GST(reinterpret_cast<uint4 *>(grow) + i, make_uint4(0, 0, 0, 0));
+        else store1<BF16>(grow, i, 0.f);
+      }
     }
     return;
   }
+  const float T = T0 < SPEC_GREEDY_T ? 1.f : T0;
   const float c = LOG2E / T;
   const char *trow = static_cast<const char *>(a.target) + (long long)(r + b) * a.V * ES;
   const char *drow = static_cast<const char *>(a.draft) + (long long)r * a.V * ES;
-
   PairStat s{NO_MAX, 0.f, 0.f, NO_MAX, 0.f};
-  for (int i = v0 + t; i < v1; i += DI_THREADS) {
-    float zt[VEC], zd[VEC];
-    load_vec<BF16, VEC>(trow, i, zt);
-    load_vec<BF16, VEC>(drow, i, zd);
-    float mt = zt[0], md = zd[0];
-#pragma unroll
-    for (int j = 1; j < VEC; ++j) mt = fmaxf(mt, zt[j]), md = fmaxf(md, zd[j]);
-    if (mt > s.mt) {
-      const float f = ex2((s.mt - mt) * c);
-      s.St *= f;
-      if (!isinf(s.A)) s.A *= f;
-      s.mt = mt;
+  if (VEC) {
+    for (int i = u0 + t; i < u1; i += DI_THREADS) {
+      const uint4 wt = GLD(reinterpret_cast<const uint4 *>(trow) + i);
+      const uint4 wd = GLD(reinterpret_cast<const uint4 *>(drow) + i);
+      add_stats<BF16, 1>(s, &wt, &wd, c);
     }
-    if (md > s.md) {
-      s.Sd *= ex2((s.md - md) * c);
-      s.md = md;
-    }
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const float e = ex2((zt[j] - s.mt) * c);
-      s.St += e;
-      s.A += e > 0.f ? e * (zt[j] - zd[j]) : 0.f;   // -inf in both rows: no part
-      s.Sd += ex2((zd[j] - s.md) * c);
+  } else {
+    for (int i = u0 + t; i < u1; i += 8 * DI_THREADS) {
+      f32x2 zt[4], zd[4];
+      load_scalars<BF16, 4>(trow, drow, i, u1, zt, zd);
+      add_stats<4>(s, zt, zd, c);
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) merge_pair(s, shfl_pair(s, o), c);
+  s.A += s.St * (s.mt - s.md);
+  warp_merge(s, c);
   if (lane == 0) s_part[warp] = s;
   __syncthreads();
   if (warp == 0) {
     s = lane < DI_THREADS / 32 ? s_part[lane] : PairStat{NO_MAX, 0.f, 0.f, NO_MAX, 0.f};
-#pragma unroll
-    for (int o = DI_THREADS / 64; o > 0; o >>= 1) merge_pair(s, shfl_pair(s, o), c);
+    warp_merge(s, c);
     if (lane == 0) s_cta = s;
   }
   cluster.sync();
-  // every thread merges the CTAs' statistics in rank order: the same bits
-  // everywhere
-  s = *cluster.map_shared_rank(&s_cta, 0);
-  for (int k = 1; k < C; ++k) merge_pair(s, *cluster.map_shared_rank(&s_cta, k), c);
-  cluster.sync();   // no CTA leaves while a peer may still read its statistics
+  // every warp merges the CTAs' statistics, a lane each, in the same order:
+  // the same bits everywhere
+  s = lane < C ? *cluster.map_shared_rank(&s_cta, lane) : PairStat{NO_MAX, 0.f, 0.f, NO_MAX, 0.f};
+  warp_merge(s, c);
 
   const bool empty = row_empty(s.mt) || row_empty(s.md);
   if (rank == 0 && t == 0) {
     if (empty) set_status(a.hdr, SPEC_ERR_INVALID_ARG, r);
-    // in 64 bits: the terms are larger than their sum
-    const double kl = 0.693147180559945309 *
-                      ((double)s.A / (double)s.St * c - ((double)s.mt - (double)s.md) * c -
-                       (double)log2f(s.St) + (double)log2f(s.Sd));
-    GST(a.loss + r, empty ? 0.f : (float)((double)w * kl));
+    GST(a.loss + r, empty ? 0.f : loss_of(s, c, w));
   }
-  if (grow == nullptr) return;
-  const float k = empty ? 0.f : w / T, lt = log2f(s.St), ld = log2f(s.Sd);
-  for (int i = v0 + t; i < v1; i += DI_THREADS) {
-    float zt[VEC], zd[VEC];
-    load_vec<BF16, VEC>(trow, i, zt);
-    load_vec<BF16, VEC>(drow, i, zd);
+  if (grow != nullptr) {
+    const GradK g = grad_of(s, c, w / T);
+    if (VEC) {
+      for (int i = u0 + t; i < u1; i += DI_THREADS) {
+        f32x2 xt[N], xd[N], o[N];
+        minus16<BF16>(GLD(reinterpret_cast<const uint4 *>(trow) + i), g.mt, xt);
+        minus16<BF16>(GLD(reinterpret_cast<const uint4 *>(drow) + i), g.md, xd);
+        gradient<N>(g, xt, xd, o);
+        GST(reinterpret_cast<uint4 *>(grow) + i, empty ? make_uint4(0, 0, 0, 0) : pack16<BF16>(o));
+      }
+    } else {
+      for (int i = u0 + t; i < u1; i += 8 * DI_THREADS) {
+        f32x2 xt[4], xd[4], o[4];
+        load_scalars<BF16, 4>(trow, drow, i, u1, xt, xd);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const float p = ex2(fmaf(zt[j] - s.mt, c, -lt)), q = ex2(fmaf(zd[j] - s.md, c, -ld));
-      zd[j] = empty ? 0.f : k * (q - p);
+        for (int j = 0; j < 4; ++j) xt[j] = add2(xt[j], pk2(-g.mt, -g.mt)), xd[j] = add2(xd[j], pk2(-g.md, -g.md));
+        gradient<4>(g, xt, xd, o);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int e = i + j * DI_THREADS;
+          if (e < u1) store1<BF16>(grow, e, empty ? 0.f : j & 1 ? hi2(o[j / 2]) : lo2(o[j / 2]));
+        }
+      }
     }
-    store_vec<BF16, VEC>(grow, i, zd);
+  }
+  cluster.sync();   // no CTA leaves while a peer may still read its statistics
+}
+
+// ------------------------------------------------------- resident schedule
+struct RowInfo {       // a weighted position, by the setup
+  int r, trow;         // position, target row
+  float c, k, w;       // log2(e) / T, w / T, w
+  int pad[3];
+};
+struct ResidentArgs {
+  DistillArgs d;
+  RowInfo *info;       // [R] weighted positions (hdr->n_list of them, any order)
+  int *zero;           // [R] positions of weight 0 (hdr->n_jobs_a)
+};
+
+__global__ void __launch_bounds__(256) k_distill_setup(ResidentArgs a) {
+  const DistillArgs &d = a.d;
+  const int g = blockIdx.x * blockDim.x + threadIdx.x;
+  for (int i = g; i < d.B; i += gridDim.x * blockDim.x) {
+    const int x = GLD(d.cu + i), y = GLD(d.cu + i + 1);
+    bool bad = y < x || (i == 0 && x != 0) || (i == d.B - 1 && y != d.R);
+    if (d.temp != nullptr) {
+      const float T = GLD(d.temp + i);
+      bad |= !(T >= 0.f) || !isfinite(T);
+    }
+    if (bad) set_status(d.hdr, SPEC_ERR_INVALID_ARG, i);
+  }
+  if (g >= d.R) return;
+  const float w = d.weight ? GLD(d.weight + g) : 1.f;
+  if (w != 0.f) {
+    int lo = 0, hi = d.B;   // the last request that starts at or before g
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (GLD(d.cu + mid) <= g) lo = mid;
+      else hi = mid;
+    }
+    const float T0 = d.temp ? GLD(d.temp + lo) : 1.f;
+    if (GLD(d.cu + lo) <= g && g < GLD(d.cu + lo + 1) && isfinite(w) && T0 >= 0.f && isfinite(T0)) {
+      const float T = T0 < SPEC_GREEDY_T ? 1.f : T0;
+      GST(a.info + atomicAdd(&d.hdr->n_list, 1), RowInfo{g, g + lo, LOG2E / T, w / T, w, {0, 0, 0}});
+      return;
+    }
+    set_status(d.hdr, SPEC_ERR_INVALID_ARG, g);
+  }
+  GST(d.loss + g, 0.f);
+  GST(a.zero + atomicAdd(&d.hdr->n_jobs_a, 1), g);
+}
+
+__device__ __forceinline__ uint32_t peer_addr(const void *local, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(local)), "r"(rank));
+  return r;
+}
+// Bounded wait for a phase that the cluster's arrivals complete.
+__device__ __forceinline__ bool cluster_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  const unsigned long long t0 = global_ns();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (*abort || global_ns() - t0 > WAIT_NS) return false;
   }
 }
 
-template <bool BF16, int VEC>
+template <bool BF16>
+__global__ void __launch_bounds__(DR_THREADS, 1) k_distill_resident(ResidentArgs a) {
+  constexpr int PER = BF16 ? 8 : 4, N = PER / 2;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int cid = blockIdx.x / C, ncl = gridDim.x / C;
+  extern __shared__ __align__(128) uint8_t ring[];   // DR_SLOTS x (target piece, draft piece)
+  __shared__ uint64_t s_full[DR_SLOTS], s_empty[DR_SLOTS];
+  __shared__ uint64_t s_parts[2], s_xch[2], s_known[2];   // by the parity of the row
+  __shared__ PairStat s_part[2][DR_WARPS];      // the warps' statistics
+  __shared__ PairStat s_stat[2][DR_MAX_CLUSTER];   // the CTAs', written by the peers
+  __shared__ GradK s_grad[2];                   // the row's law, by the merging warp
+  __shared__ int s_none[2];                     // the row holds no finite logit
+  __shared__ RowInfo s_row[16];                 // the rows in the ring, DR_SLOTS at most
+  __shared__ int s_abort;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const DistillArgs &d = a.d;
+  const int vecs = d.V / PER;   // of a row
+  const int u0 = (int)((long long)vecs * rank / C), u1 = (int)((long long)vecs * (rank + 1) / C);
+  const int P = (u1 - u0 + DR_PV - 1) / DR_PV;   // pieces of this slice
+  const int rows = d.hdr->n_list;
+  const int mine = rows > cid ? (rows - cid + ncl - 1) / ncl : 0;   // of this cluster
+  if (t == 0) {
+    s_abort = 0;
+    for (int i = 0; i < DR_SLOTS; ++i) mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], DR_WARPS);
+    for (int i = 0; i < 2; ++i) mbar_init(&s_parts[i], DR_WARPS), mbar_init(&s_xch[i], C), mbar_init(&s_known[i], 1);
+    fence_mbar_init();
+  }
+  cluster.sync();   // barriers initialised everywhere before any remote arrival
+
+  if (warp == 0) {
+    if (lane == 0) {
+      bool ok = true;
+      int it = 0;   // pieces handed out
+      RowInfo next = cid < rows ? GLD(a.info + cid) : RowInfo{};
+      for (int i = cid, k = 0; i < rows && ok; i += ncl, ++k) {
+        const RowInfo x = next;
+        if (i + ncl < rows) next = GLD(a.info + i + ncl);   // on its way during this row
+        const char *trow = static_cast<const char *>(d.target) + ((long long)x.trow * vecs + u0) * 16;
+        const char *drow = static_cast<const char *>(d.draft) + ((long long)x.r * vecs + u0) * 16;
+        for (int p = 0; p < P; ++p, ++it) {
+          const int st = it % DR_SLOTS;
+          if (it >= DR_SLOTS && !mbar_wait_bounded(&s_empty[st], (it / DR_SLOTS - 1) & 1, &s_abort)) {
+            ok = false;
+            break;
+          }
+          if (p == 0) s_row[k & 15] = x;
+          const int len = min(DR_PV, u1 - u0 - p * DR_PV) * 16;
+          uint8_t *dst = ring + st * 2 * DR_PIECE;
+          mbar_arrive_tx(&s_full[st], 2 * len);
+          bulk_g2s(dst, trow + (long long)p * DR_PIECE, len, &s_full[st]);
+          bulk_g2s(dst + DR_PIECE, drow + (long long)p * DR_PIECE, len, &s_full[st]);
+        }
+      }
+      if (!ok) {
+        s_abort = 1;
+        set_status(d.hdr, SPEC_ERR_TIMEOUT, 0);
+        int never = 0;   // its copies in flight land before the CTA leaves
+        for (int k = max(0, it - DR_SLOTS); k < it; ++k)
+          mbar_wait_bounded(&s_full[k % DR_SLOTS], (k / DR_SLOTS) & 1, &never);
+      }
+    }
+  } else if (warp == 1) {
+    // the warps' statistics of a row, then the CTAs', then the row's law
+    for (int k = 0; k < mine; ++k) {
+      const int y = k & 1, par = (k >> 1) & 1;
+      bool ok = __all_sync(~0u, mbar_wait_bounded(&s_parts[y], par, &s_abort));
+      const RowInfo x = s_row[k & 15];
+      if (ok) {
+        PairStat s = lane < DR_WARPS ? s_part[y][lane] : PairStat{NO_MAX, 0.f, 0.f, NO_MAX, 0.f};
+        warp_merge(s, x.c);
+        if (lane < C) {
+          const uint32_t to = peer_addr(&s_stat[y][rank], lane);
+          asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(s.mt), "f"(s.St),
+                       "f"(s.A), "f"(s.md)
+                       : "memory");
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 16), "f"(s.Sd) : "memory");
+          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                           peer_addr(&s_xch[y], lane))
+                       : "memory");
+        }
+        ok = __all_sync(~0u, cluster_wait(&s_xch[y], par, &s_abort));
+      }
+      if (!ok) {
+        s_abort = 1;
+        if (lane == 0) set_status(d.hdr, SPEC_ERR_TIMEOUT, 2);
+        break;
+      }
+      PairStat z = lane < C ? s_stat[y][lane] : PairStat{NO_MAX, 0.f, 0.f, NO_MAX, 0.f};
+      warp_merge(z, x.c);   // the same bits in every CTA of the cluster
+      if (lane == 0) {
+        const bool none = row_empty(z.mt) || row_empty(z.md);
+        s_none[y] = none;
+        s_grad[y] = grad_of(z, x.c, x.k);
+        mbar_arrive(&s_known[y]);
+        if (rank == 0) {
+          if (none) set_status(d.hdr, SPEC_ERR_INVALID_ARG, x.r);
+          GST(d.loss + x.r, none ? 0.f : loss_of(z, x.c, x.w));
+        }
+      }
+      __syncwarp();
+    }
+  } else {
+    const int ct = t - 64, cw = warp - 2;
+    bool ok = true;
+    auto give_up = [&](int where) {
+      ok = false;
+      s_abort = 1;
+      if (lane == 0) set_status(d.hdr, SPEC_ERR_TIMEOUT, where);
+    };
+    PairStat s{NO_MAX, 0.f, 0.f, NO_MAX, 0.f};
+    // the first pass over pieces p0 .. p1-1 of this cluster's k-th row
+    auto first_pass = [&](int k, int p0, int p1) {
+      float c = 0.f;
+      for (int p = p0; p < p1 && ok; ++p) {
+        const int it = k * P + p, st = it % DR_SLOTS;
+        if (!__all_sync(~0u, mbar_wait_bounded(&s_full[st], (it / DR_SLOTS) & 1, &s_abort))) return give_up(1);
+        c = s_row[k & 15].c;
+        const uint8_t *at = ring + st * 2 * DR_PIECE;
+        const int left = u1 - u0 - p * DR_PV;   // vectors of this piece
+        uint4 wt[DR_VECS], wd[DR_VECS];
+        if (left >= DR_PV) {
+#pragma unroll
+          for (int j = 0; j < DR_VECS; ++j) {
+            wt[j] = lds128(at + (j * 32 * DR_WARPS + ct) * 16);
+            wd[j] = lds128(at + DR_PIECE + (j * 32 * DR_WARPS + ct) * 16);
+          }
+          add_stats<BF16, DR_VECS>(s, wt, wd, c);
+        } else {
+          for (int v = ct; v < left; v += 32 * DR_WARPS) {
+            wt[0] = lds128(at + v * 16);
+            wd[0] = lds128(at + DR_PIECE + v * 16);
+            add_stats<BF16, 1>(s, wt, wd, c);
+          }
+        }
+      }
+      if (p1 < P || !ok) return;
+      s.A += s.St * (s.mt - s.md);
+      warp_merge(s, c);
+      if (lane == 0) {
+        s_part[k & 1][cw] = s;
+        mbar_arrive(&s_parts[k & 1]);
+      }
+      s = PairStat{NO_MAX, 0.f, 0.f, NO_MAX, 0.f};
+    };
+    auto second_pass = [&](int k) {
+      if (!__all_sync(~0u, mbar_wait_bounded(&s_known[k & 1], (k >> 1) & 1, &s_abort))) return give_up(3);
+      const int r = s_row[k & 15].r;
+      const GradK g = s_grad[k & 1];
+      const bool empty = s_none[k & 1];
+      uint4 *grow = reinterpret_cast<uint4 *>(static_cast<char *>(d.grad) + ((long long)r * vecs + u0) * 16);
+      for (int p = 0; p < P; ++p) {
+        const int st = (k * P + p) % DR_SLOTS;
+        if (d.grad != nullptr) {
+          const uint8_t *at = ring + st * 2 * DR_PIECE;
+          const int left = u1 - u0 - p * DR_PV;
+#pragma unroll
+          for (int j = 0; j < DR_VECS; ++j) {
+            const int v = j * 32 * DR_WARPS + ct;
+            if (v < left) {
+              f32x2 xt[N], xd[N], o[N];
+              minus16<BF16>(lds128(at + v * 16), g.mt, xt);
+              minus16<BF16>(lds128(at + DR_PIECE + v * 16), g.md, xd);
+              gradient<N>(g, xt, xd, o);
+              GST(grow + p * DR_PV + v, empty ? make_uint4(0, 0, 0, 0) : pack16<BF16>(o));
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[st]);
+      }
+    };
+    // S(0), then for every row: the next row's first pieces, this row's second
+    // pass, the rest of the next row. The last piece of a first pass comes
+    // after the second pass of the row before, so whoever writes row k + 2's
+    // statistics or law knows that every warp is through with row k's.
+    const int ahead = max(0, min(P - 1, DR_SLOTS - P));
+    // positions of weight 0 are written between the others, whose arithmetic
+    // leaves HBM time
+    const int nz = d.grad != nullptr ? d.hdr->n_jobs_a : 0;
+    auto zero_row = [&](int i) {
+      uint4 *grow = reinterpret_cast<uint4 *>(static_cast<char *>(d.grad) +
+                                              ((long long)GLD(a.zero + i) * vecs + u0) * 16);
+      for (int v = ct; v < u1 - u0; v += 32 * DR_WARPS) GST(grow + v, make_uint4(0, 0, 0, 0));
+    };
+    int z = cid;
+    if (mine > 0) first_pass(0, 0, P);
+    for (int k = 0; k < mine && ok; ++k) {
+      if (k + 1 < mine) first_pass(k + 1, 0, ahead);
+      if (ok) second_pass(k);
+      if (z < nz) zero_row(z), z += ncl;
+      if (k + 1 < mine && ok) first_pass(k + 1, ahead, P);
+    }
+    for (; z < nz; z += ncl) zero_row(z);
+  }
+  __syncwarp();
+  cluster.sync();   // no CTA leaves while a peer may still write to it
+}
+
+// Workspace of the resident schedule: header, the records, the positions of
+// weight 0.
+struct ResidentLayout {
+  size_t info, zero, total;
+};
+ResidentLayout resident_layout(int R) {
+  ResidentLayout l{};
+  l.info = sizeof(WsHeader);
+  l.zero = align256(l.info + (size_t)R * sizeof(RowInfo));
+  l.total = align256(l.zero + (size_t)R * 4);
+  return l;
+}
+
+// Whether the CTAs of a cluster of C hold a row's slices and some of the next
+// row's.
+bool resident_fits(long long vecs, int C) {
+  return ((vecs + C - 1) / C + DR_PV - 1) / DR_PV + DR_AHEAD <= DR_SLOTS;
+}
+
+template <bool BF16>
+int launch_resident(ResidentArgs a, cudaStream_t st) {
+  k_distill_setup<<<(std::max(a.d.R, std::min(a.d.B, 1 << 16)) + 255) / 256, 256, 0, st>>>(a);
+  if (launched() != SPEC_OK) return SPEC_ERR_CUDA;
+  const auto kern = k_distill_resident<BF16>;
+  const int smem = DR_SLOTS * 2 * DR_PIECE;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 1;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cfg.blockDim = dim3(DR_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  // A cluster's CTAs share one GPC, so cluster sizes leave different numbers of
+  // SMs idle: the size that runs on the most SMs, of those that hold a row
+  // (asked once per size and device).
+  static int cached[64][DR_MAX_CLUSTER + 1] = {};
+  int dev = 0, best = 0, clusters = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ERR_CUDA;
+  for (int C = 1; C <= DR_MAX_CLUSTER; ++C) {
+    if (!resident_fits((long long)a.d.V / (BF16 ? 8 : 4), C)) continue;
+    if (cached[dev][C] == 0) {
+      cfg.gridDim = dim3((unsigned)(num_sms() / C * C), 1, 1);
+      at[0].val.clusterDim.x = C;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) return SPEC_ERR_CUDA;
+      cached[dev][C] = n;
+    }
+    if (cached[dev][C] * C > clusters * best) best = C, clusters = cached[dev][C];
+  }
+  at[0].val.clusterDim.x = best;
+  cfg.gridDim = dim3((unsigned)(std::min(clusters, a.d.R) * best), 1, 1);
+  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return SPEC_ERR_CUDA;
+  return launched();
+}
+
+template <bool BF16, bool VEC>
 int launch_distill(const DistillArgs &a, int C, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)a.R * C, 1, 1);
@@ -254,7 +737,7 @@ using namespace sv;
 
 extern "C" size_t spec_distill_loss_workspace(int R_d, int V) {
   if (R_d < 0 || V <= 0 || V > SPEC_MAX_V) return 0;
-  return sizeof(WsHeader);
+  return resident_layout(R_d).total;
 }
 
 extern "C" int spec_distill_loss(const void *target, const void *draft, int dt, int R_d, int V,
@@ -269,9 +752,10 @@ extern "C" int spec_distill_loss(const void *target, const void *draft, int dt, 
   if (!aligned(target, 16) || !aligned(draft, 16) || !aligned(grad, 16) || !aligned(loss, 4) ||
       !aligned(cu_draft, 4) || !aligned(temperature, 4) || !aligned(weight, 4))
     return SPEC_ERR_INVALID_ARG;
-  if (workspace == nullptr || !aligned(workspace, 256) || ws_bytes < sizeof(WsHeader))
-    return SPEC_ERR_WORKSPACE;
   if (R_d > (1 << 27)) return SPEC_ERR_UNSUPPORTED;   // the grid: 8 CTAs per position
+  const ResidentLayout lay = resident_layout(R_d);
+  if (workspace == nullptr || !aligned(workspace, 256) || ws_bytes < lay.total)
+    return SPEC_ERR_WORKSPACE;
 
   DistillArgs a{};
   a.target = target;
@@ -289,7 +773,7 @@ extern "C" int spec_distill_loss(const void *target, const void *draft, int dt, 
   const long long es = dt == SPEC_BF16 ? 2 : 4;
 #ifdef SPEC_CHECKED
   check_begin(a.hdr);
-  check_add(workspace, sizeof(WsHeader));
+  check_add(workspace, lay.total);
   check_add(target, (unsigned long long)((long long)(R_d + (long long)B) * V * es));
   check_add(draft, (unsigned long long)((long long)R_d * V * es));
   check_add(grad, (unsigned long long)((long long)R_d * V * es));
@@ -301,9 +785,18 @@ extern "C" int spec_distill_loss(const void *target, const void *draft, int dt, 
   if (reset_header(workspace, st) != SPEC_OK) return SPEC_ERR_CUDA;
   if (R_d == 0) return SPEC_OK;
   if (check_upload(st) != SPEC_OK) return SPEC_ERR_CUDA;
-  const int C = V * es >= 65536 ? DI_MAX_CLUSTER : V * es >= 16384 ? 2 : 1;
+  if (num_sms() <= 0) return SPEC_ERR_CUDA;
   const bool vec = (V * es) % 16 == 0;
-  if (dt == SPEC_BF16)
-    return vec ? launch_distill<true, 8>(a, C, st) : launch_distill<true, 1>(a, C, st);
-  return vec ? launch_distill<false, 4>(a, C, st) : launch_distill<false, 1>(a, C, st);
+  if (vec && 2ll * R_d * V * es >= DR_MIN_BYTES && resident_fits(V * es / 16, DR_MAX_CLUSTER)) {
+    ResidentArgs s{};
+    s.d = a;
+    s.info = reinterpret_cast<RowInfo *>(static_cast<char *>(workspace) + lay.info);
+    s.zero = reinterpret_cast<int *>(static_cast<char *>(workspace) + lay.zero);
+    return dt == SPEC_BF16 ? launch_resident<true>(s, st) : launch_resident<false>(s, st);
+  }
+  // each position over as many SMs as there are, down to slices of 4 KB
+  int C = 1;
+  while (C < DI_MAX_CLUSTER && (long long)R_d * C < 4 * num_sms() && 2ll * V * es / C > 8192) C *= 2;
+  if (dt == SPEC_BF16) return vec ? launch_distill<true, true>(a, C, st) : launch_distill<true, false>(a, C, st);
+  return vec ? launch_distill<false, true>(a, C, st) : launch_distill<false, false>(a, C, st);
 }

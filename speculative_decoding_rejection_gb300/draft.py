@@ -227,7 +227,8 @@ def spec_distill_loss(target, draft, cu_draft, temperature=None, weight=None, *,
     loss, grad = (None, None) if out is None else out
     with _Call(dev, stream, (target, draft, cu_draft, temperature, weight, workspace, loss,
                              grad)) as call:
-        ws, ws_at, ws_bytes = _scratch(256, dev, workspace)
+        ws, ws_at, ws_bytes = _scratch(
+            0 if workspace is not None else spec_distill_loss_workspace(R, V), dev, workspace)
         if out is None:
             loss = torch.empty(R, dtype=f32, device=draft.device)
             grad = torch.empty_like(draft, memory_format=torch.contiguous_format) if want_grad else None

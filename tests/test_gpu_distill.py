@@ -103,6 +103,58 @@ def test_distill_large_rows():
     check(t, d, cu, temp, w, loss, grad)
 
 
+@pytest.mark.parametrize("V,R,dtype", [(201088, 60, torch.bfloat16), (32000, 700, torch.bfloat16),
+                                       (4096, 3000, torch.bfloat16), (8, 700000, torch.float32),
+                                       (50000, 200, torch.float32), (131080, 90, torch.bfloat16)])
+@pytest.mark.parametrize("zero_every", [0, 3])
+def test_distill_many_positions(V, R, dtype, zero_every):
+    """Calls that fill the SMs: rows held by clusters of each size, some of
+    one piece, ragged requests; a sample of positions against the reference,
+    the rest by the gradient's zero sum and the same bits in a second call."""
+    K = [(i * 7) % 5 for i in range(R)]
+    cu = np.concatenate([[0], np.cumsum(K)])
+    B = int(np.searchsorted(cu, R))
+    cu = np.minimum(cu[:B + 1], R).astype(np.int32)
+    g = torch.Generator(device=DEV).manual_seed(V + R)
+    t = (2 * torch.randn(R + B, V, generator=g, device=DEV)).to(dtype)
+    d = (2 * torch.randn(R, V, generator=g, device=DEV)).to(dtype)
+    temp = 0.5 + torch.rand(B, generator=g, device=DEV)
+    w = 0.1 + torch.rand(R, generator=g, device=DEV)
+    if zero_every:
+        w[::zero_every] = 0
+    cu_t = torch.tensor(cu, device=DEV)
+    loss, grad, ws = sv.spec_distill_loss(t, d, cu_t, temp, w)
+    assert sv.spec_get_status(ws) == sv.SPEC_OK
+    again = sv.spec_distill_loss(t, d, cu_t, temp, w)
+    assert torch.equal(loss, again[0]) and torch.equal(grad, again[1])
+    alone, _, _ = sv.spec_distill_loss(t, d, cu_t, temp, w, want_grad=False)
+    assert torch.equal(loss, alone)
+    assert bool((loss[w == 0] == 0).all()) and not bool(grad[w == 0].any())
+    assert bool((loss[w != 0] > 0).all())
+    # sum over x of q - p is 0: what is left are the roundings of the values and
+    # the errors of p and q (each law sums to 1; see check), times w / T
+    req = np.repeat(np.arange(B), np.diff(cu))
+    rel = U32 * (8 + 3 * 64 + V / 256 + 8 + 48)
+    left = grad.double().sum(1).abs()
+    assert bool((left <= HALF[dtype] * grad.double().abs().sum(1) +
+                 2 * rel * (w / temp[torch.tensor(req, device=DEV)]).double()).all())
+    for r in {0, 1, R // 2, R - 1}:
+        b = int(req[r])
+        check(t[r + b:r + b + 2] if r + b + 2 <= R + B else t[[r + b, r + b]], d[r:r + 1], np.array([0, 1]),
+              temp[b:b + 1], w[r:r + 1], loss[r:r + 1], grad[r:r + 1])
+
+
+def test_distill_resident_checked():
+    sv.use_checked_library(True)
+    try:
+        t, d, cu, temp, w = make(12, V=16384, K=[5] * 120, dtype=torch.bfloat16, zero_every=4)
+        loss, grad, ws = sv.spec_distill_loss(t, d, torch.tensor(cu, device=DEV), temp, w)
+        assert sv.spec_get_status(ws) == sv.SPEC_OK
+        check(t[:6], d[:5], np.array([0, 5]), temp[:1], w[:5], loss[:5], grad[:5])
+    finally:
+        sv.use_checked_library(False)
+
+
 def test_distill_defaults_and_loss_alone():
     t, d, cu, _, _ = make(9, V=300, K=[2, 2], dtype=torch.float32)
     loss, grad, _ = sv.spec_distill_loss(t, d, torch.tensor(cu, device=DEV))
