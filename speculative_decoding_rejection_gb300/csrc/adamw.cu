@@ -5,7 +5,9 @@
 // AD_ITEM elements: (tensor, first element / AD_ITEM). A CTA takes an item and
 // every thread moves 16-byte vectors of weight, gradient and states, so the
 // kernel is bound by HBM: 28 bytes per element with f32 weights and
-// states, 16.1 with bf16 weights, f32 masters and states of 8 bits.
+// states (200M elements 0.79 ms, 7.0 TB/s), 16.1 with bf16 weights, f32 masters
+// and states of 8 bits (480M elements 1.34 ms, 5.8 TB/s: about 60 instructions
+// per element come near the issue limit).
 //
 // States of 8 bits: a warp takes a block of 256 elements, 8 per lane, decodes
 // the codes, steps, finds the block's new largest magnitudes by shuffles and
@@ -14,6 +16,7 @@
 // exponent range that the codes have to span.
 #include "draft.cuh"
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -23,6 +26,9 @@ namespace {
 constexpr int AD_THREADS = 256;
 constexpr int AD_ITEM = 4096;        // elements of a work item
 constexpr int AD_PER = AD_ITEM / AD_THREADS;
+// Persistent CTAs of the 8-bit step. 480M bf16 weights with masters: 2 take 1335 us,
+// 3 (80 registers) 1438 us, 4 (64 registers, spills) 1389 us.
+constexpr int AD_CTAS_PER_SM = 2;
 constexpr uint32_t AD_MAGIC = 0x41644d57u;
 constexpr float FP8_MAX = 448.f;     // largest e4m3 value
 constexpr float FP8_TINY = 0.001953125f;                 // smallest positive one, 2^-9
@@ -70,13 +76,19 @@ struct AdStep {
   float gs, keep, lr_c1, inv_c2, eps, b1, b2, o1, o2;
 };
 
-__device__ __forceinline__ void adam(const AdStep &s, float g, float &p, float &m, float &v) {
+// One element; returns the root of the new v.
+__device__ __forceinline__ float adam(const AdStep &s, float g, float &p, float &m, float &v) {
   // each product rounded by itself: gradients of few bits put m / s_m on exact
   // ties between codes, which a fused product would round either way
   g = __fmul_rn(g, s.gs);
   m = __fadd_rn(__fmul_rn(s.b1, m), __fmul_rn(s.o1, g));
   v = __fadd_rn(__fmul_rn(s.b2, v), __fmul_rn(s.o2, __fmul_rn(g, g)));
-  p = p * s.keep - s.lr_c1 * m / (sqrtf(v) * s.inv_c2 + s.eps);
+  // root and quotient within two units of the last place, which the sum with
+  // the weight rounds away: the exact ones were a quarter of the instructions
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  p = p * s.keep - s.lr_c1 * __fdividef(m, r * s.inv_c2 + s.eps);
+  return r;
 }
 
 // N f32 values from / to a buffer of f32 (16-byte vectors).
@@ -175,94 +187,148 @@ __device__ __forceinline__ void step32(const AdStep &s, const AdTensor &x, long 
   }
 }
 
-// States of 8 bits: the warp's block of 256 elements at i0 (a multiple of
-// 256), 8 per lane.
-__device__ __forceinline__ void step8(const AdStep &s, const AdTensor &x, long long i0, int lane) {
-  const bool bf = x.bf16;
-  const long long i = i0 + lane * 8;
-  uint8_t *pm = static_cast<uint8_t *>(x.m), *pv = static_cast<uint8_t *>(x.v);
-  const long long blk = i0 / SPEC_ADAMW_BLOCK;
-  const float ms = x.ms[blk], vs = x.vs[blk];
-  const bool vec = x.vec && i + 8 <= x.n;
-  const int cnt = i >= x.n ? 0 : (int)(x.n - i < 8 ? x.n - i : 8);
-  float g[8], p[8], m[8], v[8];
-  uint32_t cm[2] = {0, 0}, cv[2] = {0, 0};
-  if (vec) {
-    const uint2 a = *reinterpret_cast<const uint2 *>(pm + i), b = *reinterpret_cast<const uint2 *>(pv + i);
-    cm[0] = a.x, cm[1] = a.y, cv[0] = b.x, cv[1] = b.y;
-    ld_w(x.grad, bf, i, g);
-    if (x.master) ld_f32<8>(x.master + i, p);
-    else ld_w(x.param, bf, i, p);
-  } else {
+// States of 8 bits: a lane's 8 elements of a block, as loaded.
+template <bool BF16, bool MASTER>
+struct Raw8 {
+  uint2 m, v;
+  float ms, vs;
+  uint4 g[BF16 ? 1 : 2];             // gradient
+  uint4 w[BF16 && !MASTER ? 1 : 2];  // bf16 weight, or f32 weight or master
+};
+__device__ __forceinline__ uint4 ld16(const void *p) { return *reinterpret_cast<const uint4 *>(p); }
+
+template <bool BF16, bool MASTER>
+__device__ __forceinline__ void load8(const AdTensor &x, long long i0, int lane, Raw8<BF16, MASTER> &r) {
+  const long long i = i0 + lane * 8, blk = i0 / SPEC_ADAMW_BLOCK;
+  r.ms = x.ms[blk], r.vs = x.vs[blk];
+  r.m = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(x.m) + i);
+  r.v = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(x.v) + i);
+  const char *g = static_cast<const char *>(x.grad) + i * (BF16 ? 2 : 4);
+  const char *w = MASTER ? reinterpret_cast<const char *>(x.master + i)
+                         : static_cast<const char *>(x.param) + i * (BF16 ? 2 : 4);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      g[j] = p[j] = 0.f;
-      if (j < cnt) {
-        cm[j / 4] |= (uint32_t)pm[i + j] << (8 * (j % 4));
-        cv[j / 4] |= (uint32_t)pv[i + j] << (8 * (j % 4));
-        g[j] = ld_w1(x.grad, bf, i + j);
-        p[j] = x.master ? x.master[i + j] : ld_w1(x.param, bf, i + j);
-      }
-    }
+  for (int k = 0; k < (BF16 ? 1 : 2); ++k) r.g[k] = ld16(g + 16 * k);
+#pragma unroll
+  for (int k = 0; k < (BF16 && !MASTER ? 1 : 2); ++k) r.w[k] = ld16(w + 16 * k);
+}
+template <bool BF16>
+__device__ __forceinline__ void values8(const uint4 *w, float *x) {
+  if (BF16) {
+    x[0] = bf16lo(w[0].x), x[1] = bf16hi(w[0].x), x[2] = bf16lo(w[0].y), x[3] = bf16hi(w[0].y);
+    x[4] = bf16lo(w[0].z), x[5] = bf16hi(w[0].z), x[6] = bf16lo(w[0].w), x[7] = bf16hi(w[0].w);
+  } else {
+    constexpr int K = BF16 ? 0 : 1;
+    x[0] = __uint_as_float(w[0].x), x[1] = __uint_as_float(w[0].y), x[2] = __uint_as_float(w[0].z);
+    x[3] = __uint_as_float(w[0].w), x[4] = __uint_as_float(w[K].x), x[5] = __uint_as_float(w[K].y);
+    x[6] = __uint_as_float(w[K].z), x[7] = __uint_as_float(w[K].w);
   }
+}
+
+// The new codes of a lane's 8 elements from m and the roots r, and the block's
+// scales.
+__device__ __forceinline__ void encode8(const AdTensor &x, long long blk, int lane, const float *m,
+                                        const float *r, uint32_t *cm, uint32_t *cv) {
   float am = 0.f, av = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; j += 2) {
-    const float2 dm = fp8x2_to_f32(cm[j / 4] >> (8 * (j % 4)));
-    const float2 dv = fp8x2_to_f32(cv[j / 4] >> (8 * (j % 4)));
-    m[j] = dm.x * ms, m[j + 1] = dm.y * ms;
-    v[j] = dv.x * vs, v[j + 1] = dv.y * vs;
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    v[j] *= v[j];
-    adam(s, g[j], p[j], m[j], v[j]);
-    v[j] = sqrtf(v[j]);   // from here on the root
-    am = fmaxf(am, fabsf(m[j]));
-    av = fmaxf(av, v[j]);
-  }
+  for (int j = 0; j < 8; ++j) am = fmaxf(am, fabsf(m[j])), av = fmaxf(av, r[j]);
   am = warp_max(am);
   av = warp_max(av);
-  const bool fm = am < TINY_ABSMAX, fv = av < TINY_ABSMAX;
-  const float im = fm ? 0.f : FP8_MAX / am, iv = fv ? 0.f : FP8_MAX / av;
-  if (lane == 0) {
-    x.ms[blk] = fm ? 0.f : am / FP8_MAX;
-    x.vs[blk] = fv ? 0.f : av / FP8_MAX;
-  }
+  // the divisions of m's and v's scales in the even and the odd lanes
+  const float most = lane & 1 ? av : am;
+  const bool none = most < TINY_ABSMAX;
+  const float inv = none ? 0.f : FP8_MAX / most;
+  if (lane < 2) (lane ? x.vs : x.ms)[blk] = none ? 0.f : most / FP8_MAX;
+  const float im = __shfl_sync(~0u, inv, 0), iv = __shfl_sync(~0u, inv, 1);
+  const float tiny = av < TINY_ABSMAX ? 0.f : FP8_TINY;
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    uint32_t wm = 0, wv = 0;
+    cm[q] = cv[q] = 0;
 #pragma unroll
     for (int j = 0; j < 4; j += 2) {
       const int e = 4 * q + j;
-      float r0 = v[e] * iv, r1 = v[e + 1] * iv;
-      if (v[e] > 0.f && !fv) r0 = fmaxf(r0, FP8_TINY);
-      if (v[e + 1] > 0.f && !fv) r1 = fmaxf(r1, FP8_TINY);
-      wm |= f32x2_to_fp8(m[e] * im, m[e + 1] * im) << (8 * j);
-      wv |= f32x2_to_fp8(r0, r1) << (8 * j);
-    }
-    cm[q] = wm, cv[q] = wv;
-  }
-  if (vec) {
-    *reinterpret_cast<uint2 *>(pm + i) = make_uint2(cm[0], cm[1]);
-    *reinterpret_cast<uint2 *>(pv + i) = make_uint2(cv[0], cv[1]);
-    if (x.master) st_f32<8>(x.master + i, p);
-    st_w(x.param, bf, i, p);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j < cnt) {
-        pm[i + j] = (uint8_t)(cm[j / 4] >> (8 * (j % 4)));
-        pv[i + j] = (uint8_t)(cv[j / 4] >> (8 * (j % 4)));
-        if (x.master) x.master[i + j] = p[j];
-        st_w1(x.param, bf, i + j, p[j]);
-      }
+      // no positive root becomes zero
+      const float r0 = r[e] > 0.f ? fmaxf(r[e] * iv, tiny) : r[e] * iv;
+      const float r1 = r[e + 1] > 0.f ? fmaxf(r[e + 1] * iv, tiny) : r[e + 1] * iv;
+      cm[q] |= f32x2_to_fp8(m[e] * im, m[e + 1] * im) << (8 * j);
+      cv[q] |= f32x2_to_fp8(r0, r1) << (8 * j);
     }
   }
 }
 
+// A block of an item that is not whole or whose tensor is not aligned, element
+// by element.
+__device__ __noinline__ void ragged8(const AdStep &s, const AdTensor &x, long long i0, int lane) {
+  const bool bf = x.bf16;
+  const long long i = i0 + lane * 8, blk = i0 / SPEC_ADAMW_BLOCK;
+  uint8_t *pm = static_cast<uint8_t *>(x.m), *pv = static_cast<uint8_t *>(x.v);
+  const float ms = x.ms[blk], vs = x.vs[blk];
+  float m[8], r[8];
+  for (int j = 0; j < 8; ++j) {
+    m[j] = r[j] = 0.f;
+    if (i + j >= x.n) continue;
+    float p = x.master ? x.master[i + j] : ld_w1(x.param, bf, i + j);
+    m[j] = fp8x2_to_f32(pm[i + j]).x * ms;
+    float v = fp8x2_to_f32(pv[i + j]).x * vs;
+    v *= v;
+    r[j] = adam(s, ld_w1(x.grad, bf, i + j), p, m[j], v);
+    if (x.master) x.master[i + j] = p;
+    st_w1(x.param, bf, i + j, p);
+  }
+  uint32_t cm[2], cv[2];
+  encode8(x, blk, lane, m, r, cm, cv);
+  for (int j = 0; j < 8 && i + j < x.n; ++j) {
+    pm[i + j] = (uint8_t)(cm[j / 4] >> (8 * (j % 4)));
+    pv[i + j] = (uint8_t)(cv[j / 4] >> (8 * (j % 4)));
+  }
+}
+
+// The warp's block of 256 elements at i0 (a multiple of 256), 8 per lane.
+template <bool BF16, bool MASTER>
+__device__ __forceinline__ void step8(const AdStep &s, const AdTensor &x, long long i0, int lane,
+                                      const Raw8<BF16, MASTER> &raw) {
+  const long long i = i0 + lane * 8;
+  float g[8], p[8], m[8], r[8];
+  values8<BF16>(raw.g, g);
+  values8<BF16 && !MASTER>(raw.w, p);
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const float2 dm = fp8x2_to_f32((j < 4 ? raw.m.x : raw.m.y) >> (8 * (j % 4)));
+    const float2 dv = fp8x2_to_f32((j < 4 ? raw.v.x : raw.v.y) >> (8 * (j % 4)));
+    m[j] = dm.x * raw.ms, m[j + 1] = dm.y * raw.ms;
+    float v0 = dv.x * raw.vs, v1 = dv.y * raw.vs;
+    v0 *= v0, v1 *= v1;
+    r[j] = adam(s, g[j], p[j], m[j], v0);
+    r[j + 1] = adam(s, g[j + 1], p[j + 1], m[j + 1], v1);
+  }
+  if (MASTER) st_f32<8>(x.master + i, p);
+  st_w(x.param, BF16, i, p);
+  uint32_t cm[2], cv[2];
+  encode8(x, i0 / SPEC_ADAMW_BLOCK, lane, m, r, cm, cv);
+  *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(x.m) + i) = make_uint2(cm[0], cm[1]);
+  *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(x.v) + i) = make_uint2(cv[0], cv[1]);
+}
+
+// A warp's two blocks of an item: both are loaded before the first is worked on.
+template <bool BF16, bool MASTER>
+__device__ __forceinline__ void item8(const AdStep &s, const AdTensor &x, int chunk, int warp, int lane) {
+  constexpr int WARPS = AD_THREADS / 32;
+  static_assert(AD_PER / 8 == 2, "two blocks of an item per warp");
+  const long long i0 = (long long)chunk * AD_ITEM + (long long)warp * SPEC_ADAMW_BLOCK;
+  const long long i1 = i0 + WARPS * SPEC_ADAMW_BLOCK;
+  if (!x.vec || i1 + SPEC_ADAMW_BLOCK > x.n) {
+    if (i0 < x.n) ragged8(s, x, i0, lane);
+    if (i1 < x.n) ragged8(s, x, i1, lane);
+    return;
+  }
+  Raw8<BF16, MASTER> r0, r1;
+  load8(x, i0, lane, r0);
+  load8(x, i1, lane, r1);
+  step8(s, x, i0, lane, r0);
+  step8(s, x, i1, lane, r1);
+}
+
 template <bool STATE8>
-__global__ void __launch_bounds__(AD_THREADS) k_adamw(AdArgs a) {
+__global__ void __launch_bounds__(AD_THREADS, STATE8 ? AD_CTAS_PER_SM : 1) k_adamw(AdArgs a) {
   const AdHeader h = *a.table;
   if (h.magic != AD_MAGIC || h.n_items != a.n_items || h.state_bits != (STATE8 ? 8 : 32)) {
     if (threadIdx.x == 0) set_status(a.hdr, SPEC_ERR_INVALID_ARG, -1);
@@ -270,8 +336,7 @@ __global__ void __launch_bounds__(AD_THREADS) k_adamw(AdArgs a) {
   }
   const AdTensor *tensors = reinterpret_cast<const AdTensor *>(a.table + 1);
   const AdItem *items = reinterpret_cast<const AdItem *>(tensors + h.n_tensors);
-  const AdItem it = items[blockIdx.x];
-  const AdTensor x = tensors[it.tensor];
+  AdItem it = items[blockIdx.x];
   AdStep s;
   s.gs = a.grad_scale ? *a.grad_scale : 1.f;
   s.keep = a.keep, s.lr_c1 = a.lr_c1, s.inv_c2 = a.inv_c2, s.eps = a.eps;
@@ -292,15 +357,35 @@ __global__ void __launch_bounds__(AD_THREADS) k_adamw(AdArgs a) {
     s.keep = 1.f - lr * a.wd;
     s.lr_c1 = lr / c1;
   }
-  const long long e0 = (long long)it.chunk * AD_ITEM;
   if (STATE8) {
+    // Persistent warps: an item's loads wait for no chain of records, as the
+    // next item is on its way during this one and the tensor's record stays in
+    // shared memory until it changes.
+    __shared__ AdTensor s_x[AD_THREADS / 32];
+    __shared__ AdStep s_step;   // in shared memory, as registers are short
+    if (threadIdx.x == 0) s_step = s;
+    __syncthreads();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int k = 0; k < AD_PER / 8; ++k) {
-      const long long i0 = e0 + (long long)(k * (AD_THREADS / 32) + warp) * SPEC_ADAMW_BLOCK;
-      if (i0 < x.n) step8(s, x, i0, lane);
+    AdTensor &y = s_x[warp];
+    int have = -1;
+    for (long long i = blockIdx.x; i < a.n_items; i += gridDim.x) {
+      AdItem next = it;
+      if (i + gridDim.x < a.n_items) next = items[i + gridDim.x];
+      if (it.tensor != have) {
+        __syncwarp();
+        if (lane < (int)(sizeof(AdTensor) / 4))
+          reinterpret_cast<uint32_t *>(&y)[lane] = reinterpret_cast<const uint32_t *>(tensors + it.tensor)[lane];
+        __syncwarp();
+        have = it.tensor;
+      }
+      if (!y.bf16) item8<false, false>(s_step, y, it.chunk, warp, lane);
+      else if (y.master) item8<true, true>(s_step, y, it.chunk, warp, lane);
+      else item8<true, false>(s_step, y, it.chunk, warp, lane);
+      it = next;
     }
   } else {
+    const AdTensor x = tensors[it.tensor];
+    const long long e0 = (long long)it.chunk * AD_ITEM;
 #pragma unroll
     for (int k = 0; k < AD_PER / 8; ++k)
       step32(s, x, e0 + (long long)(k * AD_THREADS + threadIdx.x) * 8);
@@ -422,7 +507,10 @@ extern "C" int spec_adamw_step(const void *table, int64_t n_items, int state_bit
   check_begin(a.hdr);
 #endif
   if (check_upload(st) != SPEC_OK) return SPEC_ERR_CUDA;
-  if (state_bits == 8) k_adamw<true><<<(unsigned)n_items, AD_THREADS, 0, st>>>(a);
+  const int sms = num_sms();
+  if (sms <= 0) return SPEC_ERR_CUDA;
+  if (state_bits == 8)
+    k_adamw<true><<<(unsigned)std::min<int64_t>(n_items, (int64_t)AD_CTAS_PER_SM * sms), AD_THREADS, 0, st>>>(a);
   else k_adamw<false><<<(unsigned)n_items, AD_THREADS, 0, st>>>(a);
   return launched();
 }
