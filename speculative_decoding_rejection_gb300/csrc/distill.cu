@@ -436,23 +436,6 @@ __device__ __forceinline__ uint32_t peer_addr(const void *local, int rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(local)), "r"(rank));
   return r;
 }
-// Bounded wait for a phase that the cluster's arrivals complete.
-__device__ __forceinline__ bool cluster_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-  const unsigned long long t0 = global_ns();
-  while (true) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if (*abort || global_ns() - t0 > WAIT_NS) return false;
-  }
-}
-
 template <bool BF16>
 __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_resident(ResidentArgs a) {
   constexpr int PER = BF16 ? 8 : 4, N = PER / 2;
@@ -495,7 +478,7 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_resident(ResidentArgs
         const char *drow = static_cast<const char *>(d.draft) + ((long long)x.r * vecs + u0) * 16;
         for (int p = 0; p < P; ++p, ++it) {
           const int st = it % DR_SLOTS;
-          if (it >= DR_SLOTS && !mbar_wait_bounded(&s_empty[st], (it / DR_SLOTS - 1) & 1, &s_abort)) {
+          if (it >= DR_SLOTS && !wait_phase<false>(&s_empty[st], (it / DR_SLOTS - 1) & 1, &s_abort)) {
             ok = false;
             break;
           }
@@ -512,14 +495,14 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_resident(ResidentArgs
         set_status(d.hdr, SPEC_ERR_TIMEOUT, 0);
         int never = 0;   // its copies in flight land before the CTA leaves
         for (int k = max(0, it - DR_SLOTS); k < it; ++k)
-          mbar_wait_bounded(&s_full[k % DR_SLOTS], (k / DR_SLOTS) & 1, &never);
+          wait_phase<false>(&s_full[k % DR_SLOTS], (k / DR_SLOTS) & 1, &never);
       }
     }
   } else if (warp == 1) {
     // the warps' statistics of a row, then the CTAs', then the row's law
     for (int k = 0; k < mine; ++k) {
       const int y = k & 1, par = (k >> 1) & 1;
-      bool ok = __all_sync(~0u, mbar_wait_bounded(&s_parts[y], par, &s_abort));
+      bool ok = __all_sync(~0u, wait_phase<false>(&s_parts[y], par, &s_abort));
       const RowInfo x = s_row[k & 15];
       if (ok) {
         PairStat s = lane < DR_WARPS ? s_part[y][lane] : PairStat{NO_MAX, 0.f, 0.f, NO_MAX, 0.f};
@@ -534,7 +517,7 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_resident(ResidentArgs
                            peer_addr(&s_xch[y], lane))
                        : "memory");
         }
-        ok = __all_sync(~0u, cluster_wait(&s_xch[y], par, &s_abort));
+        ok = __all_sync(~0u, wait_phase<true>(&s_xch[y], par, &s_abort));
       }
       if (!ok) {
         s_abort = 1;
@@ -569,7 +552,7 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_resident(ResidentArgs
       float c = 0.f;
       for (int p = p0; p < p1 && ok; ++p) {
         const int it = k * P + p, st = it % DR_SLOTS;
-        if (!__all_sync(~0u, mbar_wait_bounded(&s_full[st], (it / DR_SLOTS) & 1, &s_abort))) return give_up(1);
+        if (!__all_sync(~0u, wait_phase<false>(&s_full[st], (it / DR_SLOTS) & 1, &s_abort))) return give_up(1);
         c = s_row[k & 15].c;
         const uint8_t *at = ring + st * 2 * DR_PIECE;
         const int left = u1 - u0 - p * DR_PV;   // vectors of this piece
@@ -599,7 +582,7 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_resident(ResidentArgs
       s = PairStat{NO_MAX, 0.f, 0.f, NO_MAX, 0.f};
     };
     auto second_pass = [&](int k) {
-      if (!__all_sync(~0u, mbar_wait_bounded(&s_known[k & 1], (k >> 1) & 1, &s_abort))) return give_up(3);
+      if (!__all_sync(~0u, wait_phase<false>(&s_known[k & 1], (k >> 1) & 1, &s_abort))) return give_up(3);
       const int r = s_row[k & 15].r;
       const GradK g = s_grad[k & 1];
       const bool empty = s_none[k & 1];
@@ -677,8 +660,8 @@ int launch_resident(ResidentArgs a, cudaStream_t st) {
   if (launched() != SPEC_OK) return SPEC_ERR_CUDA;
   const auto kern = k_distill_resident<BF16>;
   const int smem = DR_SLOTS * 2 * DR_PIECE;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return SPEC_ERR_CUDA;
+  static SmemLimit limit;
+  if (allow_smem(limit, (const void *)kern, smem) != SPEC_OK) return SPEC_ERR_CUDA;   // the occupancy query needs it
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -709,8 +692,7 @@ int launch_resident(ResidentArgs a, cudaStream_t st) {
   }
   at[0].val.clusterDim.x = best;
   cfg.gridDim = dim3((unsigned)(std::min(clusters, a.d.R) * best), 1, 1);
-  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return SPEC_ERR_CUDA;
-  return launched();
+  return launch_retry(limit, (const void *)kern, smem, [&]() { return cudaLaunchKernelEx(&cfg, kern, a); });
 }
 
 template <bool BF16, bool VEC>

@@ -21,9 +21,64 @@ __device__ __forceinline__ uint32_t f32_to_bf16_bits(float v) {
   return f32x2_to_bf16x2(v, 0.f) & 0xffffu;
 }
 
+// Bounded wait for a phase of a shared-memory barrier; CLUSTER: acquires what
+// other CTAs of the cluster released. As mbar_wait_bounded, but the timer, whose
+// reads take longer than a ring stage, is looked at after every 64 tries only.
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  unsigned long long t0 = 0;
+  for (int tries = 0;; ++tries) {
+    uint32_t ok;
+    if (CLUSTER)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity)
+          : "memory");
+    else
+      ok = mbar_try_wait(bar, parity);
+    if (ok) return true;
+    if ((tries & 63) == 63) {
+      if (*abort) return false;
+      if (t0 == 0) t0 = global_ns();
+      else if (global_ns() - t0 > WAIT_NS) return false;
+    }
+  }
+}
+
 // Host: the status header starts every call at SPEC_OK.
 inline int reset_header(void *workspace, cudaStream_t st) {
   return cudaMemsetAsync(workspace, 0, sizeof(WsHeader), st) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+// Lets `kern` have `smem` bytes of dynamic shared memory. The call takes
+// microseconds of host time, so a kernel's largest request is remembered per
+// device (in `most`, one array per kernel); a device that was reset has
+// forgotten it, which the launch reports (launch_retry).
+struct SmemLimit {
+  int most[64] = {};
+};
+inline int allow_smem(SmemLimit &l, const void *kern, int smem) {
+  int dev = 0;
+  if (smem <= 48 * 1024) return SPEC_OK;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ERR_CUDA;
+  if (l.most[dev] >= smem) return SPEC_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  l.most[dev] = smem;
+  return SPEC_OK;
+}
+// Launches through `go` (a callable that returns a cudaError_t); on a failure once
+// more after the kernel's limit is set anew.
+template <class Go>
+int launch_retry(SmemLimit &l, const void *kern, int smem, Go go) {
+  if (allow_smem(l, kern, smem) != SPEC_OK) return SPEC_ERR_CUDA;
+  if (go() == cudaSuccess) return SPEC_OK;
+  cudaGetLastError();
+  l = SmemLimit{};
+  if (allow_smem(l, kern, smem) != SPEC_OK) return SPEC_ERR_CUDA;
+  return go() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 inline int launched() { return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA; }
 

@@ -14,18 +14,25 @@
 // rows wastes no reads: the column count of the tile follows the rows (16 at
 // the least), and every weight is read once.
 //
+// Large products run on pairs of CTAs (cta_group::2): a pair's 256 x nt tile
+// takes 128 rows of A and half of B's columns from each CTA, so a stage of r
+// needs 32 KB of a CTA's ring where a lone CTA's 128 x 256 tile needs 48 KB, and
+// six stages instead of four cover the copies' latency.
+//
 // A persistent CTA per SM: one warp feeds a ring of TMA stages (64 of r each),
 // one issues tcgen05.mma, four run the epilogue from the other of two
-// accumulators. Where the tiles alone would not fill the SMs, r is split: the
-// parts leave f32 partials, and a second launch over all SMs adds them up in
-// the order of r and runs the epilogue (joining inside the product, by the last
-// part of a tile, left one SM per tile reading the parts: 197 rows of 2880 x
-// 2880 took 96 us that way, 31 us this way).
+// accumulators. Where whole tiles would leave SMs idle in the last round, all
+// tiles' stages are laid end to end and every CTA takes an equal run of them: what
+// it has of a tile that it shares goes out as an f32 partial, and a second launch
+// over all SMs adds the partials of a tile in the order of r and runs the
+// epilogue. (Joining inside the product, by the last part of a tile, left one SM
+// per tile reading the parts: 197 rows of 2880 x 2880 took 96 us that way.)
 #include <cuda.h>   // tensor map types; the encoder is resolved at run time
 
 #include "draft.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace sv {
 namespace {
@@ -39,17 +46,18 @@ constexpr int HD_STAGE_LD = 36;       // floats between columns of a warp's stag
 constexpr int HD_STAGING = 4 * 32 * HD_STAGE_LD * 4;   // four warps, 32 columns of 32 lanes
 constexpr int HD_SMEM = 226 * 1024 - HD_STAGING - 1024;   // ring
 constexpr int HD_PLAN_SMS = 152;      // SMs the split is planned for
-constexpr int HD_MAX_SPLIT = 32;
 constexpr int HD_A_BYTES = HD_I * HD_R * 2;
 
-struct HeadArgs {
-  int tiles_i, tiles_j, S, KB, nt, stages, units;
+struct HeadArgs {   // tiles of 128 x nt; a pair's tile counts as two, one per CTA
+  int tiles_i, tiles_j, KB, nt, stages;
+  int runs;            // 0: whole tiles; else the CTAs (pairs) that take equal runs of stages
+  int run_len, longer; // a run's stages; the first `longer` runs have one more
   int I, J;            // extents of the result
   long long ldo;       // elements between columns j of the result
   const __nv_bfloat16 *bias, *residual;
   __nv_bfloat16 *out, *pre;
   int act;
-  float *part;         // [units][nt][128] partials of a split
+  float *part;         // [2 per CTA][nt][128] partials of shared tiles
   int reset;           // this launch starts the call: the status is set to OK
   int vec;             // rows of the result and of its residual suit 16-byte accesses
   WsHeader *hdr;
@@ -62,14 +70,38 @@ struct HeadSmem {
   int abort;
 };
 
-__device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-      "%3}], [%4];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
-      : "memory");
+// TMA load of a box to this CTA's shared memory. PAIR: its bytes count on the
+// barrier of the pair's first CTA (bar: that barrier's cluster address).
+template <bool PAIR>
+__device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+  if (PAIR) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  }
 }
-
+// The address of a shared variable in the pair's CTA `rank`.
+__device__ __forceinline__ uint32_t peer_u32(const void *p, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
 // Shared-memory matrix descriptor of a 128-byte swizzled tile: start address,
 // the two strides (in 16 bytes), version 1, swizzle mode 2 (128 bytes).
 // K-major: rows of 128 bytes, 8-row groups 1024 bytes apart. MN-major: blocks
@@ -81,17 +113,36 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool mn) {
          (2ull << 61);
 }
 
+template <bool PAIR>
 __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
-      : "memory");
+  if (PAIR) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+  }
 }
+// Arrival on `bar` (PAIR: in both CTAs) once the products issued so far are done.
+template <bool PAIR>
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-      : "memory");
+  if (PAIR) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], "
+        "%1;" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+        : "memory");
+  }
 }
 // 32 accumulator columns of this thread's lane.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float *v) {
@@ -111,25 +162,29 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float *v) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// Quotients within two units of the last place: results of bf16 do not see it,
+// and the exact division was a third of dz's instructions.
+__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// (1 + tanh u) / 2 = sigmoid(2u)
+__device__ __forceinline__ float gelu_gate(float z) {
+  return sigmoid(1.5957691216057308f * (z + 0.044715f * z * z * z));
+}
 __device__ __forceinline__ float act_value(float z, int act) {
-  if (act == SPEC_ACT_SILU) return z / (1.f + __expf(-z));
-  if (act == SPEC_ACT_GELU)
-    return 0.5f * z * (1.f + tanhf(0.7978845608028654f * (z + 0.044715f * z * z * z)));
+  if (act == SPEC_ACT_SILU) return z * sigmoid(z);
+  if (act == SPEC_ACT_GELU) return z * gelu_gate(z);
   return z;
 }
 __device__ __forceinline__ float act_slope(float z, int act) {
   if (act == SPEC_ACT_SILU) {
-    const float s = 1.f / (1.f + __expf(-z));
+    const float s = sigmoid(z);
     return s * (1.f + z * (1.f - s));
   }
   if (act == SPEC_ACT_GELU) {
-    const float t = tanhf(0.7978845608028654f * (z + 0.044715f * z * z * z));
-    return 0.5f * (1.f + t) +
-           0.5f * z * (1.f - t * t) * 0.7978845608028654f * (1.f + 0.134145f * z * z);
+    const float s = gelu_gate(z);
+    return s * (1.f + z * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * z * z));
   }
   return 1.f;
 }
-
 __device__ __forceinline__ float bf16_at(const __nv_bfloat16 *p, long long i) {
   return bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(p)[i]);
 }
@@ -179,16 +234,49 @@ __device__ __forceinline__ void finish8(const HeadArgs &a, float *z, int i, int 
   }
 }
 
-template <bool A_MN, bool B_MN>
+// A CTA's work, one stretch [k0, k1) of a tile's stages after another. slot: which
+// of the CTA's two partials takes it, -1 for a whole tile.
+struct Stretch {
+  int tile, k0, k1, slot;
+};
+__device__ __forceinline__ int run_start(const HeadArgs &a, int g) { return g * a.run_len + min(g, a.longer); }
+struct Walk {
+  int at, end, step;   // stages (runs) or tiles
+};
+__device__ __forceinline__ Walk walk_of(const HeadArgs &a, int tiles, int g, int n) {
+  if (a.runs == 0) return Walk{g, tiles, n};
+  return Walk{run_start(a, g), run_start(a, g + 1), 0};
+}
+__device__ __forceinline__ bool next_stretch(const HeadArgs &a, Walk &w, Stretch &s) {
+  if (w.at >= w.end) return false;
+  if (a.runs == 0) {
+    s = Stretch{w.at, 0, a.KB, -1};
+    w.at += w.step;
+  } else {
+    s.tile = w.at / a.KB;
+    s.k0 = w.at - s.tile * a.KB;
+    s.k1 = min(a.KB, s.k0 + (w.end - w.at));
+    // a run shares at most its first and its last tile; one that starts a tile
+    // is the last
+    s.slot = s.k0 == 0 && s.k1 == a.KB ? -1 : s.k0 == 0;
+    w.at += s.k1 - s.k0;
+  }
+  return true;
+}
+
+template <bool A_MN, bool B_MN, bool PAIR>
 __global__ void __launch_bounds__(HD_THREADS, 1)
     k_head(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
            const HeadArgs a) {
   extern __shared__ uint8_t dyn[];
   __shared__ HeadSmem sh;
   uint8_t *ring = reinterpret_cast<uint8_t *>(((uintptr_t)dyn + 1023) & ~(uintptr_t)1023);
-  float *staging = reinterpret_cast<float *>(ring + a.stages * (HD_A_BYTES + a.nt * HD_R * 2));
+  constexpr int CTAS = PAIR ? 2 : 1;
+  const int ntc = a.nt / CTAS;   // columns of B that this CTA loads
+  const int stage_bytes = HD_A_BYTES + ntc * HD_R * 2;
+  float *staging = reinterpret_cast<float *>(ring + a.stages * stage_bytes);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int stage_bytes = HD_A_BYTES + a.nt * HD_R * 2;
+  const int rank = PAIR ? (int)cluster_rank() : 0;
   uint32_t cols = 32;   // TMEM columns: two accumulators, a power of two
   while (cols < 2u * ((a.nt + 31) & ~31)) cols <<= 1;
   volatile int *abort = &sh.abort;
@@ -198,81 +286,89 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
     if (blockIdx.x == 0 && a.reset) a.hdr->status = SPEC_OK, a.hdr->detail = -1;
     sh.abort = 0;
     for (int s = 0; s < a.stages; ++s) mbar_init(&sh.full[s], 1), mbar_init(&sh.empty[s], 1);
-    for (int s = 0; s < 2; ++s) mbar_init(&sh.acc_full[s], 1), mbar_init(&sh.acc_empty[s], 4);
+    for (int s = 0; s < 2; ++s) mbar_init(&sh.acc_full[s], 1), mbar_init(&sh.acc_empty[s], 4 * CTAS);
     fence_mbar_init();
   }
   if (warp == 5) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(&sh.tmem)),
-                 "r"(cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(&sh.tmem)),
+                   "r"(cols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_u32(&sh.tmem)),
+                   "r"(cols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   }
   __syncthreads();
+  if (PAIR) cluster_sync();   // barriers initialised in both CTAs before any remote arrival
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = sh.tmem;
-  const int tiles = a.tiles_i * a.tiles_j;
+  const int g = blockIdx.x / CTAS;   // tiles count per pair here
+  Walk walk = walk_of(a, a.tiles_i / CTAS * a.tiles_j, g, gridDim.x / CTAS);
+  Stretch w;
 
   if (warp == 4) {
     if (lane == 0) {
       int it = 0;   // stages filled so far
-      for (int u = blockIdx.x; u < a.units && !*abort; u += gridDim.x) {
-        const int s = u / tiles, tile = u % tiles;
-        const int i0 = tile / a.tiles_j * HD_I, j0 = tile % a.tiles_j * a.nt;
-        const int k0 = (int)((long long)a.KB * s / a.S), k1 = (int)((long long)a.KB * (s + 1) / a.S);
-        for (int k = k0; k < k1; ++k, ++it) {
+      while (!*abort && next_stretch(a, walk, w)) {
+        const int i0 = (w.tile / a.tiles_j * CTAS + rank) * HD_I, j0 = w.tile % a.tiles_j * a.nt + rank * ntc;
+        for (int k = w.k0; k < w.k1; ++k, ++it) {
           const int st = it % a.stages;
-          if (it >= a.stages &&
-              !mbar_wait_bounded(&sh.empty[st], (it / a.stages - 1) & 1, abort)) {
+          if (it >= a.stages && !wait_phase<PAIR>(&sh.empty[st], (it / a.stages - 1) & 1, abort)) {
             *abort = 1;
             break;
           }
           uint8_t *pa = ring + st * stage_bytes, *pb = pa + HD_A_BYTES;
-          mbar_arrive_tx(&sh.full[st], stage_bytes);
+          const uint32_t bar = PAIR ? peer_u32(&sh.full[st], 0) : smem_u32(&sh.full[st]);
+          // both CTAs' bytes count on the first one's barrier
+          if (rank == 0) mbar_arrive_tx(&sh.full[st], CTAS * stage_bytes);
           if (A_MN) {
-            tma_2d(pa, &map_a, i0, k * HD_R, &sh.full[st]);
-            tma_2d(pa + 8192, &map_a, i0 + 64, k * HD_R, &sh.full[st]);
+            tma_2d<PAIR>(pa, &map_a, i0, k * HD_R, bar);
+            tma_2d<PAIR>(pa + 8192, &map_a, i0 + 64, k * HD_R, bar);
           } else {
-            tma_2d(pa, &map_a, k * HD_R, i0, &sh.full[st]);
+            tma_2d<PAIR>(pa, &map_a, k * HD_R, i0, bar);
           }
           if (B_MN) {
-            for (int q = 0; q < a.nt; q += 64)
-              tma_2d(pb + q * 128, &map_b, j0 + q, k * HD_R, &sh.full[st]);
+            for (int q = 0; q < ntc; q += 64) tma_2d<PAIR>(pb + q * 128, &map_b, j0 + q, k * HD_R, bar);
           } else {
-            tma_2d(pb, &map_b, k * HD_R, j0, &sh.full[st]);
+            tma_2d<PAIR>(pb, &map_b, k * HD_R, j0, bar);
           }
         }
         if (*abort) break;
       }
       if (*abort) {   // the copies in flight land before the CTA leaves
         int never = 0;
-        for (int k = max(0, it - a.stages); k < it; ++k)
-          mbar_wait_bounded(&sh.full[k % a.stages], (k / a.stages) & 1, &never);
+        if (rank == 0)
+          for (int k = max(0, it - a.stages); k < it; ++k)
+            wait_phase<PAIR>(&sh.full[k % a.stages], (k / a.stages) & 1, &never);
         set_status(a.hdr, SPEC_ERR_TIMEOUT, 4);
       }
     }
   } else if (warp == 5) {
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {   // of a pair, the first CTA issues for both
       // f32 accumulator, bf16 operands, which of them are MN-major, N, M
       const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)A_MN << 15) |
                              ((uint32_t)B_MN << 16) | ((uint32_t)(a.nt >> 3) << 17) |
-                             ((uint32_t)(HD_I >> 4) << 24);
+                             ((uint32_t)(HD_I * CTAS >> 4) << 24);
       int it = 0, n = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < a.units && ok; u += gridDim.x, ++n) {
-        const int s = u / tiles;
-        const int k0 = (int)((long long)a.KB * s / a.S), k1 = (int)((long long)a.KB * (s + 1) / a.S);
+      for (; ok && next_stretch(a, walk, w); ++n) {
         const int buf = n & 1;
-        if (n >= 2 && !mbar_wait_bounded(&sh.acc_empty[buf], ((n >> 1) - 1) & 1, abort)) {
+        if (n >= 2 && !wait_phase<PAIR>(&sh.acc_empty[buf], ((n >> 1) - 1) & 1, abort)) {
           ok = false;
           break;
         }
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t d = tmem + buf * (cols / 2);
-        for (int k = k0; k < k1; ++k, ++it) {
+        for (int k = w.k0; k < w.k1; ++k, ++it) {
           const int st = it % a.stages;
-          if (!mbar_wait_bounded(&sh.full[st], (it / a.stages) & 1, abort)) {
+          if (!wait_phase<PAIR>(&sh.full[st], (it / a.stages) & 1, abort)) {
             ok = false;
             break;
           }
@@ -280,11 +376,11 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
           const uint32_t pa = smem_u32(ring + st * stage_bytes), pb = pa + HD_A_BYTES;
 #pragma unroll
           for (int q = 0; q < HD_R / 16; ++q)   // 16 of r: 32 bytes along a row, or two 8-row groups
-            mma_bf16(d, smem_desc(pa + q * (A_MN ? 2048 : 32), A_MN),
-                     smem_desc(pb + q * (B_MN ? 2048 : 32), B_MN), idesc, k > k0 || q > 0);
-          mma_commit(&sh.empty[st]);
+            mma_bf16<PAIR>(d, smem_desc(pa + q * (A_MN ? 2048 : 32), A_MN),
+                           smem_desc(pb + q * (B_MN ? 2048 : 32), B_MN), idesc, k > w.k0 || q > 0);
+          mma_commit<PAIR>(&sh.empty[st]);
         }
-        if (ok) mma_commit(&sh.acc_full[buf]);
+        if (ok) mma_commit<PAIR>(&sh.acc_full[buf]);
       }
       if (!ok) {
         *abort = 1;
@@ -293,19 +389,18 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
     }
   } else {
     int n = 0;
-    for (int u = blockIdx.x; u < a.units; u += gridDim.x, ++n) {
-      const int tile = u % tiles, buf = n & 1;
-      const int i0 = tile / a.tiles_j * HD_I, j0 = tile % a.tiles_j * a.nt;
+    for (; next_stretch(a, walk, w); ++n) {
+      const int buf = n & 1, i0 = (w.tile / a.tiles_j * CTAS + rank) * HD_I, j0 = w.tile % a.tiles_j * a.nt;
       // one verdict for the warp, which loads from TMEM together
-      if (!__all_sync(~0u, mbar_wait_bounded(&sh.acc_full[buf], (n >> 1) & 1, abort))) {
+      if (!__all_sync(~0u, wait_phase<PAIR>(&sh.acc_full[buf], (n >> 1) & 1, abort))) {
         *abort = 1;
         if (lane == 0) set_status(a.hdr, SPEC_ERR_TIMEOUT, 0);
         break;
       }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t d = tmem + buf * (cols / 2) + ((uint32_t)(warp * 32) << 16);
-      if (a.S > 1) {   // 128 bytes per warp and column
-        float *mine = a.part + (long long)u * a.nt * HD_I + t;
+      if (w.slot >= 0) {   // 128 bytes per warp and column
+        float *mine = a.part + (long long)(blockIdx.x * 2 + w.slot) * a.nt * HD_I + t;
         for (int c = 0; c < a.nt; c += 32) {
           float v[32];
           tmem_ld32(d + c, v);
@@ -339,39 +434,138 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
+      if (lane == 0) {
+        if (PAIR)
+          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                           peer_u32(&sh.acc_empty[buf], 0))
+                       : "memory");
+        else
+          mbar_arrive(&sh.acc_empty[buf]);
+      }
     }
   }
+  __syncwarp();
   __syncthreads();
+  if (PAIR) cluster_sync();   // the pair's products and arrivals are through
   if (warp == 5) {
-    __syncwarp();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
+    if (PAIR)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
   }
 }
 
-// The parts of a split added up in the order of r, and the epilogue: a thread
-// takes 8 elements of i of one column.
-__global__ void __launch_bounds__(256) k_head_join(const HeadArgs a) {
-  const int tiles = a.tiles_i * a.tiles_j;
-  const long long n = (long long)tiles * a.nt * (HD_I / 8);
-  for (long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x; e < n;
-       e += (long long)gridDim.x * blockDim.x) {
-    const int iv = (int)(e % (HD_I / 8)), col = (int)(e / (HD_I / 8) % a.nt);
-    const int tile = (int)(e / (HD_I / 8) / a.nt);
-    const int i = tile / a.tiles_j * HD_I + iv * 8, j = tile % a.tiles_j * a.nt + col;
-    if (j >= a.J || i >= a.I) continue;
-    const float *p = a.part + ((long long)tile * a.nt + col) * HD_I + iv * 8;
-    const long long step = (long long)tiles * a.nt * HD_I;
-    float z[8] = {};
+// The partials of shared tiles added up in the order of r, and the epilogue. Block
+// x: 128 rows of a tile (ctas of them per tile); a thread takes 8 elements of i of
+// one column.
+__global__ void __launch_bounds__(256) k_head_join(const HeadArgs a, int ctas) {
+  const int tile = blockIdx.x / ctas, rank = blockIdx.x % ctas;
+  const int iv = threadIdx.x % (HD_I / 8), col = blockIdx.y * 16 + threadIdx.x / (HD_I / 8);
+  const int i = (tile / a.tiles_j * ctas + rank) * HD_I + iv * 8, j = tile % a.tiles_j * a.nt + col;
+  // the runs that have stages of this tile: g .. g + n - 1
+  const int first = tile * a.KB, head = a.longer * (a.run_len + 1);
+  auto run_of = [&](int x) { return x < head ? x / (a.run_len + 1) : a.longer + (x - head) / a.run_len; };
+  const int g = run_of(first), n = run_of(first + a.KB - 1) - g + 1;
+  if (n == 1 || col >= a.nt || j >= a.J || i >= a.I) return;   // one run: the product finished it
+  // run g's stretch starts the tile, the others' start their runs
+  const long long step = (long long)ctas * 2 * a.nt * HD_I;
+  const float *p = a.part + ((long long)(g * ctas + rank) * 2 * a.nt + col) * HD_I + iv * 8;
+  float z[8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float4 x = __ldcs(reinterpret_cast<const float4 *>(p + (long long)a.nt * HD_I) + h);
+    z[4 * h] = x.x, z[4 * h + 1] = x.y, z[4 * h + 2] = x.z, z[4 * h + 3] = x.w;
+  }
 #pragma unroll 4
-    for (int s = 0; s < a.S; ++s) {
-      const float4 x = __ldcs(reinterpret_cast<const float4 *>(p + s * step));
-      const float4 y = __ldcs(reinterpret_cast<const float4 *>(p + s * step) + 1);
-      z[0] += x.x, z[1] += x.y, z[2] += x.z, z[3] += x.w;
-      z[4] += y.x, z[5] += y.y, z[6] += y.z, z[7] += y.w;
+  for (int s = 1; s < n; ++s) {
+    const float4 x = __ldcs(reinterpret_cast<const float4 *>(p + s * step));
+    const float4 y = __ldcs(reinterpret_cast<const float4 *>(p + s * step) + 1);
+    z[0] += x.x, z[1] += x.y, z[2] += x.z, z[3] += x.w;
+    z[4] += y.x, z[5] += y.y, z[6] += y.z, z[7] += y.w;
+  }
+  finish8(a, z, i, j);
+}
+
+// Few rows (a decode step): a warp reads HD_N whole rows of W at a time, 16 bytes
+// per lane, and multiplies them with the M rows of x, which the block keeps in
+// shared memory as f32. Bound by HBM's reads of W, which come as whole rows:
+// the tiles' boxes of 128 bytes per row reach 4.8 TB/s at one row of 4096 by
+// 32000, this 6.1 TB/s (43 us). VEC: rows of W and x are 16-byte aligned.
+constexpr int HD_FEW = 4;        // rows of x at most
+constexpr int HD_N = 2;          // rows of W per warp
+constexpr int HD_FEW_CTAS = 5;   // CTAs per SM
+constexpr int HD_FEW_K = 4096;   // elements of x per row in shared memory at a time
+template <int M, bool VEC>
+__global__ void __launch_bounds__(256) k_head_few(const HeadArgs a, const uint16_t *x, const uint16_t *w, int K) {
+  extern __shared__ __align__(16) float xs[];   // [M][min(K, HD_FEW_K), rounded up to 8]
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  if (blockIdx.x == 0 && t == 0) a.hdr->status = SPEC_OK, a.hdr->detail = -1;   // nothing here sets another
+  const int groups = (a.I + HD_N - 1) / HD_N, step = gridDim.x * 8;
+  // every warp of the block goes round as often as its first one: they share xs
+  for (int gb = blockIdx.x * 8; gb < groups; gb += step) {
+    const int n0 = (gb + warp) * HD_N;
+    float acc[M][HD_N] = {};
+    for (int k0 = 0; k0 < K; k0 += HD_FEW_K) {
+      const int kn = min(HD_FEW_K, K - k0), ld = (kn + 7) & ~7;
+      if (K > HD_FEW_K || gb == blockIdx.x * 8) {   // x stays where it fits
+        __syncthreads();
+        for (int e = t; e < M * ld; e += 256) {
+          const int m = e / ld, k = e - m * ld;
+          xs[e] = m < a.J && k < kn ? bf16_bits_to_f32(x[(long long)m * K + k0 + k]) : 0.f;
+        }
+        __syncthreads();
+      }
+      if (n0 >= a.I) continue;
+      const uint16_t *row[HD_N];
+#pragma unroll
+      for (int r = 0; r < HD_N; ++r) row[r] = w + (long long)min(n0 + r, a.I - 1) * K + k0;
+      if (VEC) {
+#pragma unroll 4
+        for (int k = lane * 8; k < kn; k += 256) {
+          float v[HD_N][8];
+#pragma unroll
+          for (int r = 0; r < HD_N; ++r) unpack8(__ldcs(reinterpret_cast<const uint4 *>(row[r] + k)), v[r]);
+#pragma unroll
+          for (int m = 0; m < M; ++m) {
+            const float4 p = *reinterpret_cast<const float4 *>(xs + m * ld + k);
+            const float4 q = *reinterpret_cast<const float4 *>(xs + m * ld + k + 4);
+#pragma unroll
+            for (int r = 0; r < HD_N; ++r)
+              acc[m][r] += v[r][0] * p.x + v[r][1] * p.y + v[r][2] * p.z + v[r][3] * p.w + v[r][4] * q.x +
+                           v[r][5] * q.y + v[r][6] * q.z + v[r][7] * q.w;
+          }
+        }
+      } else {
+#pragma unroll 8
+        for (int k = lane; k < kn; k += 32) {
+#pragma unroll
+          for (int r = 0; r < HD_N; ++r) {
+            const float v = bf16_bits_to_f32(row[r][k]);
+#pragma unroll
+            for (int m = 0; m < M; ++m) acc[m][r] += v * xs[m * ld + k];
+          }
+        }
+      }
     }
-    finish8(a, z, i, j);
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int r = 0; r < HD_N; ++r)
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) acc[m][r] += __shfl_xor_sync(~0u, acc[m][r], o);
+    // a lane per result
+    const int m = lane / HD_N, n = n0 + lane % HD_N;
+    float z = 0.f;
+#pragma unroll
+    for (int q = 0; q < M * HD_N; ++q)
+      if (q == lane) z = acc[q / HD_N][q % HD_N];
+    if (lane < M * HD_N && m < a.J && n < a.I) {
+      const long long at = (long long)m * a.ldo + n;
+      if (a.bias) z += bf16_at(a.bias, n);
+      if (a.pre) bf16_to(a.pre, at, z);
+      bf16_to(a.out, at, act_value(z, a.act) + (a.residual ? bf16_at(a.residual, at) : 0.f));
+    }
   }
 }
 
@@ -399,36 +593,39 @@ __global__ void __launch_bounds__(256)
   const int c0 = (blockIdx.x * 32 + cx) * VEC;
   const int r0 = blockIdx.y * HD_DZ_ROWS, r1 = min(M, r0 + HD_DZ_ROWS);
   float acc[VEC] = {};
+  using U = typename std::conditional<VEC == 8, uint4, uint16_t>::type;
+  constexpr int BATCH = 4;   // rows whose loads are out together
   if (c0 < ld) {
-    for (int r = r0 + ry; r < r1; r += 8) {
-      uint16_t g[VEC], z[VEC];
-      const long long at = (long long)r * N + c0;
-      if (VEC == 8) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(dy + at);
-        memcpy(g, &x, VEC == 8 ? sizeof(g) : 0);
-        if (pre) {
-          const uint4 y = *reinterpret_cast<const uint4 *>(pre + at);
-          memcpy(z, &y, VEC == 8 ? sizeof(z) : 0);
-        }
-      } else {
-        g[0] = c0 < N ? dy[at] : 0;
-        if (pre) z[0] = c0 < N ? pre[at] : 0;
-      }
-      uint16_t o[VEC];
+    for (int rb = r0 + ry; rb < r1; rb += 8 * BATCH) {
+      U gv[BATCH] = {}, zv[BATCH] = {};
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        float v = bf16_bits_to_f32(g[j]);
-        if (pre) v = __fmul_rn(v, act_slope(bf16_bits_to_f32(z[j]), act));
-        acc[j] = __fadd_rn(acc[j], v);   // unfused: the same sums with and without dz
-        o[j] = (uint16_t)f32_to_bf16_bits(v);
+      for (int q = 0; q < BATCH; ++q) {
+        const int r = rb + 8 * q;
+        if (r < r1 && c0 < N) {
+          gv[q] = *reinterpret_cast<const U *>(dy + (long long)r * N + c0);
+          if (pre) zv[q] = *reinterpret_cast<const U *>(pre + (long long)r * N + c0);
+        }
       }
-      if (dz) {
+#pragma unroll
+      for (int q = 0; q < BATCH; ++q) {
+        const int r = rb + 8 * q;
+        if (r >= r1) break;
+        float g[VEC], z[VEC];
         if (VEC == 8) {
-          uint4 x;
-          memcpy(&x, o, VEC == 8 ? sizeof(x) : 0);
-          *reinterpret_cast<uint4 *>(dz + (long long)r * ld + c0) = x;
+          unpack8(*reinterpret_cast<const uint4 *>(&gv[q]), g);
+          unpack8(*reinterpret_cast<const uint4 *>(&zv[q]), z);
         } else {
-          dz[(long long)r * ld + c0] = o[0];
+          g[0] = bf16_bits_to_f32(*reinterpret_cast<const uint16_t *>(&gv[q]));
+          z[0] = bf16_bits_to_f32(*reinterpret_cast<const uint16_t *>(&zv[q]));
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          if (pre) g[j] = __fmul_rn(g[j], act_slope(z[j], act));
+          acc[j] = __fadd_rn(acc[j], g[j]);   // unfused: the same sums with and without dz
+        }
+        if (dz) {
+          if (VEC == 8) *reinterpret_cast<uint4 *>(dz + (long long)r * ld + c0) = pack8(g);
+          else dz[(long long)r * ld + c0] = (uint16_t)f32_to_bf16_bits(g[0]);
         }
       }
     }
@@ -488,60 +685,111 @@ int make_map(CUtensorMap *m, const void *p, long long rows, long long inner, lon
              : SPEC_ERR_CUDA;
 }
 
-// Tiles and split of a product D[I, J] over R.
+// Tiles of a product D[I, J] over R, whether pairs of CTAs run it, and whether they
+// take equal runs of stages.
 struct Plan {
-  int tiles_i, tiles_j, nt, KB, S;
-  long long units;
+  int tiles_i, tiles_j, nt, KB;
+  int runs;   // 0: whole tiles
+  bool pair;
   size_t part_bytes;
 };
 
-Plan make_plan(long long I, long long J, long long R, bool b_mn) {
+Plan plan_of(long long I, long long J, long long R, bool b_mn, bool pair, double *cost_out) {
   Plan p{};
+  p.pair = pair;
+  const int ctas = pair ? 2 : 1, slots = HD_PLAN_SMS / ctas;
   p.tiles_i = (int)((I + HD_I - 1) / HD_I);
+  if (pair) p.tiles_i = (p.tiles_i + 1) / 2 * 2;
   p.tiles_j = (int)((J + HD_MAX_J - 1) / HD_MAX_J);
-  const long long each = (J + p.tiles_j - 1) / p.tiles_j, step = b_mn ? 64 : 16;
+  const long long each = (J + p.tiles_j - 1) / p.tiles_j;
+  const long long step = b_mn ? (pair ? 128 : 64) : (pair ? 32 : 16);
   p.nt = (int)((each + step - 1) / step * step);
   p.KB = (int)((R + HD_R - 1) / HD_R);
-  const long long tiles = (long long)p.tiles_i * p.tiles_j;
-  // rounds of units per SM times the stages of a unit (a stage of nt = 256 takes
-  // 0.27 us); a split adds the partials' way out, and the join's launch and
-  // its reads
-  double best = 0;
-  p.S = 1;
-  for (int S = 1; S <= HD_MAX_SPLIT && S <= p.KB; ++S) {
-    const long long units = tiles * S, rounds = (units + HD_PLAN_SMS - 1) / HD_PLAN_SMS;
-    if (S > 1 && (units * p.nt * HD_I * 4 > (128ll << 20))) break;
-    const double stage = 0.25 + 0.75 * p.nt / 256;   // of a full stage: A's copy counts too
-    const double cost = (double)rounds * (((p.KB + S - 1) / S + 2.0) * stage + (S > 1 ? 4.0 * p.nt / 256 : 0)) +
-                        (S > 1 ? 10.0 + 0.1 * units * p.nt / 256 : 0);
-    if (S == 1 || cost < best) best = cost, p.S = S;
-  }
-  p.units = tiles * p.S;
-  p.part_bytes = p.S > 1 ? align256((size_t)p.units * p.nt * HD_I * 4) : 0;
+  const long long tiles = (long long)p.tiles_i / ctas * p.tiles_j, total = tiles * p.KB;
+  // Costs in stages of 0.27 us, a pair's stage at the tensor cores' full rate.
+  // Measured: a lone CTA's stage of nt = 256 takes 1.6 of them, a pair's 1.05 to
+  // 1.5; where A comes from HBM for one column of tiles alone, 16 KB of a stage
+  // take 1.35. Partials go out beside the next stretch, the join costs a launch.
+  const double full = (double)p.nt / 256;
+  const double stage = std::max(pair ? 0.45 + 0.75 * full : 0.3 + 1.3 * full, 1.35 / p.tiles_j);
+  const double whole = (double)((tiles + slots - 1) / slots) * (p.KB + 0.5) * stage;
+  const long long runs = std::min<long long>(slots, std::max<long long>(1, total / 2));
+  const double even = (double)total / runs * stage + 4.0 * full + 12.0 + 6.0 * full;
+  // whole tiles also share their operands in L2 better: a tenth has to be won
+  p.runs = 1.1 * even < whole && runs > 1 && total < (1ll << 30) ? (int)runs : 0;
+  p.part_bytes = p.runs ? align256((size_t)2 * p.runs * ctas * p.nt * HD_I * 4) : 0;
+  *cost_out = p.runs ? even : whole;
   return p;
+}
+
+Plan make_plan(long long I, long long J, long long R, bool b_mn) {
+  double one = 0, two = 0;
+  const Plan p1 = plan_of(I, J, R, b_mn, false, &one), p2 = plan_of(I, J, R, b_mn, true, &two);
+  return I > HD_I && two < one ? p2 : p1;
+}
+
+// CTAs of a launch: whole tiles over the SMs there are, or one (pair) per run.
+long long ctas_of(const Plan &p, int sms) {
+  const int ctas = p.pair ? 2 : 1;
+  if (p.runs) return (long long)p.runs * ctas;
+  return std::min<long long>((long long)p.tiles_i * p.tiles_j, sms / ctas * ctas);
+}
+
+template <bool A_MN, bool B_MN, bool PAIR>
+int launch_tiles(const Plan &p, const CUtensorMap &ma, const CUtensorMap &mb, HeadArgs a, int sms, cudaStream_t st) {
+  const int stage = HD_A_BYTES + p.nt / (PAIR ? 2 : 1) * HD_R * 2;
+  a.stages = std::min(HD_MAX_STAGES, HD_SMEM / stage);
+  const int smem = a.stages * stage + HD_STAGING + 1024;
+  const auto kern = k_head<A_MN, B_MN, PAIR>;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)ctas_of(p, sms), 1, 1);
+  cfg.blockDim = dim3(HD_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = PAIR ? 2 : 1;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = PAIR ? 1 : 0;
+  static SmemLimit limit;
+  return launch_retry(limit, (const void *)kern, smem,
+                      [&]() { return cudaLaunchKernelEx(&cfg, kern, ma, mb, (const HeadArgs)a); });
 }
 
 template <bool A_MN, bool B_MN>
 int launch_head(const Plan &p, const CUtensorMap &ma, const CUtensorMap &mb, HeadArgs a, cudaStream_t st) {
-  a.tiles_i = p.tiles_i, a.tiles_j = p.tiles_j, a.S = p.S, a.KB = p.KB, a.nt = p.nt;
-  a.units = (int)p.units;
-  const int stage = HD_A_BYTES + p.nt * HD_R * 2;
-  a.stages = std::min(HD_MAX_STAGES, HD_SMEM / stage);
-  const int smem = a.stages * stage + HD_STAGING + 1024;
+  a.tiles_i = p.tiles_i, a.tiles_j = p.tiles_j, a.KB = p.KB, a.nt = p.nt, a.runs = p.runs;
+  if (p.runs) {
+    const int total = p.tiles_i / (p.pair ? 2 : 1) * p.tiles_j * p.KB;
+    a.run_len = total / p.runs, a.longer = total % p.runs;
+  }
   a.vec = a.I % 8 == 0 && a.ldo % 8 == 0 && aligned(a.bias, 16) && aligned(a.residual, 16);
   const int sms = num_sms();
   if (sms <= 0) return SPEC_ERR_CUDA;
-  if (cudaFuncSetAttribute(k_head<A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-      cudaSuccess)
-    return SPEC_ERR_CUDA;
-  k_head<A_MN, B_MN><<<(unsigned)std::min<long long>(p.units, sms), HD_THREADS, smem, st>>>(ma, mb, a);
-  int rc = launched();
-  if (rc == SPEC_OK && p.S > 1) {
-    const long long n = (long long)p.tiles_i * p.tiles_j * p.nt * (HD_I / 8);
-    k_head_join<<<(unsigned)std::min<long long>((n + 255) / 256, 8ll * sms), 256, 0, st>>>(a);
+  int rc = p.pair ? launch_tiles<A_MN, B_MN, true>(p, ma, mb, a, sms, st)
+                  : launch_tiles<A_MN, B_MN, false>(p, ma, mb, a, sms, st);
+  if (rc == SPEC_OK && p.runs) {
+    const dim3 grid((unsigned)(p.tiles_i * p.tiles_j), (unsigned)((p.nt + 15) / 16));
+    k_head_join<<<grid, 256, 0, st>>>(a, p.pair ? 2 : 1);
     rc = launched();
   }
   return rc;
+}
+
+template <int M>
+int launch_few(const HeadArgs &a, const void *x, const void *w, int K, cudaStream_t st) {
+  const int smem = M * ((std::min(K, HD_FEW_K) + 7) & ~7) * 4;
+  const auto kern = K % 8 == 0 ? k_head_few<M, true> : k_head_few<M, false>;
+  const int sms = num_sms();
+  if (sms <= 0) return SPEC_ERR_CUDA;
+  static SmemLimit limit[2];
+  return launch_retry(limit[K % 8 == 0], (const void *)kern, smem, [&]() {
+    kern<<<std::min((a.I + 8 * HD_N - 1) / (8 * HD_N), HD_FEW_CTAS * sms), 256, smem, st>>>(
+        a, static_cast<const uint16_t *>(x), static_cast<const uint16_t *>(w), K);
+    return cudaGetLastError();
+  });
 }
 
 inline long long round8(long long x) { return (x + 7) / 8 * 8; }
@@ -601,7 +849,7 @@ extern "C" int spec_head_forward(const void *x, const void *weight, const void *
   if (workspace == nullptr || !aligned(workspace, 256) || ws_bytes < forward_bytes(M, N, K))
     return SPEC_ERR_WORKSPACE;
   const Plan p = make_plan(N, std::max(M, 1), K, false);
-  if (p.units > 0x7fffffffll) return SPEC_ERR_UNSUPPORTED;
+  if ((long long)p.tiles_i * p.tiles_j > 0x7fffffffll) return SPEC_ERR_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char *ws = static_cast<char *>(workspace);
   if (M == 0) return reset_header(ws, st);
@@ -616,12 +864,15 @@ extern "C" int spec_head_forward(const void *x, const void *weight, const void *
   a.pre = static_cast<__nv_bfloat16 *>(pre);
   a.act = act;
   a.reset = 1;
+  if (M <= HD_FEW)
+    return M == 1 ? launch_few<1>(a, x, weight, K, st) : M == 2 ? launch_few<2>(a, x, weight, K, st)
+                                                                : launch_few<4>(a, x, weight, K, st);
   int rc;
   if ((rc = operand(&x, M, K, &ws, st)) != SPEC_OK || (rc = operand(&weight, N, K, &ws, st)) != SPEC_OK)
     return rc;
   CUtensorMap ma, mb;
   if ((rc = make_map(&ma, weight, N, K, round8(K), HD_I)) != SPEC_OK ||
-      (rc = make_map(&mb, x, M, K, round8(K), p.nt)) != SPEC_OK)
+      (rc = make_map(&mb, x, M, K, round8(K), p.pair ? p.nt / 2 : p.nt)) != SPEC_OK)
     return rc;
   return launch_head<false, false>(p, ma, mb, a, st);
 }
@@ -645,7 +896,8 @@ extern "C" int spec_head_backward(const void *dy, const void *x, const void *wei
     return SPEC_ERR_WORKSPACE;
   const int m = std::max(M, 1);
   const Plan px = make_plan(K, m, N, false), pw = make_plan(K, N, m, true);
-  if (px.units > 0x7fffffffll || pw.units > 0x7fffffffll) return SPEC_ERR_UNSUPPORTED;
+  if ((long long)px.tiles_i * px.tiles_j > 0x7fffffffll || (long long)pw.tiles_i * pw.tiles_j > 0x7fffffffll)
+    return SPEC_ERR_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char *ws = static_cast<char *>(workspace);
   HeadArgs a{};
@@ -689,7 +941,7 @@ extern "C" int spec_head_backward(const void *dy, const void *x, const void *wei
   if (dx != nullptr) {
     if ((rc = operand(&weight, N, K, &ws, st)) != SPEC_OK) return rc;
     if ((rc = make_map(&ma, weight, N, K, ldk, 64)) != SPEC_OK ||
-        (rc = make_map(&mb, gz, M, N, ldz, px.nt)) != SPEC_OK)
+        (rc = make_map(&mb, gz, M, N, ldz, px.pair ? px.nt / 2 : px.nt)) != SPEC_OK)
       return rc;
     a.I = K, a.J = M, a.ldo = K;
     a.out = static_cast<__nv_bfloat16 *>(dx);

@@ -41,6 +41,8 @@ FORWARD = [
     (5, 63, 77, "silu", 1, 1), (1, 1, 1, "none", 1, 1), (2, 9, 4099, "none", 0, 1),
     (100, 300, 520, "gelu", 0, 1), (257, 320, 1000, "silu", 1, 1), (300, 2880, 260, "none", 1, 0),
     (513, 65, 200, "gelu", 1, 1), (700, 1024, 6000, "none", 0, 0), (129, 8192, 128, "silu", 1, 0),
+    (1100, 512, 9000, "gelu", 1, 1), (600, 200, 20001, "silu", 1, 1), (256, 4096, 8192, "none", 0, 0),
+    (2, 5000, 3000, "gelu", 1, 1), (4, 4104, 999, "silu", 1, 0), (3, 9001, 70, "none", 1, 1), (5, 4096, 32000, "none", 0, 0),
 ]
 
 
@@ -69,6 +71,7 @@ BACKWARD = [
     (1, 64, 64, "none"), (1, 256, 1000, "silu"), (7, 63, 65, "gelu"), (16, 520, 384, "none"),
     (100, 300, 520, "silu"), (257, 320, 1000, "gelu"), (300, 136, 2881, "none"), (513, 65, 200, "silu"),
     (64, 1024, 4096, "none"), (1000, 128, 3000, "silu"), (1, 1, 1, "gelu"), (2000, 200, 72, "none"),
+    (900, 1100, 6000, "silu"), (513, 2050, 3001, "none"), (1024, 1024, 4096, "gelu"),
 ]
 
 
