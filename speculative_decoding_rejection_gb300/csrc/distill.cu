@@ -19,7 +19,10 @@
 //
 // Other calls (few positions, rows that bulk copies cannot address or a cluster
 // cannot hold) run as one launch with a cluster per position (k_distill): each
-// CTA passes over its slice twice, the second time from L2.
+// CTA passes over its slice twice, the second time from L2. Vectors lie on the
+// draft row's 16-byte grid, which is the gradient's too; a target row on another
+// grid is put together from two vectors by shifts (64 requests of 32003 bf16
+// logits: 19 us, element by element 23 us).
 //
 // Measured at 4096 positions of 201088 bf16 logits, 3/4 of them weighted: 0.81 ms
 // (5.1 TB/s of the bytes that have to move); a cluster per position 1.06 ms (1.18 ms with its slices in shared memory but no
@@ -120,19 +123,25 @@ __device__ __forceinline__ void store1(char *row, int i, float g) {
   else GST(reinterpret_cast<float *>(row) + i, g);
 }
 
-// 2 N elements of both rows, DI_THREADS apart; -inf behind the row's end.
-template <bool BF16, int N>
-__device__ __forceinline__ void load_scalars(const char *trow, const char *drow, int i0, int end, f32x2 *zt,
-                                             f32x2 *zd) {
-  float xt[2 * N], xd[2 * N];
+// 16 bytes from `shift` bytes into the 32 of two vectors (0 < shift < 16, whole
+// elements).
+__device__ __forceinline__ uint4 shift16(const uint4 &a, const uint4 &b, int shift) {
+  uint32_t w[7] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z};
+  const uint32_t last = b.w;
+  if (shift & 8) {
 #pragma unroll
-  for (int j = 0; j < 2 * N; ++j) {
-    const int i = i0 + j * DI_THREADS;
-    xt[j] = i < end ? load1<BF16>(trow, i) : -INFINITY;
-    xd[j] = i < end ? load1<BF16>(drow, i) : -INFINITY;
+    for (int j = 0; j < 5; ++j) w[j] = w[j + 2];
+    w[5] = last;
   }
+  if (shift & 4) {
 #pragma unroll
-  for (int j = 0; j < N; ++j) zt[j] = pk2(xt[2 * j], xt[2 * j + 1]), zd[j] = pk2(xd[2 * j], xd[2 * j + 1]);
+    for (int j = 0; j < 5; ++j) w[j] = w[j + 1];
+  }
+  if (shift & 2) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // The thread's maxima become at least mt and md. s.A is kept as the sum of
@@ -154,12 +163,13 @@ template <int N>
 __device__ __forceinline__ void add_pairs(PairStat &s, const f32x2 *xt, const f32x2 *xd, float c) {
   const f32x2 cc = pk2(c, c), minus = pk2(-1.f, -1.f);
   f32x2 St = 0, Sd = 0, A = 0;   // pairs of +0
+  f32x2 et[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    const f32x2 et = ex2_2(mul2(xt[j], cc)), ed = ex2_2(mul2(xd[j], cc));
-    St = add2(St, et);
-    Sd = add2(Sd, ed);
-    A = fma2(et, fma2(xd[j], minus, xt[j]), A);
+    et[j] = ex2_2(mul2(xt[j], cc));
+    St = add2(St, et[j]);
+    Sd = add2(Sd, ex2_2(mul2(xd[j], cc)));
+    A = fma2(et[j], fma2(xd[j], minus, xt[j]), A);
   }
   s.St += lo2(St) + hi2(St);
   s.Sd += lo2(Sd) + hi2(Sd);
@@ -168,9 +178,8 @@ __device__ __forceinline__ void add_pairs(PairStat &s, const f32x2 *xt, const f3
     a = 0.f;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const f32x2 et = ex2_2(mul2(xt[j], cc));
-      if (lo2(et) > 0.f) a += lo2(et) * (lo2(xt[j]) - lo2(xd[j]));
-      if (hi2(et) > 0.f) a += hi2(et) * (hi2(xt[j]) - hi2(xd[j]));
+      if (lo2(et[j]) > 0.f) a += lo2(et[j]) * (lo2(xt[j]) - lo2(xd[j]));
+      if (hi2(et[j]) > 0.f) a += hi2(et[j]) * (hi2(xt[j]) - hi2(xd[j]));
     }
   }
   s.A += a;
@@ -275,8 +284,8 @@ __device__ int find_request(const int32_t *cu, int B, int r, int *slot) {
   return -1;
 }
 
-// A cluster per position. VEC: the rows are 16-byte aligned.
-template <bool BF16, bool VEC>
+// A cluster per position.
+template <bool BF16>
 __global__ void __launch_bounds__(DI_THREADS) k_distill(DistillArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -300,9 +309,6 @@ __global__ void __launch_bounds__(DI_THREADS) k_distill(DistillArgs a) {
     if (bad) set_status(a.hdr, SPEC_ERR_INVALID_ARG, 0);
   }
   float w = a.weight ? GLD(a.weight + r) : 1.f;
-  // this CTA's part of the row, in units of 16 bytes or of elements
-  const int units = VEC ? a.V / PER : a.V;
-  const int u0 = (int)((long long)units * rank / C), u1 = (int)((long long)units * (rank + 1) / C);
   char *grow = a.grad ? static_cast<char *>(a.grad) + (long long)r * a.V * ES : nullptr;
   const int b = w != 0.f ? find_request(a.cu, a.B, r, &s_slot) : 0;
   const float T0 = a.temp && b >= 0 && w != 0.f ? GLD(a.temp + b) : 1.f;
@@ -310,33 +316,50 @@ __global__ void __launch_bounds__(DI_THREADS) k_distill(DistillArgs a) {
     if (t == 0) set_status(a.hdr, SPEC_ERR_INVALID_ARG, r);
     w = 0.f;
   }
+  const char *drow = static_cast<const char *>(a.draft) + (long long)r * a.V * ES;
+  const char *trow = static_cast<const char *>(a.target) + (long long)(r + max(b, 0)) * a.V * ES;
+  // `head` elements, nv vectors of the draft row's grid, and the rest
+  const int head = min(a.V, (int)((16 - ((uintptr_t)drow & 15)) & 15) / ES);
+  const char *tv = trow + (long long)head * ES;
+  const int shift = (int)((uintptr_t)tv & 15);
+  tv -= shift;
+  int nv = (a.V - head) / PER;
+  if (shift != 0) nv = max(0, min(nv, (int)((trow + (long long)a.V * ES - tv) / 16) - 1));
+  const uint4 *dvec = reinterpret_cast<const uint4 *>(drow + (long long)head * ES);
+  const uint4 *tvec = reinterpret_cast<const uint4 *>(tv);
+  uint4 *gvec = reinterpret_cast<uint4 *>(grow + (long long)head * ES);
+  const int v0 = (int)((long long)nv * rank / C), v1 = (int)((long long)nv * (rank + 1) / C);
+  // what no vector has goes to the last CTA, an element per thread, else -1
+  const int rest = a.V - nv * PER;
+  const int single = rank == C - 1 && t < rest ? (t < head ? t : t + nv * PER) : -1;
   if (w == 0.f) {   // the whole cluster leaves: nobody waits for its statistics
     if (rank == 0 && t == 0) GST(a.loss + r, 0.f);
     if (grow != nullptr) {
-      for (int i = u0 + t; i < u1; i += DI_THREADS) {
-        if (VEC) GST(reinterpret_cast<uint4 *>(grow) + i, make_uint4(0, 0, 0, 0));
-        else store1<BF16>(grow, i, 0.f);
-      }
+      for (int i = v0 + t; i < v1; i += DI_THREADS) GST(gvec + i, make_uint4(0, 0, 0, 0));
+      if (single >= 0) store1<BF16>(grow, single, 0.f);
     }
     return;
   }
   const float T = T0 < SPEC_GREEDY_T ? 1.f : T0;
   const float c = LOG2E / T;
-  const char *trow = static_cast<const char *>(a.target) + (long long)(r + b) * a.V * ES;
-  const char *drow = static_cast<const char *>(a.draft) + (long long)r * a.V * ES;
+  auto target16 = [&](int i) -> uint4 {
+    const uint4 x = GLD(tvec + i);
+    return shift == 0 ? x : shift16(x, GLD(tvec + i + 1), shift);
+  };
   PairStat s{NO_MAX, 0.f, 0.f, NO_MAX, 0.f};
-  if (VEC) {
-    for (int i = u0 + t; i < u1; i += DI_THREADS) {
-      const uint4 wt = GLD(reinterpret_cast<const uint4 *>(trow) + i);
-      const uint4 wd = GLD(reinterpret_cast<const uint4 *>(drow) + i);
-      add_stats<BF16, 1>(s, &wt, &wd, c);
-    }
-  } else {
-    for (int i = u0 + t; i < u1; i += 8 * DI_THREADS) {
-      f32x2 zt[4], zd[4];
-      load_scalars<BF16, 4>(trow, drow, i, u1, zt, zd);
-      add_stats<4>(s, zt, zd, c);
-    }
+  int i = v0 + t;
+  for (; i + DI_THREADS < v1; i += 2 * DI_THREADS) {
+    const uint4 wd[2] = {GLD(dvec + i), GLD(dvec + i + DI_THREADS)};
+    const uint4 wt[2] = {target16(i), target16(i + DI_THREADS)};
+    add_stats<BF16, 2>(s, wt, wd, c);
+  }
+  if (i < v1) {
+    const uint4 wd = GLD(dvec + i), wt = target16(i);
+    add_stats<BF16, 1>(s, &wt, &wd, c);
+  }
+  if (single >= 0) {
+    const f32x2 zt = pk2(load1<BF16>(trow, single), -INFINITY), zd = pk2(load1<BF16>(drow, single), -INFINITY);
+    add_stats<1>(s, &zt, &zd, c);
   }
   s.A += s.St * (s.mt - s.md);
   warp_merge(s, c);
@@ -360,27 +383,19 @@ __global__ void __launch_bounds__(DI_THREADS) k_distill(DistillArgs a) {
   }
   if (grow != nullptr) {
     const GradK g = grad_of(s, c, w / T);
-    if (VEC) {
-      for (int i = u0 + t; i < u1; i += DI_THREADS) {
-        f32x2 xt[N], xd[N], o[N];
-        minus16<BF16>(GLD(reinterpret_cast<const uint4 *>(trow) + i), g.mt, xt);
-        minus16<BF16>(GLD(reinterpret_cast<const uint4 *>(drow) + i), g.md, xd);
-        gradient<N>(g, xt, xd, o);
-        GST(reinterpret_cast<uint4 *>(grow) + i, empty ? make_uint4(0, 0, 0, 0) : pack16<BF16>(o));
-      }
-    } else {
-      for (int i = u0 + t; i < u1; i += 8 * DI_THREADS) {
-        f32x2 xt[4], xd[4], o[4];
-        load_scalars<BF16, 4>(trow, drow, i, u1, xt, xd);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) xt[j] = add2(xt[j], pk2(-g.mt, -g.mt)), xd[j] = add2(xd[j], pk2(-g.md, -g.md));
-        gradient<4>(g, xt, xd, o);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int e = i + j * DI_THREADS;
-          if (e < u1) store1<BF16>(grow, e, empty ? 0.f : j & 1 ? hi2(o[j / 2]) : lo2(o[j / 2]));
-        }
-      }
+#pragma unroll 2
+    for (int i = v0 + t; i < v1; i += DI_THREADS) {
+      f32x2 xt[N], xd[N], o[N];
+      minus16<BF16>(target16(i), g.mt, xt);
+      minus16<BF16>(GLD(dvec + i), g.md, xd);
+      gradient<N>(g, xt, xd, o);
+      GST(gvec + i, empty ? make_uint4(0, 0, 0, 0) : pack16<BF16>(o));
+    }
+    if (single >= 0) {
+      const f32x2 xt = pk2(load1<BF16>(trow, single) - g.mt, 0.f), xd = pk2(load1<BF16>(drow, single) - g.md, 0.f);
+      f32x2 o;
+      gradient<1>(g, &xt, &xd, &o);
+      store1<BF16>(grow, single, empty ? 0.f : lo2(o));
     }
   }
   cluster.sync();   // no CTA leaves while a peer may still read its statistics
@@ -695,7 +710,7 @@ int launch_resident(ResidentArgs a, cudaStream_t st) {
   return launch_retry(limit, (const void *)kern, smem, [&]() { return cudaLaunchKernelEx(&cfg, kern, a); });
 }
 
-template <bool BF16, bool VEC>
+template <bool BF16>
 int launch_distill(const DistillArgs &a, int C, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)a.R * C, 1, 1);
@@ -708,7 +723,7 @@ int launch_distill(const DistillArgs &a, int C, cudaStream_t st) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, k_distill<BF16, VEC>, a) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, k_distill<BF16>, a) != cudaSuccess) return SPEC_ERR_CUDA;
   return launched();
 }
 
@@ -778,7 +793,6 @@ extern "C" int spec_distill_loss(const void *target, const void *draft, int dt, 
   }
   // each position over as many SMs as there are, down to slices of 4 KB
   int C = 1;
-  while (C < DI_MAX_CLUSTER && (long long)R_d * C < 4 * num_sms() && 2ll * V * es / C > 8192) C *= 2;
-  if (dt == SPEC_BF16) return vec ? launch_distill<true, true>(a, C, st) : launch_distill<true, false>(a, C, st);
-  return vec ? launch_distill<false, true>(a, C, st) : launch_distill<false, false>(a, C, st);
+  while (C < DI_MAX_CLUSTER && (long long)R_d * C < 2 * num_sms() && 2ll * V * es / C > 8192) C *= 2;
+  return dt == SPEC_BF16 ? launch_distill<true>(a, C, st) : launch_distill<false>(a, C, st);
 }

@@ -587,7 +587,9 @@ __global__ void k_pad_rows(const uint16_t *src, uint16_t *dst, long long rows, i
 constexpr int HD_DZ_ROWS = 64;
 template <int VEC>
 __global__ void __launch_bounds__(256)
-    k_dz(const uint16_t *dy, const uint16_t *pre, uint16_t *dz, float *psum, int M, int N, int ld, int act) {
+    k_dz(const uint16_t *dy, const uint16_t *pre, uint16_t *dz, float *psum, int M, int N, int ld, int act,
+         WsHeader *hdr) {
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) hdr->status = SPEC_OK, hdr->detail = -1;
   __shared__ float sums[8][32 * VEC + 1];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int c0 = (blockIdx.x * 32 + cx) * VEC;
@@ -902,15 +904,16 @@ extern "C" int spec_head_backward(const void *dy, const void *x, const void *wei
   char *ws = static_cast<char *>(workspace);
   HeadArgs a{};
   a.hdr = reinterpret_cast<WsHeader *>(ws);
-  if (reset_header(ws, st) != SPEC_OK) return SPEC_ERR_CUDA;
   ws += sizeof(WsHeader);
   a.part = reinterpret_cast<float *>(ws);
   ws += std::max(px.part_bytes, pw.part_bytes);
   if (M == 0) {   // no rows: the weights' gradients are zero
+    if (reset_header(workspace, st) != SPEC_OK) return SPEC_ERR_CUDA;
     if (dw && cudaMemsetAsync(dw, 0, (size_t)N * K * 2, st) != cudaSuccess) return SPEC_ERR_CUDA;
     if (db && cudaMemsetAsync(db, 0, (size_t)N * 4, st) != cudaSuccess) return SPEC_ERR_CUDA;
     return SPEC_OK;
   }
+  if (dx == nullptr && dw == nullptr && db == nullptr) return reset_header(workspace, st);
   int rc;
   // dz: dy itself where no activation changes it and TMA can address its rows
   const int ldz = (int)round8(N);
@@ -925,17 +928,17 @@ extern "C" int spec_head_backward(const void *dy, const void *x, const void *wei
     const int vec = N % 8 == 0 ? 8 : 1;
     const dim3 grid((unsigned)((ldz + 32 * vec - 1) / (32 * vec)), (unsigned)dz_segments(M));
     if (grid.y > 65535) return SPEC_ERR_UNSUPPORTED;
-    if (vec == 8)
-      k_dz<8><<<grid, 256, 0, st>>>(g, z, own_dz ? dz : nullptr, db ? psum : nullptr, M, N, ldz, act);
-    else
-      k_dz<1><<<grid, 256, 0, st>>>(g, z, own_dz ? dz : nullptr, db ? psum : nullptr, M, N, ldz, act);
+    float *sums = db == nullptr ? nullptr : grid.y == 1 ? db : psum;   // one segment: the sums themselves
+    if (vec == 8) k_dz<8><<<grid, 256, 0, st>>>(g, z, own_dz ? dz : nullptr, sums, M, N, ldz, act, a.hdr);
+    else k_dz<1><<<grid, 256, 0, st>>>(g, z, own_dz ? dz : nullptr, sums, M, N, ldz, act, a.hdr);
     if ((rc = launched()) != SPEC_OK) return rc;
-    if (db != nullptr) {
+    if (sums == psum && db != nullptr) {
       k_db<<<(N + 255) / 256, 256, 0, st>>>(psum, db, N, dz_segments(M));
       if ((rc = launched()) != SPEC_OK) return rc;
     }
   }
   const void *gz = own_dz ? dz : dy;
+  a.reset = !own_dz && db == nullptr;   // the call's first launch sets the status
   const long long ldk = round8(K);
   CUtensorMap ma, mb;
   if (dx != nullptr) {
@@ -946,6 +949,7 @@ extern "C" int spec_head_backward(const void *dy, const void *x, const void *wei
     a.I = K, a.J = M, a.ldo = K;
     a.out = static_cast<__nv_bfloat16 *>(dx);
     if ((rc = launch_head<true, false>(px, ma, mb, a, st)) != SPEC_OK) return rc;
+    a.reset = 0;
   }
   if (dw != nullptr) {
     if ((rc = operand(&x, M, K, &ws, st)) != SPEC_OK) return rc;

@@ -73,6 +73,11 @@ CASES = [
     ("f32 two CTAs", dict(V=5000, K=[2, 1], dtype=torch.float32)),
     ("f32 eight CTAs", dict(V=20000, K=[2, 1], dtype=torch.float32)),
     ("bf16", dict(V=1000, K=[3, 2], dtype=torch.bfloat16)),
+    ("bf16 shifts", dict(V=1009, K=[3, 4, 2, 5, 3], dtype=torch.bfloat16)),
+    ("bf16 even shifts", dict(V=2050, K=[1, 2, 1, 3, 1, 2, 2, 1, 1], dtype=torch.bfloat16)),
+    ("f32 shifts", dict(V=1022, K=[1, 3, 1, 2, 2], dtype=torch.float32)),
+    ("few tokens", dict(V=9, K=[1, 3, 2, 4, 2], dtype=torch.bfloat16)),
+    ("fewer than a vector", dict(V=3, K=[2, 3, 2], dtype=torch.float32)),
     ("bf16 odd", dict(V=32003, K=[1, 2], dtype=torch.bfloat16)),
     ("bf16 cluster", dict(V=32008, K=[2, 2], dtype=torch.bfloat16)),
     ("masked", dict(V=9000, K=[2, 3], dtype=torch.bfloat16, masked=0.6)),

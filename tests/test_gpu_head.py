@@ -106,6 +106,14 @@ def test_backward_parts_alone():
             assert part[i] is None if i != k else torch.equal(part[i], full[i])
 
 
+def test_backward_of_nothing_is_ok():
+    x, w = torch.ones(3, 64, dtype=torch.bfloat16, device=DEV), torch.ones(8, 64, dtype=torch.bfloat16, device=DEV)
+    ws = torch.full((1 << 16,), 255, dtype=torch.uint8, device=DEV)
+    assert sv.spec_head_backward_workspace(3, 8, 64) <= ws.numel()
+    sv.spec_head_backward(x[:, :8].contiguous(), x, w, out=(None, None, None), workspace=ws)
+    assert sv.spec_get_status(ws) == sv.SPEC_OK
+
+
 def test_no_rows():
     x, w = torch.zeros(0, 64, dtype=torch.bfloat16, device=DEV), torch.ones(40, 64, dtype=torch.bfloat16, device=DEV)
     y, _, ws = sv.spec_head_forward(x, w)
