@@ -123,27 +123,6 @@ __device__ __forceinline__ void store1(char *row, int i, float g) {
   else GST(reinterpret_cast<float *>(row) + i, g);
 }
 
-// 16 bytes from `shift` bytes into the 32 of two vectors (0 < shift < 16, whole
-// elements).
-__device__ __forceinline__ uint4 shift16(const uint4 &a, const uint4 &b, int shift) {
-  uint32_t w[7] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z};
-  const uint32_t last = b.w;
-  if (shift & 8) {
-#pragma unroll
-    for (int j = 0; j < 5; ++j) w[j] = w[j + 2];
-    w[5] = last;
-  }
-  if (shift & 4) {
-#pragma unroll
-    for (int j = 0; j < 5; ++j) w[j] = w[j + 1];
-  }
-  if (shift & 2) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], 16);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // The thread's maxima become at least mt and md. s.A is kept as the sum of
 // e_t ((z_t - m_t) - (z_d - m_d)) at the thread's own maxima.
 __device__ __forceinline__ void raise(PairStat &s, float mt, float md, float c) {

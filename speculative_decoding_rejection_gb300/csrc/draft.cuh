@@ -21,6 +21,27 @@ __device__ __forceinline__ uint32_t f32_to_bf16_bits(float v) {
   return f32x2_to_bf16x2(v, 0.f) & 0xffffu;
 }
 
+// 16 bytes from `shift` bytes into the 32 of two vectors (0 < shift < 16, whole
+// elements).
+__device__ __forceinline__ uint4 shift16(const uint4 &a, const uint4 &b, int shift) {
+  uint32_t w[7] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z};
+  const uint32_t last = b.w;
+  if (shift & 8) {
+#pragma unroll
+    for (int j = 0; j < 5; ++j) w[j] = w[j + 2];
+    w[5] = last;
+  }
+  if (shift & 4) {
+#pragma unroll
+    for (int j = 0; j < 5; ++j) w[j] = w[j + 1];
+  }
+  if (shift & 2) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Bounded wait for a phase of a shared-memory barrier; CLUSTER: acquires what
 // other CTAs of the cluster released. As mbar_wait_bounded, but the timer, whose
 // reads take longer than a ring stage, is looked at after every 64 tries only.

@@ -20,8 +20,8 @@
 // six stages instead of four cover the copies' latency.
 //
 // A persistent CTA per SM: one warp feeds a ring of TMA stages (64 of r each),
-// one issues tcgen05.mma, four run the epilogue from the other of two
-// accumulators. Where whole tiles would leave SMs idle in the last round, all
+// one issues tcgen05.mma, eight run the epilogue from the other of two
+// accumulators (four, one per scheduler, took twice as long with an activation). Where whole tiles would leave SMs idle in the last round, all
 // tiles' stages are laid end to end and every CTA takes an equal run of them: what
 // it has of a tile that it shares goes out as an f32 partial, and a second launch
 // over all SMs adds the partials of a tile in the order of r and runs the
@@ -32,18 +32,19 @@
 #include "draft.cuh"
 
 #include <algorithm>
-#include <type_traits>
 
 namespace sv {
 namespace {
 
-constexpr int HD_THREADS = 192;   // warps 0-3 epilogue, 4 TMA, 5 MMA
+constexpr int HD_EPI = 8;         // epilogue warps: two per 32 TMEM lanes, on every other 32 columns
+constexpr int HD_TMA = HD_EPI, HD_MMA = HD_EPI + 1;   // the other two warps
+constexpr int HD_THREADS = 32 * (HD_EPI + 2);
 constexpr int HD_I = 128;         // rows of a tile (TMEM lanes)
 constexpr int HD_R = 64;          // reduction elements of a stage (128 bytes)
 constexpr int HD_MAX_J = 256;     // columns of a tile
 constexpr int HD_MAX_STAGES = 12;
 constexpr int HD_STAGE_LD = 36;       // floats between columns of a warp's staging (no bank conflicts)
-constexpr int HD_STAGING = 4 * 32 * HD_STAGE_LD * 4;   // four warps, 32 columns of 32 lanes
+constexpr int HD_STAGING = HD_EPI * 16 * HD_STAGE_LD * 4;   // 16 columns of 32 lanes per warp
 constexpr int HD_SMEM = 226 * 1024 - HD_STAGING - 1024;   // ring
 constexpr int HD_PLAN_SMS = 152;      // SMs the split is planned for
 constexpr int HD_A_BYTES = HD_I * HD_R * 2;
@@ -200,37 +201,54 @@ __device__ __forceinline__ uint4 pack8(const float *x) {
                     f32x2_to_bf16x2(x[4], x[5]), f32x2_to_bf16x2(x[6], x[7]));
 }
 
-// The epilogue of 8 elements i .. i+7 of column j: bias, activation,
-// residual, one rounding to bf16.
-__device__ __forceinline__ void finish8(const HeadArgs &a, float *z, int i, int j) {
+// The epilogue of 8 elements i .. i+7 of column j: bias, activation, residual,
+// one rounding to bf16. For results whose rows are 16-byte aligned (a.vec). The
+// residual is loaded ahead (residual8), as its latency is a tile's stages.
+__device__ __forceinline__ uint4 residual8(const HeadArgs &a, int i, int j) {
+  if (a.residual == nullptr || j >= a.J || i >= a.I) return make_uint4(0, 0, 0, 0);
+  return *reinterpret_cast<const uint4 *>(a.residual + (long long)j * a.ldo + i);
+}
+__device__ __forceinline__ void finish8(const HeadArgs &a, float *z, int i, int j, const uint4 &res) {
   if (j >= a.J || i >= a.I) return;
   const long long at = (long long)j * a.ldo + i;
-  if (a.vec) {   // I is a multiple of 8 then
-    float x[8];
-    if (a.bias) {
-      unpack8(*reinterpret_cast<const uint4 *>(a.bias + i), x);
+  float x[8];
+  if (a.bias) {
+    unpack8(*reinterpret_cast<const uint4 *>(a.bias + i), x);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) z[q] += x[q];
-    }
-    if (a.pre) *reinterpret_cast<uint4 *>(a.pre + at) = pack8(z);
-    if (a.act != SPEC_ACT_NONE) {
+    for (int q = 0; q < 8; ++q) z[q] += x[q];
+  }
+  if (a.pre) *reinterpret_cast<uint4 *>(a.pre + at) = pack8(z);
+  if (a.act != SPEC_ACT_NONE) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) z[q] = act_value(z[q], a.act);
-    }
-    if (a.residual) {
-      unpack8(*reinterpret_cast<const uint4 *>(a.residual + at), x);
+    for (int q = 0; q < 8; ++q) z[q] = act_value(z[q], a.act);
+  }
+  if (a.residual) {
+    unpack8(res, x);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) z[q] += x[q];
-    }
-    *reinterpret_cast<uint4 *>(a.out + at) = pack8(z);
-  } else {
+    for (int q = 0; q < 8; ++q) z[q] += x[q];
+  }
+  *reinterpret_cast<uint4 *>(a.out + at) = pack8(z);
+}
+// The same for N columns j .. of element i, for any result: the lanes of a warp
+// take neighbouring i, so an access is 64 bytes of a row.
+template <int N>
+__device__ __forceinline__ void residual_column(const HeadArgs &a, int i, int j, uint16_t *res) {
+  const bool on = a.residual != nullptr && i < a.I;
+  const uint16_t *r = reinterpret_cast<const uint16_t *>(a.residual) + (long long)j * a.ldo + i;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      if (i + q >= a.I) break;
-      const float v = z[q] + (a.bias ? bf16_at(a.bias, i + q) : 0.f);
-      if (a.pre) bf16_to(a.pre, at + q, v);
-      bf16_to(a.out, at + q, act_value(v, a.act) + (a.residual ? bf16_at(a.residual, at + q) : 0.f));
-    }
+  for (int q = 0; q < N; ++q) res[q] = on && j + q < a.J ? r[q * a.ldo] : (uint16_t)0;
+}
+template <int N>
+__device__ __forceinline__ void finish_column(const HeadArgs &a, const float *z, int i, int j, const uint16_t *res) {
+  if (i >= a.I) return;
+  const float bias = a.bias ? bf16_at(a.bias, i) : 0.f;
+  const long long at = (long long)j * a.ldo + i;
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    if (j + q >= a.J) break;
+    const float v = z[q] + bias;
+    if (a.pre) bf16_to(a.pre, at + q * a.ldo, v);
+    bf16_to(a.out, at + q * a.ldo, act_value(v, a.act) + bf16_bits_to_f32(res[q]));
   }
 }
 
@@ -286,10 +304,10 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
     if (blockIdx.x == 0 && a.reset) a.hdr->status = SPEC_OK, a.hdr->detail = -1;
     sh.abort = 0;
     for (int s = 0; s < a.stages; ++s) mbar_init(&sh.full[s], 1), mbar_init(&sh.empty[s], 1);
-    for (int s = 0; s < 2; ++s) mbar_init(&sh.acc_full[s], 1), mbar_init(&sh.acc_empty[s], 4 * CTAS);
+    for (int s = 0; s < 2; ++s) mbar_init(&sh.acc_full[s], 1), mbar_init(&sh.acc_empty[s], HD_EPI * CTAS);
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == HD_MMA) {
     if (PAIR) {
       asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                        smem_u32(&sh.tmem)),
@@ -313,7 +331,7 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
   Walk walk = walk_of(a, a.tiles_i / CTAS * a.tiles_j, g, gridDim.x / CTAS);
   Stretch w;
 
-  if (warp == 4) {
+  if (warp == HD_TMA) {
     if (lane == 0) {
       int it = 0;   // stages filled so far
       while (!*abort && next_stretch(a, walk, w)) {
@@ -350,7 +368,7 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
         set_status(a.hdr, SPEC_ERR_TIMEOUT, 4);
       }
     }
-  } else if (warp == 5) {
+  } else if (warp == HD_MMA) {
     if (lane == 0 && rank == 0) {   // of a pair, the first CTA issues for both
       // f32 accumulator, bf16 operands, which of them are MN-major, N, M
       const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)A_MN << 15) |
@@ -388,6 +406,8 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
       }
     }
   } else {
+    const int quad = warp & 3, half = warp >> 2;   // TMEM lanes, columns
+    const int li = quad * 32 + lane;
     int n = 0;
     for (; next_stretch(a, walk, w); ++n) {
       const int buf = n & 1, i0 = (w.tile / a.tiles_j * CTAS + rank) * HD_I, j0 = w.tile % a.tiles_j * a.nt;
@@ -398,37 +418,66 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
         break;
       }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint32_t d = tmem + buf * (cols / 2) + ((uint32_t)(warp * 32) << 16);
+      const uint32_t d = tmem + buf * (cols / 2) + ((uint32_t)(quad * 32) << 16);
+      const int last = min(a.J, j0 + a.nt);   // columns behind it belong to the next tile
+      constexpr int STEP = HD_EPI / 4 * 32;
       if (w.slot >= 0) {   // 128 bytes per warp and column
-        float *mine = a.part + (long long)(blockIdx.x * 2 + w.slot) * a.nt * HD_I + t;
-        for (int c = 0; c < a.nt; c += 32) {
+        float *mine = a.part + (long long)(blockIdx.x * 2 + w.slot) * a.nt * HD_I + li;
+        for (int c = half * 32; c < a.nt; c += STEP) {
           float v[32];
           tmem_ld32(d + c, v);
 #pragma unroll
           for (int q = 0; q < 32; ++q)
-            if (c + q < a.nt && j0 + c + q < a.J) mine[(c + q) * HD_I] = v[q];
+            if (j0 + c + q < last) mine[(c + q) * HD_I] = v[q];
+        }
+      } else if (!a.vec) {
+        uint16_t next[32];   // the residual of the next columns, on its way
+        residual_column<32>(a, i0 + li, j0 + half * 32, next);
+        for (int c = half * 32; c < a.nt; c += STEP) {
+          float v[32];
+          uint16_t res[32];
+#pragma unroll
+          for (int q = 0; q < 32; ++q) res[q] = next[q];
+          if (c + STEP < a.nt) residual_column<32>(a, i0 + li, j0 + c + STEP, next);
+          tmem_ld32(d + c, v);
+#pragma unroll
+          for (int q = 0; q < 32; q += 8)
+            if (j0 + c + q < last) finish_column<8>(a, v + q, i0 + li, j0 + c + q, res + q);
         }
       } else {
-        // turned through shared memory, 32 columns of the warp's 32 lanes at a
+        // turned through shared memory, 16 columns of the warp's 32 lanes at a
         // time, so that the result leaves in 16-byte stores of 64 bytes a row
-        float *st = staging + warp * 32 * HD_STAGE_LD;
-        for (int c = 0; c < a.nt; c += 32) {
-          float v[32];
-          tmem_ld32(d + c, v);
-          __syncwarp();
+        float *st = staging + warp * 16 * HD_STAGE_LD;
+        const int il = i0 + quad * 32 + lane % 4 * 8;
+        uint4 next[4];   // the residual of the next columns, on its way
 #pragma unroll
-          for (int q = 0; q < 32; ++q) st[q * HD_STAGE_LD + lane] = v[q];
-          __syncwarp();
+        for (int q = 0; q < 4; ++q) next[q] = residual8(a, il, j0 + half * 32 + q * 8 + lane / 4);
+        for (int c = half * 32; c < a.nt; c += STEP) {
+          uint4 res[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int col = q * 8 + lane / 4;
-            float z[8];
+            res[q] = next[q];
+            if (c + STEP < a.nt) next[q] = residual8(a, il, j0 + c + STEP + q * 8 + lane / 4);
+          }
+          float v[32];
+          tmem_ld32(d + c, v);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float4 w = *reinterpret_cast<const float4 *>(st + col * HD_STAGE_LD + lane % 4 * 8 + h * 4);
-              z[4 * h] = w.x, z[4 * h + 1] = w.y, z[4 * h + 2] = w.z, z[4 * h + 3] = w.w;
+          for (int h = 0; h < 2; ++h) {
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 16; ++q) st[q * HD_STAGE_LD + lane] = v[16 * h + q];
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int col = q * 8 + lane / 4;
+              float z[8];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float4 x = *reinterpret_cast<const float4 *>(st + col * HD_STAGE_LD + lane % 4 * 8 + e * 4);
+                z[4 * e] = x.x, z[4 * e + 1] = x.y, z[4 * e + 2] = x.z, z[4 * e + 3] = x.w;
+              }
+              if (j0 + c + 16 * h + col < last) finish8(a, z, il, j0 + c + 16 * h + col, res[2 * h + q]);
             }
-            if (c + col < a.nt) finish8(a, z, i0 + warp * 32 + lane % 4 * 8, j0 + c + col);
           }
         }
       }
@@ -447,7 +496,7 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
   __syncwarp();
   __syncthreads();
   if (PAIR) cluster_sync();   // the pair's products and arrivals are through
-  if (warp == 5) {
+  if (warp == HD_MMA) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     if (PAIR)
       asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
@@ -457,12 +506,14 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
 }
 
 // The partials of shared tiles added up in the order of r, and the epilogue. Block
-// x: 128 rows of a tile (ctas of them per tile); a thread takes 8 elements of i of
-// one column.
+// x: 128 rows of a tile (ctas of them per tile), block y: 16 columns. VEC (a.vec):
+// a thread takes 8 elements of i of one column, else 8 columns of one i.
+template <bool VEC>
 __global__ void __launch_bounds__(256) k_head_join(const HeadArgs a, int ctas) {
   const int tile = blockIdx.x / ctas, rank = blockIdx.x % ctas;
-  const int iv = threadIdx.x % (HD_I / 8), col = blockIdx.y * 16 + threadIdx.x / (HD_I / 8);
-  const int i = (tile / a.tiles_j * ctas + rank) * HD_I + iv * 8, j = tile % a.tiles_j * a.nt + col;
+  const int il = VEC ? threadIdx.x % (HD_I / 8) * 8 : threadIdx.x % HD_I;
+  const int col = blockIdx.y * 16 + (VEC ? threadIdx.x / (HD_I / 8) : threadIdx.x / HD_I * 8);
+  const int i = (tile / a.tiles_j * ctas + rank) * HD_I + il, j = tile % a.tiles_j * a.nt + col;
   // the runs that have stages of this tile: g .. g + n - 1
   const int first = tile * a.KB, head = a.longer * (a.run_len + 1);
   auto run_of = [&](int x) { return x < head ? x / (a.run_len + 1) : a.longer + (x - head) / a.run_len; };
@@ -470,21 +521,32 @@ __global__ void __launch_bounds__(256) k_head_join(const HeadArgs a, int ctas) {
   if (n == 1 || col >= a.nt || j >= a.J || i >= a.I) return;   // one run: the product finished it
   // run g's stretch starts the tile, the others' start their runs
   const long long step = (long long)ctas * 2 * a.nt * HD_I;
-  const float *p = a.part + ((long long)(g * ctas + rank) * 2 * a.nt + col) * HD_I + iv * 8;
+  const float *p = a.part + ((long long)(g * ctas + rank) * 2 * a.nt + col) * HD_I + il;
+  uint4 res;
+  uint16_t res_column[8];
+  if (VEC) res = residual8(a, i, j);
+  else residual_column<8>(a, i, j, res_column);
   float z[8];
+  auto add = [&](const float *from, bool start) {
+    float x[8];
+    if (VEC) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const float4 x = __ldcs(reinterpret_cast<const float4 *>(p + (long long)a.nt * HD_I) + h);
-    z[4 * h] = x.x, z[4 * h + 1] = x.y, z[4 * h + 2] = x.z, z[4 * h + 3] = x.w;
-  }
+      for (int h = 0; h < 2; ++h) {
+        const float4 y = __ldcs(reinterpret_cast<const float4 *>(from) + h);
+        x[4 * h] = y.x, x[4 * h + 1] = y.y, x[4 * h + 2] = y.z, x[4 * h + 3] = y.w;
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) x[q] = j + q < a.J ? __ldcs(from + q * HD_I) : 0.f;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) z[q] = start ? x[q] : z[q] + x[q];
+  };
+  add(p + (long long)a.nt * HD_I, true);
 #pragma unroll 4
-  for (int s = 1; s < n; ++s) {
-    const float4 x = __ldcs(reinterpret_cast<const float4 *>(p + s * step));
-    const float4 y = __ldcs(reinterpret_cast<const float4 *>(p + s * step) + 1);
-    z[0] += x.x, z[1] += x.y, z[2] += x.z, z[3] += x.w;
-    z[4] += y.x, z[5] += y.y, z[6] += y.z, z[7] += y.w;
-  }
-  finish8(a, z, i, j);
+  for (int s = 1; s < n; ++s) add(p + s * step, false);
+  if (VEC) finish8(a, z, i, j, res);
+  else finish_column<8>(a, z, i, j, res_column);
 }
 
 // Few rows (a decode step): a warp reads HD_N whole rows of W at a time, 16 bytes
@@ -569,80 +631,109 @@ __global__ void __launch_bounds__(256) k_head_few(const HeadArgs a, const uint16
   }
 }
 
+// 8 elements of a matrix at p (any element of it; end: the matrix's), by aligned
+// loads inside the matrix; n of them exist, the others are zero.
+__device__ __forceinline__ uint4 load8_any(const uint16_t *p, const uint16_t *end, int n) {
+  const int shift = (int)((uintptr_t)p & 15);
+  const uint4 *v = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(p) - shift);
+  if (n >= 8 && shift == 0) return v[0];
+  if (n >= 8 && reinterpret_cast<const uint16_t *>(v + 2) <= end) return shift16(v[0], v[1], shift);
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = j < n ? p[j] : 0u;
+  return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+}
+
 // Rows of C elements copied to rows of ld (a multiple of 8) elements, zeros
-// behind them: operands whose rows TMA cannot address (C not a multiple of 8).
-__global__ void k_pad_rows(const uint16_t *src, uint16_t *dst, long long rows, int C, int ld) {
-  const long long n = rows * ld;
-  for (long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x; e < n;
-       e += (long long)gridDim.x * blockDim.x) {
-    const long long r = e / ld;
-    const int c = (int)(e - r * ld);
-    dst[e] = c < C ? src[r * C + c] : (uint16_t)0;
+// behind them: operands whose rows TMA cannot address (C not a multiple of 8). A
+// thread makes 16 bytes of a row out of two aligned vectors. Block z: which of two
+// matrices.
+struct Pad {
+  const uint16_t *src;
+  uint16_t *dst;
+  long long rows;
+};
+__global__ void __launch_bounds__(256) k_pad_rows(Pad p0, Pad p1, int C, int ld) {
+  const Pad p = blockIdx.z ? p1 : p0;
+  const int c = (blockIdx.x * 32 + (threadIdx.x & 31)) * 8;
+  if (c >= ld) return;
+  const uint16_t *end = p.src + p.rows * C;
+  for (long long r = blockIdx.y * 8ll + (threadIdx.x >> 5); r < p.rows; r += gridDim.y * 8ll) {
+    const uint4 x = load8_any(p.src + r * C + c, end, C - c);
+    *reinterpret_cast<uint4 *>(p.dst + r * ld + c) = x;
   }
 }
 
 // dz = dy act'(pre), rounded once to bf16 (the products' operand; rows of ld
 // elements, zeros behind N), and the column sums of the unrounded dz over
-// HD_DZ_ROWS rows. A CTA takes 32 x VEC columns, 8 threads per column.
+// HD_DZ_ROWS rows. A CTA takes 256 columns, 8 threads for every 8 of them.
 constexpr int HD_DZ_ROWS = 64;
-template <int VEC>
+// ALIGNED: N is a multiple of 8.
+template <bool ALIGNED>
 __global__ void __launch_bounds__(256)
     k_dz(const uint16_t *dy, const uint16_t *pre, uint16_t *dz, float *psum, int M, int N, int ld, int act,
          WsHeader *hdr) {
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) hdr->status = SPEC_OK, hdr->detail = -1;
-  __shared__ float sums[8][32 * VEC + 1];
+  __shared__ float sums[8][32 * 8 + 1];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
-  const int c0 = (blockIdx.x * 32 + cx) * VEC;
+  const int c0 = (blockIdx.x * 32 + cx) * 8;
   const int r0 = blockIdx.y * HD_DZ_ROWS, r1 = min(M, r0 + HD_DZ_ROWS);
-  float acc[VEC] = {};
-  using U = typename std::conditional<VEC == 8, uint4, uint16_t>::type;
-  constexpr int BATCH = 4;   // rows whose loads are out together
-  if (c0 < ld) {
+  float acc[8] = {};
+  auto row = [&](int r, const uint4 &gw, const uint4 &zw) {
+    float g[8], z[8];
+    unpack8(gw, g);
+    if (pre) unpack8(zw, z);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (pre) g[j] = __fmul_rn(g[j], act_slope(z[j], act));
+      acc[j] = __fadd_rn(acc[j], g[j]);   // unfused: the same sums with and without dz
+    }
+    if (dz) *reinterpret_cast<uint4 *>(dz + (long long)r * ld + c0) = pack8(g);
+  };
+  // 16 bytes at any element whose two aligned vectors lie in its row
+  auto get = [&](const uint16_t *p) -> uint4 {
+    if (ALIGNED) return *reinterpret_cast<const uint4 *>(p);
+    const int shift = (int)((uintptr_t)p & 15);
+    const uint4 *v = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(p) - shift);
+    return shift == 0 ? v[0] : shift16(v[0], v[1], shift);
+  };
+  if (ALIGNED ? c0 < N : c0 + 16 <= N) {
+    constexpr int BATCH = ALIGNED ? 4 : 2;   // rows whose loads are out together
     for (int rb = r0 + ry; rb < r1; rb += 8 * BATCH) {
-      U gv[BATCH] = {}, zv[BATCH] = {};
+      uint4 gv[BATCH], zv[BATCH];
 #pragma unroll
       for (int q = 0; q < BATCH; ++q) {
         const int r = rb + 8 * q;
-        if (r < r1 && c0 < N) {
-          gv[q] = *reinterpret_cast<const U *>(dy + (long long)r * N + c0);
-          if (pre) zv[q] = *reinterpret_cast<const U *>(pre + (long long)r * N + c0);
+        if (r < r1) {
+          gv[q] = get(dy + (long long)r * N + c0);
+          if (pre) zv[q] = get(pre + (long long)r * N + c0);
         }
       }
 #pragma unroll
-      for (int q = 0; q < BATCH; ++q) {
-        const int r = rb + 8 * q;
-        if (r >= r1) break;
-        float g[VEC], z[VEC];
-        if (VEC == 8) {
-          unpack8(*reinterpret_cast<const uint4 *>(&gv[q]), g);
-          unpack8(*reinterpret_cast<const uint4 *>(&zv[q]), z);
-        } else {
-          g[0] = bf16_bits_to_f32(*reinterpret_cast<const uint16_t *>(&gv[q]));
-          z[0] = bf16_bits_to_f32(*reinterpret_cast<const uint16_t *>(&zv[q]));
-        }
+      for (int q = 0; q < BATCH; ++q)
+        if (rb + 8 * q < r1) row(rb + 8 * q, gv[q], zv[q]);
+    }
+  } else if (c0 < ld) {   // a row's last elements
+    for (int r = r0 + ry; r < r1; r += 8) {
+      uint32_t g[8], z[8];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          if (pre) g[j] = __fmul_rn(g[j], act_slope(z[j], act));
-          acc[j] = __fadd_rn(acc[j], g[j]);   // unfused: the same sums with and without dz
-        }
-        if (dz) {
-          if (VEC == 8) *reinterpret_cast<uint4 *>(dz + (long long)r * ld + c0) = pack8(g);
-          else dz[(long long)r * ld + c0] = (uint16_t)f32_to_bf16_bits(g[0]);
-        }
+      for (int j = 0; j < 8; ++j) {
+        g[j] = c0 + j < N ? dy[(long long)r * N + c0 + j] : 0u;
+        z[j] = pre && c0 + j < N ? pre[(long long)r * N + c0 + j] : 0u;
       }
+      row(r, make_uint4(g[0] | g[1] << 16, g[2] | g[3] << 16, g[4] | g[5] << 16, g[6] | g[7] << 16),
+          make_uint4(z[0] | z[1] << 16, z[2] | z[3] << 16, z[4] | z[5] << 16, z[6] | z[7] << 16));
     }
   }
   if (psum == nullptr) return;
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) sums[ry][cx * VEC + j] = acc[j];
+  for (int j = 0; j < 8; ++j) sums[ry][cx * 8 + j] = acc[j];
   __syncthreads();
-  for (int c = threadIdx.x; c < 32 * VEC; c += 256) {
-    const int col = blockIdx.x * 32 * VEC + c;
-    float s = 0.f;
+  const int col = blockIdx.x * 256 + threadIdx.x;
+  float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += sums[k][c];
-    if (col < N) psum[(long long)blockIdx.y * N + col] = s;
-  }
+  for (int k = 0; k < 8; ++k) s += sums[k][threadIdx.x];
+  if (col < N) psum[(long long)blockIdx.y * N + col] = s;
 }
 
 __global__ void k_db(const float *psum, float *db, int N, int segs) {
@@ -774,7 +865,8 @@ int launch_head(const Plan &p, const CUtensorMap &ma, const CUtensorMap &mb, Hea
                   : launch_tiles<A_MN, B_MN, false>(p, ma, mb, a, sms, st);
   if (rc == SPEC_OK && p.runs) {
     const dim3 grid((unsigned)(p.tiles_i * p.tiles_j), (unsigned)((p.nt + 15) / 16));
-    k_head_join<<<grid, 256, 0, st>>>(a, p.pair ? 2 : 1);
+    if (a.vec) k_head_join<true><<<grid, 256, 0, st>>>(a, p.pair ? 2 : 1);
+    else k_head_join<false><<<grid, 256, 0, st>>>(a, p.pair ? 2 : 1);
     rc = launched();
   }
   return rc;
@@ -799,15 +891,22 @@ inline size_t padded_bytes(long long rows, long long C) {
   return C % 8 == 0 ? 0 : align256((size_t)rows * round8(C) * 2);
 }
 
-// An operand as TMA can read it: itself, or a padded copy at *ws (advanced).
-int operand(const void **p, long long rows, int C, char **ws, cudaStream_t st) {
+// Operands (of C columns) as TMA can read them: themselves, or padded copies at
+// *ws (advanced). q NULL: one operand.
+int operands(const void **p, long long p_rows, const void **q, long long q_rows, int C, char **ws, cudaStream_t st) {
   if (C % 8 == 0) return SPEC_OK;
   const int ld = (int)round8(C);
-  uint16_t *dst = reinterpret_cast<uint16_t *>(*ws);
-  *ws += padded_bytes(rows, C);
-  const long long blocks = std::min<long long>((rows * ld + 1023) / 1024, 16384);
-  k_pad_rows<<<(unsigned)blocks, 256, 0, st>>>(static_cast<const uint16_t *>(*p), dst, rows, C, ld);
-  *p = dst;
+  auto pad = [&](const void **m, long long rows) {
+    uint16_t *dst = reinterpret_cast<uint16_t *>(*ws);
+    *ws += padded_bytes(rows, C);
+    const Pad d{static_cast<const uint16_t *>(*m), dst, rows};
+    *m = dst;
+    return d;
+  };
+  const Pad d0 = pad(p, p_rows), d1 = q ? pad(q, q_rows) : Pad{};
+  const long long rows = std::max(p_rows, q ? q_rows : 0);
+  const dim3 grid((unsigned)((ld + 255) / 256), (unsigned)std::min<long long>((rows + 7) / 8, 4096), q ? 2 : 1);
+  k_pad_rows<<<grid, 256, 0, st>>>(d0, d1, C, ld);
   return launched();
 }
 
@@ -870,8 +969,7 @@ extern "C" int spec_head_forward(const void *x, const void *weight, const void *
     return M == 1 ? launch_few<1>(a, x, weight, K, st) : M == 2 ? launch_few<2>(a, x, weight, K, st)
                                                                 : launch_few<4>(a, x, weight, K, st);
   int rc;
-  if ((rc = operand(&x, M, K, &ws, st)) != SPEC_OK || (rc = operand(&weight, N, K, &ws, st)) != SPEC_OK)
-    return rc;
+  if ((rc = operands(&x, M, &weight, N, K, &ws, st)) != SPEC_OK) return rc;
   CUtensorMap ma, mb;
   if ((rc = make_map(&ma, weight, N, K, round8(K), HD_I)) != SPEC_OK ||
       (rc = make_map(&mb, x, M, K, round8(K), p.pair ? p.nt / 2 : p.nt)) != SPEC_OK)
@@ -925,12 +1023,11 @@ extern "C" int spec_head_backward(const void *dy, const void *x, const void *wei
   if (own_dz || db != nullptr) {
     const uint16_t *g = static_cast<const uint16_t *>(dy);
     const uint16_t *z = act != SPEC_ACT_NONE ? static_cast<const uint16_t *>(pre) : nullptr;
-    const int vec = N % 8 == 0 ? 8 : 1;
-    const dim3 grid((unsigned)((ldz + 32 * vec - 1) / (32 * vec)), (unsigned)dz_segments(M));
+    const dim3 grid((unsigned)((ldz + 255) / 256), (unsigned)dz_segments(M));
     if (grid.y > 65535) return SPEC_ERR_UNSUPPORTED;
     float *sums = db == nullptr ? nullptr : grid.y == 1 ? db : psum;   // one segment: the sums themselves
-    if (vec == 8) k_dz<8><<<grid, 256, 0, st>>>(g, z, own_dz ? dz : nullptr, sums, M, N, ldz, act, a.hdr);
-    else k_dz<1><<<grid, 256, 0, st>>>(g, z, own_dz ? dz : nullptr, sums, M, N, ldz, act, a.hdr);
+    if (N % 8 == 0) k_dz<true><<<grid, 256, 0, st>>>(g, z, own_dz ? dz : nullptr, sums, M, N, ldz, act, a.hdr);
+    else k_dz<false><<<grid, 256, 0, st>>>(g, z, own_dz ? dz : nullptr, sums, M, N, ldz, act, a.hdr);
     if ((rc = launched()) != SPEC_OK) return rc;
     if (sums == psum && db != nullptr) {
       k_db<<<(N + 255) / 256, 256, 0, st>>>(psum, db, N, dz_segments(M));
@@ -942,7 +1039,7 @@ extern "C" int spec_head_backward(const void *dy, const void *x, const void *wei
   const long long ldk = round8(K);
   CUtensorMap ma, mb;
   if (dx != nullptr) {
-    if ((rc = operand(&weight, N, K, &ws, st)) != SPEC_OK) return rc;
+    if ((rc = operands(&weight, N, dw ? &x : nullptr, M, K, &ws, st)) != SPEC_OK) return rc;
     if ((rc = make_map(&ma, weight, N, K, ldk, 64)) != SPEC_OK ||
         (rc = make_map(&mb, gz, M, N, ldz, px.pair ? px.nt / 2 : px.nt)) != SPEC_OK)
       return rc;
@@ -952,7 +1049,7 @@ extern "C" int spec_head_backward(const void *dy, const void *x, const void *wei
     a.reset = 0;
   }
   if (dw != nullptr) {
-    if ((rc = operand(&x, M, K, &ws, st)) != SPEC_OK) return rc;
+    if (dx == nullptr && (rc = operands(&x, M, nullptr, 0, K, &ws, st)) != SPEC_OK) return rc;
     if ((rc = make_map(&ma, x, M, K, ldk, 64)) != SPEC_OK ||
         (rc = make_map(&mb, gz, M, N, ldz, 64)) != SPEC_OK)
       return rc;
