@@ -42,6 +42,9 @@ namespace cg = cooperative_groups;
 
 constexpr int DI_THREADS = 256;
 constexpr int DI_MAX_CLUSTER = 8;
+// Bytes of the rows that clusters work on at a time: 2560 positions of 50257 bf16
+// logits take 192 us with 96 MB, 250 us with 48 MB, 233 us without a limit.
+constexpr long long DI_L2_BYTES = 96ll << 20;
 // resident schedule
 constexpr int DR_WARPS = 16;               // consumer warps of a CTA, after a producer and a merging warp
 constexpr int DR_THREADS = 32 * (2 + DR_WARPS);
@@ -771,7 +774,10 @@ extern "C" int spec_distill_loss(const void *target, const void *draft, int dt, 
     return dt == SPEC_BF16 ? launch_resident<true>(s, st) : launch_resident<false>(s, st);
   }
   // each position over as many SMs as there are, down to slices of 4 KB
+  const long long pair = 2ll * V * es;
   int C = 1;
-  while (C < DI_MAX_CLUSTER && (long long)R_d * C < 2 * num_sms() && 2ll * V * es / C > 8192) C *= 2;
+  while (C < DI_MAX_CLUSTER && (long long)R_d * C < 2 * num_sms() && pair / C > 8192) C *= 2;
+  // and the positions in flight within L2
+  while (C < DI_MAX_CLUSTER && std::min<long long>(R_d, 5ll * num_sms() / C) * pair > DI_L2_BYTES) C *= 2;
   return dt == SPEC_BF16 ? launch_distill<true>(a, C, st) : launch_distill<false>(a, C, st);
 }

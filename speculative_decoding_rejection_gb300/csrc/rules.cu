@@ -67,16 +67,18 @@ template <> struct Elem<uint32_t> {
   __device__ static uint32_t from_f32(float v) { return __float_as_uint(v); }
 };
 
-// A thread's unit of access: 16 bytes, or one element where rows are not
-// 16-byte aligned.
-template <typename E, int VEC> struct Unit { using T = uint4; };
-template <> struct Unit<uint16_t, 1> { using T = uint16_t; };
-template <> struct Unit<uint32_t, 1> { using T = uint32_t; };
+// A thread's unit of access: the most bytes, up to 16, that every row is aligned
+// to.
+template <int BYTES> struct Unit;
+template <> struct Unit<2> { using T = uint16_t; };
+template <> struct Unit<4> { using T = uint32_t; };
+template <> struct Unit<8> { using T = uint2; };
+template <> struct Unit<16> { using T = uint4; };
 
 // E: the element's bits; VEC elements per access; P tokens per thread.
 template <typename E, int VEC, int P>
 __global__ void __launch_bounds__(RU_THREADS) k_rules(RulesArgs a) {
-  using U = typename Unit<E, VEC>::T;
+  using U = typename Unit<VEC * sizeof(E)>::T;
   constexpr int CH = RU_THREADS * P;
   constexpr int NV = P / VEC;                    // accesses of a thread per row
   constexpr uint32_t VFULL = VEC == 1 ? 1u : (1u << VEC) - 1;
@@ -85,7 +87,7 @@ __global__ void __launch_bounds__(RU_THREADS) k_rules(RulesArgs a) {
   RulesSmem<CH> &sm = *reinterpret_cast<RulesSmem<CH> *>(dyn);
   const bool tree = a.r.parent != nullptr;
 
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int t = threadIdx.x, lane = t & 31;
   const int c = blockIdx.x % a.nch;
   const int b = (blockIdx.x / a.nch) % a.B;
   const int i0 = (blockIdx.x / a.nch) / a.B * a.seg;
@@ -184,10 +186,8 @@ __global__ void __launch_bounds__(RU_THREADS) k_rules(RulesArgs a) {
     for (int v = 0; v < NV; ++v) {
       if (VEC == 1) {
         A |= ((__shfl_sync(~0u, raw[0], v) >> lane) & 1u) << v;
-      } else if (VEC == 8) {
-        A |= (raw[v % NRAW] & 0xffu) << (v * VEC % 32);
-      } else {
-        A |= ((raw[v % NRAW] >> ((t & 1) * 4)) & 0xfu) << (v * VEC % 32);
+      } else {   // a byte of the mask holds the access's bits
+        A |= ((raw[v % NRAW] >> (t * VEC & 7)) & VFULL) << (v * VEC % 32);
       }
     }
     return A & valid;
@@ -300,13 +300,8 @@ __global__ void __launch_bounds__(RU_THREADS) k_rules(RulesArgs a) {
   uint32_t F = 0;   // tokens of this thread that the history or a bias touches
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    if (VEC == 8)
-      F |= (uint32_t)reinterpret_cast<const uint8_t *>(sm.bits)[v * RU_THREADS + t] << (v * VEC % 32);
-    else if (VEC == 4)
-      F |= ((reinterpret_cast<const uint8_t *>(sm.bits)[(v * RU_THREADS + t) >> 1] >> ((t & 1) * 4)) & 0xfu)
-           << (v * VEC % 32);
-    else
-      F |= ((sm.bits[v * (RU_THREADS / 32) + warp] >> lane) & 1u) << v;
+    const int e = (v * RU_THREADS + t) * VEC;
+    F |= ((reinterpret_cast<const uint8_t *>(sm.bits)[e >> 3] >> (e & 7)) & VFULL) << (v * VEC % 32);
   }
 
   const float inv_rho = 1.f / rho;
@@ -344,21 +339,23 @@ __global__ void __launch_bounds__(RU_THREADS) k_rules(RulesArgs a) {
       if (VEC == 1) {
         GST(out + v * RU_THREADS + t, av ? *reinterpret_cast<const E *>(&cur[v]) : (E)Elem<E>::NEG_INF);
       } else {
-        uint4 x = *reinterpret_cast<const uint4 *>(&cur[v]);
+        U x = cur[v];
         if (av != VFULL) {
-          uint32_t *w = &x.x;
-          if (VEC == 8) {
+          constexpr int WORDS = sizeof(U) < 4 ? 1 : sizeof(U) / 4, PER = 4 / sizeof(E);
+          uint32_t w[WORDS];
+          memcpy(w, &x, VEC == 1 ? 0 : sizeof(w));
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < WORDS; ++q) {
+            if (PER == 2) {
               const uint32_t keep = ((av >> (2 * q)) & 1u) * 0xffffu | ((av >> (2 * q + 1)) & 1u) * 0xffff0000u;
               w[q] = (w[q] & keep) | (0xff80ff80u & ~keep);
+            } else {
+              w[q] = (av >> q) & 1u ? w[q] : 0xff800000u;
             }
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) w[q] = (av >> q) & 1u ? w[q] : 0xff800000u;
           }
+          memcpy(&x, w, VEC == 1 ? 0 : sizeof(w));
         }
-        GST(reinterpret_cast<uint4 *>(out) + v * RU_THREADS + t, x);
+        GST(reinterpret_cast<U *>(out) + v * RU_THREADS + t, x);
       }
     }
     for (uint32_t todo = Fi & A; todo != 0; todo &= todo - 1) {
@@ -497,12 +494,15 @@ extern "C" int spec_process_logits(const void *logits, int dt, int R, int V,
   if (R == 0) return SPEC_OK;
   if (check_upload(st) != SPEC_OK) return SPEC_ERR_CUDA;
 
-  const int vec = (V * es) % 16 == 0 ? (int)(16 / es) : 1;
+  const int bytes_per = (V * es) % 16 == 0 ? 16 : (V * es) % 8 == 0 ? 8 : (V * es) % 4 == 0 ? 4 : 2;
+  const int vec = (int)(bytes_per / es);
   // Long calls: wide ranges and segments of many rows, so that a table serves
-  // many rows. Calls that would not fill the SMs: shorter segments, then
-  // narrow ranges.
-  // A thread's row is 64 bytes in registers (16 elements where rows are not
-  // 16-byte aligned).
+  // many rows. Calls that would not fill the SMs four times over: shorter
+  // segments; that would leave SMs idle even so: narrow ranges. (64 requests of
+  // 2..6 rows of 32000 bf16 logits: 14.4 us, with segments for two or eight CTAs
+  // per SM 16.5 us. Two trees of 64 nodes of 32000: 12.4 us, with narrow ranges
+  // already below four CTAs per SM 20.6 us.)
+  // A thread's row is at most 64 bytes in registers, and at most 16 accesses.
   const int wide = dt == SPEC_BF16 && vec == 8 ? 32 : 16;
   int P = wide;
   int seg = std::min(max_rows, RU_MAX_SEG);
@@ -511,7 +511,7 @@ extern "C" int spec_process_logits(const void *logits, int dt, int R, int V,
   };
   const long long want = 4ll * num_sms();
   while (seg > 1 && ctas(P, seg) < want) seg = (seg + 1) / 2;
-  if (ctas(P, seg) < want) P = 8;
+  if (ctas(P, seg) < num_sms()) P = 8;
   a.seg = seg;
   a.nch = (V + RU_THREADS * P - 1) / (RU_THREADS * P);
   const long long n = ctas(P, seg);
@@ -519,9 +519,15 @@ extern "C" int spec_process_logits(const void *logits, int dt, int R, int V,
   if (dt == SPEC_BF16) {
     if (vec == 8)
       return P == 32 ? launch_rules<uint16_t, 8, 32>(a, n, st) : launch_rules<uint16_t, 8, 8>(a, n, st);
+    if (vec == 4)
+      return P == 16 ? launch_rules<uint16_t, 4, 16>(a, n, st) : launch_rules<uint16_t, 4, 8>(a, n, st);
+    if (vec == 2)
+      return P == 16 ? launch_rules<uint16_t, 2, 16>(a, n, st) : launch_rules<uint16_t, 2, 8>(a, n, st);
     return P == 16 ? launch_rules<uint16_t, 1, 16>(a, n, st) : launch_rules<uint16_t, 1, 8>(a, n, st);
   }
   if (vec == 4)
     return P == 16 ? launch_rules<uint32_t, 4, 16>(a, n, st) : launch_rules<uint32_t, 4, 8>(a, n, st);
+  if (vec == 2)
+    return P == 16 ? launch_rules<uint32_t, 2, 16>(a, n, st) : launch_rules<uint32_t, 2, 8>(a, n, st);
   return P == 16 ? launch_rules<uint32_t, 1, 16>(a, n, st) : launch_rules<uint32_t, 1, 8>(a, n, st);
 }

@@ -92,6 +92,11 @@ CASES = [
     ("f32 ranges", dict(V=8192 + 2052, rows=[4, 3], dtype=torch.float32, hist=300)),
     ("bf16", dict(V=8200, rows=[6, 2, 3], dtype=torch.bfloat16, hist=500)),
     ("bf16 odd", dict(V=20011, rows=[1, 3, 2], dtype=torch.bfloat16, hist=500)),
+    ("bf16 by 4", dict(V=20012, rows=[2, 3, 2], dtype=torch.bfloat16, hist=500)),
+    ("bf16 by 2", dict(V=9002, rows=[6, 3, 2], dtype=torch.bfloat16, hist=300, mask="index")),
+    ("f32 by 2", dict(V=5002, rows=[6, 3, 2], dtype=torch.float32, hist=300)),
+    ("bf16 by 2, long", dict(V=30002, rows=[3] * 200, dtype=torch.bfloat16, hist=20)),
+    ("f32 by 1, long", dict(V=12289, rows=[3] * 260, dtype=torch.float32, hist=20)),
     ("bf16 vector end", dict(V=16392, rows=[3, 3], dtype=torch.bfloat16)),
     ("mask by index", dict(V=2056, rows=[4, 4, 4], dtype=torch.bfloat16, mask="index")),
     ("no mask", dict(V=2056, rows=[4, 1], dtype=torch.bfloat16, mask=None)),
@@ -114,7 +119,7 @@ def test_rules(name, case, inplace):
     check(z, cu, c, got)
 
 
-@pytest.mark.parametrize("name,case", CASES[1:8] + CASES[13:15], ids=[c[0] for c in CASES[1:8] + CASES[13:15]])
+@pytest.mark.parametrize("name,case", CASES[1:9] + CASES[18:20], ids=[c[0] for c in CASES[1:9] + CASES[18:20]])
 def test_rules_checked(name, case):
     """The same on the bounds-checked build: no access leaves its buffers."""
     sv.use_checked_library(True)
