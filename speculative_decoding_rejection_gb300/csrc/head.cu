@@ -145,6 +145,14 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
         : "memory");
   }
 }
+// True in one lane of a converged warp. The products' operands sit in uniform
+// registers: the compiler sees by this instruction, not by a test of the lane,
+// that one thread issues them.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t on;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+  return on != 0;
+}
 // 32 accumulator columns of this thread's lane.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float *v) {
   uint32_t r[32];
@@ -332,16 +340,17 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
   Stretch w;
 
   if (warp == HD_TMA) {
-    if (lane == 0) {
-      int it = 0;   // stages filled so far
-      while (!*abort && next_stretch(a, walk, w)) {
-        const int i0 = (w.tile / a.tiles_j * CTAS + rank) * HD_I, j0 = w.tile % a.tiles_j * a.nt + rank * ntc;
-        for (int k = w.k0; k < w.k1; ++k, ++it) {
-          const int st = it % a.stages;
-          if (it >= a.stages && !wait_phase<PAIR>(&sh.empty[st], (it / a.stages - 1) & 1, abort)) {
-            *abort = 1;
-            break;
-          }
+    int it = 0;   // stages filled so far
+    bool ok = true;
+    while (ok && next_stretch(a, walk, w)) {
+      const int i0 = (w.tile / a.tiles_j * CTAS + rank) * HD_I, j0 = w.tile % a.tiles_j * a.nt + rank * ntc;
+      for (int k = w.k0; k < w.k1; ++k, ++it) {
+        const int st = it % a.stages;
+        if (it >= a.stages && !__all_sync(~0u, wait_phase<PAIR>(&sh.empty[st], (it / a.stages - 1) & 1, abort))) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
           uint8_t *pa = ring + st * stage_bytes, *pb = pa + HD_A_BYTES;
           const uint32_t bar = PAIR ? peer_u32(&sh.full[st], 0) : smem_u32(&sh.full[st]);
           // both CTAs' bytes count on the first one's barrier
@@ -358,18 +367,19 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
             tma_2d<PAIR>(pb, &map_b, k * HD_R, j0, bar);
           }
         }
-        if (*abort) break;
-      }
-      if (*abort) {   // the copies in flight land before the CTA leaves
-        int never = 0;
-        if (rank == 0)
-          for (int k = max(0, it - a.stages); k < it; ++k)
-            wait_phase<PAIR>(&sh.full[k % a.stages], (k / a.stages) & 1, &never);
-        set_status(a.hdr, SPEC_ERR_TIMEOUT, 4);
+        __syncwarp();
       }
     }
+    if (!ok) {   // the copies in flight land before the CTA leaves
+      *abort = 1;
+      int never = 0;
+      if (rank == 0)
+        for (int k = max(0, it - a.stages); k < it; ++k)
+          wait_phase<PAIR>(&sh.full[k % a.stages], (k / a.stages) & 1, &never);
+      if (lane == 0) set_status(a.hdr, SPEC_ERR_TIMEOUT, 4);
+    }
   } else if (warp == HD_MMA) {
-    if (lane == 0 && rank == 0) {   // of a pair, the first CTA issues for both
+    if (rank == 0) {   // of a pair, the first CTA issues for both
       // f32 accumulator, bf16 operands, which of them are MN-major, N, M
       const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)A_MN << 15) |
                              ((uint32_t)B_MN << 16) | ((uint32_t)(a.nt >> 3) << 17) |
@@ -378,7 +388,7 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
       bool ok = true;
       for (; ok && next_stretch(a, walk, w); ++n) {
         const int buf = n & 1;
-        if (n >= 2 && !wait_phase<PAIR>(&sh.acc_empty[buf], ((n >> 1) - 1) & 1, abort)) {
+        if (n >= 2 && !__all_sync(~0u, wait_phase<PAIR>(&sh.acc_empty[buf], ((n >> 1) - 1) & 1, abort))) {
           ok = false;
           break;
         }
@@ -386,23 +396,27 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
         const uint32_t d = tmem + buf * (cols / 2);
         for (int k = w.k0; k < w.k1; ++k, ++it) {
           const int st = it % a.stages;
-          if (!wait_phase<PAIR>(&sh.full[st], (it / a.stages) & 1, abort)) {
+          if (!__all_sync(~0u, wait_phase<PAIR>(&sh.full[st], (it / a.stages) & 1, abort))) {
             ok = false;
             break;
           }
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t pa = smem_u32(ring + st * stage_bytes), pb = pa + HD_A_BYTES;
+          if (elect_one()) {
+            const uint32_t pa = smem_u32(ring + st * stage_bytes), pb = pa + HD_A_BYTES;
+            const uint64_t da = smem_desc(pa, A_MN), db = smem_desc(pb, B_MN);
 #pragma unroll
-          for (int q = 0; q < HD_R / 16; ++q)   // 16 of r: 32 bytes along a row, or two 8-row groups
-            mma_bf16<PAIR>(d, smem_desc(pa + q * (A_MN ? 2048 : 32), A_MN),
-                           smem_desc(pb + q * (B_MN ? 2048 : 32), B_MN), idesc, k > w.k0 || q > 0);
-          mma_commit<PAIR>(&sh.empty[st]);
+            for (int q = 0; q < HD_R / 16; ++q)   // 16 of r: 32 bytes along a row, or two 8-row groups
+              mma_bf16<PAIR>(d, da + q * ((A_MN ? 2048 : 32) >> 4), db + q * ((B_MN ? 2048 : 32) >> 4), idesc,
+                             k > w.k0 || q > 0);
+            mma_commit<PAIR>(&sh.empty[st]);
+            if (k == w.k1 - 1) mma_commit<PAIR>(&sh.acc_full[buf]);
+          }
+          __syncwarp();
         }
-        if (ok) mma_commit<PAIR>(&sh.acc_full[buf]);
       }
       if (!ok) {
         *abort = 1;
-        set_status(a.hdr, SPEC_ERR_TIMEOUT, 5);
+        if (lane == 0) set_status(a.hdr, SPEC_ERR_TIMEOUT, 5);
       }
     }
   } else {
