@@ -21,7 +21,7 @@ __device__ __forceinline__ uint32_t f32_to_bf16_bits(float v) {
   return f32x2_to_bf16x2(v, 0.f) & 0xffffu;
 }
 
-// 16 bytes from `shift` bytes into the 32 of two vectors (0 < shift < 16, whole
+// 16 bytes from `shift` bytes into the 32 of two vectors (0 <= shift < 16, whole
 // elements).
 __device__ __forceinline__ uint4 shift16(const uint4 &a, const uint4 &b, int shift) {
   uint32_t w[7] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z};

@@ -16,13 +16,16 @@
 //
 // Large products run on pairs of CTAs (cta_group::2): a pair's 256 x nt tile
 // takes 128 rows of A and half of B's columns from each CTA, so a stage of r
-// needs 32 KB of a CTA's ring where a lone CTA's 128 x 256 tile needs 48 KB, and
-// six stages instead of four cover the copies' latency.
+// moves 32 KB into an SM where a lone CTA's 128 x 256 tile moves 48 KB (1280 rows
+// of 4096 to 128256 columns: 732 us, 1840 TFLOP/s; lone CTAs 841 us). What
+// bounds the rest: the SMs' intake (with half of B's loads left out the same call
+// takes 694 us) and the epilogue (without its stores 708 us).
 //
 // A persistent CTA per SM: one warp feeds a ring of TMA stages (64 of r each),
 // one issues tcgen05.mma, eight run the epilogue from the other of two
-// accumulators (four, one per scheduler, took twice as long with an activation). Where whole tiles would leave SMs idle in the last round, all
-// tiles' stages are laid end to end and every CTA takes an equal run of them: what
+// accumulators (with four, one per scheduler, 1631 rows of 1749 to 59915 columns
+// with SiLU, residual and pre-activation took 636 us, with eight 448 us). Where
+// whole tiles would leave SMs idle in the last round, all tiles' stages are laid end to end and every CTA takes an equal run of them: what
 // it has of a tile that it shares goes out as an f32 partial, and a second launch
 // over all SMs adds the partials of a tile in the order of r and runs the
 // epilogue. (Joining inside the product, by the last part of a tile, left one SM
@@ -721,39 +724,53 @@ __global__ void __launch_bounds__(256)
     }
     if (dz) *reinterpret_cast<uint4 *>(dz + (long long)r * ld + c0) = pack8(g);
   };
-  // 16 bytes at any element whose two aligned vectors lie in its row
+  // 8 elements of a row, zeros behind its end. Rows off the 16-byte grid: by two
+  // aligned vectors, where both lie in the matrix; its last elements one by one.
+  const long long total = (long long)M * N;
+  const int n = N - c0;
+  uint32_t keep[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) keep[j] = (2 * j < n ? 0xffffu : 0u) | (2 * j + 1 < n ? 0xffff0000u : 0u);
+  // the rows before this one
+  const int whole = ALIGNED || (long long)(r1 - 1) * N + c0 + 16 <= total
+                        ? r1
+                        : max(r0, (int)((total - c0 - 16 + N) / N));
   auto get = [&](const uint16_t *p) -> uint4 {
     if (ALIGNED) return *reinterpret_cast<const uint4 *>(p);
     const int shift = (int)((uintptr_t)p & 15);
     const uint4 *v = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(p) - shift);
-    return shift == 0 ? v[0] : shift16(v[0], v[1], shift);
+    uint4 x = shift16(v[0], v[1], shift);   // (no shift at all is one, too)
+    x.x &= keep[0], x.y &= keep[1], x.z &= keep[2], x.w &= keep[3];
+    return x;
   };
-  if (ALIGNED ? c0 < N : c0 + 16 <= N) {
-    constexpr int BATCH = ALIGNED ? 4 : 2;   // rows whose loads are out together
-    for (int rb = r0 + ry; rb < r1; rb += 8 * BATCH) {
+  if (c0 < N) {   // (c0 < ld too, as ld is N rounded up to 8)
+    constexpr int BATCH = ALIGNED ? 4 : 1;   // rows whose loads are out together (the shifts take registers)
+    for (int rb = r0 + ry; rb < whole; rb += 8 * BATCH) {
       uint4 gv[BATCH], zv[BATCH];
 #pragma unroll
       for (int q = 0; q < BATCH; ++q) {
         const int r = rb + 8 * q;
-        if (r < r1) {
+        if (r < whole) {
           gv[q] = get(dy + (long long)r * N + c0);
           if (pre) zv[q] = get(pre + (long long)r * N + c0);
         }
       }
 #pragma unroll
       for (int q = 0; q < BATCH; ++q)
-        if (rb + 8 * q < r1) row(rb + 8 * q, gv[q], zv[q]);
+        if (rb + 8 * q < whole) row(rb + 8 * q, gv[q], zv[q]);
     }
-  } else if (c0 < ld) {   // a row's last elements
-    for (int r = r0 + ry; r < r1; r += 8) {
-      uint32_t g[8], z[8];
+    if (!ALIGNED && whole < r1) {
+      for (int r = r0 + ry; r < r1; r += 8) {
+        if (r < whole) continue;
+        uint32_t g[8], z[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        g[j] = c0 + j < N ? dy[(long long)r * N + c0 + j] : 0u;
-        z[j] = pre && c0 + j < N ? pre[(long long)r * N + c0 + j] : 0u;
+        for (int j = 0; j < 8; ++j) {
+          g[j] = j < n ? dy[(long long)r * N + c0 + j] : 0u;
+          z[j] = pre && j < n ? pre[(long long)r * N + c0 + j] : 0u;
+        }
+        row(r, make_uint4(g[0] | g[1] << 16, g[2] | g[3] << 16, g[4] | g[5] << 16, g[6] | g[7] << 16),
+            make_uint4(z[0] | z[1] << 16, z[2] | z[3] << 16, z[4] | z[5] << 16, z[6] | z[7] << 16));
       }
-      row(r, make_uint4(g[0] | g[1] << 16, g[2] | g[3] << 16, g[4] | g[5] << 16, g[6] | g[7] << 16),
-          make_uint4(z[0] | z[1] << 16, z[2] | z[3] << 16, z[4] | z[5] << 16, z[6] | z[7] << 16));
     }
   }
   if (psum == nullptr) return;
