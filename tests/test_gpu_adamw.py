@@ -218,3 +218,44 @@ def test_adamw_binding_refuses_mixed_lists():
         sv.spec_adamw_table(s["p"], [s["g"][0].bfloat16()], s["m"], s["v"])
     with pytest.raises(sv.SpecError):
         sv.spec_adamw_table(s["p"], s["g"], s["m"], s["v"], master=[s["m"][0]])
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_squares_below_and_beyond_the_normal_range(bits, shift):
+    """Gradients whose squares are subnormal or zero in 32 bits, one block per
+    magnitude, and one that overflows: its root is infinite, so its weight only
+    decays and nothing else is touched."""
+    mags = 10.0 ** np.arange(-26, -14)
+    n = 256 * len(mags)
+    s = make(5, torch.float32, bits, False, [n + 256], shift=shift)
+    for x in (s["m"], s["v"]):
+        x[0].zero_()
+    u = 0.5 + np.random.default_rng(5).random(n)
+    g = np.zeros(n + 256, np.float32)
+    g[:n] = (np.repeat(mags, 256) * u).astype(np.float32)
+    g[n + 3] = 1e25
+    s["g"][0].copy_(torch.from_numpy(g))
+    w0 = f64(s["p"][0])
+    h = dict(H, eps=1e-30)
+    sv.spec_adamw_step(table(s), 1, **h)
+    x = g[:n].astype(np.float64)
+    w, m, v = O.adamw(w0[:n], x, 0.0 * x, 0.0 * x, 1, **h)
+    # g^2 and its product are off by half of 2^-149 each where subnormal
+    tv = 2.0 ** -149 + 8 * U32 * v
+    got_w, got_m, got_v = snapshot(s, 0)
+    r, tr = np.sqrt(v), tv / np.maximum(np.sqrt(v), 2.0 ** -75)
+    if bits == 32:
+        assert np.all(np.abs(got_v[:n] - v) <= tv)
+    else:
+        # half a step of e4m3 at the block's scale beside that
+        half = np.maximum(r * 2.0 ** -4, np.repeat(r.reshape(-1, 256).max(1) / 448 * 2.0 ** -9, 256))
+        assert np.all(np.abs(np.sqrt(got_v[:n]) - r) <= (half + tr) * (1 + 64 * U32))
+    # where the root is known to a quarter, the weight follows
+    c1, c2 = 0.1, np.sqrt(0.05)
+    sure = tr <= r / 4
+    upd = np.abs(H["lr"] * (m / c1) / (np.maximum(r, 1e-300) / c2))
+    tw = 8 * U32 * np.abs(w0[:n]) + upd * (32 * U32 + 2 * tr / np.maximum(r, 1e-300))
+    assert sure.sum() > n // 3
+    assert np.all((np.abs(got_w[:n] - w) <= tw)[sure])
+    assert abs(got_w[n + 3] - w0[n + 3] * (1 - H["lr"] * H["weight_decay"])) <= 4 * U32 * abs(w0[n + 3])
