@@ -370,8 +370,11 @@ __device__ __forceinline__ void item8(const AdStep &s, const AdTensor &x, int ch
 template <bool STATE8>
 __global__ void __launch_bounds__(AD_THREADS, STATE8 ? AD_CTAS_PER_SM : 1) k_adamw(AdArgs a) {
   const AdHeader h = *a.table;
+  // every CTA comes to the same status, the first one writes it
+  const bool first = blockIdx.x == 0 && threadIdx.x == 0;
+  if (first) a.hdr->status = SPEC_OK, a.hdr->detail = -1;
   if (h.magic != AD_MAGIC || h.n_items != a.n_items || h.state_bits != (STATE8 ? 8 : 32)) {
-    if (threadIdx.x == 0) set_status(a.hdr, SPEC_ERR_INVALID_ARG, -1);
+    if (first) set_status(a.hdr, SPEC_ERR_INVALID_ARG, -1);
     return;
   }
   const AdTensor *tensors = reinterpret_cast<const AdTensor *>(a.table + 1);
@@ -387,7 +390,7 @@ __global__ void __launch_bounds__(AD_THREADS, STATE8 ? AD_CTAS_PER_SM : 1) k_ada
     if (a.step_dev != nullptr) {
       const int t = *a.step_dev;
       if (t < 1) {
-        if (threadIdx.x == 0) set_status(a.hdr, SPEC_ERR_INVALID_ARG, t);
+        if (first) set_status(a.hdr, SPEC_ERR_INVALID_ARG, t);
         return;
       }
       // 1 - b^t by expm1, which keeps its digits; b = 0: ln b = -inf gives 1
@@ -540,8 +543,7 @@ extern "C" int spec_adamw_step(const void *table, int64_t n_items, int state_bit
   a.step_dev = h.step_dev;
   a.hdr = static_cast<WsHeader *>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (reset_header(workspace, st) != SPEC_OK) return SPEC_ERR_CUDA;
-  if (n_items == 0) return SPEC_OK;
+  if (n_items == 0) return reset_header(workspace, st);
 #ifdef SPEC_CHECKED
   // the tensors are known to the table alone: each access is bounded by its n
   check_begin(a.hdr);

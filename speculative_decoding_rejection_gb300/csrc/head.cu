@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
   volatile int *abort = &sh.abort;
 
   if (t == 0) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // k_head_join, which waits
     // the only error is a wait that runs out, seconds after this
     if (blockIdx.x == 0 && a.reset) a.hdr->status = SPEC_OK, a.hdr->detail = -1;
     sh.abort = 0;
@@ -543,6 +544,10 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
 // a thread takes 8 elements of i of one column, else 8 columns of one i.
 template <bool VEC>
 __global__ void __launch_bounds__(256) k_head_join(const HeadArgs a, int ctas) {
+  // The blocks are on their SMs before the product ends (197 rows of 2880 x
+  // 2880: @A us, launched after its end @B us). Each waits, also where it has
+  // nothing to add, so that this grid does not end before the product's.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tile = blockIdx.x / ctas, rank = blockIdx.x % ctas;
   const int il = VEC ? threadIdx.x % (HD_I / 8) * 8 : threadIdx.x % HD_I;
   const int col = blockIdx.y * 16 + (VEC ? threadIdx.x / (HD_I / 8) : threadIdx.x / HD_I * 8);
@@ -913,8 +918,17 @@ int launch_head(const Plan &p, const CUtensorMap &ma, const CUtensorMap &mb, Hea
                   : launch_tiles<A_MN, B_MN, false>(p, ma, mb, a, sms, st);
   if (rc == SPEC_OK && p.runs) {
     const dim3 grid((unsigned)(p.tiles_i * p.tiles_j), (unsigned)((p.nt + 15) / 16));
-    if (a.vec) k_head_join<true><<<grid, 256, 0, st>>>(a, p.pair ? 2 : 1);
-    else k_head_join<false><<<grid, 256, 0, st>>>(a, p.pair ? 2 : 1);
+    cudaLaunchAttribute early[1];
+    early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t jc{};
+    jc.gridDim = grid;
+    jc.blockDim = dim3(256);
+    jc.stream = st;
+    jc.attrs = early;
+    jc.numAttrs = 1;
+    const auto join = a.vec ? k_head_join<true> : k_head_join<false>;
+    if (cudaLaunchKernelEx(&jc, join, (const HeadArgs)a, p.pair ? 2 : 1) != cudaSuccess) return SPEC_ERR_CUDA;
     rc = launched();
   }
   return rc;
