@@ -73,6 +73,16 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volat
 inline int reset_header(void *workspace, cudaStream_t st) {
   return cudaMemsetAsync(workspace, 0, sizeof(WsHeader), st) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
+// A launch with the attribute launch_early() begins when every block of the
+// kernel before it has executed griddepcontrol.launch_dependents, and each of its
+// threads waits in after_previous() for that kernel's end and memory.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+inline cudaLaunchAttribute launch_early() {
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
 // Lets `kern` have `smem` bytes of dynamic shared memory. The call takes
 // microseconds of host time, so a kernel's largest request is remembered per
 // device (in `most`, one array per kernel); a device that was reset has

@@ -74,7 +74,7 @@ def _arg(name, t, dtype, numel, dev):
     dtype, at least that many elements, contiguous, on device `dev`."""
     if t is None:
         return None
-    if t.dtype is dtype and t.get_device() == dev and t.numel() >= numel and t.is_contiguous():
+    if t.dtype is dtype and t.get_device() == dev and (not numel or t.numel() >= numel) and t.is_contiguous():
         return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -191,9 +191,10 @@ def spec_process_logits(logits, cu_rows, *, max_rows: int, history=None, cu_hist
         _arg("bias_values", bias_values, f32, n_bias, dev) or 0,
         _arg("cu_bias", cu_bias, i32, B + 1, dev) or 0,
         _arg("mask", mask, i32, 0, dev) or 0, _arg("mask_rows", mask_rows, i32, R, dev) or 0, n_mask)
-    with _Call(dev, stream, (logits, cu_rows, history, cu_history, prompt_len, tokens, cu_tokens,
-                             parent, repetition, frequency, presence, bias_ids, bias_values,
-                             cu_bias, mask, mask_rows, workspace, out)) as call:
+    used = () if stream is None else (
+        logits, cu_rows, history, cu_history, prompt_len, tokens, cu_tokens, parent, repetition,
+        frequency, presence, bias_ids, bias_values, cu_bias, mask, mask_rows, workspace, out)
+    with _Call(dev, stream, used) as call:
         ws, ws_at, ws_bytes = _scratch(256, dev, workspace)
         if out is None:
             out = torch.empty_like(logits, memory_format=torch.contiguous_format)
