@@ -25,10 +25,10 @@
 // one issues tcgen05.mma, eight run the epilogue from the other of two
 // accumulators (with four, one per scheduler, 1631 rows of 1749 to 59915 columns
 // with SiLU, residual and pre-activation took 636 us, with eight 448 us). Where
-// whole tiles would leave SMs idle in the last round, all tiles' stages are laid end to end and every CTA takes an equal run of them: what
-// it has of a tile that it shares goes out as an f32 partial, and a second launch
-// over all SMs adds the partials of a tile in the order of r and runs the
-// epilogue. (Joining inside the product, by the last part of a tile, left one SM
+// whole tiles would leave SMs idle in the last round, every CTA takes an equal run
+// of the stages: what it has of a tile that it shares goes out as an f32 partial,
+// and a second launch over all SMs adds the partials of a tile in the order of r
+// and runs the epilogue. (Joining inside the product, by the last part of a tile, left one SM
 // per tile reading the parts: 197 rows of 2880 x 2880 took 96 us that way.)
 #include <cuda.h>   // tensor map types; the encoder is resolved at run time
 
@@ -47,6 +47,10 @@ constexpr int HD_R = 64;          // reduction elements of a stage (128 bytes)
 constexpr int HD_MAX_J = 256;     // columns of a tile
 constexpr int HD_MAX_STAGES = 12;
 constexpr int HD_BAND = 8;        // tile columns of a band
+// Stages that the partials of rests cost their runs. 197 rows of 2880 x 2880 (six
+// runs of 8 stages per tile, or of 7 and rests of 3) take 16.4 us without rests,
+// 20.5 us with; 256 rows of 4096 x 4096 23.6 and 28.7 us.
+constexpr int HD_REST_COST = 4;
 constexpr int HD_STAGE_LD = 36;       // floats between columns of a warp's staging (no bank conflicts)
 constexpr int HD_STAGING = HD_EPI * 16 * HD_STAGE_LD * 4;   // 16 columns of 32 lanes per warp
 constexpr int HD_SMEM = 226 * 1024 - HD_STAGING - 1024;   // ring
@@ -56,14 +60,17 @@ constexpr int HD_A_BYTES = HD_I * HD_R * 2;
 struct HeadArgs {   // tiles of 128 x nt; a pair's tile counts as two, one per CTA
   int tiles_i, tiles_j, KB, nt, stages;
   int runs;            // 0: whole tiles; else the CTAs (pairs) that take equal runs of stages
-  int run_len, longer; // a run's stages; the first `longer` runs have one more
+  int q, len;          // the tiles' first q * len stages go in q runs of len each
+  int rest;            // the stages after these; all tiles' rests laid end to end are the other runs'
+  int run_len, longer; // stages of such a run; the first `longer` of them have one more
   int I, J;            // extents of the result
   long long ldo;       // elements between columns j of the result
   const __nv_bfloat16 *bias, *residual;
   __nv_bfloat16 *out, *pre;
   int act;
-  float *part;         // [2 per CTA][nt][128] partials of shared tiles
+  float *part;         // [part][CTAs of a tile][nt][128] partials of shared tiles
   int reset;           // this launch starts the call: the status is set to OK
+  int ctas;            // CTAs of a tile
   int vec;             // rows of the result and of its residual suit 16-byte accesses
   WsHeader *hdr;
 };
@@ -180,11 +187,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float *v) {
 __device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 // (1 + tanh u) / 2 = sigmoid(2u)
 __device__ __forceinline__ float gelu_gate(float z) {
-  return sigmoid(1.5957691216057308f * (z + 0.044715f * z * z * z));
+  return sigmoid(__fmul_rn(1.5957691216057308f, fmaf(__fmul_rn(0.044715f, z), __fmul_rn(z, z), z)));
 }
+// Products rounded by themselves: one fused with the residual's sum in some copies
+// of the epilogue would make the result depend on which of them runs.
 __device__ __forceinline__ float act_value(float z, int act) {
-  if (act == SPEC_ACT_SILU) return z * sigmoid(z);
-  if (act == SPEC_ACT_GELU) return z * gelu_gate(z);
+  if (act == SPEC_ACT_SILU) return __fmul_rn(z, sigmoid(z));
+  if (act == SPEC_ACT_GELU) return __fmul_rn(z, gelu_gate(z));
   return z;
 }
 __device__ __forceinline__ float act_slope(float z, int act) {
@@ -277,32 +286,59 @@ __device__ __forceinline__ Place place_of(const HeadArgs &a, int tile, int tiles
   return Place{r / width, band * HD_BAND + r % width};
 }
 
-// A CTA's work, one stretch [k0, k1) of a tile's stages after another. slot: which
-// of the CTA's two partials takes it, -1 for a whole tile.
+// A CTA's work, one stretch [k0, k1) of a tile's stages after another. part: the
+// partial that takes it, -1 for a whole tile.
+//
+// Runs: of a tile that q >= 1 runs fit into, run (tile, s) takes stages s len ..
+// (s + 1) len - 1, so that all tiles of a row or column are at the same r at a
+// time and share their operands in L2 (dx of 1001 rows, 32000 x 2048, with its
+// dz: 92 us; with all stages in one line over the runs 116 us, as each weight came
+// from HBM four times). What is left of the tiles is laid end to end over the
+// other runs. These are longer than a rest, so that a rest lies in two of them at
+// most; with q = 0 the rests are the tiles.
 struct Stretch {
-  int tile, k0, k1, slot;
+  int tile, k0, k1, part;
 };
-__device__ __forceinline__ int run_start(const HeadArgs &a, int g) { return g * a.run_len + min(g, a.longer); }
-struct Walk {
-  int at, end, step;   // stages (runs) or tiles
-};
-__device__ __forceinline__ Walk walk_of(const HeadArgs &a, int tiles, int g, int n) {
-  if (a.runs == 0) return Walk{g, tiles, n};
-  return Walk{run_start(a, g), run_start(a, g + 1), 0};
+__host__ __device__ __forceinline__ int rest_start(const HeadArgs &a, int e) {
+  return e * a.run_len + (e < a.longer ? e : a.longer);
 }
-__device__ __forceinline__ bool next_stretch(const HeadArgs &a, Walk &w, Stretch &s) {
+// The partial of a tile's run s.
+__host__ __device__ __forceinline__ int tile_part(const HeadArgs &a, int tile, int s) { return tile * (a.q + 2) + s; }
+// The partial of a rest that starts (piece 0) or ends (1) in run e.
+__host__ __device__ __forceinline__ int rest_part(const HeadArgs &a, int tile, int e, int piece) {
+  return a.q ? tile * (a.q + 2) + a.q + piece : 2 * e + (piece == 0);
+}
+struct Walk {
+  int at, end, step;   // stages of the rests, or tiles
+  int run;             // of the q per tile (at, end: 0, 1) or behind them; -1: whole tiles
+};
+__host__ __device__ __forceinline__ Walk walk_of(const HeadArgs &a, int tiles, int g, int n) {
+  if (a.runs == 0) return Walk{g, tiles, n, -1};
+  if (g < a.q * tiles) return Walk{0, 1, tiles, g};
+  const int e = g - a.q * tiles;
+  return Walk{rest_start(a, e), rest_start(a, e + 1), 0, g};
+}
+__host__ __device__ __forceinline__ bool next_stretch(const HeadArgs &a, Walk &w, Stretch &s) {
   if (w.at >= w.end) return false;
-  if (a.runs == 0) {
+  if (w.run < 0) {
     s = Stretch{w.at, 0, a.KB, -1};
     w.at += w.step;
+  } else if (w.step) {
+    const int split = w.run / w.step;
+    s.tile = w.run - split * w.step;
+    s.k0 = split * a.len;
+    s.k1 = a.KB < s.k0 + a.len ? a.KB : s.k0 + a.len;
+    s.part = s.k0 == 0 && s.k1 == a.KB ? -1 : tile_part(a, s.tile, split);
+    w.at = w.end;
   } else {
-    s.tile = w.at / a.KB;
-    s.k0 = w.at - s.tile * a.KB;
-    s.k1 = min(a.KB, s.k0 + (w.end - w.at));
-    // a run shares at most its first and its last tile; one that starts a tile
-    // is the last
-    s.slot = s.k0 == 0 && s.k1 == a.KB ? -1 : s.k0 == 0;
-    w.at += s.k1 - s.k0;
+    s.tile = w.at / a.rest;
+    const int r0 = w.at - s.tile * a.rest, left = w.end - w.at;
+    const int r1 = a.rest < r0 + left ? a.rest : r0 + left;
+    s.k0 = a.q * a.len + r0;
+    s.k1 = a.q * a.len + r1;
+    const int tiles = a.tiles_i / a.ctas * a.tiles_j;
+    s.part = s.k0 == 0 && s.k1 == a.KB ? -1 : rest_part(a, s.tile, w.run - a.q * tiles, r0 > 0);
+    w.at += r1 - r0;
   }
   return true;
 }
@@ -455,8 +491,8 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
       const uint32_t d = tmem + buf * (cols / 2) + ((uint32_t)(quad * 32) << 16);
       const int last = min(a.J, j0 + a.nt);   // columns behind it belong to the next tile
       constexpr int STEP = HD_EPI / 4 * 32;
-      if (w.slot >= 0) {   // 128 bytes per warp and column
-        float *mine = a.part + (long long)(blockIdx.x * 2 + w.slot) * a.nt * HD_I + li;
+      if (w.part >= 0) {   // 128 bytes per warp and column
+        float *mine = a.part + ((long long)w.part * CTAS + rank) * a.nt * HD_I + li;
         for (int c = half * 32; c < a.nt; c += STEP) {
           float v[32];
           tmem_ld32(d + c, v);
@@ -545,7 +581,7 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
 template <bool VEC>
 __global__ void __launch_bounds__(256) k_head_join(const HeadArgs a, int ctas) {
   // The blocks are on their SMs before the product ends (197 rows of 2880 x
-  // 2880: 18.4 us, launched after its end 19.2 us). Each waits, also where it has
+  // 2880: 0.8 us less than launched after its end). Each waits, also where it has
   // nothing to add, so that this grid does not end before the product's.
   after_previous();
   const int tile = blockIdx.x / ctas, rank = blockIdx.x % ctas;
@@ -553,14 +589,20 @@ __global__ void __launch_bounds__(256) k_head_join(const HeadArgs a, int ctas) {
   const int col = blockIdx.y * 16 + (VEC ? threadIdx.x / (HD_I / 8) : threadIdx.x / HD_I * 8);
   const Place at = place_of(a, tile, a.tiles_i / ctas);
   const int i = (at.ti * ctas + rank) * HD_I + il, j = at.tj * a.nt + col;
-  // the runs that have stages of this tile: g .. g + n - 1
-  const int first = tile * a.KB, head = a.longer * (a.run_len + 1);
-  auto run_of = [&](int x) { return x < head ? x / (a.run_len + 1) : a.longer + (x - head) / a.run_len; };
-  const int g = run_of(first), n = run_of(first + a.KB - 1) - g + 1;
+  // the partials of this tile: its q runs', then its rest's one or two
+  int e = 0, rests = 0;
+  if (a.rest) {
+    const int x0 = tile * a.rest, x1 = x0 + a.rest - 1, head = a.longer * (a.run_len + 1);
+    auto run_of = [&](int x) { return x < head ? x / (a.run_len + 1) : a.longer + (x - head) / a.run_len; };
+    e = run_of(x0);
+    rests = run_of(x1) - e + 1;
+  }
+  const int n = a.q + rests;
   if (n == 1 || col >= a.nt || j >= a.J || i >= a.I) return;   // one run: the product finished it
-  // run g's stretch starts the tile, the others' start their runs
-  const long long step = (long long)ctas * 2 * a.nt * HD_I;
-  const float *p = a.part + ((long long)(g * ctas + rank) * 2 * a.nt + col) * HD_I + il;
+  auto at_part = [&](int s) {
+    const int k = s < a.q ? tile_part(a, tile, s) : rest_part(a, tile, e + s - a.q, s - a.q);
+    return a.part + (((long long)k * ctas + rank) * a.nt + col) * HD_I + il;
+  };
   uint4 res;
   uint16_t res_column[8];
   if (VEC) res = residual8(a, i, j);
@@ -581,9 +623,9 @@ __global__ void __launch_bounds__(256) k_head_join(const HeadArgs a, int ctas) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) z[q] = start ? x[q] : z[q] + x[q];
   };
-  add(p + (long long)a.nt * HD_I, true);
+  add(at_part(0), true);
 #pragma unroll 4
-  for (int s = 1; s < n; ++s) add(p + s * step, false);
+  for (int s = 1; s < n; ++s) add(at_part(s), false);
   if (VEC) finish8(a, z, i, j, res);
   else finish_column<8>(a, z, i, j, res_column);
 }
@@ -836,6 +878,7 @@ int make_map(CUtensorMap *m, const void *p, long long rows, long long inner, lon
 struct Plan {
   int tiles_i, tiles_j, nt, KB;
   int runs;   // 0: whole tiles
+  int q, len, rest;   // as in HeadArgs
   bool pair;
   size_t part_bytes;
 };
@@ -863,7 +906,23 @@ Plan plan_of(long long I, long long J, long long R, bool b_mn, bool pair, double
   const double even = (double)total / runs * stage + 4.0 * full + 12.0 + 6.0 * full;
   // whole tiles also share their operands in L2 better: a tenth has to be won
   p.runs = 1.1 * even < whole && runs > 1 && total < (1ll << 30) ? (int)runs : 0;
-  p.part_bytes = p.runs ? align256((size_t)2 * p.runs * ctas * p.nt * HD_I * 4) : 0;
+  if (p.runs) {
+    p.q = (int)(runs / tiles);
+    if (p.q) {
+      // runs for the tiles' rests where these shorten the others by more than the
+      // partials that they add cost, about four stages
+      const int even_len = (int)((total + runs - 1) / runs);
+      p.len = (p.KB + p.q - 1) / p.q;
+      if (p.len > even_len + HD_REST_COST) p.len = even_len;
+      p.rest = std::max(0, p.KB - p.q * p.len);
+      if (p.rest == 0) {   // no rests, and no run without stages
+        p.q = (p.KB + p.len - 1) / p.len;
+        p.runs = (int)(p.q * tiles);
+      }
+    } else p.rest = p.KB;
+    const size_t parts = p.q ? (size_t)tiles * (p.q + 2) : (size_t)2 * p.runs;
+    p.part_bytes = align256(parts * ctas * p.nt * HD_I * 4);
+  }
   *cost_out = p.runs ? even : whole;
   return p;
 }
@@ -906,10 +965,12 @@ int launch_tiles(const Plan &p, const CUtensorMap &ma, const CUtensorMap &mb, He
 
 template <bool A_MN, bool B_MN>
 int launch_head(const Plan &p, const CUtensorMap &ma, const CUtensorMap &mb, HeadArgs a, cudaStream_t st) {
+  a.ctas = p.pair ? 2 : 1;
   a.tiles_i = p.tiles_i, a.tiles_j = p.tiles_j, a.KB = p.KB, a.nt = p.nt, a.runs = p.runs;
   if (p.runs) {
-    const int total = p.tiles_i / (p.pair ? 2 : 1) * p.tiles_j * p.KB;
-    a.run_len = total / p.runs, a.longer = total % p.runs;
+    const int tiles = p.tiles_i / (p.pair ? 2 : 1) * p.tiles_j, others = p.runs - p.q * tiles;
+    a.q = p.q, a.len = p.len, a.rest = p.rest;
+    if (others) a.run_len = tiles * p.rest / others, a.longer = tiles * p.rest % others;
   }
   a.vec = a.I % 8 == 0 && a.ldo % 8 == 0 && aligned(a.bias, 16) && aligned(a.residual, 16);
   const int sms = num_sms();
