@@ -137,9 +137,12 @@ size_t spec_distill_loss_workspace(int R_d, int V);
  *   loss[r]    = w KL(p || q)                 (nats, f32)
  *   grad[r, x] = (w / T) (q(x) - p(x))        = d loss[r] / d z_d[r, x]
  *
- * A token that is -inf in both rows takes no part; one that is -inf in the
- * draft row alone makes the loss +inf, its gradient stays finite. A
- * position of weight 0 has loss 0 and gradient 0, and its rows are not read.
+ * A token that is -inf in both rows takes no part. One that is -inf in the
+ * draft row alone makes the loss +inf (for a weight above 0), unless its p is 0
+ * in 64 bits, z_t more than 745 T below the row's largest: then it takes no part
+ * either. The gradient stays finite. Masks of finite values (-1e9, the type's
+ * lowest) are logits like any other. A position of weight 0 has loss 0 and
+ * gradient 0, and its rows are not read.
  *
  *   target       [R_d + B, V] (dt): request b's rows start at cu_draft[b] + b,
  *                its last one (the bonus position) is not used.
@@ -153,7 +156,7 @@ size_t spec_distill_loss_workspace(int R_d, int V);
  *
  * The status word reads SPEC_ERR_INVALID_ARG after bad offsets, a bad
  * temperature or weight, or a position of nonzero weight with a row that
- * holds no finite logit (its loss and gradient are then 0).
+ * holds no logit above the lowest finite f32 (its loss and gradient are then 0).
  */
 int spec_distill_loss(const void *target, const void *draft, int dt, int R_d,
                       int V, const int32_t *cu_draft, int B,

@@ -87,8 +87,8 @@ def distill(target, draft, cu, temperature=None, weight=None):
             et, ed = np.exp(zt - mt), np.exp(zd - md)
             p, q = et / et.sum(), ed / ed.sum()
             on = p > 0
-            with np.errstate(divide="ignore"):
-                lp, lq = np.log(p[on]), np.log(q[on])
+            # by the logits: a q that is 0 in 64 bits has a logarithm still
+            lp, lq = zt[on] - mt - np.log(et.sum()), zd[on] - md - np.log(ed.sum())
             loss[r] = w * float(np.sum(p[on] * (lp - lq)))
             grad[r] = w / T * (q - p)
             d = np.abs(zt[on] - zd[on])

@@ -2,10 +2,20 @@
 // (spec_distill_loss of specdraft.h).
 //
 // Two passes over a position's target row and draft row. The first keeps, per
-// thread and with running maxima, S_t = sum 2^((z_t - m_t) c), S_d likewise and
-// A = sum 2^((z_t - m_t) c) (z_t - z_d), c = log2(e) / T. Merged over the row,
-//   KL = ln 2 (A c / S_t - (m_t - m_d) c - log2 S_t + log2 S_d)
+// thread and with running maxima, S_t = sum e, e = 2^((z_t - m_t) c), S_d likewise
+// and A = sum e ((z_t - m_t) - (z_d - m_d)), c = log2(e) / T. Merged over the row,
+//   KL = ln 2 (A c / S_t - log2 S_t + log2 S_d)
 // and the second pass writes (w / T) (q - p).
+//
+// Where the maxima become M_t and M_d, A becomes
+//   f (A + S_t ((M_d - m_d) - (M_t - m_t))), f = 2^((m_t - M_t) c):
+// S_t is scaled by f before the product, so that tokens of a mask value (-1e9,
+// the type's lowest), which are all that a thread has seen at first, leave nothing
+// behind. A thread whose A is infinite or large at its share's end sums it anew,
+// token by token (add_rare): what a draft's mask value adds under a target's weight can
+// exceed f32 and is kept in units of FAR, and a token that the draft holds at -inf
+// makes the loss infinite by the largest z_t of such tokens, at the row's end, so
+// that neither the order of the tokens nor the schedule decides it.
 //
 // Resident schedule (k_distill_setup, k_distill_resident), for calls that fill
 // the SMs: a persistent cluster takes one position after another, each CTA a
@@ -24,7 +34,7 @@
 // grid is put together from two vectors by shifts (64 requests of 32003 bf16
 // logits: 18.4 us, element by element about 4 us more).
 //
-// Measured at 4096 positions of 201088 bf16 logits, 3/4 of them weighted: 0.81 ms
+// Measured at 4096 positions of 201088 bf16 logits, 3/4 of them weighted: 0.82 ms
 // (5.1 TB/s of the bytes that have to move); a cluster per position 1.06 ms (1.18 ms with its slices in shared memory but no
 // overlap of positions); persistent CTAs whose second-pass units follow the
 // first-pass units of later rows 1.04 to 1.8 ms, as L2 does not hold the rows
@@ -34,6 +44,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <cfloat>
 
 namespace sv {
 namespace {
@@ -67,10 +78,15 @@ struct DistillArgs {
   WsHeader *hdr;
 };
 
-// Statistics of part of a row pair.
+// Statistics of part of a row pair. far: what of A comes from differences beyond
+// NEAR, in units of FAR. hole: the largest z_t of the tokens that are -inf in the
+// draft alone.
 struct __align__(16) PairStat {
-  float mt, St, A, md, Sd;
+  float mt, St, A, md, Sd, far, hole;
 };
+__device__ __forceinline__ PairStat no_stat() { return PairStat{NO_MAX, 0.f, 0.f, NO_MAX, 0.f, 0.f, -INFINITY}; }
+constexpr float FAR = 18446744073709551616.f;   // 2^64
+constexpr float NEAR = 281474976710656.f;       // 2^48
 
 __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   f32x2 r;
@@ -126,20 +142,18 @@ __device__ __forceinline__ void store1(char *row, int i, float g) {
   else GST(reinterpret_cast<float *>(row) + i, g);
 }
 
-// The thread's maxima become at least mt and md. s.A is kept as the sum of
-// e_t ((z_t - m_t) - (z_d - m_d)) at the thread's own maxima.
+// The thread's maxima become at least mt and md. An A that is no longer finite
+// stays so.
 __device__ __forceinline__ void raise(PairStat &s, float mt, float md, float c) {
   if (mt > s.mt || md > s.md) {
     const float Mt = fmaxf(mt, s.mt), Md = fmaxf(md, s.md);
     const float f = ex2((s.mt - Mt) * c);
-    // an infinite A (a draft probability of 0) stays infinite
-    if (!isinf(s.A)) s.A = f * (s.A + s.St * ((Md - s.md) - (Mt - s.mt)));
     s.St *= f;
+    s.A = fmaf(s.A, f, s.St * ((Md - s.md) - (Mt - s.mt)));
     s.Sd *= ex2((s.md - Md) * c);
     s.mt = Mt, s.md = Md;
   }
 }
-
 // 2 N elements, less the maxima, into the sums.
 template <int N>
 __device__ __forceinline__ void add_pairs(PairStat &s, const f32x2 *xt, const f32x2 *xd, float c) {
@@ -157,12 +171,16 @@ __device__ __forceinline__ void add_pairs(PairStat &s, const f32x2 *xt, const f3
   s.Sd += lo2(Sd) + hi2(Sd);
   float a = lo2(A) + hi2(A);
   if (isnan(a)) {   // tokens that are -inf take no part where 2^(z_t) is 0
+    float most = 0.f;   // infinite with a token that is -inf in the draft alone
     a = 0.f;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      if (lo2(et[j]) > 0.f) a += lo2(et[j]) * (lo2(xt[j]) - lo2(xd[j]));
-      if (hi2(et[j]) > 0.f) a += hi2(et[j]) * (hi2(xt[j]) - hi2(xd[j]));
+      const float lo = lo2(xt[j]) - lo2(xd[j]), hi = hi2(xt[j]) - hi2(xd[j]);
+      if (lo2(et[j]) > 0.f) a += lo2(et[j]) * lo;
+      if (hi2(et[j]) > 0.f) a += hi2(et[j]) * hi;
+      most = fmaxf(most, fmaxf(lo, hi));
     }
+    if (most == INFINITY) a = INFINITY;
   }
   s.A += a;
 }
@@ -194,6 +212,38 @@ __device__ __forceinline__ void add_stats(PairStat &s, const f32x2 *zt, const f3
   add_pairs<N>(s, xt, xd, c);
 }
 
+// A anew, where it is not below FAR, from the share's elements at its maxima. Called
+// by the element, as inlined it takes the registers of the loops before it.
+__device__ __noinline__ float3 add_rare(float3 r, float xt, float xd, float mt, float c) {   // (A, far, hole)
+  const float e = ex2(xt * c);
+  if (xd == -INFINITY) {
+    if (xt > -INFINITY) r.z = fmaxf(r.z, xt + mt);
+  } else if (e > 0.f) {
+    const float d = xt - xd;
+    if (fabsf(d) < NEAR) r.x += e * d;
+    else r.y += e * (d * (1.f / FAR));
+  }
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void add_rare(PairStat &s, const f32x2 *xt, const f32x2 *xd, float c) {
+  float3 r = make_float3(s.A, s.far, s.hole);
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    r = add_rare(r, lo2(xt[j]), lo2(xd[j]), s.mt, c);
+    r = add_rare(r, hi2(xt[j]), hi2(xd[j]), s.mt, c);
+  }
+  s.A = r.x, s.far = r.y, s.hole = r.z;
+}
+template <bool BF16>
+__device__ __forceinline__ void add_rare16(PairStat &s, const uint4 &wt, const uint4 &wd, float c) {
+  constexpr int N = BF16 ? 4 : 2;
+  f32x2 xt[N], xd[N];
+  minus16<BF16>(wt, s.mt, xt);
+  minus16<BF16>(wd, s.md, xd);
+  add_rare<N>(s, xt, xd, c);
+}
+
 // The gradient's scalars: g = kd 2^((z_d - m_d) c) - kt 2^((z_t - m_t) c), kd = w / (T S_d)
 // and kt = w / (T S_t).
 struct GradK {
@@ -220,10 +270,24 @@ __device__ __forceinline__ void warp_merge(PairStat &s, float c) {
     M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
     D = fmaxf(D, __shfl_xor_sync(~0u, D, o));
   }
-  const float f = ex2((s.mt - M) * c);
+  const float f = ex2((s.mt - M) * c), move = (D - s.md) - (M - s.mt);
   s.St *= f;
-  if (!isinf(s.A)) s.A *= f;
+  s.A *= f;
   s.Sd *= ex2((s.md - D) * c);
+  float a = s.St * move;
+  if (__any_sync(~0u, !(fabsf(a) < FAR) || s.far != 0.f || s.hole > -INFINITY)) {
+    s.far *= f;
+    if (!(fabsf(a) < FAR)) {   // nothing, where St is 0 and `move` not finite
+      if (s.St > 0.f) s.far += s.St * (fminf(fmaxf(move, -FLT_MAX), FLT_MAX) * (1.f / FAR));
+      a = 0.f;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s.far += __shfl_xor_sync(~0u, s.far, o);
+      s.hole = fmaxf(s.hole, __shfl_xor_sync(~0u, s.hole, o));
+    }
+  }
+  s.A += a;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     s.St += __shfl_xor_sync(~0u, s.St, o);
@@ -235,10 +299,12 @@ __device__ __forceinline__ void warp_merge(PairStat &s, float c) {
 }
 
 __device__ __forceinline__ float loss_of(const PairStat &s, float c, float w) {
+  // a probability under a draft's 0 counts unless it is 0 itself in 64 bits,
+  // whose smallest value is 2^-1074
+  if (((double)s.hole - (double)s.mt) * c > -1075.0) return w * INFINITY;
   // in 64 bits: the terms are larger than their sum
-  const double kl = 0.693147180559945309 *
-                    ((double)s.A / (double)s.St * c - ((double)s.mt - (double)s.md) * c -
-                     (double)log2f(s.St) + (double)log2f(s.Sd));
+  const double kl = 0.693147180559945309 * (((double)s.A + (double)s.far * FAR) / (double)s.St * c -
+                                            (double)log2f(s.St) + (double)log2f(s.Sd));
   return (float)((double)w * kl);
 }
 
@@ -329,7 +395,7 @@ __global__ void __launch_bounds__(DI_THREADS) k_distill(DistillArgs a) {
     const uint4 x = GLD(tvec + i);
     return shift == 0 ? x : shift16(x, GLD(tvec + i + 1), shift);
   };
-  PairStat s{NO_MAX, 0.f, 0.f, NO_MAX, 0.f};
+  PairStat s = no_stat();
   int i = v0 + t;
   for (; i + DI_THREADS < v1; i += 2 * DI_THREADS) {
     const uint4 wd[2] = {GLD(dvec + i), GLD(dvec + i + DI_THREADS)};
@@ -344,19 +410,27 @@ __global__ void __launch_bounds__(DI_THREADS) k_distill(DistillArgs a) {
     const f32x2 zt = pk2(load1<BF16>(trow, single), -INFINITY), zd = pk2(load1<BF16>(drow, single), -INFINITY);
     add_stats<1>(s, &zt, &zd, c);
   }
-  s.A += s.St * (s.mt - s.md);
+  if (!(fabsf(s.A) < FAR)) {
+    s.A = 0.f;
+    for (int i = v0 + t; i < v1; i += DI_THREADS) add_rare16<BF16>(s, target16(i), GLD(dvec + i), c);
+    if (single >= 0) {
+      const f32x2 xt = pk2(load1<BF16>(trow, single) - s.mt, -INFINITY);
+      const f32x2 xd = pk2(load1<BF16>(drow, single) - s.md, -INFINITY);
+      add_rare<1>(s, &xt, &xd, c);
+    }
+  }
   warp_merge(s, c);
   if (lane == 0) s_part[warp] = s;
   __syncthreads();
   if (warp == 0) {
-    s = lane < DI_THREADS / 32 ? s_part[lane] : PairStat{NO_MAX, 0.f, 0.f, NO_MAX, 0.f};
+    s = lane < DI_THREADS / 32 ? s_part[lane] : no_stat();
     warp_merge(s, c);
     if (lane == 0) s_cta = s;
   }
   cluster.sync();
   // every warp merges the CTAs' statistics, a lane each, in the same order:
   // the same bits everywhere
-  s = lane < C ? *cluster.map_shared_rank(&s_cta, lane) : PairStat{NO_MAX, 0.f, 0.f, NO_MAX, 0.f};
+  s = lane < C ? *cluster.map_shared_rank(&s_cta, lane) : no_stat();
   warp_merge(s, c);
 
   const bool empty = row_empty(s.mt) || row_empty(s.md);
@@ -503,14 +577,16 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_resident(ResidentArgs
       bool ok = __all_sync(~0u, wait_phase<false>(&s_parts[y], par, &s_abort));
       const RowInfo x = s_row[k & 15];
       if (ok) {
-        PairStat s = lane < DR_WARPS ? s_part[y][lane] : PairStat{NO_MAX, 0.f, 0.f, NO_MAX, 0.f};
+        PairStat s = lane < DR_WARPS ? s_part[y][lane] : no_stat();
         warp_merge(s, x.c);
         if (lane < C) {
           const uint32_t to = peer_addr(&s_stat[y][rank], lane);
           asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(s.mt), "f"(s.St),
                        "f"(s.A), "f"(s.md)
                        : "memory");
-          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 16), "f"(s.Sd) : "memory");
+          asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %3};" ::"r"(to + 16), "f"(s.Sd), "f"(s.far),
+                       "f"(s.hole)
+                       : "memory");
           asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
                            peer_addr(&s_xch[y], lane))
                        : "memory");
@@ -522,7 +598,7 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_resident(ResidentArgs
         if (lane == 0) set_status(d.hdr, SPEC_ERR_TIMEOUT, 2);
         break;
       }
-      PairStat z = lane < C ? s_stat[y][lane] : PairStat{NO_MAX, 0.f, 0.f, NO_MAX, 0.f};
+      PairStat z = lane < C ? s_stat[y][lane] : no_stat();
       warp_merge(z, x.c);   // the same bits in every CTA of the cluster
       if (lane == 0) {
         const bool none = row_empty(z.mt) || row_empty(z.md);
@@ -544,7 +620,7 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_resident(ResidentArgs
       s_abort = 1;
       if (lane == 0) set_status(d.hdr, SPEC_ERR_TIMEOUT, where);
     };
-    PairStat s{NO_MAX, 0.f, 0.f, NO_MAX, 0.f};
+    PairStat s = no_stat();
     // the first pass over pieces p0 .. p1-1 of this cluster's k-th row
     auto first_pass = [&](int k, int p0, int p1) {
       float c = 0.f;
@@ -571,13 +647,20 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_resident(ResidentArgs
         }
       }
       if (p1 < P || !ok) return;
-      s.A += s.St * (s.mt - s.md);
+      if (!(fabsf(s.A) < FAR)) {   // the row's pieces stay until its second pass
+        s.A = 0.f;
+        for (int p = 0; p < P; ++p) {
+          const uint8_t *at = ring + (k * P + p) % DR_SLOTS * 2 * DR_PIECE;
+          for (int v = ct; v < min(DR_PV, u1 - u0 - p * DR_PV); v += 32 * DR_WARPS)
+            add_rare16<BF16>(s, lds128(at + v * 16), lds128(at + DR_PIECE + v * 16), c);
+        }
+      }
       warp_merge(s, c);
       if (lane == 0) {
         s_part[k & 1][cw] = s;
         mbar_arrive(&s_parts[k & 1]);
       }
-      s = PairStat{NO_MAX, 0.f, 0.f, NO_MAX, 0.f};
+      s = no_stat();
     };
     auto second_pass = [&](int k) {
       if (!__all_sync(~0u, wait_phase<false>(&s_known[k & 1], (k >> 1) & 1, &s_abort))) return give_up(3);
