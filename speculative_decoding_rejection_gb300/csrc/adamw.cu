@@ -65,7 +65,7 @@ struct AdArgs {
   const AdHeader *table;
   long long n_items;
   float b1, b2, o1, o2, eps;    // o = 1 - b, taken in 64 bits
-  float keep, lr_c1, inv_c2;    // 1 - lr wd, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+  float lr_wd, lr_c1, inv_c2;   // lr wd, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
   float lr, wd, c1, lb1, lb2;   // for lr or t read on the device: 1 - b1^t, ln b1, ln b2
   const float *grad_scale, *lr_dev;
   const int32_t *step_dev;
@@ -74,7 +74,7 @@ struct AdArgs {
 
 // The scalars of a step.
 struct AdStep {
-  float gs, keep, lr_c1, inv_c2, eps, b1, b2, o1, o2;
+  float gs, lr_wd, lr_c1, inv_c2, eps, b1, b2, o1, o2;
 };
 
 // One element's moments. Each product is rounded by itself: gradients of few
@@ -105,14 +105,16 @@ __device__ __forceinline__ bool is_normal(float least, float most) { return leas
 // The weight. The quotient is within two units of the last place; the divisor
 // is zero or normal, as eps is. With 32-bit states the quotient as one operation
 // leaves the loads better placed (200M elements 785 us, as a reciprocal 828);
-// with 8 bits its three instructions more count (1390 us to 1353).
+// with 8 bits its three instructions more count (1390 us to 1353). What changes is
+// summed before it meets the weight: 1 - lr wd has few digits of a small lr wd, and
+// none below 2^-25.
 template <bool STATE8>
 __device__ __forceinline__ float updated(const AdStep &s, float p, float m, float r) {
   const float d = r * s.inv_c2 + s.eps;
-  if (!STATE8) return p * s.keep - s.lr_c1 * __fdividef(m, d);
+  if (!STATE8) return p - fmaf(s.lr_wd, p, s.lr_c1 * __fdividef(m, d));
   float q;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(d));
-  return p * s.keep - s.lr_c1 * (m * q);
+  return p - fmaf(s.lr_wd, p, s.lr_c1 * (m * q));
 }
 
 // N f32 values from / to a buffer of f32 (16-byte vectors).
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(AD_THREADS, STATE8 ? AD_CTAS_PER_SM : 1) k_ada
   AdItem it = items[blockIdx.x];
   AdStep s;
   s.gs = a.grad_scale ? *a.grad_scale : 1.f;
-  s.keep = a.keep, s.lr_c1 = a.lr_c1, s.inv_c2 = a.inv_c2, s.eps = a.eps;
+  s.lr_wd = a.lr_wd, s.lr_c1 = a.lr_c1, s.inv_c2 = a.inv_c2, s.eps = a.eps;
   s.b1 = a.b1, s.b2 = a.b2, s.o1 = a.o1, s.o2 = a.o2;
   if (a.lr_dev != nullptr || a.step_dev != nullptr) {
     const float lr = a.lr_dev ? *a.lr_dev : a.lr;
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(AD_THREADS, STATE8 ? AD_CTAS_PER_SM : 1) k_ada
       c1 = -expm1f((float)t * a.lb1);
       s.inv_c2 = 1.f / sqrtf(-expm1f((float)t * a.lb2));
     }
-    s.keep = 1.f - lr * a.wd;
+    s.lr_wd = lr * a.wd;
     s.lr_c1 = lr / c1;
   }
   if (STATE8) {
@@ -533,7 +535,7 @@ extern "C" int spec_adamw_step(const void *table, int64_t n_items, int state_bit
   a.b1 = (float)h.beta1, a.b2 = (float)h.beta2;
   a.o1 = (float)(1.0 - h.beta1), a.o2 = (float)(1.0 - h.beta2);
   a.eps = h.eps > 0.0 ? std::max((float)h.eps, FLT_MIN) : 0.f;   // normal, as updated() takes it
-  a.keep = (float)(1.0 - h.lr * h.weight_decay);
+  a.lr_wd = (float)(h.lr * h.weight_decay);
   a.lr_c1 = (float)(h.lr / c1);
   a.inv_c2 = (float)(1.0 / std::sqrt(c2));
   a.lr = (float)h.lr, a.wd = (float)h.weight_decay, a.c1 = (float)c1;
