@@ -64,6 +64,11 @@ extern "C" {
  *                1 if token x is allowed.
  *   mask_rows    [R] int32: the mask's row that row r goes by, -1 for none.
  *                NULL: row r goes by mask row r (then n_mask >= R).
+ *   n_history, n_tokens, n_bias  how many entries history, tokens (of a linear
+ *                batch) and bias_ids have: offsets past them are reported, and
+ *                nothing behind them is read. 0: not given, the offsets are
+ *                taken as they are. Below 0: none (the address, which must not
+ *                be NULL, is not read).
  */
 typedef struct {
   const int32_t *history;
@@ -81,6 +86,9 @@ typedef struct {
   const uint32_t *mask;
   const int32_t *mask_rows;
   int32_t n_mask;
+  int32_t n_history;
+  int32_t n_tokens;
+  int32_t n_bias;
 } spec_logits_rules;
 
 /* Bytes of workspace spec_process_logits needs: the 256-byte header. */

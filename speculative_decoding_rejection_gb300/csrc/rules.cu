@@ -22,6 +22,7 @@
 #include "draft.cuh"
 
 #include <algorithm>
+#include <climits>
 
 namespace sv {
 namespace {
@@ -38,6 +39,7 @@ struct RulesArgs {
   const int32_t *cu_rows;
   int R, V, B, max_rows, nch, seg, inplace;
   spec_logits_rules r;
+  int n_history, n_tokens, n_bias;   // bounds on the lists' offsets
   WsHeader *hdr;
 };
 
@@ -109,16 +111,17 @@ __global__ void __launch_bounds__(RU_THREADS) k_rules(RulesArgs a) {
   bool bad = !(rho > 0.f) || !isfinite(rho) || !isfinite(fr) || !isfinite(pr);
   if (a.r.history != nullptr) {
     h0 = GLD(a.r.cu_history + b), h1 = GLD(a.r.cu_history + b + 1);
-    if (h0 < 0 || h1 < h0) bad = true, h1 = h0 = 0;
+    if (h0 < 0 || h1 < h0 || h1 > a.n_history) bad = true, h1 = h0 = 0;
     hp = a.r.prompt_len ? GLD(a.r.prompt_len + b) : 0;
   }
   if (a.r.bias_ids != nullptr) {
     b0 = GLD(a.r.cu_bias + b), b1 = GLD(a.r.cu_bias + b + 1);
-    if (b0 < 0 || b1 < b0) bad = true, b1 = b0 = 0;
+    if (b0 < 0 || b1 < b0 || b1 > a.n_bias) bad = true, b1 = b0 = 0;
   }
   if (a.r.tokens != nullptr && !tree) {
-    k0 = GLD(a.r.cu_tokens + b), K = GLD(a.r.cu_tokens + b + 1) - k0;
-    if (k0 < 0 || K < 0) bad = true, K = 0;
+    const int k1 = GLD(a.r.cu_tokens + b + 1);
+    k0 = GLD(a.r.cu_tokens + b), K = k1 - k0;
+    if (k0 < 0 || k1 < k0 || k1 > a.n_tokens) bad = true, K = 0;
   }
   int held[RU_HELD];   // this thread's first history tokens, on their way early
 #pragma unroll
@@ -453,6 +456,10 @@ extern "C" int spec_process_logits(const void *logits, int dt, int R, int V,
   a.B = B;
   a.max_rows = max_rows;
   a.inplace = logits == out;
+  auto bound = [](int n) { return n == 0 ? INT_MAX : std::max(n, 0); };
+  a.n_history = bound(r.n_history);
+  a.n_tokens = bound(r.n_tokens);
+  a.n_bias = bound(r.n_bias);
   a.hdr = static_cast<WsHeader *>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
 
@@ -465,7 +472,7 @@ extern "C" int spec_process_logits(const void *logits, int dt, int R, int V,
   int total = 0;
   if (r.history != nullptr) {
     if (check_read_int(r.cu_history + B, st, &total) != SPEC_OK) return SPEC_ERR_CUDA;
-    check_add(r.history, (unsigned long long)std::max(total, 0) * 4);
+    check_add(r.history, (unsigned long long)std::min(std::max(total, 0), a.n_history) * 4);
     check_add(r.cu_history, (B + 1) * 4ull);
     check_add(r.prompt_len, B * 4ull);
   }
@@ -473,6 +480,7 @@ extern "C" int spec_process_logits(const void *logits, int dt, int R, int V,
     total = R;
     if (r.cu_tokens != nullptr) {
       if (check_read_int(r.cu_tokens + B, st, &total) != SPEC_OK) return SPEC_ERR_CUDA;
+      total = std::min(total, a.n_tokens);
       check_add(r.cu_tokens, (B + 1) * 4ull);
     }
     check_add(r.tokens, (unsigned long long)std::max(total, 0) * 4);
@@ -483,6 +491,7 @@ extern "C" int spec_process_logits(const void *logits, int dt, int R, int V,
   check_add(r.presence, B * 4ull);
   if (r.bias_ids != nullptr) {
     if (check_read_int(r.cu_bias + B, st, &total) != SPEC_OK) return SPEC_ERR_CUDA;
+    total = std::min(total, a.n_bias);
     check_add(r.bias_ids, (unsigned long long)std::max(total, 0) * 4);
     check_add(r.bias_values, (unsigned long long)std::max(total, 0) * 4);
     check_add(r.cu_bias, (B + 1) * 4ull);

@@ -26,7 +26,8 @@ class SpecLogitsRules(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("history", "cu_history", "prompt_len", "tokens", "cu_tokens", "parent",
                  "repetition", "frequency", "presence", "bias_ids", "bias_values", "cu_bias",
-                 "mask", "mask_rows")] + [("n_mask", ctypes.c_int32)]
+                 "mask", "mask_rows")] + [(n, ctypes.c_int32) for n in
+                                          ("n_mask", "n_history", "n_tokens", "n_bias")]
 
 
 class SpecAdamwTensor(ctypes.Structure):
@@ -45,7 +46,7 @@ class SpecAdamwHyper(ctypes.Structure):
 
 # the two records as they lie in memory, for calls (less host time than a
 # Structure's fields)
-_RULES = struct.Struct("@14Pi4x")
+_RULES = struct.Struct("@14P4i")
 _HYPER = struct.Struct("@5dq3P")
 assert _RULES.size == ctypes.sizeof(SpecLogitsRules)
 assert _HYPER.size == ctypes.sizeof(SpecAdamwHyper)
@@ -82,6 +83,17 @@ def _arg(name, t, dtype, numel, dev):
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{dev}")
     raise ValueError(f"{name} has {t.numel()} elements, {numel} are needed")
+
+
+def _list(name, t, dtype, offsets_at, dev):
+    """(address, entries) of a list that offsets divide, as spec_logits_rules takes
+    them. An empty list has no address: the offsets' stands for it, unread."""
+    if t is None:
+        return 0, 0
+    n = t.numel()
+    if n == 0:
+        return (offsets_at, -1) if offsets_at else (0, 0)
+    return _arg(name, t, dtype, 0, dev), min(n, 0x7fffffff)
 
 
 def _device(name, t):
@@ -168,29 +180,27 @@ def spec_process_logits(logits, cu_rows, *, max_rows: int, history=None, cu_hist
             raise ValueError(f"mask must be [n, {(V + 31) // 32}] int32 words")
         if n_mask == 0 and mask_rows is not None:   # no row goes by a mask
             mask = mask_rows = None
-    # an empty list has no address: without entries the step is left out
-    if history is not None and history.numel() == 0:
-        history = cu_history = prompt_len = None
-    if tokens is not None and tokens.numel() == 0:
-        tokens = cu_tokens = parent = None
-    if bias_ids is not None and bias_ids.numel() == 0:
-        bias_ids = bias_values = cu_bias = None
-    n_tokens = R if parent is not None else 0
-    n_bias = bias_ids.numel() if bias_ids is not None else 0
+    cu_history_at = _arg("cu_history", cu_history, i32, B + 1, dev) or 0
+    cu_tokens_at = _arg("cu_tokens", cu_tokens, i32, B + 1, dev) or 0
+    cu_bias_at = _arg("cu_bias", cu_bias, i32, B + 1, dev) or 0
+    history_at, n_history = _list("history", history, i32, cu_history_at, dev)
+    bias_at, n_bias = _list("bias_ids", bias_ids, i32, cu_bias_at, dev)
+    values_at = cu_bias_at if n_bias < 0 else _arg("bias_values", bias_values, f32, n_bias, dev) or 0
+    if parent is None:
+        tokens_at, n_tokens = _list("tokens", tokens, i32, cu_tokens_at, dev)
+    else:
+        tokens_at, n_tokens = _arg("tokens", tokens, i32, R, dev) or 0, 0
     rules = _RULES.pack(
-        _arg("history", history, i32, 0, dev) or 0,
-        _arg("cu_history", cu_history, i32, B + 1, dev) or 0,
-        _arg("prompt_len", prompt_len, i32, B, dev) or 0,
-        _arg("tokens", tokens, i32, n_tokens, dev) or 0,
-        _arg("cu_tokens", cu_tokens, i32, B + 1, dev) or 0,
+        history_at, cu_history_at,
+        _arg("prompt_len", prompt_len, i32, B, dev) or 0 if history_at else 0,
+        tokens_at, cu_tokens_at,
         _arg("parent", parent, i32, R, dev) or 0,
         _arg("repetition", repetition, f32, B, dev) or 0,
         _arg("frequency", frequency, f32, B, dev) or 0,
         _arg("presence", presence, f32, B, dev) or 0,
-        _arg("bias_ids", bias_ids, i32, 0, dev) or 0,
-        _arg("bias_values", bias_values, f32, n_bias, dev) or 0,
-        _arg("cu_bias", cu_bias, i32, B + 1, dev) or 0,
-        _arg("mask", mask, i32, 0, dev) or 0, _arg("mask_rows", mask_rows, i32, R, dev) or 0, n_mask)
+        bias_at, values_at, cu_bias_at,
+        _arg("mask", mask, i32, 0, dev) or 0, _arg("mask_rows", mask_rows, i32, R, dev) or 0,
+        n_mask, n_history, n_tokens, n_bias)
     used = () if stream is None else (
         logits, cu_rows, history, cu_history, prompt_len, tokens, cu_tokens, parent, repetition,
         frequency, presence, bias_ids, bias_values, cu_bias, mask, mask_rows, workspace, out)

@@ -1,0 +1,62 @@
+"""The lists of spec_process_logits (histories, drafts, biases): offsets past
+their ends are reported and nothing behind them is read; empty lists."""
+import numpy as np
+import pytest
+import torch
+
+import speculative_decoding_rejection_gb300 as sv
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+LISTS = {"history": ("history", "cu_history"), "drafts": ("tokens", "cu_tokens"), "biases": ("bias_ids", "cu_bias")}
+
+
+def ints(*x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def rules(which, entries, offsets):
+    ids, cu = LISTS[which]
+    r = {ids: ints(*entries), cu: ints(*offsets)}
+    if which == "biases":
+        r["bias_values"] = torch.ones(len(entries), device=DEV)
+    return r
+
+
+def call(r, rows=(3, 3), V=200, dtype=torch.float32):
+    cu = np.concatenate([[0], np.cumsum(rows)])
+    z = torch.randn(int(cu[-1]), V, generator=torch.Generator().manual_seed(1)).to(dtype).to(DEV)
+    out, ws = sv.spec_process_logits(z, ints(*cu.tolist()), max_rows=max(rows),
+                                     repetition=torch.full((len(rows),), 1.5, device=DEV), **r)
+    return z, out, sv.spec_get_status(ws)
+
+
+@pytest.mark.parametrize("checked", [True, False])
+@pytest.mark.parametrize("which", LISTS)
+@pytest.mark.parametrize("entries,offsets", [
+    ([5, 6, 7, 8], [0, 2, 5]),        # one past the end
+    ([5, 6, 7, 8], [0, 2, 1 << 28]),
+    ([5, 6, 7, 8], [0, 1 << 30, (1 << 30) + 2]),
+    ([], [0, 0, 2]), ([], [0, 1, 1])])
+def test_offsets_past_a_list_are_reported(which, entries, offsets, checked):
+    sv.use_checked_library(checked)
+    try:
+        assert call(rules(which, entries, offsets))[2] == sv.SPEC_ERR_INVALID_ARG
+    finally:
+        sv.use_checked_library(False)
+
+
+@pytest.mark.parametrize("which", LISTS)
+def test_offsets_up_to_the_end_are_taken(which):
+    z, out, status = call(rules(which, [5, 6, 7, 8], [0, 2, 4]))
+    assert status == sv.SPEC_OK and not torch.equal(z, out)
+
+
+@pytest.mark.parametrize("which", LISTS)
+def test_empty_lists_change_nothing(which):
+    z, out, status = call(rules(which, [], [0, 0, 0]))
+    assert status == sv.SPEC_OK and torch.equal(z, out)
+    r = rules(which, [], [0, 0, 0])   # without offsets too
+    r.pop(LISTS[which][1])
+    z, out, status = call(r)
+    assert status == sv.SPEC_OK and torch.equal(z, out)
