@@ -123,12 +123,15 @@ __global__ void __launch_bounds__(RU_THREADS) k_rules(RulesArgs a) {
     k0 = GLD(a.r.cu_tokens + b), K = k1 - k0;
     if (k0 < 0 || k1 < k0 || k1 > a.n_tokens) bad = true, K = 0;
   }
+  // Entries of the lists are counted in 32 bits without a sign: a step behind the
+  // last one of 2^31 - 1 must not come out below the first.
+  const uint32_t uh0 = h0, uh1 = h1, ub0 = b0, ub1 = b1;
   int held[RU_HELD];   // this thread's first history tokens, on their way early
 #pragma unroll
   for (int q = 0; q < RU_HELD; ++q) {
-    const int j = h0 + q * RU_THREADS + t;
-    held[q] = j < h1 ? GLD(a.r.history + j) : -1;
-    if (j < h1 && (held[q] < 0 || held[q] >= a.V)) bad = true, held[q] = -1;
+    const uint32_t j = uh0 + q * RU_THREADS + t;
+    held[q] = j < uh1 ? GLD(a.r.history + j) : -1;
+    if (j < uh1 && (held[q] < 0 || held[q] >= a.V)) bad = true, held[q] = -1;
   }
 
   if (t < CH / 32) sm.bits[t] = 0;
@@ -252,7 +255,7 @@ __global__ void __launch_bounds__(RU_THREADS) k_rules(RulesArgs a) {
 #pragma unroll
   for (int q = 0; q < RU_HELD; ++q)
     if (held[q] >= 0) touch(held[q]);
-  for (int j = h0 + RU_HELD * RU_THREADS + t; j < h1; j += RU_THREADS) {
+  for (uint32_t j = uh0 + RU_HELD * RU_THREADS + t; j < uh1; j += RU_THREADS) {
     const int tok = GLD(a.r.history + j);
     if (tok < 0 || tok >= a.V) bad = true;
     else touch(tok);
@@ -264,7 +267,7 @@ __global__ void __launch_bounds__(RU_THREADS) k_rules(RulesArgs a) {
       else touch(tok);
     }
   }
-  for (int j = b0 + t; j < b1; j += RU_THREADS) {
+  for (uint32_t j = ub0 + t; j < ub1; j += RU_THREADS) {
     const int id = GLD(a.r.bias_ids + j);
     const float bv = GLD(a.r.bias_values + j);
     if (id < 0 || id >= a.V || isnan(bv) || bv == INFINITY) {
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(RU_THREADS) k_rules(RulesArgs a) {
     } else if (id >= c0 && id < c0 + CH) {
       touch(id);
       const int k = atomicAdd(&sm.n_bias, 1);
-      if (k < RU_BIASES) sm.bias[k] = make_int2(id - c0, j);
+      if (k < RU_BIASES) sm.bias[k] = make_int2(id - c0, (int)j);
     }
   }
   if (t < n) {   // what comes in with the rows: a count, no bit yet
@@ -294,8 +297,8 @@ __global__ void __launch_bounds__(RU_THREADS) k_rules(RulesArgs a) {
 #pragma unroll
   for (int q = 0; q < RU_HELD; ++q)
     if (held[q] >= 0) count(held[q], q * RU_THREADS + t < hp);
-  for (int j = h0 + RU_HELD * RU_THREADS + t; j < h1; j += RU_THREADS)
-    count(GLD(a.r.history + j), j - h0 < hp);
+  for (uint32_t j = uh0 + RU_HELD * RU_THREADS + t; j < uh1; j += RU_THREADS)
+    count(GLD(a.r.history + j), (int)(j - uh0) < hp);
   if (!tree)
     for (int j = t; j < min(i0, K); j += RU_THREADS) count(GLD(a.r.tokens + k0 + j), false);
   __syncthreads();

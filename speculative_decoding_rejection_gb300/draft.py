@@ -93,7 +93,7 @@ def _list(name, t, dtype, offsets_at, dev):
     n = t.numel()
     if n == 0:
         return (offsets_at, -1) if offsets_at else (0, 0)
-    return _arg(name, t, dtype, 0, dev), min(n, 0x7fffffff)
+    return _arg(name, t, dtype, 0, dev), n if n < 0x7fffffff else 0x7fffffff
 
 
 def _device(name, t):

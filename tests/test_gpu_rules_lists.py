@@ -60,3 +60,27 @@ def test_empty_lists_change_nothing(which):
     r.pop(LISTS[which][1])
     z, out, status = call(r)
     assert status == sv.SPEC_OK and torch.equal(z, out)
+
+
+def test_lists_that_end_at_the_last_offset():
+    """Offsets up to 2^31 - 1: the last entries of the longest lists."""
+    n, used, V = (1 << 31) - 1, 601, 5000
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 26 GB")
+    g = torch.Generator().manual_seed(3)
+    tail = torch.randint(0, V, (used,), generator=g, dtype=torch.int32)
+    ids = torch.randperm(V, generator=g)[:used].to(torch.int32)
+    short = dict(history=tail, bias_ids=ids, bias_values=torch.randn(used, generator=g))
+    results = []
+    for size in (used, n):
+        r = {}
+        for name, x in short.items():
+            r[name] = torch.empty(size, dtype=x.dtype, device=DEV)
+            r[name][size - used:] = x.to(DEV)
+        for cu in ("cu_history", "cu_bias"):
+            r[cu] = ints(size - used, size)
+        z, out, status = call({**r, "prompt_len": ints(100), "frequency": torch.ones(1, device=DEV)}, rows=(2,), V=V)
+        assert status == sv.SPEC_OK and not torch.equal(z, out)
+        results.append(out)
+        del r
+    assert torch.equal(*results)
