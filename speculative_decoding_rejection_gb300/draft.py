@@ -178,8 +178,8 @@ def spec_process_logits(logits, cu_rows, *, max_rows: int, history=None, cu_hist
         n_mask, words = mask.shape
         if words != (V + 31) // 32:
             raise ValueError(f"mask must be [n, {(V + 31) // 32}] int32 words")
-        if n_mask == 0 and mask_rows is not None:   # no row goes by a mask
-            mask = mask_rows = None
+        if mask_rows is None and n_mask < R:
+            raise ValueError(f"mask has {n_mask} rows, the logits {R}")
     cu_history_at = _arg("cu_history", cu_history, i32, B + 1, dev) or 0
     cu_tokens_at = _arg("cu_tokens", cu_tokens, i32, B + 1, dev) or 0
     cu_bias_at = _arg("cu_bias", cu_bias, i32, B + 1, dev) or 0
@@ -190,6 +190,10 @@ def spec_process_logits(logits, cu_rows, *, max_rows: int, history=None, cu_hist
         tokens_at, n_tokens = _list("tokens", tokens, i32, cu_tokens_at, dev)
     else:
         tokens_at, n_tokens = _arg("tokens", tokens, i32, R, dev) or 0, 0
+    mask_rows_at = _arg("mask_rows", mask_rows, i32, R, dev) or 0
+    mask_at = _arg("mask", mask, i32, 0, dev) or 0
+    if mask_at == 0 and mask is not None:   # no rows: an address that is not read, and any mask row >= 0 is bad
+        mask_at = mask_rows_at
     rules = _RULES.pack(
         history_at, cu_history_at,
         _arg("prompt_len", prompt_len, i32, B, dev) or 0 if history_at else 0,
@@ -199,8 +203,7 @@ def spec_process_logits(logits, cu_rows, *, max_rows: int, history=None, cu_hist
         _arg("frequency", frequency, f32, B, dev) or 0,
         _arg("presence", presence, f32, B, dev) or 0,
         bias_at, values_at, cu_bias_at,
-        _arg("mask", mask, i32, 0, dev) or 0, _arg("mask_rows", mask_rows, i32, R, dev) or 0,
-        n_mask, n_history, n_tokens, n_bias)
+        mask_at, mask_rows_at, n_mask, n_history, n_tokens, n_bias)
     used = () if stream is None else (
         logits, cu_rows, history, cu_history, prompt_len, tokens, cu_tokens, parent, repetition,
         frequency, presence, bias_ids, bias_values, cu_bias, mask, mask_rows, workspace, out)
