@@ -85,6 +85,20 @@ def _arg(name, t, dtype, numel, dev):
     raise ValueError(f"{name} has {t.numel()} elements, {numel} are needed")
 
 
+def _matrix(name, t, dtype, rows, width, dev):
+    """The address of `rows` rows of `width` elements: a flat buffer, or a tensor
+    whose trailing dimensions make up a row."""
+    if t is not None and t.dim() > 1 and t.shape[-1] != width:
+        row = 1
+        for n in reversed(t.shape):
+            row *= n
+            if row == width:
+                break
+        else:
+            raise ValueError(f"{name} must have rows of {width} elements, its shape is {tuple(t.shape)}")
+    return _arg(name, t, dtype, rows * width, dev)
+
+
 def _list(name, t, dtype, offsets_at, dev):
     """(address, entries) of a list that offsets divide, as spec_logits_rules takes
     them. An empty list has no address: the offsets' stands for it, unread."""
@@ -192,7 +206,7 @@ def spec_process_logits(logits, cu_rows, *, max_rows: int, history=None, cu_hist
         tokens_at, n_tokens = _arg("tokens", tokens, i32, R, dev) or 0, 0
     mask_rows_at = _arg("mask_rows", mask_rows, i32, R, dev) or 0
     mask_at = _arg("mask", mask, i32, 0, dev) or 0
-    if mask_at == 0 and mask is not None:   # no rows: an address that is not read, and any mask row >= 0 is bad
+    if mask_at == 0 and mask is not None:   # no rows: an address that is not read
         mask_at = mask_rows_at
     rules = _RULES.pack(
         history_at, cu_history_at,
@@ -214,7 +228,7 @@ def spec_process_logits(logits, cu_rows, *, max_rows: int, history=None, cu_hist
         code = _sv.lib().spec_process_logits(
             _arg("logits", logits, logits.dtype, 0, dev), _f32_or_bf16(logits), R, V,
             _arg("cu_rows", cu_rows, i32, 1, dev), B, max_rows, rules,
-            _arg("out", out, logits.dtype, R * V, dev), ws_at, ws_bytes, call.raw)
+            _matrix("out", out, logits.dtype, R, V, dev), ws_at, ws_bytes, call.raw)
     _sv._check(code, "spec_process_logits")
     return out, ws
 
@@ -250,7 +264,7 @@ def spec_distill_loss(target, draft, cu_draft, temperature=None, weight=None, *,
             _arg("target", target, dt, 0, dev), _arg("draft", draft, dt, 0, dev),
             _f32_or_bf16(draft), R, V, _arg("cu_draft", cu_draft, torch.int32, 1, dev), B,
             _arg("temperature", temperature, f32, B, dev), _arg("weight", weight, f32, R, dev),
-            _arg("loss", loss, f32, R, dev), _arg("grad", grad, dt, R * V, dev), ws_at, ws_bytes,
+            _arg("loss", loss, f32, R, dev), _matrix("grad", grad, dt, R, V, dev), ws_at, ws_bytes,
             call.raw)
     _sv._check(code, "spec_distill_loss")
     return loss, grad, ws
@@ -302,8 +316,8 @@ def spec_head_forward(x, weight, bias=None, residual=None, *, act: int = SPEC_AC
             pre = torch.empty_like(y) if want_pre else None
         code = _sv.lib().spec_head_forward(
             _arg("x", x, bf, 0, dev), _arg("weight", weight, bf, 0, dev),
-            _arg("bias", bias, bf, N, dev), _arg("residual", residual, bf, M * N, dev), M, N, K,
-            act, _arg("y", y, bf, M * N, dev), _arg("pre", pre, bf, M * N, dev), ws_at, ws_bytes,
+            _arg("bias", bias, bf, N, dev), _matrix("residual", residual, bf, M, N, dev), M, N, K,
+            act, _matrix("y", y, bf, M, N, dev), _matrix("pre", pre, bf, M, N, dev), ws_at, ws_bytes,
             call.raw)
     _sv._check(code, "spec_head_forward")
     return y, pre, ws
@@ -332,8 +346,8 @@ def spec_head_backward(dy, x, weight, pre=None, *, act: int = SPEC_ACT_NONE, wan
             db = torch.empty(N, dtype=torch.float32, device=x.device) if want_db else None
         code = _sv.lib().spec_head_backward(
             _arg("dy", dy, bf, M * N, dev), _arg("x", x, bf, 0, dev),
-            _arg("weight", weight, bf, 0, dev), _arg("pre", pre, bf, M * N, dev), M, N, K, act,
-            _arg("dx", dx, bf, M * K, dev), _arg("dw", dw, bf, N * K, dev),
+            _arg("weight", weight, bf, 0, dev), _matrix("pre", pre, bf, M, N, dev), M, N, K, act,
+            _matrix("dx", dx, bf, M, K, dev), _matrix("dw", dw, bf, N, K, dev),
             _arg("db", db, torch.float32, N, dev), ws_at, ws_bytes, call.raw)
     _sv._check(code, "spec_head_backward")
     return dx, dw, db, ws

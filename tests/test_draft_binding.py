@@ -1,0 +1,51 @@
+"""CPU tests of the checks that the binding of the draft operators makes before a
+call: the shapes of matrices."""
+import pytest
+import torch
+
+from speculative_decoding_rejection_gb300 import draft as D
+
+HOST = -1   # Tensor.get_device() of a host tensor
+BF16 = torch.bfloat16
+
+
+@pytest.mark.parametrize("shape", [(6, 8), (9, 8), (48,), (60,), (2, 3, 8), (6, 2, 4), (1, 6, 8), (6, 1, 8)])
+def test_matrices_of_the_right_rows_pass(shape):
+    """Rows of 8, at least 6 of them, however they are viewed; flat buffers too."""
+    t = torch.zeros(shape, dtype=BF16)
+    assert D._matrix("residual", t, BF16, 6, 8, HOST) == t.data_ptr()
+
+
+@pytest.mark.parametrize("shape", [(8, 6), (4, 12), (2, 24), (16, 4, 5), (5, 8), (47,)])
+def test_matrices_of_other_rows_are_refused(shape):
+    with pytest.raises(ValueError):
+        D._matrix("residual", torch.zeros(shape, dtype=BF16), BF16, 6, 8, HOST)
+
+
+def test_no_matrix_and_other_types():
+    assert D._matrix("residual", None, BF16, 6, 8, HOST) is None
+    with pytest.raises(TypeError):
+        D._matrix("residual", torch.zeros(6, 8), BF16, 6, 8, HOST)
+
+
+@pytest.mark.gpu
+def test_calls_refuse_transposed_matrices():
+    import speculative_decoding_rejection_gb300 as sv
+
+    def z(*shape, dtype=BF16):
+        return torch.zeros(shape, dtype=dtype, device="cuda:0")
+
+    M, N, K = 6, 8, 16
+    x, w, y = z(M, K), z(N, K), z(M, N)
+    for kw in (dict(residual=z(N, M)), dict(out=(z(N, M), None)), dict(out=(y, z(N, M)))):
+        with pytest.raises(ValueError):
+            sv.spec_head_forward(x, w, **kw)
+    ok = (z(M, K), z(N, K), z(N, dtype=torch.float32))
+    for kw in (dict(pre=z(N, M)), dict(out=(z(K, M), *ok[1:])), dict(out=(ok[0], z(K, N), ok[2]))):
+        with pytest.raises(ValueError):
+            sv.spec_head_backward(y, x, w, **{"pre": y, **kw}, act=sv.SPEC_ACT_SILU)
+    cu = torch.tensor([0, M], dtype=torch.int32, device="cuda:0")
+    with pytest.raises(ValueError):
+        sv.spec_process_logits(y, cu, max_rows=M, out=z(N, M))
+    with pytest.raises(ValueError):
+        sv.spec_distill_loss(z(M + 1, N), y, cu, out=(z(M, dtype=torch.float32), z(N, M)))
