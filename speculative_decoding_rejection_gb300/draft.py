@@ -14,6 +14,7 @@ import speculative_decoding_rejection_gb300 as _sv
 
 # the current stream's handle without a Stream object (less host time per call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 SPEC_ADAMW_BLOCK = 256
 SPEC_ACT_NONE, SPEC_ACT_SILU, SPEC_ACT_GELU = 0, 1, 2
@@ -120,19 +121,24 @@ def _device(name, t):
 
 
 class _Call:
-    """The stream of a call, as a context in which its buffers are allocated.
-    Where that is not torch's current stream, the tensors the caller made
-    elsewhere are marked as in use there, so that their memory is not handed
-    out before the call's work is done."""
+    """The stream of a call, as a context in which its buffers are allocated and
+    its device is the current one (the default stream's handle is the same on
+    every device). Where the stream is not torch's current stream, the tensors
+    the caller made elsewhere are marked as in use there, so that their memory
+    is not handed out before the call's work is done."""
 
     __slots__ = ("raw", "ctx")
 
     def __init__(self, dev, stream, tensors):
         self.ctx = None
         if stream is None:
+            if _current_device() != dev:
+                self.ctx = torch.cuda.device(dev)
             self.raw = torch.cuda.current_stream(dev).cuda_stream if _raw_stream is None \
                 else _raw_stream(dev)
             return
+        if stream.device.index != dev:
+            raise ValueError(f"the stream is on {stream.device}, the call runs on cuda:{dev}")
         self.raw = stream.cuda_stream
         if stream != torch.cuda.current_stream(dev):
             for t in tensors:

@@ -49,3 +49,37 @@ def test_calls_refuse_transposed_matrices():
         sv.spec_process_logits(y, cu, max_rows=M, out=z(N, M))
     with pytest.raises(ValueError):
         sv.spec_distill_loss(z(M + 1, N), y, cu, out=(z(M, dtype=torch.float32), z(N, M)))
+
+
+class FakeDevice:
+    entered = []
+
+    def __init__(self, index):
+        self.index = index
+
+    def __enter__(self):
+        self.entered.append(self.index)
+
+    def __exit__(self, *_):
+        self.entered.append(None)
+
+
+@pytest.mark.parametrize("current,entered", [(0, [1, None]), (1, [])])
+def test_a_call_runs_on_the_device_of_its_tensors(monkeypatch, current, entered):
+    monkeypatch.setattr(FakeDevice, "entered", [])
+    monkeypatch.setattr(torch.cuda, "device", FakeDevice)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current)
+    monkeypatch.setattr(D, "_current_device", lambda: current, raising=False)
+    monkeypatch.setattr(D, "_raw_stream", lambda dev: 100 + dev)
+    with D._Call(1, None, ()) as call:
+        assert call.raw == 101 and FakeDevice.entered == entered[:1]
+    assert FakeDevice.entered == entered
+
+
+def test_a_stream_of_another_device_is_refused():
+    class FakeStream:
+        device = torch.device("cuda", 0)
+        cuda_stream = 5
+
+    with pytest.raises(ValueError):
+        D._Call(1, FakeStream(), ())
