@@ -39,6 +39,7 @@
 // overlap of positions); persistent CTAs whose second-pass units follow the
 // first-pass units of later rows 1.04 to 1.8 ms, as L2 does not hold the rows
 // between the two.
+#include "cluster_choice.h"
 #include "draft.cuh"
 
 #include <cooperative_groups.h>
@@ -735,46 +736,60 @@ bool resident_fits(long long vecs, int C) {
   return ((vecs + C - 1) / C + DR_PV - 1) / DR_PV + DR_AHEAD <= DR_SLOTS;
 }
 
+// A cluster's CTAs share one GPC, so cluster sizes leave different numbers of SMs
+// idle: the size that runs on the most SMs, of those that hold a row. On a device or
+// in a context that runs none of them the call goes by a cluster per position.
+constexpr int DR_SMEM = DR_SLOTS * 2 * DR_PIECE;
 template <bool BF16>
-int launch_resident(ResidentArgs a, cudaStream_t st) {
-  k_distill_setup<<<(std::max(a.d.R, std::min(a.d.B, 1 << 16)) + 255) / 256, 256, 0, st>>>(a);
-  if (launched() != SPEC_OK) return SPEC_ERR_CUDA;
-  const auto kern = k_distill_resident<BF16>;
-  const int smem = DR_SLOTS * 2 * DR_PIECE;
+struct Resident {
   static SmemLimit limit;
-  if (allow_smem(limit, (const void *)kern, smem) != SPEC_OK) return SPEC_ERR_CUDA;   // the occupancy query needs it
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 1;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  cfg.blockDim = dim3(DR_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  // A cluster's CTAs share one GPC, so cluster sizes leave different numbers of
-  // SMs idle: the size that runs on the most SMs, of those that hold a row
-  // (asked once per size and device).
-  static int cached[64][DR_MAX_CLUSTER + 1] = {};
-  int dev = 0, best = 0, clusters = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ERR_CUDA;
-  for (int C = 1; C <= DR_MAX_CLUSTER; ++C) {
-    if (!resident_fits((long long)a.d.V / (BF16 ? 8 : 4), C)) continue;
-    if (cached[dev][C] == 0) {
-      cfg.gridDim = dim3((unsigned)(num_sms() / C * C), 1, 1);
-      at[0].val.clusterDim.x = C;
-      int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) return SPEC_ERR_CUDA;
-      cached[dev][C] = n;
-    }
-    if (cached[dev][C] * C > clusters * best) best = C, clusters = cached[dev][C];
+  static cudaLaunchConfig_t config(cudaLaunchAttribute *at, int C, int clusters, cudaStream_t st) {
+    cudaLaunchConfig_t cfg{};
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = C;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3((unsigned)(clusters * C), 1, 1);
+    cfg.blockDim = dim3(DR_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = DR_SMEM;
+    cfg.stream = st;
+    return cfg;
   }
-  at[0].val.clusterDim.x = best;
-  cfg.gridDim = dim3((unsigned)(std::min(clusters, a.d.R) * best), 1, 1);
-  return launch_retry(limit, (const void *)kern, smem, [&]() { return cudaLaunchKernelEx(&cfg, kern, a); });
-}
+  static ClusterChoice choose(int V) {
+    static std::atomic<int> counts[64][DR_MAX_CLUSTER + 1] = {};
+    const auto kern = k_distill_resident<BF16>;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 ||
+        allow_smem(limit, (const void *)kern, DR_SMEM) != SPEC_OK) {   // the query below needs it
+      cudaGetLastError();
+      return ClusterChoice{0, 0};
+    }
+    return choose_cluster(
+        counts[dev], DR_MAX_CLUSTER, [&](int C) { return resident_fits((long long)V / (BF16 ? 8 : 4), C); },
+        [&](int C) {
+          cudaLaunchAttribute at[1];
+          const cudaLaunchConfig_t cfg = config(at, C, num_sms() / C, nullptr);
+          int n = 0;
+          if (num_sms() < C || cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+          }
+          return n;
+        });
+  }
+  static int launch(ResidentArgs a, ClusterChoice c, cudaStream_t st) {
+    k_distill_setup<<<(std::max(a.d.R, std::min(a.d.B, 1 << 16)) + 255) / 256, 256, 0, st>>>(a);
+    if (launched() != SPEC_OK) return SPEC_ERR_CUDA;
+    const auto kern = k_distill_resident<BF16>;
+    cudaLaunchAttribute at[1];
+    const cudaLaunchConfig_t cfg = config(at, c.size, std::min(c.count, a.d.R), st);
+    return launch_retry(limit, (const void *)kern, DR_SMEM, [&]() { return cudaLaunchKernelEx(&cfg, kern, a); });
+  }
+};
+template <bool BF16>
+SmemLimit Resident<BF16>::limit;
 
 // The status header's reset as a kernel, which k_distill's launch overlaps: 64
 // requests of 32003 bf16 logits 18.4 us, after a memset 19.3 us. (A kernel takes
@@ -860,13 +875,16 @@ extern "C" int spec_distill_loss(const void *target, const void *draft, int dt, 
   if (check_upload(st) != SPEC_OK) return SPEC_ERR_CUDA;
   if (num_sms() <= 0) return SPEC_ERR_CUDA;
   const bool vec = (V * es) % 16 == 0;
-  if (vec && 2ll * R_d * V * es >= DR_MIN_BYTES && resident_fits(V * es / 16, DR_MAX_CLUSTER)) {
+  ClusterChoice c{0, 0};
+  if (vec && 2ll * R_d * V * es >= DR_MIN_BYTES)
+    c = dt == SPEC_BF16 ? Resident<true>::choose(V) : Resident<false>::choose(V);
+  if (c.size != 0) {
     ResidentArgs s{};
     s.d = a;
     s.info = reinterpret_cast<RowInfo *>(static_cast<char *>(workspace) + lay.info);
     s.zero = reinterpret_cast<int *>(static_cast<char *>(workspace) + lay.zero);
     if (reset_header(workspace, st) != SPEC_OK) return SPEC_ERR_CUDA;
-    return dt == SPEC_BF16 ? launch_resident<true>(s, st) : launch_resident<false>(s, st);
+    return dt == SPEC_BF16 ? Resident<true>::launch(s, c, st) : Resident<false>::launch(s, c, st);
   }
   // each position over as many SMs as there are, down to slices of 4 KB
   const long long pair = 2ll * V * es;

@@ -3,6 +3,8 @@
 
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 #include "specdraft.h"
@@ -88,16 +90,16 @@ inline cudaLaunchAttribute launch_early() {
 // device (in `most`, one array per kernel); a device that was reset has
 // forgotten it, which the launch reports (launch_retry).
 struct SmemLimit {
-  int most[64] = {};
+  std::atomic<int> most[64] = {};   // shared by the callers' threads
 };
 inline int allow_smem(SmemLimit &l, const void *kern, int smem) {
   int dev = 0;
   if (smem <= 48 * 1024) return SPEC_OK;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPEC_ERR_CUDA;
-  if (l.most[dev] >= smem) return SPEC_OK;
+  if (l.most[dev].load(std::memory_order_relaxed) >= smem) return SPEC_OK;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return SPEC_ERR_CUDA;
-  l.most[dev] = smem;
+  l.most[dev].store(smem, std::memory_order_relaxed);
   return SPEC_OK;
 }
 // Launches through `go` (a callable that returns a cudaError_t); on a failure once
@@ -107,7 +109,7 @@ int launch_retry(SmemLimit &l, const void *kern, int smem, Go go) {
   if (allow_smem(l, kern, smem) != SPEC_OK) return SPEC_ERR_CUDA;
   if (go() == cudaSuccess) return SPEC_OK;
   cudaGetLastError();
-  l = SmemLimit{};
+  for (std::atomic<int> &m : l.most) m.store(0, std::memory_order_relaxed);
   if (allow_smem(l, kern, smem) != SPEC_OK) return SPEC_ERR_CUDA;
   return go() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
