@@ -11,11 +11,13 @@
 //   f (A + S_t ((M_d - m_d) - (M_t - m_t))), f = 2^((m_t - M_t) c):
 // S_t is scaled by f before the product, so that tokens of a mask value (-1e9,
 // the type's lowest), which are all that a thread has seen at first, leave nothing
-// behind. A thread whose A is infinite or large at its share's end sums it anew,
-// token by token (add_rare): what a draft's mask value adds under a target's weight can
-// exceed f32 and is kept in units of FAR, and a token that the draft holds at -inf
-// makes the loss infinite by the largest z_t of such tokens, at the row's end, so
-// that neither the order of the tokens nor the schedule decides it.
+// behind. A warp whose A is infinite or large at its share's end sums it anew at
+// its maxima, token by token (add_rare): what a draft's mask value adds under a
+// target's weight can exceed f32 and is kept in units of FAR, and a token that the
+// draft holds at -inf makes the loss infinite by the largest z_t of such tokens, at
+// the row's end, so that neither the order of the tokens nor the schedule decides
+// it. (4096 positions as below: 0.81 ms; with the parts in every thread's statistics
+// 0.82 ms.)
 //
 // Resident schedule (k_distill_setup, k_distill_resident), for calls that fill
 // the SMs: a persistent cluster takes one position after another, each CTA a
@@ -34,7 +36,7 @@
 // grid is put together from two vectors by shifts (64 requests of 32003 bf16
 // logits: 18.4 us, element by element about 4 us more).
 //
-// Measured at 4096 positions of 201088 bf16 logits, 3/4 of them weighted: 0.82 ms
+// Measured at 4096 positions of 201088 bf16 logits, 3/4 of them weighted: 0.81 ms
 // (5.1 TB/s of the bytes that have to move); a cluster per position 1.06 ms (1.18 ms with its slices in shared memory but no
 // overlap of positions); persistent CTAs whose second-pass units follow the
 // first-pass units of later rows 1.04 to 1.8 ms, as L2 does not hold the rows
@@ -79,13 +81,19 @@ struct DistillArgs {
   WsHeader *hdr;
 };
 
-// Statistics of part of a row pair. far: what of A comes from differences beyond
-// NEAR, in units of FAR. hole: the largest z_t of the tokens that are -inf in the
-// draft alone.
-struct __align__(16) PairStat {
-  float mt, St, A, md, Sd, far, hole;
+// Statistics of part of a row pair.
+struct PairStat {
+  float mt, St, A, md, Sd;
 };
-__device__ __forceinline__ PairStat no_stat() { return PairStat{NO_MAX, 0.f, 0.f, NO_MAX, 0.f, 0.f, -INFINITY}; }
+__device__ __forceinline__ PairStat no_stat() { return PairStat{NO_MAX, 0.f, 0.f, NO_MAX, 0.f}; }
+// Those of a warp or more: A is below FAR, or it is NaN and in parts: near and far (in
+// units of FAR) are what tokens of differences below and beyond NEAR make of it, hole
+// the largest z_t of the tokens that are -inf in the draft alone.
+struct __align__(16) WarpStat {
+  PairStat s;
+  float near, far, hole;
+};
+__device__ __forceinline__ WarpStat no_warp_stat() { return WarpStat{no_stat(), 0.f, 0.f, -INFINITY}; }
 constexpr float FAR = 18446744073709551616.f;   // 2^64
 constexpr float NEAR = 281474976710656.f;       // 2^48
 
@@ -213,9 +221,9 @@ __device__ __forceinline__ void add_stats(PairStat &s, const f32x2 *zt, const f3
   add_pairs<N>(s, xt, xd, c);
 }
 
-// A anew, where it is not below FAR, from the share's elements at its maxima. Called
-// by the element, as inlined it takes the registers of the loops before it.
-__device__ __noinline__ float3 add_rare(float3 r, float xt, float xd, float mt, float c) {   // (A, far, hole)
+// What an element adds to a sum in parts, (near, far, hole). Called by the element, as
+// inlined it takes the registers of the loops before it.
+__device__ __noinline__ float3 add_rare(float3 r, float xt, float xd, float mt, float c) {
   const float e = ex2(xt * c);
   if (xd == -INFINITY) {
     if (xt > -INFINITY) r.z = fmaxf(r.z, xt + mt);
@@ -226,23 +234,17 @@ __device__ __noinline__ float3 add_rare(float3 r, float xt, float xd, float mt, 
   }
   return r;
 }
-template <int N>
-__device__ __forceinline__ void add_rare(PairStat &s, const f32x2 *xt, const f32x2 *xd, float c) {
-  float3 r = make_float3(s.A, s.far, s.hole);
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    r = add_rare(r, lo2(xt[j]), lo2(xd[j]), s.mt, c);
-    r = add_rare(r, hi2(xt[j]), hi2(xd[j]), s.mt, c);
-  }
-  s.A = r.x, s.far = r.y, s.hole = r.z;
-}
 template <bool BF16>
-__device__ __forceinline__ void add_rare16(PairStat &s, const uint4 &wt, const uint4 &wd, float c) {
+__device__ __forceinline__ void add_rare16(float3 &r, const uint4 &wt, const uint4 &wd, float mt, float md, float c) {
   constexpr int N = BF16 ? 4 : 2;
   f32x2 xt[N], xd[N];
-  minus16<BF16>(wt, s.mt, xt);
-  minus16<BF16>(wd, s.md, xd);
-  add_rare<N>(s, xt, xd, c);
+  minus16<BF16>(wt, mt, xt);
+  minus16<BF16>(wd, md, xd);
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    r = add_rare(r, lo2(xt[j]), lo2(xd[j]), mt, c);
+    r = add_rare(r, hi2(xt[j]), hi2(xd[j]), mt, c);
+  }
 }
 
 // The gradient's scalars: g = kd 2^((z_d - m_d) c) - kt 2^((z_t - m_t) c), kd = w / (T S_d)
@@ -262,50 +264,64 @@ __device__ __forceinline__ void gradient(const GradK &g, const f32x2 *xt, const 
     out[j] = fma2(ex2_2(mul2(xt[j], g.c)), g.kt, mul2(ex2_2(mul2(xd[j], g.c)), g.kd));
 }
 
-// The warp's statistics in every lane: sums at the warp's maxima, added in a
-// butterfly.
-__device__ __forceinline__ void warp_merge(PairStat &s, float c) {
-  float M = s.mt, D = s.md;
+// The lanes' statistics merged, in every lane: sums at the warp's maxima, added in a
+// butterfly. A is what comes of it, finite or not.
+__device__ __forceinline__ PairStat sum_stats(const PairStat &p, float c) {
+  PairStat s = p;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
-    D = fmaxf(D, __shfl_xor_sync(~0u, D, o));
+    s.mt = fmaxf(s.mt, __shfl_xor_sync(~0u, s.mt, o));
+    s.md = fmaxf(s.md, __shfl_xor_sync(~0u, s.md, o));
   }
-  const float f = ex2((s.mt - M) * c), move = (D - s.md) - (M - s.mt);
+  const float f = ex2((p.mt - s.mt) * c);
   s.St *= f;
-  s.A *= f;
-  s.Sd *= ex2((s.md - D) * c);
-  float a = s.St * move;
-  if (__any_sync(~0u, !(fabsf(a) < FAR) || s.far != 0.f || s.hole > -INFINITY)) {
-    s.far *= f;
-    if (!(fabsf(a) < FAR)) {   // nothing, where St is 0 and `move` not finite
-      if (s.St > 0.f) s.far += s.St * (fminf(fmaxf(move, -FLT_MAX), FLT_MAX) * (1.f / FAR));
-      a = 0.f;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      s.far += __shfl_xor_sync(~0u, s.far, o);
-      s.hole = fmaxf(s.hole, __shfl_xor_sync(~0u, s.hole, o));
-    }
-  }
-  s.A += a;
+  s.A = fmaf(s.A, f, s.St * ((s.md - p.md) - (s.mt - p.mt)));
+  s.Sd *= ex2((p.md - s.md) * c);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     s.St += __shfl_xor_sync(~0u, s.St, o);
     s.A += __shfl_xor_sync(~0u, s.A, o);
     s.Sd += __shfl_xor_sync(~0u, s.Sd, o);
   }
-  s.mt = M;
-  s.md = D;
+  return s;
+}
+__device__ __forceinline__ bool in_parts(const PairStat &s) { return !(fabsf(s.A) < FAR); }
+// A of the lanes together, from its parts.
+__device__ __forceinline__ WarpStat sum_parts(PairStat s, float near, float far, float hole) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    near += __shfl_xor_sync(~0u, near, o);
+    far += __shfl_xor_sync(~0u, far, o);
+    hole = fmaxf(hole, __shfl_xor_sync(~0u, hole, o));
+  }
+  s.A = NAN;
+  return WarpStat{s, near, far, hole};
+}
+// Statistics of warps or CTAs, a lane each, merged in every lane.
+__device__ __forceinline__ WarpStat warp_merge(const WarpStat &w, float c) {
+  const PairStat &p = w.s, s = sum_stats(p, c);
+  if (!in_parts(s)) return WarpStat{s, 0.f, 0.f, -INFINITY};   // the same in every lane
+  const bool parts = in_parts(p);
+  const float f = ex2((p.mt - s.mt) * c), St = f * p.St, move = (s.md - p.md) - (s.mt - p.mt);
+  float near = f * (parts ? w.near : p.A), far = f * (parts ? w.far : 0.f);
+  if (St > 0.f) {
+    if (fabsf(St * move) < FAR) near += St * move;
+    else far += St * (fminf(fmaxf(move, -FLT_MAX), FLT_MAX) * (1.f / FAR));
+  }
+  return sum_parts(s, near, far, parts ? w.hole : -INFINITY);
 }
 
-__device__ __forceinline__ float loss_of(const PairStat &s, float c, float w) {
-  // a probability under a draft's 0 counts unless it is 0 itself in 64 bits,
-  // whose smallest value is 2^-1074
-  if (((double)s.hole - (double)s.mt) * c > -1075.0) return w * INFINITY;
+__device__ __forceinline__ float loss_of(const WarpStat &x, float c, float w) {
+  const PairStat &s = x.s;
+  double A = s.A;
+  if (in_parts(s)) {
+    // a probability under a draft's 0 counts unless it is 0 itself in 64 bits,
+    // whose smallest value is 2^-1074
+    if (((double)x.hole - (double)s.mt) * c > -1075.0) return w * INFINITY;
+    A = (double)x.near + (double)x.far * FAR;
+  }
   // in 64 bits: the terms are larger than their sum
-  const double kl = 0.693147180559945309 * (((double)s.A + (double)s.far * FAR) / (double)s.St * c -
-                                            (double)log2f(s.St) + (double)log2f(s.Sd));
+  const double kl = 0.693147180559945309 * (A / (double)s.St * c - (double)log2f(s.St) + (double)log2f(s.Sd));
   return (float)((double)w * kl);
 }
 
@@ -339,8 +355,8 @@ __global__ void __launch_bounds__(DI_THREADS) k_distill(DistillArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   __shared__ int s_slot;
-  __shared__ PairStat s_part[DI_THREADS / 32];
-  __shared__ PairStat s_cta;     // this CTA's statistics, read by its peers
+  __shared__ WarpStat s_part[DI_THREADS / 32];
+  __shared__ WarpStat s_cta;     // this CTA's statistics, read by its peers
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int r = blockIdx.x / C;
   constexpr int ES = BF16 ? 2 : 4, PER = 16 / ES, N = PER / 2;
@@ -411,33 +427,30 @@ __global__ void __launch_bounds__(DI_THREADS) k_distill(DistillArgs a) {
     const f32x2 zt = pk2(load1<BF16>(trow, single), -INFINITY), zd = pk2(load1<BF16>(drow, single), -INFINITY);
     add_stats<1>(s, &zt, &zd, c);
   }
-  if (!(fabsf(s.A) < FAR)) {
-    s.A = 0.f;
-    for (int i = v0 + t; i < v1; i += DI_THREADS) add_rare16<BF16>(s, target16(i), GLD(dvec + i), c);
-    if (single >= 0) {
-      const f32x2 xt = pk2(load1<BF16>(trow, single) - s.mt, -INFINITY);
-      const f32x2 xd = pk2(load1<BF16>(drow, single) - s.md, -INFINITY);
-      add_rare<1>(s, &xt, &xd, c);
-    }
+  s = sum_stats(s, c);
+  WarpStat x{s, 0.f, 0.f, -INFINITY};
+  if (in_parts(s)) {
+    float3 r = make_float3(0.f, 0.f, -INFINITY);
+    for (int i = v0 + t; i < v1; i += DI_THREADS) add_rare16<BF16>(r, target16(i), GLD(dvec + i), s.mt, s.md, c);
+    if (single >= 0) r = add_rare(r, load1<BF16>(trow, single) - s.mt, load1<BF16>(drow, single) - s.md, s.mt, c);
+    x = sum_parts(s, r.x, r.y, r.z);
   }
-  warp_merge(s, c);
-  if (lane == 0) s_part[warp] = s;
+  if (lane == 0) s_part[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    s = lane < DI_THREADS / 32 ? s_part[lane] : no_stat();
-    warp_merge(s, c);
-    if (lane == 0) s_cta = s;
+    x = warp_merge(lane < DI_THREADS / 32 ? s_part[lane] : no_warp_stat(), c);
+    if (lane == 0) s_cta = x;
   }
   cluster.sync();
   // every warp merges the CTAs' statistics, a lane each, in the same order:
   // the same bits everywhere
-  s = lane < C ? *cluster.map_shared_rank(&s_cta, lane) : no_stat();
-  warp_merge(s, c);
+  x = warp_merge(lane < C ? *cluster.map_shared_rank(&s_cta, lane) : no_warp_stat(), c);
+  s = x.s;
 
   const bool empty = row_empty(s.mt) || row_empty(s.md);
   if (rank == 0 && t == 0) {
     if (empty) set_status(a.hdr, SPEC_ERR_INVALID_ARG, r);
-    GST(a.loss + r, empty ? 0.f : loss_of(s, c, w));
+    GST(a.loss + r, empty ? 0.f : loss_of(x, c, w));
   }
   if (grow != nullptr) {
     const GradK g = grad_of(s, c, w / T);
@@ -509,6 +522,19 @@ __device__ __forceinline__ uint32_t peer_addr(const void *local, int rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(local)), "r"(rank));
   return r;
 }
+// A consumer thread's share of a slice, whose first piece is the ring's `it`-th, in
+// parts. Called, for the same reason.
+template <bool BF16>
+__device__ __noinline__ float3 rare_slice(const uint8_t *ring, int it, int len, int ct, float mt, float md, float c) {
+  float3 r = make_float3(0.f, 0.f, -INFINITY);
+  for (int left = len; left > 0; left -= DR_PV, ++it) {
+    const uint8_t *at = ring + it % DR_SLOTS * 2 * DR_PIECE;
+    for (int v = ct; v < min(DR_PV, left); v += 32 * DR_WARPS)
+      add_rare16<BF16>(r, lds128(at + v * 16), lds128(at + DR_PIECE + v * 16), mt, md, c);
+  }
+  return r;
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_resident(ResidentArgs a) {
   constexpr int PER = BF16 ? 8 : 4, N = PER / 2;
@@ -518,8 +544,8 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_resident(ResidentArgs
   extern __shared__ __align__(128) uint8_t ring[];   // DR_SLOTS x (target piece, draft piece)
   __shared__ uint64_t s_full[DR_SLOTS], s_empty[DR_SLOTS];
   __shared__ uint64_t s_parts[2], s_xch[2], s_known[2];   // by the parity of the row
-  __shared__ PairStat s_part[2][DR_WARPS];      // the warps' statistics
-  __shared__ PairStat s_stat[2][DR_MAX_CLUSTER];   // the CTAs', written by the peers
+  __shared__ WarpStat s_part[2][DR_WARPS];      // the warps' statistics
+  __shared__ WarpStat s_stat[2][DR_MAX_CLUSTER];   // the CTAs', written by the peers
   __shared__ GradK s_grad[2];                   // the row's law, by the merging warp
   __shared__ int s_none[2];                     // the row holds no finite logit
   __shared__ RowInfo s_row[16];                 // the rows in the ring, DR_SLOTS at most
@@ -578,15 +604,15 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_resident(ResidentArgs
       bool ok = __all_sync(~0u, wait_phase<false>(&s_parts[y], par, &s_abort));
       const RowInfo x = s_row[k & 15];
       if (ok) {
-        PairStat s = lane < DR_WARPS ? s_part[y][lane] : no_stat();
-        warp_merge(s, x.c);
+        const WarpStat w = warp_merge(lane < DR_WARPS ? s_part[y][lane] : no_warp_stat(), x.c);
+        const PairStat &s = w.s;
         if (lane < C) {
           const uint32_t to = peer_addr(&s_stat[y][rank], lane);
           asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(s.mt), "f"(s.St),
                        "f"(s.A), "f"(s.md)
                        : "memory");
-          asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %3};" ::"r"(to + 16), "f"(s.Sd), "f"(s.far),
-                       "f"(s.hole)
+          asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to + 16), "f"(s.Sd), "f"(w.near),
+                       "f"(w.far), "f"(w.hole)
                        : "memory");
           asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
                            peer_addr(&s_xch[y], lane))
@@ -599,12 +625,12 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_resident(ResidentArgs
         if (lane == 0) set_status(d.hdr, SPEC_ERR_TIMEOUT, 2);
         break;
       }
-      PairStat z = lane < C ? s_stat[y][lane] : no_stat();
-      warp_merge(z, x.c);   // the same bits in every CTA of the cluster
+      // the same bits in every CTA of the cluster
+      const WarpStat z = warp_merge(lane < C ? s_stat[y][lane] : no_warp_stat(), x.c);
       if (lane == 0) {
-        const bool none = row_empty(z.mt) || row_empty(z.md);
+        const bool none = row_empty(z.s.mt) || row_empty(z.s.md);
         s_none[y] = none;
-        s_grad[y] = grad_of(z, x.c, x.k);
+        s_grad[y] = grad_of(z.s, x.c, x.k);
         mbar_arrive(&s_known[y]);
         if (rank == 0) {
           if (none) set_status(d.hdr, SPEC_ERR_INVALID_ARG, x.r);
@@ -648,17 +674,13 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_resident(ResidentArgs
         }
       }
       if (p1 < P || !ok) return;
-      if (!(fabsf(s.A) < FAR)) {   // the row's pieces stay until its second pass
-        s.A = 0.f;
-        for (int p = 0; p < P; ++p) {
-          const uint8_t *at = ring + (k * P + p) % DR_SLOTS * 2 * DR_PIECE;
-          for (int v = ct; v < min(DR_PV, u1 - u0 - p * DR_PV); v += 32 * DR_WARPS)
-            add_rare16<BF16>(s, lds128(at + v * 16), lds128(at + DR_PIECE + v * 16), c);
-        }
+      WarpStat w{sum_stats(s, c), 0.f, 0.f, -INFINITY};
+      if (in_parts(w.s)) {   // the row's pieces stay until its second pass
+        const float3 r = rare_slice<BF16>(ring, k * P, u1 - u0, ct, w.s.mt, w.s.md, c);
+        w = sum_parts(w.s, r.x, r.y, r.z);
       }
-      warp_merge(s, c);
       if (lane == 0) {
-        s_part[k & 1][cw] = s;
+        s_part[k & 1][cw] = w;
         mbar_arrive(&s_parts[k & 1]);
       }
       s = no_stat();
