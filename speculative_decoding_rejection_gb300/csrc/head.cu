@@ -762,18 +762,21 @@ __global__ void __launch_bounds__(256) k_pad_rows(Pad p0, Pad p1, int C, int ld)
 
 // dz = dy act'(pre), rounded once to bf16 (the products' operand; rows of ld
 // elements, zeros behind N), and the column sums of the unrounded dz over
-// HD_DZ_ROWS rows. A CTA takes 256 columns, 8 threads for every 8 of them.
+// HD_DZ_ROWS rows. A CTA takes 256 columns, 8 threads for every 8 of them; the CTAs
+// of the same rows follow one another in the grid's only dimension (the others end at
+// 65535).
 constexpr int HD_DZ_ROWS = 64;
 // ALIGNED: N is a multiple of 8.
 template <bool ALIGNED>
 __global__ void __launch_bounds__(256)
     k_dz(const uint16_t *dy, const uint16_t *pre, uint16_t *dz, float *psum, int M, int N, int ld, int act,
          WsHeader *hdr) {
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) hdr->status = SPEC_OK, hdr->detail = -1;
+  if (blockIdx.x == 0 && threadIdx.x == 0) hdr->status = SPEC_OK, hdr->detail = -1;
   __shared__ float sums[8][32 * 8 + 1];
+  const int per_row = (ld + 255) / 256, seg = blockIdx.x / per_row, bx = blockIdx.x - seg * per_row;
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
-  const int c0 = (blockIdx.x * 32 + cx) * 8;
-  const int r0 = blockIdx.y * HD_DZ_ROWS, r1 = min(M, r0 + HD_DZ_ROWS);
+  const int c0 = (bx * 32 + cx) * 8;
+  const int r0 = seg * HD_DZ_ROWS, r1 = min(M, r0 + HD_DZ_ROWS);
   float acc[8] = {};
   auto row = [&](int r, const uint4 &gw, const uint4 &zw) {
     float g[8], z[8];
@@ -839,11 +842,11 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int j = 0; j < 8; ++j) sums[ry][cx * 8 + j] = acc[j];
   __syncthreads();
-  const int col = blockIdx.x * 256 + threadIdx.x;
+  const int col = bx * 256 + threadIdx.x;
   float s = 0.f;
 #pragma unroll
   for (int k = 0; k < 8; ++k) s += sums[k][threadIdx.x];
-  if (col < N) psum[(long long)blockIdx.y * N + col] = s;
+  if (col < N) psum[(long long)seg * N + col] = s;
 }
 
 __global__ void k_db(const float *psum, float *db, int N, int segs) {
@@ -1159,11 +1162,11 @@ extern "C" int spec_head_backward(const void *dy, const void *x, const void *wei
   if (own_dz || db != nullptr) {
     const uint16_t *g = static_cast<const uint16_t *>(dy);
     const uint16_t *z = act != SPEC_ACT_NONE ? static_cast<const uint16_t *>(pre) : nullptr;
-    const dim3 grid((unsigned)((ldz + 255) / 256), (unsigned)dz_segments(M));
-    if (grid.y > 65535) return SPEC_ERR_UNSUPPORTED;
-    float *sums = db == nullptr ? nullptr : grid.y == 1 ? db : psum;   // one segment: the sums themselves
-    if (N % 8 == 0) k_dz<true><<<grid, 256, 0, st>>>(g, z, own_dz ? dz : nullptr, sums, M, N, ldz, act, a.hdr);
-    else k_dz<false><<<grid, 256, 0, st>>>(g, z, own_dz ? dz : nullptr, sums, M, N, ldz, act, a.hdr);
+    const long long grid = (long long)((ldz + 255) / 256) * dz_segments(M);
+    if (grid > 0x7fffffffll) return SPEC_ERR_UNSUPPORTED;
+    float *sums = db == nullptr ? nullptr : dz_segments(M) == 1 ? db : psum;   // one segment: the sums themselves
+    if (N % 8 == 0) k_dz<true><<<(unsigned)grid, 256, 0, st>>>(g, z, own_dz ? dz : nullptr, sums, M, N, ldz, act, a.hdr);
+    else k_dz<false><<<(unsigned)grid, 256, 0, st>>>(g, z, own_dz ? dz : nullptr, sums, M, N, ldz, act, a.hdr);
     if ((rc = launched()) != SPEC_OK) return rc;
     if (sums == psum && db != nullptr) {
       k_db<<<(N + 255) / 256, 256, 0, st>>>(psum, db, N, dz_segments(M));
