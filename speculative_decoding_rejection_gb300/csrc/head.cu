@@ -202,8 +202,10 @@ __device__ __forceinline__ float act_slope(float z, int act) {
     return s * (1.f + z * (1.f - s));
   }
   if (act == SPEC_ACT_GELU) {
+    // s is 0 or 1 long before z^2 is 1e10, which bounds the factor behind it: 0 times
+    // its infinity would be NaN
     const float s = gelu_gate(z);
-    return s * (1.f + z * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * z * z));
+    return s + s * z * ((1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * fminf(z * z, 1e10f)));
   }
   return 1.f;
 }
