@@ -218,10 +218,12 @@ typedef struct {
 
 /*
  * A table of tensors, built once on the host and copied to the device by the
- * caller. spec_adamw_table_bytes: its size (0 on invalid arguments).
- * spec_adamw_table fills `table` (host memory, at least that many bytes) and
- * writes the number of work items, which spec_adamw_step needs, to
- * *n_items. state_bits is 32 or 8, for all tensors. n_tensors >= 0. Returns
+ * caller; it holds their addresses, so that a tensor that is replaced (a gradient
+ * that is dropped and made anew for each step) needs a new table.
+ * spec_adamw_table_bytes: its size (0 on invalid arguments). spec_adamw_table
+ * fills `table` (host memory, at least that many bytes) and writes the number of
+ * work items, which spec_adamw_step needs, to *n_items. state_bits is 32 or 8,
+ * for all tensors. n_tensors >= 0. Returns
  * SPEC_OK, SPEC_ERR_INVALID_ARG (a bad pointer, type or size),
  * SPEC_ERR_UNSUPPORTED (over 2^31 work items) or SPEC_ERR_WORKSPACE (table
  * too small).

@@ -361,10 +361,21 @@ def spec_head_backward(dy, x, weight, pre=None, *, act: int = SPEC_ACT_NONE, wan
 
 # ------------------------------------------------------------------- AdamW
 class SpecAdamwTable:
-    """The device table of spec_adamw_table, with the tensors it names."""
+    """The device table of spec_adamw_table, with the tensors it names (weights and
+    gradients first)."""
 
     def __init__(self, data, n_items, state_bits, tensors):
         self.data, self.n_items, self.state_bits, self.tensors = data, n_items, state_bits, tensors
+        # weights whose gradient is autograd's own: it may be replaced behind the table
+        self.followed = [(p, g.data_ptr()) for p, g in zip(*tensors[:2])
+                         if p.is_leaf and p.grad is not None and p.grad.data_ptr() == g.data_ptr()]
+
+    def check(self):
+        """Raises where a weight's .grad is no longer the tensor of the table."""
+        for p, at in self.followed:
+            if p.grad is None or p.grad.data_ptr() != at:
+                raise ValueError("the gradient of a weight is not the table's tensor any more: keep the "
+                                 "gradients (zero_grad(set_to_none=False)) or build the table anew")
 
 
 def spec_adamw_table(params, grads, exp_avg, exp_avg_sq, *, exp_avg_scale=None,
@@ -374,7 +385,9 @@ def spec_adamw_table(params, grads, exp_avg, exp_avg_sq, *, exp_avg_scale=None,
     are f32 tensors, or torch.float8_e4m3fn (or uint8) codes with lists of f32
     scales, one per SPEC_ADAMW_BLOCK elements. `master` lists f32 copies of
     bf16 weights (entries may be None). The tensors' addresses must stay as
-    they are while the table is used."""
+    they are while the table is used: gradients are zeroed in place
+    (zero_grad(set_to_none=False)), not dropped. A step refuses a weight whose
+    .grad was the table's and has been replaced."""
     n = len(params)
     if not (len(grads) == len(exp_avg) == len(exp_avg_sq) == n):
         raise ValueError("params, grads and states must be lists of the same length")
@@ -426,6 +439,8 @@ def spec_adamw_step(table, step: int = 1, *, lr: float, beta1: float = 0.9, beta
     `lr_dev` (f32) and `step_dev` (int32) are one-element device tensors read
     when the kernel runs. See include/specdraft.h for the semantics. Returns
     the workspace."""
+    if table.followed:
+        table.check()
     dev, f32 = table.data.get_device(), torch.float32
     hyper = _HYPER.pack(lr, beta1, beta2, eps, weight_decay, step,
                         _arg("grad_scale", grad_scale, f32, 1, dev) or 0,

@@ -83,3 +83,48 @@ def test_a_stream_of_another_device_is_refused():
 
     with pytest.raises(ValueError):
         D._Call(1, FakeStream(), ())
+
+
+def weights():
+    p = [torch.zeros(4, requires_grad=True) for _ in range(3)]
+    p[0].grad, p[1].grad = torch.ones(4), torch.ones(4)
+    return p, [p[0].grad, p[1].grad.detach(), torch.ones(4)]   # the last one is not autograd's
+
+
+def test_an_adamw_table_follows_the_gradients_of_its_weights():
+    p, g = weights()
+    table = D.SpecAdamwTable(None, 1, 32, (p, g, [], []))
+    table.check()
+    p[0].grad.add_(1)
+    p[2].grad = torch.zeros(4)   # was none of the table's
+    table.check()
+
+
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("new", [None, torch.zeros(4)])
+def test_an_adamw_table_refuses_gradients_that_moved(which, new):
+    """zero_grad() leaves None, the next backward pass another tensor."""
+    p, g = weights()
+    table = D.SpecAdamwTable(None, 1, 32, (p, g, [], []))
+    p[which].grad = new
+    with pytest.raises(ValueError, match="gradient"):
+        table.check()
+
+
+@pytest.mark.gpu
+def test_an_adamw_step_refuses_gradients_that_moved():
+    import speculative_decoding_rejection_gb300 as sv
+    p = torch.ones(300, device="cuda:0", requires_grad=True)
+    (p * p).sum().backward()
+    state = [[torch.zeros(300, device="cuda:0")] for _ in range(2)]
+    table = sv.spec_adamw_table([p], [p.grad], *state)
+    for step in (1, 2):
+        p.grad.zero_()
+        (p * p).sum().backward()
+        assert sv.spec_get_status(sv.spec_adamw_step(table, step, lr=0.1)) == sv.SPEC_OK
+    keep = p.detach().clone()
+    p.grad = None
+    (p * p).sum().backward()
+    with pytest.raises(ValueError, match="gradient"):
+        sv.spec_adamw_step(table, 3, lr=0.1)
+    assert torch.equal(p, keep)
