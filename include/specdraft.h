@@ -189,8 +189,9 @@ int spec_distill_loss(const void *target, const void *draft, int dt, int R_d,
  * e4m3(sqrt(v) / s_v), s_v = max sqrt(v) / 448, where a positive root is held
  * as 2^-9 at least, so that no update divides by a root that became zero. A
  * block whose largest magnitude is below 2^-100 is held as zeros with scale
- * 0. The step itself goes by the new m and v before they are rounded. All
- * states zero is the start of training.
+ * 0. A magnitude that is not finite is held as NaN and is no block's largest. The
+ * step itself goes by the new m and v before they are rounded. All states zero is
+ * the start of training.
  *
  *   param       [n] f32 or bf16 (dtype), grad the same type.
  *   exp_avg     [n] f32, or e4m3 codes (1 byte) for states of 8 bits;

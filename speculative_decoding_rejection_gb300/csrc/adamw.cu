@@ -255,14 +255,26 @@ __device__ __forceinline__ void values8(const uint4 *w, float *x) {
 }
 
 // The new codes of a lane's 8 elements from m and the roots r, and the block's
-// scales.
-__device__ __forceinline__ void encode8(const AdTensor &x, long long blk, int lane, const float *m,
-                                        const float *r, uint32_t *cm, uint32_t *cv) {
+// scales. e4m3 has no infinity, and a scale of one would make NaN of the whole block
+// at the next step: what is infinite is held as NaN and counts for no scale.
+__device__ __forceinline__ void encode8(const AdTensor &x, long long blk, int lane, float *m, float *r,
+                                        uint32_t *cm, uint32_t *cv) {
   float am = 0.f, av = 0.f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) am = fmaxf(am, fabsf(m[j])), av = fmaxf(av, r[j]);
   am = warp_max(am);
   av = warp_max(av);
+  if (fmaxf(am, av) == INFINITY) {
+    am = av = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (isinf(m[j])) m[j] = NAN;
+      if (isinf(r[j])) r[j] = NAN;
+      am = fmaxf(am, fabsf(m[j])), av = fmaxf(av, r[j]);   // (NaN is passed over)
+    }
+    am = warp_max(am);
+    av = warp_max(av);
+  }
   // the reciprocals of m's and v's largest in the even and the odd lanes
   const float most = lane & 1 ? av : am;
   const bool none = most < TINY_ABSMAX;
