@@ -54,7 +54,7 @@ extern "C" {
  *   parent       [R] int32: LOCAL parent of each row's node, -1 for a root
  *                (local node 0); parent[c] < c; at most
  *                SPEC_MAX_TREE_DEPTH nodes below the root on a path.
- *   repetition   [B] f32 > 0, finite: rho.
+ *   repetition   [B] f32, 2^-126 to 2^126: rho.
  *   frequency    [B] f32, finite: f.
  *   presence     [B] f32, finite: p.
  *   bias_ids     [cu_bias[B]] int32, bias_values the same length f32 (finite

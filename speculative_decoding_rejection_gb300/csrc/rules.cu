@@ -32,6 +32,7 @@ constexpr int RU_MAX_SEG = 16;             // rows of one CTA
 constexpr int RU_BIASES = 256;             // biases of a range listed in shared memory
 constexpr int RU_HELD = 4;                 // history tokens a thread keeps between the scans
 constexpr int RU_SEEN = (int)0x80000000u;  // table: the prompt holds the token
+constexpr float RU_RHO_MIN = 0x1p-126f, RU_RHO_MAX = 0x1p126f;   // 1 / rho is normal too
 
 struct RulesArgs {
   const void *in;
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(RU_THREADS) k_rules(RulesArgs a) {
   const float fr = a.r.frequency ? GLD(a.r.frequency + b) : 0.f;
   const float pr = a.r.presence ? GLD(a.r.presence + b) : 0.f;
   int h0 = 0, h1 = 0, hp = 0, b0 = 0, b1 = 0, k0 = 0, K = 0;
-  bool bad = !(rho > 0.f) || !isfinite(rho) || !isfinite(fr) || !isfinite(pr);
+  bool bad = !(rho >= RU_RHO_MIN && rho <= RU_RHO_MAX) || !isfinite(fr) || !isfinite(pr);
   if (a.r.history != nullptr) {
     h0 = GLD(a.r.cu_history + b), h1 = GLD(a.r.cu_history + b + 1);
     if (h0 < 0 || h1 < h0 || h1 > a.n_history) bad = true, h1 = h0 = 0;
@@ -310,6 +311,8 @@ __global__ void __launch_bounds__(RU_THREADS) k_rules(RulesArgs a) {
     F |= ((reinterpret_cast<const uint8_t *>(sm.bits)[e >> 3] >> (e & 7)) & VFULL) << (v * VEC % 32);
   }
 
+  // a rounding more than the quotient's, which takes longer (1024 requests of 2..6
+  // rows of 201088: 516 us, so 509)
   const float inv_rho = 1.f / rho;
   const int n_bias = sm.n_bias;
   for (int i = 0; i < n; ++i) {
