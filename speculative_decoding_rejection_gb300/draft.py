@@ -17,6 +17,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 SPEC_ADAMW_BLOCK = 256
+_INT_MAX = 0x7fffffff
 SPEC_ACT_NONE, SPEC_ACT_SILU, SPEC_ACT_GELU = 0, 1, 2
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
@@ -89,26 +90,17 @@ def _arg(name, t, dtype, numel, dev):
 def _matrix(name, t, dtype, rows, width, dev):
     """The address of `rows` rows of `width` elements: a flat buffer, or a tensor
     whose trailing dimensions make up a row."""
-    if t is not None and t.dim() > 1 and t.shape[-1] != width:
-        row = 1
-        for n in reversed(t.shape):
-            row *= n
-            if row == width:
-                break
-        else:
-            raise ValueError(f"{name} must have rows of {width} elements, its shape is {tuple(t.shape)}")
+    if t is not None:
+        shape = t.shape
+        if shape and shape[-1] != width and len(shape) > 1:
+            row = 1
+            for n in reversed(shape):
+                row *= n
+                if row == width:
+                    break
+            else:
+                raise ValueError(f"{name} must have rows of {width} elements, its shape is {tuple(shape)}")
     return _arg(name, t, dtype, rows * width, dev)
-
-
-def _list(name, t, dtype, offsets_at, dev):
-    """(address, entries) of a list that offsets divide, as spec_logits_rules takes
-    them. An empty list has no address: the offsets' stands for it, unread."""
-    if t is None:
-        return 0, 0
-    n = t.numel()
-    if n == 0:
-        return (offsets_at, -1) if offsets_at else (0, 0)
-    return _arg(name, t, dtype, 0, dev), n if n < 0x7fffffff else 0x7fffffff
 
 
 def _device(name, t):
@@ -203,13 +195,32 @@ def spec_process_logits(logits, cu_rows, *, max_rows: int, history=None, cu_hist
     cu_history_at = _arg("cu_history", cu_history, i32, B + 1, dev) or 0
     cu_tokens_at = _arg("cu_tokens", cu_tokens, i32, B + 1, dev) or 0
     cu_bias_at = _arg("cu_bias", cu_bias, i32, B + 1, dev) or 0
-    history_at, n_history = _list("history", history, i32, cu_history_at, dev)
-    bias_at, n_bias = _list("bias_ids", bias_ids, i32, cu_bias_at, dev)
-    values_at = cu_bias_at if n_bias < 0 else _arg("bias_values", bias_values, f32, n_bias, dev) or 0
-    if parent is None:
-        tokens_at, n_tokens = _list("tokens", tokens, i32, cu_tokens_at, dev)
+    # an empty list has no address: its offsets' stands for it, unread (entries: -1)
+    history_at = n_history = tokens_at = n_tokens = bias_at = n_bias = 0
+    if history is not None:
+        n_history = history.numel()
+        if n_history:
+            history_at = _arg("history", history, i32, 0, dev)
+        else:
+            history_at, n_history = cu_history_at, -1
+    if parent is not None:
+        tokens_at, n_tokens = _arg("tokens", tokens, i32, R, dev) or 0, R
+    elif tokens is not None:
+        n_tokens = tokens.numel()
+        if n_tokens:
+            tokens_at = _arg("tokens", tokens, i32, 0, dev)
+        else:
+            tokens_at, n_tokens = cu_tokens_at, -1
+    if bias_ids is not None:
+        n_bias = bias_ids.numel()
+    if n_bias or bias_ids is None:
+        bias_at = _arg("bias_ids", bias_ids, i32, 0, dev) or 0
+        values_at = _arg("bias_values", bias_values, f32, n_bias, dev) or 0
     else:
-        tokens_at, n_tokens = _arg("tokens", tokens, i32, R, dev) or 0, 0
+        bias_at = values_at = cu_bias_at
+        n_bias = -1
+    if n_history + n_tokens + n_bias > _INT_MAX:   # a list may be longer than offsets reach
+        n_history, n_tokens, n_bias = (min(n, _INT_MAX) for n in (n_history, n_tokens, n_bias))
     mask_rows_at = _arg("mask_rows", mask_rows, i32, R, dev) or 0
     mask_at = _arg("mask", mask, i32, 0, dev) or 0
     if mask_at == 0 and mask is not None:   # no rows: an address that is not read
