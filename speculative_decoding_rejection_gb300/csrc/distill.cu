@@ -37,8 +37,8 @@
 // logits: 18.4 us, element by element about 4 us more).
 //
 // Measured at 4096 positions of 201088 bf16 logits, 3/4 of them weighted: 0.81 ms
-// (5.1 TB/s of the bytes that have to move); a cluster per position 1.06 ms (1.18 ms with its slices in shared memory but no
-// overlap of positions); persistent CTAs whose second-pass units follow the
+// (5.1 TB/s of the bytes that have to move); a cluster per position 1.06 ms (1.18 ms
+// with its slices in shared memory but no overlap of positions); persistent CTAs whose second-pass units follow the
 // first-pass units of later rows 1.04 to 1.8 ms, as L2 does not hold the rows
 // between the two.
 #include "cluster_choice.h"
@@ -68,7 +68,10 @@ constexpr int DR_PIECE = DR_PV * 16;       // bytes of each row in a ring slot
 constexpr int DR_SLOTS = 6;                // 192 KB
 constexpr int DR_AHEAD = 1;                // pieces of the next row between a row's two passes, at least
 constexpr int DR_MAX_CLUSTER = 8;
-// calls whose rows hold less than this run as a cluster per position
+// Calls whose rows hold less than this run as a cluster per position. bf16 rows of
+// 32000, persistent clusters and a cluster per position: 8 MB 20.1 and 19.1 us, 32 MB
+// 24.2 and 26.2, 128 MB 59 and 70; of 201088: 16 MB 20.1 and 19.1, 128 MB 61 and 79.
+// (Rows of 4096 stay better off with the latter: 128 MB 151 and 130 us.)
 constexpr long long DR_MIN_BYTES = 32ll << 20;
 
 struct DistillArgs {

@@ -17,7 +17,8 @@
 // Large products run on pairs of CTAs (cta_group::2): a pair's 256 x nt tile
 // takes 128 rows of A and half of B's columns from each CTA, so a stage of r
 // moves 32 KB into an SM where a lone CTA's 128 x 256 tile moves 48 KB (1280 rows
-// of 4096 to 128256 columns: 732 us, 1840 TFLOP/s; lone CTAs 841 us). What
+// of 4096 to 128256 columns, with pauses between the calls: 732 us, 1840 TFLOP/s;
+// lone CTAs 841 us; back to back, where the clock falls, 857 us by pairs). What
 // bounds the rest: the SMs' intake (with half of B's loads left out the same call
 // takes 694 us) and the epilogue (without its stores 708 us).
 //
@@ -54,7 +55,10 @@ constexpr int HD_REST_COST = 4;
 constexpr int HD_STAGE_LD = 36;       // floats between columns of a warp's staging (no bank conflicts)
 constexpr int HD_STAGING = HD_EPI * 16 * HD_STAGE_LD * 4;   // 16 columns of 32 lanes per warp
 constexpr int HD_SMEM = 226 * 1024 - HD_STAGING - 1024;   // ring
-constexpr int HD_PLAN_SMS = 152;      // SMs the split is planned for
+// SMs the split is planned for: a number of its own, not the device's, so that a
+// workspace's size and a result's bits are the same on every one. (With fewer SMs the
+// runs follow one another; none waits for another.)
+constexpr int HD_PLAN_SMS = 152;
 constexpr int HD_A_BYTES = HD_I * HD_R * 2;
 
 struct HeadArgs {   // tiles of 128 x nt; a pair's tile counts as two, one per CTA
@@ -636,7 +640,7 @@ __global__ void __launch_bounds__(256) k_head_join(const HeadArgs a, int ctas) {
 // per lane, and multiplies them with the M rows of x, which the block keeps in
 // shared memory as f32. Bound by HBM's reads of W, which come as whole rows:
 // the tiles' boxes of 128 bytes per row reach 4.8 TB/s at one row of 4096 by
-// 32000, this 6.1 TB/s (43 us). VEC: rows of W and x are 16-byte aligned.
+// 32000, this 6.0 TB/s (44 us). VEC: rows of W and x are 16-byte aligned.
 constexpr int HD_FEW = 4;        // rows of x at most
 constexpr int HD_N = 2;          // rows of W per warp
 constexpr int HD_AHEAD = 2;      // pieces of 8 elements per lane and row that are loaded ahead
@@ -668,8 +672,8 @@ __global__ void __launch_bounds__(256) k_head_few(const HeadArgs a, const uint16
       for (int r = 0; r < HD_N; ++r) row[r] = w + (long long)min(n0 + r, a.I - 1) * K + k0;
       if (VEC) {
         // HD_AHEAD pieces' loads are out together, those of two rounds where the
-        // registers allow: one row of 4096 by 32000 in 45.0 us, by one piece and four
-        // rounds 47.2 us, by four pieces 49.2 us
+        // registers allow (one row of 4096 by 32000; by one piece and four rounds 2 us
+        // more, by four pieces 4 us more)
 #pragma unroll 2
         for (int k1 = lane * 8; k1 < kn; k1 += 256 * HD_AHEAD) {
           uint4 raw[HD_AHEAD][HD_N];
