@@ -71,7 +71,13 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volat
   }
 }
 
-// Host: the status header starts every call at SPEC_OK.
+// The status header starts every call at SPEC_OK: by the call's first kernel, or (in the
+// checked build, where another block may have reported an access already) by the host.
+__device__ __forceinline__ void start_status(WsHeader *h) {
+#ifndef SPEC_CHECKED
+  h->status = SPEC_OK, h->detail = -1;
+#endif
+}
 inline int reset_header(void *workspace, cudaStream_t st) {
   return cudaMemsetAsync(workspace, 0, sizeof(WsHeader), st) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }

@@ -214,10 +214,10 @@ __device__ __forceinline__ float act_slope(float z, int act) {
   return 1.f;
 }
 __device__ __forceinline__ float bf16_at(const __nv_bfloat16 *p, long long i) {
-  return bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(p)[i]);
+  return bf16_bits_to_f32(GLD(reinterpret_cast<const uint16_t *>(p) + i));
 }
 __device__ __forceinline__ void bf16_to(__nv_bfloat16 *p, long long i, float v) {
-  reinterpret_cast<uint16_t *>(p)[i] = (uint16_t)f32_to_bf16_bits(v);
+  GST(reinterpret_cast<uint16_t *>(p) + i, (uint16_t)f32_to_bf16_bits(v));
 }
 __device__ __forceinline__ void unpack8(const uint4 &w, float *x) {
   x[0] = bf16lo(w.x), x[1] = bf16hi(w.x), x[2] = bf16lo(w.y), x[3] = bf16hi(w.y);
@@ -233,18 +233,18 @@ __device__ __forceinline__ uint4 pack8(const float *x) {
 // residual is loaded ahead (residual8), as its latency is a tile's stages.
 __device__ __forceinline__ uint4 residual8(const HeadArgs &a, int i, int j) {
   if (a.residual == nullptr || j >= a.J || i >= a.I) return make_uint4(0, 0, 0, 0);
-  return *reinterpret_cast<const uint4 *>(a.residual + (long long)j * a.ldo + i);
+  return GLD(reinterpret_cast<const uint4 *>(a.residual + (long long)j * a.ldo + i));
 }
 __device__ __forceinline__ void finish8(const HeadArgs &a, float *z, int i, int j, const uint4 &res) {
   if (j >= a.J || i >= a.I) return;
   const long long at = (long long)j * a.ldo + i;
   float x[8];
   if (a.bias) {
-    unpack8(*reinterpret_cast<const uint4 *>(a.bias + i), x);
+    unpack8(GLD(reinterpret_cast<const uint4 *>(a.bias + i)), x);
 #pragma unroll
     for (int q = 0; q < 8; ++q) z[q] += x[q];
   }
-  if (a.pre) *reinterpret_cast<uint4 *>(a.pre + at) = pack8(z);
+  if (a.pre) GST(reinterpret_cast<uint4 *>(a.pre + at), pack8(z));
   if (a.act != SPEC_ACT_NONE) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) z[q] = act_value(z[q], a.act);
@@ -254,7 +254,7 @@ __device__ __forceinline__ void finish8(const HeadArgs &a, float *z, int i, int 
 #pragma unroll
     for (int q = 0; q < 8; ++q) z[q] += x[q];
   }
-  *reinterpret_cast<uint4 *>(a.out + at) = pack8(z);
+  GST(reinterpret_cast<uint4 *>(a.out + at), pack8(z));
 }
 // The same for N columns j .. of element i, for any result: the lanes of a warp
 // take neighbouring i, so an access is 64 bytes of a row.
@@ -263,7 +263,7 @@ __device__ __forceinline__ void residual_column(const HeadArgs &a, int i, int j,
   const bool on = a.residual != nullptr && i < a.I;
   const uint16_t *r = reinterpret_cast<const uint16_t *>(a.residual) + (long long)j * a.ldo + i;
 #pragma unroll
-  for (int q = 0; q < N; ++q) res[q] = on && j + q < a.J ? r[q * a.ldo] : (uint16_t)0;
+  for (int q = 0; q < N; ++q) res[q] = on && j + q < a.J ? GLD(r + q * a.ldo) : (uint16_t)0;
 }
 template <int N>
 __device__ __forceinline__ void finish_column(const HeadArgs &a, const float *z, int i, int j, const uint16_t *res) {
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
   if (t == 0) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // k_head_join, which waits
     // the only error is a wait that runs out, seconds after this
-    if (blockIdx.x == 0 && a.reset) a.hdr->status = SPEC_OK, a.hdr->detail = -1;
+    if (blockIdx.x == 0 && a.reset) start_status(a.hdr);
     sh.abort = 0;
     for (int s = 0; s < a.stages; ++s) mbar_init(&sh.full[s], 1), mbar_init(&sh.empty[s], 1);
     for (int s = 0; s < 2; ++s) mbar_init(&sh.acc_full[s], 1), mbar_init(&sh.acc_empty[s], HD_EPI * CTAS);
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(HD_THREADS, 1)
           tmem_ld32(d + c, v);
 #pragma unroll
           for (int q = 0; q < 32; ++q)
-            if (j0 + c + q < last) mine[(c + q) * HD_I] = v[q];
+            if (j0 + c + q < last) GST(mine + (c + q) * HD_I, v[q]);
         }
       } else if (!a.vec) {
         uint16_t next[32];   // the residual of the next columns, on its way
@@ -619,12 +619,12 @@ __global__ void __launch_bounds__(256) k_head_join(const HeadArgs a, int ctas) {
     if (VEC) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float4 y = __ldcs(reinterpret_cast<const float4 *>(from) + h);
+        const float4 y = GLDCS(reinterpret_cast<const float4 *>(from) + h);
         x[4 * h] = y.x, x[4 * h + 1] = y.y, x[4 * h + 2] = y.z, x[4 * h + 3] = y.w;
       }
     } else {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) x[q] = j + q < a.J ? __ldcs(from + q * HD_I) : 0.f;
+      for (int q = 0; q < 8; ++q) x[q] = j + q < a.J ? GLDCS(from + q * HD_I) : 0.f;
     }
 #pragma unroll
     for (int q = 0; q < 8; ++q) z[q] = start ? x[q] : z[q] + x[q];
@@ -650,7 +650,7 @@ template <int M, bool VEC>
 __global__ void __launch_bounds__(256) k_head_few(const HeadArgs a, const uint16_t *x, const uint16_t *w, int K) {
   extern __shared__ __align__(16) float xs[];   // [M][min(K, HD_FEW_K), rounded up to 8]
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  if (blockIdx.x == 0 && t == 0) a.hdr->status = SPEC_OK, a.hdr->detail = -1;   // nothing here sets another
+  if (blockIdx.x == 0 && t == 0) start_status(a.hdr);   // nothing here sets another
   const int groups = (a.I + HD_N - 1) / HD_N, step = gridDim.x * 8;
   // every warp of the block goes round as often as its first one: they share xs
   for (int gb = blockIdx.x * 8; gb < groups; gb += step) {
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(256) k_head_few(const HeadArgs a, const uint16
         __syncthreads();
         for (int e = t; e < M * ld; e += 256) {
           const int m = e / ld, k = e - m * ld;
-          xs[e] = m < a.J && k < kn ? bf16_bits_to_f32(x[(long long)m * K + k0 + k]) : 0.f;
+          xs[e] = m < a.J && k < kn ? bf16_bits_to_f32(GLD(x + (long long)m * K + k0 + k)) : 0.f;
         }
         __syncthreads();
       }
@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(256) k_head_few(const HeadArgs a, const uint16
           for (int u = 0; u < HD_AHEAD; ++u)
 #pragma unroll
             for (int r = 0; r < HD_N; ++r)
-              if (k1 + 256 * u < kn) raw[u][r] = __ldcs(reinterpret_cast<const uint4 *>(row[r] + k1 + 256 * u));
+              if (k1 + 256 * u < kn) raw[u][r] = GLDCS(reinterpret_cast<const uint4 *>(row[r] + k1 + 256 * u));
 #pragma unroll
           for (int u = 0; u < HD_AHEAD; ++u) {
             const int k = k1 + 256 * u;
@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(256) k_head_few(const HeadArgs a, const uint16
         for (int k = lane; k < kn; k += 32) {
 #pragma unroll
           for (int r = 0; r < HD_N; ++r) {
-            const float v = bf16_bits_to_f32(row[r][k]);
+            const float v = bf16_bits_to_f32(GLD(row[r] + k));
 #pragma unroll
             for (int m = 0; m < M; ++m) acc[m][r] += v * xs[m * ld + k];
           }
@@ -738,11 +738,11 @@ __global__ void __launch_bounds__(256) k_head_few(const HeadArgs a, const uint16
 __device__ __forceinline__ uint4 load8_any(const uint16_t *p, const uint16_t *end, int n) {
   const int shift = (int)((uintptr_t)p & 15);
   const uint4 *v = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(p) - shift);
-  if (n >= 8 && shift == 0) return v[0];
-  if (n >= 8 && reinterpret_cast<const uint16_t *>(v + 2) <= end) return shift16(v[0], v[1], shift);
+  if (n >= 8 && shift == 0) return GLD(v);
+  if (n >= 8 && reinterpret_cast<const uint16_t *>(v + 2) <= end) return shift16(GLD(v), GLD(v + 1), shift);
   uint32_t w[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = j < n ? p[j] : 0u;
+  for (int j = 0; j < 8; ++j) w[j] = j < n ? GLD(p + j) : 0u;
   return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
 }
 
@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(256) k_pad_rows(Pad p0, Pad p1, int C, int ld)
   const uint16_t *end = p.src + p.rows * C;
   for (long long r = blockIdx.y * 8ll + (threadIdx.x >> 5); r < p.rows; r += gridDim.y * 8ll) {
     const uint4 x = load8_any(p.src + r * C + c, end, C - c);
-    *reinterpret_cast<uint4 *>(p.dst + r * ld + c) = x;
+    GST(reinterpret_cast<uint4 *>(p.dst + r * ld + c), x);
   }
 }
 
@@ -777,7 +777,7 @@ template <bool ALIGNED>
 __global__ void __launch_bounds__(256)
     k_dz(const uint16_t *dy, const uint16_t *pre, uint16_t *dz, float *psum, int M, int N, int ld, int act,
          WsHeader *hdr) {
-  if (blockIdx.x == 0 && threadIdx.x == 0) hdr->status = SPEC_OK, hdr->detail = -1;
+  if (blockIdx.x == 0 && threadIdx.x == 0) start_status(hdr);
   __shared__ float sums[8][32 * 8 + 1];
   const int per_row = (ld + 255) / 256, seg = blockIdx.x / per_row, bx = blockIdx.x - seg * per_row;
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
@@ -793,7 +793,7 @@ __global__ void __launch_bounds__(256)
       if (pre) g[j] = __fmul_rn(g[j], act_slope(z[j], act));
       acc[j] = __fadd_rn(acc[j], g[j]);   // unfused: the same sums with and without dz
     }
-    if (dz) *reinterpret_cast<uint4 *>(dz + (long long)r * ld + c0) = pack8(g);
+    if (dz) GST(reinterpret_cast<uint4 *>(dz + (long long)r * ld + c0), pack8(g));
   };
   // 8 elements of a row, zeros behind its end. Rows off the 16-byte grid: by two
   // aligned vectors, where both lie in the matrix; its last elements one by one.
@@ -807,10 +807,10 @@ __global__ void __launch_bounds__(256)
                         ? r1
                         : max(r0, (int)((total - c0 - 16 + N) / N));
   auto get = [&](const uint16_t *p) -> uint4 {
-    if (ALIGNED) return *reinterpret_cast<const uint4 *>(p);
+    if (ALIGNED) return GLD(reinterpret_cast<const uint4 *>(p));
     const int shift = (int)((uintptr_t)p & 15);
     const uint4 *v = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(p) - shift);
-    uint4 x = shift16(v[0], v[1], shift);   // (no shift at all is one, too)
+    uint4 x = shift16(GLD(v), GLD(v + 1), shift);   // (no shift at all is one, too)
     x.x &= keep[0], x.y &= keep[1], x.z &= keep[2], x.w &= keep[3];
     return x;
   };
@@ -836,8 +836,8 @@ __global__ void __launch_bounds__(256)
         uint32_t g[8], z[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          g[j] = j < n ? dy[(long long)r * N + c0 + j] : 0u;
-          z[j] = pre && j < n ? pre[(long long)r * N + c0 + j] : 0u;
+          g[j] = j < n ? GLD(dy + (long long)r * N + c0 + j) : 0u;
+          z[j] = pre && j < n ? GLD(pre + (long long)r * N + c0 + j) : 0u;
         }
         row(r, make_uint4(g[0] | g[1] << 16, g[2] | g[3] << 16, g[4] | g[5] << 16, g[6] | g[7] << 16),
             make_uint4(z[0] | z[1] << 16, z[2] | z[3] << 16, z[4] | z[5] << 16, z[6] | z[7] << 16));
@@ -852,15 +852,15 @@ __global__ void __launch_bounds__(256)
   float s = 0.f;
 #pragma unroll
   for (int k = 0; k < 8; ++k) s += sums[k][threadIdx.x];
-  if (col < N) psum[(long long)seg * N + col] = s;
+  if (col < N) GST(psum + (long long)seg * N + col, s);
 }
 
 __global__ void k_db(const float *psum, float *db, int N, int segs) {
   const int c = blockIdx.x * blockDim.x + threadIdx.x;
   if (c >= N) return;
   float s = 0.f;
-  for (int k = 0; k < segs; ++k) s += psum[(long long)k * N + c];
-  db[c] = s;
+  for (int k = 0; k < segs; ++k) s += GLD(psum + (long long)k * N + c);
+  GST(db + c, s);
 }
 
 // --------------------------------------------------------------- the host
@@ -1099,6 +1099,18 @@ extern "C" int spec_head_forward(const void *x, const void *weight, const void *
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char *ws = static_cast<char *>(workspace);
   if (M == 0) return reset_header(ws, st);
+#ifdef SPEC_CHECKED
+  check_begin(static_cast<WsHeader *>(workspace));
+  check_add(workspace, forward_bytes(M, N, K));
+  check_add(x, 2ull * M * K);
+  check_add(weight, 2ull * N * K);
+  check_add(bias, 2ull * N);
+  check_add(residual, 2ull * M * N);
+  check_add(y, 2ull * M * N);
+  check_add(pre, 2ull * M * N);
+  if (reset_header(workspace, st) != SPEC_OK) return SPEC_ERR_CUDA;
+#endif
+  if (check_upload(st) != SPEC_OK) return SPEC_ERR_CUDA;
   HeadArgs a{};
   a.hdr = reinterpret_cast<WsHeader *>(ws);
   a.part = reinterpret_cast<float *>(ws + sizeof(WsHeader));
@@ -1157,6 +1169,19 @@ extern "C" int spec_head_backward(const void *dy, const void *x, const void *wei
     return SPEC_OK;
   }
   if (dx == nullptr && dw == nullptr && db == nullptr) return reset_header(workspace, st);
+#ifdef SPEC_CHECKED
+  check_begin(a.hdr);
+  check_add(workspace, backward_bytes(M, N, K));
+  check_add(dy, 2ull * M * N);
+  check_add(x, 2ull * M * K);
+  check_add(weight, 2ull * N * K);
+  check_add(pre, 2ull * M * N);
+  check_add(dx, 2ull * M * K);
+  check_add(dw, 2ull * N * K);
+  check_add(db, 4ull * N);
+  if (reset_header(workspace, st) != SPEC_OK) return SPEC_ERR_CUDA;
+#endif
+  if (check_upload(st) != SPEC_OK) return SPEC_ERR_CUDA;
   int rc;
   // dz: dy itself where no activation changes it and TMA can address its rows
   const int ldz = (int)round8(N);
