@@ -59,8 +59,7 @@ static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
 // of the kernels goes through the accessors below (other than copies by a
 // tensor map, which bounds its own, and the optimizer's, whose tensors are
 // known to its device table alone and bounded by their sizes there). They
-// check it against
-// the byte ranges of the buffers of the call being run (its inputs,
+// check it against the byte ranges of the buffers of the call being run (its inputs,
 // outputs and workspace). An access outside them is skipped (a load gives
 // zero, a store or a copy is dropped, a skipped bulk copy still completes
 // its barrier's transaction) and reported in the status word as
