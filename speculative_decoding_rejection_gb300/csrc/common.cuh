@@ -56,10 +56,8 @@ static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
 
 // ------------------------------------------------------- checked build
 // Built with SPEC_CHECKED (libspecverify_checked.so), every global access
-// of the kernels goes through the accessors below (other than copies by a
-// tensor map, which bounds its own, and the optimizer's, whose tensors are
-// known to its device table alone and bounded by their sizes there). They
-// check it against the byte ranges of the buffers of the call being run (its inputs,
+// of the kernels goes through the accessors below, which check it against
+// the byte ranges of the buffers of the call being run (its inputs,
 // outputs and workspace). An access outside them is skipped (a load gives
 // zero, a store or a copy is dropped, a skipped bulk copy still completes
 // its barrier's transaction) and reported in the status word as
@@ -92,7 +90,7 @@ __device__ __forceinline__ bool gchk(const void *p, unsigned long long bytes, in
 __device__ __forceinline__ bool gchk(const void *, unsigned long long, int) { return true; }
 #endif
 // Checked global accesses: plain load, non-coherent load, L2-only load,
-// streaming load, store, and a range test for atomics and copies.
+// store, and a range test for atomics and copies.
 template <class T>
 __device__ __forceinline__ T gld(const T *p, int line) {
   return gchk(p, sizeof(T), line) ? *p : T{};
@@ -104,10 +102,6 @@ __device__ __forceinline__ T gldg(const T *p, int line) {
 template <class T>
 __device__ __forceinline__ T gldcg(const T *p, int line) {
   return gchk(p, sizeof(T), line) ? __ldcg(p) : T{};
-}
-template <class T>
-__device__ __forceinline__ T gldcs(const T *p, int line) {
-  return gchk(p, sizeof(T), line) ? __ldcs(p) : T{};
 }
 template <class T, class U>
 __device__ __forceinline__ void gst(T *p, const U &v, int line) {
@@ -135,7 +129,6 @@ static inline void check_add(const void *, unsigned long long) {}
 #define GLD(p) ::sv::gld((p), __LINE__)
 #define GLDG(p) ::sv::gldg((p), __LINE__)
 #define GLDCG(p) ::sv::gldcg((p), __LINE__)
-#define GLDCS(p) ::sv::gldcs((p), __LINE__)
 #define GST(p, ...) ::sv::gst((p), (__VA_ARGS__), __LINE__)
 #define GCHK(p, n) ::sv::gchk((p), (n), __LINE__)
 

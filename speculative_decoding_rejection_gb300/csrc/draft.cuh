@@ -11,6 +11,16 @@
 
 namespace sv {
 
+// A checked streaming load, beside common.cuh's accessors. Two kinds of access of the
+// kernels here go by none: copies by a tensor map, which bounds its own, and the
+// optimizer's, whose tensors are known to its device table alone and bounded by their
+// sizes there.
+template <class T>
+__device__ __forceinline__ T gldcs(const T *p, int line) {
+  return gchk(p, sizeof(T), line) ? __ldcs(p) : T{};
+}
+#define GLDCS(p) ::sv::gldcs((p), __LINE__)
+
 __device__ __forceinline__ float bf16_bits_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
 // Two roundings to bf16 (to nearest, ties to even), packed, lo in the low half.
 __device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
