@@ -17,10 +17,10 @@
 // Large products run on pairs of CTAs (cta_group::2): a pair's 256 x nt tile
 // takes 128 rows of A and half of B's columns from each CTA, so a stage of r
 // moves 32 KB into an SM where a lone CTA's 128 x 256 tile moves 48 KB (1280 rows
-// of 4096 to 128256 columns, with pauses between the calls: 732 us, 1840 TFLOP/s;
-// lone CTAs 841 us; back to back, where the clock falls, 857 us by pairs). What
-// bounds the rest: the SMs' intake (with half of B's loads left out the same call
-// takes 694 us) and the epilogue (without its stores 708 us).
+// of 4096 to 128256 columns, by pairs 732 us, by lone CTAs 841 us, both with pauses
+// between the calls on one card; another one took 762 us with pauses and 818 us back to
+// back, where the clock falls). What bounds the rest: the SMs' intake (with half of B's
+// loads left out 694 us instead of 732) and the epilogue (without its stores 708 us).
 //
 // A persistent CTA per SM: one warp feeds a ring of TMA stages (64 of r each),
 // one issues tcgen05.mma, eight run the epilogue from the other of two
