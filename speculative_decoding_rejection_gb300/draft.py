@@ -227,7 +227,7 @@ def spec_process_logits(logits, cu_rows, *, max_rows: int, history=None, cu_hist
         mask_at = mask_rows_at
     rules = _RULES.pack(
         history_at, cu_history_at,
-        _arg("prompt_len", prompt_len, i32, B, dev) or 0 if history_at else 0,
+        0 if history is not None and not history_at else _arg("prompt_len", prompt_len, i32, B, dev) or 0,
         tokens_at, cu_tokens_at,
         _arg("parent", parent, i32, R, dev) or 0,
         _arg("repetition", repetition, f32, B, dev) or 0,

@@ -84,3 +84,10 @@ def test_lists_that_end_at_the_last_offset():
         results.append(out)
         del r
     assert torch.equal(*results)
+
+
+def test_prompt_lengths_want_a_history():
+    with pytest.raises(sv.SpecError):
+        call(dict(prompt_len=ints(1, 1)))
+    z, out, status = call(dict(prompt_len=ints(1, 1), history=ints()))   # an empty one, without offsets
+    assert status == sv.SPEC_OK and torch.equal(z, out)
