@@ -15,7 +15,13 @@
  *   - spec_head_forward, spec_head_backward: a product with bias, activation
  *     and residual in its epilogue, and its gradients;
  *   - spec_adamw_step: one AdamW step over many tensors at once, with
- *     states in 32 bits or in 8.
+ *     states in 32 bits or in 8;
+ *   - spec_grad_norm, spec_clip_grads: the norm over all gradients of the
+ *     optimizer's table, and their clipping by it;
+ *   - spec_head4_forward: the head's product for few rows with weights of 4
+ *     bits and group scales, as it is served;
+ *   - spec_sample: a token of every row's law after min-p, top-k and top-p,
+ *     from given random numbers, and the row with what was dropped at -inf.
  *
  * The conventions of specverify.h hold: device pointers owned by the caller,
  * no allocation, asynchronous on `stream`, negative return values for errors
@@ -269,6 +275,36 @@ int spec_adamw_step(const void *table, int64_t n_items, int state_bits,
                     const spec_adamw_hyper *hyper, void *workspace,
                     size_t ws_bytes, spec_stream_t stream);
 
+/*
+ * The norm over the gradients of an optimizer's table (spec_adamw_table), and the
+ * factor that clips them. With s = *grad_scale (1 for NULL):
+ *
+ *   norm   = sqrt(sum (s g)^2), or max |s g| with `inf` not 0
+ *   factor = s min(1, max_norm / (norm + 1e-6))
+ *
+ * out[0] = norm, out[1] = factor (f32, device; out + 1 is what spec_adamw_step
+ * takes as grad_scale). Squares neither overflow nor vanish on the way: a norm
+ * that f32 can hold is found. A gradient that is NaN makes norm and factor NaN; an
+ * infinite one makes the norm infinite and the factor 0, so that a step by it has
+ * NaN for that weight. A table without elements has norm 0.
+ *
+ * spec_clip_grads also multiplies every gradient by the factor, in place, rounded
+ * once to its type; gradients whose factor is 1 keep their bits. A table that does
+ * not fit n_items and state_bits is not used: the status word reads
+ * SPEC_ERR_INVALID_ARG and out is set to NaN.
+ *
+ *   max_norm    > 0, may be infinite (nothing is clipped).
+ *   grad_scale  optional device f32; not `out` or a part of it.
+ *   workspace   spec_grad_norm_workspace() bytes, 256-byte aligned.
+ */
+size_t spec_grad_norm_workspace(void);
+int spec_grad_norm(const void *table, int64_t n_items, int state_bits, int inf,
+                   double max_norm, const float *grad_scale, float *out,
+                   void *workspace, size_t ws_bytes, spec_stream_t stream);
+int spec_clip_grads(const void *table, int64_t n_items, int state_bits, int inf,
+                    double max_norm, const float *grad_scale, float *out,
+                    void *workspace, size_t ws_bytes, spec_stream_t stream);
+
 /* Activations of a head's product. */
 typedef enum {
   SPEC_ACT_NONE = 0,
@@ -316,6 +352,116 @@ int spec_head_backward(const void *dy, const void *x, const void *weight,
                        const void *pre, int M, int N, int K, int act,
                        void *dx, void *dw, float *db, void *workspace,
                        size_t ws_bytes, spec_stream_t stream);
+
+/*
+ * A head's weight in 4 bits. Element (n, k) stands for
+ *
+ *   scale[n, k / group] (code[n, k] - zero[n, k / group])
+ *
+ * with codes and zeros 0 .. 15 (zeros NULL: 8 throughout) and bf16 scales; group
+ * is 32, 64 or 128, and a row's last group may be shorter. The kernel reads the
+ * codes in an order of its own (`packed`), laid out once:
+ *
+ *   codes   [N, ceil(K / 2)] bytes, the code of an even column in the low 4 bits.
+ *   scales  [N, ceil(K / group)] bf16.
+ *   zeros   [N, ceil(K / group)] bytes (their low 4 bits count), or NULL.
+ *   packed  spec_head4_packed_bytes(N, K) bytes, 16-byte aligned.
+ *
+ * spec_head4_pack lays codes out. spec_head4_quantize makes codes and scales of a
+ * bf16 weight [N, K]: scale = max|w| / 7 over the group, rounded to bf16, code = 8 +
+ * w / scale rounded to the nearest (ties to even, at most 7 from 8); a group of
+ * zeros, or whose scale is no positive normal number, has scale 0. A weight
+ * that is not finite is reported (the status word reads SPEC_ERR_INVALID_ARG) and
+ * counts as 0. spec_head4_unpack writes the weight's values, rounded once to bf16
+ * [N, K], for calls of more rows (spec_head_forward) and for gradients.
+ */
+#define SPEC_HEAD4_MAX_ROWS 64
+size_t spec_head4_packed_bytes(int N, int K);
+int spec_head4_pack(const void *codes, int N, int K, void *packed,
+                    spec_stream_t stream);
+int spec_head4_quantize(const void *weight, int N, int K, int group, void *packed,
+                        void *scales, void *workspace, size_t ws_bytes,
+                        spec_stream_t stream);
+int spec_head4_unpack(const void *packed, const void *scales, const void *zeros,
+                      int N, int K, int group, void *weight, spec_stream_t stream);
+
+/*
+ * y = act(x W^T + bias) + residual for up to SPEC_HEAD4_MAX_ROWS rows and a W of
+ * 4 bits (see above), as spec_head_forward. Products of x with code - zero are exact, their
+ * sums and the scaled sums of the groups are held in 32 bits, y is rounded once.
+ *
+ *   x         [M, K] bf16, 0 <= M <= SPEC_HEAD4_MAX_ROWS; bias [N] or NULL;
+ *             residual [M, N] or NULL. 1 <= N, K <= 2^24. x is 16-byte aligned, the
+ *             others to their elements.
+ *   y         [M, N] bf16. May be `residual` itself, not another input.
+ *   workspace spec_head4_forward_workspace(M, N, K) bytes (0 on invalid sizes),
+ *             256-byte aligned.
+ */
+size_t spec_head4_forward_workspace(int M, int N, int K);
+int spec_head4_forward(const void *x, const void *packed, const void *scales,
+                       const void *zeros, const void *bias, const void *residual,
+                       int M, int N, int K, int group, int act, void *y,
+                       void *workspace, size_t ws_bytes, spec_stream_t stream);
+
+/*
+ * What every request samples by (host memory, read during the call; device
+ * pointers). A NULL array leaves its step out.
+ *
+ *   temperature  [B] f32 >= 0, finite; NULL: 1. Below SPEC_GREEDY_T: the first of
+ *                the largest logits is the whole law.
+ *   min_p        [B] f32, 0 .. 1: 0 leaves the step out.
+ *   top_k        [B] int32; 0 and below: left out.
+ *   top_p        [B] f32, 0 .. 1: 1 leaves the step out.
+ */
+typedef struct {
+  const float *temperature;
+  const float *min_p;
+  const int32_t *top_k;
+  const float *top_p;
+} spec_sampling;
+
+/* Bytes of workspace spec_sample needs (0 on invalid sizes). */
+size_t spec_sample_workspace(int R, int V);
+
+/*
+ * A token of each of R rows, drawn with the random number u[r], and the rows with
+ * what is not in the law at -inf. With m the row's largest logit and the tokens in
+ * the order of falling logits (equal ones by rising id; -inf takes no part):
+ *
+ *   weight   w_n = exp((z_n - m) / T)
+ *   min-p    drops tokens with (z - m) / T < ln min_p
+ *   top-k    keeps the first k of what is left
+ *   top-p    keeps the first n of those, n the smallest number whose weights
+ *            reach top_p times the weight of all of them (one at least)
+ *   token    the first whose weight and those before it are over u times the
+ *            weight of all that is kept
+ *   prob     its share of that weight, the q(d) of a draft
+ *   kept     how many tokens are kept
+ *
+ * The filtered rows, with the same temperature, are logits of the law that was
+ * sampled, for spec_verify_linear as draft or as target. Weights are summed exactly as
+ * integers of about 2^-61 of their sum, each within 2^-38 of itself, so that results
+ * do not go by the order of sums; a weight below 2^-62 counts as none.
+ *
+ *   logits    [R, V] (dt), 16-byte aligned, rows contiguous. -inf is a token that
+ *             a mask forbids.
+ *   cu_rows   [B+1] int32: request b owns rows cu_rows[b] .. cu_rows[b+1]-1,
+ *             cu_rows[0] = 0, cu_rows[B] = R. NULL: a row for each request, B = R.
+ *   params    see above; NULL: the plain softmax.
+ *   uniform   [R] f32, 0 <= u < 1. NULL: no token is drawn (tokens, prob NULL).
+ *   tokens    [R] int32; prob, kept: [R], each may be NULL.
+ *   filtered  [R, V] (dt), 16-byte aligned, or NULL: apart from `logits`, or the
+ *             same pointer.
+ *
+ * A row with a parameter or a u outside its range, with a NaN or +inf, or without a
+ * logit above -inf has token -1, prob 0, kept 0 and a filtered row of -inf, and the status
+ * word reads SPEC_ERR_INVALID_ARG with a row as its detail; the other rows are as
+ * they should. After bad offsets no row of a request is certain.
+ */
+int spec_sample(const void *logits, int dt, int R, int V, const int32_t *cu_rows,
+                int B, const spec_sampling *params, const float *uniform,
+                int32_t *tokens, float *prob, int32_t *kept, void *filtered,
+                void *workspace, size_t ws_bytes, spec_stream_t stream);
 
 #ifdef __cplusplus
 }

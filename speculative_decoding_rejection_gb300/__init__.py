@@ -26,6 +26,9 @@ __all__ = [
     "spec_distill_loss", "spec_distill_loss_workspace", "spec_adamw_table", "spec_adamw_step",
     "SPEC_ACT_NONE", "SPEC_ACT_SILU", "SPEC_ACT_GELU", "spec_head_forward",
     "spec_head_forward_workspace", "spec_head_backward", "spec_head_backward_workspace",
+    "spec_sample", "spec_sample_workspace", "SPEC_HEAD4_MAX_ROWS", "SpecHead4", "spec_head4_pack",
+    "spec_head4_quantize", "spec_head4_unpack", "spec_head4_forward", "spec_head4_forward_workspace",
+    "spec_grad_norm", "spec_clip_grads", "spec_grad_norm_workspace",
 ]
 
 SPEC_OK = 0
@@ -442,7 +445,9 @@ def spec_profile_pending() -> bool:
 # the operators around a draft head
 from .draft import (  # noqa: E402
     SIGS as _DRAFT_SIGS, SPEC_ACT_GELU, SPEC_ACT_NONE, SPEC_ACT_SILU, SPEC_ADAMW_BLOCK,
-    SpecAdamwTable, spec_adamw_step, spec_adamw_table, spec_distill_loss,
-    spec_distill_loss_workspace, spec_head_backward, spec_head_backward_workspace,
+    SPEC_HEAD4_MAX_ROWS, SpecAdamwTable, SpecHead4, spec_adamw_step, spec_adamw_table,
+    spec_clip_grads, spec_distill_loss, spec_distill_loss_workspace, spec_grad_norm,
+    spec_grad_norm_workspace, spec_head4_forward, spec_head4_forward_workspace, spec_head4_pack,
+    spec_head4_quantize, spec_head4_unpack, spec_head_backward, spec_head_backward_workspace,
     spec_head_forward, spec_head_forward_workspace, spec_process_logits,
-    spec_process_logits_workspace)
+    spec_process_logits_workspace, spec_sample, spec_sample_workspace)

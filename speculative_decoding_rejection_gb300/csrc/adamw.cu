@@ -14,7 +14,7 @@
 // encodes. e4m3 keeps the relative error of a value within 2^-4 down to
 // 2^-15 of its block's largest; v is held by its root, which halves the
 // exponent range that the codes have to span.
-#include "draft.cuh"
+#include "adamw.cuh"
 
 #include <algorithm>
 #include <cfloat>
@@ -25,41 +25,13 @@ namespace sv {
 namespace {
 
 constexpr int AD_THREADS = 256;
-constexpr int AD_ITEM = 4096;        // elements of a work item
 constexpr int AD_PER = AD_ITEM / AD_THREADS;
 // Persistent CTAs of the 8-bit step. 480M bf16 weights with masters: 2 take 1335 us,
 // 3 (80 registers) 1438 us, 4 (64 registers, spills) 1389 us.
 constexpr int AD_CTAS_PER_SM = 2;
-constexpr uint32_t AD_MAGIC = 0x41644d57u;
 constexpr float FP8_MAX = 448.f;     // largest e4m3 value
 constexpr float FP8_TINY = 0.001953125f;                 // smallest positive one, 2^-9
 constexpr float TINY_ABSMAX = 7.888609052210118e-31f;    // 2^-100
-
-struct AdTensor {
-  void *param;
-  const void *grad;
-  void *m, *v;
-  float *ms, *vs;
-  float *master;
-  long long n;
-  int bf16;      // weight and gradient type
-  int vec;       // every pointer suits 16-byte vectors
-};
-static_assert(sizeof(AdTensor) == 72, "table layout");
-
-struct AdHeader {      // first 64 bytes of a table
-  uint32_t magic;
-  int n_tensors;
-  long long n_items;
-  int state_bits;
-  int pad[11];
-};
-static_assert(sizeof(AdHeader) == 64, "table layout");
-
-struct AdItem {
-  int tensor;
-  int chunk;   // element offset / AD_ITEM
-};
 
 struct AdArgs {
   const AdHeader *table;

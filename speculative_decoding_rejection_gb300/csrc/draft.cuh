@@ -33,6 +33,28 @@ __device__ __forceinline__ uint32_t f32_to_bf16_bits(float v) {
   return f32x2_to_bf16x2(v, 0.f) & 0xffffu;
 }
 
+__device__ __forceinline__ float bf16_at(const __nv_bfloat16 *p, long long i) {
+  return bf16_bits_to_f32(GLD(reinterpret_cast<const uint16_t *>(p) + i));
+}
+__device__ __forceinline__ void bf16_to(__nv_bfloat16 *p, long long i, float v) {
+  GST(reinterpret_cast<uint16_t *>(p) + i, (uint16_t)f32_to_bf16_bits(v));
+}
+
+// Quotients within two units of the last place: results of bf16 do not see it,
+// and the exact division was a third of the backward pass's dz.
+__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// (1 + tanh u) / 2 = sigmoid(2u)
+__device__ __forceinline__ float gelu_gate(float z) {
+  return sigmoid(__fmul_rn(1.5957691216057308f, fmaf(__fmul_rn(0.044715f, z), __fmul_rn(z, z), z)));
+}
+// Products rounded by themselves: one fused with the residual's sum in some copies
+// of the epilogue would make the result depend on which of them runs.
+__device__ __forceinline__ float act_value(float z, int act) {
+  if (act == SPEC_ACT_SILU) return __fmul_rn(z, sigmoid(z));
+  if (act == SPEC_ACT_GELU) return __fmul_rn(z, gelu_gate(z));
+  return z;
+}
+
 // 16 bytes from `shift` bytes into the 32 of two vectors (0 <= shift < 16, whole
 // elements).
 __device__ __forceinline__ uint4 shift16(const uint4 &a, const uint4 &b, int shift) {

@@ -186,20 +186,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float *v) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Quotients within two units of the last place: results of bf16 do not see it,
-// and the exact division was a third of dz's instructions.
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
-// (1 + tanh u) / 2 = sigmoid(2u)
-__device__ __forceinline__ float gelu_gate(float z) {
-  return sigmoid(__fmul_rn(1.5957691216057308f, fmaf(__fmul_rn(0.044715f, z), __fmul_rn(z, z), z)));
-}
-// Products rounded by themselves: one fused with the residual's sum in some copies
-// of the epilogue would make the result depend on which of them runs.
-__device__ __forceinline__ float act_value(float z, int act) {
-  if (act == SPEC_ACT_SILU) return __fmul_rn(z, sigmoid(z));
-  if (act == SPEC_ACT_GELU) return __fmul_rn(z, gelu_gate(z));
-  return z;
-}
 __device__ __forceinline__ float act_slope(float z, int act) {
   if (act == SPEC_ACT_SILU) {
     const float s = sigmoid(z);
@@ -212,12 +198,6 @@ __device__ __forceinline__ float act_slope(float z, int act) {
     return s + s * z * ((1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * fminf(z * z, 1e10f)));
   }
   return 1.f;
-}
-__device__ __forceinline__ float bf16_at(const __nv_bfloat16 *p, long long i) {
-  return bf16_bits_to_f32(GLD(reinterpret_cast<const uint16_t *>(p) + i));
-}
-__device__ __forceinline__ void bf16_to(__nv_bfloat16 *p, long long i, float v) {
-  GST(reinterpret_cast<uint16_t *>(p) + i, (uint16_t)f32_to_bf16_bits(v));
 }
 __device__ __forceinline__ void unpack8(const uint4 &w, float *x) {
   x[0] = bf16lo(w.x), x[1] = bf16hi(w.x), x[2] = bf16lo(w.y), x[3] = bf16hi(w.y);

@@ -1,5 +1,6 @@
 """Binding of the operators around a draft head (include/specdraft.h): rules
-on the logits, the distillation loss, the head's products and AdamW. As in
+on the logits, sampling, the distillation loss, the head's products (its weights in
+bf16 or in 4 bits), the gradients' norm and AdamW. As in
 the package's other calls, the functions here only marshal arguments and raise
 on a non-zero return code; the kernels of libspecverify.so do the work.
 """
@@ -19,6 +20,7 @@ _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device
 SPEC_ADAMW_BLOCK = 256
 _INT_MAX = 0x7fffffff
 SPEC_ACT_NONE, SPEC_ACT_SILU, SPEC_ACT_GELU = 0, 1, 2
+SPEC_HEAD4_MAX_ROWS = 64
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
 
@@ -46,12 +48,19 @@ class SpecAdamwHyper(ctypes.Structure):
         ("step_dev", ctypes.c_void_p)]
 
 
-# the two records as they lie in memory, for calls (less host time than a
+class SpecSampling(ctypes.Structure):
+    """spec_sampling of include/specdraft.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("temperature", "min_p", "top_k", "top_p")]
+
+
+# the records as they lie in memory, for calls (less host time than a
 # Structure's fields)
 _RULES = struct.Struct("@14P4i")
 _HYPER = struct.Struct("@5dq3P")
+_SAMPLING = struct.Struct("@4P")
 assert _RULES.size == ctypes.sizeof(SpecLogitsRules)
 assert _HYPER.size == ctypes.sizeof(SpecAdamwHyper)
+assert _SAMPLING.size == ctypes.sizeof(SpecSampling)
 
 SIGS = {
     "spec_process_logits_workspace": (_sz, []),
@@ -69,6 +78,18 @@ SIGS = {
     "spec_head_backward": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _sz,
                                   _vp]),
     "spec_adamw_step": (_i32, [_vp, _i64, _i32, _vp, _vp, _sz, _vp]),
+    "spec_grad_norm_workspace": (_sz, []),
+    "spec_grad_norm": (_i32, [_vp, _i64, _i32, _i32, ctypes.c_double, _vp, _vp, _vp, _sz, _vp]),
+    "spec_clip_grads": (_i32, [_vp, _i64, _i32, _i32, ctypes.c_double, _vp, _vp, _vp, _sz, _vp]),
+    "spec_head4_packed_bytes": (_sz, [_i32, _i32]),
+    "spec_head4_pack": (_i32, [_vp, _i32, _i32, _vp, _vp]),
+    "spec_head4_quantize": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "spec_head4_unpack": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp]),
+    "spec_head4_forward_workspace": (_sz, [_i32, _i32, _i32]),
+    "spec_head4_forward": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp,
+                                  _sz, _vp]),
+    "spec_sample_workspace": (_sz, [_i32, _i32]),
+    "spec_sample": (_i32, [_vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 
 
@@ -250,6 +271,51 @@ def spec_process_logits(logits, cu_rows, *, max_rows: int, history=None, cu_hist
     return out, ws
 
 
+# ---------------------------------------------------------------- sampling
+def spec_sample_workspace(R: int, V: int) -> int:
+    return int(_sv.lib().spec_sample_workspace(R, V))
+
+
+def spec_sample(logits, uniform, cu_rows=None, *, temperature=None, top_k=None, top_p=None, min_p=None,
+                want_kept=False, want_filtered=False, workspace=None, out=None, stream=None):
+    """A token of each row's law after min-p, top-k and top-p by the random numbers
+    `uniform` [R] (None: no token is drawn), each request's rows with its parameters
+    (cu_rows None: a request for each row). `want_kept` returns the number of tokens
+    that the law keeps, `want_filtered` the rows with the others at -inf: logits of that
+    law, for spec_verify_linear. `out` is the four results' tensors (None for what is
+    not wanted); its last may be `logits` itself. See include/specdraft.h for the
+    semantics.
+
+    Returns (tokens [R] int32, prob [R] f32, kept [R] int32, filtered [R, V],
+    workspace), None for what is not wanted.
+    """
+    R, V = logits.shape
+    B = R if cu_rows is None else cu_rows.numel() - 1
+    dev, i32, f32 = _device("logits", logits), torch.int32, torch.float32
+    tokens, prob, kept, filtered = (None,) * 4 if out is None else out
+    used = () if stream is None else (logits, uniform, cu_rows, temperature, top_k, top_p, min_p, tokens,
+                                      prob, kept, filtered, workspace)
+    with _Call(dev, stream, used) as call:
+        ws, ws_at, ws_bytes = _scratch(256, dev, workspace)
+        if out is None:
+            if uniform is not None:
+                tokens = torch.empty(R, dtype=i32, device=logits.device)
+                prob = torch.empty(R, dtype=f32, device=logits.device)
+            kept = torch.empty(R, dtype=i32, device=logits.device) if want_kept else None
+            filtered = torch.empty_like(logits, memory_format=torch.contiguous_format) if want_filtered else None
+        law = _SAMPLING.pack(
+            _arg("temperature", temperature, f32, B, dev) or 0, _arg("min_p", min_p, f32, B, dev) or 0,
+            _arg("top_k", top_k, i32, B, dev) or 0, _arg("top_p", top_p, f32, B, dev) or 0)
+        code = _sv.lib().spec_sample(
+            _arg("logits", logits, logits.dtype, 0, dev), _f32_or_bf16(logits), R, V,
+            _arg("cu_rows", cu_rows, i32, 1, dev), B, law, _arg("uniform", uniform, f32, R, dev),
+            _arg("tokens", tokens, i32, R, dev), _arg("prob", prob, f32, R, dev),
+            _arg("kept", kept, i32, R, dev), _matrix("filtered", filtered, logits.dtype, R, V, dev),
+            ws_at, ws_bytes, call.raw)
+    _sv._check(code, "spec_sample")
+    return tokens, prob, kept, filtered, ws
+
+
 # ------------------------------------------------------- distillation loss
 def spec_distill_loss_workspace(R_d: int, V: int) -> int:
     return int(_sv.lib().spec_distill_loss_workspace(R_d, V))
@@ -370,6 +436,120 @@ def spec_head_backward(dy, x, weight, pre=None, *, act: int = SPEC_ACT_NONE, wan
     return dx, dw, db, ws
 
 
+# ------------------------------------------ a head's weight held in 4 bits
+class SpecHead4:
+    """A weight [N, K] in 4 bits as spec_head4_forward reads it: packed codes, bf16
+    scales [N, ceil(K / group)] and zeros (uint8, the same shape, or None)."""
+
+    __slots__ = ("packed", "scales", "zeros", "N", "K", "group")
+
+    def __init__(self, packed, scales, zeros, N, K, group):
+        self.packed, self.scales, self.zeros, self.N, self.K, self.group = packed, scales, zeros, N, K, group
+
+
+def _head4_packed(N, K, dev):
+    nbytes = int(_sv.lib().spec_head4_packed_bytes(N, K))
+    if nbytes == 0:
+        raise _sv.SpecError(_sv.SPEC_ERR_INVALID_ARG, "spec_head4_packed_bytes")
+    return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+
+
+def _head4_groups(K, group):
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    return -(-K // group)
+
+
+def spec_head4_pack(codes, scales, zeros=None, *, K: int, group: int, stream=None) -> SpecHead4:
+    """A weight of given codes [N, ceil(K / 2)] (uint8, the code of an even column in the
+    low 4 bits), bf16 scales [N, ceil(K / group)] and zeros (uint8, 0 .. 15, the same
+    shape; None: 8), laid out once for spec_head4_forward. The scales and zeros are
+    kept, not copied. See include/specdraft.h."""
+    N, G, dev = codes.shape[0], _head4_groups(K, group), _device("codes", codes)
+    if tuple(codes.shape) != (N, -(-K // 2)):
+        raise ValueError(f"codes must be [N, {-(-K // 2)}]")
+    for name, t, dtype in (("scales", scales, torch.bfloat16), ("zeros", zeros, torch.uint8)):
+        _arg(name, t, dtype, N * G, dev)
+        if t is not None and tuple(t.shape) != (N, G):
+            raise ValueError(f"{name} must be [{N}, {G}]")
+    with _Call(dev, stream, (codes, scales, zeros)) as call:
+        packed = _head4_packed(N, K, dev)
+        code = _sv.lib().spec_head4_pack(_arg("codes", codes, torch.uint8, 0, dev), N, K, packed.data_ptr(),
+                                         call.raw)
+    _sv._check(code, "spec_head4_pack")
+    return SpecHead4(packed, scales, zeros, N, K, group)
+
+
+def spec_head4_quantize(weight, *, group: int, workspace=None, out=None, stream=None):
+    """A bf16 weight [N, K] in 4 bits with a scale per `group` columns, rounded to the
+    nearest. `out` is a SpecHead4 of the same sizes without zeros to be written anew (a
+    head that learns while it serves). See include/specdraft.h.
+
+    Returns (SpecHead4, workspace)."""
+    N, K = weight.shape
+    G, dev, bf = _head4_groups(K, group), _device("weight", weight), torch.bfloat16
+    if out is not None and ((out.N, out.K, out.group) != (N, K, group) or out.zeros is not None):
+        raise ValueError("out is a weight of other sizes, or with zeros")
+    with _Call(dev, stream, (weight, workspace) if out is None else (weight, workspace, out.packed,
+                                                                    out.scales)) as call:
+        ws, ws_at, ws_bytes = _scratch(256, dev, workspace)
+        if out is None:
+            out = SpecHead4(_head4_packed(N, K, dev), torch.empty(N, G, dtype=bf, device=weight.device), None,
+                            N, K, group)
+        code = _sv.lib().spec_head4_quantize(
+            _arg("weight", weight, bf, 0, dev), N, K, group, _arg("out.packed", out.packed, torch.uint8, 0, dev),
+            _arg("out.scales", out.scales, bf, N * G, dev), ws_at, ws_bytes, call.raw)
+    _sv._check(code, "spec_head4_quantize")
+    return out, ws
+
+
+def spec_head4_unpack(weight, *, out=None, stream=None):
+    """The values of a weight in 4 bits, rounded to bf16 [N, K]: for calls of more than
+    SPEC_HEAD4_MAX_ROWS rows (spec_head_forward) and for gradients."""
+    dev, bf = _device("weight", weight.packed), torch.bfloat16
+    G = _head4_groups(weight.K, weight.group)
+    with _Call(dev, stream, (weight.packed, weight.scales, weight.zeros, out)) as call:
+        if out is None:
+            out = torch.empty(weight.N, weight.K, dtype=bf, device=weight.packed.device)
+        code = _sv.lib().spec_head4_unpack(
+            _arg("packed", weight.packed, torch.uint8, 0, dev),
+            _arg("scales", weight.scales, bf, weight.N * G, dev),
+            _arg("zeros", weight.zeros, torch.uint8, weight.N * G, dev), weight.N, weight.K, weight.group,
+            _matrix("out", out, bf, weight.N, weight.K, dev), call.raw)
+    _sv._check(code, "spec_head4_unpack")
+    return out
+
+
+def spec_head4_forward_workspace(M: int, N: int, K: int) -> int:
+    return int(_sv.lib().spec_head4_forward_workspace(M, N, K))
+
+
+def spec_head4_forward(x, weight, bias=None, residual=None, *, act: int = SPEC_ACT_NONE, workspace=None,
+                       out=None, stream=None):
+    """y = act(x weight^T + bias) + residual for up to SPEC_HEAD4_MAX_ROWS rows x [M, K]
+    and a SpecHead4 weight. See include/specdraft.h for the semantics.
+
+    Returns (y [M, N], workspace).
+    """
+    M, K = x.shape
+    N, G = weight.N, -(-weight.K // weight.group)
+    if K != weight.K:
+        raise ValueError(f"x must be [M, {weight.K}]")
+    dev, bf = _device("x", x), torch.bfloat16
+    used = () if stream is None else (x, weight.packed, weight.scales, weight.zeros, bias, residual, out, workspace)
+    with _Call(dev, stream, used) as call:
+        ws, ws_at, ws_bytes = _scratch(256, dev, workspace)
+        if out is None:
+            out = torch.empty(M, N, dtype=bf, device=x.device)
+        code = _sv.lib().spec_head4_forward(
+            _arg("x", x, bf, 0, dev), _arg("packed", weight.packed, torch.uint8, 0, dev),
+            _arg("scales", weight.scales, bf, N * G, dev), _arg("zeros", weight.zeros, torch.uint8, N * G, dev),
+            _arg("bias", bias, bf, N, dev), _matrix("residual", residual, bf, M, N, dev), M, N, K, weight.group,
+            act, _matrix("out", out, bf, M, N, dev), ws_at, ws_bytes, call.raw)
+    _sv._check(code, "spec_head4_forward")
+    return out, ws
+
+
 # ------------------------------------------------------------------- AdamW
 class SpecAdamwTable:
     """The device table of spec_adamw_table, with the tensors it names (weights and
@@ -466,3 +646,48 @@ def spec_adamw_step(table, step: int = 1, *, lr: float, beta1: float = 0.9, beta
                                          hyper, ws_at, ws_bytes, call.raw)
     _sv._check(code, "spec_adamw_step")
     return ws
+
+
+# ------------------------------------------------- the norm of all gradients
+def spec_grad_norm_workspace() -> int:
+    return int(_sv.lib().spec_grad_norm_workspace())
+
+
+def _grad_norm(name, table, max_norm, inf, grad_scale, workspace, out, stream):
+    if table.followed:
+        table.check()
+    dev, f32 = table.data.get_device(), torch.float32
+    used = () if stream is None else (
+        table.data, grad_scale, workspace, out,
+        *(t for group in table.tensors if group is not None for t in group))
+    with _Call(dev, stream, used) as call:
+        ws, ws_at, ws_bytes = _scratch(0 if workspace is not None else spec_grad_norm_workspace(), dev, workspace)
+        if out is None:
+            out = torch.empty(2, dtype=f32, device=table.data.device)
+        code = getattr(_sv.lib(), name)(
+            table.data.data_ptr(), table.n_items, table.state_bits, int(inf), max_norm,
+            _arg("grad_scale", grad_scale, f32, 1, dev), _arg("out", out, f32, 2, dev), ws_at, ws_bytes, call.raw)
+    _sv._check(code, name)
+    return out, ws
+
+
+def spec_grad_norm(table, *, max_norm: float = float("inf"), inf=False, grad_scale=None, workspace=None,
+                   out=None, stream=None):
+    """The norm over all gradients of an AdamW table (the largest magnitude with `inf`)
+    after their multiplication by `grad_scale` (a one-element device tensor), and the factor that
+    clips them to max_norm: out[1:] is what spec_adamw_step takes as grad_scale. See
+    include/specdraft.h for the semantics.
+
+    Returns (out [2] f32: norm, factor; workspace).
+    """
+    return _grad_norm("spec_grad_norm", table, max_norm, inf, grad_scale, workspace, out, stream)
+
+
+def spec_clip_grads(table, *, max_norm: float, inf=False, grad_scale=None, workspace=None, out=None,
+                    stream=None):
+    """spec_grad_norm, with every gradient of the table multiplied by the factor in
+    place: a step behind it takes no grad_scale.
+
+    Returns (out [2] f32: norm, factor; workspace).
+    """
+    return _grad_norm("spec_clip_grads", table, max_norm, inf, grad_scale, workspace, out, stream)
