@@ -439,9 +439,9 @@ size_t spec_sample_workspace(int R, int V);
  *   kept     how many tokens are kept
  *
  * The filtered rows, with the same temperature, are logits of the law that was
- * sampled, for spec_verify_linear as draft or as target. Weights are summed exactly as
- * integers of about 2^-61 of their sum, each within 2^-38 of itself, so that results
- * do not go by the order of sums; a weight below 2^-62 counts as none.
+ * sampled, for spec_verify_linear as draft or as target. Weights are whole numbers of
+ * a small unit, whose sums are exact: results do not go by the order of sums, and no
+ * border is further than 2^-38 of the mass from where exact weights put it.
  *
  *   logits    [R, V] (dt), 16-byte aligned, rows contiguous. -inf is a token that
  *             a mask forbids.

@@ -157,3 +157,79 @@ def act_slope(z, name):
         t = np.tanh(c * (z + 0.044715 * z ** 3))
         return 0.5 * (1 + t) + 0.5 * z * (1 - t * t) * c * (1 + 3 * 0.044715 * z * z)
     return np.ones_like(z)
+
+
+# -------------------------------------------------------------- sampling
+def sample_row(z, u=None, T=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """One row's law and draw. Returns a dict: order (ids that are kept, by falling
+    logits, equal ones by rising id), law (their probabilities), token, prob, and the
+    distances of top-p's border (edge) and of u (edge_u) from the nearest sum of the law, as
+    a share of the mass (exact hits, which 64 bits decide, count as far)."""
+    z = np.asarray(z, np.float64)
+    ids = np.lexsort((np.arange(len(z)), -z))
+    ids = ids[z[ids] > NEG_INF]
+    edge = 1.0
+    if T < np.float32(0.05):
+        ids, law = ids[:1], np.ones(1)
+    else:
+        gap = z[ids] - z[ids[0]]
+        if min_p > 0:
+            least = T * np.log(min_p)
+            ids, gap = ids[gap >= least], gap[gap >= least]
+        if top_k > 0:
+            ids, gap = ids[:top_k], gap[:top_k]
+        w = np.exp(gap / T)
+        c = np.cumsum(w)
+        if top_p < 1:
+            n = max(1, int(np.sum(c - w < top_p * c[-1])))
+            edge = min(edge, _edge(c, top_p * c[-1]))
+            ids, w, c = ids[:n], w[:n], c[:n]
+        law = w / c[-1]
+    out = dict(order=ids, law=law, token=-1, prob=0.0, edge=edge, edge_u=1.0)
+    if u is not None:
+        c = np.cumsum(law)
+        at = min(int(np.sum(c <= u * c[-1])), len(ids) - 1)
+        out.update(token=int(ids[at]), prob=float(law[at]), edge_u=_edge(c, u * c[-1]))
+    return out
+
+
+def _edge(c, x):
+    d = np.abs(c - x) / c[-1]
+    return float(d[d > 0].min(initial=1.0))
+
+
+# ---------------------------------------------- weights held in 4 bits
+def to_bf16(x):
+    """The nearest value of bf16 (ties to even), as f64; x within its normal range."""
+    m, e = np.frexp(np.asarray(x, np.float64))
+    return np.ldexp(np.rint(m * 256) / 256, e)
+
+
+def quantize4(w, group):
+    """(codes [N, K], scales [N, G]) of a weight."""
+    N, K = w.shape
+    G = -(-K // group)
+    scales = np.zeros((N, G))
+    codes = np.full((N, K), 8)
+    for g in range(G):
+        part = np.asarray(w[:, g * group:(g + 1) * group], np.float64)
+        s = to_bf16(np.abs(part).max(1) / 7)
+        s[s < 2.0 ** -126] = 0
+        scales[:, g] = s
+        on = s > 0
+        codes[on, g * group:g * group + part.shape[1]] = 8 + np.clip(np.rint(part[on] / s[on, None]), -7, 7)
+    return codes, scales
+
+
+def dequantize4(codes, scales, zeros, group):
+    K = codes.shape[1]
+    z = 8.0 if zeros is None else np.repeat(np.asarray(zeros, np.float64), group, 1)[:, :K]
+    return (np.asarray(codes, np.float64) - z) * np.repeat(np.asarray(scales, np.float64), group, 1)[:, :K]
+
+
+# ------------------------------------------- the norm of all gradients
+def grad_norm(grads, max_norm=np.inf, scale=1.0, inf=False):
+    """(norm, factor) of a list of arrays."""
+    flat = np.concatenate([np.asarray(g, np.float64).reshape(-1) for g in grads] + [np.zeros(1)])
+    norm = abs(scale) * (np.abs(flat).max() if inf else np.sqrt(np.sum(flat * flat)))
+    return norm, scale * (np.minimum(1.0, max_norm / (norm + 1e-6)))

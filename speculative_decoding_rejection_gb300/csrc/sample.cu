@@ -185,15 +185,17 @@ __device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// 2^(-(m - z) c) in units of 2^-S, S <= 61. The difference and its product with c are
-// taken in two words each: t is right within 2^-41 (63 at most, its second word under
-// 2^-18 and rounded twice) and the units of 2^-44, the fixed-point product within a few
-// units of 2^-44, so a weight within 2^-40 of itself and its own rounding to 2^-S.
-__device__ __forceinline__ unsigned long long weight(const unsigned long long *pow2, float m, float ch,
-                                                     float cl, int S, float z) {
+// 2^-t for t = (m - z) c, as a fraction in units of 2^-62 (over a half) and a power: the
+// result is fraction 2^-power, 0 for t of 63 and more. The difference and its product with c are
+// taken in two words each: t is right within 2^-41 (its second word is under 2^-18 and
+// rounded twice) and the units of 2^-44, the fixed-point product within a few units of
+// 2^-44, so a weight within 2^-40 of itself.
+__device__ __forceinline__ unsigned long long fraction(const unsigned long long *pow2, float m, float ch, float cl,
+                                                       float z, int &power) {
   const float dh = m - z, bb = dh - m;
   const float dl = (m - (dh - bb)) - (z + bb);
   const float ph = dh * ch;
+  power = 0;
   if (!(ph < 63.f)) return 0;
   const float pl = fmaf(dh, ch, -ph) + fmaf(dh, cl, dl * ch);
   const long long t = __float2ll_rn(ph * 17592186044416.f) + __float2ll_rn(pl * 17592186044416.f);
@@ -205,8 +207,23 @@ __device__ __forceinline__ unsigned long long weight(const unsigned long long *p
   const uint32_t e = y - (q >> 13) + (((__umulhi(q, y) >> 16) * 43u) >> 16);
   unsigned long long w = __umul64hi(pow2[(f >> 38) & 63], pow2[64 + ((f >> 32) & 63)]);   // in 2^-62
   w -= __umul64hi(w, (unsigned long long)e << 20);
-  const int shift = 62 - S + (int)(f >> 44);
+  power = (int)(f >> 44);
+  return w;
+}
+// The weight rounded to units of 2^-S, S <= 61.
+__device__ __forceinline__ unsigned long long weight(const unsigned long long *pow2, float m, float ch, float cl,
+                                                     int S, float z) {
+  int power;
+  const unsigned long long w = fraction(pow2, m, ch, cl, z, power);
+  const int shift = 62 - S + power;
   return shift < 64 ? (w + (1ull << (shift - 1))) >> shift : 0ull;
+}
+// Its share of a mass in units of 2^-S.
+__device__ __forceinline__ float share(const unsigned long long *pow2, float m, float ch, float cl, int S, float z,
+                                       unsigned long long mass) {
+  int power;
+  const unsigned long long w = fraction(pow2, m, ch, cl, z, power);
+  return (float)(ldexp((double)w, S - 62 - power) / (double)mass);
 }
 
 // The first whole number that is not below x p, and what u falls on: the mass has to
@@ -479,7 +496,7 @@ __device__ void decide_values(SampleSmem &s, float m) {
       const unsigned long long w = max(1ull, d.mass / max(1u, d.cnt));
       v.tok = bin_value(max(d.bin, 0));
       v.tok_at = (int)div_up(d.target - d.c0, w) - 1;
-      v.prob = (float)((double)w / (double)kept_mass);
+      v.prob = share(s.pow2, m, law.ch, law.cl, S, v.tok, kept_mass);
     }
     if (t == 0) s.verdict = v;
   }
@@ -668,7 +685,7 @@ __device__ __noinline__ void decide_divisions(cg::cluster_group &cluster, Sample
     const unsigned long long w = max(1ull, f.mass / max(1u, f.cnt));
     v.tok = of_key(top - d);
     v.tok_at = (int)div_up(f.target - f.c0, w) - 1;
-    v.prob = (float)((double)w / (double)f.total);
+    v.prob = share(s.pow2, m, law.ch, law.cl, l.S, v.tok, f.total);
     if (v.kept < 0) v.kept = (int)f.total_n;
   } else if (v.kept < 0) {
     l.masses = 0, l.first = 0, l.shift = level_shift((unsigned long long)l.last + 1);
@@ -722,6 +739,12 @@ __global__ void __launch_bounds__(SA_THREADS, 2) k_sample(const SampleArgs a) {
   constexpr bool BF = sizeof(E) == 2;
   const int r = blockIdx.x / C;
 
+  if (a.cu_rows != nullptr && blockIdx.x == 0) {   // offsets that fall belong to no row
+    bool fall = false;
+    for (int i = t; i < a.B; i += SA_THREADS) fall |= GLDG(a.cu_rows + i) > GLDG(a.cu_rows + i + 1);
+    if (fall || (t == 0 && (GLDG(a.cu_rows) != 0 || GLDG(a.cu_rows + a.B) != a.R)))
+      set_status(a.hdr, SPEC_ERR_INVALID_ARG, -1);
+  }
   // the law, by a thread of the last warp while the others clear the histogram
   if (t == SA_THREADS - 1) s.law = law_of(a, r), s.tiny = 0;
   if (t < 128) s.pow2[t] = g_pow2[t];
