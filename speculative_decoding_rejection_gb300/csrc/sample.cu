@@ -11,45 +11,53 @@
 //     bits of the fraction each) and a cubic in the 32 bits left, all in 64-bit
 //     fixed point. Masses are sums of these, the same in whatever order they are taken.
 //
-// One cluster works on a row, each CTA on a slice of it. The tokens are taken in the
-// order of falling logits, so that the histogram of the row's values is all that the
-// borders and the drawn value need:
+// One cluster works on a row, each CTA on a slice of it, in the order of falling logits.
 //
-//   bf16  A row has few distinct values. The row is read once from HBM into a histogram
-//         of counts in shared memory with a bin for each value of magnitude 2^-21 to
-//         2^10; one weight per bin and a scan over the bins give min-p's, top-k's and
-//         top-p's borders, the mass that is kept and the value that u falls on. A row
-//         whose decisions need a value outside that range goes the way of f32.
-//   f32   Bins of the distance below the row's largest key (2048 of them), counts and
-//         masses; the bin a border falls in is divided again until it holds one value.
-//         The passes after the first come from L2.
-//
-// Which of the equal values it is goes by id: the matches are counted per chunk of the
-// row, in the chunks whose largest logit reaches the value.
+//   Lists. Where min-p or top-k bounds the law, the row is read once from HBM and the
+//   tokens above the border (min-p's below the largest logit so far; for top-k the k-th
+//   largest of the threads' first maxima) go to a list in shared memory. Counts and
+//   masses of 2048 equal intervals of the list's logits, and a look at the tokens of the
+//   one interval that a border falls in, give every border and the token.
+//   Values, bf16. A row has few distinct values: a histogram of counts in shared memory
+//   has a bin for each value of magnitude 2^-21 to 2^11; one weight per bin and a scan
+//   over the bins give the borders and the value that u falls on. A row whose decisions
+//   need a value outside that range goes by divisions.
+//   Divisions. Bins of the distance below the row's largest key (2048 of them), counts
+//   and masses; the bin a border falls in is divided again until it holds one value.
+//   The passes after the first come from L2.
+//   Which of the equal values it is goes by id there: the matches are counted per chunk
+//   of the row, in the chunks whose largest logit reaches the value.
 #include "draft.cuh"
 
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <climits>
 
 namespace sv {
 namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int SA_THREADS = 512;
+constexpr int SA_THREADS = 256;
 constexpr int SA_WARPS = SA_THREADS / 32;
-constexpr int SA_BINS = 8192;          // bf16: a bin for each value, 16 per thread
-constexpr int SA_LEVEL = 2048;         // f32: bins of a division, 4 per thread
-constexpr int SA_CHUNKS = 512;         // chunks of a CTA's slice
+constexpr int SA_LEVEL = 2048;         // bins of a division, intervals of a list
+constexpr int SA_CHUNKS = 256;         // chunks of a CTA's slice
+constexpr int SA_CTAS_PER_SM = 3;
+constexpr int SA_ENTRIES = 6144;       // values that a histogram's law may have
+constexpr int SA_LIST = 2560;          // tokens of a list
+constexpr int SA_FULL = 1536;          // a row that short goes to it whole
+constexpr int SA_NEAR = SA_THREADS;    // tokens that are ranked one by one
+constexpr int SA_TOP_K = 256;          // top-k up to which the threads' maxima give a border
+static_assert(SA_TOP_K <= SA_THREADS && SA_TOP_K <= SA_NEAR, "top-k's border and its tokens");
 constexpr int SA_MAX_CLUSTER = 8;
-// bf16 magnitudes 2^-21 .. 2^10 have bins of their own: 3968 of each sign. Bin 0 and the
-// last one hold what is larger, the two in the middle zero and what is smaller.
-constexpr int SA_LO = (127 - 21) << 7, SA_HI = (127 + 10) << 7;
-constexpr int SA_MAGS = SA_HI - SA_LO;
-constexpr int SA_ZERO = SA_MAGS + 1;             // bin of zero
-constexpr int SA_LAST = 2 * SA_MAGS + 3;         // bin of what is below -2^10
-static_assert(SA_LAST < SA_BINS, "bins");
+// bf16 magnitudes 2^-21 .. 2^11 have bins of their own: 4096 of each sign, index
+// sign << 12 | (bits - SA_LO). One more for zero, one for what is below -2^11.
+constexpr int SA_LO = (127 - 21) << 7;
+constexpr int SA_BINS = 8192, SA_ZERO = SA_BINS, SA_LAST = SA_BINS + 1;
+constexpr int SA_ROWS = 33;            // a warp's places in the order of falling values, by 32
+constexpr int SA_ORDER = SA_ROWS * 32 * SA_WARPS;   // all of them; behind the last bin's they are empty
+static_assert(SA_ORDER >= SA_BINS + 2, "places");
 
 // 2^(-i/64) and 2^(-i/4096) in units of 2^-63, by the definition.
 __device__ const uint64_t g_pow2[128] = {
@@ -121,46 +129,71 @@ union Vec {
 
 // The row's law before any token is looked at.
 struct Law {
-  float ch, cl;        // log2(e) / T in two words
-  float top_p, u;
-  double log_min;      // T ln(min_p), -inf without
-  int top_k;           // 0: none
+  float ch, cl;               // log2(e) / T in two words
+  float top_p;
+  unsigned long long p, u;    // top_p and u in units of 2^-64
+  double log_min;             // T ln(min_p), -inf without
+  float head;                 // how far below the largest logit a list goes
+  int top_k;                  // 0: none
   int greedy, bad, draw;
+  int list, ranked;           // the row goes by a list, and top-k bounds it
 };
 
 // What the row's leader says to the other CTAs of the cluster.
 struct Found {
-  unsigned long long c0, mass;   // mass before the bin, of the bin
+  unsigned long long c0, mass;   // mass before the entry, of the entry
+  unsigned long long w;          // weight of one of its tokens
   unsigned long long total;      // of the level
   unsigned long long target;
-  uint32_t n0, cnt;              // tokens before the bin, in it
+  uint32_t n0, cnt;              // tokens before the entry, in it
   uint32_t total_n;
-  int bin;                       // -1: the target lies behind the last one
+  int at;                        // the entry; -1: the target lies behind the last one
 };
 struct Verdict {
   float tok, cut;      // the drawn value, the last value that is kept
   int tok_at;          // which of its equals it is
+  int tok_id;          // the token, -1: not known yet
   int cut_n;           // how many of the last value's are kept
-  int cut_whole;       // all of them
+  int cut_id;          // the last of them, -1: not known yet
   int kept;
   float prob;
-  int bad, slow;
+  int slow;            // the next way has to decide
 };
 
 struct SampleSmem {
-  uint32_t hist[SA_BINS];          // or cnt[SA_LEVEL], lo[SA_LEVEL], hi[SA_LEVEL]
+  union {
+    struct {
+      uint32_t hist[SA_BINS + 32];
+      uint16_t bins[SA_ENTRIES];            // those of the histogram that hold tokens of the law
+    };
+    struct {
+      unsigned long long list[SA_LIST];     // key of the logit, then ~id: falls in the tokens' order
+      struct {                              // counts and masses of intervals or of a division
+        uint32_t cnt[SA_LEVEL], lo[SA_LEVEL], hi[SA_LEVEL];
+      } level;
+    };
+  };
+  unsigned long long near[SA_NEAR], near_w[SA_NEAR];
   unsigned long long pow2[128];
   unsigned long long pre_mass[SA_THREADS + 1];
   uint32_t pre_n[SA_THREADS + 1];
   float cmax[SA_CHUNKS];
   uint32_t tok_n[SA_CHUNKS], cut_n[SA_CHUNKS];   // matches of a chunk, then those before it
   unsigned long long warp_mass[SA_WARPS];
-  uint32_t warp_n[SA_WARPS];
-  float warp_f[SA_WARPS];
-  float cta_max, bound;
-  uint32_t cta_tok, cta_cut;       // matches of this CTA's slice
-  uint32_t tok_end;                // and of those before it
-  int tiny;                        // a value between 0 and 2^-21 was seen
+  uint32_t warp_n[SA_WARPS], warp_k[SA_WARPS];
+  float warp_f[SA_WARPS], warp_low[SA_WARPS];
+  float cta_max, cta_sum;          // this CTA's slice: the largest logit, the f32 sum of weights by it
+  uint32_t cta_tok, cta_cut;       // its matches
+  uint32_t tok_end, cut_end;       // and with those before it
+  uint32_t run;                    // key of the largest logit so far
+  int n_list, cut_short, n_near;
+  unsigned long long key, key_w, key_before;   // the token told apart, its weight, the mass before it
+  uint32_t key_rank;                           // in its interval
+  float border;                    // top-k's, of this CTA
+  int part_bin;                    // the value that top-k cuts, and what it keeps of it
+  uint32_t part_n;
+  int tok_id, cut_id;
+  int odd;                         // a value without a bin was seen: between 0 and 2^-21, or from 2^11 on
   Law law;
   Found found;
   Verdict verdict;
@@ -218,25 +251,32 @@ __device__ __forceinline__ unsigned long long weight(const unsigned long long *p
   const int shift = 62 - S + power;
   return shift < 64 ? (w + (1ull << (shift - 1))) >> shift : 0ull;
 }
-// Its share of a mass in units of 2^-S.
+// Its share of a mass in units of 2^-S, a quotient of two words each.
 __device__ __forceinline__ float share(const unsigned long long *pow2, float m, float ch, float cl, int S, float z,
                                        unsigned long long mass) {
   int power;
   const unsigned long long w = fraction(pow2, m, ch, cl, z, power);
-  return (float)(ldexp((double)w, S - 62 - power) / (double)mass);
+  const float a = (float)w, b = (float)mass;
+  const float a2 = (float)(long long)(w - (unsigned long long)a), b2 = (float)(long long)(mass - (unsigned long long)b);
+  const float q = a / b, r = fmaf(-q, b, a) + fmaf(-q, b2, a2);
+  return ldexpf(q + r / b, S - 62 - power);
 }
 
 // The first whole number that is not below x p, and what u falls on: the mass has to
-// exceed floor(x u).
-__device__ __forceinline__ unsigned long long reach(unsigned long long x, float p) {
-  return __double2ull_ru((double)x * (double)p);
+// exceed floor(x u). p, u in units of 2^-64.
+__device__ __forceinline__ unsigned long long reach(unsigned long long x, unsigned long long p) {
+  return max(1ull, __umul64hi(x, p) + (x * p != 0));
 }
-__device__ __forceinline__ unsigned long long beyond(unsigned long long x, float u) {
-  const unsigned long long t = __double2ull_rd((double)x * (double)u);
-  return min(t, x - 1) + 1;
+__device__ __forceinline__ unsigned long long beyond(unsigned long long x, unsigned long long u) {
+  return __umul64hi(x, u) + 1;
 }
-__device__ __forceinline__ uint32_t div_up(unsigned long long a, unsigned long long b) {
-  return (uint32_t)((a + b - 1) / b);
+// ceil(a / b), at least 1 and at most n
+__device__ __forceinline__ uint32_t div_up(unsigned long long a, unsigned long long b, uint32_t n) {
+  if (n <= 1 || b == 0) return 1;
+  uint32_t q = (uint32_t)fminf((float)a / (float)b, (float)n);
+  while (q > 1 && (q - 1) * b >= a) --q;
+  while (q < n && q * b < a) ++q;
+  return max(q, 1u);
 }
 
 // -------------------------------------------------------- a row of a cluster
@@ -273,22 +313,30 @@ struct Row {
         if (p + i >= off && p + i < end) GST(out + p + i, x.e[i]);
     }
   }
+  // this lane's vectors of group g of chunk c, -inf where there are none
+  __device__ __forceinline__ void fetch(int c, int g, uint4 (&v)[U]) const {
+    constexpr int GROUP = U * 32 * PER;
+    const int at = (c0 + c) * chunk + g * GROUP, p = at + (threadIdx.x & 31) * PER;
+    if (c < nc && at >= off && at + GROUP <= end) {
+      const uint4 *q = reinterpret_cast<const uint4 *>(base + p);
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = GLD(q + u * 32);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = load(c < nc ? min(p + u * 32 * PER, end) : end);
+    }
+  }
   // f(vectors) for every group of U vectors of chunk c of this CTA: position of the
   // first one of this lane, the others 32 * PER apart
   template <class F>
   __device__ __forceinline__ void groups(int c, F f) const {
-    const int lane = threadIdx.x & 31;
-    const long long first = (long long)(c0 + c) * chunk;
-    for (int g = 0; g < chunk; g += U * 32 * PER) {
-      const long long at = first + g;
+    constexpr int GROUP = U * 32 * PER;
+    for (int g = 0; g < chunk / GROUP; ++g) {
+      const int at = (c0 + c) * chunk + g * GROUP;
       if (at >= end) break;
       uint4 v[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const long long p = at + (u * 32 + lane) * PER;
-        v[u] = p < end ? load((int)p) : load(end);
-      }
-      f((int)at + lane * PER, v);
+      fetch(c, g, v);
+      f(at + (int)(threadIdx.x & 31) * PER, v);
     }
   }
 };
@@ -307,199 +355,510 @@ __device__ __forceinline__ void block_scan(SampleSmem &s, uint32_t n, unsigned l
   }
   if (lane == 31) s.warp_n[warp] = sn, s.warp_mass[warp] = sm;
   __syncthreads();
-  uint32_t bn = 0;
-  unsigned long long bm = 0;
-  for (int w = 0; w < warp; ++w) bn += s.warp_n[w], bm += s.warp_mass[w];
+  uint32_t bn = lane < SA_WARPS ? s.warp_n[lane] : 0;
+  unsigned long long bm = lane < SA_WARPS ? s.warp_mass[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < SA_WARPS; o <<= 1) {
+    const uint32_t a = __shfl_up_sync(~0u, bn, o);
+    const unsigned long long b = __shfl_up_sync(~0u, bm, o);
+    if (lane >= o) bn += a, bm += b;
+  }
+  const uint32_t all_n = __shfl_sync(~0u, bn, SA_WARPS - 1);
+  const unsigned long long all_m = __shfl_sync(~0u, bm, SA_WARPS - 1);
+  bn = __shfl_sync(~0u, bn, max(warp - 1, 0)), bm = __shfl_sync(~0u, bm, max(warp - 1, 0));
+  if (warp == 0) bn = 0, bm = 0;
   s.pre_n[t] = bn + sn - n;
   s.pre_mass[t] = bm + sm - mass;
-  if (t == SA_THREADS - 1) s.pre_n[SA_THREADS] = bn + sn, s.pre_mass[SA_THREADS] = bm + sm;
+  if (t == 0) s.pre_n[SA_THREADS] = all_n, s.pre_mass[SA_THREADS] = all_m;
   __syncthreads();
 }
-__device__ __forceinline__ float block_sum(SampleSmem &s, float x) {
+// Sums over the block, the same in every thread.
+__device__ __forceinline__ void block_sums(SampleSmem &s, float &x, uint32_t &n, uint32_t &k) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-  if ((threadIdx.x & 31) == 0) s.warp_f[threadIdx.x >> 5] = x;
+  n = __reduce_add_sync(~0u, n);
+  k = __reduce_add_sync(~0u, k);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __syncthreads();
-  float r = 0.f;
+  if (lane == 0) s.warp_f[warp] = x, s.warp_n[warp] = n, s.warp_k[warp] = k;
+  __syncthreads();
+  x = lane < SA_WARPS ? s.warp_f[lane] : 0.f;
+  n = lane < SA_WARPS ? s.warp_n[lane] : 0;
+  k = lane < SA_WARPS ? s.warp_k[lane] : 0;
 #pragma unroll
-  for (int w = 0; w < SA_WARPS; ++w) r += s.warp_f[w];
-  return r;
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+  n = __reduce_add_sync(~0u, n);
+  k = __reduce_add_sync(~0u, k);
 }
 
-// By one warp: the bin in which the counts (by_n) or masses before and in it first reach
-// the target (at least 1). of(bin, n before it) gives the bin's count and mass; PT bins
-// per thread of the scan.
-template <int PT, class F>
-__device__ Found find_bin(const SampleSmem &s, unsigned long long target, bool by_n, F of) {
+// By one warp: the entry in which the counts (by_n) or masses before and in it first reach
+// the target (at least 1). of(entry) gives the entry's count and the weight of one of its
+// tokens (nothing for -1 and behind the last); a thread of the scan had `per` <= 32 entries.
+template <class F>
+__device__ Found find_entry(const SampleSmem &s, unsigned long long target, bool by_n, int per, F of) {
   const int lane = threadIdx.x & 31;
   Found r{};
   r.target = target;
   r.total = s.pre_mass[SA_THREADS];
   r.total_n = s.pre_n[SA_THREADS];
-  r.bin = -1;
+  r.at = -1;
   if (target > (by_n ? (unsigned long long)r.total_n : r.total)) return r;
   int lo = 0, hi = SA_THREADS;   // before `lo` less than the target, before `hi` no less
   while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if ((by_n ? (unsigned long long)s.pre_n[mid] : s.pre_mass[mid]) < target) lo = mid;
-    else hi = mid;
+    const int step = (hi - lo + 31) / 32, mid = lo + step * lane;
+    const bool less = mid < hi && (by_n ? (unsigned long long)s.pre_n[mid] : s.pre_mass[mid]) < target;
+    const int k = 31 - __clz(__ballot_sync(~0u, less || lane == 0));
+    lo += step * k;
+    hi = min(hi, lo + step);
   }
-  const unsigned long long base_m = s.pre_mass[lo];
   uint32_t cnt = 0;
-  unsigned long long mass = 0;
-  // counts first: what is behind the last kept token has no mass
-  uint32_t raw = lane < PT ? s.pre_n[lo] : 0;
-  of(lane < PT ? lo * PT + lane : -1, raw, cnt, mass);
+  unsigned long long w = 0;
+  of(lane < per ? lo * per + lane : -1, cnt, w);
+  const unsigned long long mass = cnt * w;
   uint32_t sn = cnt;
   unsigned long long sm = mass;
 #pragma unroll
-  for (int o = 1; o < PT; o <<= 1) {
+  for (int o = 1; o < 32; o <<= 1) {
     const uint32_t a = __shfl_up_sync(~0u, sn, o);
     const unsigned long long b = __shfl_up_sync(~0u, sm, o);
     if (lane >= o) sn += a, sm += b;
   }
-  const unsigned long long have = by_n ? (unsigned long long)(s.pre_n[lo] + sn) : base_m + sm;
-  const uint32_t hit = __ballot_sync(~0u, lane < PT && have >= target);
-  const int at = __ffs(hit) - 1;
-  r.bin = lo * PT + at;
+  sn += s.pre_n[lo], sm += s.pre_mass[lo];
+  const uint32_t hit = __ballot_sync(~0u, lane < per && (by_n ? (unsigned long long)sn : sm) >= target);
+  const int at = max(__ffs(hit) - 1, 0);
+  r.at = lo * per + at;
   r.cnt = __shfl_sync(~0u, cnt, at);
+  r.w = __shfl_sync(~0u, w, at);
   r.mass = __shfl_sync(~0u, mass, at);
-  r.n0 = s.pre_n[lo] + __shfl_sync(~0u, sn, at) - r.cnt;
-  r.c0 = base_m + __shfl_sync(~0u, sm, at) - r.mass;
+  r.n0 = __shfl_sync(~0u, sn, at) - r.cnt;
+  r.c0 = __shfl_sync(~0u, sm, at) - r.mass;
   return r;
 }
 
-// The largest power that keeps a mass of z below 2^61 in units of 2^-S.
+// The largest S that keeps a mass of z below 2^62 in units of 2^-S.
 __device__ __forceinline__ int unit_of(float z) {
   int e;
-  frexpf(fmaxf(z * 1.01f, 1.f), &e);   // z < 2^e
-  return 61 - e;
+  frexpf(fmaxf(z * 1.01f, 1.f), &e);   // z < 2^e, e >= 1
+  return 62 - e;
 }
 
 // ------------------------------------------------------------- bf16: by values
 __device__ __forceinline__ float bin_value(int bin) {
-  const int mag = bin <= SA_ZERO ? SA_ZERO - bin : bin - SA_ZERO - 1;
-  const uint32_t b = mag == 0 ? 0u : (uint32_t)(mag + SA_LO - 1);
-  return __uint_as_float((b | (bin > SA_ZERO ? 0x8000u : 0u)) << 16);
+  if (bin >= SA_BINS) return bin == SA_ZERO ? 0.f : -2048.f;
+  return __uint_as_float((uint32_t)(((bin & 4095) + SA_LO) | (bin >> 12) << 15) << 16);
 }
+// The bin at a place of the falling order, -1 behind the last.
+__device__ __forceinline__ int bin_at(int place) {
+  return place < 4096 ? 4095 - place : place == 4096 ? SA_ZERO : place <= SA_BINS ? place - 1 : place == SA_LAST ? SA_LAST : -1;
+}
+// Values without a bin of their own.
 __device__ __noinline__ void count_rare(SampleSmem &s, uint32_t b) {
   const uint32_t a = b & 0x7fffu;
   if (b == 0xff80u) return;   // -inf takes no part
-  if (a == 0) {
-    atomicAdd(&s.hist[SA_ZERO], 1u);
-  } else if (a < SA_LO) {
-    s.tiny = 1;
-    atomicAdd(&s.hist[SA_ZERO], 1u);
-  } else {
-    atomicAdd(&s.hist[b & 0x8000u ? SA_LAST : 0], 1u);
+  if (a == 0) atomicAdd(&s.hist[SA_ZERO], 1u);
+  else if (a < SA_LO || (b & 0x8000u) == 0) s.odd = 1;
+  else atomicAdd(&s.hist[SA_LAST], 1u);
+}
+// Two values at once: both magnitudes less SA_LO, with bit 15 set where that is not
+// negative, are in range where the four leading bits are 8; the sign goes to bit 12.
+__device__ __forceinline__ void count_two(SampleSmem &s, uint32_t w) {
+  const uint32_t d = (w & 0x7fff7fffu) + (0x8000u - SA_LO) * 0x10001u;
+  const uint32_t out = (d ^ 0x80008000u) & 0xf000f000u;
+  const uint32_t bin = (d & 0x0fff0fffu) | ((w >> 3) & 0x10001000u);
+  if ((out & 0xffffu) == 0) atomicAdd(&s.hist[bin & 0xffffu], 1u);
+  if ((out >> 16) == 0) atomicAdd(&s.hist[bin >> 16], 1u);
+  if (out != 0) {
+    if ((out & 0xffffu) != 0 && (w & 0xffffu) != 0xff80u) count_rare(s, w & 0xffffu);
+    if ((out >> 16) != 0 && (w >> 16) != 0xff80u) count_rare(s, w >> 16);
   }
 }
-__device__ __forceinline__ void count_value(SampleSmem &s, uint32_t b) {
-  const int mag = (int)(b & 0x7fffu) - (SA_LO - 1), neg = -(int)(b >> 15);
-  if ((unsigned)(mag - 1) < (unsigned)SA_MAGS) atomicAdd(&s.hist[SA_ZERO - (mag ^ neg)], 1u);
-  else count_rare(s, b);
+
+// The leader: top-p's border and the token from `entries` values in falling order, the tokens
+// of the law before top-p. of(entry, z) gives an entry's count and value.
+struct Drawn {
+  Found cut, tok;
+  uint32_t cut_n, tok_at;   // tokens of the cut entry that are kept; which of its entry's the token is
+  int kept;
+  float prob;
+};
+template <class F>
+__device__ Drawn decide(SampleSmem &s, float m, int entries, int S, F of) {
+  const int t = threadIdx.x;
+  const int per = (entries + SA_THREADS - 1) / SA_THREADS;
+  const float ch = s.law.ch, cl = s.law.cl;
+  auto entry = [&](int i, uint32_t &cnt, unsigned long long &w) {
+    cnt = 0, w = 0;
+    if (i < 0 || i >= entries) return;
+    float z;
+    cnt = of(i, z);
+    w = weight(s.pow2, m, ch, cl, S, z);
+  };
+  uint32_t n = 0;
+  unsigned long long mass = 0;
+  for (int k = 0; k < per; ++k) {
+    uint32_t c;
+    unsigned long long w;
+    entry(t * per + k, c, w);
+    n += c, mass += c * w;
+  }
+  block_scan(s, n, mass);
+  Drawn d{};
+  if (t >= 32) return d;
+  const Law &law = s.law;
+  unsigned long long kept_mass = s.pre_mass[SA_THREADS];
+  if (law.top_p < 1.f) {
+    d.cut = find_entry(s, reach(kept_mass, law.p), false, per, entry);
+    d.cut_n = div_up(d.cut.target - d.cut.c0, d.cut.w, d.cut.cnt);
+    d.kept = (int)(d.cut.n0 + d.cut_n);
+    kept_mass = d.cut.c0 + d.cut_n * d.cut.w;
+  } else {
+    d.cut = find_entry(s, s.pre_n[SA_THREADS], true, per, entry);
+    d.cut_n = d.cut.cnt;
+    d.kept = (int)s.pre_n[SA_THREADS];
+  }
+  if (law.draw) {
+    d.tok = find_entry(s, beyond(kept_mass, law.u), false, per, entry);
+    d.tok_at = div_up(d.tok.target - d.tok.c0, d.tok.w, d.tok.cnt) - 1;
+    float z = m;
+    if (d.tok.at >= 0) of(d.tok.at, z);
+    d.prob = share(s.pow2, m, ch, cl, S, z, kept_mass);
+  }
+  return d;
 }
 
 // The leader: the verdict from the histogram of the row's values.
 __device__ void decide_values(SampleSmem &s, float m) {
-  constexpr int PT = SA_BINS / SA_THREADS;
-  const int t = threadIdx.x;
-  const Law law = s.law;
-  uint32_t n = 0;
-#pragma unroll 4
-  for (int i = 0; i < PT; ++i) n += s.hist[t * PT + i];
-  block_scan(s, n, 0);
-  const uint32_t total = s.pre_n[SA_THREADS];
-  uint32_t keep = total;
-  if (law.top_k > 0) keep = min(keep, (uint32_t)law.top_k);
-  const float least = __double2float_ru((double)m + law.log_min);   // min-p's border
-  uint32_t before = s.pre_n[t];
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const float ch = s.law.ch;
+  const float least = __double2float_ru((double)m + s.law.log_min);   // min-p's border
+  // the bins that hold tokens min-p leaves, in their order: how many each warp has
+  uint32_t have = 0, n = 0;
+  for (int j = 0; j < SA_ROWS; ++j) {
+    const int bin = bin_at((warp * SA_ROWS + j) * 32 + lane);
+    const uint32_t c = bin < 0 ? 0 : s.hist[bin];
+    n += c;
+    have += __popc(__ballot_sync(~0u, c != 0 && bin_value(bin) >= least));
+  }
+  if (lane == 0) s.warp_k[warp] = have;
+  __syncthreads();
+  uint32_t at = 0, entries = 0;
+  for (int w = 0; w < SA_WARPS; ++w) {
+    if (w == warp) at = entries;
+    entries += s.warp_k[w];
+  }
   float rough = 0.f;
-  uint32_t part = 0;   // tokens of this thread's bins that min-p and top-k keep
-  for (int i = 0; i < PT; ++i) {
-    const int bin = t * PT + i;
-    const uint32_t c = s.hist[bin];
-    if (c != 0 && before < keep) {
+  if (entries <= SA_ENTRIES)
+    for (int j = 0; j < SA_ROWS && have != 0; ++j) {
+      const int bin = bin_at((warp * SA_ROWS + j) * 32 + lane);
+      const uint32_t c = bin < 0 ? 0 : s.hist[bin];
       const float z = bin_value(bin);
-      if (z >= least) {
-        const uint32_t k = min(c, keep - before);
-        part += k;
-        rough += (float)k * ex2((z - m) * law.ch);
+      const bool in = c != 0 && z >= least;
+      const uint32_t who = __ballot_sync(~0u, in);
+      if (in) {
+        s.bins[at + __popc(who & ((1u << lane) - 1))] = (uint16_t)bin;
+        rough += (float)c * ex2((z - m) * ch);
       }
+      at += __popc(who);
     }
-    before += c;
+  uint32_t none = 0;
+  block_sums(s, rough, n, none);
+  const uint32_t total = n;
+  // values without a bin of their own: what has no weight needs none, unless the
+  // last token kept is among them
+  const uint32_t low = s.hist[SA_LAST];
+  const bool light = (m + 2048.f) * ch > 63.f;
+  Verdict v{};
+  v.slow = s.odd != 0 || entries > SA_ENTRIES || entries == 0 || (low != 0 && !light);
+  if (v.slow) {
+    if (t == 0) s.verdict = v;
+    return;
   }
-  rough = block_sum(s, rough);
-  const int S = unit_of(rough);
-  const uint32_t first = s.pre_n[t];
-  auto of = [&](int bin, uint32_t at, uint32_t &cnt, unsigned long long &mass) {
-    cnt = 0, mass = 0;
-    const uint32_t c = bin >= 0 ? s.hist[bin] : 0;
-    const float z = bin >= 0 ? bin_value(bin) : 0.f;
-    if (c == 0 || at >= keep || !(z >= least)) return;
-    cnt = min(c, keep - at);
-    mass = cnt * weight(s.pow2, m, law.ch, law.cl, S, z);
-  };
+  // top-k: the entry it ends in, and what it keeps of that
+  int part = -1;
+  uint32_t part_n = 0;
+  if (s.law.top_k > 0 && (uint32_t)s.law.top_k < total) {
+    const int per = ((int)entries + SA_THREADS - 1) / SA_THREADS;
+    uint32_t c = 0;
+    for (int k = 0; k < per; ++k)
+      if (t * per + k < (int)entries) c += s.hist[s.bins[t * per + k]];
+    block_scan(s, c, 0);
+    if (t < 32) {
+      const Found f = find_entry(s, (unsigned long long)s.law.top_k, true, per, [&](int i, uint32_t &cnt, unsigned long long &w) {
+        cnt = i >= 0 && i < (int)entries ? s.hist[s.bins[i]] : 0, w = 0;
+      });
+      if (t == 0) s.part_bin = f.at, s.part_n = (uint32_t)s.law.top_k - f.n0;
+    }
+    __syncthreads();
+    if (s.part_bin >= 0) part = s.part_bin, part_n = s.part_n, entries = part + 1;
+  }
+  const Drawn d = decide(s, m, (int)entries, unit_of(rough), [&](int i, float &z) {
+    const int bin = s.bins[i];
+    z = bin_value(bin);
+    return i == part ? part_n : s.hist[bin];
+  });
+  if (t >= 32) return;
+  const int cut_bin = s.bins[max(d.cut.at, 0)];
+  v.kept = d.kept;
+  v.cut = bin_value(cut_bin);
+  v.cut_n = (int)d.cut_n;
+  v.cut_id = d.cut_n == s.hist[cut_bin] ? INT_MAX : -1;
+  v.tok_id = -1;
+  if (low != 0 && (uint32_t)v.kept + low > total) {
+    if (v.kept == (int)total && least == -INFINITY) v.cut = -INFINITY, v.cut_id = INT_MAX;
+    else v.slow = 1;
+  }
+  if (s.law.draw) {
+    v.tok = bin_value(s.bins[max(d.tok.at, 0)]);
+    v.tok_at = (int)d.tok_at;
+    v.prob = d.prob;
+  }
+  if (t == 0) s.verdict = v;
+}
+
+// ------------------------------------------------------------- by a list
+// Counts (and with `masses` the masses) of the intervals of the list's tokens with keys from
+// `from` on, scanned; 4 intervals per thread.
+struct Intervals {
+  float m, scale;
+  __device__ __forceinline__ int of(float z) const { return min(SA_LEVEL - 1, (int)((m - z) * scale)); }
+};
+__device__ __forceinline__ float list_value(unsigned long long key) { return of_key((uint32_t)(key >> 32)); }
+__device__ void add_mass(uint32_t *lo, uint32_t *hi, unsigned long long w) {
+  const uint32_t old = atomicAdd(lo, (uint32_t)w);
+  const uint32_t up = (uint32_t)(w >> 32) + (old + (uint32_t)w < old ? 1u : 0u);
+  if (up != 0) atomicAdd(hi, up);
+}
+__device__ void count_list(SampleSmem &s, int n, const Intervals &iv, unsigned long long from, bool masses, int S) {
+  constexpr int PT = SA_LEVEL / SA_THREADS;
+  const int t = threadIdx.x;
+  for (int i = t; i < SA_LEVEL * (masses ? 3 : 1); i += SA_THREADS) s.level.cnt[i] = 0;   // lo and hi lie behind it
+  __syncthreads();
+  for (int i = t; i < n; i += SA_THREADS) {
+    const unsigned long long key = s.list[i];
+    if (key < from) continue;
+    const float z = list_value(key);
+    const int b = iv.of(z);
+    atomicAdd(&s.level.cnt[b], 1u);
+    if (masses) add_mass(&s.level.lo[b], &s.level.hi[b], weight(s.pow2, iv.m, s.law.ch, s.law.cl, S, z));
+  }
+  __syncthreads();
+  uint32_t c = 0;
   unsigned long long mass = 0;
-  before = first;
-  for (int i = 0; i < PT; ++i) {
-    uint32_t c;
-    unsigned long long w;
-    of(t * PT + i, before, c, w);
-    mass += w;
-    before += s.hist[t * PT + i];
-  }
-  __syncthreads();   // pre_n is read above
-  block_scan(s, part, mass);
-  if (t < 32) {
-    // of the tokens before a bin those that are kept: pre_n, as the kept ones come first
-    auto in_warp = [&](int bin, uint32_t at, uint32_t &cnt, unsigned long long &mass) {
-      const uint32_t c = bin >= 0 ? s.hist[bin] : 0;
-      uint32_t run = c;
 #pragma unroll
-      for (int o = 1; o < PT; o <<= 1) {
-        const uint32_t a = __shfl_up_sync(~0u, run, o);
-        if (t >= o) run += a;
+  for (int i = 0; i < PT; ++i) {
+    const int b = t * PT + i;
+    c += s.level.cnt[b];
+    if (masses) mass += s.level.lo[b] + ((unsigned long long)s.level.hi[b] << 32);
+  }
+  block_scan(s, c, mass);
+}
+// The token that a count or a mass (of the tokens from `from` on) reaches: its key, rank and
+// weight to key, key_rank (of the whole list), key_w, key_before. False: its interval
+// holds too many.
+__device__ bool find_key(SampleSmem &s, int n, const Intervals &iv, unsigned long long from, int S,
+                         unsigned long long target, bool by_n) {
+  constexpr int PT = SA_LEVEL / SA_THREADS;
+  const int t = threadIdx.x;
+  if (t < 32) {
+    const Found f = find_entry(s, target, by_n, PT, [&](int b, uint32_t &c, unsigned long long &w) {
+      c = 0, w = 0;
+      if (b < 0) return;
+      if (by_n) c = s.level.cnt[b];
+      else c = 1, w = s.level.lo[b] + ((unsigned long long)s.level.hi[b] << 32);
+    });
+    if (t == 0) {
+      s.found = f;
+      s.n_near = 0;
+      if (f.at >= 0) {   // tokens and mass before the interval
+        const int t0 = f.at / PT;
+        uint32_t n0 = s.pre_n[t0];
+        unsigned long long c0 = s.pre_mass[t0];
+        for (int i = t0 * PT; i < f.at; ++i) {
+          n0 += s.level.cnt[i];
+          if (!by_n) c0 += s.level.lo[i] + ((unsigned long long)s.level.hi[i] << 32);
+        }
+        s.found.n0 = n0, s.found.c0 = c0;
       }
-      of(bin, at + run - c, cnt, mass);
-    };
-    const uint32_t in_law = s.pre_n[SA_THREADS];
-    const unsigned long long all = s.pre_mass[SA_THREADS];
-    Verdict v{};
-    v.kept = (int)in_law;
-    unsigned long long kept_mass = all;
-    // the last value that is kept
-    const bool by_mass = law.top_p < 1.f;
-    Found f = find_bin<PT>(s, by_mass ? max(1ull, reach(all, law.top_p)) : in_law, !by_mass, in_warp);
-    v.cut = bin_value(max(f.bin, 0));
-    v.cut_n = (int)f.cnt;
-    if (by_mass) {
-      const unsigned long long w = max(1ull, f.mass / max(1u, f.cnt));
-      v.cut_n = (int)div_up(f.target - f.c0, w);
-      v.kept = (int)f.n0 + v.cut_n;
-      kept_mass = f.c0 + v.cut_n * w;
     }
-    v.cut_whole = (uint32_t)v.cut_n == s.hist[max(f.bin, 0)];
-    // values without a bin of their own: what has no weight needs none, unless the
-    // last token kept is among them
-    const uint32_t low = s.hist[SA_LAST];
-    v.slow = s.hist[0] != 0 || s.tiny != 0;
-    if (low != 0 && (uint32_t)v.kept + low > total) {
-      const bool none = (m + 1024.f) * law.ch > 63.f;
-      if (v.kept == (int)total && none && law.log_min == -INFINITY) v.cut = -INFINITY, v.cut_n = 0, v.cut_whole = 1;
-      else v.slow = 1;
-    } else if (low != 0 && !((m + 1024.f) * law.ch > 63.f)) {
+  }
+  __syncthreads();
+  const int at = s.found.at;
+  const uint32_t many = at < 0 ? SA_NEAR + 1 : s.level.cnt[at];
+  if (many > SA_NEAR) return false;
+  for (int i = t; i < n; i += SA_THREADS) {
+    const unsigned long long key = s.list[i];
+    if (key < from) continue;
+    const float z = list_value(key);
+    if (iv.of(z) != at) continue;
+    const int k = atomicAdd(&s.n_near, 1);
+    s.near[k] = key;
+    s.near_w[k] = by_n ? 0 : weight(s.pow2, iv.m, s.law.ch, s.law.cl, S, z);
+  }
+  __syncthreads();
+  const uint32_t n0 = s.found.n0;
+  const unsigned long long c0 = s.found.c0;
+  if (t < (int)many) {
+    const unsigned long long key = s.near[t], w = s.near_w[t];
+    uint32_t rank = 0;
+    unsigned long long before = 0;
+    for (int i = 0; i < (int)many; ++i) {
+      const bool first = s.near[i] > key;
+      rank += first;
+      before += first ? s.near_w[i] : 0ull;
+    }
+    rank += n0, before += c0;
+    if (by_n ? rank + 1 == target : (before < target && target <= before + w))
+      s.key = key, s.key_w = w, s.key_rank = rank, s.key_before = before;
+  }
+  __syncthreads();
+  return true;
+}
+
+// The leader: the verdict from the at most SA_NEAR tokens of the list with keys from `from` on, a
+// thread each, in the order of their ranks.
+__device__ void decide_few(SampleSmem &s, float m, int n, unsigned long long from) {
+  const int t = threadIdx.x;
+  const Law &law = s.law;
+  if (t == 0) s.n_near = 0;
+  s.near[t] = 0;
+  __syncthreads();
+  for (int i = t; i < n; i += SA_THREADS) {
+    const unsigned long long key = s.list[i];
+    if (key >= from) s.near[atomicAdd(&s.n_near, 1)] = key;
+  }
+  __syncthreads();
+  const int many = s.n_near;
+  const unsigned long long key = s.near[t];
+  int rank = 0;
+  if (t < ((many + 31) & ~31))
+    for (int i = 0; i < many; i += 4) {   // zeros behind the last
+      const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(s.near + i);
+      const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(s.near + i + 2);
+      rank += (a.x > key) + (a.y > key) + (b.x > key) + (b.y > key);
+    }
+  const int kept = law.top_k > 0 ? min(many, law.top_k) : many;
+  constexpr int S = 62 - 9;   // at most 256 weights
+  static_assert(SA_NEAR <= 256, "units");
+  const float z = list_value(key);
+  const bool in = t < many && rank < kept;
+  const unsigned long long w = in ? weight(s.pow2, m, law.ch, law.cl, S, z) : 0;
+  s.near_w[t] = 0;
+  __syncthreads();
+  if (in) s.near_w[rank] = w;
+  __syncthreads();
+  block_scan(s, 0, s.near_w[t]);
+  unsigned long long mass = s.pre_mass[SA_THREADS];
+  const unsigned long long before = in ? s.pre_mass[rank] : 0;
+  int last = kept - 1;   // the rank of the last token
+  if (law.top_p < 1.f) {
+    const unsigned long long target = reach(mass, law.p);
+    if (in && before < target && target <= before + w) s.key_rank = (uint32_t)rank, s.key_w = before + w;
+    __syncthreads();
+    last = (int)s.key_rank, mass = s.key_w;
+  }
+  if (t < many && rank == last) {
+    s.verdict.kept = last + 1;
+    s.verdict.cut = z, s.verdict.cut_id = (int)~(uint32_t)key;
+    s.verdict.slow = 0;
+  }
+  if (law.draw) {
+    const unsigned long long target = beyond(mass, law.u);
+    if (in && before < target && target <= before + w) {
+      s.verdict.tok = z, s.verdict.tok_id = (int)~(uint32_t)key;
+      s.verdict.prob = share(s.pow2, m, law.ch, law.cl, S, z, mass);
+    }
+  }
+}
+
+// The leader: the verdict from the list of n tokens, which holds all of the law.
+__device__ void decide_list(SampleSmem &s, float m, int n) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const Law &law = s.law;
+  // the key of min-p's border; the least value from there on, and a rough sum of the weights
+  const float least = law.greedy ? m : fmaxf(__double2float_ru((double)m + law.log_min), -3.402823466e38f);
+  unsigned long long from = (unsigned long long)key_of(least) << 32, first = 0;
+  float low = m, rough = 0.f;
+  uint32_t in = 0;
+  for (int i = t; i < n; i += SA_THREADS) {
+    const unsigned long long key = s.list[i];
+    if (key < from) continue;
+    const float z = list_value(key);
+    ++in;
+    low = fminf(low, z);
+    first = max(first, key);
+    rough += ex2((z - m) * law.ch);
+  }
+  in = __reduce_add_sync(~0u, in);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    low = fminf(low, __shfl_xor_sync(~0u, low, o));
+    rough += __shfl_xor_sync(~0u, rough, o);
+    if (law.greedy) first = max(first, __shfl_xor_sync(~0u, first, o));
+  }
+  if (lane == 0) s.warp_low[warp] = low, s.warp_f[warp] = rough, s.warp_n[warp] = in, s.warp_mass[warp] = first;
+  __syncthreads();
+  in = 0, rough = 0.f;
+#pragma unroll
+  for (int w = 0; w < SA_WARPS; ++w) {
+    low = fminf(low, s.warp_low[w]);
+    rough += s.warp_f[w];
+    in += s.warp_n[w];
+    first = max(first, s.warp_mass[w]);
+  }
+  Verdict v{};
+  if (law.greedy) {
+    v.tok = v.cut = m;
+    v.tok_id = v.cut_id = (int)~(uint32_t)first;
+    v.kept = 1;
+    v.prob = 1.f;
+    if (t == 0) s.verdict = v;
+    return;
+  }
+  if (in <= SA_NEAR) {
+    decide_few(s, m, n, from);
+    return;
+  }
+  const Intervals iv{m, m > low ? (float)SA_LEVEL / (m - low) : 0.f};
+  const int S = unit_of(rough);
+  if (law.top_k > 0 && law.top_k <= (int)in) {
+    count_list(s, n, iv, from, false, S);
+    if (find_key(s, n, iv, from, S, (unsigned long long)law.top_k, true)) {
+      from = s.key;
+      in = (uint32_t)law.top_k;
+      __syncthreads();
+      if (in <= SA_NEAR) {
+        decide_few(s, m, n, from);
+        return;
+      }
+    } else {
       v.slow = 1;
     }
-    if (law.draw) {
-      const Found d = find_bin<PT>(s, beyond(kept_mass, law.u), false, in_warp);
-      const unsigned long long w = max(1ull, d.mass / max(1u, d.cnt));
-      v.tok = bin_value(max(d.bin, 0));
-      v.tok_at = (int)div_up(d.target - d.c0, w) - 1;
-      v.prob = share(s.pow2, m, law.ch, law.cl, S, v.tok, kept_mass);
-    }
-    if (t == 0) s.verdict = v;
   }
+  v.kept = (int)in;
+  // from: the last token's key, or min-p's border
+  v.cut = list_value(from), v.cut_id = (uint32_t)from == 0 ? INT_MAX : (int)~(uint32_t)from;
+  if (!v.slow && (law.top_p < 1.f || law.draw)) {
+    count_list(s, n, iv, from, true, S);
+    unsigned long long mass = s.pre_mass[SA_THREADS];
+    if (law.top_p < 1.f) {
+      if (!find_key(s, n, iv, from, S, reach(mass, law.p), false)) v.slow = 1;
+      else {
+        v.kept = (int)s.key_rank + 1;
+        v.cut = list_value(s.key), v.cut_id = (int)~(uint32_t)s.key;
+        mass = s.key_before + s.key_w;
+      }
+      __syncthreads();   // the key is read
+    }
+    if (!v.slow && law.draw) {
+      // what lies behind top-p's border is behind this target too
+      if (!find_key(s, n, iv, from, S, beyond(mass, law.u), false)) v.slow = 1;
+      else {
+        v.tok = list_value(s.key), v.tok_id = (int)~(uint32_t)s.key;
+        v.prob = share(s.pow2, m, law.ch, law.cl, S, v.tok, mass);
+      }
+    }
+  }
+  if (t == 0) s.verdict = v;
 }
 
 // ------------------------------------------------- any values: by divisions
@@ -515,8 +874,8 @@ struct Level {
 
 template <class E, int U>
 __device__ void level_count(SampleSmem &s, const Row<E, U> &row, const Level &l) {
-  uint32_t *cnt = s.hist, *lo = s.hist + SA_LEVEL, *hi = s.hist + 2 * SA_LEVEL;
-  for (int i = threadIdx.x; i < 3 * SA_LEVEL; i += SA_THREADS) s.hist[i] = 0;
+  uint32_t *cnt = s.level.cnt, *lo = s.level.lo, *hi = s.level.hi;
+  for (int i = threadIdx.x; i < SA_LEVEL; i += SA_THREADS) cnt[i] = lo[i] = hi[i] = 0;
   __syncthreads();
   const uint32_t top = key_of(l.m);
   const float least = of_key(top - l.last);
@@ -538,10 +897,7 @@ __device__ void level_count(SampleSmem &s, const Row<E, U> &row, const Level &l)
           atomicAdd(cnt + bin, 1u);
           if (l.masses) {
             const unsigned long long w = weight(s.pow2, l.m, ch, cl, l.S, z);
-            const uint32_t old = atomicAdd(lo + bin, (uint32_t)w);
-            const uint32_t carry = old + (uint32_t)w < old ? 1u : 0u;
-            const uint32_t up = (uint32_t)(w >> 32) + carry;
-            if (up != 0) atomicAdd(hi + bin, up);
+            add_mass(lo + bin, hi + bin, w);
           }
         }
       }
@@ -559,7 +915,7 @@ __device__ Found level_find(cg::cluster_group &cluster, SampleSmem &s, const Row
   constexpr int PT = SA_LEVEL / SA_THREADS;
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), t = threadIdx.x;
   level_count(s, row, l);
-  uint32_t *cnt = s.hist, *lo = s.hist + SA_LEVEL, *hi = s.hist + 2 * SA_LEVEL;
+  uint32_t *cnt = s.level.cnt, *lo = s.level.lo, *hi = s.level.hi;
   if (C > 1) {
     cluster.sync();
     // each CTA sums its share of the bins over the cluster, into the leader's
@@ -567,11 +923,11 @@ __device__ Found level_find(cg::cluster_group &cluster, SampleSmem &s, const Row
       uint32_t n = 0;
       unsigned long long w = 0;
       for (int r = 0; r < C; ++r) {
-        const uint32_t *h = cluster.map_shared_rank(s.hist, r);
+        const uint32_t *h = cluster.map_shared_rank(s.level.cnt, r);   // lo and hi lie behind it
         n += h[i];
         w += h[SA_LEVEL + i] + ((unsigned long long)h[2 * SA_LEVEL + i] << 32);
       }
-      uint32_t *h = cluster.map_shared_rank(s.hist, 0);
+      uint32_t *h = cluster.map_shared_rank(s.level.cnt, 0);
       h[i] = n, h[SA_LEVEL + i] = (uint32_t)w, h[2 * SA_LEVEL + i] = (uint32_t)(w >> 32);
     }
     cluster.sync();
@@ -598,12 +954,21 @@ __device__ Found level_find(cg::cluster_group &cluster, SampleSmem &s, const Row
     }
     block_scan(s, n, mass);
     if (t < 32) {
-      if (kind == 3) target = max(1ull, reach(s.pre_mass[SA_THREADS], s.law.top_p));
+      if (kind == 3) target = reach(s.pre_mass[SA_THREADS], s.law.p);
       if (kind == 4) target = beyond(s.pre_mass[SA_THREADS], s.law.u);
-      const Found f = find_bin<PT>(s, kind == 0 ? ~0ull : target, kind == 1, [&](int bin, uint32_t, uint32_t &c, unsigned long long &w) {
-        c = bin >= 0 ? cnt[bin] : 0;
-        w = bin >= 0 ? lo[bin] + ((unsigned long long)hi[bin] << 32) : 0;
+      // a bin's mass as one token's weight, and its tokens besides
+      Found f = find_entry(s, kind == 0 ? ~0ull : target, kind == 1, PT, [&](int bin, uint32_t &c, unsigned long long &w) {
+        c = 0, w = 0;
+        if (bin < 0) return;
+        if (kind == 1) c = cnt[bin];
+        else c = 1, w = lo[bin] + ((unsigned long long)hi[bin] << 32);
       });
+      if (f.at >= 0) {
+        const int t0 = f.at / PT;
+        f.cnt = cnt[f.at], f.mass = lo[f.at] + ((unsigned long long)hi[f.at] << 32);
+        f.n0 = s.pre_n[t0], f.c0 = s.pre_mass[t0];
+        for (int i = t0 * PT; i < f.at; ++i) f.n0 += cnt[i], f.c0 += lo[i] + ((unsigned long long)hi[i] << 32);
+      }
       if (t == 0) s.found = f;
     }
   }
@@ -631,61 +996,59 @@ __device__ Found descend(cg::cluster_group &cluster, SampleSmem &s, const Row<E,
   const uint32_t total_n = f.total_n;
   unsigned long long c0 = f.c0;
   uint32_t n0 = f.n0;
-  while (f.bin >= 0 && l.shift > 0) {
-    l.first += (uint32_t)f.bin << l.shift;
+  while (f.at >= 0 && l.shift > 0) {
+    l.first += (uint32_t)f.at << l.shift;
     l.shift = level_shift(1ull << l.shift);
     const bool by_n = kind == 1;
     f = level_find(cluster, s, row, l, by_n ? 1 : 2, wanted - (by_n ? n0 : c0));
     c0 += f.c0, n0 += f.n0;
   }
-  *key_distance = f.bin < 0 ? l.last : l.first + ((uint32_t)f.bin << l.shift);
+  *key_distance = f.at < 0 ? l.last : l.first + ((uint32_t)f.at << l.shift);
   f.c0 = c0, f.n0 = n0, f.total = total, f.total_n = total_n, f.target = wanted;
   return f;
 }
 
 template <class E, int U>
-__device__ __noinline__ void decide_divisions(cg::cluster_group &cluster, SampleSmem &s, const Row<E, U> &row, float m) {
-  const Law law = s.law;
+__device__ __noinline__ void decide_divisions(cg::cluster_group &cluster, SampleSmem &s, const Row<E, U> &row, float m,
+                                              float rough) {
   const uint32_t top = key_of(m);
+  const int top_k = s.law.top_k;
   Level l{};
   l.m = m;
   l.whole = 1;
-  const float least = __double2float_ru((double)m + law.log_min);
+  const float least = __double2float_ru((double)m + s.law.log_min);
   l.last = top - key_of(fmaxf(least, -3.402823466e38f));
-  l.S = unit_of((float)min(row.end - row.off, law.top_k > 0 ? law.top_k : row.end));
+  l.S = unit_of(top_k > 0 ? fminf(rough, (float)top_k) : rough);
   Verdict v{};
-  v.cut = -INFINITY, v.cut_whole = 1;
+  v.cut = least, v.cut_id = INT_MAX, v.tok_id = -1;
   v.kept = -1;
-  if (law.log_min > -INFINITY) v.cut = of_key(top - l.last);
   uint32_t d;
-  if (law.top_k > 0) {
-    const Found f = descend(cluster, s, row, l, 1, (unsigned long long)law.top_k, &d);
-    if (f.bin >= 0) {
+  if (top_k > 0) {
+    const Found f = descend(cluster, s, row, l, 1, (unsigned long long)top_k, &d);
+    if (f.at >= 0) {
       l.last = d;
-      l.ties = law.top_k - f.n0;
+      l.ties = top_k - f.n0;
       l.whole = l.ties == f.cnt;
-      v.cut = of_key(top - d), v.cut_n = (int)l.ties, v.cut_whole = l.whole;
-      v.kept = law.top_k;
+      v.cut = of_key(top - d), v.cut_n = (int)l.ties, v.cut_id = l.whole ? INT_MAX : -1;
+      v.kept = top_k;
     } else {
       v.kept = (int)f.total_n;
     }
   }
   l.masses = 1;
-  if (law.top_p < 1.f) {
+  if (s.law.top_p < 1.f) {
     const Found f = descend(cluster, s, row, l, 3, 0, &d);
-    const unsigned long long w = f.mass / max(1u, f.cnt);
-    const uint32_t ties = div_up(f.target - f.c0, max(1ull, w));
+    const uint32_t ties = div_up(f.target - f.c0, weight(s.pow2, m, s.law.ch, s.law.cl, l.S, of_key(top - d)), f.cnt);
     l.whole = ties == f.cnt && (l.whole || d != l.last);
     l.last = d, l.ties = ties;
-    v.cut = of_key(top - d), v.cut_n = (int)ties, v.cut_whole = l.whole;
+    v.cut = of_key(top - d), v.cut_n = (int)ties, v.cut_id = l.whole ? INT_MAX : -1;
     v.kept = (int)(f.n0 + ties);
   }
-  if (law.draw) {
+  if (s.law.draw) {
     const Found f = descend(cluster, s, row, l, 4, 0, &d);
-    const unsigned long long w = max(1ull, f.mass / max(1u, f.cnt));
     v.tok = of_key(top - d);
-    v.tok_at = (int)div_up(f.target - f.c0, w) - 1;
-    v.prob = share(s.pow2, m, law.ch, law.cl, l.S, v.tok, f.total);
+    v.tok_at = (int)div_up(f.target - f.c0, weight(s.pow2, m, s.law.ch, s.law.cl, l.S, v.tok), f.cnt) - 1;
+    v.prob = share(s.pow2, m, s.law.ch, s.law.cl, l.S, v.tok, f.total);
     if (v.kept < 0) v.kept = (int)f.total_n;
   } else if (v.kept < 0) {
     l.masses = 0, l.first = 0, l.shift = level_shift((unsigned long long)l.last + 1);
@@ -695,16 +1058,19 @@ __device__ __noinline__ void decide_divisions(cg::cluster_group &cluster, Sample
   __syncthreads();
 }
 
-// The parameters of row r's law.
-__device__ Law law_of(const SampleArgs &a, int r) {
+// The parameters of row r's law, by a warp.
+__device__ __forceinline__ Law law_of(const SampleArgs &a, int r) {
+  const int lane = threadIdx.x & 31;
   Law l{};
   int b = r;
   if (a.cu_rows != nullptr) {
     int lo = 0, hi = a.B;   // the last request that starts at or before r
     while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (GLDG(a.cu_rows + mid) <= r) lo = mid;
-      else hi = mid;
+      const int step = (hi - lo + 31) / 32, mid = lo + step * lane;
+      const bool at = mid < hi && GLDG(a.cu_rows + min(mid, a.B)) <= r;
+      const int k = 31 - __clz(__ballot_sync(~0u, at || lane == 0));
+      lo += step * k;
+      hi = min(hi, lo + step);
     }
     b = lo;
     l.bad = !(GLDG(a.cu_rows + b) <= r && r < GLDG(a.cu_rows + b + 1));
@@ -714,22 +1080,421 @@ __device__ Law law_of(const SampleArgs &a, int r) {
   l.top_p = a.p.top_p ? GLDG(a.p.top_p + b) : 1.f;
   l.top_k = a.p.top_k ? max(0, GLDG(a.p.top_k + b)) : 0;
   l.draw = a.uniform != nullptr;
-  l.u = l.draw ? GLDG(a.uniform + r) : 0.f;
+  const float u = l.draw ? GLDG(a.uniform + r) : 0.f;
   l.bad |= !(T >= 0.f && T <= 3.402823466e38f) || !(min_p >= 0.f && min_p <= 1.f) ||
-           !(l.top_p >= 0.f && l.top_p <= 1.f) || !(l.u >= 0.f && l.u < 1.f);
+           !(l.top_p >= 0.f && l.top_p <= 1.f) || !(u >= 0.f && u < 1.f);
   l.greedy = T < SPEC_GREEDY_T;
   l.log_min = -INFINITY;
-  if (!l.greedy && !l.bad) {
-    const double c = 1.4426950408889634074 / (double)T;
-    l.ch = (float)c;
-    l.cl = (float)(c - (double)l.ch);
-    if (min_p > 0.f) l.log_min = (double)T * log((double)min_p);
+  if (l.bad) return l;
+  l.list = l.greedy || min_p > 0.f || (l.top_k > 0 && l.top_k <= SA_TOP_K) || a.V <= SA_FULL;
+  if (l.greedy) return l;
+  l.p = l.top_p < 1.f ? __float2ull_rz(l.top_p * 18446744073709551616.f) : ~0ull;
+  l.u = __float2ull_rz(u * 18446744073709551616.f);
+  const double c = 1.4426950408889634074 / (double)T;
+  l.ch = (float)c;
+  l.cl = (float)(c - (double)l.ch);
+  l.head = INFINITY;
+  if (min_p > 0.f) {
+    l.log_min = (double)T * log((double)min_p);
+    l.head = __double2float_ru(-l.log_min);
   }
+  l.ranked = l.top_k > 0 && l.top_k <= SA_TOP_K && a.V > SA_FULL;
   return l;
 }
 
+// ------------------------------------------------------------- the row's passes
+__device__ __forceinline__ float warp_max_nan(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = max_nan(x, __shfl_xor_sync(~0u, x, o));
+  return x;
+}
+// The largest of a lane's vectors.
 template <class E, int U>
-__global__ void __launch_bounds__(SA_THREADS, 2) k_sample(const SampleArgs a) {
+__device__ __forceinline__ float lane_max(const uint4 (&v)[U]) {
+  if (sizeof(E) == 2) {
+    uint32_t x = max_nan2(max_nan2(v[0].x, v[0].y), max_nan2(v[0].z, v[0].w));
+#pragma unroll
+    for (int u = 1; u < U; ++u) x = max_nan2(x, max_nan2(max_nan2(v[u].x, v[u].y), max_nan2(v[u].z, v[u].w)));
+    return max_nan(bf16lo(x), bf16hi(x));
+  }
+  float x = -INFINITY;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    x = max_nan(x, max_nan(max_nan(__uint_as_float(v[u].x), __uint_as_float(v[u].y)),
+                           max_nan(__uint_as_float(v[u].z), __uint_as_float(v[u].w))));
+  return x;
+}
+// The CTA's largest logit, from the warps'.
+__device__ __forceinline__ void cta_max(SampleSmem &s, float most) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) s.warp_f[warp] = most;
+  __syncthreads();
+  if (warp == 0) {
+    const float m = warp_max_nan(lane < SA_WARPS ? s.warp_f[lane] : -INFINITY);
+    if (lane == 0) s.cta_max = m;
+  }
+}
+
+// By the block: a value that k of the n keys reach, the k-th largest of them or a little
+// less (the 16 leading bits of its key). key_at(i), i < n.
+template <class F>
+__device__ float rank_border(SampleSmem &s, int n, int k, F key_at) {
+  const int t = threadIdx.x;
+  uint32_t *cnt = s.level.cnt;   // 256 counts of each round
+  for (int i = t; i < 512; i += SA_THREADS) cnt[i] = 0;
+  uint32_t lead = 0;
+#pragma unroll
+  for (int round = 0; round < 2; ++round) {
+    __syncthreads();
+    for (int i = t; i < n; i += SA_THREADS) {
+      const uint32_t key = key_at(i) >> 16;
+      if (round == 0) atomicAdd(&cnt[255 - (key >> 8)], 1u);
+      else if (key >> 8 == lead) atomicAdd(&cnt[256 + 255 - (key & 255)], 1u);
+    }
+    __syncthreads();
+    if (t < 32) {
+      uint32_t c[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = cnt[256 * round + t * 8 + i], sum += c[i];
+      uint32_t run = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(~0u, run, o);
+        if (t >= o) run += y;
+      }
+      run -= sum;
+      if ((int)run < k && k <= (int)(run + sum)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if ((int)run < k && k <= (int)(run + c[i])) s.part_bin = 255 - (t * 8 + i), s.part_n = run;
+          run += c[i];
+        }
+      }
+    }
+    __syncthreads();
+    lead = round == 0 ? (uint32_t)s.part_bin : lead << 8 | (uint32_t)s.part_bin;
+    k -= (int)s.part_n;
+  }
+  return of_key(lead << 16);
+}
+
+// The list without what cannot be among its first k; returns the border. By the block.
+__device__ __noinline__ float tighten(SampleSmem &s, int k) {
+  constexpr int PER = (SA_LIST + SA_THREADS - 1) / SA_THREADS;
+  const int t = threadIdx.x, n = s.n_list;
+  if (n > SA_LIST || n < k) return -INFINITY;   // full, or all of it
+  const float border = rank_border(s, n, k, [&](int i) { return (uint32_t)(s.list[i] >> 32); });
+  unsigned long long keep[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int i = t + j * SA_THREADS;
+    keep[j] = i < n && list_value(s.list[i]) >= border ? s.list[i] : 0;
+  }
+  __syncthreads();
+  if (t == 0) s.n_list = 0;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < PER; ++j)
+    if (keep[j] != 0) s.list[atomicAdd(&s.n_list, 1)] = keep[j];
+  __syncthreads();
+  return border;
+}
+
+// The tokens of this CTA's slice that the border leaves to its list, the chunks' largest
+// logits to cmax. A list that is full ends it (cut_short). v: this lane's first vectors.
+template <class E, int U>
+__device__ __forceinline__ void list_pass(SampleSmem &s, const Row<E, U> &row, int C, uint4 (&v)[U]) {
+  constexpr int PER = Val<E>::PER, GROUP = U * 32 * PER;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int groups = row.chunk / GROUP;
+  int c = warp, g = 0;
+  const float head = s.law.head;
+  float border = -3.402823466e38f;   // (-inf takes no part)
+  const bool ranked = s.law.ranked, cut_too = row.out != nullptr;
+  const int top_k = s.law.top_k;
+  if (ranked) {   // first of all by the largest of what each thread has already
+    const uint32_t mine = key_of(lane_max<E, U>(v));
+    border = fmaxf(border, rank_border(s, SA_THREADS, top_k, [&](int) { return mine; }));
+  }
+  float most = -INFINITY, cm = -INFINITY;   // a lane's own
+  uint32_t run = 0;
+  while (c - warp < row.nc) {   // as often by every warp
+    int nc = c, ng = g + 1;
+    if (ng == groups) ng = 0, nc += SA_WARPS;
+    uint4 next[U];
+    row.fetch(nc, ng, next);
+    const float lm = lane_max<E, U>(v);
+    most = max_nan(most, lm);
+    if (cut_too) cm = max_nan(cm, lm);
+    float bound = border;
+    if (head < INFINITY) {
+      const uint32_t key = key_of(lm);
+      run = max(run, *(volatile uint32_t *)&s.run);
+      if (__any_sync(~0u, key > run)) {
+        run = max(run, __reduce_max_sync(~0u, key));
+        if (lane == 0) atomicMax(&s.run, run);
+      }
+      bound = fmaxf(bound, __fsub_rd(of_key(run), head));
+    }
+    if (__any_sync(~0u, lm >= bound)) {
+      // which of the lane's elements, a bit each; then the lanes' next ones together
+      const int at = (row.c0 + c) * row.chunk + g * GROUP + lane * PER - row.off;
+      uint32_t hits = 0;
+      if (lm >= bound) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          Vec<E> x;
+          x.v = v[u];
+#pragma unroll
+          for (int i = 0; i < PER; ++i) hits |= Val<E>::f32(x.e[i]) >= bound ? 1u << (u * PER + i) : 0u;
+        }
+      }
+      while (true) {
+        const uint32_t who = __ballot_sync(~0u, hits != 0);
+        if (who == 0) break;
+        int pos = 0;
+        if (lane == 0) pos = atomicAdd(&s.n_list, __popc(who));
+        pos = __shfl_sync(~0u, pos, 0) + __popc(who & ((1u << lane) - 1));
+        if (hits != 0) {
+          const int k = __ffs(hits) - 1;
+          hits &= hits - 1;
+          E e = 0;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            Vec<E> x;
+            x.v = v[u];
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+              if (k == u * PER + i) e = x.e[i];
+          }
+          const int id = at + k / PER * 32 * PER + k % PER;
+          if (pos < SA_LIST) s.list[pos] = (unsigned long long)key_of(Val<E>::f32(e)) << 32 | ~(uint32_t)id;
+        }
+      }
+    }
+    if (nc != c) {
+      if (cut_too) {
+        cm = warp_max_nan(cm);
+        if (lane == 0 && c < row.nc) s.cmax[c] = cm;
+        cm = -INFINITY;
+      }
+      const int have = *(volatile int *)&s.n_list;
+      if (!ranked) {
+        if (have > SA_LIST) {
+          s.cut_short = 1;
+          break;
+        }
+      } else if (__syncthreads_or(have > SA_LIST / 2)) {
+        if (s.n_list > SA_LIST) {
+          s.cut_short = 1;
+          break;
+        }
+        border = fmaxf(border, tighten(s, top_k));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = next[u];
+    c = nc, g = ng;
+  }
+  most = warp_max_nan(most);
+  cta_max(s, most);
+  if (ranked && C > 1) {   // the cluster's lists have to fit one
+    __syncthreads();
+    if (s.n_list > SA_LIST / C) tighten(s, top_k);
+  }
+}
+
+// An f32 sum of weights by a reference that rises with the largest logit.
+struct RunningSum {
+  float ref = -INFINITY;
+  f32x2 sum[2] = {0, 0};
+  __device__ __forceinline__ void raise(float top, float c) {
+    if (!(top > ref)) return;
+    const float f = ex2((ref - top) * c);
+    sum[0] = mul2(sum[0], pk2(f, f)), sum[1] = mul2(sum[1], pk2(f, f));
+    ref = top;
+  }
+  __device__ __forceinline__ void add(float a, float b, int k, float c) {
+    const f32x2 d = mul2(pk2(a - ref, b - ref), pk2(c, c));
+    sum[k] = add2(sum[k], pk2(ex2(lo2(d)), ex2(hi2(d))));
+  }
+};
+
+// The chunks' largest logits and, with `weights`, bf16: the histogram, f32: a rough sum.
+template <class E, int U>
+__device__ void value_pass(SampleSmem &s, const Row<E, U> &row, bool weights) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr bool BF = sizeof(E) == 2;
+  if (BF && weights) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < (SA_BINS + 32) / 4; i += SA_THREADS) reinterpret_cast<uint4 *>(s.hist)[i] = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x == 0) s.odd = 0;
+    __syncthreads();
+  }
+  float most = -INFINITY;
+  const float ch = s.law.ch;
+  RunningSum sum;
+  const int groups = row.chunk / (U * 32 * Val<E>::PER);
+  int c = warp, g = 0;
+  uint4 v[U];
+  row.fetch(c, g, v);
+  float cm = -INFINITY;   // a lane's own
+  while (c < row.nc) {
+    int nc = c, ng = g + 1;
+    if (ng == groups) ng = 0, nc += SA_WARPS;
+    uint4 next[U];
+    row.fetch(nc, ng, next);
+    const float lm = lane_max<E, U>(v);
+    cm = max_nan(cm, lm);
+    if (weights && BF) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) count_two(s, v[u].x), count_two(s, v[u].y), count_two(s, v[u].z), count_two(s, v[u].w);
+    } else if (weights) {
+      sum.raise(lm, ch);   // a lane's own reference
+      if (sum.ref > -INFINITY) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          sum.add(__uint_as_float(v[u].x), __uint_as_float(v[u].y), 0, ch);
+          sum.add(__uint_as_float(v[u].z), __uint_as_float(v[u].w), 1, ch);
+        }
+      }
+    }
+    if (nc != c) {
+      cm = warp_max_nan(cm);
+      if (lane == 0) s.cmax[c] = cm;
+      most = max_nan(most, cm);
+      cm = -INFINITY;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = next[u];
+    c = nc, g = ng;
+  }
+  cta_max(s, most);
+  if (!BF && weights) {
+    __syncthreads();
+    float x = (lo2(sum.sum[0]) + hi2(sum.sum[0])) + (lo2(sum.sum[1]) + hi2(sum.sum[1]));
+    x = sum.ref > -INFINITY ? x * ex2((sum.ref - s.cta_max) * ch) : 0.f;
+    uint32_t none = 0, none2 = 0;
+    block_sums(s, x, none, none2);
+    if (threadIdx.x == 0) s.cta_sum = x;
+  }
+}
+
+// The ids of a value's equal number `at` and of the last one kept.
+template <class E, int U>
+__device__ void locate(cg::cluster_group &cluster, SampleSmem &s, const Row<E, U> &row, bool find_tok, bool find_cut) {
+  constexpr int PER = Val<E>::PER;
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float tok = s.verdict.tok, cut = s.verdict.cut;
+  const float low = find_tok && find_cut ? fminf(tok, cut) : find_tok ? tok : cut;
+  uint32_t my_tok = 0, my_cut = 0;
+  for (int c = warp; c < row.nc; c += SA_WARPS) {
+    uint32_t nt = 0, nk = 0;
+    if (s.cmax[c] >= low) {
+      row.groups(c, [&](int, const uint4 *x) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          Vec<E> w;
+          w.v = x[u];
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const float z = Val<E>::f32(w.e[i]);
+            nt += z == tok;
+            nk += z == cut;
+          }
+        }
+      });
+      nt = __reduce_add_sync(~0u, nt);
+      nk = __reduce_add_sync(~0u, nk);
+    }
+    if (lane == 0) s.tok_n[c] = nt, s.cut_n[c] = nk;
+    my_tok += nt, my_cut += nk;
+  }
+  if (lane == 0) s.warp_n[warp] = my_tok, s.warp_k[warp] = my_cut;
+  if (threadIdx.x == 0) s.tok_id = s.cut_id = -1;
+  __syncthreads();
+  if (warp == 0) {
+    const uint32_t x = __reduce_add_sync(~0u, lane < SA_WARPS ? s.warp_n[lane] : 0);
+    const uint32_t y = __reduce_add_sync(~0u, lane < SA_WARPS ? s.warp_k[lane] : 0);
+    if (lane == 0) s.cta_tok = x, s.cta_cut = y;
+  }
+  cluster.sync();
+  if (warp == 0) {   // matches before each chunk
+    uint32_t tok0 = 0, cut0 = 0;
+    for (int q = 0; q < rank; ++q)
+      tok0 += *cluster.map_shared_rank(&s.cta_tok, q), cut0 += *cluster.map_shared_rank(&s.cta_cut, q);
+    for (int c1 = 0; c1 < row.nc; c1 += 32) {
+      const int c = c1 + lane;
+      const uint32_t x = c < row.nc ? s.tok_n[c] : 0, y = c < row.nc ? s.cut_n[c] : 0;
+      uint32_t sx = x, sy = y;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t p = __shfl_up_sync(~0u, sx, o), q = __shfl_up_sync(~0u, sy, o);
+        if (lane >= o) sx += p, sy += q;
+      }
+      if (c < row.nc) s.tok_n[c] = tok0 + sx - x, s.cut_n[c] = cut0 + sy - y;
+      tok0 += __shfl_sync(~0u, sx, 31), cut0 += __shfl_sync(~0u, sy, 31);
+    }
+    if (lane == 0) s.tok_end = tok0, s.cut_end = cut0;
+  }
+  __syncthreads();
+  // the warp whose chunk holds it looks again
+  auto pick = [&](const uint32_t *before, uint32_t all, float value, uint32_t at, int *id) {
+    for (int c = warp; c < row.nc; c += SA_WARPS) {
+      const uint32_t n0 = before[c], n1 = c + 1 < row.nc ? before[c + 1] : all;
+      if (at < n0 || at >= n1) continue;
+      uint32_t left = at - n0;   // equals to pass over
+      bool done = false;
+      row.groups(c, [&](int p, const uint4 *x) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          Vec<E> w;
+          w.v = x[u];
+          uint32_t n = 0;
+#pragma unroll
+          for (int i = 0; i < PER; ++i) n += Val<E>::f32(w.e[i]) == value;
+          if (done || !__any_sync(~0u, n != 0)) continue;
+          uint32_t run = n;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(~0u, run, o);
+            if (lane >= o) run += y;
+          }
+          const uint32_t sum = __shfl_sync(~0u, run, 31);
+          if (left < sum) {
+            if (left >= run - n && left < run) {
+              uint32_t k = left - (run - n);
+#pragma unroll
+              for (int i = 0; i < PER; ++i)
+                if (Val<E>::f32(w.e[i]) == value && k-- == 0) *id = p + u * 32 * PER + i - row.off;
+            }
+            done = true;
+          } else {
+            left -= sum;
+          }
+        }
+      });
+    }
+  };
+  if (find_tok) pick(s.tok_n, s.tok_end, tok, (uint32_t)s.verdict.tok_at, &s.tok_id);
+  if (find_cut) pick(s.cut_n, s.cut_end, cut, (uint32_t)s.verdict.cut_n - 1, &s.cut_id);
+  cluster.sync();
+  int ti = -1, ci = -1;
+  for (int q = 0; q < C; ++q) {
+    ti = max(ti, *cluster.map_shared_rank(&s.tok_id, q));
+    ci = max(ci, *cluster.map_shared_rank(&s.cut_id, q));
+  }
+  __syncthreads();   // the verdict's values are read
+  if (threadIdx.x == 0) {
+    if (find_tok) s.verdict.tok_id = ti;
+    if (find_cut) s.verdict.cut_id = ci;
+  }
+  __syncthreads();
+}
+
+template <class E, int U>
+__global__ void __launch_bounds__(SA_THREADS, SA_CTAS_PER_SM) k_sample(const SampleArgs a) {
   extern __shared__ __align__(16) unsigned char raw[];
   SampleSmem &s = *reinterpret_cast<SampleSmem *>(raw);
   cg::cluster_group cluster = cg::this_cluster();
@@ -745,11 +1510,12 @@ __global__ void __launch_bounds__(SA_THREADS, 2) k_sample(const SampleArgs a) {
     if (fall || (t == 0 && (GLDG(a.cu_rows) != 0 || GLDG(a.cu_rows + a.B) != a.R)))
       set_status(a.hdr, SPEC_ERR_INVALID_ARG, -1);
   }
-  // the law, by a thread of the last warp while the others clear the histogram
-  if (t == SA_THREADS - 1) s.law = law_of(a, r), s.tiny = 0;
+  if (warp == SA_WARPS - 1) {
+    const Law l = law_of(a, r);
+    if (lane == 0) s.law = l;
+  }
   if (t < 128) s.pow2[t] = g_pow2[t];
-  if (BF)
-    for (int i = t; i < SA_BINS / 4; i += SA_THREADS) reinterpret_cast<uint4 *>(s.hist)[i] = make_uint4(0, 0, 0, 0);
+  if (t == 0) s.n_list = 0, s.cut_short = 0, s.run = 0, s.odd = 0;
 
   Row<E, U> row;
   const E *at = static_cast<const E *>(a.logits) + (long long)r * a.V;
@@ -761,242 +1527,137 @@ __global__ void __launch_bounds__(SA_THREADS, 2) k_sample(const SampleArgs a) {
   const int chunks = (row.end + row.chunk - 1) / row.chunk, per = (chunks + C - 1) / C;
   row.c0 = min(rank * per, chunks);
   row.nc = min(per, chunks - row.c0);
+  uint4 first[U];   // on their way while the law is made
+  row.fetch(warp, 0, first);
   __syncthreads();
-  const Law law = s.law;
-  const bool count = BF && !law.greedy && !law.bad;
 
-  // The row's one pass from HBM: the chunks' largest logits, bf16: the histogram.
-  float most = -INFINITY;
-  if (!law.bad) {
-    for (int c = warp; c < row.nc; c += SA_WARPS) {
-      float cm = -INFINITY;
-      row.groups(c, [&](int, const uint4 *v) {
-        if (BF) {
-          uint32_t mx = 0xff80ff80u;
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-            mx = max_nan2(mx, max_nan2(max_nan2(v[u].x, v[u].y), max_nan2(v[u].z, v[u].w)));
-          cm = max_nan(cm, max_nan(bf16lo(mx), bf16hi(mx)));
-          if (count) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                count_value(s, w[i] & 0xffffu);
-                count_value(s, w[i] >> 16);
-              }
-            }
-          }
-        } else {
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-            cm = max_nan(cm, max_nan(max_nan(__uint_as_float(v[u].x), __uint_as_float(v[u].y)),
-                                     max_nan(__uint_as_float(v[u].z), __uint_as_float(v[u].w))));
-        }
-      });
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) cm = max_nan(cm, __shfl_xor_sync(~0u, cm, o));
-      if (lane == 0) s.cmax[c] = cm;
-      most = max_nan(most, cm);
-    }
-  }
-  if (lane == 0) s.warp_f[warp] = most;
-  __syncthreads();
-  if (t == 0) {
+  // every CTA of the cluster comes to the same
+  auto largest = [&]() {
     float m = -INFINITY;
-    for (int w = 0; w < SA_WARPS; ++w) m = max_nan(m, s.warp_f[w]);
-    s.cta_max = m;
-  }
-  cluster.sync();
+    for (int q = 0; q < C; ++q) m = max_nan(m, *cluster.map_shared_rank(&s.cta_max, q));
+    return m;
+  };
+  bool bad = s.law.bad, known = false;
   float m = -INFINITY;
-  int tiny = 0;
-  for (int q = 0; q < C; ++q) m = max_nan(m, *cluster.map_shared_rank(&s.cta_max, q)), tiny |= *cluster.map_shared_rank(&s.tiny, q);
-  const bool bad = law.bad || !(m > -INFINITY && m < INFINITY);
-  if (bad) {   // the whole cluster
-    if (rank == 0 && t == 0) {
-      set_status(a.hdr, SPEC_ERR_INVALID_ARG, r);
-      if (a.tokens) GST(a.tokens + r, -1);
-      if (a.prob) GST(a.prob + r, 0.f);
-      if (a.kept) GST(a.kept + r, 0);
+  if (!bad && s.law.list) {
+    list_pass(s, row, C, first);
+    cluster.sync();
+    bool full = false;
+    int n = 0;
+    for (int q = 0; q < C; ++q) {
+      n += *cluster.map_shared_rank(&s.n_list, q);
+      full |= *cluster.map_shared_rank(&s.cut_short, q) != 0;
     }
-    s.verdict.cut = INFINITY, s.verdict.cut_whole = 1;
-  } else if (law.greedy) {
-    if (t == 0) {
-      Verdict v{};
-      v.tok = v.cut = m;
-      v.cut_n = v.kept = 1;
-      v.prob = 1.f;
-      s.verdict = v;
-    }
-  } else {
-    bool slow = !BF;
-    if (BF) {
-      if (C > 1) {
-        // each CTA sums its share of the bins over the cluster, into the leader's
-        constexpr int VECS = SA_BINS / 4;
-        for (int i = rank * (VECS / C) + t; i < (rank + 1) * (VECS / C); i += SA_THREADS) {
-          uint4 n = make_uint4(0, 0, 0, 0);
-          for (int q = 0; q < C; ++q) {
-            const uint4 h = reinterpret_cast<const uint4 *>(cluster.map_shared_rank(s.hist, q))[i];
-            n.x += h.x, n.y += h.y, n.z += h.z, n.w += h.w;
-          }
-          reinterpret_cast<uint4 *>(cluster.map_shared_rank(s.hist, 0))[i] = n;
-        }
-        cluster.sync();
-      }
+    full |= n > SA_LIST;
+    m = largest();
+    if (!full && !(m > -INFINITY && m < INFINITY)) bad = true;
+    if (!full && !bad) {
       if (rank == 0) {
-        if (t == 0) s.tiny = tiny;
+        int have = s.n_list;
         __syncthreads();
-        decide_values(s, m);
+        for (int q = 1; q < C; ++q) {
+          const int k = *cluster.map_shared_rank(&s.n_list, q);
+          const unsigned long long *from = cluster.map_shared_rank(s.list, q);
+          for (int i = t; i < k; i += SA_THREADS) s.list[have + i] = from[i];
+          have += k;
+        }
         __syncthreads();
+        decide_list(s, m, n);
       }
       cluster.sync();
       const Verdict v = *cluster.map_shared_rank(&s.verdict, 0);
       cluster.sync();
-      slow = v.slow;
       if (t == 0) s.verdict = v;
+      known = v.slow == 0;
     }
-    if (slow) decide_divisions(cluster, s, row, m);
+    __syncthreads();
+  }
+  if (!bad && !known) {
+    cluster.sync();   // the peers have read what the next pass writes
+    value_pass(s, row, !s.law.greedy);
+    cluster.sync();
+    m = largest();
+    int odd = 0;
+    float rough = 0.f;
+    for (int q = 0; q < C; ++q) {
+      odd |= *cluster.map_shared_rank(&s.odd, q);
+      if (!BF && !s.law.greedy)
+        rough += *cluster.map_shared_rank(&s.cta_sum, q) * ex2((*cluster.map_shared_rank(&s.cta_max, q) - m) * s.law.ch);
+    }
+    if (BF) rough = (float)a.V;   // where a bf16 row goes by divisions
+    bad = !(m > -INFINITY && m < INFINITY);
+    if (!bad && s.law.greedy) {   // more equals of the largest than a list holds
+      Verdict v{};
+      v.tok = v.cut = m;
+      v.tok_id = v.cut_id = -1;
+      v.cut_n = v.kept = 1;
+      v.prob = 1.f;
+      if (t == 0) s.verdict = v;
+    } else if (!bad) {
+      bool slow = !BF;
+      if (BF) {
+        if (C > 1) {
+          // each CTA sums its share of the bins over the cluster, into the leader's
+          constexpr int VECS = (SA_BINS + 32) / 4;
+          for (int i = rank * (VECS / C) + t; i < (rank + 1) * (VECS / C); i += SA_THREADS) {
+            uint4 n = make_uint4(0, 0, 0, 0);
+            for (int q = 0; q < C; ++q) {
+              const uint4 h = reinterpret_cast<const uint4 *>(cluster.map_shared_rank(s.hist, q))[i];
+              n.x += h.x, n.y += h.y, n.z += h.z, n.w += h.w;
+            }
+            reinterpret_cast<uint4 *>(cluster.map_shared_rank(s.hist, 0))[i] = n;
+          }
+          cluster.sync();
+        }
+        if (rank == 0) {
+          if (t == 0) s.odd = odd;
+          __syncthreads();
+          decide_values(s, m);
+        }
+        cluster.sync();
+        const Verdict v = *cluster.map_shared_rank(&s.verdict, 0);
+        cluster.sync();
+        slow = v.slow != 0;
+        if (t == 0) s.verdict = v;
+      }
+      if (slow) decide_divisions(cluster, s, row, m, rough);
+    }
+    __syncthreads();
+    if (!bad) {
+      const bool find_tok = s.law.draw && s.verdict.tok_id < 0, find_cut = row.out != nullptr && s.verdict.cut_id < 0;
+      if (find_tok || find_cut) locate(cluster, s, row, find_tok, find_cut);
+    }
   }
   __syncthreads();
   const Verdict v = s.verdict;
-  if (!bad && rank == 0 && t == 0) {
-    if (a.prob) GST(a.prob + r, v.prob);
-    if (a.kept) GST(a.kept + r, v.kept);
-  }
-
-  // How many equals of the two values the chunks hold.
-  const bool find_tok = law.draw && a.tokens != nullptr && !bad, find_cut = row.out != nullptr && !v.cut_whole && !bad;
-  uint32_t my_tok = 0, my_cut = 0;
-  if (find_tok || find_cut) {
-    const float low = find_tok && find_cut ? fminf(v.tok, v.cut) : find_tok ? v.tok : v.cut;
-    for (int c = warp; c < row.nc; c += SA_WARPS) {
-      uint32_t nt = 0, ncut = 0;
-      if (s.cmax[c] >= low) {
-        row.groups(c, [&](int, const uint4 *x) {
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            Vec<E> w;
-            w.v = x[u];
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-              const float z = Val<E>::f32(w.e[i]);
-              nt += z == v.tok;
-              ncut += z == v.cut;
-            }
-          }
-        });
-        nt = __reduce_add_sync(~0u, nt);
-        ncut = __reduce_add_sync(~0u, ncut);
-      }
-      if (lane == 0) s.tok_n[c] = nt, s.cut_n[c] = ncut;
-      my_tok += nt, my_cut += ncut;
-    }
-    if (lane == 0) s.warp_n[warp] = my_tok, s.warp_mass[warp] = my_cut;
-    __syncthreads();
-    if (t == 0) {
-      uint32_t x = 0, y = 0;
-      for (int w = 0; w < SA_WARPS; ++w) x += s.warp_n[w], y += (uint32_t)s.warp_mass[w];
-      s.cta_tok = x, s.cta_cut = y;
-    }
-    cluster.sync();
-    uint32_t tok0 = 0, cut0 = 0;   // in the slices before this one
-    for (int q = 0; q < rank; ++q) tok0 += *cluster.map_shared_rank(&s.cta_tok, q), cut0 += *cluster.map_shared_rank(&s.cta_cut, q);
-    if (warp == 0) {   // matches before each chunk
-      for (int c1 = 0; c1 < row.nc; c1 += 32) {
-        const int c = c1 + lane;
-        const uint32_t x = c < row.nc ? s.tok_n[c] : 0, y = c < row.nc ? s.cut_n[c] : 0;
-        uint32_t sx = x, sy = y;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t p = __shfl_up_sync(~0u, sx, o), q = __shfl_up_sync(~0u, sy, o);
-          if (lane >= o) sx += p, sy += q;
-        }
-        if (c < row.nc) s.tok_n[c] = tok0 + sx - x, s.cut_n[c] = cut0 + sy - y;
-        tok0 += __shfl_sync(~0u, sx, 31), cut0 += __shfl_sync(~0u, sy, 31);
-      }
-      if (lane == 0) s.tok_end = tok0;
-    }
-    cluster.sync();
-    if (find_tok) {
-      for (int c = warp; c < row.nc; c += SA_WARPS) {
-        const uint32_t before = s.tok_n[c], after = c + 1 < row.nc ? s.tok_n[c + 1] : s.tok_end;
-        if ((uint32_t)v.tok_at < before || (uint32_t)v.tok_at >= after) continue;
-        uint32_t left = (uint32_t)v.tok_at - before;   // equals to pass over
-        bool done = false;
-        row.groups(c, [&](int p, const uint4 *x) {
-          for (int u = 0; u < U && !done; ++u) {
-            Vec<E> w;
-            w.v = x[u];
-            uint32_t n = 0;
-            for (int i = 0; i < PER; ++i) n += Val<E>::f32(w.e[i]) == v.tok;
-            uint32_t run = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-              const uint32_t y = __shfl_up_sync(~0u, run, o);
-              if (lane >= o) run += y;
-            }
-            const uint32_t all = __shfl_sync(~0u, run, 31);
-            if (left < all) {
-              if (left >= run - n && left < run) {
-                uint32_t k = left - (run - n);
-                for (int i = 0; i < PER; ++i)
-                  if (Val<E>::f32(w.e[i]) == v.tok && k-- == 0)
-                    GST(a.tokens + r, p + u * 32 * PER + i - row.off);
-              }
-              done = true;
-            } else {
-              left -= all;
-            }
-          }
-        });
-      }
-    }
+  if (rank == 0 && t == 0) {
+    if (bad) set_status(a.hdr, SPEC_ERR_INVALID_ARG, r);
+    if (a.tokens) GST(a.tokens + r, bad ? -1 : v.tok_id);
+    if (a.prob) GST(a.prob + r, bad ? 0.f : v.prob);
+    if (a.kept) GST(a.kept + r, bad ? 0 : v.kept);
   }
   if (row.out != nullptr) {
-    for (int c = warp; c < row.nc; c += SA_WARPS) {
-      const bool none = bad || !(s.cmax[c] >= v.cut);
-      const long long first = (long long)(row.c0 + c) * row.chunk;
-      if (none) {
-        Vec<E> x;
+    Vec<E> none;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) x.e[i] = Val<E>::NEG_INF;
+    for (int i = 0; i < PER; ++i) none.e[i] = Val<E>::NEG_INF;
+    for (int c = warp; c < row.nc; c += SA_WARPS) {
+      const long long first = (long long)(row.c0 + c) * row.chunk;
+      if (bad || !(s.cmax[c] >= v.cut)) {
         for (int g = lane * PER; g < row.chunk; g += 32 * PER)
-          if (first + g < row.end) row.store((int)first + g, x.v);
+          if (first + g < row.end) row.store((int)first + g, none.v);
         continue;
       }
-      uint32_t seen = find_cut ? s.cut_n[c] : 0;
       row.groups(c, [&](int p, const uint4 *x) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+          const long long q = (long long)p + u * 32 * PER;
           Vec<E> w;
           w.v = x[u];
-          if (!find_cut) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i)
-              if (!(Val<E>::f32(w.e[i]) >= v.cut)) w.e[i] = Val<E>::NEG_INF;
-          } else {
-            uint32_t n = 0;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) n += Val<E>::f32(w.e[i]) == v.cut;
-            uint32_t run = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-              const uint32_t y = __shfl_up_sync(~0u, run, o);
-              if (lane >= o) run += y;
-            }
-            uint32_t k = seen + run - n;
-            seen += __shfl_sync(~0u, run, 31);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-              const float z = Val<E>::f32(w.e[i]);
-              const bool tie = z == v.cut;
-              if (!(z > v.cut) && !(tie && k < (uint32_t)v.cut_n)) w.e[i] = Val<E>::NEG_INF;
-              k += tie;
-            }
+          for (int i = 0; i < PER; ++i) {
+            const float z = Val<E>::f32(w.e[i]);
+            if (!(z > v.cut) && !(z == v.cut && (int)q + i - row.off <= v.cut_id)) w.e[i] = Val<E>::NEG_INF;
           }
-          const long long q = (long long)p + u * 32 * PER;
           if (q < row.end) row.store((int)q, w.v);
         }
       });
@@ -1087,14 +1748,13 @@ extern "C" int spec_sample(const void *logits, int dt, int R, int V, const int32
   // A cluster of up to eight CTAs per row while there are too few rows for the SMs and
   // every CTA keeps 4096 elements.
   int C = 1;
-  while (C < SA_MAX_CLUSTER && (long long)R * C * 2 <= 2 * sms && V / (C * 2) >= 4096) C *= 2;
-  while (C < SA_MAX_CLUSTER && V / C > SA_CHUNKS * 32768) C *= 2;
-  // Chunks of a row: a vector per lane where the row is short, eight where each warp has
-  // eight all the same.
+  while (C < SA_MAX_CLUSTER && (long long)R * C * 2 <= SA_CTAS_PER_SM * sms && V / (C * 2) >= 4096) C *= 2;
+  // Chunks of a row: a vector per lane where the row is short, four where each warp has
+  // four all the same.
   const int per = 32 * (int)(16 / es);
-  const bool few = V / C < per * 8 * SA_WARPS;
-  const int chunk = per * (few ? 1 : 8);
+  const bool few = V / C < per * 4 * SA_WARPS;
+  const int chunk = per * (few ? 1 : 4);
   a.reps = (V / C + 2 * chunk) / chunk / SA_CHUNKS + 1;
-  if (dt == SPEC_BF16) return few ? launch_sample<uint16_t, 1>(a, C, st) : launch_sample<uint16_t, 8>(a, C, st);
-  return few ? launch_sample<uint32_t, 1>(a, C, st) : launch_sample<uint32_t, 8>(a, C, st);
+  if (dt == SPEC_BF16) return few ? launch_sample<uint16_t, 1>(a, C, st) : launch_sample<uint16_t, 4>(a, C, st);
+  return few ? launch_sample<uint32_t, 1>(a, C, st) : launch_sample<uint32_t, 4>(a, C, st);
 }
