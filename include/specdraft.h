@@ -359,31 +359,31 @@ int spec_head_backward(const void *dy, const void *x, const void *weight,
  *   scale[n, k / group] (code[n, k] - zero[n, k / group])
  *
  * with codes and zeros 0 .. 15 (zeros NULL: 8 throughout) and bf16 scales; group
- * is 32, 64 or 128, and a row's last group may be shorter. The kernel reads the
- * codes in an order of its own (`packed`), laid out once:
+ * is 32, 64 or 128, and a row's last group may be shorter. The kernels read codes,
+ * scales and zeros as one stream in an order of their own (`packed`), laid out once:
  *
  *   codes   [N, ceil(K / 2)] bytes, the code of an even column in the low 4 bits.
  *   scales  [N, ceil(K / group)] bf16.
  *   zeros   [N, ceil(K / group)] bytes (their low 4 bits count), or NULL.
- *   packed  spec_head4_packed_bytes(N, K) bytes, 16-byte aligned.
+ *   packed  spec_head4_packed_bytes(N, K, group, has_zeros) bytes (0 on invalid
+ *           sizes), 16-byte aligned.
  *
- * spec_head4_pack lays codes out. spec_head4_quantize makes codes and scales of a
+ * spec_head4_pack lays these out. spec_head4_quantize makes codes and scales of a
  * bf16 weight [N, K]: scale = max|w| / 7 over the group, rounded to bf16, code = 8 +
- * w / scale rounded to the nearest (ties to even, at most 7 from 8); a group of
- * zeros, or whose scale is no positive normal number, has scale 0. A weight
+ * w / scale rounded to the nearest (ties to even, at most 7 from 8), without zeros; a
+ * group of zeros, or whose scale is no positive normal number, has scale 0. A weight
  * that is not finite is reported (the status word reads SPEC_ERR_INVALID_ARG) and
  * counts as 0. spec_head4_unpack writes the weight's values, rounded once to bf16
  * [N, K], for calls of more rows (spec_head_forward) and for gradients.
  */
 #define SPEC_HEAD4_MAX_ROWS 64
-size_t spec_head4_packed_bytes(int N, int K);
-int spec_head4_pack(const void *codes, int N, int K, void *packed,
-                    spec_stream_t stream);
+size_t spec_head4_packed_bytes(int N, int K, int group, int has_zeros);
+int spec_head4_pack(const void *codes, const void *scales, const void *zeros,
+                    int N, int K, int group, void *packed, spec_stream_t stream);
 int spec_head4_quantize(const void *weight, int N, int K, int group, void *packed,
-                        void *scales, void *workspace, size_t ws_bytes,
-                        spec_stream_t stream);
-int spec_head4_unpack(const void *packed, const void *scales, const void *zeros,
-                      int N, int K, int group, void *weight, spec_stream_t stream);
+                        void *workspace, size_t ws_bytes, spec_stream_t stream);
+int spec_head4_unpack(const void *packed, int has_zeros, int N, int K, int group,
+                      void *weight, spec_stream_t stream);
 
 /*
  * y = act(x W^T + bias) + residual for up to SPEC_HEAD4_MAX_ROWS rows and a W of
@@ -398,10 +398,10 @@ int spec_head4_unpack(const void *packed, const void *scales, const void *zeros,
  *             256-byte aligned.
  */
 size_t spec_head4_forward_workspace(int M, int N, int K);
-int spec_head4_forward(const void *x, const void *packed, const void *scales,
-                       const void *zeros, const void *bias, const void *residual,
-                       int M, int N, int K, int group, int act, void *y,
-                       void *workspace, size_t ws_bytes, spec_stream_t stream);
+int spec_head4_forward(const void *x, const void *packed, int has_zeros,
+                       const void *bias, const void *residual, int M, int N, int K,
+                       int group, int act, void *y, void *workspace,
+                       size_t ws_bytes, spec_stream_t stream);
 
 /*
  * What every request samples by (host memory, read during the call; device

@@ -81,13 +81,13 @@ SIGS = {
     "spec_grad_norm_workspace": (_sz, []),
     "spec_grad_norm": (_i32, [_vp, _i64, _i32, _i32, ctypes.c_double, _vp, _vp, _vp, _sz, _vp]),
     "spec_clip_grads": (_i32, [_vp, _i64, _i32, _i32, ctypes.c_double, _vp, _vp, _vp, _sz, _vp]),
-    "spec_head4_packed_bytes": (_sz, [_i32, _i32]),
-    "spec_head4_pack": (_i32, [_vp, _i32, _i32, _vp, _vp]),
-    "spec_head4_quantize": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp]),
-    "spec_head4_unpack": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp]),
+    "spec_head4_packed_bytes": (_sz, [_i32, _i32, _i32, _i32]),
+    "spec_head4_pack": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp]),
+    "spec_head4_quantize": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp, _sz, _vp]),
+    "spec_head4_unpack": (_i32, [_vp, _i32, _i32, _i32, _i32, _vp, _vp]),
     "spec_head4_forward_workspace": (_sz, [_i32, _i32, _i32]),
-    "spec_head4_forward": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp,
-                                  _sz, _vp]),
+    "spec_head4_forward": (_i32, [_vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _sz,
+                                  _vp]),
     "spec_sample_workspace": (_sz, [_i32, _i32]),
     "spec_sample": (_i32, [_vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
@@ -438,46 +438,37 @@ def spec_head_backward(dy, x, weight, pre=None, *, act: int = SPEC_ACT_NONE, wan
 
 # ------------------------------------------ a head's weight held in 4 bits
 class SpecHead4:
-    """A weight [N, K] in 4 bits as spec_head4_forward reads it: packed codes, bf16
-    scales [N, ceil(K / group)] and zeros (uint8, the same shape, or None)."""
+    """A weight [N, K] in 4 bits as spec_head4_forward reads it: codes, scales of `group`
+    columns and, with `zeros` true, zeros, in the kernels' order."""
 
-    __slots__ = ("packed", "scales", "zeros", "N", "K", "group")
+    __slots__ = ("packed", "zeros", "N", "K", "group")
 
-    def __init__(self, packed, scales, zeros, N, K, group):
-        self.packed, self.scales, self.zeros, self.N, self.K, self.group = packed, scales, zeros, N, K, group
-
-
-def _head4_packed(N, K, dev):
-    nbytes = int(_sv.lib().spec_head4_packed_bytes(N, K))
-    if nbytes == 0:
-        raise _sv.SpecError(_sv.SPEC_ERR_INVALID_ARG, "spec_head4_packed_bytes")
-    return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
-
-
-def _head4_groups(K, group):
-    if group not in (32, 64, 128):
-        raise ValueError(f"group must be 32, 64 or 128, got {group}")
-    return -(-K // group)
+    def __init__(self, N, K, group, zeros, device):
+        nbytes = int(_sv.lib().spec_head4_packed_bytes(N, K, group, int(zeros)))
+        if nbytes == 0:
+            raise _sv.SpecError(_sv.SPEC_ERR_INVALID_ARG, "spec_head4_packed_bytes")
+        self.packed = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.zeros, self.N, self.K, self.group = bool(zeros), N, K, group
 
 
 def spec_head4_pack(codes, scales, zeros=None, *, K: int, group: int, stream=None) -> SpecHead4:
     """A weight of given codes [N, ceil(K / 2)] (uint8, the code of an even column in the
     low 4 bits), bf16 scales [N, ceil(K / group)] and zeros (uint8, 0 .. 15, the same
-    shape; None: 8), laid out once for spec_head4_forward. The scales and zeros are
-    kept, not copied. See include/specdraft.h."""
-    N, G, dev = codes.shape[0], _head4_groups(K, group), _device("codes", codes)
+    shape; None: 8), laid out once for spec_head4_forward. See include/specdraft.h."""
+    N, dev = codes.shape[0], _device("codes", codes)
     if tuple(codes.shape) != (N, -(-K // 2)):
         raise ValueError(f"codes must be [N, {-(-K // 2)}]")
-    for name, t, dtype in (("scales", scales, torch.bfloat16), ("zeros", zeros, torch.uint8)):
-        _arg(name, t, dtype, N * G, dev)
-        if t is not None and tuple(t.shape) != (N, G):
-            raise ValueError(f"{name} must be [{N}, {G}]")
     with _Call(dev, stream, (codes, scales, zeros)) as call:
-        packed = _head4_packed(N, K, dev)
-        code = _sv.lib().spec_head4_pack(_arg("codes", codes, torch.uint8, 0, dev), N, K, packed.data_ptr(),
-                                         call.raw)
+        weight = SpecHead4(N, K, group, zeros is not None, codes.device)
+        G = -(-K // group)
+        for name, t in (("scales", scales), ("zeros", zeros)):
+            if t is not None and tuple(t.shape) != (N, G):
+                raise ValueError(f"{name} must be [{N}, {G}]")
+        code = _sv.lib().spec_head4_pack(
+            _arg("codes", codes, torch.uint8, 0, dev), _arg("scales", scales, torch.bfloat16, N * G, dev),
+            _arg("zeros", zeros, torch.uint8, N * G, dev), N, K, group, weight.packed.data_ptr(), call.raw)
     _sv._check(code, "spec_head4_pack")
-    return SpecHead4(packed, scales, zeros, N, K, group)
+    return weight
 
 
 def spec_head4_quantize(weight, *, group: int, workspace=None, out=None, stream=None):
@@ -487,18 +478,16 @@ def spec_head4_quantize(weight, *, group: int, workspace=None, out=None, stream=
 
     Returns (SpecHead4, workspace)."""
     N, K = weight.shape
-    G, dev, bf = _head4_groups(K, group), _device("weight", weight), torch.bfloat16
-    if out is not None and ((out.N, out.K, out.group) != (N, K, group) or out.zeros is not None):
+    dev = _device("weight", weight)
+    if out is not None and (out.N, out.K, out.group, out.zeros) != (N, K, group, False):
         raise ValueError("out is a weight of other sizes, or with zeros")
-    with _Call(dev, stream, (weight, workspace) if out is None else (weight, workspace, out.packed,
-                                                                    out.scales)) as call:
+    with _Call(dev, stream, (weight, workspace, None if out is None else out.packed)) as call:
         ws, ws_at, ws_bytes = _scratch(256, dev, workspace)
         if out is None:
-            out = SpecHead4(_head4_packed(N, K, dev), torch.empty(N, G, dtype=bf, device=weight.device), None,
-                            N, K, group)
+            out = SpecHead4(N, K, group, False, weight.device)
         code = _sv.lib().spec_head4_quantize(
-            _arg("weight", weight, bf, 0, dev), N, K, group, _arg("out.packed", out.packed, torch.uint8, 0, dev),
-            _arg("out.scales", out.scales, bf, N * G, dev), ws_at, ws_bytes, call.raw)
+            _arg("weight", weight, torch.bfloat16, 0, dev), N, K, group,
+            _arg("out", out.packed, torch.uint8, 0, dev), ws_at, ws_bytes, call.raw)
     _sv._check(code, "spec_head4_quantize")
     return out, ws
 
@@ -507,14 +496,11 @@ def spec_head4_unpack(weight, *, out=None, stream=None):
     """The values of a weight in 4 bits, rounded to bf16 [N, K]: for calls of more than
     SPEC_HEAD4_MAX_ROWS rows (spec_head_forward) and for gradients."""
     dev, bf = _device("weight", weight.packed), torch.bfloat16
-    G = _head4_groups(weight.K, weight.group)
-    with _Call(dev, stream, (weight.packed, weight.scales, weight.zeros, out)) as call:
+    with _Call(dev, stream, (weight.packed, out)) as call:
         if out is None:
             out = torch.empty(weight.N, weight.K, dtype=bf, device=weight.packed.device)
         code = _sv.lib().spec_head4_unpack(
-            _arg("packed", weight.packed, torch.uint8, 0, dev),
-            _arg("scales", weight.scales, bf, weight.N * G, dev),
-            _arg("zeros", weight.zeros, torch.uint8, weight.N * G, dev), weight.N, weight.K, weight.group,
+            weight.packed.data_ptr(), weight.zeros, weight.N, weight.K, weight.group,
             _matrix("out", out, bf, weight.N, weight.K, dev), call.raw)
     _sv._check(code, "spec_head4_unpack")
     return out
@@ -532,18 +518,17 @@ def spec_head4_forward(x, weight, bias=None, residual=None, *, act: int = SPEC_A
     Returns (y [M, N], workspace).
     """
     M, K = x.shape
-    N, G = weight.N, -(-weight.K // weight.group)
+    N = weight.N
     if K != weight.K:
         raise ValueError(f"x must be [M, {weight.K}]")
     dev, bf = _device("x", x), torch.bfloat16
-    used = () if stream is None else (x, weight.packed, weight.scales, weight.zeros, bias, residual, out, workspace)
-    with _Call(dev, stream, used) as call:
-        ws, ws_at, ws_bytes = _scratch(256, dev, workspace)
+    with _Call(dev, stream, (x, weight.packed, bias, residual, out, workspace)) as call:
+        ws, ws_at, ws_bytes = _scratch(
+            0 if workspace is not None else spec_head4_forward_workspace(M, N, K), dev, workspace)
         if out is None:
             out = torch.empty(M, N, dtype=bf, device=x.device)
         code = _sv.lib().spec_head4_forward(
-            _arg("x", x, bf, 0, dev), _arg("packed", weight.packed, torch.uint8, 0, dev),
-            _arg("scales", weight.scales, bf, N * G, dev), _arg("zeros", weight.zeros, torch.uint8, N * G, dev),
+            _arg("x", x, bf, 0, dev), _arg("weight", weight.packed, torch.uint8, 0, dev), weight.zeros,
             _arg("bias", bias, bf, N, dev), _matrix("residual", residual, bf, M, N, dev), M, N, K, weight.group,
             act, _matrix("out", out, bf, M, N, dev), ws_at, ws_bytes, call.raw)
     _sv._check(code, "spec_head4_forward")

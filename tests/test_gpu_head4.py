@@ -38,11 +38,11 @@ def weight(rng, N, K, group, zeros):
 
 def reference(x, w, bias, residual, act, group):
     """(y, tolerance): sums of K products in 32 bits, a step of 2^-22 of the magnitudes for each
-    instruction, group and warp that they go through (the tensor cores' sums may be cut, not
+    instruction, group, warp and slice that they go through (the tensor cores' sums may be cut, not
     rounded), an activation of slope 1.13 at most within 2^-20, one rounding to bf16."""
     K = x.shape[1]
     z, size = x @ w.T, np.abs(x) @ np.abs(w).T
-    steps = group // 16 + -(-K // group) + 8
+    steps = group // 16 + -(-K // group) + 16 + -(-K // 128)
     if bias is not None:
         z, size = z + bias, size + np.abs(bias)
     y = O.act(z, act)
@@ -121,22 +121,24 @@ def test_residual_in_place_and_no_rows():
 
 
 def test_rows_that_are_not_aligned():
-    """A weight's scales, zeros, bias and residual at any element, y too."""
+    """Bias, residual and y at any element; codes, scales and zeros too."""
     rng = np.random.default_rng(7)
     N, K, group = 70, 200, 32
-    w, ref_w = weight(rng, N, K, group, 1)
-    G = w.scales.shape[1]
-    s = torch.empty(N * G + 1, dtype=BF16, device=DEV)[1:].view(N, G)
-    z = torch.empty(N * G + 1, dtype=torch.uint8, device=DEV)[1:].view(N, G)
-    s.copy_(w.scales)
-    z.copy_(w.zeros)
-    moved = sv.SpecHead4(w.packed, s, z, N, K, group)
-    x = bf(rng.normal(size=(5, K)))
-    b = torch.empty(N + 1, dtype=BF16, device=DEV)[1:]
-    b.copy_(bf(rng.normal(size=N)))
-    y = torch.empty(5 * N + 1, dtype=BF16, device=DEV)[1:].view(5, N)
-    sv.spec_head4_forward(x, moved, b, out=y)
-    want, tol = reference(f64(x), ref_w, f64(b), None, "none", group)
+
+    def moved(t):
+        out = torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)[1:].view(t.shape)
+        out.copy_(t)
+        return out
+
+    codes = rng.integers(0, 16, (N, K)).astype(np.uint8)
+    scales, zeros = bf(rng.uniform(0.01, 0.1, (N, 7))), rng.integers(0, 16, (N, 7)).astype(np.uint8)
+    w = sv.spec_head4_pack(moved(torch.tensor(codes[:, 0::2] | codes[:, 1::2] << 4, device=DEV)), moved(scales),
+                           moved(torch.tensor(zeros, device=DEV)), K=K, group=group)
+    ref_w = O.dequantize4(codes, f64(scales), zeros, group)
+    x, b, r = bf(rng.normal(size=(5, K))), moved(bf(rng.normal(size=N))), moved(bf(rng.normal(size=(5, N))))
+    y = moved(torch.zeros(5, N, dtype=BF16, device=DEV))
+    sv.spec_head4_forward(x, w, b, r, out=y)
+    want, tol = reference(f64(x), ref_w, f64(b), f64(r), "none", group)
     assert (np.abs(f64(y) - want) <= tol).all()
 
 
@@ -161,7 +163,6 @@ def test_quantize(N, K, group):
     q, ws = sv.spec_head4_quantize(wt, group=group)
     assert sv.spec_get_status(ws) == sv.SPEC_OK
     codes, scales = O.quantize4(f64(wt), group)
-    assert np.array_equal(f64(q.scales), scales)
     assert np.array_equal(f64(sv.spec_head4_unpack(q)), O.to_bf16(O.dequantize4(codes, scales, None, group)))
     # no value further than half a step, a little more where the scale was rounded down
     err = np.abs(f64(wt) - O.dequantize4(codes, scales, None, group))
@@ -170,7 +171,7 @@ def test_quantize(N, K, group):
     wt2 = bf(rng.normal(size=(N, K)))
     sv.spec_head4_quantize(wt2, group=group, out=q)
     fresh, _ = sv.spec_head4_quantize(wt2, group=group)
-    assert torch.equal(fresh.packed, q.packed) and torch.equal(fresh.scales, q.scales)
+    assert torch.equal(fresh.packed, q.packed)
 
 
 def test_quantize_reports_what_is_not_finite():
@@ -192,7 +193,6 @@ def test_quantize_of_the_smallest_weights():
     wt[1] = 2.0 ** -120
     q, ws = sv.spec_head4_quantize(wt, group=64)
     assert sv.spec_get_status(ws) == sv.SPEC_OK
-    assert float(q.scales[0, 0]) == 0 and float(q.scales[1, 0]) > 0
     got = sv.spec_head4_unpack(q)
     assert bool((got[0] == 0).all()) and abs(float(got[1, 0]) / 2.0 ** -120 - 1) <= 7 * HALF
 
@@ -203,7 +203,7 @@ def test_unaligned_weights_are_quantized_alike():
     odd.copy_(wt)
     a, _ = sv.spec_head4_quantize(wt, group=64)
     b, _ = sv.spec_head4_quantize(odd, group=64)
-    assert torch.equal(a.packed, b.packed) and torch.equal(a.scales, b.scales)
+    assert torch.equal(a.packed, b.packed)
 
 
 def test_wrong_tensors_are_refused():
@@ -221,7 +221,7 @@ def test_wrong_tensors_are_refused():
     s = torch.ones(8, 1, dtype=BF16, device=DEV)
     for c, sc, z, kw in ((codes, s, None, dict(K=40, group=32)), (codes, s[:, :0], None, dict(K=32, group=32)),
                          (codes, s, codes, dict(K=32, group=32)), (codes, s, None, dict(K=32, group=48))):
-        with pytest.raises((TypeError, ValueError)):
+        with pytest.raises((TypeError, ValueError, sv.SpecError)):
             sv.spec_head4_pack(c, sc, z, **kw)
     with pytest.raises(ValueError):
         sv.spec_head4_quantize(torch.zeros(8, 64, dtype=BF16, device=DEV), group=32, out=w)
@@ -232,7 +232,7 @@ def test_replays_in_a_graph():
     w, ref_w = weight(rng, 500, 640, 64, 1)
     x = bf(rng.normal(size=(6, 640)))
     y = torch.empty(6, 500, dtype=BF16, device=DEV)
-    ws = torch.empty(256, dtype=torch.uint8, device=DEV)
+    ws = torch.empty(sv.spec_head4_forward_workspace(6, 500, 640), dtype=torch.uint8, device=DEV)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):

@@ -55,48 +55,50 @@ def test_sample_refuses_host_tensors():
 
 
 # --------------------------------------------------------------- 4-bit head
-HEAD4_OK = dict(x=FAKE, packed=FAKE, scales=FAKE, zeros=None, bias=None, residual=None, M=4, N=64, K=64,
-                group=32, act=0, y=FAKE, ws=FAKE, ws_bytes=256, stream=None)
+HEAD4_OK = dict(x=FAKE, packed=FAKE, zeros=0, bias=None, residual=None, M=4, N=64, K=64, group=32, act=0,
+                y=FAKE, ws=FAKE, ws_bytes=1 << 30, stream=None)
 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(M=-1), INV), (dict(N=0), INV), (dict(K=0), INV), (dict(K=(1 << 24) + 1), INV),
     (dict(M=sv.SPEC_HEAD4_MAX_ROWS + 1), UNSUP), (dict(group=16), INV), (dict(group=48), INV),
     (dict(group=256), INV), (dict(act=3), INV), (dict(x=None), INV), (dict(packed=None), INV),
-    (dict(scales=None), INV), (dict(y=None), INV), (dict(x=FAKE + 8), INV), (dict(packed=FAKE + 4), INV),
-    (dict(scales=FAKE + 1), INV), (dict(bias=FAKE + 1), INV), (dict(y=FAKE + 1), INV),
-    (dict(N=1 << 24, K=1 << 24), UNSUP), (dict(ws=None), WS), (dict(ws=FAKE + 64), WS), (dict(ws_bytes=8), WS)])
+    (dict(y=None), INV), (dict(x=FAKE + 8), INV), (dict(packed=FAKE + 4), INV),
+    (dict(bias=FAKE + 1), INV), (dict(y=FAKE + 1), INV), (dict(ws=None), WS), (dict(ws=FAKE + 64), WS),
+    (dict(ws_bytes=8), WS), (dict(M=64, K=8192, ws_bytes=256), WS)])
 def test_head4_forward_refuses_bad_arguments(L, kw, code):
     assert L.spec_head4_forward(*{**HEAD4_OK, **kw}.values()) == code
 
 
-@pytest.mark.parametrize("args,code", [
-    ((None, 4, 8, FAKE, None), INV), ((FAKE, 0, 8, FAKE, None), INV), ((FAKE, 4, 0, FAKE, None), INV),
-    ((FAKE, 4, 8, None, None), INV), ((FAKE, 4, 8, FAKE + 8, None), INV),
-    ((FAKE, 1 << 24, 1 << 24, FAKE, None), UNSUP)])
-def test_head4_pack_refuses_bad_arguments(L, args, code):
-    assert L.spec_head4_pack(*args) == code
+@pytest.mark.parametrize("kw,code", [
+    (dict(codes=None), INV), (dict(scales=None), INV), (dict(N=0), INV), (dict(K=0), INV), (dict(group=96), INV),
+    (dict(packed=None), INV), (dict(packed=FAKE + 8), INV), (dict(scales=FAKE + 1), INV),
+    (dict(N=1 << 24, K=1 << 24), UNSUP)])
+def test_head4_pack_refuses_bad_arguments(L, kw, code):
+    a = dict(codes=FAKE, scales=FAKE, zeros=None, N=4, K=64, group=32, packed=FAKE, stream=None)
+    assert L.spec_head4_pack(*{**a, **kw}.values()) == code
 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(w=None), INV), (dict(w=FAKE + 1), INV), (dict(N=0), INV), (dict(group=100), INV),
-    (dict(packed=FAKE + 2), INV), (dict(scales=None), INV), (dict(ws=None), WS), (dict(ws_bytes=0), WS)])
+    (dict(packed=FAKE + 2), INV), (dict(ws=None), WS), (dict(ws_bytes=0), WS)])
 def test_head4_quantize_refuses_bad_arguments(L, kw, code):
-    a = dict(w=FAKE, N=4, K=64, group=32, packed=FAKE, scales=FAKE, ws=FAKE, ws_bytes=256, stream=None)
+    a = dict(w=FAKE, N=4, K=64, group=32, packed=FAKE, ws=FAKE, ws_bytes=256, stream=None)
     assert L.spec_head4_quantize(*{**a, **kw}.values()) == code
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(packed=None), INV), (dict(scales=None), INV), (dict(out=None), INV), (dict(group=0), INV),
-    (dict(out=FAKE + 1), INV), (dict(K=-3), INV)])
+    (dict(packed=None), INV), (dict(out=None), INV), (dict(group=0), INV), (dict(out=FAKE + 1), INV),
+    (dict(K=-3), INV)])
 def test_head4_unpack_refuses_bad_arguments(L, kw, code):
-    a = dict(packed=FAKE, scales=FAKE, zeros=None, N=4, K=64, group=32, out=FAKE, stream=None)
+    a = dict(packed=FAKE, zeros=0, N=4, K=64, group=32, out=FAKE, stream=None)
     assert L.spec_head4_unpack(*{**a, **kw}.values()) == code
 
 
 def test_head4_sizes(L):
-    assert L.spec_head4_packed_bytes(3, 1) == 3 * 64 and L.spec_head4_packed_bytes(3, 129) == 3 * 128
-    assert L.spec_head4_packed_bytes(0, 8) == 0
+    size = L.spec_head4_packed_bytes      # blocks of 16 rows and 128 columns, scales and zeros behind each
+    assert size(3, 1, 128, 0) == 1024 + 32 and size(17, 129, 32, 0) == 4 * (1024 + 128)
+    assert size(16, 128, 64, 1) == 1024 + 64 + 32 and size(0, 8, 32, 0) == 0 and size(8, 8, 8, 0) == 0
     assert sv.spec_head4_forward_workspace(0, 4, 4) >= 256
     assert sv.spec_head4_forward_workspace(65, 4, 4) == 0
 
