@@ -22,7 +22,7 @@
 //
 // Work. x stays in shared memory. A CTA per SM takes unit after unit: up to 16 rows of x, a
 // tile whose columns its 16 warps share and join through shared memory; more rows, more
-// tiles with fewer warps each, as the join grows with x. Where x does not fit, CTAs take a
+// tiles with a warp each, as the join grows with x. Where x does not fit, CTAs take a
 // slice of the columns each and a second kernel joins their f32 sums.
 #include "draft.cuh"
 
@@ -31,7 +31,11 @@
 namespace sv {
 namespace {
 
-constexpr int H4_WARPS = 16, H4_THREADS = 32 * H4_WARPS;
+// Warps that multiply: more rows of x need more registers of each. One more fills the ring,
+// and some join the sums of those that share a tile. Registers are given to warps by four.
+__host__ __device__ constexpr int warps_of(int nt) { return nt <= 2 ? 16 : 8; }
+constexpr int H4_JOINERS = 3;
+__host__ __device__ constexpr int threads_of(int nt) { return 32 * (warps_of(nt) + 1 + (nt <= 2 ? H4_JOINERS : 0)); }
 constexpr int H4_TILE = 16;          // rows of a tile
 constexpr int H4_CHUNK = 128;        // columns of a block
 constexpr int H4_CODES = H4_TILE * H4_CHUNK / 2;
@@ -59,14 +63,15 @@ struct Plan4 {
 Plan4 plan4(int M, int N, int K) {
   Plan4 p{};
   p.nt = M <= 8 ? 1 : M <= 16 ? 2 : M <= 32 ? 4 : 8;
-  p.ks = p.nt <= 2 ? 16 : 1;   // more rows make the join too large
+  p.ks = p.nt == 1 ? 8 : p.nt == 2 ? 4 : 1;   // more rows make the join too large
   const int chunks = chunks_of(K);
   const long long most = (p.nt <= 2 ? 100 : p.nt == 4 ? 110 : 140) * 1024;   // bytes of x
   const long long fit = std::max(1ll, (most / (2 * (M + 1)) - H4_PAD) / H4_CHUNK);
   int slices = (int)((chunks + fit - 1) / fit);
   while (p.ks > 1 && p.ks > chunks) p.ks /= 2;
   // few units: more slices, as long as a slice has work for all warps that share a tile
-  const long long units = (tiles_of(N) + H4_WARPS / p.ks - 1) / (H4_WARPS / p.ks);
+  const int groups = warps_of(p.nt) / p.ks;
+  const long long units = (tiles_of(N) + groups - 1) / groups;
   while (units * slices * 2 <= H4_PLAN_SMS && chunks / (2 * slices) >= std::max(2, p.ks)) slices *= 2;
   p.panel = (chunks + slices - 1) / slices;
   p.slices = (chunks + p.panel - 1) / p.panel;
@@ -89,11 +94,35 @@ struct Head4Args {
   WsHeader *hdr;
 };
 
+// c = a b + (ADD ? c : 0)
+template <bool ADD>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  if (ADD)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// Loads by the shared-memory address.
+__device__ __forceinline__ uint4 ld_s128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_s32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_s16(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+  return v;
 }
 // Fields i and i + 4 of a word less the zero (128 + z in both halves), as bf16.
 __device__ __forceinline__ uint32_t less_zero(uint32_t w, uint32_t zero) {
@@ -104,26 +133,22 @@ __device__ __forceinline__ uint32_t less_zero(uint32_t w, uint32_t zero) {
 }
 
 // The sums of one block: acc += scale * (x times code - zero) group by group.
+// blk: the block's address; xs[q]: that of this lane's part of x for instruction q, at
+// the block's first column.
 template <int NT, int SUBS>
-__device__ __forceinline__ void block_product(float (&acc)[NT][4], const char *blk, const uint16_t *xs, int ld, int rows,
+__device__ __forceinline__ void block_product(float (&acc)[NT][4], uint32_t blk, const uint32_t (&xs)[NT], uint32_t col,
                                               bool zeros) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const uint4 w[2] = {lds128(blk + lane * 16), lds128(blk + 512 + lane * 16)};
-  const uint32_t *scale = reinterpret_cast<const uint32_t *>(blk + H4_CODES) + g;         // rows g and g + 8
-  const uint16_t *zero = reinterpret_cast<const uint16_t *>(blk + H4_CODES + SUBS * 32) + g;
+  constexpr int PER = 4 / SUBS;   // words of a group
+  const uint32_t lane = threadIdx.x & 31, g = lane >> 2;
+  const uint4 w[2] = {ld_s128(blk + lane * 16), ld_s128(blk + lane * 16 + 512)};
   float part[NT][4];
   uint32_t z0 = 0x43084308u, z1 = 0x43084308u;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    constexpr int PER = 4 / SUBS;   // words of a group
-    if (j % PER == 0) {
-#pragma unroll
-      for (int q = 0; q < NT; ++q) part[q][0] = part[q][1] = part[q][2] = part[q][3] = 0.f;
-      if (zeros) {
-        const uint32_t z = zero[j / PER * 8];
-        z0 = 0x43004300u | (z & 15u) * 0x10001u;
-        z1 = 0x43004300u | (z >> 8 & 15u) * 0x10001u;
-      }
+    if (j % PER == 0 && zeros) {
+      const uint32_t z = ld_s16(blk + H4_CODES + SUBS * 32 + j / PER * 16 + g * 2);   // rows g and g + 8
+      z0 = 0x43004300u | (z & 15u) * 0x10001u;
+      z1 = 0x43004300u | (z >> 8 & 15u) * 0x10001u;
     }
     const uint32_t w0 = j == 0 ? w[0].x : j == 1 ? w[0].y : j == 2 ? w[0].z : w[0].w;
     const uint32_t w1 = j == 0 ? w[1].x : j == 1 ? w[1].y : j == 2 ? w[1].z : w[1].w;
@@ -137,13 +162,13 @@ __device__ __forceinline__ void block_product(float (&acc)[NT][4], const char *b
     }
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
-      // the rows behind the last read the one of zeros
-      const uint4 v = lds128(xs + (size_t)min(q * 8 + g, rows - 1) * ld + 32 * j + 8 * c);
-      mma(part[q], f[0], v.x, v.y);
-      mma(part[q], f[1], v.z, v.w);
+      const uint4 v = ld_s128(xs[q] + col + 64 * j);
+      if (j % PER == 0) mma<false>(part[q], f[0], v.x, v.y);
+      else mma<true>(part[q], f[0], v.x, v.y);
+      mma<true>(part[q], f[1], v.z, v.w);
     }
     if (j % PER == PER - 1) {
-      const uint32_t s = scale[j / PER * 8];
+      const uint32_t s = ld_s32(blk + H4_CODES + j / PER * 32 + g * 4);
       const float s0 = bf16lo(s), s1 = bf16hi(s);
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
@@ -168,13 +193,14 @@ __device__ __forceinline__ void result(const Head4Args &a, int slice, int m, int
 }
 
 template <int NT, int SUBS>
-__global__ void __launch_bounds__(H4_THREADS, 1) k_head4(const Head4Args a) {
+__global__ void __launch_bounds__(threads_of(NT), 1) k_head4(const Head4Args a) {
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ uint64_t full[H4_MAX_STAGES];
+  constexpr int THREADS = threads_of(NT), WARPS = warps_of(NT);
+  __shared__ uint64_t full[H4_MAX_STAGES], empty[H4_MAX_STAGES], sums[2], joined[2];
   __shared__ int abort;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int rows = a.M + 1, ld = a.panel * H4_CHUNK + H4_PAD;
-  const int groups = H4_WARPS / a.ks, ks = warp % a.ks, rg = warp / a.ks;   // tiles of a unit; this warp's part
+  const int groups = WARPS / a.ks;   // tiles of a unit
   char *ring = reinterpret_cast<char *>(smem);
   uint16_t *xs = reinterpret_cast<uint16_t *>(ring + (size_t)a.stages * a.stage_bytes);   // [rows][ld]
   float *red = reinterpret_cast<float *>(xs + (size_t)rows * ld);                         // [2][warps][NT][8][H4_COL]
@@ -188,7 +214,8 @@ __global__ void __launch_bounds__(H4_THREADS, 1) k_head4(const Head4Args a) {
 
   if (t == 0) {
     abort = 0;
-    for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1);
+    for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], WARPS);
+    for (int s = 0; s < 2; ++s) mbar_init(&sums[s], WARPS), mbar_init(&joined[s], H4_JOINERS);
     fence_mbar_init();
   }
   __syncthreads();
@@ -203,12 +230,12 @@ __global__ void __launch_bounds__(H4_THREADS, 1) k_head4(const Head4Args a) {
       bulk_g2s(dst + (size_t)g * a.per_stage * a.block,
                a.packed + ((long long)(u * groups + g) * a.chunks + k0 + c0) * a.block, (uint32_t)(n * a.block), bar);
   };
-  if (t == 0)
+  if (t == 32 * WARPS)
     for (int i = 0; i < min(a.stages, total); ++i) fill(i);
 
   // x's slice, zeros behind its end and in the last row
   const int vecs = a.panel * (H4_CHUNK / 8);
-  for (int e = t; e < rows * vecs; e += H4_THREADS) {
+  for (int e = t; e < rows * vecs; e += THREADS) {
     const int m = e / vecs, v = e - m * vecs, k = k0 * H4_CHUNK + v * 8;
     uint4 w = make_uint4(0, 0, 0, 0);
     if (m < a.M && k < a.K) {
@@ -226,71 +253,98 @@ __global__ void __launch_bounds__(H4_THREADS, 1) k_head4(const Head4Args a) {
   }
   __syncthreads();
 
-  float acc[NT][4] = {};
-  bool timeout = false;
-  int slot = 0, part = 0, unit = 0;
-  uint32_t phase = 0;
-  for (int i = 0; i < total; ++i) {
-    if (!wait_phase<false>(&full[slot], phase, &abort)) abort = 1;
-    const int c0 = part * a.per_stage, n = min(a.per_stage, kn - c0);
-    const int tile = (cta + unit * a.ctas) * groups + rg;
-    if (tile < a.tiles) {
-      const char *blk = ring + (size_t)slot * a.stage_bytes + (size_t)rg * a.per_stage * a.block;
-      for (int j = ks; j < n; j += a.ks)
-        block_product<NT, SUBS>(acc, blk + j * a.block, xs + (c0 + j) * H4_CHUNK, ld, rows, a.zeros);
-    }
-    const bool done = part + 1 == parts;
-    float *r = red + (size_t)(unit & 1) * (H4_WARPS * NT * 8 * H4_COL);
-    if (done && a.ks > 1) {
-      // a tile's warps join: sums to shared memory
-      float *to = r + (size_t)warp * (NT * 8 * H4_COL) + (lane >> 2);
+  constexpr int WARP_SUMS = NT * 8 * H4_COL;
+  if (warp < WARPS) {
+    const int ks = warp % a.ks, rg = warp / a.ks, g = lane >> 2, c = lane & 3;
+    uint32_t xp[NT];   // the rows behind the last read the one of zeros
 #pragma unroll
-      for (int q = 0; q < NT; ++q)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) to[(q * 8 + 2 * (lane & 3) + (e & 1)) * H4_COL + 8 * (e >> 1)] = acc[q][e];
-    }
-    __syncthreads();   // the stage is read and the sums are there
-    timeout = abort != 0;
-    if (timeout) break;
-    if (t == 0 && i + a.stages < total) fill(i + a.stages);
-    if (done) {
+    for (int q = 0; q < NT; ++q) xp[q] = smem_u32(xs + (size_t)min(q * 8 + g, rows - 1) * ld + 8 * c);
+    float acc[NT][4] = {};
+    const bool zeros = a.zeros;
+    int slot = 0, part = 0, unit = 0;
+    uint32_t phase = 0;
+    for (int i = 0; i < total; ++i) {
+      if (!wait_phase<false>(&full[slot], phase, &abort)) {
+        abort = 1;
+        break;
+      }
+      const int c0 = part * a.per_stage, n = min(a.per_stage, kn - c0);
+      const int tile = (cta + unit * a.ctas) * groups + rg;
+      if (tile < a.tiles) {
+        const uint32_t blk = smem_u32(ring) + slot * a.stage_bytes + rg * a.per_stage * a.block;
+#pragma unroll NT == 1 ? 2 : 1
+        for (int j = ks; j < n; j += a.ks)
+          block_product<NT, SUBS>(acc, blk + j * a.block, xp, (c0 + j) * (2 * H4_CHUNK), zeros);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[slot]);
+      if (++slot == a.stages) slot = 0, phase ^= 1;
+      if (++part < parts) continue;
+      part = 0;
       if (a.ks > 1) {
-        // a thread per result; other warps take the first ones of the next unit
-        const int first = (t + H4_THREADS - unit * 128 % H4_THREADS) % H4_THREADS;
-        const int tile_rows = H4_TILE * groups;
-        for (int e = first; e < a.M * tile_rows; e += H4_THREADS) {
-          const int m = e / tile_rows, k = e - m * tile_rows;
-          const int nn = (cta + unit * a.ctas) * tile_rows + k;
-          if (nn >= a.N) continue;
-          const float *from = r + ((size_t)(k / H4_TILE * a.ks) * NT * 8 + m) * H4_COL + k % H4_TILE;
-          float z = 0.f;
-          for (int w = 0; w < a.ks; ++w) z += from[(size_t)w * (NT * 8 * H4_COL)];
-          result(a, slice, m, nn, z);
+        // to the joiners, who have read this buffer's last sums
+        if (unit >= 2 && !wait_phase<false>(&joined[unit & 1], (unit / 2 - 1) & 1, &abort)) {
+          abort = 1;
+          break;
         }
+        float *to = red + (size_t)((unit & 1) * WARPS + warp) * WARP_SUMS + g;
+#pragma unroll
+        for (int q = 0; q < NT; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to[(q * 8 + 2 * c + (e & 1)) * H4_COL + 8 * (e >> 1)] = acc[q][e];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sums[unit & 1]);
       } else {
 #pragma unroll
         for (int q = 0; q < NT; ++q)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int m = q * 8 + 2 * (lane & 3) + (e & 1), nn = tile * H4_TILE + (lane >> 2) + 8 * (e >> 1);
-            if (m < a.M && nn < a.N) result(a, slice, m, nn, acc[q][e]);
+            const int m = q * 8 + 2 * c + (e & 1), n1 = tile * H4_TILE + g + 8 * (e >> 1);
+            if (m < a.M && n1 < a.N) result(a, slice, m, n1, acc[q][e]);
           }
       }
 #pragma unroll
       for (int q = 0; q < NT; ++q) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.f;
+      ++unit;
     }
-    part = done ? 0 : part + 1;
-    unit += done;
-    if (++slot == a.stages) slot = 0, phase ^= 1;
-  }
-  if (timeout) {   // copies in flight end before the CTA does
-    if (t == 0) {
-      set_status(a.hdr, SPEC_ERR_TIMEOUT, blockIdx.x);
+  } else if (warp == WARPS) {
+    if (lane == 0) {
+      int issued = min(a.stages, total);
+      for (; issued < total; ++issued) {
+        if (!wait_phase<false>(&empty[issued % a.stages], (issued / a.stages - 1) & 1, &abort)) {
+          abort = 1;
+          break;
+        }
+        fill(issued);
+      }
+      // no copy is in flight when the CTA ends
       int none = 0;
-      for (int s = 0; s < a.stages; ++s) wait_phase<false>(&full[s], phase ^ (s < slot ? 1u : 0u), &none);
+      for (int i = max(0, issued - a.stages); i < issued; ++i) wait_phase<false>(&full[i % a.stages], (i / a.stages) & 1, &none);
     }
-    __syncthreads();
+  } else if (a.ks > 1) {
+    // a thread per result
+    const int tile_rows = H4_TILE * groups;
+    for (int unit = 0; unit < mine; ++unit) {
+      if (!wait_phase<false>(&sums[unit & 1], (unit / 2) & 1, &abort)) {
+        abort = 1;
+        break;
+      }
+      for (int e = t - 32 * (WARPS + 1); e < a.M * tile_rows; e += 32 * H4_JOINERS) {
+        const int m = e / tile_rows, k = e - m * tile_rows;
+        const int n1 = (cta + unit * a.ctas) * tile_rows + k;
+        if (n1 >= a.N) continue;
+        const float *from = red + (size_t)((unit & 1) * WARPS + k / H4_TILE * a.ks) * WARP_SUMS + m * H4_COL + k % H4_TILE;
+        float z = 0.f;
+#pragma unroll 4
+        for (int w = 0; w < a.ks; ++w) z += from[(size_t)w * WARP_SUMS];
+        result(a, slice, m, n1, z);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&joined[unit & 1]);
+    }
   }
+  __syncthreads();
+  if (t == 0 && abort) set_status(a.hdr, SPEC_ERR_TIMEOUT, blockIdx.x);
 }
 
 __global__ void __launch_bounds__(256) k_head4_join(Head4Args a) {
@@ -450,9 +504,9 @@ size_t forward4_bytes(int M, int N, int K) {
 
 template <int NT, int SUBS>
 int launch_head4(Head4Args &a, cudaStream_t st) {
-  const int rows = a.M + 1, groups = H4_WARPS / a.ks;
+  const int rows = a.M + 1, groups = warps_of(NT) / a.ks;
   const size_t x = (size_t)rows * (a.panel * H4_CHUNK + H4_PAD) * 2;
-  const size_t red = a.ks > 1 ? (size_t)2 * H4_WARPS * NT * 8 * H4_COL * 4 : 0;
+  const size_t red = a.ks > 1 ? (size_t)2 * warps_of(NT) * NT * 8 * H4_COL * 4 : 0;
   // whole rounds of the warps that share a tile, in four stages at least
   const size_t stage = std::min<size_t>(H4_STAGE, (H4_SMEM - x - red) / 4);
   const int rounds = std::max(1, (int)(stage / ((size_t)groups * a.block * a.ks)));
@@ -466,7 +520,7 @@ int launch_head4(Head4Args &a, cudaStream_t st) {
   const auto kern = k_head4<NT, SUBS>;
   static SmemLimit limit;
   return launch_retry(limit, (const void *)kern, smem, [&]() {
-    kern<<<(unsigned)(a.ctas * a.slices), H4_THREADS, smem, st>>>(a);
+    kern<<<(unsigned)(a.ctas * a.slices), threads_of(NT), smem, st>>>(a);
     return cudaGetLastError();
   });
 }
