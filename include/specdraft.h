@@ -387,8 +387,10 @@ int spec_head4_unpack(const void *packed, int has_zeros, int N, int K, int group
 
 /*
  * y = act(x W^T + bias) + residual for up to SPEC_HEAD4_MAX_ROWS rows and a W of
- * 4 bits (see above), as spec_head_forward. Products of x with code - zero are exact, their
- * sums and the scaled sums of the groups are held in 32 bits, y is rounded once.
+ * 4 bits (see above), as spec_head_forward. code - zero is exact, sums are held in 32 bits, y
+ * is rounded once. A row of x takes part in fp16, times a power of two that brings its largest value
+ * to 2^15: that is exact for what is down to 2^-29 of it, and further below
+ * within 2^-40 of it. A row of x with an infinity or NaN has results that are not finite.
  *
  *   x         [M, K] bf16, 0 <= M <= SPEC_HEAD4_MAX_ROWS; bias [N] or NULL;
  *             residual [M, N] or NULL. 1 <= N, K <= 2^24. x is 16-byte aligned, the

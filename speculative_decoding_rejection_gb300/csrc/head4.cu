@@ -3,27 +3,33 @@
 //
 //   y[m, n] = act(sum over groups g of s[n, g] sum over k in g of x[m, k] (q[n, k] - z[n, g]) + b[n]) + r[m, n]
 //
-// The weights are read once and bound the call: half a byte each, 2 to 64 multiply-adds
-// per weight. q - z is a small whole number, exact in bf16, so the inner sums are products of
-// the 16-bit tensor instruction (m16n8k16, f32 sums): 16 rows of the weight by 8 rows of
-// x. That leaves the SM about 16 instructions for 256 weights, where multiply-adds per
-// weight would take several times as many even for one row of x. The scales meet the
-// groups' sums in f32.
+// The weights are read once: half a byte each, and 2 to 64 multiply-adds per weight. The inner
+// sums are products of the 16-bit tensor instruction (m16n8k16, f32 sums): 16 rows of the
+// weight by 8 rows of x. Making 16-bit operands of the codes is what it costs, as at HBM's
+// rate an SM has 48 cycles for 2048 weights. So the operands are fp16: a code's 4 bits under
+// the exponent of 256 are 256 + q, under that of 16, four bits further left, 16 + q: one mask
+// each, one rotation for the other half of a word, and a subtraction of 256 + z or 16 + z, two
+// at a time. q - z is exact.
+//
+// x is held in fp16, each row times a power of two that brings its largest value to 2^15: 11 bits
+// hold bf16's 8, and what is more than 2^29 below a row's largest loses digits that no
+// sum of it would show.
 //
 // Layout. 16 rows and 128 columns make a block: 1024 bytes of codes, then their groups'
-// scales and zeros; a tile's blocks (16 rows, all columns) lie one behind the other and
-// the tiles too, so that what a CTA takes next is one run of memory, which bulk copies
-// bring to a ring in shared memory. Lane 4 g + c of the tensor instruction holds rows g and g +
+// scales and zeros. Two tiles (of 16 rows, all columns) make a pair, whose blocks lie one behind
+// the other chunk by chunk, and the pairs too, so that what a CTA takes next is one run of
+// memory, which bulk copies bring to a ring in shared memory. Lane 4 g + c of the tensor instruction holds rows g and g +
 // 8: 16 bytes of each, at 16 times the lane. Word j of them has the codes of columns 32 j + 8 c .. +
-// 7, so that every instruction's 16 columns lie in one group of 32, and its 4-bit fields
-// are in the order 0 2 4 6 1 3 5 7: fields i and i + 4, one mask apart, are two
-// neighbouring columns. 0x4300 | q is 128 + q in bf16, from which 128 + z is
-// subtracted, two at a time. The same lane's part of x is then 16 bytes of x as it lies.
+// 7, so that every instruction's 16 columns lie in one group of 32: 4-bit fields in the order 0 2 4
+// 6 1 3 5 7, so that fields i and i + 4, one mask apart, are two neighbouring columns, all
+// rotated left by two bits. The same lane's part of x is then 16 bytes of x as it lies.
 //
-// Work. x stays in shared memory. A CTA per SM takes unit after unit: up to 16 rows of x, a
-// tile whose columns its 16 warps share and join through shared memory; more rows, more
-// tiles with a warp each, as the join grows with x. Where x does not fit, CTAs take a
-// slice of the columns each and a second kernel joins their f32 sums.
+// Work. A CTA per SM takes unit after unit. Up to 8 rows of x: x stays in shared memory, and a
+// tile's columns are shared by 8 warps, whose sums three more warps join. More rows: a
+// warp has a tile to itself, and x, brought to fp16 and to the order of shared memory by a
+// kernel before, comes through the ring with the weights, from L2: for 256 rows of the
+// weight as many bytes as theirs. Where x does not fit (long rows), or where there are few
+// tiles, CTAs take a slice of the columns each and a last kernel joins their f32 sums.
 #include "draft.cuh"
 
 #include <algorithm>
@@ -31,11 +37,11 @@
 namespace sv {
 namespace {
 
-// Warps that multiply: more rows of x need more registers of each. One more fills the ring,
-// and some join the sums of those that share a tile. Registers are given to warps by four.
-__host__ __device__ constexpr int warps_of(int nt) { return nt <= 2 ? 16 : 8; }
+constexpr int H4_WARPS = 16;         // that multiply
+// Up to 8 rows of x: one more warp fills the ring and three join the sums of those that share a
+// tile. More: the first warp fills the ring too, as the others' registers are needed.
 constexpr int H4_JOINERS = 3;
-__host__ __device__ constexpr int threads_of(int nt) { return 32 * (warps_of(nt) + 1 + (nt <= 2 ? H4_JOINERS : 0)); }
+__host__ __device__ constexpr int threads_of(int nt) { return 32 * (H4_WARPS + (nt == 1 ? 1 + H4_JOINERS : 0)); }
 constexpr int H4_TILE = 16;          // rows of a tile
 constexpr int H4_CHUNK = 128;        // columns of a block
 constexpr int H4_CODES = H4_TILE * H4_CHUNK / 2;
@@ -44,10 +50,12 @@ constexpr int H4_COL = 20;           // floats between columns of a warp's sums,
 constexpr int H4_SMEM = 225 * 1024;
 constexpr int H4_STAGE = 36 * 1024;  // bytes of a ring stage, at most (or one round of the warps)
 constexpr int H4_MAX_STAGES = 8;
+constexpr int H4_DEPTH = 2;          // chunks of a stage with x
+constexpr int H4_X = 100 * 1024;     // bytes of x in shared memory, at most
 constexpr int H4_PLAN_SMS = 152;     // as the head's other products: a result's bits are the same on every device
 
 __host__ __device__ inline int chunks_of(int K) { return (K + H4_CHUNK - 1) / H4_CHUNK; }
-__host__ __device__ inline int tiles_of(int N) { return (N + H4_TILE - 1) / H4_TILE; }
+__host__ __device__ inline int tiles_of(int N) { return (N + 2 * H4_TILE - 1) / (2 * H4_TILE) * 2; }   // whole pairs
 // bytes of a block: codes, 16 bf16 scales and 16 zeros for each group
 __host__ __device__ inline int block_bytes(int group, bool zeros) {
   return H4_CODES + (H4_CHUNK / group) * H4_TILE * (zeros ? 3 : 2);
@@ -63,20 +71,22 @@ struct Plan4 {
 Plan4 plan4(int M, int N, int K) {
   Plan4 p{};
   p.nt = M <= 8 ? 1 : M <= 16 ? 2 : M <= 32 ? 4 : 8;
-  p.ks = p.nt == 1 ? 8 : p.nt == 2 ? 4 : 1;   // more rows make the join too large
   const int chunks = chunks_of(K);
-  const long long most = (p.nt <= 2 ? 100 : p.nt == 4 ? 110 : 140) * 1024;   // bytes of x
-  const long long fit = std::max(1ll, (most / (2 * (M + 1)) - H4_PAD) / H4_CHUNK);
+  p.ks = p.nt == 1 ? 8 : 1;
+  while (p.ks > chunks) p.ks /= 2;
+  const long long fit = p.nt == 1 ? (H4_X / (2 * (M + 1)) - H4_PAD) / H4_CHUNK : chunks;
   int slices = (int)((chunks + fit - 1) / fit);
-  while (p.ks > 1 && p.ks > chunks) p.ks /= 2;
-  // few units: more slices, as long as a slice has work for all warps that share a tile
-  const int groups = warps_of(p.nt) / p.ks;
+  // few units: more slices, as long as a slice has two chunks for all warps that share a tile
+  const int groups = H4_WARPS / p.ks;
   const long long units = (tiles_of(N) + groups - 1) / groups;
-  while (units * slices * 2 <= H4_PLAN_SMS && chunks / (2 * slices) >= std::max(2, p.ks)) slices *= 2;
+  while (units * slices * 2 <= H4_PLAN_SMS && chunks / (2 * slices) >= (p.nt == 1 ? p.ks : 2)) slices *= 2;
   p.panel = (chunks + slices - 1) / slices;
   p.slices = (chunks + p.panel - 1) / p.panel;
-  while (p.ks > 1 && p.ks > p.panel) p.ks /= 2;
+  while (p.ks > p.panel) p.ks /= 2;
   return p;
+}
+inline size_t x_bytes(const Plan4 &p, int K) {   // x in fp16, and its rows' powers
+  return p.nt == 1 ? 0 : align256((size_t)chunks_of(K) * 8 * p.nt * 2 * H4_CHUNK) + align256(8 * p.nt * 4);
 }
 
 struct Head4Args {
@@ -84,6 +94,8 @@ struct Head4Args {
   const char *packed;
   const __nv_bfloat16 *bias, *residual;
   __nv_bfloat16 *y;
+  uint4 *x16;        // more than 8 rows: [chunks][8 nt][16 pieces] of x in fp16, and
+  int *power;        // [8 nt]: that its rows' results are to be multiplied by, as powers of two
   float *part;       // [slices][M][N] sums of the slices, where there are several
   int M, N, K, group, zeros, act;
   int chunks, panel, slices, ks;
@@ -94,19 +106,11 @@ struct Head4Args {
   WsHeader *hdr;
 };
 
-// c = a b + (ADD ? c : 0)
-template <bool ADD>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if (ADD)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // Loads by the shared-memory address.
 __device__ __forceinline__ uint4 ld_s128(uint32_t at) {
@@ -124,48 +128,53 @@ __device__ __forceinline__ uint32_t ld_s16(uint32_t at) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
   return v;
 }
-// Fields i and i + 4 of a word less the zero (128 + z in both halves), as bf16.
+// Two codes at bits 2 to 5 of the halves less their zero (256 + z in both halves).
 __device__ __forceinline__ uint32_t less_zero(uint32_t w, uint32_t zero) {
   uint32_t v, r;
-  asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(v) : "r"(w));   // (w & mask) | 128.0
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(zero));
+  asm("lop3.b32 %0, %1, 0x003c003c, 0x5c005c00, 0xea;" : "=r"(v) : "r"(w));   // (w & mask) | 256.0
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(zero));
+  return r;
+}
+// Two codes at bits 6 to 9 of the halves less theirs (16 + z).
+__device__ __forceinline__ uint32_t less_zero_high(uint32_t w, uint32_t zero) {
+  uint32_t v, r;
+  asm("lop3.b32 %0, %1, 0x03c003c0, 0x4c004c00, 0xea;" : "=r"(v) : "r"(w));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(zero));
   return r;
 }
 
 // The sums of one block: acc += scale * (x times code - zero) group by group.
-// blk: the block's address; xs[q]: that of this lane's part of x for instruction q, at
-// the block's first column.
-template <int NT, int SUBS>
-__device__ __forceinline__ void block_product(float (&acc)[NT][4], uint32_t blk, const uint32_t (&xs)[NT], uint32_t col,
-                                              bool zeros) {
+// blk: the block's address; x(q, j): the 16 bytes of this lane's row of x of instruction q and
+// columns of word j.
+template <int NT, int SUBS, class X>
+__device__ __forceinline__ void block_product(float (&acc)[NT][4], uint32_t blk, bool zeros, X x) {
   constexpr int PER = 4 / SUBS;   // words of a group
   const uint32_t lane = threadIdx.x & 31, g = lane >> 2;
   const uint4 w[2] = {ld_s128(blk + lane * 16), ld_s128(blk + lane * 16 + 512)};
   float part[NT][4];
-  uint32_t z0 = 0x43084308u, z1 = 0x43084308u;
+  uint32_t z0 = 0x5c205c20u, z1 = 0x5c205c20u, h0 = 0x4e004e00u, h1 = 0x4e004e00u;   // 264 and 24
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    if (j % PER == 0 && zeros) {
-      const uint32_t z = ld_s16(blk + H4_CODES + SUBS * 32 + j / PER * 16 + g * 2);   // rows g and g + 8
-      z0 = 0x43004300u | (z & 15u) * 0x10001u;
-      z1 = 0x43004300u | (z >> 8 & 15u) * 0x10001u;
+    if (j % PER == 0) {
+#pragma unroll
+      for (int q = 0; q < NT; ++q) part[q][0] = part[q][1] = part[q][2] = part[q][3] = 0.f;
+      if (zeros) {
+        const uint32_t z = ld_s16(blk + H4_CODES + SUBS * 32 + j / PER * 16 + g * 2);   // rows g and g + 8
+        z0 = 0x5c005c00u | (z & 15u) * 0x40004u, h0 = 0x4c004c00u | (z & 15u) * 0x400040u;
+        z1 = 0x5c005c00u | (z >> 8 & 15u) * 0x40004u, h1 = 0x4c004c00u | (z >> 8 & 15u) * 0x400040u;
+      }
     }
     const uint32_t w0 = j == 0 ? w[0].x : j == 1 ? w[0].y : j == 2 ? w[0].z : w[0].w;
     const uint32_t w1 = j == 0 ? w[1].x : j == 1 ? w[1].y : j == 2 ? w[1].z : w[1].w;
-    uint32_t f[2][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      f[h][0] = less_zero(w0 >> (8 * h), z0);
-      f[h][1] = less_zero(w1 >> (8 * h), z1);
-      f[h][2] = less_zero(w0 >> (8 * h + 4), z0);
-      f[h][3] = less_zero(w1 >> (8 * h + 4), z1);
-    }
+    const uint32_t r0 = __funnelshift_r(w0, w0, 8), r1 = __funnelshift_r(w1, w1, 8);
+    const uint32_t f[2][4] = {
+        {less_zero(w0, z0), less_zero(w1, z1), less_zero_high(w0, h0), less_zero_high(w1, h1)},
+        {less_zero(r0, z0), less_zero(r1, z1), less_zero_high(r0, h0), less_zero_high(r1, h1)}};
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
-      const uint4 v = ld_s128(xs[q] + col + 64 * j);
-      if (j % PER == 0) mma<false>(part[q], f[0], v.x, v.y);
-      else mma<true>(part[q], f[0], v.x, v.y);
-      mma<true>(part[q], f[1], v.z, v.w);
+      const uint4 v = x(q, j);
+      mma(part[q], f[0], v.x, v.y);
+      mma(part[q], f[1], v.z, v.w);
     }
     if (j % PER == PER - 1) {
       const uint32_t s = ld_s32(blk + H4_CODES + j / PER * 32 + g * 4);
@@ -181,29 +190,103 @@ __device__ __forceinline__ void block_product(float (&acc)[NT][4], uint32_t blk,
   }
 }
 
-// A result: to y, or its slice's sum to `part`.
-__device__ __forceinline__ void result(const Head4Args &a, int slice, int m, int n, float z) {
+// x in fp16: eight columns of a row, 0 where it has none.
+__device__ __forceinline__ uint4 load_x(const Head4Args &a, int m, int k) {
+  uint4 w = make_uint4(0, 0, 0, 0);
+  if (m < a.M && k < a.K) {
+    const uint16_t *at = a.x + (long long)m * a.K + k;
+    if (k + 8 <= a.K && ((uintptr_t)at & 15) == 0) {
+      w = GLDG(reinterpret_cast<const uint4 *>(at));
+    } else {
+      uint32_t q[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = k + i < a.K ? GLDG(at + i) : 0u;
+      w = make_uint4(q[0] | q[1] << 16, q[2] | q[3] << 16, q[4] | q[5] << 16, q[6] | q[7] << 16);
+    }
+  }
+  return w;
+}
+__device__ __forceinline__ uint32_t largest(const uint4 &w) {   // magnitude, as bits of bf16
+  auto larger = [](uint32_t x) { return max(x & 0x7fffu, (x >> 16) & 0x7fffu); };
+  return max(max(larger(w.x), larger(w.y)), max(larger(w.z), larger(w.w)));
+}
+// The power of two that brings a row's largest value to 2^15; 0 for zeros, infinities and NaN.
+__device__ __forceinline__ int power_up(uint32_t largest) {
+  const float big = bf16_bits_to_f32(largest);
+  int up = 0;
+  if (!(big > 0.f && big <= 3.4e38f)) return 0;
+  frexpf(big, &up);
+  return 16 - up;
+}
+__device__ __forceinline__ uint4 to_f16(const uint4 &w, int up) {
+  const float f0 = ldexpf(1.f, up / 2), f1 = ldexpf(1.f, up - up / 2);
+  const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r[i]) : "f"(bf16hi(q[i]) * f0 * f1), "f"(bf16lo(q[i]) * f0 * f1));
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+// Piece v of row m of a chunk, in the order of shared memory: two rows' pieces lie in
+// different banks.
+__device__ __forceinline__ int piece_at(int m, int v) { return m * 16 + (v ^ (m & 1) << 2); }
+
+// More than 8 rows: a CTA per row brings it to fp16 and to the order of the ring.
+__global__ void __launch_bounds__(512) k_head4_x(Head4Args a, int rows) {
+  __shared__ uint32_t s_most;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int m = blockIdx.x, t = threadIdx.x, vecs = a.chunks * (H4_CHUNK / 8);
+  if (t == 0) s_most = 0;
+  __syncthreads();
+  constexpr int KEEP = 4;   // of a thread's pieces, those that are not read again
+  uint4 keep[KEEP];
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i) {
+    const int v = t + i * 512;
+    keep[i] = load_x(a, v < vecs ? m : a.M, v * 8);
+    most = max(most, largest(keep[i]));
+  }
+  for (int v = t + KEEP * 512; v < vecs; v += 512) most = max(most, largest(load_x(a, m, v * 8)));
+  most = __reduce_max_sync(~0u, most);
+  if ((t & 31) == 0) atomicMax(&s_most, most);
+  __syncthreads();
+  const int up = power_up(s_most);
+  if (t == 0) GST(a.power + m, -up);
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i) {
+    const int v = t + i * 512;
+    if (v < vecs) GST(a.x16 + (long long)(v / 16) * rows * 16 + piece_at(m, v % 16), to_f16(keep[i], up));
+  }
+  for (int v = t + KEEP * 512; v < vecs; v += 512)
+    GST(a.x16 + (long long)(v / 16) * rows * 16 + piece_at(m, v % 16), to_f16(load_x(a, m, v * 8), up));
+}
+
+// A result: to y, or its slice's sum to `part`. power: that of x's row.
+__device__ __forceinline__ void result(const Head4Args &a, int slice, int m, int n, float z, int power, float bias) {
   const long long at = (long long)m * a.N + n;
+  z = ldexpf(z, power);
   if (a.slices > 1) {
     GST(a.part + (long long)slice * a.M * a.N + at, z);
     return;
   }
-  if (a.bias) z += bf16_at(a.bias, n);
-  bf16_to(a.y, at, act_value(z, a.act) + (a.residual ? bf16_at(a.residual, at) : 0.f));
+  bf16_to(a.y, at, act_value(z + bias, a.act) + (a.residual ? bf16_at(a.residual, at) : 0.f));
 }
 
-template <int NT, int SUBS>
-__global__ void __launch_bounds__(threads_of(NT), 1) k_head4(const Head4Args a) {
+// Up to 8 rows of x.
+template <int SUBS>
+__global__ void __launch_bounds__(threads_of(1), 1) k_head4(const Head4Args a) {
   extern __shared__ __align__(128) unsigned char smem[];
-  constexpr int THREADS = threads_of(NT), WARPS = warps_of(NT);
+  constexpr int THREADS = threads_of(1), WARP_SUMS = 8 * H4_COL, KEEP = 8;
   __shared__ uint64_t full[H4_MAX_STAGES], empty[H4_MAX_STAGES], sums[2], joined[2];
   __shared__ int abort;
+  __shared__ uint32_t most[8];   // largest magnitudes of x's rows
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int rows = a.M + 1, ld = a.panel * H4_CHUNK + H4_PAD;
-  const int groups = WARPS / a.ks;   // tiles of a unit
+  const int groups = H4_WARPS / a.ks;   // tiles of a unit
   char *ring = reinterpret_cast<char *>(smem);
   uint16_t *xs = reinterpret_cast<uint16_t *>(ring + (size_t)a.stages * a.stage_bytes);   // [rows][ld]
-  float *red = reinterpret_cast<float *>(xs + (size_t)rows * ld);                         // [2][warps][NT][8][H4_COL]
+  float *red = reinterpret_cast<float *>(xs + (size_t)rows * ld);                         // [2][warps][8][H4_COL]
   const int slice = blockIdx.x / a.ctas, cta = blockIdx.x % a.ctas;
   const int k0 = slice * a.panel, kn = min(a.panel, a.chunks - k0);   // chunks of this slice
   const int parts = (kn + a.per_stage - 1) / a.per_stage;             // stages of a unit
@@ -214,10 +297,11 @@ __global__ void __launch_bounds__(threads_of(NT), 1) k_head4(const Head4Args a) 
 
   if (t == 0) {
     abort = 0;
-    for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], WARPS);
-    for (int s = 0; s < 2; ++s) mbar_init(&sums[s], WARPS), mbar_init(&joined[s], H4_JOINERS);
+    for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], H4_WARPS);
+    for (int s = 0; s < 2; ++s) mbar_init(&sums[s], H4_WARPS), mbar_init(&joined[s], H4_JOINERS);
     fence_mbar_init();
   }
+  if (t < 8) most[t] = 0;
   __syncthreads();
   // stage i of this CTA: unit i / parts, chunks from (i % parts) per_stage on
   auto fill = [&](int i) {
@@ -226,41 +310,55 @@ __global__ void __launch_bounds__(threads_of(NT), 1) k_head4(const Head4Args a) 
     char *dst = ring + (size_t)(i % a.stages) * a.stage_bytes;
     uint64_t *bar = &full[i % a.stages];
     mbar_arrive_tx(bar, (uint32_t)(tiles * n * a.block));
-    for (int g = 0; g < tiles; ++g)
+    for (int g = 0; g < tiles; g += 2)
       bulk_g2s(dst + (size_t)g * a.per_stage * a.block,
-               a.packed + ((long long)(u * groups + g) * a.chunks + k0 + c0) * a.block, (uint32_t)(n * a.block), bar);
+               a.packed + ((long long)(u * groups + g) * a.chunks + 2 * (k0 + c0)) * a.block, (uint32_t)(2 * n * a.block), bar);
   };
-  if (t == 32 * WARPS)
+  if (t == 32 * H4_WARPS)
     for (int i = 0; i < min(a.stages, total); ++i) fill(i);
 
-  // x's slice, zeros behind its end and in the last row
+  // x's slice in fp16, zeros behind its end and in the last row; 16 threads have 128 columns
+  // of a row. What a thread reads first it keeps.
   const int vecs = a.panel * (H4_CHUNK / 8);
-  for (int e = t; e < rows * vecs; e += THREADS) {
-    const int m = e / vecs, v = e - m * vecs, k = k0 * H4_CHUNK + v * 8;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (m < a.M && k < a.K) {
-      const uint16_t *at = a.x + (long long)m * a.K + k;
-      if (k + 8 <= a.K && ((uintptr_t)at & 15) == 0) {
-        w = GLDG(reinterpret_cast<const uint4 *>(at));
-      } else {
-        uint32_t q[8];
+  {
+    const uint32_t half = 0xffffu << (lane & 16);
+    uint4 keep[KEEP];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = k + i < a.K ? GLDG(at + i) : 0u;
-        w = make_uint4(q[0] | q[1] << 16, q[2] | q[3] << 16, q[4] | q[5] << 16, q[6] | q[7] << 16);
-      }
+    for (int i = 0; i < KEEP; ++i) {
+      const int e = t + i * THREADS, m = e / vecs;
+      keep[i] = load_x(a, e < rows * vecs ? m : a.M, (k0 * (H4_CHUNK / 8) + e - m * vecs) * 8);
     }
-    *reinterpret_cast<uint4 *>(xs + (size_t)m * ld + v * 8) = w;
+    auto raise = [&](int m, const uint4 &w) {
+      const uint32_t x = __reduce_max_sync(half, largest(w));
+      if ((lane & 15) == 0 && x != 0) atomicMax(&most[m], x);
+    };
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i)
+      if (t + i * THREADS < a.M * vecs) raise((t + i * THREADS) / vecs, keep[i]);
+    for (int e = t + KEEP * THREADS; e < a.M * vecs; e += THREADS)
+      raise(e / vecs, load_x(a, e / vecs, (k0 * (H4_CHUNK / 8) + e % vecs) * 8));
+    __syncthreads();
+    auto place = [&](int e, const uint4 &w) {
+      const int m = e / vecs, v = e - m * vecs;
+      *reinterpret_cast<uint4 *>(xs + (size_t)m * ld + v * 8) = to_f16(w, m < a.M ? power_up(most[m]) : 0);
+    };
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i)
+      if (t + i * THREADS < rows * vecs) place(t + i * THREADS, keep[i]);
+    for (int e = t + KEEP * THREADS; e < rows * vecs; e += THREADS)
+      place(e, load_x(a, e / vecs, (k0 * (H4_CHUNK / 8) + e % vecs) * 8));
   }
   __syncthreads();
 
-  constexpr int WARP_SUMS = NT * 8 * H4_COL;
-  if (warp < WARPS) {
+  if (warp < H4_WARPS) {
     const int ks = warp % a.ks, rg = warp / a.ks, g = lane >> 2, c = lane & 3;
-    uint32_t xp[NT];   // the rows behind the last read the one of zeros
-#pragma unroll
-    for (int q = 0; q < NT; ++q) xp[q] = smem_u32(xs + (size_t)min(q * 8 + g, rows - 1) * ld + 8 * c);
-    float acc[NT][4] = {};
+    // addresses of this warp's first block of a stage and the steps between its blocks
+    const int ks_all = a.ks, stage_bytes = a.stage_bytes;
+    const uint32_t step_blk = 2 * ks_all * a.block, step_col = ks_all * (2 * H4_CHUNK), part_cols = a.per_stage * (2 * H4_CHUNK);
+    const uint32_t at_ring = smem_u32(ring) + ((rg / 2 * a.per_stage + ks) * 2 + rg % 2) * a.block;
+    const uint32_t col0 = smem_u32(xs + (size_t)min(g, rows - 1) * ld + 8 * c) + ks * (2 * H4_CHUNK);   // the last row is zero
     const bool zeros = a.zeros;
+    float acc[1][4] = {};
     int slot = 0, part = 0, unit = 0;
     uint32_t phase = 0;
     for (int i = 0; i < total; ++i) {
@@ -268,46 +366,33 @@ __global__ void __launch_bounds__(threads_of(NT), 1) k_head4(const Head4Args a) 
         abort = 1;
         break;
       }
-      const int c0 = part * a.per_stage, n = min(a.per_stage, kn - c0);
-      const int tile = (cta + unit * a.ctas) * groups + rg;
-      if (tile < a.tiles) {
-        const uint32_t blk = smem_u32(ring) + slot * a.stage_bytes + rg * a.per_stage * a.block;
-#pragma unroll NT == 1 ? 2 : 1
-        for (int j = ks; j < n; j += a.ks)
-          block_product<NT, SUBS>(acc, blk + j * a.block, xp, (c0 + j) * (2 * H4_CHUNK), zeros);
+      const int n = min(a.per_stage, kn - part * a.per_stage);
+      if ((cta + unit * a.ctas) * groups + rg < a.tiles) {
+        uint32_t blk = at_ring + slot * stage_bytes, col = col0 + part * part_cols;
+        for (int j = ks; j < n; j += ks_all) {
+          block_product<1, SUBS>(acc, blk, zeros, [&](int, int w) { return ld_s128(col + 64 * w); });
+          blk += step_blk, col += step_col;
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[slot]);
       if (++slot == a.stages) slot = 0, phase ^= 1;
       if (++part < parts) continue;
       part = 0;
-      if (a.ks > 1) {
-        // to the joiners, who have read this buffer's last sums
-        if (unit >= 2 && !wait_phase<false>(&joined[unit & 1], (unit / 2 - 1) & 1, &abort)) {
-          abort = 1;
-          break;
-        }
-        float *to = red + (size_t)((unit & 1) * WARPS + warp) * WARP_SUMS + g;
-#pragma unroll
-        for (int q = 0; q < NT; ++q)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) to[(q * 8 + 2 * c + (e & 1)) * H4_COL + 8 * (e >> 1)] = acc[q][e];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sums[unit & 1]);
-      } else {
-#pragma unroll
-        for (int q = 0; q < NT; ++q)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int m = q * 8 + 2 * c + (e & 1), n1 = tile * H4_TILE + g + 8 * (e >> 1);
-            if (m < a.M && n1 < a.N) result(a, slice, m, n1, acc[q][e]);
-          }
+      // to the joiners, who have read this buffer's last sums
+      if (unit >= 2 && !wait_phase<false>(&joined[unit & 1], (unit / 2 - 1) & 1, &abort)) {
+        abort = 1;
+        break;
       }
+      float *to = red + (size_t)((unit & 1) * H4_WARPS + warp) * WARP_SUMS + g;
 #pragma unroll
-      for (int q = 0; q < NT; ++q) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.f;
+      for (int e = 0; e < 4; ++e) to[(2 * c + (e & 1)) * H4_COL + 8 * (e >> 1)] = acc[0][e];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sums[unit & 1]);
+      acc[0][0] = acc[0][1] = acc[0][2] = acc[0][3] = 0.f;
       ++unit;
     }
-  } else if (warp == WARPS) {
+  } else if (warp == H4_WARPS) {
     if (lane == 0) {
       int issued = min(a.stages, total);
       for (; issued < total; ++issued) {
@@ -321,27 +406,133 @@ __global__ void __launch_bounds__(threads_of(NT), 1) k_head4(const Head4Args a) 
       int none = 0;
       for (int i = max(0, issued - a.stages); i < issued; ++i) wait_phase<false>(&full[i % a.stages], (i / a.stages) & 1, &none);
     }
-  } else if (a.ks > 1) {
-    // a thread per result
-    const int tile_rows = H4_TILE * groups;
+  } else {
+    // a lane per row of the weight, a warp per row of x
+    const int first = warp - H4_WARPS - 1, tile_rows = H4_TILE * groups;
     for (int unit = 0; unit < mine; ++unit) {
+      const int n0 = (cta + unit * a.ctas) * tile_rows + lane;
+      // the bias is on its way while the sums are made
+      float bias = a.bias != nullptr && a.slices == 1 && lane < tile_rows && n0 < a.N ? bf16_at(a.bias, n0) : 0.f;
       if (!wait_phase<false>(&sums[unit & 1], (unit / 2) & 1, &abort)) {
         abort = 1;
         break;
       }
-      for (int e = t - 32 * (WARPS + 1); e < a.M * tile_rows; e += 32 * H4_JOINERS) {
-        const int m = e / tile_rows, k = e - m * tile_rows;
-        const int n1 = (cta + unit * a.ctas) * tile_rows + k;
-        if (n1 >= a.N) continue;
-        const float *from = red + (size_t)((unit & 1) * WARPS + k / H4_TILE * a.ks) * WARP_SUMS + m * H4_COL + k % H4_TILE;
-        float z = 0.f;
-#pragma unroll 4
-        for (int w = 0; w < a.ks; ++w) z += from[(size_t)w * WARP_SUMS];
-        result(a, slice, m, n1, z);
+      for (int k = lane; k < tile_rows; k += 32) {
+        const int n = n0 - lane + k;
+        if (n >= a.N) continue;
+        if (k != lane) bias = a.bias != nullptr && a.slices == 1 ? bf16_at(a.bias, n) : 0.f;
+        const float *from = red + (size_t)((unit & 1) * H4_WARPS + k / H4_TILE * a.ks) * WARP_SUMS + k % H4_TILE;
+        for (int m = first; m < a.M; m += H4_JOINERS) {
+          float z = 0.f;
+#pragma unroll 8
+          for (int w = 0; w < a.ks; ++w) z += from[(size_t)w * WARP_SUMS + m * H4_COL];
+          result(a, slice, m, n, z, -power_up(most[m]), bias);
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&joined[unit & 1]);
     }
+  }
+  __syncthreads();
+  if (t == 0 && abort) set_status(a.hdr, SPEC_ERR_TIMEOUT, blockIdx.x);
+}
+
+// More than 8 rows of x: a stage is two chunks of columns, of x first, then of a tile per warp.
+template <int NT, int SUBS>
+__global__ void __launch_bounds__(threads_of(NT), 1) k_head4_rows(const Head4Args a) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  constexpr int XB = 8 * NT * 2 * H4_CHUNK;   // bytes of x's chunk
+  __shared__ uint64_t full[H4_MAX_STAGES], empty[H4_MAX_STAGES];
+  __shared__ int abort;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, g = lane >> 2, c = lane & 3;
+  char *ring = reinterpret_cast<char *>(smem);
+  const int slice = blockIdx.x / a.ctas, cta = blockIdx.x % a.ctas;
+  const int k0 = slice * a.panel, kn = min(a.panel, a.chunks - k0);   // chunks of this slice
+  const int parts = (kn + H4_DEPTH - 1) / H4_DEPTH;
+  const int units = (a.tiles + H4_WARPS - 1) / H4_WARPS;
+  const int mine = cta < units ? (units - cta + a.ctas - 1) / a.ctas : 0;
+  const int total = mine * parts;                                     // stages of this CTA
+  if (blockIdx.x == 0 && t == 0) start_status(a.hdr);
+  if (t == 0) {
+    abort = 0;
+    for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], H4_WARPS);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  // by the first warp, a copy per lane: the weights of stage i, and x's part
+  auto fill_w = [&](int i) {
+    const int u = cta + i / parts * a.ctas, c0 = i % parts * H4_DEPTH, n = min(H4_DEPTH, kn - c0);
+    const int tiles = min(H4_WARPS, a.tiles - u * H4_WARPS);
+    uint64_t *bar = &full[i % a.stages];
+    if (lane == 0) mbar_arrive_tx(bar, (uint32_t)(n * (tiles * a.block + XB)));
+    __syncwarp();
+    if (2 * lane < tiles)
+      bulk_g2s(ring + (size_t)(i % a.stages) * a.stage_bytes + H4_DEPTH * (XB + (size_t)2 * lane * a.block),
+               a.packed + ((long long)(u * H4_WARPS + 2 * lane) * a.chunks + 2 * (k0 + c0)) * a.block,
+               (uint32_t)(2 * n * a.block), bar);
+  };
+  auto fill_x = [&](int i) {
+    const int c0 = i % parts * H4_DEPTH, n = min(H4_DEPTH, kn - c0);
+    if (lane == 0)
+      bulk_g2s(ring + (size_t)(i % a.stages) * a.stage_bytes, reinterpret_cast<const char *>(a.x16) + (long long)(k0 + c0) * XB,
+               (uint32_t)(n * XB), &full[i % a.stages]);
+  };
+  const int ahead = min(a.stages, total);
+  if (warp == 0)
+    for (int i = 0; i < ahead; ++i) fill_w(i);   // these wait for no other kernel
+  after_previous();
+  if (warp == 0)
+    for (int i = 0; i < ahead; ++i) fill_x(i);
+  int issued = ahead;
+
+  uint32_t xp[4];   // this lane's piece of word j in row g of 8 rows of x
+#pragma unroll
+  for (int j = 0; j < 4; ++j) xp[j] = smem_u32(ring) + 16 * piece_at(g, 4 * j + c);
+  const uint32_t wp = smem_u32(ring) + H4_DEPTH * (XB + warp / 2 * 2 * a.block) + warp % 2 * a.block;
+  const bool zeros = a.zeros;
+  float acc[NT][4] = {};
+  int slot = 0, part = 0, unit = 0;
+  uint32_t phase = 0;
+  for (int i = 0; i < total; ++i) {
+    if (!wait_phase<false>(&full[slot], phase, &abort)) {
+      abort = 1;
+      break;
+    }
+    const int tile = (cta + unit * a.ctas) * H4_WARPS + warp, n = min(H4_DEPTH, kn - part * H4_DEPTH);
+    if (tile < a.tiles) {
+      uint32_t x = slot * a.stage_bytes, blk = wp + x;
+      for (int k = 0; k < n; ++k) {
+        block_product<NT, SUBS>(acc, blk, zeros, [&](int q, int j) { return ld_s128(xp[j] + x + q * (8 * 2 * H4_CHUNK)); });
+        x += XB, blk += 2 * a.block;
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[slot]);
+    if (warp == 0 && i > 0 && issued < total) {   // the stage before is read by all, or soon
+      if (!wait_phase<false>(&empty[issued % a.stages], (issued / a.stages - 1) & 1, &abort)) {
+        abort = 1;
+        break;
+      }
+      fill_w(issued), fill_x(issued);
+      ++issued;
+    }
+    if (++slot == a.stages) slot = 0, phase ^= 1;
+    if (++part < parts) continue;
+    part = 0;
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int m = q * 8 + 2 * c + (e & 1), n1 = tile * H4_TILE + g + 8 * (e >> 1);
+        if (m < a.M && n1 < a.N)
+          result(a, slice, m, n1, acc[q][e], GLD(a.power + m), a.bias != nullptr && a.slices == 1 ? bf16_at(a.bias, n1) : 0.f);
+        acc[q][e] = 0.f;
+      }
+    ++unit;
+  }
+  if (t == 0) {   // no copy is in flight when the CTA ends
+    int none = 0;
+    for (int i = max(0, issued - a.stages); i < issued; ++i) wait_phase<false>(&full[i % a.stages], (i / a.stages) & 1, &none);
   }
   __syncthreads();
   if (t == 0 && abort) set_status(a.hdr, SPEC_ERR_TIMEOUT, blockIdx.x);
@@ -356,7 +547,8 @@ __global__ void __launch_bounds__(256) k_head4_join(Head4Args a) {
     float z = 0.f;
     for (int s = 0; s < slices; ++s) z += GLDCG(a.part + s * n + i);
     const int m = (int)(i / a.N);
-    result(a, 0, m, (int)(i - (long long)m * a.N), z);
+    const int j = (int)(i - (long long)m * a.N);
+    result(a, 0, m, j, z, 0, a.bias ? bf16_at(a.bias, j) : 0.f);
   }
 }
 
@@ -376,16 +568,17 @@ __device__ __forceinline__ bool word_of(long long i, int tiles, int chunks, Word
   const int j = e / 4, c = e % 4, r = (int)(n % H4_TILE);
   w.row = (int)n;
   w.col = k * H4_CHUNK + e * 8;
-  w.block = n / H4_TILE * chunks + k;
+  w.block = (n / (2 * H4_TILE) * chunks + k) * 2 + n / H4_TILE % 2;
   w.at = (r / 8) * 128 + ((r % 8) * 4 + c) * 4 + j;
   return true;
 }
-// Codes of eight columns, 4 bits each in their order, in the order of a word, and back.
+// Codes of eight columns, 4 bits each in their order, in the order of a word.
 __device__ __forceinline__ uint32_t in_word_order(uint32_t v) {
   uint32_t even = v & 0x0f0f0f0fu, odd = (v >> 4) & 0x0f0f0f0fu;
   even = (even | even >> 4) & 0x00ff00ffu;
   odd = (odd | odd >> 4) & 0x00ff00ffu;
-  return ((even | even >> 8) & 0xffffu) | (odd | odd >> 8) << 16;
+  v = ((even | even >> 8) & 0xffffu) | (odd | odd >> 8) << 16;
+  return v << 2 | v >> 30;
 }
 // Place of a row's scale (or zero) of a group: rows g and g + 8 side by side.
 __device__ __forceinline__ int pair_at(int row, int sub) {
@@ -471,7 +664,8 @@ __global__ void __launch_bounds__(256) k_unpack4(Layout4 l, uint16_t *weight) {
   Word w;
   if (!word_of((long long)blockIdx.x * 256 + threadIdx.x, l.tiles, l.chunks, w) || w.row >= l.N || w.col >= l.K) return;
   const char *blk = l.packed + w.block * l.block;
-  const uint32_t v = GLDG(reinterpret_cast<const uint32_t *>(blk) + w.at);
+  uint32_t v = GLDG(reinterpret_cast<const uint32_t *>(blk) + w.at);
+  v = v >> 2 | v << 30;
   const int at = pair_at(w.row, w.col % H4_CHUNK / l.group);
   const float s = bf16_bits_to_f32(GLDG(reinterpret_cast<const uint16_t *>(blk + H4_CODES) + at));
   const int z = l.zeros ? GLDG(reinterpret_cast<const uint8_t *>(blk + H4_CODES + H4_CHUNK / l.group * 32) + at) : 8;
@@ -499,14 +693,13 @@ Layout4 layout4(void *packed, int N, int K, int group, bool zeros) {
 
 size_t forward4_bytes(int M, int N, int K) {
   const Plan4 p = plan4(std::max(M, 1), N, K);
-  return sizeof(WsHeader) + (p.slices > 1 ? align256((size_t)p.slices * M * N * 4) : 0);
+  return sizeof(WsHeader) + x_bytes(p, K) + (p.slices > 1 ? align256((size_t)p.slices * M * N * 4) : 0);
 }
 
-template <int NT, int SUBS>
+template <int SUBS>
 int launch_head4(Head4Args &a, cudaStream_t st) {
-  const int rows = a.M + 1, groups = warps_of(NT) / a.ks;
-  const size_t x = (size_t)rows * (a.panel * H4_CHUNK + H4_PAD) * 2;
-  const size_t red = a.ks > 1 ? (size_t)2 * warps_of(NT) * NT * 8 * H4_COL * 4 : 0;
+  const int rows = a.M + 1, groups = H4_WARPS / a.ks;
+  const size_t x = (size_t)rows * (a.panel * H4_CHUNK + H4_PAD) * 2, red = (size_t)2 * H4_WARPS * 8 * H4_COL * 4;
   // whole rounds of the warps that share a tile, in four stages at least
   const size_t stage = std::min<size_t>(H4_STAGE, (H4_SMEM - x - red) / 4);
   const int rounds = std::max(1, (int)(stage / ((size_t)groups * a.block * a.ks)));
@@ -517,17 +710,37 @@ int launch_head4(Head4Args &a, cudaStream_t st) {
   const int smem = (int)(a.stages * a.stage_bytes + x + red);
   const int units = (a.tiles + groups - 1) / groups;
   a.ctas = std::max(1, std::min(units, H4_PLAN_SMS / a.slices));
-  const auto kern = k_head4<NT, SUBS>;
+  const auto kern = k_head4<SUBS>;
   static SmemLimit limit;
   return launch_retry(limit, (const void *)kern, smem, [&]() {
-    kern<<<(unsigned)(a.ctas * a.slices), threads_of(NT), smem, st>>>(a);
+    kern<<<(unsigned)(a.ctas * a.slices), threads_of(1), smem, st>>>(a);
     return cudaGetLastError();
   });
 }
-template <int NT>
-int launch_head4(Head4Args &a, cudaStream_t st) {
-  return a.group == 128 ? launch_head4<NT, 1>(a, st)
-                        : a.group == 64 ? launch_head4<NT, 2>(a, st) : launch_head4<NT, 4>(a, st);
+template <int NT, int SUBS>
+int launch_rows(Head4Args &a, cudaStream_t st) {
+  k_head4_x<<<8 * NT, 512, 0, st>>>(a, 8 * NT);
+  if (launched() != SPEC_OK) return SPEC_ERR_CUDA;
+  a.stage_bytes = (H4_DEPTH * (8 * NT * 2 * H4_CHUNK + H4_WARPS * a.block) + 127) / 128 * 128;
+  a.stages = std::min(H4_MAX_STAGES, H4_SMEM / a.stage_bytes);
+  const int smem = a.stages * a.stage_bytes, units = (a.tiles + H4_WARPS - 1) / H4_WARPS;
+  a.ctas = std::max(1, std::min(units, H4_PLAN_SMS / a.slices));
+  const auto kern = k_head4_rows<NT, SUBS>;
+  static SmemLimit limit;
+  cudaLaunchAttribute at[1] = {launch_early()};
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(a.ctas * a.slices), 1, 1);
+  cfg.blockDim = dim3(threads_of(NT), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return launch_retry(limit, (const void *)kern, smem, [&]() { return cudaLaunchKernelEx(&cfg, kern, a); });
+}
+template <int SUBS>
+int launch_group(Head4Args &a, int nt, cudaStream_t st) {
+  return nt == 1 ? launch_head4<SUBS>(a, st) : nt == 2 ? launch_rows<2, SUBS>(a, st)
+         : nt == 4 ? launch_rows<4, SUBS>(a, st) : launch_rows<8, SUBS>(a, st);
 }
 
 }  // namespace
@@ -623,7 +836,10 @@ extern "C" int spec_head4_forward(const void *x, const void *packed, int has_zer
   a.bias = static_cast<const __nv_bfloat16 *>(bias);
   a.residual = static_cast<const __nv_bfloat16 *>(residual);
   a.y = static_cast<__nv_bfloat16 *>(y);
-  a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + sizeof(WsHeader));
+  char *ws = static_cast<char *>(workspace) + sizeof(WsHeader);
+  a.x16 = reinterpret_cast<uint4 *>(ws);
+  a.part = reinterpret_cast<float *>(ws + x_bytes(p, K));
+  a.power = reinterpret_cast<int *>(reinterpret_cast<char *>(a.part) - align256(8 * p.nt * 4));   // (with x16 alone)
   a.M = M, a.N = N, a.K = K, a.group = group, a.zeros = has_zeros != 0, a.act = act;
   a.chunks = chunks_of(K), a.panel = p.panel, a.slices = p.slices, a.ks = p.ks;
   a.tiles = tiles_of(N), a.block = block_bytes(group, a.zeros);
@@ -639,8 +855,8 @@ extern "C" int spec_head4_forward(const void *x, const void *packed, int has_zer
   if (reset_header(workspace, st) != SPEC_OK) return SPEC_ERR_CUDA;
 #endif
   if (check_upload(st) != SPEC_OK) return SPEC_ERR_CUDA;
-  const int rc = p.nt == 1 ? launch_head4<1>(a, st) : p.nt == 2 ? launch_head4<2>(a, st)
-                 : p.nt == 4 ? launch_head4<4>(a, st) : launch_head4<8>(a, st);
+  const int rc = group == 128 ? launch_group<1>(a, p.nt, st)
+                 : group == 64 ? launch_group<2>(a, p.nt, st) : launch_group<4>(a, p.nt, st);
   if (rc != SPEC_OK || a.slices == 1) return rc;
   cudaLaunchAttribute at[1] = {launch_early()};
   cudaLaunchConfig_t cfg{};

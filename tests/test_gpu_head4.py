@@ -39,14 +39,16 @@ def weight(rng, N, K, group, zeros):
 def reference(x, w, bias, residual, act, group):
     """(y, tolerance): sums of K products in 32 bits, a step of 2^-22 of the magnitudes for each
     instruction, group, warp and slice that they go through (the tensor cores' sums may be cut, not
-    rounded), an activation of slope 1.13 at most within 2^-20, one rounding to bf16."""
+    rounded), x within 2^-40 of its row's largest, an activation of slope 1.13 at most within 2^-20,
+    one rounding to bf16."""
     K = x.shape[1]
     z, size = x @ w.T, np.abs(x) @ np.abs(w).T
     steps = group // 16 + -(-K // group) + 16 + -(-K // 128)
+    lost = 2.0 ** -40 * np.abs(x).max(1, initial=0)[:, None] * np.abs(w).sum(1)[None]
     if bias is not None:
         z, size = z + bias, size + np.abs(bias)
     y = O.act(z, act)
-    err = 1.2 * steps * 2.0 ** -22 * size + 2.0 ** -20 * np.abs(y)
+    err = 1.2 * (steps * 2.0 ** -22 * size + lost) + 2.0 ** -20 * np.abs(y)
     if residual is not None:
         y = y + residual
     return y, err + HALF * (np.abs(y) + err) + 1e-38
@@ -92,6 +94,23 @@ def test_many_tiles():
         assert (np.abs(f64(y) - want) <= tol).all()
         for m in range(3):
             assert torch.equal(sv.spec_head4_forward(x[m:m + 1], w)[0], y[m:m + 1])
+
+
+@pytest.mark.parametrize("scale", [1e-37, 1e-12, 1e20, 3e37])
+def test_rows_of_any_size(scale):
+    """x of few and of many binades: rows are brought to fp16's range."""
+    rng = np.random.default_rng(8)
+    w, ref_w = weight(rng, 100, 520, 64, 1)
+    x = rng.normal(size=(6, 520)) * min(scale, 1e36)
+    x[1] *= 2.0 ** rng.integers(-60, 0, 520)
+    x[2, 3:] = 0
+    x[3] = 0
+    x[4, 100] *= 2.0 ** 30 if scale < 1e20 else 4
+    x = bf(x)
+    y, _ = sv.spec_head4_forward(x, w)
+    want, tol = reference(f64(x), ref_w, None, None, "none", 64)
+    assert (np.abs(f64(y) - want) <= tol).all()
+    assert bool((y[3] == 0).all())
 
 
 @pytest.mark.parametrize("M", [1, 12, 64])

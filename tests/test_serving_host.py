@@ -96,9 +96,9 @@ def test_head4_unpack_refuses_bad_arguments(L, kw, code):
 
 
 def test_head4_sizes(L):
-    size = L.spec_head4_packed_bytes      # blocks of 16 rows and 128 columns, scales and zeros behind each
-    assert size(3, 1, 128, 0) == 1024 + 32 and size(17, 129, 32, 0) == 4 * (1024 + 128)
-    assert size(16, 128, 64, 1) == 1024 + 64 + 32 and size(0, 8, 32, 0) == 0 and size(8, 8, 8, 0) == 0
+    size = L.spec_head4_packed_bytes      # two blocks of 16 rows and 128 columns, scales and zeros behind each
+    assert size(3, 1, 128, 0) == 2 * (1024 + 32) and size(33, 129, 32, 0) == 8 * (1024 + 128)
+    assert size(32, 128, 64, 1) == 2 * (1024 + 64 + 32) and size(0, 8, 32, 0) == 0 and size(8, 8, 8, 0) == 0
     assert sv.spec_head4_forward_workspace(0, 4, 4) >= 256
     assert sv.spec_head4_forward_workspace(65, 4, 4) == 0
 
