@@ -28,7 +28,7 @@ struct NormArgs {
   const AdHeader *table;
   long long n_items;
   int state_bits, inf;
-  double max_norm;
+  float max_norm;
   const float *grad_scale;
   float *out;
   double *part;      // one per CTA of the first kernel
@@ -182,6 +182,16 @@ __global__ void __launch_bounds__(GN_THREADS, GN_CTAS_PER_SM) k_grad_norm(const 
   if (threadIdx.x == 0) a.part[blockIdx.x] = sum;
 }
 
+// The root of a sum of squares in f32: of the leading 24 bits of a mantissa over an even
+// power, within a step of the last place. (A root and a quotient of 64 bits take microseconds.)
+__device__ __forceinline__ float root(double x) {
+  if (!(x > 0.0 && x <= 1.7976931348623157e308)) return (float)x;   // zero, infinity, NaN
+  const long long bits = __double_as_longlong(x);
+  const int e = (int)(bits >> 52) - 1023, even = e & ~1;   // (a sum of squares that are no f32 zero is normal)
+  const float m = (float)__longlong_as_double((bits & 0xfffffffffffffll) | (long long)(1023 + e - even) << 52);
+  return ldexpf(__fsqrt_rn(m), even / 2);
+}
+
 // The norm and the factor, in thread 0.
 __device__ __forceinline__ void join(const NormArgs &a, float *norm, float *factor) {
   double x = 0.0;
@@ -190,12 +200,12 @@ __device__ __forceinline__ void join(const NormArgs &a, float *norm, float *fact
     x = a.inf ? (x >= y || x != x ? x : y) : x + y;
   }
   x = block_join(x, a.inf);
-  const double s = a.grad_scale ? (double)*a.grad_scale : 1.0;
-  const double n = fabs(s) * (a.inf ? x : sqrt(x));
-  const double f = a.max_norm / (n + 1e-6);
-  *norm = (float)n;
-  // a NaN passes through: it is below nothing
-  *factor = (float)(s * (f >= 1.0 ? 1.0 : f));
+  if (threadIdx.x != 0) return;
+  const float s = a.grad_scale ? *a.grad_scale : 1.f;
+  const float n = fabsf(s) * (a.inf ? (float)x : root(x));
+  const float f = a.max_norm / (n + 1e-6f);
+  *norm = n;
+  *factor = s * (f >= 1.f ? 1.f : f);   // a NaN passes through: it is below nothing
 }
 
 __device__ __forceinline__ bool usable(const NormArgs &a, const AdHeader &h) {
@@ -291,7 +301,7 @@ int grad_norm(const void *table, int64_t n_items, int state_bits, int inf, doubl
   a.n_items = n_items;
   a.state_bits = state_bits;
   a.inf = inf != 0;
-  a.max_norm = max_norm;
+  a.max_norm = (float)std::min(max_norm, 3.4028234663852886e38);   // over any norm, or infinite: nothing is clipped
   a.grad_scale = grad_scale;
   a.out = out;
   a.hdr = static_cast<WsHeader *>(workspace);
