@@ -21,8 +21,10 @@
 //   Values, bf16. A row has few distinct values: a histogram of counts in shared memory
 //   has a bin for each value of magnitude 2^-21 to 2^11; one weight per bin and a scan
 //   over the bins give the borders and the value that u falls on. A row whose decisions
-//   need a value outside that range goes by divisions.
-//   Divisions. Bins of the distance below the row's largest key (2048 of them), counts
+//   need a value outside that range goes by intervals.
+//   Intervals. As a list's, of all of the row's tokens: a pass for their counts and masses
+//   and one for the tokens of an interval that a border falls in, from L2.
+//   Divisions, where an interval holds too many to tell apart. Bins of the distance below the row's largest key (2048 of them), counts
 //   and masses; the bin a border falls in is divided again until it holds one value.
 //   The passes after the first come from L2.
 //   Which of the equal values it is goes by id there: the matches are counted per chunk
@@ -57,7 +59,7 @@ constexpr int SA_LO = (127 - 21) << 7;
 constexpr int SA_BINS = 8192, SA_ZERO = SA_BINS, SA_LAST = SA_BINS + 1;
 constexpr int SA_ROWS = 33;            // a warp's places in the order of falling values, by 32
 constexpr int SA_ORDER = SA_ROWS * 32 * SA_WARPS;   // all of them; behind the last bin's they are empty
-static_assert(SA_ORDER >= SA_BINS + 2, "places");
+static_assert(SA_ORDER >= SA_BINS + 2 && SA_ROWS == 33, "places");
 
 // 2^(-i/64) and 2^(-i/4096) in units of 2^-63, by the definition.
 __device__ const uint64_t g_pow2[128] = {
@@ -251,8 +253,13 @@ __device__ __forceinline__ unsigned long long weight(const unsigned long long *p
   const int shift = 62 - S + power;
   return shift < 64 ? (w + (1ull << (shift - 1))) >> shift : 0ull;
 }
+// The same out of line: most of a row's code runs once, and is fetched for it.
+__device__ __noinline__ unsigned long long weight_of(const unsigned long long *pow2, float m, float ch, float cl, int S,
+                                                     float z) {
+  return weight(pow2, m, ch, cl, S, z);
+}
 // Its share of a mass in units of 2^-S, a quotient of two words each.
-__device__ __forceinline__ float share(const unsigned long long *pow2, float m, float ch, float cl, int S, float z,
+__device__ __noinline__ float share(const unsigned long long *pow2, float m, float ch, float cl, int S, float z,
                                        unsigned long long mass) {
   int power;
   const unsigned long long w = fraction(pow2, m, ch, cl, z, power);
@@ -491,7 +498,7 @@ __device__ Drawn decide(SampleSmem &s, float m, int entries, int S, F of) {
     if (i < 0 || i >= entries) return;
     float z;
     cnt = of(i, z);
-    w = weight(s.pow2, m, ch, cl, S, z);
+    w = weight_of(s.pow2, m, ch, cl, S, z);
   };
   uint32_t n = 0;
   unsigned long long mass = 0;
@@ -531,35 +538,43 @@ __device__ void decide_values(SampleSmem &s, float m) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const float ch = s.law.ch;
   const float least = __double2float_ru((double)m + s.law.log_min);   // min-p's border
-  // the bins that hold tokens min-p leaves, in their order: how many each warp has
-  uint32_t have = 0, n = 0;
+  // the bins that hold tokens min-p leaves, in their order: how many each warp has. Lane j
+  // keeps which of row j's bins those are.
+  uint32_t have = 0, n = 0, mine = 0, last = 0;
+#pragma unroll 3
   for (int j = 0; j < SA_ROWS; ++j) {
     const int bin = bin_at((warp * SA_ROWS + j) * 32 + lane);
     const uint32_t c = bin < 0 ? 0 : s.hist[bin];
     n += c;
-    have += __popc(__ballot_sync(~0u, c != 0 && bin_value(bin) >= least));
+    const uint32_t who = __ballot_sync(~0u, c != 0 && bin_value(bin) >= least);
+    have += __popc(who);
+    if (j < 32) mine = lane == j ? who : mine;
+    else last = who;
   }
   if (lane == 0) s.warp_k[warp] = have;
   __syncthreads();
   uint32_t at = 0, entries = 0;
+#pragma unroll
   for (int w = 0; w < SA_WARPS; ++w) {
     if (w == warp) at = entries;
     entries += s.warp_k[w];
   }
   float rough = 0.f;
-  if (entries <= SA_ENTRIES)
-    for (int j = 0; j < SA_ROWS && have != 0; ++j) {
+  if (entries <= SA_ENTRIES) {
+    auto take = [&](int j, uint32_t who) {
       const int bin = bin_at((warp * SA_ROWS + j) * 32 + lane);
-      const uint32_t c = bin < 0 ? 0 : s.hist[bin];
-      const float z = bin_value(bin);
-      const bool in = c != 0 && z >= least;
-      const uint32_t who = __ballot_sync(~0u, in);
-      if (in) {
+      if (who >> lane & 1) {
         s.bins[at + __popc(who & ((1u << lane) - 1))] = (uint16_t)bin;
-        rough += (float)c * ex2((z - m) * ch);
+        rough += (float)s.hist[bin] * ex2((bin_value(bin) - m) * ch);
       }
       at += __popc(who);
+    };
+    for (uint32_t rows = __ballot_sync(~0u, mine != 0); rows != 0; rows &= rows - 1) {
+      const int j = __ffs(rows) - 1;
+      take(j, __shfl_sync(~0u, mine, j));
     }
+    if (last != 0) take(32, last);
+  }
   uint32_t none = 0;
   block_sums(s, rough, n, none);
   const uint32_t total = n;
@@ -618,9 +633,16 @@ __device__ void decide_values(SampleSmem &s, float m) {
 // ------------------------------------------------------------- by a list
 // Counts (and with `masses` the masses) of the intervals of the list's tokens with keys from
 // `from` on, scanned; 4 intervals per thread.
+// inside: the one that these intervals divide again, -1 for the first division.
 struct Intervals {
   float m, scale;
-  __device__ __forceinline__ int of(float z) const { return min(SA_LEVEL - 1, (int)((m - z) * scale)); }
+  int inside;
+  __device__ __forceinline__ int of(float z) const {   // -1: outside
+    const float x = (m - z) * scale;
+    const int b = min(SA_LEVEL - 1, (int)x);
+    if (inside < 0) return b;
+    return b != inside ? -1 : min(SA_LEVEL - 1, (int)((x - (float)inside) * (float)SA_LEVEL));
+  }
 };
 __device__ __forceinline__ float list_value(unsigned long long key) { return of_key((uint32_t)(key >> 32)); }
 __device__ void add_mass(uint32_t *lo, uint32_t *hi, unsigned long long w) {
@@ -628,8 +650,20 @@ __device__ void add_mass(uint32_t *lo, uint32_t *hi, unsigned long long w) {
   const uint32_t up = (uint32_t)(w >> 32) + (old + (uint32_t)w < old ? 1u : 0u);
   if (up != 0) atomicAdd(hi, up);
 }
-__device__ void count_list(SampleSmem &s, int n, const Intervals &iv, unsigned long long from, bool masses, int S) {
+// The sums of the level's counts (and masses) before each thread's bins.
+__device__ void scan_level(SampleSmem &s, bool masses) {
   constexpr int PT = SA_LEVEL / SA_THREADS;
+  uint32_t c = 0;
+  unsigned long long mass = 0;
+#pragma unroll
+  for (int i = 0; i < PT; ++i) {
+    const int b = threadIdx.x * PT + i;
+    c += s.level.cnt[b];
+    if (masses) mass += s.level.lo[b] + ((unsigned long long)s.level.hi[b] << 32);
+  }
+  block_scan(s, c, mass);
+}
+__device__ void count_list(SampleSmem &s, int n, const Intervals &iv, unsigned long long from, bool masses, int S) {
   const int t = threadIdx.x;
   for (int i = t; i < SA_LEVEL * (masses ? 3 : 1); i += SA_THREADS) s.level.cnt[i] = 0;   // lo and hi lie behind it
   __syncthreads();
@@ -639,24 +673,14 @@ __device__ void count_list(SampleSmem &s, int n, const Intervals &iv, unsigned l
     const float z = list_value(key);
     const int b = iv.of(z);
     atomicAdd(&s.level.cnt[b], 1u);
-    if (masses) add_mass(&s.level.lo[b], &s.level.hi[b], weight(s.pow2, iv.m, s.law.ch, s.law.cl, S, z));
+    if (masses) add_mass(&s.level.lo[b], &s.level.hi[b], weight_of(s.pow2, iv.m, s.law.ch, s.law.cl, S, z));
   }
   __syncthreads();
-  uint32_t c = 0;
-  unsigned long long mass = 0;
-#pragma unroll
-  for (int i = 0; i < PT; ++i) {
-    const int b = t * PT + i;
-    c += s.level.cnt[b];
-    if (masses) mass += s.level.lo[b] + ((unsigned long long)s.level.hi[b] << 32);
-  }
-  block_scan(s, c, mass);
+  scan_level(s, masses);
 }
-// The token that a count or a mass (of the tokens from `from` on) reaches: its key, rank and
-// weight to key, key_rank (of the whole list), key_w, key_before. False: its interval
-// holds too many.
-__device__ bool find_key(SampleSmem &s, int n, const Intervals &iv, unsigned long long from, int S,
-                         unsigned long long target, bool by_n) {
+// The interval that a count or a mass reaches, with the tokens and the mass before it, to
+// `found` (at -1: the target lies behind the last one). By the block.
+__device__ void find_interval(SampleSmem &s, unsigned long long target, bool by_n) {
   constexpr int PT = SA_LEVEL / SA_THREADS;
   const int t = threadIdx.x;
   if (t < 32) {
@@ -669,7 +693,7 @@ __device__ bool find_key(SampleSmem &s, int n, const Intervals &iv, unsigned lon
     if (t == 0) {
       s.found = f;
       s.n_near = 0;
-      if (f.at >= 0) {   // tokens and mass before the interval
+      if (f.at >= 0) {
         const int t0 = f.at / PT;
         uint32_t n0 = s.pre_n[t0];
         unsigned long long c0 = s.pre_mass[t0];
@@ -677,40 +701,51 @@ __device__ bool find_key(SampleSmem &s, int n, const Intervals &iv, unsigned lon
           n0 += s.level.cnt[i];
           if (!by_n) c0 += s.level.lo[i] + ((unsigned long long)s.level.hi[i] << 32);
         }
-        s.found.n0 = n0, s.found.c0 = c0;
+        s.found.n0 = n0, s.found.c0 = c0, s.found.cnt = s.level.cnt[f.at];
       }
     }
   }
   __syncthreads();
-  const int at = s.found.at;
-  const uint32_t many = at < 0 ? SA_NEAR + 1 : s.level.cnt[at];
-  if (many > SA_NEAR) return false;
-  for (int i = t; i < n; i += SA_THREADS) {
-    const unsigned long long key = s.list[i];
-    if (key < from) continue;
-    const float z = list_value(key);
-    if (iv.of(z) != at) continue;
-    const int k = atomicAdd(&s.n_near, 1);
-    s.near[k] = key;
-    s.near_w[k] = by_n ? 0 : weight(s.pow2, iv.m, s.law.ch, s.law.cl, S, z);
+}
+// The token among the `many` near ones that found's target falls on: its key, its rank and weight
+// and the mass before it, of all tokens, to key, key_rank, key_w, key_before. By the block.
+__device__ void rank_near(SampleSmem &s, float m, int S, int many, bool by_n) {
+  const int t = threadIdx.x;
+  unsigned long long key = 0, w = 0;
+  if (t < many) {
+    key = s.near[t];
+    w = by_n ? 0 : weight_of(s.pow2, m, s.law.ch, s.law.cl, S, list_value(key));
+    s.near_w[t] = w;
   }
   __syncthreads();
-  const uint32_t n0 = s.found.n0;
-  const unsigned long long c0 = s.found.c0;
-  if (t < (int)many) {
-    const unsigned long long key = s.near[t], w = s.near_w[t];
-    uint32_t rank = 0;
-    unsigned long long before = 0;
-    for (int i = 0; i < (int)many; ++i) {
+  if (t < many) {
+    uint32_t rank = s.found.n0;
+    unsigned long long before = s.found.c0;
+#pragma unroll 4
+    for (int i = 0; i < many; ++i) {
       const bool first = s.near[i] > key;
       rank += first;
       before += first ? s.near_w[i] : 0ull;
     }
-    rank += n0, before += c0;
+    const unsigned long long target = s.found.target;
     if (by_n ? rank + 1 == target : (before < target && target <= before + w))
       s.key = key, s.key_w = w, s.key_rank = rank, s.key_before = before;
   }
   __syncthreads();
+}
+// The token of the list (from `from` on) that a count or a mass reaches, as rank_near gives it.
+// False: its interval holds too many.
+__device__ bool find_key(SampleSmem &s, int n, const Intervals &iv, unsigned long long from, int S,
+                         unsigned long long target, bool by_n) {
+  find_interval(s, target, by_n);
+  const int at = s.found.at, many = at < 0 ? SA_NEAR + 1 : (int)s.found.cnt;
+  if (many > SA_NEAR) return false;
+  for (int i = threadIdx.x; i < n; i += SA_THREADS) {
+    const unsigned long long key = s.list[i];
+    if (key >= from && iv.of(list_value(key)) == at) s.near[atomicAdd(&s.n_near, 1)] = key;
+  }
+  __syncthreads();
+  rank_near(s, iv.m, S, many, by_n);
   return true;
 }
 
@@ -741,7 +776,7 @@ __device__ void decide_few(SampleSmem &s, float m, int n, unsigned long long fro
   static_assert(SA_NEAR <= 256, "units");
   const float z = list_value(key);
   const bool in = t < many && rank < kept;
-  const unsigned long long w = in ? weight(s.pow2, m, law.ch, law.cl, S, z) : 0;
+  const unsigned long long w = in ? weight_of(s.pow2, m, law.ch, law.cl, S, z) : 0;
   s.near_w[t] = 0;
   __syncthreads();
   if (in) s.near_w[rank] = w;
@@ -818,7 +853,7 @@ __device__ void decide_list(SampleSmem &s, float m, int n) {
     decide_few(s, m, n, from);
     return;
   }
-  const Intervals iv{m, m > low ? (float)SA_LEVEL / (m - low) : 0.f};
+  const Intervals iv{m, m > low ? (float)SA_LEVEL / (m - low) : 0.f, -1};
   const int S = unit_of(rough);
   if (law.top_k > 0 && law.top_k <= (int)in) {
     count_list(s, n, iv, from, false, S);
@@ -909,38 +944,47 @@ __device__ void level_count(SampleSmem &s, const Row<E, U> &row, const Level &l)
 // kind 0: totals alone, 1: the bin that `target` tokens reach, 2: the bin that a mass of
 // `target` reaches, 3: the one that the fraction top_p of the level's mass reaches,
 // 4: the one that u falls on.
+// The cluster's levels into the leader's: each CTA sums its share of the bins.
+__device__ void merge_levels(cg::cluster_group &cluster, SampleSmem &s) {
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  if (C == 1) {
+    __syncthreads();
+    return;
+  }
+  cluster.sync();
+  for (int i = rank * (SA_LEVEL / C) + threadIdx.x; i < (rank + 1) * (SA_LEVEL / C); i += SA_THREADS) {
+    uint32_t n = 0, lo[SA_MAX_CLUSTER], hi[SA_MAX_CLUSTER];
+    unsigned long long w = 0;
+#pragma unroll
+    for (int r = 0; r < SA_MAX_CLUSTER; ++r) {
+      if (r >= C) break;
+      const uint32_t *h = cluster.map_shared_rank(s.level.cnt, r);   // lo and hi lie behind it
+      n += h[i], lo[r] = h[SA_LEVEL + i], hi[r] = h[2 * SA_LEVEL + i];
+    }
+#pragma unroll
+    for (int r = 0; r < SA_MAX_CLUSTER; ++r)
+      if (r < C) w += lo[r] + ((unsigned long long)hi[r] << 32);
+    uint32_t *h = cluster.map_shared_rank(s.level.cnt, 0);
+    h[i] = n, h[SA_LEVEL + i] = (uint32_t)w, h[2 * SA_LEVEL + i] = (uint32_t)(w >> 32);
+  }
+  cluster.sync();
+}
+
 template <class E, int U>
 __device__ Found level_find(cg::cluster_group &cluster, SampleSmem &s, const Row<E, U> &row, const Level &l, int kind,
                             unsigned long long target) {
   constexpr int PT = SA_LEVEL / SA_THREADS;
-  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), t = threadIdx.x;
+  const int rank = (int)cluster.block_rank(), t = threadIdx.x;
   level_count(s, row, l);
   uint32_t *cnt = s.level.cnt, *lo = s.level.lo, *hi = s.level.hi;
-  if (C > 1) {
-    cluster.sync();
-    // each CTA sums its share of the bins over the cluster, into the leader's
-    for (int i = rank * (SA_LEVEL / C) + t; i < (rank + 1) * (SA_LEVEL / C); i += SA_THREADS) {
-      uint32_t n = 0;
-      unsigned long long w = 0;
-      for (int r = 0; r < C; ++r) {
-        const uint32_t *h = cluster.map_shared_rank(s.level.cnt, r);   // lo and hi lie behind it
-        n += h[i];
-        w += h[SA_LEVEL + i] + ((unsigned long long)h[2 * SA_LEVEL + i] << 32);
-      }
-      uint32_t *h = cluster.map_shared_rank(s.level.cnt, 0);
-      h[i] = n, h[SA_LEVEL + i] = (uint32_t)w, h[2 * SA_LEVEL + i] = (uint32_t)(w >> 32);
-    }
-    cluster.sync();
-  } else {
-    __syncthreads();
-  }
+  merge_levels(cluster, s);
   if (rank == 0) {
     if (t == 0 && !l.whole && l.last >= l.first && (l.last - l.first) >> l.shift < (uint32_t)SA_LEVEL) {
       const uint32_t bin = (l.last - l.first) >> l.shift;   // the last key's tokens that are kept
       cnt[bin] += l.ties;
       if (l.masses) {
         unsigned long long w = lo[bin] + ((unsigned long long)hi[bin] << 32);
-        w += l.ties * weight(s.pow2, l.m, s.law.ch, s.law.cl, l.S, of_key(key_of(l.m) - l.last));
+        w += l.ties * weight_of(s.pow2, l.m, s.law.ch, s.law.cl, l.S, of_key(key_of(l.m) - l.last));
         lo[bin] = (uint32_t)w, hi[bin] = (uint32_t)(w >> 32);
       }
     }
@@ -1038,7 +1082,7 @@ __device__ __noinline__ void decide_divisions(cg::cluster_group &cluster, Sample
   l.masses = 1;
   if (s.law.top_p < 1.f) {
     const Found f = descend(cluster, s, row, l, 3, 0, &d);
-    const uint32_t ties = div_up(f.target - f.c0, weight(s.pow2, m, s.law.ch, s.law.cl, l.S, of_key(top - d)), f.cnt);
+    const uint32_t ties = div_up(f.target - f.c0, weight_of(s.pow2, m, s.law.ch, s.law.cl, l.S, of_key(top - d)), f.cnt);
     l.whole = ties == f.cnt && (l.whole || d != l.last);
     l.last = d, l.ties = ties;
     v.cut = of_key(top - d), v.cut_n = (int)ties, v.cut_id = l.whole ? INT_MAX : -1;
@@ -1047,13 +1091,165 @@ __device__ __noinline__ void decide_divisions(cg::cluster_group &cluster, Sample
   if (s.law.draw) {
     const Found f = descend(cluster, s, row, l, 4, 0, &d);
     v.tok = of_key(top - d);
-    v.tok_at = (int)div_up(f.target - f.c0, weight(s.pow2, m, s.law.ch, s.law.cl, l.S, v.tok), f.cnt) - 1;
+    v.tok_at = (int)div_up(f.target - f.c0, weight_of(s.pow2, m, s.law.ch, s.law.cl, l.S, v.tok), f.cnt) - 1;
     v.prob = share(s.pow2, m, s.law.ch, s.law.cl, l.S, v.tok, f.total);
     if (v.kept < 0) v.kept = (int)f.total_n;
   } else if (v.kept < 0) {
     l.masses = 0, l.first = 0, l.shift = level_shift((unsigned long long)l.last + 1);
     v.kept = (int)level_find(cluster, s, row, l, 0, 0).total_n;
   }
+  if (threadIdx.x == 0) s.verdict = v;
+  __syncthreads();
+}
+
+// ------------------------------------------- any values: intervals of the row
+// As a list's: counts (and masses) of the intervals of the row's tokens from `from` on, in the
+// leader's level and scanned.
+template <class E, int U>
+__device__ void count_row(cg::cluster_group &cluster, SampleSmem &s, const Row<E, U> &row, const Intervals &iv,
+                          unsigned long long from, bool masses, int S) {
+  for (int i = threadIdx.x; i < SA_LEVEL * 3; i += SA_THREADS) s.level.cnt[i] = 0;   // lo and hi lie behind it
+  __syncthreads();
+  const float least = list_value(from), ch = s.law.ch, cl = s.law.cl;
+  for (int c = threadIdx.x >> 5; c < row.nc; c += SA_WARPS) {
+    if (!(s.cmax[c] >= least)) continue;
+    row.groups(c, [&](int p, const uint4 *v) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        Vec<E> x;
+        x.v = v[u];
+#pragma unroll
+        for (int i = 0; i < Val<E>::PER; ++i) {
+          const float z = Val<E>::f32(x.e[i]);
+          const int id = p + u * 32 * Val<E>::PER + i - row.off;
+          if (!(z > least) && !(z == least && ~(uint32_t)id >= (uint32_t)from)) continue;
+          const int b = iv.of(z);
+          if (b < 0) continue;
+          atomicAdd(&s.level.cnt[b], 1u);
+          if (masses) add_mass(&s.level.lo[b], &s.level.hi[b], weight(s.pow2, iv.m, ch, cl, S, z));
+        }
+      }
+    });
+  }
+  merge_levels(cluster, s);
+  if (cluster.block_rank() == 0) scan_level(s, masses);
+}
+
+// What find_row says.
+struct Near {
+  unsigned long long key, w, before, total, target;
+  uint32_t rank, total_n;
+  int state;   // 0: found, 1: the target lies behind the last token, 2: too many in its interval,
+  int at;      // which is this one; before and rank are its mass and tokens
+};
+// The token that a count (by_n) or a mass reaches; frac: `target` is the part of the level's mass in
+// units of 2^-64 that has to be reached.
+template <class E, int U>
+__device__ Near find_row(cg::cluster_group &cluster, SampleSmem &s, const Row<E, U> &row, const Intervals &iv,
+                         unsigned long long from, int S, unsigned long long target, bool by_n, bool frac) {
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), t = threadIdx.x;
+  if (rank == 0) find_interval(s, frac ? reach(s.pre_mass[SA_THREADS], target) : target, by_n);
+  else if (t == 0) s.n_near = 0;
+  cluster.sync();
+  const Found f = *cluster.map_shared_rank(&s.found, 0);
+  Near r{};
+  r.total = f.total, r.total_n = f.total_n, r.target = f.target, r.at = f.at;
+  r.before = f.c0, r.rank = f.n0;
+  r.state = f.at < 0 ? 1 : f.cnt > (uint32_t)SA_NEAR ? 2 : 0;
+  if (r.state == 0) {
+    const float least = list_value(from);
+    for (int c = t >> 5; c < row.nc; c += SA_WARPS) {
+      if (!(s.cmax[c] >= least)) continue;
+      row.groups(c, [&](int p, const uint4 *v) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          Vec<E> x;
+          x.v = v[u];
+#pragma unroll
+          for (int i = 0; i < Val<E>::PER; ++i) {
+            const float z = Val<E>::f32(x.e[i]);
+            const int id = p + u * 32 * Val<E>::PER + i - row.off;
+            if (z >= least && iv.of(z) == f.at) {
+              const unsigned long long key = (unsigned long long)key_of(z) << 32 | ~(uint32_t)id;
+              if (key >= from) s.near[atomicAdd(&s.n_near, 1)] = key;
+            }
+          }
+        }
+      });
+    }
+    cluster.sync();
+    if (rank == 0) {
+      int have = s.n_near;
+      __syncthreads();
+      for (int q = 1; q < C; ++q) {
+        const int k = *cluster.map_shared_rank(&s.n_near, q);
+        if (t < k) s.near[have + t] = *cluster.map_shared_rank(&s.near[t], q);
+        have += k;
+      }
+      __syncthreads();
+      rank_near(s, iv.m, S, (int)f.cnt, by_n);
+    }
+    cluster.sync();
+    r.key = *cluster.map_shared_rank(&s.key, 0);
+    r.w = *cluster.map_shared_rank(&s.key_w, 0);
+    r.before = *cluster.map_shared_rank(&s.key_before, 0);
+    r.rank = *cluster.map_shared_rank(&s.key_rank, 0);
+  }
+  cluster.sync();   // the leader's may change again
+  return r;
+}
+
+// The verdict of a row of any values, by every CTA; slow where an interval holds too many.
+template <class E, int U>
+__device__ __noinline__ void decide_row(cg::cluster_group &cluster, SampleSmem &s, const Row<E, U> &row, float m, float rough) {
+  const int top_k = s.law.top_k;
+  const float least = fmaxf(__double2float_ru((double)m + s.law.log_min), -3.402823466e38f);
+  unsigned long long from = (unsigned long long)key_of(least) << 32;
+  // what is further below than the last interval has no weight
+  const Intervals iv{m, (float)SA_LEVEL * s.law.ch / 63.f, -1};
+  bool counted = false;   // the level holds the first division's
+  // a find in two divisions where one interval is too full
+  auto find = [&](int S, unsigned long long target, bool by_n, bool frac) {
+    if (!counted) count_row(cluster, s, row, iv, from, !by_n, S);
+    counted = true;
+    Near n = find_row(cluster, s, row, iv, from, S, target, by_n, frac);
+    if (n.state != 2) return n;
+    const Intervals part{iv.m, iv.scale, n.at};
+    count_row(cluster, s, row, part, from, !by_n, S);
+    counted = false;
+    Near r = find_row(cluster, s, row, part, from, S, n.target - (by_n ? (unsigned long long)n.rank : n.before), by_n, false);
+    r.before += n.before, r.rank += n.rank, r.total = n.total, r.total_n = n.total_n;
+    return r;
+  };
+  const int S = unit_of(top_k > 0 ? fminf(rough, (float)top_k) : rough);
+  Verdict v{};
+  v.tok_id = -1, v.kept = -1;
+  if (top_k > 0) {
+    const Near n = find(S, (unsigned long long)top_k, true, false);
+    if (n.state == 0) from = n.key, v.kept = top_k;
+    else v.kept = (int)n.total_n, v.slow = n.state == 2;
+    counted = false;
+  }
+  unsigned long long cut = from;
+  if (!v.slow && (s.law.top_p < 1.f || s.law.draw || v.kept < 0)) {
+    unsigned long long mass = 0;
+    if (s.law.top_p < 1.f) {
+      const Near n = find(S, s.law.p, false, true);
+      v.slow = n.state != 0;
+      cut = n.key, v.kept = (int)n.rank + 1, mass = n.before + n.w;
+    } else {
+      const Near n = find(S, ~0ull, !s.law.draw, false);   // the totals
+      mass = n.total;
+      if (v.kept < 0) v.kept = (int)n.total_n;
+    }
+    if (!v.slow && s.law.draw) {
+      const Near n = find(S, beyond(mass, s.law.u), false, false);
+      v.slow |= n.state != 0;
+      v.tok = list_value(n.key), v.tok_id = (int)~(uint32_t)n.key;
+      v.prob = share(s.pow2, m, s.law.ch, s.law.cl, S, v.tok, mass);
+    }
+  }
+  v.cut = list_value(cut), v.cut_id = (uint32_t)cut == 0 ? INT_MAX : (int)~(uint32_t)cut;
   if (threadIdx.x == 0) s.verdict = v;
   __syncthreads();
 }
@@ -1620,7 +1816,10 @@ __global__ void __launch_bounds__(SA_THREADS, SA_CTAS_PER_SM) k_sample(const Sam
         slow = v.slow != 0;
         if (t == 0) s.verdict = v;
       }
-      if (slow) decide_divisions(cluster, s, row, m, rough);
+      if (slow) {
+        decide_row(cluster, s, row, m, rough);
+        if (s.verdict.slow) decide_divisions(cluster, s, row, m, rough);
+      }
     }
     __syncthreads();
     if (!bad) {
