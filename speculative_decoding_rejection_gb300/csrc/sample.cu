@@ -41,15 +41,15 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int SA_THREADS = 256;
+constexpr int SA_THREADS = 512;
 constexpr int SA_WARPS = SA_THREADS / 32;
 constexpr int SA_LEVEL = 2048;         // bins of a division, intervals of a list
 constexpr int SA_CHUNKS = 256;         // chunks of a CTA's slice
-constexpr int SA_CTAS_PER_SM = 3;
+constexpr int SA_CTAS_PER_SM = 2;
 constexpr int SA_ENTRIES = 6144;       // values that a histogram's law may have
 constexpr int SA_LIST = 2560;          // tokens of a list
 constexpr int SA_FULL = 1536;          // a row that short goes to it whole
-constexpr int SA_NEAR = SA_THREADS;    // tokens that are ranked one by one
+constexpr int SA_NEAR = 256;    // tokens that are ranked one by one
 constexpr int SA_TOP_K = 256;          // top-k up to which the threads' maxima give a border
 static_assert(SA_TOP_K <= SA_THREADS && SA_TOP_K <= SA_NEAR, "top-k's border and its tokens");
 constexpr int SA_MAX_CLUSTER = 8;
@@ -57,9 +57,9 @@ constexpr int SA_MAX_CLUSTER = 8;
 // sign << 12 | (bits - SA_LO). One more for zero, one for what is below -2^11.
 constexpr int SA_LO = (127 - 21) << 7;
 constexpr int SA_BINS = 8192, SA_ZERO = SA_BINS, SA_LAST = SA_BINS + 1;
-constexpr int SA_ROWS = 33;            // a warp's places in the order of falling values, by 32
+constexpr int SA_ROWS = 17;            // a warp's places in the order of falling values, by 32
 constexpr int SA_ORDER = SA_ROWS * 32 * SA_WARPS;   // all of them; behind the last bin's they are empty
-static_assert(SA_ORDER >= SA_BINS + 2 && SA_ROWS == 33, "places");
+static_assert(SA_ORDER >= SA_BINS + 2 && SA_ROWS <= 32, "places");
 
 // 2^(-i/64) and 2^(-i/4096) in units of 2^-63, by the definition.
 __device__ const uint64_t g_pow2[128] = {
@@ -116,13 +116,57 @@ struct Val<uint16_t> {
   static constexpr int PER = 8;   // elements of a 16-byte vector
   static __device__ __forceinline__ float f32(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
   static constexpr uint16_t NEG_INF = 0xff80;
+  // a bit for each element that is not below bound: bit w for the lower half of word w, 16 + w for the upper
+  template <int U>
+  static __device__ __forceinline__ uint32_t at_least(const uint4 (&v)[U], float bound) {
+    const uint32_t b = __float_as_uint(bound), up = (b >> 31 ? b : b + 0xffffu) >> 16;   // the next of bf16
+    const uint32_t two = up | up << 16;
+    uint32_t hits = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      hits |= ge2(v[u].x, two) & 0x10001u << (4 * u);
+      hits |= ge2(v[u].y, two) & 0x10001u << (4 * u + 1);
+      hits |= ge2(v[u].z, two) & 0x10001u << (4 * u + 2);
+      hits |= ge2(v[u].w, two) & 0x10001u << (4 * u + 3);
+    }
+    return hits;
+  }
+  static __device__ __forceinline__ uint32_t ge2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("set.ge.u32.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
 };
 template <>
 struct Val<uint32_t> {
   static constexpr int PER = 4;
   static __device__ __forceinline__ float f32(uint32_t x) { return __uint_as_float(x); }
   static constexpr uint32_t NEG_INF = 0xff800000u;
+  template <int U>
+  static __device__ __forceinline__ uint32_t at_least(const uint4 (&v)[U], float bound) {
+    uint32_t hits = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      hits |= f32(v[u].x) >= bound ? 1u << (4 * u) : 0;
+      hits |= f32(v[u].y) >= bound ? 2u << (4 * u) : 0;
+      hits |= f32(v[u].z) >= bound ? 4u << (4 * u) : 0;
+      hits |= f32(v[u].w) >= bound ? 8u << (4 * u) : 0;
+    }
+    return hits;
+  }
 };
+// Word w of the vectors.
+template <int U>
+__device__ __forceinline__ uint32_t word_at(const uint4 (&v)[U], int w) {
+  uint32_t x[U * 4];
+#pragma unroll
+  for (int u = 0; u < U; ++u) x[4 * u] = v[u].x, x[4 * u + 1] = v[u].y, x[4 * u + 2] = v[u].z, x[4 * u + 3] = v[u].w;
+#pragma unroll
+  for (int h = U * 2; h > 0; h /= 2)
+#pragma unroll
+    for (int i = 0; i < h; ++i) x[i] = w & h ? x[i + h] : x[i];
+  return x[0];
+}
 template <class E>
 union Vec {
   uint4 v;
@@ -540,7 +584,7 @@ __device__ void decide_values(SampleSmem &s, float m) {
   const float least = __double2float_ru((double)m + s.law.log_min);   // min-p's border
   // the bins that hold tokens min-p leaves, in their order: how many each warp has. Lane j
   // keeps which of row j's bins those are.
-  uint32_t have = 0, n = 0, mine = 0, last = 0;
+  uint32_t have = 0, n = 0, mine = 0;
 #pragma unroll 3
   for (int j = 0; j < SA_ROWS; ++j) {
     const int bin = bin_at((warp * SA_ROWS + j) * 32 + lane);
@@ -548,8 +592,7 @@ __device__ void decide_values(SampleSmem &s, float m) {
     n += c;
     const uint32_t who = __ballot_sync(~0u, c != 0 && bin_value(bin) >= least);
     have += __popc(who);
-    if (j < 32) mine = lane == j ? who : mine;
-    else last = who;
+    mine = lane == j ? who : mine;
   }
   if (lane == 0) s.warp_k[warp] = have;
   __syncthreads();
@@ -573,7 +616,6 @@ __device__ void decide_values(SampleSmem &s, float m) {
       const int j = __ffs(rows) - 1;
       take(j, __shfl_sync(~0u, mine, j));
     }
-    if (last != 0) take(32, last);
   }
   uint32_t none = 0;
   block_sums(s, rough, n, none);
@@ -755,7 +797,7 @@ __device__ void decide_few(SampleSmem &s, float m, int n, unsigned long long fro
   const int t = threadIdx.x;
   const Law &law = s.law;
   if (t == 0) s.n_near = 0;
-  s.near[t] = 0;
+  if (t < SA_NEAR) s.near[t] = 0;
   __syncthreads();
   for (int i = t; i < n; i += SA_THREADS) {
     const unsigned long long key = s.list[i];
@@ -763,7 +805,7 @@ __device__ void decide_few(SampleSmem &s, float m, int n, unsigned long long fro
   }
   __syncthreads();
   const int many = s.n_near;
-  const unsigned long long key = s.near[t];
+  const unsigned long long key = t < SA_NEAR ? s.near[t] : 0;
   int rank = 0;
   if (t < ((many + 31) & ~31))
     for (int i = 0; i < many; i += 4) {   // zeros behind the last
@@ -777,11 +819,11 @@ __device__ void decide_few(SampleSmem &s, float m, int n, unsigned long long fro
   const float z = list_value(key);
   const bool in = t < many && rank < kept;
   const unsigned long long w = in ? weight_of(s.pow2, m, law.ch, law.cl, S, z) : 0;
-  s.near_w[t] = 0;
+  if (t < SA_NEAR) s.near_w[t] = 0;
   __syncthreads();
   if (in) s.near_w[rank] = w;
   __syncthreads();
-  block_scan(s, 0, s.near_w[t]);
+  block_scan(s, 0, t < SA_NEAR ? s.near_w[t] : 0);
   unsigned long long mass = s.pre_mass[SA_THREADS];
   const unsigned long long before = in ? s.pre_mass[rank] : 0;
   int last = kept - 1;   // the rank of the last token
@@ -1435,16 +1477,7 @@ __device__ __forceinline__ void list_pass(SampleSmem &s, const Row<E, U> &row, i
     if (__any_sync(~0u, lm >= bound)) {
       // which of the lane's elements, a bit each; then the lanes' next ones together
       const int at = (row.c0 + c) * row.chunk + g * GROUP + lane * PER - row.off;
-      uint32_t hits = 0;
-      if (lm >= bound) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          Vec<E> x;
-          x.v = v[u];
-#pragma unroll
-          for (int i = 0; i < PER; ++i) hits |= Val<E>::f32(x.e[i]) >= bound ? 1u << (u * PER + i) : 0u;
-        }
-      }
+      uint32_t hits = lm >= bound ? Val<E>::at_least(v, bound) : 0;
       while (true) {
         const uint32_t who = __ballot_sync(~0u, hits != 0);
         if (who == 0) break;
@@ -1454,17 +1487,9 @@ __device__ __forceinline__ void list_pass(SampleSmem &s, const Row<E, U> &row, i
         if (hits != 0) {
           const int k = __ffs(hits) - 1;
           hits &= hits - 1;
-          E e = 0;
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            Vec<E> x;
-            x.v = v[u];
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-              if (k == u * PER + i) e = x.e[i];
-          }
-          const int id = at + k / PER * 32 * PER + k % PER;
-          if (pos < SA_LIST) s.list[pos] = (unsigned long long)key_of(Val<E>::f32(e)) << 32 | ~(uint32_t)id;
+          const int w = k & 15, id = at + w / 4 * 32 * PER + w % 4 * (PER / 4) + k / 16;
+          const uint32_t key = key_of(Val<E>::f32((E)(word_at(v, w) >> (k & 16))));
+          if (pos < SA_LIST) s.list[pos] = (unsigned long long)key << 32 | ~(uint32_t)id;
         }
       }
     }
