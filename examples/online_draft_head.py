@@ -1,13 +1,16 @@
 """A draft head that learns while it serves, on a toy target.
 
 Every round drafts K tokens per request with a small head, applies the
-requests' rules to the draft's and the target's logits, verifies the drafts,
-commits what was accepted, and takes one distillation step of the head on the
-target's logits ("Test-Time Speculation", §2). All of it runs in the package's
-kernels: the head's products (spec_head_forward, spec_head_backward), the rules
-(spec_process_logits), the verification (spec_verify_linear), the loss with its
-gradient (spec_distill_loss) and the update (spec_adamw_step, bf16 weights with
-f32 masters and 8-bit states).
+requests' rules and laws (top-k, top-p, min-p) to the draft's and the target's
+logits, verifies the drafts, commits what was accepted, and takes one
+distillation step of the head on the target's logits ("Test-Time Speculation",
+§2). All of it runs in the package's kernels: the head's products
+(spec_head_forward, spec_head_backward; the drafts' from a copy of the
+vocabulary's weights in 4 bits, spec_head4_forward, rounded anew after every
+step), the rules (spec_process_logits), the draws and the laws' rows
+(spec_sample), the verification (spec_verify_linear), the loss with its gradient
+(spec_distill_loss), the gradients' norm (spec_grad_norm) and the update
+(spec_adamw_step, bf16 weights with f32 masters and 8-bit states).
 
 The target is a fixed random head over token embeddings, so its next-token law
 depends on the last token; the draft head starts from other weights and has to
@@ -48,6 +51,12 @@ class DraftHead:
                                          exp_avg_sq_scale=scales[1],
                                          master=[p.float() for p in self.params])
         self.steps = 0
+        self.wv4, _ = sv.spec_head4_quantize(self.wv, group=64)
+
+    def draft(self, h):
+        """The logits from the 4-bit weights, for at most SPEC_HEAD4_MAX_ROWS rows."""
+        y, _, _ = sv.spec_head_forward(h, self.w1, self.b1, residual=h, act=sv.SPEC_ACT_SILU)
+        return sv.spec_head4_forward(y, self.wv4)[0]
 
     def forward(self, h):
         y, pre, _ = sv.spec_head_forward(h, self.w1, self.b1, residual=h, act=sv.SPEC_ACT_SILU, want_pre=True)
@@ -62,7 +71,10 @@ class DraftHead:
                                             out=(None, g1, torch.empty(gb.numel(), device=DEV)))
         gb.copy_(db)
         self.steps += 1
-        return sv.spec_adamw_step(self.table, self.steps, lr=lr, weight_decay=0.0)
+        norm, _ = sv.spec_grad_norm(self.table, max_norm=1.0)
+        ws = sv.spec_adamw_step(self.table, self.steps, lr=lr, weight_decay=0.0, grad_scale=norm[1:])
+        sv.spec_head4_quantize(self.wv, group=64, out=self.wv4)
+        return ws
 
 
 def run(rounds=200, B=64, K=4, vocab=2048, hidden=256, lr=2e-3, seed=1, report=print):
@@ -82,6 +94,9 @@ def run(rounds=200, B=64, K=4, vocab=2048, hidden=256, lr=2e-3, seed=1, report=p
     requests = torch.arange(B, dtype=I32, device=DEV)
     rules = dict(repetition=torch.full((B,), 1.05, device=DEV), presence=torch.full((B,), 0.1, device=DEV),
                  mask=mask)
+    # and has a law of its own
+    law = dict(temperature=temperature, top_k=torch.where(requests % 2 == 0, 0, 200).to(I32),
+               top_p=torch.where(requests % 3 == 0, 1.0, 0.98), min_p=torch.where(requests % 4 == 0, 1e-4, 0.0))
     last = torch.randint(0, vocab, (B,), generator=g, device=DEV)
     history = [[int(t)] for t in last]
     accepted_mean, losses = [], []
@@ -94,7 +109,7 @@ def run(rounds=200, B=64, K=4, vocab=2048, hidden=256, lr=2e-3, seed=1, report=p
         hidden_rows = [embed[last]]
         draft_rows = []
         for i in range(K):
-            raw, _ = head.forward(hidden_rows[-1])
+            raw = head.draft(hidden_rows[-1])
             # the row's context: the history, then the drafts so far, which
             # lie between it and the row as in a batch of i + 1 rows
             so_far = tokens[:, :i].contiguous()
@@ -103,9 +118,11 @@ def run(rounds=200, B=64, K=4, vocab=2048, hidden=256, lr=2e-3, seed=1, report=p
                 history=torch.cat([torch.cat([seen[a:b], so_far[r]]) for r, (a, b) in enumerate(
                     zip(cu_seen[:-1].tolist(), cu_seen[1:].tolist()))]) if i else seen,
                 cu_history=(cu_seen + i * cu_one).to(I32), **rules)
+            u = torch.rand(B, generator=g, device=DEV)
+            drawn, _, _, row, ws = sv.spec_sample(row, u, want_filtered=True, **law)
+            assert sv.spec_get_status(ws) == sv.SPEC_OK
             draft_rows.append(row)
-            q = torch.softmax(row.float() / temperature[:, None], 1)
-            tokens[:, i] = torch.multinomial(q, 1, generator=g)[:, 0].to(I32)
+            tokens[:, i] = drawn
             hidden_rows.append(embed[tokens[:, i].long()])
         states = torch.stack(hidden_rows, 1)                       # [B, K + 1, hidden]
         target_raw, _, _ = sv.spec_head_forward(states.reshape(-1, hidden), target_w)
@@ -114,6 +131,7 @@ def run(rounds=200, B=64, K=4, vocab=2048, hidden=256, lr=2e-3, seed=1, report=p
                                             cu_tokens=cu_draft, **context,
                                             mask_rows=requests.repeat_interleave(K + 1), **rules)
         assert sv.spec_get_status(ws) == sv.SPEC_OK
+        target = sv.spec_sample(target, None, cu_target, want_filtered=True, **law)[3]
         draft = torch.stack(draft_rows, 1).reshape(B * K, vocab)
         out, accepted, _, ws = sv.spec_verify_linear(target, draft, flat, cu_draft, temperature, seed + n, max_k=K)
         assert sv.spec_get_status(ws) == sv.SPEC_OK
