@@ -7,8 +7,8 @@
 //
 //   - Logits are compared and counted exactly.
 //   - A weight 2^-t, t = (m - z) log2(e) / T, is a 64-bit whole number: t is formed in two
-//     f32 words and taken in units of 2^-44, 2^-t is the product of two table entries (6
-//     bits of the fraction each) and a cubic in the 32 bits left, all in 64-bit
+//     f32 words and taken in units of 2^-42, 2^-t is the product of a table's entry (10
+//     bits of the fraction) and a cubic in the 32 bits left, all in 64-bit
 //     fixed point. Masses are sums of these, the same in whatever order they are taken.
 //
 // One cluster works on a row, each CTA on a slice of it, in the order of falling logits.
@@ -61,8 +61,8 @@ constexpr int SA_ROWS = 17;            // a warp's places in the order of fallin
 constexpr int SA_ORDER = SA_ROWS * 32 * SA_WARPS;   // all of them; behind the last bin's they are empty
 static_assert(SA_ORDER >= SA_BINS + 2 && SA_ROWS <= 32, "places");
 
-// 2^(-i/64) and 2^(-i/4096) in units of 2^-63, by the definition.
-__device__ const uint64_t g_pow2[128] = {
+// 2^(-i/64) and 2^(-i/1024) in units of 2^-63, by the definition.
+__device__ const uint64_t g_pow2[80] = {
     0x8000000000000000ull, 0x7e9f06067a4360baull, 0x7d41d96db915019dull, 0x7be86fb985689ddcull,
     0x7a92be8a92436616ull, 0x7940bb9e2cffd89dull, 0x77f25ccdee6d7ae6ull, 0x76a7980f6cca15c2ull,
     0x75606373ee921c97ull, 0x741cb5281e25ee34ull, 0x72dc8373be41a454ull, 0x719fc4b95f452d29ull,
@@ -79,22 +79,10 @@ __device__ const uint64_t g_pow2[128] = {
     0x48e1e9b9d588e19bull, 0x4818ee218a3358eeull, 0x47521cc5a2e6a9e0ull, 0x468d6fadbf2dd4f3ull,
     0x45cae0f1f545eb73ull, 0x450a6abaa4b77ecdull, 0x444c0740496d4294ull, 0x438fb0cb4f468808ull,
     0x42d561b3e6243d8aull, 0x421d1461d66f2023ull, 0x4166c34c5615d0ecull, 0x40b268f9de0183baull,
-    0x8000000000000000ull, 0x7ffa748dff8dc61full, 0x7ff4e9597bed93abull, 0x7fef5e6272758c21ull,
-    0x7fe9d3a8e07bf086ull, 0x7fe4492cc3571f68ull, 0x7fdebeee185d94ddull, 0x7fd934ecdce5ea7dull,
-    0x7fd3ab290e46d769ull, 0x7fce21a2a9d73041ull, 0x7fc89859acede72aull, 0x7fc30f4e14e20bc6ull,
-    0x7fbd867fdf0acb3bull, 0x7fb7fdef08bf7027ull, 0x7fb2759b8f5762aaull, 0x7faced85702a285dull,
-    0x7fa765aca88f6453ull, 0x7fa1de1135ded717ull, 0x7f9c56b315705eaeull, 0x7f96cf92449bf692ull,
-    0x7f9148aec0b9b7b1ull, 0x7f8bc2088721d86full, 0x7f863b9f952caca0ull, 0x7f80b573e832a58bull,
-    0x7f7b2f857d8c51e5ull, 0x7f75a9d452925dd4ull, 0x7f702460649d92eaull, 0x7f6a9f29b106d825ull,
-    0x7f651a30352731eeull, 0x7f5f9573ee57c218ull, 0x7f5a10f4d9f1c7ddull, 0x7f548cb2f54e9fdfull,
-    0x7f4f08ae3dc7c426ull, 0x7f4984e6b0b6cc1dull, 0x7f44015c4b756c94ull, 0x7f3e7e0f0b5d77bcull,
-    0x7f38fafeedc8dd26ull, 0x7f33782bf011a9c2ull, 0x7f2df5960f9207e1ull, 0x7f28733d49a43f2dull,
-    0x7f22f1219ba2b4aeull, 0x7f1d6f4302e7eac6ull, 0x7f17eda17cce812eull, 0x7f126c3d06b134faull,
-    0x7f0ceb159deae091ull, 0x7f076a2b3fd67bb2ull, 0x7f01e97de9cf1b6eull, 0x7efc690d992ff22aull,
-    0x7ef6e8da4b544f9aull, 0x7ef168e3fd97a0c6ull, 0x7eebe92aad557001ull, 0x7ee669ae57e964edull,
-    0x7ee0ea6efaaf4479ull, 0x7edb6b6c9302f0dfull, 0x7ed5eca71e4069a1ull, 0x7ed06e1e99c3cb8bull,
-    0x7ecaefd302e950afull, 0x7ec571c4570d5067ull, 0x7ebff3f2938c3f4full, 0x7eba765db5c2af49ull,
-    0x7eb4f905bb0d4f78ull, 0x7eaf7beaa0c8ec3eull, 0x7ea9ff0c64526f40ull, 0x7ea4826b0306df5full};
+    0x8000000000000000ull, 0x7fe9d3a8e07bf086ull, 0x7fd3ab290e46d769ull, 0x7fbd867fdf0acb3bull,
+    0x7fa765aca88f6453ull, 0x7f9148aec0b9b7b1ull, 0x7f7b2f857d8c51e5ull, 0x7f651a30352731eeull,
+    0x7f4f08ae3dc7c426ull, 0x7f38fafeedc8dd26ull, 0x7f22f1219ba2b4aeull, 0x7f0ceb159deae091ull,
+    0x7ef6e8da4b544f9aull, 0x7ee0ea6efaaf4479ull, 0x7ecaefd302e950afull, 0x7eb4f905bb0d4f78ull};
 
 struct SampleArgs {
   const void *logits;
@@ -220,7 +208,7 @@ struct SampleSmem {
     };
   };
   unsigned long long near[SA_NEAR], near_w[SA_NEAR];
-  unsigned long long pow2[128];
+  unsigned long long pow2[1024];   // 2^(-i/1024) in units of 2^-62
   unsigned long long pre_mass[SA_THREADS + 1];
   uint32_t pre_n[SA_THREADS + 1];
   float cmax[SA_CHUNKS];
@@ -267,8 +255,8 @@ __device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
 // 2^-t for t = (m - z) c, as a fraction in units of 2^-62 (over a half) and a power: the
 // result is fraction 2^-power, 0 for t of 63 and more. The difference and its product with c are
 // taken in two words each: t is right within 2^-41 (its second word is under 2^-18 and
-// rounded twice) and the units of 2^-44, the fixed-point product within a few units of
-// 2^-44, so a weight within 2^-40 of itself.
+// rounded twice) and the units of 2^-42, the fixed-point product within a few units of
+// 2^-42, so a weight within 2^-39 of itself.
 __device__ __forceinline__ unsigned long long fraction(const unsigned long long *pow2, float m, float ch, float cl,
                                                        float z, int &power) {
   const float dh = m - z, bb = dh - m;
@@ -277,17 +265,15 @@ __device__ __forceinline__ unsigned long long fraction(const unsigned long long 
   power = 0;
   if (!(ph < 63.f)) return 0;
   const float pl = fmaf(dh, ch, -ph) + fmaf(dh, cl, dl * ch);
-  const long long t = __float2ll_rn(ph * 17592186044416.f) + __float2ll_rn(pl * 17592186044416.f);
+  const long long t = __float2ll_rn(ph * 4398046511104.f) + __float2int_rn(pl * 4398046511104.f);
   const unsigned long long f = t < 0 ? 0 : (unsigned long long)t;
-  const uint32_t r = (uint32_t)f;
-  // 1 - 2^-r = y - y^2 / 2 + y^3 / 6 in units of 2^-44, y = r ln 2 < 2^-12.5
-  const uint32_t y = __umulhi(r, 2977044472u);
-  const uint32_t q = __umulhi(y, y);                                // y^2 in 2^-56
-  const uint32_t e = y - (q >> 13) + (((__umulhi(q, y) >> 16) * 43u) >> 16);
-  unsigned long long w = __umul64hi(pow2[(f >> 38) & 63], pow2[64 + ((f >> 32) & 63)]);   // in 2^-62
-  w -= __umul64hi(w, (unsigned long long)e << 20);
-  power = (int)(f >> 44);
-  return w;
+  // 1 - 2^-r = y - y^2 / 2 + y^3 / 6 in units of 2^-42, y = r ln 2 < 2^-10.5
+  const uint32_t y = __umulhi((uint32_t)f, 2977044472u);
+  const uint32_t q = __umulhi(y, y);                                // y^2 in 2^-52
+  const uint32_t e = y - (q >> 11) + (__umulhi(__umulhi(q, y), 715827883u) >> 20);
+  const unsigned long long w = pow2[(f >> 32) & 1023];
+  power = (int)(f >> 42);
+  return w - (((w >> 32) * e + __umulhi((uint32_t)w, e)) >> 10);
 }
 // The weight rounded to units of 2^-S, S <= 61.
 __device__ __forceinline__ unsigned long long weight(const unsigned long long *pow2, float m, float ch, float cl,
@@ -1735,7 +1721,7 @@ __global__ void __launch_bounds__(SA_THREADS, SA_CTAS_PER_SM) k_sample(const Sam
     const Law l = law_of(a, r);
     if (lane == 0) s.law = l;
   }
-  if (t < 128) s.pow2[t] = g_pow2[t];
+  for (int i = t; i < 1024; i += SA_THREADS) s.pow2[i] = __umul64hi(g_pow2[i >> 4], g_pow2[64 + (i & 15)]);
   if (t == 0) s.n_list = 0, s.cut_short = 0, s.run = 0, s.odd = 0;
 
   Row<E, U> row;
