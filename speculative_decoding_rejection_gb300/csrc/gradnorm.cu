@@ -29,6 +29,7 @@ struct NormArgs {
   long long n_items;
   int state_bits, inf;
   float max_norm;
+  float max_low;         // what f32 leaves of it
   const float *grad_scale;
   float *out;
   double *part;      // one per CTA of the first kernel
@@ -182,14 +183,17 @@ __global__ void __launch_bounds__(GN_THREADS, GN_CTAS_PER_SM) k_grad_norm(const 
   if (threadIdx.x == 0) a.part[blockIdx.x] = sum;
 }
 
-// The root of a sum of squares in f32: of the leading 24 bits of a mantissa over an even
-// power, within a step of the last place. (A root and a quotient of 64 bits take microseconds.)
-__device__ __forceinline__ float root(double x) {
-  if (!(x > 0.0 && x <= 1.7976931348623157e308)) return (float)x;   // zero, infinity, NaN
+// The root of a sum of squares in two words of f32: of a mantissa over an even power, the
+// first word corrected by what its square leaves. (A root and a quotient of 64 bits take microseconds.)
+__device__ __forceinline__ void root(double x, float &hi, float &lo) {
+  hi = (float)x, lo = 0.f;
+  if (!(x > 0.0 && x <= 1.7976931348623157e308)) return;   // zero, infinity, NaN
   const long long bits = __double_as_longlong(x);
   const int e = (int)(bits >> 52) - 1023, even = e & ~1;   // (a sum of squares that are no f32 zero is normal)
-  const float m = (float)__longlong_as_double((bits & 0xfffffffffffffll) | (long long)(1023 + e - even) << 52);
-  return ldexpf(__fsqrt_rn(m), even / 2);
+  const double m = __longlong_as_double((bits & 0xfffffffffffffll) | (long long)(1023 + e - even) << 52);
+  const float m0 = (float)m, r = __fsqrt_rn(m0);
+  hi = ldexpf(r, even / 2);
+  lo = ldexpf((fmaf(-r, r, m0) + (float)(m - (double)m0)) * 0.5f / r, even / 2);
 }
 
 // The norm and the factor, in thread 0.
@@ -202,9 +206,20 @@ __device__ __forceinline__ void join(const NormArgs &a, float *norm, float *fact
   x = block_join(x, a.inf);
   if (threadIdx.x != 0) return;
   const float s = a.grad_scale ? *a.grad_scale : 1.f;
-  const float n = fabsf(s) * (a.inf ? (float)x : root(x));
-  const float f = a.max_norm / (n + 1e-6f);
+  float hi, lo = 0.f;
+  if (a.inf) hi = (float)x;
+  else root(x, hi, lo);
+  const float n = fabsf(s) * hi, rest = fmaf(fabsf(s), hi, -n) + fabsf(s) * lo;
   *norm = n;
+  float d = n + 1e-6f, f;
+  if (n <= 3.402823466e38f) {
+    *norm = n + rest;
+    const float back = d - n, left = (n - (d - back)) + (1e-6f - back) + rest + 2.525e-15f;   // 1e-6 is over 1e-6f by this
+    f = a.max_norm / d;
+    if (f > 1e-30f && f < 2.f) f += (fmaf(-f, d, a.max_norm) + a.max_low - f * left) / d;
+  } else {
+    f = a.max_norm / d;
+  }
   *factor = s * (f >= 1.f ? 1.f : f);   // a NaN passes through: it is below nothing
 }
 
@@ -302,6 +317,7 @@ int grad_norm(const void *table, int64_t n_items, int state_bits, int inf, doubl
   a.state_bits = state_bits;
   a.inf = inf != 0;
   a.max_norm = (float)std::min(max_norm, 3.4028234663852886e38);   // over any norm, or infinite: nothing is clipped
+  a.max_low = max_norm < 3e38 ? (float)(max_norm - (double)a.max_norm) : 0.f;
   a.grad_scale = grad_scale;
   a.out = out;
   a.hdr = static_cast<WsHeader *>(workspace);
