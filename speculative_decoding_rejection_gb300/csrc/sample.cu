@@ -24,11 +24,18 @@
 //   need a value outside that range goes by intervals.
 //   Intervals. As a list's, of all of the row's tokens: a pass for their counts and masses
 //   and one for the tokens of an interval that a border falls in, from L2.
-//   Divisions, where an interval holds too many to tell apart. Bins of the distance below the row's largest key (2048 of them), counts
-//   and masses; the bin a border falls in is divided again until it holds one value.
-//   The passes after the first come from L2.
+//   Divisions, where an interval holds too many to tell apart. Bins of the distance below
+//   the row's largest key (2048 of them), counts and masses; the bin a border falls in is
+//   divided again until it holds one value. The passes after the first come from L2.
 //   Which of the equal values it is goes by id there: the matches are counted per chunk
 //   of the row, in the chunks whose largest logit reaches the value.
+//
+// Measured, 1024 rows of 201088 bf16 logits (the copy rate would take 61.5 us): min-p 126 us,
+// top-k 154, top-p alone 244, mixed 180. Lists come at 0.74 of the copy rate; then a row's
+// decision is a chain of barriers, 10 to 25 thousand clocks, which the other CTA of the SM covers in
+// part. A histogram costs an atomic per logit (3.7 clocks for 32). f32 by intervals: a weight and three
+// atomics per logit, 250 rows of 128256 in 359 us. Few rows are latency: 4 x 1024 f32 14 us,
+// most of it code that runs once and is fetched for it, so loops stay rolled up.
 #include "draft.cuh"
 
 #include <cooperative_groups.h>
@@ -41,6 +48,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
+// Two CTAs of 512 threads per SM: 1024 rows of 201088 bf16 with mixed laws 212 us, 128 of 128256 f32 153;
+// three of 256 threads 215 and 190, one of 512 268, all before the list's comparisons were packed.
 constexpr int SA_THREADS = 512;
 constexpr int SA_WARPS = SA_THREADS / 32;
 constexpr int SA_LEVEL = 2048;         // bins of a division, intervals of a list
@@ -48,7 +57,7 @@ constexpr int SA_CHUNKS = 256;         // chunks of a CTA's slice
 constexpr int SA_CTAS_PER_SM = 2;
 constexpr int SA_ENTRIES = 6144;       // values that a histogram's law may have
 constexpr int SA_LIST = 2560;          // tokens of a list
-constexpr int SA_FULL = 1536;          // a row that short goes to it whole
+constexpr int SA_FULL = 1536;          // a row that short goes to it whole (4 x 1500 f32 22 us, by intervals 36)
 constexpr int SA_NEAR = 256;    // tokens that are ranked one by one
 constexpr int SA_TOP_K = 256;          // top-k up to which the threads' maxima give a border
 static_assert(SA_TOP_K <= SA_THREADS && SA_TOP_K <= SA_NEAR, "top-k's border and its tokens");
@@ -1956,11 +1965,11 @@ extern "C" int spec_sample(const void *logits, int dt, int R, int V, const int32
   const int sms = num_sms();
   if (sms <= 0) return SPEC_ERR_CUDA;
   // A cluster of up to eight CTAs per row while there are too few rows for the SMs and
-  // every CTA keeps 4096 elements.
+  // every CTA keeps 4096 elements. (Two for each of 256 rows of 151936 bf16: 208 us, one 79.)
   int C = 1;
   while (C < SA_MAX_CLUSTER && (long long)R * C * 2 <= SA_CTAS_PER_SM * sms && V / (C * 2) >= 4096) C *= 2;
   // Chunks of a row: a vector per lane where the row is short, four where each warp has
-  // four all the same.
+  // four all the same (8 rows of 128256 bf16 40 us; with four where it has two 47).
   const int per = 32 * (int)(16 / es);
   const bool few = V / C < per * 4 * SA_WARPS;
   const int chunk = per * (few ? 1 : 4);
