@@ -7,7 +7,7 @@
 //
 //   - Logits are compared and counted exactly.
 //   - A weight 2^-t, t = (m - z) log2(e) / T, is a 64-bit whole number: t is formed in two
-//     f32 words and taken in units of 2^-42, 2^-t is the product of a table's entry (10
+//     f32 words and taken in units of 2^-41, 2^-t is the product of a table's entry (10
 //     bits of the fraction) and a cubic in the 32 bits left, all in 64-bit
 //     fixed point. Masses are sums of these, the same in whatever order they are taken.
 //
@@ -263,8 +263,8 @@ __device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
 
 // 2^-t for t = (m - z) c, as a fraction in units of 2^-62 (over a half) and a power: the
 // result is fraction 2^-power, 0 for t of 63 and more. The difference and its product with c are
-// taken in two words each: t is right within 2^-41 (its second word is under 2^-18 and
-// rounded twice) and the units of 2^-42, the fixed-point product within a few units of
+// taken in two words each: t is right within 2^-41 (its second word is under 2^-17), what it
+// has over a 1024th is rounded to units of 2^-41, the fixed-point product is right within a few units of
 // 2^-42, so a weight within 2^-39 of itself.
 __device__ __forceinline__ unsigned long long fraction(const unsigned long long *pow2, float m, float ch, float cl,
                                                        float z, int &power) {
@@ -274,23 +274,26 @@ __device__ __forceinline__ unsigned long long fraction(const unsigned long long 
   power = 0;
   if (!(ph < 63.f)) return 0;
   const float pl = fmaf(dh, ch, -ph) + fmaf(dh, cl, dl * ch);
-  const long long t = __float2ll_rn(ph * 4398046511104.f) + __float2int_rn(pl * 4398046511104.f);
-  const unsigned long long f = t < 0 ? 0 : (unsigned long long)t;
-  // 1 - 2^-r = y - y^2 / 2 + y^3 / 6 in units of 2^-42, y = r ln 2 < 2^-10.5
-  const uint32_t y = __umulhi((uint32_t)f, 2977044472u);
-  const uint32_t q = __umulhi(y, y);                                // y^2 in 2^-52
-  const uint32_t e = y - (q >> 11) + (__umulhi(__umulhi(q, y), 715827883u) >> 20);
-  const unsigned long long w = pow2[(f >> 32) & 1023];
-  power = (int)(f >> 42);
-  return w - (((w >> 32) * e + __umulhi((uint32_t)w, e)) >> 10);
+  // a 1024th below, by 2^-16 at least but for the first, so that the second word leaves the rest positive
+  const float at = fmaxf(fmaf(ph, 1024.f, -0.516f), 0.f) + 12582912.f;
+  const int index = __float_as_int(at) - __float_as_int(12582912.f);
+  const float rest = fmaf(at - 12582912.f, -0.0009765625f, ph);   // exact
+  const uint32_t r = __float2uint_rn(rest * 2199023255552.f) + (uint32_t)__float2int_rn(pl * 2199023255552.f);
+  // 1 - 2^-r = y - y^2 / 2 + y^3 / 6 in units of 2^-41, y = r ln 2
+  const uint32_t y = __umulhi(r, 2977044472u);
+  const uint32_t q = __umulhi(y, y);                                // y^2 in 2^-50
+  const uint32_t e = y - (q >> 10) + (__umulhi(__umulhi(q, y), 715827883u) >> 18);
+  const unsigned long long w = pow2[index & 1023];
+  power = index >> 10;
+  return w - (((w >> 32) * e + __umulhi((uint32_t)w, e)) >> 9);
 }
-// The weight rounded to units of 2^-S, S <= 61.
+// The weight in whole units of 2^-S, S <= 61.
 __device__ __forceinline__ unsigned long long weight(const unsigned long long *pow2, float m, float ch, float cl,
                                                      int S, float z) {
   int power;
   const unsigned long long w = fraction(pow2, m, ch, cl, z, power);
   const int shift = 62 - S + power;
-  return shift < 64 ? (w + (1ull << (shift - 1))) >> shift : 0ull;
+  return shift < 64 ? w >> shift : 0ull;
 }
 // The same out of line: most of a row's code runs once, and is fetched for it.
 __device__ __noinline__ unsigned long long weight_of(const unsigned long long *pow2, float m, float ch, float cl, int S,
