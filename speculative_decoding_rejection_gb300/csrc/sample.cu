@@ -16,7 +16,7 @@
 //   Lists. Where min-p or top-k bounds the law, the row is read once from HBM and the
 //   tokens above the border (min-p's below the largest logit so far; for top-k the k-th
 //   largest of the threads' first maxima) go to a list in shared memory. Counts and
-//   masses of 2048 equal intervals of the list's logits, and a look at the tokens of the
+//   masses of equal intervals of the list's logits, and a look at the tokens of the
 //   one interval that a border falls in, give every border and the token.
 //   Values, bf16. A row has few distinct values: a histogram of counts in shared memory
 //   has a bin for each value of magnitude 2^-21 to 2^11; one weight per bin and a scan
@@ -25,7 +25,7 @@
 //   Intervals. As a list's, of all of the row's tokens: a pass for their counts and masses
 //   and one for the tokens of an interval that a border falls in, from L2.
 //   Divisions, where an interval holds too many to tell apart. Bins of the distance below
-//   the row's largest key (2048 of them), counts and masses; the bin a border falls in is
+//   the row's largest key, counts and masses; the bin a border falls in is
 //   divided again until it holds one value. The passes after the first come from L2.
 //   Which of the equal values it is goes by id there: the matches are counted per chunk
 //   of the row, in the chunks whose largest logit reaches the value.
@@ -34,7 +34,7 @@
 // top-k 154, top-p alone 244, mixed 180. Lists come at 0.74 of the copy rate; then a row's
 // decision is a chain of barriers, 10 to 25 thousand clocks, which the other CTA of the SM covers in
 // part. A histogram costs an atomic per logit (3.7 clocks for 32). f32 by intervals: a weight and three
-// atomics per logit, 250 rows of 128256 in 359 us. Few rows are latency: 4 x 1024 f32 14 us,
+// atomics per logit, 250 rows of 128256 in 235 us. Few rows are latency: 4 x 1024 f32 14 us,
 // most of it code that runs once and is fetched for it, so loops stay rolled up.
 #include "draft.cuh"
 
@@ -52,15 +52,19 @@ namespace cg = cooperative_groups;
 // three of 256 threads 215 and 190, one of 512 268, all before the list's comparisons were packed.
 constexpr int SA_THREADS = 512;
 constexpr int SA_WARPS = SA_THREADS / 32;
-constexpr int SA_LEVEL = 2048;         // bins of a division, intervals of a list
+// Bins of a division and intervals of a row; intervals of a list. (250 rows of 128256 f32, top-p: with
+// 2048 of a row 340 us, as some hold too many, with 4096 235. With 4096 of a list too, which are 24 KB
+// more of what loads on their way want, top-k of 1024 x 201088 bf16 takes 166 us, not 153.)
+constexpr int SA_LEVEL = 4096, SA_LIST_LEVEL = 2048;
 constexpr int SA_CHUNKS = 256;         // chunks of a CTA's slice
 constexpr int SA_CTAS_PER_SM = 2;
 constexpr int SA_ENTRIES = 6144;       // values that a histogram's law may have
 constexpr int SA_LIST = 2560;          // tokens of a list
 constexpr int SA_FULL = 1536;          // a row that short goes to it whole (4 x 1500 f32 22 us, by intervals 36)
-constexpr int SA_NEAR = 256;    // tokens that are ranked one by one
+constexpr int SA_NEAR = SA_THREADS;    // tokens of an interval that are ranked one by one, a thread each
+constexpr int SA_FEW = 256;            // tokens of a whole law that are
 constexpr int SA_TOP_K = 256;          // top-k up to which the threads' maxima give a border
-static_assert(SA_TOP_K <= SA_THREADS && SA_TOP_K <= SA_NEAR, "top-k's border and its tokens");
+static_assert(SA_TOP_K <= SA_THREADS && SA_TOP_K <= SA_FEW, "top-k's border and its tokens");
 constexpr int SA_MAX_CLUSTER = 8;
 // bf16 magnitudes 2^-21 .. 2^11 have bins of their own: 4096 of each sign, index
 // sign << 12 | (bits - SA_LO). One more for zero, one for what is below -2^11.
@@ -203,6 +207,10 @@ struct Verdict {
   int slow;            // the next way has to decide
 };
 
+template <int L>
+struct Bins {   // counts and masses of intervals or of a division
+  uint32_t cnt[L], lo[L], hi[L];
+};
 struct SampleSmem {
   union {
     struct {
@@ -211,10 +219,9 @@ struct SampleSmem {
     };
     struct {
       unsigned long long list[SA_LIST];     // key of the logit, then ~id: falls in the tokens' order
-      struct {                              // counts and masses of intervals or of a division
-        uint32_t cnt[SA_LEVEL], lo[SA_LEVEL], hi[SA_LEVEL];
-      } level;
+      Bins<SA_LIST_LEVEL> level;
     };
+    Bins<SA_LEVEL> rows;
   };
   unsigned long long near[SA_NEAR], near_w[SA_NEAR];
   unsigned long long pow2[1024];   // 2^(-i/1024) in units of 2^-62
@@ -674,14 +681,15 @@ __device__ void decide_values(SampleSmem &s, float m) {
 // Counts (and with `masses` the masses) of the intervals of the list's tokens with keys from
 // `from` on, scanned; 4 intervals per thread.
 // inside: the one that these intervals divide again, -1 for the first division.
+template <int L>
 struct Intervals {
   float m, scale;
   int inside;
   __device__ __forceinline__ int of(float z) const {   // -1: outside
     const float x = (m - z) * scale;
-    const int b = min(SA_LEVEL - 1, (int)x);
+    const int b = min(L - 1, (int)x);
     if (inside < 0) return b;
-    return b != inside ? -1 : min(SA_LEVEL - 1, (int)((x - (float)inside) * (float)SA_LEVEL));
+    return b != inside ? -1 : min(L - 1, (int)((x - (float)inside) * (float)L));
   }
 };
 __device__ __forceinline__ float list_value(unsigned long long key) { return of_key((uint32_t)(key >> 32)); }
@@ -691,21 +699,31 @@ __device__ void add_mass(uint32_t *lo, uint32_t *hi, unsigned long long w) {
   if (up != 0) atomicAdd(hi, up);
 }
 // The sums of the level's counts (and masses) before each thread's bins.
+template <int L>
+__device__ __forceinline__ const Bins<L> &bins_of(const SampleSmem &s) {
+  if constexpr (L == SA_LEVEL) return s.rows;
+  else return s.level;
+}
+template <int L>
 __device__ void scan_level(SampleSmem &s, bool masses) {
-  constexpr int PT = SA_LEVEL / SA_THREADS;
+  const Bins<L> &level = bins_of<L>(s);
+  constexpr int PT = L / SA_THREADS;
   uint32_t c = 0;
   unsigned long long mass = 0;
 #pragma unroll
   for (int i = 0; i < PT; ++i) {
     const int b = threadIdx.x * PT + i;
-    c += s.level.cnt[b];
-    if (masses) mass += s.level.lo[b] + ((unsigned long long)s.level.hi[b] << 32);
+    c += level.cnt[b];
+    if (masses) mass += level.lo[b] + ((unsigned long long)level.hi[b] << 32);
   }
   block_scan(s, c, mass);
 }
-__device__ void count_list(SampleSmem &s, int n, const Intervals &iv, unsigned long long from, bool masses, int S) {
+__device__ void count_list(SampleSmem &s, int n, const Intervals<SA_LIST_LEVEL> &iv, unsigned long long from, bool masses, int S) {
   const int t = threadIdx.x;
-  for (int i = t; i < SA_LEVEL * (masses ? 3 : 1); i += SA_THREADS) s.level.cnt[i] = 0;   // lo and hi lie behind it
+  for (int i = t; i < SA_LIST_LEVEL; i += SA_THREADS) {
+    s.level.cnt[i] = 0;
+    if (masses) s.level.lo[i] = s.level.hi[i] = 0;
+  }
   __syncthreads();
   for (int i = t; i < n; i += SA_THREADS) {
     const unsigned long long key = s.list[i];
@@ -716,19 +734,21 @@ __device__ void count_list(SampleSmem &s, int n, const Intervals &iv, unsigned l
     if (masses) add_mass(&s.level.lo[b], &s.level.hi[b], weight_of(s.pow2, iv.m, s.law.ch, s.law.cl, S, z));
   }
   __syncthreads();
-  scan_level(s, masses);
+  scan_level<SA_LIST_LEVEL>(s, masses);
 }
 // The interval that a count or a mass reaches, with the tokens and the mass before it, to
 // `found` (at -1: the target lies behind the last one). By the block.
+template <int L>
 __device__ void find_interval(SampleSmem &s, unsigned long long target, bool by_n) {
-  constexpr int PT = SA_LEVEL / SA_THREADS;
+  constexpr int PT = L / SA_THREADS;
   const int t = threadIdx.x;
+  const Bins<L> &level = bins_of<L>(s);
   if (t < 32) {
     const Found f = find_entry(s, target, by_n, PT, [&](int b, uint32_t &c, unsigned long long &w) {
       c = 0, w = 0;
       if (b < 0) return;
-      if (by_n) c = s.level.cnt[b];
-      else c = 1, w = s.level.lo[b] + ((unsigned long long)s.level.hi[b] << 32);
+      if (by_n) c = level.cnt[b];
+      else c = 1, w = level.lo[b] + ((unsigned long long)level.hi[b] << 32);
     });
     if (t == 0) {
       s.found = f;
@@ -738,10 +758,10 @@ __device__ void find_interval(SampleSmem &s, unsigned long long target, bool by_
         uint32_t n0 = s.pre_n[t0];
         unsigned long long c0 = s.pre_mass[t0];
         for (int i = t0 * PT; i < f.at; ++i) {
-          n0 += s.level.cnt[i];
-          if (!by_n) c0 += s.level.lo[i] + ((unsigned long long)s.level.hi[i] << 32);
+          n0 += level.cnt[i];
+          if (!by_n) c0 += level.lo[i] + ((unsigned long long)level.hi[i] << 32);
         }
-        s.found.n0 = n0, s.found.c0 = c0, s.found.cnt = s.level.cnt[f.at];
+        s.found.n0 = n0, s.found.c0 = c0, s.found.cnt = level.cnt[f.at];
       }
     }
   }
@@ -775,9 +795,9 @@ __device__ void rank_near(SampleSmem &s, float m, int S, int many, bool by_n) {
 }
 // The token of the list (from `from` on) that a count or a mass reaches, as rank_near gives it.
 // False: its interval holds too many.
-__device__ bool find_key(SampleSmem &s, int n, const Intervals &iv, unsigned long long from, int S,
+__device__ bool find_key(SampleSmem &s, int n, const Intervals<SA_LIST_LEVEL> &iv, unsigned long long from, int S,
                          unsigned long long target, bool by_n) {
-  find_interval(s, target, by_n);
+  find_interval<SA_LIST_LEVEL>(s, target, by_n);
   const int at = s.found.at, many = at < 0 ? SA_NEAR + 1 : (int)s.found.cnt;
   if (many > SA_NEAR) return false;
   for (int i = threadIdx.x; i < n; i += SA_THREADS) {
@@ -789,13 +809,13 @@ __device__ bool find_key(SampleSmem &s, int n, const Intervals &iv, unsigned lon
   return true;
 }
 
-// The leader: the verdict from the at most SA_NEAR tokens of the list with keys from `from` on, a
+// The leader: the verdict from the at most SA_FEW tokens of the list with keys from `from` on, a
 // thread each, in the order of their ranks.
 __device__ void decide_few(SampleSmem &s, float m, int n, unsigned long long from) {
   const int t = threadIdx.x;
   const Law &law = s.law;
   if (t == 0) s.n_near = 0;
-  if (t < SA_NEAR) s.near[t] = 0;
+  s.near[t] = 0;
   __syncthreads();
   for (int i = t; i < n; i += SA_THREADS) {
     const unsigned long long key = s.list[i];
@@ -803,7 +823,7 @@ __device__ void decide_few(SampleSmem &s, float m, int n, unsigned long long fro
   }
   __syncthreads();
   const int many = s.n_near;
-  const unsigned long long key = t < SA_NEAR ? s.near[t] : 0;
+  const unsigned long long key = s.near[t];
   int rank = 0;
   if (t < ((many + 31) & ~31))
     for (int i = 0; i < many; i += 4) {   // zeros behind the last
@@ -813,15 +833,15 @@ __device__ void decide_few(SampleSmem &s, float m, int n, unsigned long long fro
     }
   const int kept = law.top_k > 0 ? min(many, law.top_k) : many;
   constexpr int S = 62 - 9;   // at most 256 weights
-  static_assert(SA_NEAR <= 256, "units");
+  static_assert(SA_FEW <= 256 && SA_FEW <= SA_NEAR, "units");
   const float z = list_value(key);
   const bool in = t < many && rank < kept;
   const unsigned long long w = in ? weight_of(s.pow2, m, law.ch, law.cl, S, z) : 0;
-  if (t < SA_NEAR) s.near_w[t] = 0;
+  s.near_w[t] = 0;
   __syncthreads();
   if (in) s.near_w[rank] = w;
   __syncthreads();
-  block_scan(s, 0, t < SA_NEAR ? s.near_w[t] : 0);
+  block_scan(s, 0, s.near_w[t]);
   unsigned long long mass = s.pre_mass[SA_THREADS];
   const unsigned long long before = in ? s.pre_mass[rank] : 0;
   int last = kept - 1;   // the rank of the last token
@@ -889,11 +909,11 @@ __device__ void decide_list(SampleSmem &s, float m, int n) {
     if (t == 0) s.verdict = v;
     return;
   }
-  if (in <= SA_NEAR) {
+  if (in <= SA_FEW) {
     decide_few(s, m, n, from);
     return;
   }
-  const Intervals iv{m, m > low ? (float)SA_LEVEL / (m - low) : 0.f, -1};
+  const Intervals<SA_LIST_LEVEL> iv{m, m > low ? (float)SA_LIST_LEVEL / (m - low) : 0.f, -1};
   const int S = unit_of(rough);
   if (law.top_k > 0 && law.top_k <= (int)in) {
     count_list(s, n, iv, from, false, S);
@@ -901,7 +921,7 @@ __device__ void decide_list(SampleSmem &s, float m, int n) {
       from = s.key;
       in = (uint32_t)law.top_k;
       __syncthreads();
-      if (in <= SA_NEAR) {
+      if (in <= SA_FEW) {
         decide_few(s, m, n, from);
         return;
       }
@@ -949,7 +969,7 @@ struct Level {
 
 template <class E, int U>
 __device__ void level_count(SampleSmem &s, const Row<E, U> &row, const Level &l) {
-  uint32_t *cnt = s.level.cnt, *lo = s.level.lo, *hi = s.level.hi;
+  uint32_t *cnt = s.rows.cnt, *lo = s.rows.lo, *hi = s.rows.hi;
   for (int i = threadIdx.x; i < SA_LEVEL; i += SA_THREADS) cnt[i] = lo[i] = hi[i] = 0;
   __syncthreads();
   const uint32_t top = key_of(l.m);
@@ -998,13 +1018,13 @@ __device__ void merge_levels(cg::cluster_group &cluster, SampleSmem &s) {
 #pragma unroll
     for (int r = 0; r < SA_MAX_CLUSTER; ++r) {
       if (r >= C) break;
-      const uint32_t *h = cluster.map_shared_rank(s.level.cnt, r);   // lo and hi lie behind it
+      const uint32_t *h = cluster.map_shared_rank(s.rows.cnt, r);   // lo and hi lie behind it
       n += h[i], lo[r] = h[SA_LEVEL + i], hi[r] = h[2 * SA_LEVEL + i];
     }
 #pragma unroll
     for (int r = 0; r < SA_MAX_CLUSTER; ++r)
       if (r < C) w += lo[r] + ((unsigned long long)hi[r] << 32);
-    uint32_t *h = cluster.map_shared_rank(s.level.cnt, 0);
+    uint32_t *h = cluster.map_shared_rank(s.rows.cnt, 0);
     h[i] = n, h[SA_LEVEL + i] = (uint32_t)w, h[2 * SA_LEVEL + i] = (uint32_t)(w >> 32);
   }
   cluster.sync();
@@ -1016,7 +1036,7 @@ __device__ Found level_find(cg::cluster_group &cluster, SampleSmem &s, const Row
   constexpr int PT = SA_LEVEL / SA_THREADS;
   const int rank = (int)cluster.block_rank(), t = threadIdx.x;
   level_count(s, row, l);
-  uint32_t *cnt = s.level.cnt, *lo = s.level.lo, *hi = s.level.hi;
+  uint32_t *cnt = s.rows.cnt, *lo = s.rows.lo, *hi = s.rows.hi;
   merge_levels(cluster, s);
   if (rank == 0) {
     if (t == 0 && !l.whole && l.last >= l.first && (l.last - l.first) >> l.shift < (uint32_t)SA_LEVEL) {
@@ -1146,9 +1166,9 @@ __device__ __noinline__ void decide_divisions(cg::cluster_group &cluster, Sample
 // As a list's: counts (and masses) of the intervals of the row's tokens from `from` on, in the
 // leader's level and scanned.
 template <class E, int U>
-__device__ void count_row(cg::cluster_group &cluster, SampleSmem &s, const Row<E, U> &row, const Intervals &iv,
+__device__ void count_row(cg::cluster_group &cluster, SampleSmem &s, const Row<E, U> &row, const Intervals<SA_LEVEL> &iv,
                           unsigned long long from, bool masses, int S) {
-  for (int i = threadIdx.x; i < SA_LEVEL * 3; i += SA_THREADS) s.level.cnt[i] = 0;   // lo and hi lie behind it
+  for (int i = threadIdx.x; i < SA_LEVEL * 3; i += SA_THREADS) s.rows.cnt[i] = 0;   // lo and hi lie behind it
   __syncthreads();
   const float least = list_value(from), ch = s.law.ch, cl = s.law.cl;
   for (int c = threadIdx.x >> 5; c < row.nc; c += SA_WARPS) {
@@ -1165,14 +1185,14 @@ __device__ void count_row(cg::cluster_group &cluster, SampleSmem &s, const Row<E
           if (!(z > least) && !(z == least && ~(uint32_t)id >= (uint32_t)from)) continue;
           const int b = iv.of(z);
           if (b < 0) continue;
-          atomicAdd(&s.level.cnt[b], 1u);
-          if (masses) add_mass(&s.level.lo[b], &s.level.hi[b], weight(s.pow2, iv.m, ch, cl, S, z));
+          atomicAdd(&s.rows.cnt[b], 1u);
+          if (masses) add_mass(&s.rows.lo[b], &s.rows.hi[b], weight(s.pow2, iv.m, ch, cl, S, z));
         }
       }
     });
   }
   merge_levels(cluster, s);
-  if (cluster.block_rank() == 0) scan_level(s, masses);
+  if (cluster.block_rank() == 0) scan_level<SA_LEVEL>(s, masses);
 }
 
 // What find_row says.
@@ -1185,10 +1205,10 @@ struct Near {
 // The token that a count (by_n) or a mass reaches; frac: `target` is the part of the level's mass in
 // units of 2^-64 that has to be reached.
 template <class E, int U>
-__device__ Near find_row(cg::cluster_group &cluster, SampleSmem &s, const Row<E, U> &row, const Intervals &iv,
+__device__ Near find_row(cg::cluster_group &cluster, SampleSmem &s, const Row<E, U> &row, const Intervals<SA_LEVEL> &iv,
                          unsigned long long from, int S, unsigned long long target, bool by_n, bool frac) {
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), t = threadIdx.x;
-  if (rank == 0) find_interval(s, frac ? reach(s.pre_mass[SA_THREADS], target) : target, by_n);
+  if (rank == 0) find_interval<SA_LEVEL>(s, frac ? reach(s.pre_mass[SA_THREADS], target) : target, by_n);
   else if (t == 0) s.n_near = 0;
   cluster.sync();
   const Found f = *cluster.map_shared_rank(&s.found, 0);
@@ -1246,7 +1266,7 @@ __device__ __noinline__ void decide_row(cg::cluster_group &cluster, SampleSmem &
   const float least = fmaxf(__double2float_ru((double)m + s.law.log_min), -3.402823466e38f);
   unsigned long long from = (unsigned long long)key_of(least) << 32;
   // what is further below than the last interval has no weight
-  const Intervals iv{m, (float)SA_LEVEL * s.law.ch / 63.f, -1};
+  const Intervals<SA_LEVEL> iv{m, (float)SA_LEVEL * s.law.ch / 63.f, -1};
   bool counted = false;   // the level holds the first division's
   // a find in two divisions where one interval is too full
   auto find = [&](int S, unsigned long long target, bool by_n, bool frac) {
@@ -1254,7 +1274,7 @@ __device__ __noinline__ void decide_row(cg::cluster_group &cluster, SampleSmem &
     counted = true;
     Near n = find_row(cluster, s, row, iv, from, S, target, by_n, frac);
     if (n.state != 2) return n;
-    const Intervals part{iv.m, iv.scale, n.at};
+    const Intervals<SA_LEVEL> part{iv.m, iv.scale, n.at};
     count_row(cluster, s, row, part, from, !by_n, S);
     counted = false;
     Near r = find_row(cluster, s, row, part, from, S, n.target - (by_n ? (unsigned long long)n.rank : n.before), by_n, false);
