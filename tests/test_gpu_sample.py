@@ -365,3 +365,47 @@ def test_no_access_leaves_the_call(R, V, dtype, checked):
         got, status = run(z, u, law, want_kept=True, want_filtered=True)
         assert status == sv.SPEC_OK
         check(z, u, law, got, rows=range(0, R, 1 + R // 40))
+
+
+@pytest.mark.parametrize("per", [200, 255, 256, 257, 511, 512, 513, 1700])
+@pytest.mark.parametrize("kind", ["none", "top_p"])
+def test_crowded_intervals(per, kind):
+    """f32 rows whose tokens crowd in eight steps of the logits, `per` to a step, so that a
+    border's neighbours are few, as many as are ranked, or too many to be."""
+    rng = np.random.default_rng(per)
+    step = 63 / 4096 * np.log(2)
+    R, V = 6, max(8 * per, 1700)
+    z = np.full((R, V), -200.0)
+    for r in range(R):
+        at = rng.permutation(V)[:8 * per]
+        z[r, at] = -step * (np.repeat(np.arange(8) * 3, per) + rng.uniform(0.05, 0.95, 8 * per))
+        z[r, at[0]] = 0.0
+    z = torch.tensor(z, dtype=F32, device=DEV)
+    law = dict(temperature=np.ones(R, np.float32))
+    if kind == "top_p":
+        law["top_p"] = rng.uniform(0.1, 0.95, R).astype(np.float32)
+    u = rng.random(R).astype(np.float32)
+    got, status = run(z, u, law, want_kept=True, want_filtered=True)
+    assert status == sv.SPEC_OK
+    check(z, u, law, got)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("many", [200, 300, 510, 520, 1500])
+def test_crowded_lists(many, dtype):
+    """A law by min-p with many tokens next to one another and one far above them: they share an
+    interval of the list."""
+    rng = np.random.default_rng(many)
+    R, V = 4, 6001
+    z = np.full((R, V), -30.0)
+    for r in range(R):
+        at = rng.permutation(V)[:many + 1]
+        z[r, at[:many]] = rng.uniform(1, 1 + 1e-4, many)
+        z[r, at[many]] = 6.0
+    z = torch.tensor(z).to(dtype).to(DEV)
+    law = dict(temperature=np.ones(R, np.float32), min_p=np.full(R, 1e-3, np.float32),
+               top_p=np.array([1.0, 0.3, 0.6, 0.9], np.float32), top_k=np.array([0, many // 2, 0, 400], np.int32))
+    u = np.array([0.2, 0.9, 0.5, 0.7], np.float32)
+    got, status = run(z, u, law, want_kept=True, want_filtered=True)
+    assert status == sv.SPEC_OK
+    check(z, u, law, got)
