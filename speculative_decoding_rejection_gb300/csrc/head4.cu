@@ -33,7 +33,7 @@
 //
 // Measured, 4096 columns to 128256 (263 to 279 MB of weights): 1 row 64 us, 5 rows 68 (groups of 64,
 // 4.1 TB/s, 0.62 of the copy rate), 8 rows 72; issue slots bound them, the ring alone would take
-// 62. 16, 32, 64 rows 120, 175, 262 us: latency with four warps per scheduler, the tensor
+// 62. 16, 32, 64 rows 120, 150, 245 us: latency with four or five warps per scheduler, the tensor
 // instructions alone would take 113 us for 64. 4096 to 32000, 1 row: 22.5 us.
 #include "draft.cuh"
 
@@ -43,10 +43,11 @@ namespace sv {
 namespace {
 
 constexpr int H4_WARPS = 16;         // that multiply
+constexpr int H4_MORE_WARPS = 20;    // where they save a round
 // Up to 8 rows of x: one more warp fills the ring and three join the sums of those that share a
 // tile. More: the first warp fills the ring too, as the others' registers are needed.
 constexpr int H4_JOINERS = 3;
-__host__ __device__ constexpr int threads_of(int nt) { return 32 * (H4_WARPS + (nt == 1 ? 1 + H4_JOINERS : 0)); }
+constexpr int H4_FEW_THREADS = 32 * (H4_WARPS + 1 + H4_JOINERS);
 constexpr int H4_TILE = 16;          // rows of a tile
 constexpr int H4_CHUNK = 128;        // columns of a block
 constexpr int H4_CODES = H4_TILE * H4_CHUNK / 2;
@@ -75,7 +76,7 @@ struct Plan4 {
 // Without the group: the workspace does not depend on it.
 Plan4 plan4(int M, int N, int K) {
   Plan4 p{};
-  // (5 rows, 4096 to 128256, by the kernel for more rows: 123 against 72 us, 8 rows 118 against 72)
+  // (5 rows, 4096 to 128256, by the kernel for more rows: 120 against 72 us, 8 rows 115 against 72)
   p.nt = M <= 8 ? 1 : M <= 16 ? 2 : M <= 32 ? 4 : 8;
   const int chunks = chunks_of(K);
   p.ks = p.nt == 1 ? 8 : 1;
@@ -107,6 +108,7 @@ struct Head4Args {
   int M, N, K, group, zeros, act;
   int chunks, panel, slices, ks;
   int ctas;          // of a slice
+  int units, warps;  // of a CTA, for more than 8 rows
   int tiles, block;
   int per_stage;     // chunks of a stage
   int stages, stage_bytes;
@@ -282,9 +284,9 @@ __device__ __forceinline__ void result(const Head4Args &a, int slice, int m, int
 
 // Up to 8 rows of x.
 template <int SUBS>
-__global__ void __launch_bounds__(threads_of(1), 1) k_head4(const Head4Args a) {
+__global__ void __launch_bounds__(H4_FEW_THREADS, 1) k_head4(const Head4Args a) {
   extern __shared__ __align__(128) unsigned char smem[];
-  constexpr int THREADS = threads_of(1), WARP_SUMS = 8 * H4_COL, KEEP = 8;
+  constexpr int THREADS = H4_FEW_THREADS, WARP_SUMS = 8 * H4_COL, KEEP = 8;
   __shared__ uint64_t full[H4_MAX_STAGES], empty[H4_MAX_STAGES], sums[2], joined[2];
   __shared__ int abort;
   __shared__ uint32_t most[8];   // largest magnitudes of x's rows
@@ -445,8 +447,8 @@ __global__ void __launch_bounds__(threads_of(1), 1) k_head4(const Head4Args a) {
 }
 
 // More than 8 rows of x: a stage is two chunks of columns, of x first, then of a tile per warp.
-template <int NT, int SUBS>
-__global__ void __launch_bounds__(threads_of(NT), 1) k_head4_rows(const Head4Args a) {
+template <int NT, int SUBS, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, 1) k_head4_rows(const Head4Args a) {
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int XB = 8 * NT * 2 * H4_CHUNK;   // bytes of x's chunk
   __shared__ uint64_t full[H4_MAX_STAGES], empty[H4_MAX_STAGES];
@@ -456,26 +458,28 @@ __global__ void __launch_bounds__(threads_of(NT), 1) k_head4_rows(const Head4Arg
   const int slice = blockIdx.x / a.ctas, cta = blockIdx.x % a.ctas;
   const int k0 = slice * a.panel, kn = min(a.panel, a.chunks - k0);   // chunks of this slice
   const int parts = (kn + H4_DEPTH - 1) / H4_DEPTH;
-  const int units = (a.tiles + H4_WARPS - 1) / H4_WARPS;
-  const int mine = cta < units ? (units - cta + a.ctas - 1) / a.ctas : 0;
-  const int total = mine * parts;                                     // stages of this CTA
+  // this CTA's pairs of tiles, in as many units as every CTA has, as even as they can be: a tile per
+  // warp at most, as no CTA has more than ceil(pairs / ctas)
+  const int p0 = (int)((long long)(a.tiles / 2) * cta / a.ctas), pairs = (int)((long long)(a.tiles / 2) * (cta + 1) / a.ctas) - p0;
+  auto unit_at = [&](int u) { return 2 * (p0 + pairs * u / a.units); };   // its first tile
+  const int total = a.units * parts;                                     // stages of this CTA
   if (blockIdx.x == 0 && t == 0) start_status(a.hdr);
   if (t == 0) {
     abort = 0;
-    for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], H4_WARPS);
+    for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], a.warps);
     fence_mbar_init();
   }
   __syncthreads();
   // by the first warp, a copy per lane: the weights of stage i, and x's part
   auto fill_w = [&](int i) {
-    const int u = cta + i / parts * a.ctas, c0 = i % parts * H4_DEPTH, n = min(H4_DEPTH, kn - c0);
-    const int tiles = min(H4_WARPS, a.tiles - u * H4_WARPS);
+    const int c0 = i % parts * H4_DEPTH, n = min(H4_DEPTH, kn - c0);
+    const int first = unit_at(i / parts), tiles = unit_at(i / parts + 1) - first;
     uint64_t *bar = &full[i % a.stages];
     if (lane == 0) mbar_arrive_tx(bar, (uint32_t)(n * (tiles * a.block + XB)));
     __syncwarp();
     if (2 * lane < tiles)
       bulk_g2s(ring + (size_t)(i % a.stages) * a.stage_bytes + H4_DEPTH * (XB + (size_t)2 * lane * a.block),
-               a.packed + ((long long)(u * H4_WARPS + 2 * lane) * a.chunks + 2 * (k0 + c0)) * a.block,
+               a.packed + ((long long)(first + 2 * lane) * a.chunks + 2 * (k0 + c0)) * a.block,
                (uint32_t)(2 * n * a.block), bar);
   };
   auto fill_x = [&](int i) {
@@ -498,15 +502,16 @@ __global__ void __launch_bounds__(threads_of(NT), 1) k_head4_rows(const Head4Arg
   const uint32_t wp = smem_u32(ring) + H4_DEPTH * (XB + warp / 2 * 2 * a.block) + warp % 2 * a.block;
   const bool zeros = a.zeros;
   float acc[NT][4] = {};
-  int slot = 0, part = 0, unit = 0;
+  int slot = 0, part = 0, unit = 0, first = 0, behind = 0;   // the unit's tiles
   uint32_t phase = 0;
   for (int i = 0; i < total; ++i) {
     if (!wait_phase<false>(&full[slot], phase, &abort)) {
       abort = 1;
       break;
     }
-    const int tile = (cta + unit * a.ctas) * H4_WARPS + warp, n = min(H4_DEPTH, kn - part * H4_DEPTH);
-    if (tile < a.tiles) {
+    if (part == 0) first = unit_at(unit), behind = unit_at(unit + 1);
+    const int tile = first + warp, n = min(H4_DEPTH, kn - part * H4_DEPTH);
+    if (tile < behind) {
       uint32_t x = slot * a.stage_bytes, blk = wp + x;
       for (int k = 0; k < n; ++k) {
         block_product<NT, SUBS>(acc, blk, zeros, [&](int q, int j) { return ld_s128(xp[j] + x + q * (8 * 2 * H4_CHUNK)); });
@@ -531,7 +536,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1) k_head4_rows(const Head4Arg
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int m = q * 8 + 2 * c + (e & 1), n1 = tile * H4_TILE + g + 8 * (e >> 1);
-        if (m < a.M && n1 < a.N)
+        if (tile < behind && m < a.M && n1 < a.N)
           result(a, slice, m, n1, acc[q][e], GLD(a.power + m), a.bias != nullptr && a.slices == 1 ? bf16_at(a.bias, n1) : 0.f);
         acc[q][e] = 0.f;
       }
@@ -720,29 +725,42 @@ int launch_head4(Head4Args &a, cudaStream_t st) {
   const auto kern = k_head4<SUBS>;
   static SmemLimit limit;
   return launch_retry(limit, (const void *)kern, smem, [&]() {
-    kern<<<(unsigned)(a.ctas * a.slices), threads_of(1), smem, st>>>(a);
+    kern<<<(unsigned)(a.ctas * a.slices), H4_FEW_THREADS, smem, st>>>(a);
     return cudaGetLastError();
   });
 }
-template <int NT, int SUBS>
-int launch_rows(Head4Args &a, cudaStream_t st) {
-  k_head4_x<<<8 * NT, 512, 0, st>>>(a, 8 * NT);
-  if (launched() != SPEC_OK) return SPEC_ERR_CUDA;
-  a.stage_bytes = (H4_DEPTH * (8 * NT * 2 * H4_CHUNK + H4_WARPS * a.block) + 127) / 128 * 128;
+template <int NT, int SUBS, int WARPS>
+int launch_warps(Head4Args &a, cudaStream_t st) {
+  // as few rounds as the warps allow, and as many warps as the rounds need
+  const int pairs = (a.tiles / 2 + a.ctas - 1) / a.ctas;
+  a.units = (2 * pairs + WARPS - 1) / WARPS;
+  a.warps = 2 * ((pairs + a.units - 1) / a.units);
+  a.stage_bytes = (H4_DEPTH * (8 * NT * 2 * H4_CHUNK + a.warps * a.block) + 127) / 128 * 128;
   a.stages = std::min(H4_MAX_STAGES, H4_SMEM / a.stage_bytes);
-  const int smem = a.stages * a.stage_bytes, units = (a.tiles + H4_WARPS - 1) / H4_WARPS;
-  a.ctas = std::max(1, std::min(units, H4_PLAN_SMS / a.slices));
-  const auto kern = k_head4_rows<NT, SUBS>;
+  const int smem = a.stages * a.stage_bytes;
+  const auto kern = k_head4_rows<NT, SUBS, WARPS>;
   static SmemLimit limit;
   cudaLaunchAttribute at[1] = {launch_early()};
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.ctas * a.slices), 1, 1);
-  cfg.blockDim = dim3(threads_of(NT), 1, 1);
+  cfg.blockDim = dim3(32 * a.warps, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return launch_retry(limit, (const void *)kern, smem, [&]() { return cudaLaunchKernelEx(&cfg, kern, a); });
+}
+template <int NT, int SUBS>
+int launch_rows(Head4Args &a, cudaStream_t st) {
+  static_assert(H4_SMEM / (H4_DEPTH * (8 * NT * 2 * H4_CHUNK + H4_MORE_WARPS * (H4_CODES + 192)) + 127) >= 2, "stages");
+  k_head4_x<<<8 * NT, 512, 0, st>>>(a, 8 * NT);
+  if (launched() != SPEC_OK) return SPEC_ERR_CUDA;
+  a.ctas = std::max(1, std::min((a.tiles + 7) / 8, H4_PLAN_SMS / a.slices));
+  // Up to 32 rows: 20 warps, with fewer registers each, where they save a round (32 rows, 4096 to
+  // 128256: 150 us, 16 warps 166; 2048 to 65000, which are two rounds for both: 57 and 55).
+  const int tiles = (a.tiles / 2 + a.ctas - 1) / a.ctas * 2;
+  if (NT == 4 && (tiles + H4_MORE_WARPS - 1) / H4_MORE_WARPS < (tiles + H4_WARPS - 1) / H4_WARPS) return launch_warps<NT, SUBS, NT == 4 ? H4_MORE_WARPS : H4_WARPS>(a, st);
+  return launch_warps<NT, SUBS, H4_WARPS>(a, st);
 }
 template <int SUBS>
 int launch_group(Head4Args &a, int nt, cudaStream_t st) {

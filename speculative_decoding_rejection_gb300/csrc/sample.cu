@@ -1000,10 +1000,6 @@ __device__ void level_count(SampleSmem &s, const Row<E, U> &row, const Level &l)
   }
 }
 
-// One division over the cluster; every CTA returns with what the leader found.
-// kind 0: totals alone, 1: the bin that `target` tokens reach, 2: the bin that a mass of
-// `target` reaches, 3: the one that the fraction top_p of the level's mass reaches,
-// 4: the one that u falls on.
 // The cluster's levels into the leader's: each CTA sums its share of the bins.
 __device__ void merge_levels(cg::cluster_group &cluster, SampleSmem &s) {
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -1030,6 +1026,10 @@ __device__ void merge_levels(cg::cluster_group &cluster, SampleSmem &s) {
   cluster.sync();
 }
 
+// One division over the cluster; every CTA returns with what the leader found.
+// kind 0: totals alone, 1: the bin that `target` tokens reach, 2: the bin that a mass of
+// `target` reaches, 3: the one that the fraction top_p of the level's mass reaches,
+// 4: the one that u falls on.
 template <class E, int U>
 __device__ Found level_find(cg::cluster_group &cluster, SampleSmem &s, const Row<E, U> &row, const Level &l, int kind,
                             unsigned long long target) {
