@@ -3,7 +3,7 @@
 //
 // The first kernel reads every gradient once, each CTA an equal run of the table's work
 // items, and leaves a partial of 64 bits per CTA; a second one of one block joins them in
-// a fixed order. HBM bounds it: 480M bf16 in 144 us, 6.7 TB/s (12 tensors of 20000: 7.9 us,
+// a fixed order. HBM bounds it: 480M bf16 in 144 us, 6.7 TB/s (12 tensors of 20000: 8 us,
 // two launches). Clipping cannot start before the norm is known, so its gradients are
 // read twice: the second kernel's CTAs take their runs backwards, so that what was read
 // last, and may still be in L2, is read first, and the first pass's loads then leave their lines

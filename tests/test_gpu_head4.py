@@ -279,3 +279,21 @@ def test_no_access_leaves_the_call(checked):
     test_unpack(7, 129, 128, 1)
     test_quantize(9, 129, 128)
     test_quantize(3, 31, 32)
+
+
+@pytest.mark.parametrize("M,K,N,group", [(32, 256, 40000, 64), (20, 130, 48641, 32), (12, 200, 50257, 128), (64, 130, 77777, 64),
+                                         (17, 384, 128256, 128), (9, 40, 39000, 32), (28, 300, 95001, 64)])
+def test_many_tiles_of_more_rows(M, K, N, group):
+    """Tiles that come to one round of the warps, to several, and to uneven ones."""
+    rng = np.random.default_rng(M + N)
+    w, ref_w = weight(rng, N, K, group, 1)
+    x, b, r = bf(rng.normal(size=(M, K))), bf(rng.normal(size=N)), bf(rng.normal(size=(M, N)))
+    guard = torch.full((M * N + 64,), 3.0, dtype=BF16, device=DEV)
+    y, ws = sv.spec_head4_forward(x, w, b, r, act=sv.SPEC_ACT_SILU, out=guard[:M * N].view(M, N))
+    assert sv.spec_get_status(ws) == sv.SPEC_OK
+    want, tol = reference(f64(x), ref_w, f64(b), f64(r), "silu", group)
+    assert (np.abs(f64(y) - want) <= tol).all() and bool((guard[M * N:] == 3).all())
+    # fewer rows of the same
+    again, _ = sv.spec_head4_forward(x[:9], w, b, r[:9].contiguous(), act=sv.SPEC_ACT_SILU)
+    want, tol = reference(f64(x[:9]), ref_w, f64(b), f64(r[:9]), "silu", group)
+    assert (np.abs(f64(again) - want) <= tol).all()
