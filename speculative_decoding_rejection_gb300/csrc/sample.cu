@@ -445,6 +445,7 @@ __device__ __forceinline__ void block_sums(SampleSmem &s, float &x, uint32_t &n,
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
   n = __reduce_add_sync(~0u, n);
   k = __reduce_add_sync(~0u, k);
+  __syncthreads();   // the warps' sums are read: what comes next may write them
 }
 
 // By one warp: the entry in which the counts (by_n) or masses before and in it first reach
