@@ -11,9 +11,9 @@
 // 381 us, 6.3 TB/s). A norm alone marks them: 160 against 168 us between flushes of L2.
 //
 // Squares are summed in f32 over 16 bytes x 4 of a thread, these sums in two f32 words. Where
-// such a sum is not between 1e-24 and 3e38 (values that square to nothing or to infinity) its
-// values are squared again in 64 bits, unless they are all zero: FP64 is too slow here for
-// all of them (two multiply-adds per SM and cycle).
+// such a sum is not over 1e-24, or takes the thread's to 3e38 (values that square to nothing, to
+// infinity or to more than f32 adds up), its values are squared again in 64 bits, unless they are all
+// zero: FP64 is too slow here for all of them (two multiply-adds per SM and cycle).
 #include "adamw.cuh"
 
 #include <algorithm>
@@ -88,8 +88,9 @@ __device__ __forceinline__ void add_values(Acc &a, const float (&x)[N], bool inf
 #pragma unroll
   for (int i = 0; i < N; ++i) s[i % 4] = fmaf(x[i], x[i], s[i % 4]);
   const float sum = (s[0] + s[1]) + (s[2] + s[3]);
-  if (sum > 1e-24f && sum < 3e38f) {
-    const float t = a.hi + sum, b = t - a.hi;
+  const float t = a.hi + sum;
+  if (sum > 1e-24f && t < 3e38f) {
+    const float b = t - a.hi;
     a.lo += (a.hi - (t - b)) + (sum - b);
     a.hi = t;
   } else {
