@@ -284,9 +284,10 @@ int spec_adamw_step(const void *table, int64_t n_items, int state_bits,
  *
  * out[0] = norm, out[1] = factor (f32, device; out + 1 is what spec_adamw_step
  * takes as grad_scale). Squares neither overflow nor vanish on the way: a norm
- * that f32 can hold is found. A gradient that is NaN makes norm and factor NaN; an
- * infinite one makes the norm infinite and the factor 0, so that a step by it has
- * NaN for that weight. A table without elements has norm 0.
+ * that f32 can hold is found, also where the gradients' own norm is none; one that it
+ * cannot hold is infinite, with factor 0. A gradient that is NaN makes norm and factor
+ * NaN; an infinite one makes the norm infinite and the factor 0, so that a step by it
+ * has NaN for that weight. A table without elements has norm 0.
  *
  * spec_clip_grads also multiplies every gradient by the factor, in place, rounded
  * once to its type; gradients whose factor is 1 keep their bits. A table that does

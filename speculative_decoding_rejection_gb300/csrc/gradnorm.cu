@@ -190,17 +190,26 @@ __global__ void __launch_bounds__(GN_THREADS, ctas_per_sm(KEEP)) k_grad_norm(con
   if (threadIdx.x == 0) a.part[blockIdx.x] = sum;
 }
 
-// The root of a sum of squares in two words of f32: of a mantissa over an even power, the
-// first word corrected by what its square leaves. (A root and a quotient of 64 bits take microseconds.)
-__device__ __forceinline__ void root(double x, float &hi, float &lo) {
-  hi = (float)x, lo = 0.f;
-  if (!(x > 0.0 && x <= 1.7976931348623157e308)) return;   // zero, infinity, NaN
+// s times the root of a sum of squares x, s >= 0, in two words of f32: the root of a mantissa over an
+// even power, its first word corrected by what its square leaves, times s's mantissa; the power
+// is applied last, so that a root that f32 does not hold is no loss where the norm is held. (A root
+// and a quotient of 64 bits take microseconds.)
+__device__ __forceinline__ void scaled_root(double x, float s, float &hi, float &lo) {
+  const bool ordinary = x > 0.0 && x <= 1.7976931348623157e308;
+  if (!ordinary || !(s > 0.f && s <= 3.402823466e38f)) {   // zeros, infinities, NaN
+    hi = (ordinary ? 1.f : (float)x) * s, lo = 0.f;
+    return;
+  }
   const long long bits = __double_as_longlong(x);
   const int e = (int)(bits >> 52) - 1023, even = e & ~1;   // (a sum of squares that are no f32 zero is normal)
   const double m = __longlong_as_double((bits & 0xfffffffffffffll) | (long long)(1023 + e - even) << 52);
   const float m0 = (float)m, r = __fsqrt_rn(m0);
-  hi = ldexpf(r, even / 2);
-  lo = ldexpf((fmaf(-r, r, m0) + (float)(m - (double)m0)) * 0.5f / r, even / 2);
+  const float left = (fmaf(-r, r, m0) + (float)(m - (double)m0)) * 0.5f / r;
+  int power;
+  const float f = frexpf(s, &power), p = f * r;
+  power += even / 2;
+  hi = ldexpf(p, power);
+  lo = ldexpf(fmaf(f, r, -p) + f * left, power);
 }
 
 // The norm and the factor, in thread 0.
@@ -213,10 +222,9 @@ __device__ __forceinline__ void join(const NormArgs &a, float *norm, float *fact
   x = block_join(x, a.inf);
   if (threadIdx.x != 0) return;
   const float s = a.grad_scale ? *a.grad_scale : 1.f;
-  float hi, lo = 0.f;
-  if (a.inf) hi = (float)x;
-  else root(x, hi, lo);
-  const float n = fabsf(s) * hi, rest = fmaf(fabsf(s), hi, -n) + fabsf(s) * lo;
+  float n, rest;
+  if (a.inf) n = fabsf(s) * (float)x, rest = fmaf(fabsf(s), (float)x, -n);
+  else scaled_root(x, fabsf(s), n, rest);
   *norm = n;
   float d = n + 1e-6f, f;
   if (n <= 3.402823466e38f) {

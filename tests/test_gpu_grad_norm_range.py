@@ -62,3 +62,51 @@ def test_a_large_gradient_among_ordinary_ones():
     for at, v in ((0, 1.5e19), (1, -1.2e19), (2_999_999, 3e38)):
         g[at] = v
         check_norm_and_clip([g.clone()])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n,value,scale", [
+    (5000, 3e38, 1e-3), (5000, 3e38, 1e-30), (4, 2e38, 2.0 ** -16), (4, 2e38, -2.0 ** -16), (3, 1e38, 1e-38),
+    (5000, 1e-38, 2.0 ** 100), (3, 1e-30, 1e-5), (3000, 7e-39, 3e38), (4097, 1.0, 0.37), (2, 0.6, 1e-44)])
+def test_a_scale_that_brings_the_norm_into_range(n, value, scale, dtype):
+    """The norm of the scaled gradients is held where the norm of the gradients is not, or has lost digits."""
+    g = torch.full((n,), value, dtype=dtype, device=DEV)
+    g[::2] *= -0.75
+    s = torch.tensor([scale], device=DEV)
+    norm = abs(float(s)) * norm_of([g])
+    tiny = 2.0 ** -148      # two roundings of a norm that is no normal number
+    for inf in (False, True):
+        want = abs(float(s)) * float(g.double().abs().max()) if inf else norm
+        if want > 3.4e38:
+            continue
+        out, ws = sv.spec_grad_norm(table_of([g]), max_norm=0.5 * want + 2e-38, inf=inf, grad_scale=s)
+        assert sv.spec_get_status(ws) == sv.SPEC_OK
+        factor = float(s) * min(1.0, (0.5 * want + 2e-38) / (want + 1e-6))
+        assert abs(float(out[0]) - want) <= TOL * want + tiny, (float(out[0]), want)
+        assert abs(float(out[1]) - factor) <= 2 * TOL * abs(factor) + tiny, (float(out[1]), factor)
+
+
+def test_denormal_gradients_under_a_scale():
+    g = torch.full((900,), 1e-42, device=DEV)
+    s = torch.tensor([2.0 ** 16], device=DEV)
+    norm = 2.0 ** 16 * norm_of([g])
+    out, _ = sv.spec_grad_norm(table_of([g]), grad_scale=s)
+    assert abs(float(out[0]) - norm) <= TOL * norm and float(out[1]) == 2.0 ** 16
+    keep = g.clone()
+    out, _ = sv.spec_clip_grads(table_of([g]), max_norm=1.0, grad_scale=s)
+    assert float(out[1]) == 2.0 ** 16 and torch.equal(g, keep * 2.0 ** 16)
+
+
+def test_scales_that_are_no_ordinary_numbers():
+    g = torch.full((50,), 2.0, device=DEV)
+    big = torch.full((50,), float("inf"), device=DEV)
+    for x, s, want in ((g, 0.0, 0.0), (g, -0.0, 0.0), (g, math.inf, math.inf), (g, math.nan, math.nan),
+                       (g * 0, math.inf, math.nan), (g * 0, 0.0, 0.0), (big, 0.0, math.nan), (big, 1e-30, math.inf),
+                       (g * 1e-38, math.inf, math.inf), (g, -3.0, 6 * math.sqrt(50))):
+        for inf in (False, True):
+            if inf and math.isfinite(want) and want > 0:
+                want = 6.0
+            out, ws = sv.spec_grad_norm(table_of([x]), inf=inf, grad_scale=torch.tensor([s], device=DEV))
+            assert sv.spec_get_status(ws) == sv.SPEC_OK
+            got = float(out[0])
+            assert (math.isnan(got) and math.isnan(want)) or got == want or abs(got - want) <= TOL * want, (s, inf, got)
