@@ -1620,6 +1620,34 @@ __device__ void value_pass(SampleSmem &s, const Row<E, U> &row, bool weights) {
   }
 }
 
+// The row's mass in f32, from L2, where its histogram has not told it. (By the largest it could be, V,
+// units would be too coarse for the tail of a row that one token leads.)
+template <class E, int U>
+__device__ __noinline__ float rough_mass(cg::cluster_group &cluster, SampleSmem &s, const Row<E, U> &row, float m) {
+  const float ch = s.law.ch;
+  float sum[4] = {};
+  for (int c = threadIdx.x >> 5; c < row.nc; c += SA_WARPS) {
+    if (!((m - s.cmax[c]) * ch < 64.f)) continue;
+    row.groups(c, [&](int, const uint4 *v) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        Vec<E> x;
+        x.v = v[u];
+#pragma unroll
+        for (int i = 0; i < Val<E>::PER; ++i) sum[i & 3] += ex2((Val<E>::f32(x.e[i]) - m) * ch);
+      }
+    });
+  }
+  float x = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  uint32_t none = 0, none2 = 0;
+  block_sums(s, x, none, none2);
+  if (threadIdx.x == 0) s.cta_sum = x;
+  cluster.sync();
+  float mass = 0.f;
+  for (int q = 0; q < (int)cluster.num_blocks(); ++q) mass += *cluster.map_shared_rank(&s.cta_sum, q);
+  return mass;
+}
+
 // The ids of a value's equal number `at` and of the last one kept.
 template <class E, int U>
 __device__ void locate(cg::cluster_group &cluster, SampleSmem &s, const Row<E, U> &row, bool find_tok, bool find_cut) {
@@ -1824,7 +1852,6 @@ __global__ void __launch_bounds__(SA_THREADS, SA_CTAS_PER_SM) k_sample(const Sam
       if (!BF && !s.law.greedy)
         rough += *cluster.map_shared_rank(&s.cta_sum, q) * ex2((*cluster.map_shared_rank(&s.cta_max, q) - m) * s.law.ch);
     }
-    if (BF) rough = (float)a.V;   // where a bf16 row goes by divisions
     bad = !(m > -INFINITY && m < INFINITY);
     if (!bad && s.law.greedy) {   // more equals of the largest than a list holds
       Verdict v{};
@@ -1861,6 +1888,7 @@ __global__ void __launch_bounds__(SA_THREADS, SA_CTAS_PER_SM) k_sample(const Sam
         if (t == 0) s.verdict = v;
       }
       if (slow) {
+        if constexpr (BF) rough = rough_mass(cluster, s, row, m);
         decide_row(cluster, s, row, m, rough);
         if (s.verdict.slow) decide_divisions(cluster, s, row, m, rough);
       }

@@ -1,5 +1,8 @@
 """spec_sample on the GPU where its sums decide: rows of values that go by the histogram, the same
 results in every row and every run, and borders far down in a row's tail."""
+import math
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -9,6 +12,7 @@ import speculative_decoding_rejection_gb300 as sv
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 BF16, F32 = torch.bfloat16, torch.float32
+U24 = 1 - 2.0 ** -24
 
 
 @pytest.mark.parametrize("filters", ["none", "top_p", "top_k"])
@@ -33,3 +37,112 @@ def test_equal_rows_have_equal_results(R, V, filters):
         first = first or [t[:1].clone() for t in got]
         for t, f in zip(got, first):
             assert torch.equal(t, f.expand(R))
+
+
+def weights_of(z, T):
+    """The values of a row in falling order, how many tokens each has, and the weight of one in units
+    of 2^-120 (whole numbers, so that sums of millions lose nothing)."""
+    values, counts = np.unique(z[z > -np.inf], return_counts=True)
+    values, counts = values[::-1], counts[::-1]
+    return values, counts, [int(math.exp((v - values[0]) / T) * 2.0 ** 120) for v in values]
+
+
+def mass_of(counts, weights, n):
+    """The weight of the first n tokens."""
+    total = 0
+    for c, w in zip(counts, weights):
+        total += min(n, int(c)) * w
+        n -= min(n, int(c))
+    return total
+
+
+def check_borders(z, T, top_k, top_p, u, token, prob, kept, filtered, bound):
+    """Each border where exact weights put it, but for `bound` of the mass."""
+    values, counts, weights = weights_of(z, T)
+    all_n = int(counts.sum()) if top_k <= 0 else min(int(counts.sum()), top_k)
+    mass = mass_of(counts, weights, all_n)
+    e = Fraction(bound)
+    p = Fraction(top_p)
+    if top_p < 1:
+        assert 1 <= kept <= all_n
+        assert mass_of(counts, weights, kept) >= (p - e) * mass, (kept, "too few")
+        assert mass_of(counts, weights, kept - 1) < (p + e) * mass, (kept, "too many")
+    else:
+        assert kept == all_n
+    law = mass_of(counts, weights, kept)
+    at = z[token]
+    rank = int((z > at).sum() + (z[:token] == at).sum())
+    assert rank < kept
+    before, upto = mass_of(counts, weights, rank), mass_of(counts, weights, rank + 1)
+    assert before <= (Fraction(u) + e) * law and upto > (Fraction(u) - e) * law, (rank, kept)
+    assert abs(prob - (upto - before) / law) <= 2.0 ** -22 * prob
+    if filtered is not None:
+        order = np.lexsort((np.arange(len(z)), -z))[:kept]
+        want = np.full(len(z), -np.inf)
+        want[order] = z[order]
+        assert np.array_equal(filtered, want)
+
+
+def peaked(rng, V, kind):
+    """A token that leads, and a tail of small weights, with values that have no bin of their own."""
+    z = np.full(V, -27.75)
+    if kind == "tiny":                     # one logit of 1e-7, the largest
+        z[rng.integers(V)] = 1e-7
+    elif kind == "tiny tail":
+        z = np.where(rng.random(V) < 0.5, 1e-7, 0.0)
+        z[rng.integers(V)] = 27.0
+    elif kind == "large":                  # from 2048 on
+        z[:] = 2976.0
+        z[rng.integers(V)] = 3008.0
+    elif kind == "far below":
+        z[:] = -2128.0
+        z[rng.integers(V)] = -2096.0
+    elif kind == "spread":
+        z = np.round(rng.normal(size=V) * 8) / 8 - 28
+        z[rng.integers(0, V, 3)] = [1e-7, 2.0, 3.0]
+    return z
+
+
+LAWS = [(0, U24, 0.5), (0, 1 - 2.0 ** -21, U24), (0, 1.0, U24), (0, 1.0, 1 - 2.0 ** -20), (30000, 1.0, U24),
+        (30000, U24, 1 - 2.0 ** -22), (0, 0.9, 0.3)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kind", ["tiny", "tiny tail", "large", "far below", "spread"])
+@pytest.mark.parametrize("R,V", [(7, 50257), (7, 201088), (322, 50257)])
+def test_borders_in_the_tail_of_a_peaked_row(R, V, kind, dtype):
+    rng = np.random.default_rng(V)
+    T = 1.2 if kind in ("large", "far below") else 1.0
+    z = peaked(rng, V, kind)
+    rows = torch.tensor(z).to(dtype).to(DEV)
+    zz = rows.double().cpu().numpy()
+    laws = [LAWS[r % len(LAWS)] for r in range(R)]
+    top_k, top_p, u = (np.array([law[i] for law in laws]) for i in range(3))
+    tokens, prob, kept, filtered, ws = sv.spec_sample(
+        rows.expand(R, V).contiguous(), torch.tensor(u, dtype=F32, device=DEV),
+        temperature=torch.full((R,), T, device=DEV), top_k=torch.tensor(top_k, dtype=torch.int32, device=DEV),
+        top_p=torch.tensor(top_p, dtype=F32, device=DEV), want_kept=True, want_filtered=True)
+    assert sv.spec_get_status(ws) == sv.SPEC_OK
+    for r in range(len(LAWS)):
+        k, p, x = laws[r]
+        check_borders(zz, float(np.float32(T)), k, float(np.float32(p)), float(np.float32(x)), int(tokens[r]), float(prob[r]),
+                      int(kept[r]), filtered[r].double().cpu().numpy(), 2.0 ** -37)
+    for r in range(len(LAWS), R):          # the same law, the same result
+        for t in (tokens, prob, kept, filtered):
+            assert torch.equal(t[r], t[r % len(LAWS)])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_borders_in_the_tail_of_the_longest_row(dtype):
+    V = 1 << 24
+    z = torch.full((3, V), -26.0, dtype=dtype, device=DEV)
+    z[:, 777] = 1e-7
+    u = np.array([1 - 2.0 ** -14, U24, 0.9999])
+    top_p = np.array([1.0, 1 - 2.0 ** -15, 1.0])
+    tokens, prob, kept, _, ws = sv.spec_sample(
+        z, torch.tensor(u, dtype=F32, device=DEV), top_p=torch.tensor(top_p, dtype=F32, device=DEV), want_kept=True)
+    assert sv.spec_get_status(ws) == sv.SPEC_OK
+    zz = z[0].double().cpu().numpy()
+    for r in range(3):
+        check_borders(zz, 1.0, 0, float(np.float32(top_p[r])), float(np.float32(u[r])), int(tokens[r]), float(prob[r]),
+                      int(kept[r]), None, 2.0 ** -36)
