@@ -233,6 +233,7 @@ struct SampleSmem {
   uint32_t warp_n[SA_WARPS], warp_k[SA_WARPS];
   float warp_f[SA_WARPS], warp_low[SA_WARPS];
   float cta_max, cta_sum;          // this CTA's slice: the largest logit, the f32 sum of weights by it
+  float cta_rough;                 // and by the row's
   uint32_t cta_tok, cta_cut;       // its matches
   uint32_t tok_end, cut_end;       // and with those before it
   uint32_t run;                    // key of the largest logit so far
@@ -499,6 +500,18 @@ __device__ __forceinline__ int unit_of(float z) {
   return 62 - e;
 }
 
+// A list's order and what it holds besides the law go by when its tokens were found, so a row may be
+// decided by its list in one call and, the list full, otherwise in the next. The unit of its weights
+// goes by what is the same in both: min-p's tokens, how many and their rough mass in whole 2^-20ths,
+// or `rough` for more than a list holds.
+__device__ __forceinline__ uint32_t weight20(float gap, float ch) { return __float2uint_ru(ex2(gap * ch) * 1048576.f); }
+__device__ __forceinline__ int unit_of_law(const Law &law, uint32_t in, uint32_t mass20, float rough) {
+  static_assert(SA_FEW <= 256 && SA_LIST < 4096, "units");
+  const float k = law.top_k > 0 ? (float)law.top_k : INFINITY;   // weights are 1 at most
+  if ((float)in <= (float)SA_FEW || k <= (float)SA_FEW) return 62 - 9;
+  return unit_of(fminf(in <= (uint32_t)SA_LIST ? (float)mass20 * 0x1p-20f : rough, k));
+}
+
 // ------------------------------------------------------------- bf16: by values
 __device__ __forceinline__ float bin_value(int bin) {
   if (bin >= SA_BINS) return bin == SA_ZERO ? 0.f : -2048.f;
@@ -609,11 +622,13 @@ __device__ void decide_values(SampleSmem &s, float m) {
     entries += s.warp_k[w];
   }
   float rough = 0.f;
+  uint32_t in = 0;   // how many tokens min-p leaves
   if (entries <= SA_ENTRIES) {
     auto take = [&](int j, uint32_t who) {
       const int bin = bin_at((warp * SA_ROWS + j) * 32 + lane);
       if (who >> lane & 1) {
         s.bins[at + __popc(who & ((1u << lane) - 1))] = (uint16_t)bin;
+        in += s.hist[bin];
         rough += (float)s.hist[bin] * ex2((bin_value(bin) - m) * ch);
       }
       at += __popc(who);
@@ -623,18 +638,27 @@ __device__ void decide_values(SampleSmem &s, float m) {
       take(j, __shfl_sync(~0u, mine, j));
     }
   }
-  uint32_t none = 0;
-  block_sums(s, rough, n, none);
+  block_sums(s, rough, n, in);
   const uint32_t total = n;
   // values without a bin of their own: what has no weight needs none, unless the
-  // last token kept is among them
+  // last token kept, or min-p's border, is among them
   const uint32_t low = s.hist[SA_LAST];
   const bool light = (m + 2048.f) * ch > 63.f;
   Verdict v{};
-  v.slow = s.odd != 0 || entries > SA_ENTRIES || entries == 0 || (low != 0 && !light);
+  v.slow = s.odd != 0 || entries > SA_ENTRIES || entries == 0 ||
+           (low != 0 && (!light || (least > -INFINITY && least <= -2048.f)));
   if (v.slow) {
     if (t == 0) s.verdict = v;
     return;
+  }
+  int S = unit_of(rough);
+  if (s.law.list) {
+    uint32_t mass20 = 0, none = 0;
+    for (int i = t; in <= (uint32_t)SA_LIST && i < (int)entries; i += SA_THREADS)
+      mass20 += s.hist[s.bins[i]] * weight20(bin_value(s.bins[i]) - m, ch);
+    float zero = 0.f;
+    block_sums(s, zero, mass20, none);
+    S = unit_of_law(s.law, in, mass20, rough);
   }
   // top-k: the entry it ends in, and what it keeps of that
   int part = -1;
@@ -654,7 +678,7 @@ __device__ void decide_values(SampleSmem &s, float m) {
     __syncthreads();
     if (s.part_bin >= 0) part = s.part_bin, part_n = s.part_n, entries = part + 1;
   }
-  const Drawn d = decide(s, m, (int)entries, unit_of(rough), [&](int i, float &z) {
+  const Drawn d = decide(s, m, (int)entries, S, [&](int i, float &z) {
     const int bin = s.bins[i];
     z = bin_value(bin);
     return i == part ? part_n : s.hist[bin];
@@ -834,7 +858,7 @@ __device__ void decide_few(SampleSmem &s, float m, int n, unsigned long long fro
     }
   const int kept = law.top_k > 0 ? min(many, law.top_k) : many;
   constexpr int S = 62 - 9;   // at most 256 weights
-  static_assert(SA_FEW <= 256 && SA_FEW <= SA_NEAR, "units");
+  static_assert(SA_FEW <= 256 && SA_FEW <= SA_NEAR, "unit_of_law's");
   const float z = list_value(key);
   const bool in = t < many && rank < kept;
   const unsigned long long w = in ? weight_of(s.pow2, m, law.ch, law.cl, S, z) : 0;
@@ -870,11 +894,11 @@ __device__ void decide_few(SampleSmem &s, float m, int n, unsigned long long fro
 __device__ void decide_list(SampleSmem &s, float m, int n) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const Law &law = s.law;
-  // the key of min-p's border; the least value from there on, and a rough sum of the weights
+  // the key of min-p's border; the tokens from there on, the least value and a rough sum of the weights
   const float least = law.greedy ? m : fmaxf(__double2float_ru((double)m + law.log_min), -3.402823466e38f);
   unsigned long long from = (unsigned long long)key_of(least) << 32, first = 0;
-  float low = m, rough = 0.f;
-  uint32_t in = 0;
+  float low = m;
+  uint32_t in = 0, mass20 = 0;
   for (int i = t; i < n; i += SA_THREADS) {
     const unsigned long long key = s.list[i];
     if (key < from) continue;
@@ -882,22 +906,22 @@ __device__ void decide_list(SampleSmem &s, float m, int n) {
     ++in;
     low = fminf(low, z);
     first = max(first, key);
-    rough += ex2((z - m) * law.ch);
+    mass20 += weight20(z - m, law.ch);
   }
   in = __reduce_add_sync(~0u, in);
+  mass20 = __reduce_add_sync(~0u, mass20);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     low = fminf(low, __shfl_xor_sync(~0u, low, o));
-    rough += __shfl_xor_sync(~0u, rough, o);
     if (law.greedy) first = max(first, __shfl_xor_sync(~0u, first, o));
   }
-  if (lane == 0) s.warp_low[warp] = low, s.warp_f[warp] = rough, s.warp_n[warp] = in, s.warp_mass[warp] = first;
+  if (lane == 0) s.warp_low[warp] = low, s.warp_k[warp] = mass20, s.warp_n[warp] = in, s.warp_mass[warp] = first;
   __syncthreads();
-  in = 0, rough = 0.f;
+  in = 0, mass20 = 0;
 #pragma unroll
   for (int w = 0; w < SA_WARPS; ++w) {
     low = fminf(low, s.warp_low[w]);
-    rough += s.warp_f[w];
+    mass20 += s.warp_k[w];
     in += s.warp_n[w];
     first = max(first, s.warp_mass[w]);
   }
@@ -915,7 +939,7 @@ __device__ void decide_list(SampleSmem &s, float m, int n) {
     return;
   }
   const Intervals<SA_LIST_LEVEL> iv{m, m > low ? (float)SA_LIST_LEVEL / (m - low) : 0.f, -1};
-  const int S = unit_of(rough);
+  const int S = unit_of_law(law, in, mass20, 0.f);
   if (law.top_k > 0 && law.top_k <= (int)in) {
     count_list(s, n, iv, from, false, S);
     if (find_key(s, n, iv, from, S, (unsigned long long)law.top_k, true)) {
@@ -1115,7 +1139,7 @@ __device__ Found descend(cg::cluster_group &cluster, SampleSmem &s, const Row<E,
 
 template <class E, int U>
 __device__ __noinline__ void decide_divisions(cg::cluster_group &cluster, SampleSmem &s, const Row<E, U> &row, float m,
-                                              float rough) {
+                                              int S) {
   const uint32_t top = key_of(m);
   const int top_k = s.law.top_k;
   Level l{};
@@ -1123,7 +1147,7 @@ __device__ __noinline__ void decide_divisions(cg::cluster_group &cluster, Sample
   l.whole = 1;
   const float least = __double2float_ru((double)m + s.law.log_min);
   l.last = top - key_of(fmaxf(least, -3.402823466e38f));
-  l.S = unit_of(top_k > 0 ? fminf(rough, (float)top_k) : rough);
+  l.S = S;
   Verdict v{};
   v.cut = least, v.cut_id = INT_MAX, v.tok_id = -1;
   v.kept = -1;
@@ -1262,7 +1286,7 @@ __device__ Near find_row(cg::cluster_group &cluster, SampleSmem &s, const Row<E,
 
 // The verdict of a row of any values, by every CTA; slow where an interval holds too many.
 template <class E, int U>
-__device__ __noinline__ void decide_row(cg::cluster_group &cluster, SampleSmem &s, const Row<E, U> &row, float m, float rough) {
+__device__ __noinline__ void decide_row(cg::cluster_group &cluster, SampleSmem &s, const Row<E, U> &row, float m, int S) {
   const int top_k = s.law.top_k;
   const float least = fmaxf(__double2float_ru((double)m + s.law.log_min), -3.402823466e38f);
   unsigned long long from = (unsigned long long)key_of(least) << 32;
@@ -1282,7 +1306,6 @@ __device__ __noinline__ void decide_row(cg::cluster_group &cluster, SampleSmem &
     r.before += n.before, r.rank += n.rank, r.total = n.total, r.total_n = n.total_n;
     return r;
   };
-  const int S = unit_of(top_k > 0 ? fminf(rough, (float)top_k) : rough);
   Verdict v{};
   v.tok_id = -1, v.kept = -1;
   if (top_k > 0) {
@@ -1620,32 +1643,57 @@ __device__ void value_pass(SampleSmem &s, const Row<E, U> &row, bool weights) {
   }
 }
 
-// The row's mass in f32, from L2, where its histogram has not told it. (By the largest it could be, V,
-// units would be too coarse for the tail of a row that one token leads.)
+// The unit of a row's weights where its passes have not told it, from L2: of a bf16 row, or of one whose
+// list was full. (By the largest mass there could be, V, units would be too coarse for the tail of a row
+// that one token leads.) rough: an f32 row's mass. Where that serves, as its law is more than a list
+// holds, the pass ends early (250 x 128256, min-p 1e-5: 214 us, with a whole pass 235).
 template <class E, int U>
-__device__ __noinline__ float rough_mass(cg::cluster_group &cluster, SampleSmem &s, const Row<E, U> &row, float m) {
+__device__ __noinline__ int unit_of_row(cg::cluster_group &cluster, SampleSmem &s, const Row<E, U> &row, float m, float rough) {
+  constexpr bool BF = sizeof(E) == 2;
   const float ch = s.law.ch;
+  const float least = fmaxf(__double2float_ru((double)m + s.law.log_min), -3.402823466e38f);
   float sum[4] = {};
+  uint32_t mass20 = 0;
+  if (threadIdx.x == 0) s.n_near = 0;   // min-p's tokens
+  __syncthreads();
   for (int c = threadIdx.x >> 5; c < row.nc; c += SA_WARPS) {
-    if (!((m - s.cmax[c]) * ch < 64.f)) continue;
+    if (!(s.cmax[c] >= least)) continue;
+    if (!BF && __any_sync(~0u, *(volatile int *)&s.n_near > SA_LIST)) break;
+    uint32_t in = 0;
     row.groups(c, [&](int, const uint4 *v) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         Vec<E> x;
         x.v = v[u];
 #pragma unroll
-        for (int i = 0; i < Val<E>::PER; ++i) sum[i & 3] += ex2((Val<E>::f32(x.e[i]) - m) * ch);
+        for (int i = 0; i < Val<E>::PER; ++i) {
+          const float z = Val<E>::f32(x.e[i]);
+          if (!(z >= least)) continue;
+          const float w = ex2((z - m) * ch);
+          ++in;
+          mass20 += __float2uint_ru(w * 1048576.f);
+          if (BF) sum[i & 3] += w;
+        }
       }
     });
+    in = __reduce_add_sync(~0u, in);
+    if ((threadIdx.x & 31) == 0) atomicAdd(&s.n_near, (int)in);
   }
   float x = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-  uint32_t none = 0, none2 = 0;
-  block_sums(s, x, none, none2);
-  if (threadIdx.x == 0) s.cta_sum = x;
+  uint32_t none = 0;
+  block_sums(s, x, mass20, none);
+  if (threadIdx.x == 0) s.cta_rough = x, s.cta_tok = (uint32_t)s.n_near, s.cta_cut = mass20;
   cluster.sync();
-  float mass = 0.f;
-  for (int q = 0; q < (int)cluster.num_blocks(); ++q) mass += *cluster.map_shared_rank(&s.cta_sum, q);
-  return mass;
+  uint32_t in = 0;
+  x = 0.f, mass20 = 0;
+  for (int q = 0; q < (int)cluster.num_blocks(); ++q) {
+    x += *cluster.map_shared_rank(&s.cta_rough, q);
+    in += *cluster.map_shared_rank(&s.cta_tok, q);
+    mass20 += *cluster.map_shared_rank(&s.cta_cut, q);
+  }
+  if (BF) rough = x;
+  if (s.law.list) return unit_of_law(s.law, in, mass20, rough);
+  return unit_of(s.law.top_k > 0 ? fminf(rough, (float)s.law.top_k) : rough);
 }
 
 // The ids of a value's equal number `at` and of the last one kept.
@@ -1888,9 +1936,10 @@ __global__ void __launch_bounds__(SA_THREADS, SA_CTAS_PER_SM) k_sample(const Sam
         if (t == 0) s.verdict = v;
       }
       if (slow) {
-        if constexpr (BF) rough = rough_mass(cluster, s, row, m);
-        decide_row(cluster, s, row, m, rough);
-        if (s.verdict.slow) decide_divisions(cluster, s, row, m, rough);
+        const int S = BF || s.law.list ? unit_of_row(cluster, s, row, m, rough)
+                                       : unit_of(s.law.top_k > 0 ? fminf(rough, (float)s.law.top_k) : rough);
+        decide_row(cluster, s, row, m, S);
+        if (s.verdict.slow) decide_divisions(cluster, s, row, m, S);
       }
     }
     __syncthreads();

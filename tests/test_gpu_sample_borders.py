@@ -146,3 +146,60 @@ def test_borders_in_the_tail_of_the_longest_row(dtype):
     for r in range(3):
         check_borders(zz, 1.0, 0, float(np.float32(top_p[r])), float(np.float32(u[r])), int(tokens[r]), float(prob[r]),
                       int(kept[r]), None, 2.0 ** -36)
+
+
+# The value of half of a law's 256 tokens, the temperature, and a u whose part of the mass is so near to
+# the other half's that the unit of the weights decides on which side of the border it falls.
+NEAR = [(0.625, "0x1.a4c48p+0", "0x1.301846p-1"), (0.75, "0x1.5b43d6p+0", "0x1.450554p-1"),
+        (2.625, "0x1.d608d8p-1", "0x1.e43ffep-1"), (2.75, "0x1.73a8dp+0", "0x1.bd0c4ep-1"),
+        (2.875, "0x1.99f698p+0", "0x1.b71386p-1")]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("gap,T,u", NEAR)
+@pytest.mark.parametrize("filters", ["min_p", "min_p and top_k"])
+def test_results_do_not_go_by_the_way_a_row_is_decided(gap, T, u, filters, dtype):
+    """The tokens of a law all over the row, so that its list holds them and little else, and behind the
+    rest of the row, whose tokens fill the list before the largest logit is seen."""
+    R, V, half = 400, 60000, 128
+    T, u = float.fromhex(T), float.fromhex(u)
+    z = torch.full((2, V), -gap - 0.125)
+    all_over = torch.arange(2 * half) * (V // (2 * half))
+    for row, at in ((0, all_over), (1, torch.arange(V - 2 * half, V))):
+        z[row, at[::2]] = 0.0
+        z[row, at[1::2]] = -gap
+    z = z.to(dtype).to(DEV).repeat(R // 2, 1)
+    law = dict(temperature=torch.full((R,), T, device=DEV),
+               min_p=torch.full((R,), math.exp(-(gap + 0.0625) / T), device=DEV))
+    if filters != "min_p":
+        law["top_k"] = torch.full((R,), 2 * half, dtype=torch.int32, device=DEV)
+    tokens, prob, kept, _, ws = sv.spec_sample(z, torch.full((R,), u, device=DEV), want_kept=True, **law)
+    assert sv.spec_get_status(ws) == sv.SPEC_OK
+    assert bool((kept == 2 * half).all())
+    drawn = z.gather(1, tokens.long()[:, None])[:, 0]
+    assert bool((drawn == drawn[0]).all()) and bool((prob == prob[0]).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("many", [100, 256, 257, 1000, 2540, 2560, 2561, 4000])
+def test_lists_that_are_nearly_full(many, dtype):
+    """Laws of as many tokens as a list may hold, and a few more or less, in rows of every order."""
+    rng = np.random.default_rng(many)
+    V, B = 12000, 40
+    base = np.concatenate([np.round(rng.uniform(-4, 0, many) * 64) / 64, np.full(V - many, -9.0)])
+    base[0] = 0.0
+    z = torch.tensor(np.stack([rng.permutation(base) for _ in range(B - 1)] + [np.sort(base)])).to(dtype).to(DEV)
+    z = z.repeat(10, 1)
+    R = z.shape[0]
+    law = dict(temperature=np.float32(0.9), min_p=np.float32(0.003), top_p=np.float32(0.97))
+    u = np.float32(0.71)
+    t = {k: torch.full((R,), float(v), device=DEV) for k, v in law.items()}
+    tokens, prob, kept, _, ws = sv.spec_sample(z, torch.full((R,), float(u), device=DEV), want_kept=True, **t)
+    assert sv.spec_get_status(ws) == sv.SPEC_OK
+    drawn = z.gather(1, tokens.long()[:, None])[:, 0]
+    assert bool((drawn == drawn[0]).all()) and bool((prob == prob[0]).all()) and bool((kept == kept[0]).all())
+    inside = z[0].double().cpu().numpy()
+    inside[inside < -5] = -np.inf
+    assert float(law["temperature"]) * math.log(float(law["min_p"])) > -9
+    check_borders(inside, float(law["temperature"]), 0, float(law["top_p"]), float(u), int(tokens[0]), float(prob[0]),
+                  int(kept[0]), None, 2.0 ** -37)
