@@ -392,6 +392,7 @@ int spec_head4_unpack(const void *packed, int has_zeros, int N, int K, int group
  * is rounded once. A row of x takes part in fp16, times a power of two that brings its largest value
  * to 2^15: that is exact for what is down to 2^-29 of it, and further below
  * within 2^-40 of it. A row of x with an infinity or NaN has results that are not finite.
+ * (Sums of such rows stay in f32 where K times the largest weight is under 2^112.)
  *
  *   x         [M, K] bf16, 0 <= M <= SPEC_HEAD4_MAX_ROWS; bias [N] or NULL;
  *             residual [M, N] or NULL. 1 <= N, K <= 2^24. x is 16-byte aligned, the
@@ -444,7 +445,9 @@ size_t spec_sample_workspace(int R, int V);
  * The filtered rows, with the same temperature, are logits of the law that was
  * sampled, for spec_verify_linear as draft or as target. Weights are whole numbers of
  * a small unit, whose sums are exact: results do not go by the order of sums, and no
- * border is further than 2^-38 of the mass from where exact weights put it.
+ * border is further than 2^-38 of the mass (2^-36 for V over 2^22) from where exact
+ * weights put it. (At temperatures over 2^100 that takes logits under 2^107; a difference
+ * of logits that f32 does not hold is infinite.)
  *
  *   logits    [R, V] (dt), 16-byte aligned, rows contiguous. -inf is a token that
  *             a mask forbids.

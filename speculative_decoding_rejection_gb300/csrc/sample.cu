@@ -272,8 +272,9 @@ __device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
 // 2^-t for t = (m - z) c, as a fraction in units of 2^-62 (over a half) and a power: the
 // result is fraction 2^-power, 0 for t of 63 and more. The difference and its product with c are
 // taken in two words each: t is right within 2^-41 (its second word is under 2^-17), what it
-// has over a 1024th is rounded to units of 2^-41, the fixed-point product is right within a few units of
-// 2^-42, so a weight within 2^-39 of itself.
+// has over a 1024th is rounded to units of 2^-41, the fixed-point product errs by three of these at
+// most, so a weight by 2^-38.5 of itself. (c's second word is no normal number for T of over 2^100:
+// all this holds for differences up to 2^108 then.)
 __device__ __forceinline__ unsigned long long fraction(const unsigned long long *pow2, float m, float ch, float cl,
                                                        float z, int &power) {
   const float dh = m - z, bb = dh - m;
@@ -493,7 +494,10 @@ __device__ Found find_entry(const SampleSmem &s, unsigned long long target, bool
   return r;
 }
 
-// The largest S that keeps a mass of z below 2^62 in units of 2^-S.
+// The largest S that keeps a mass of z below 2^62 in units of 2^-S. What is cut off of V weights is
+// V 2^-S, under 2.02 V 2^-62 of the mass: 2^-39 for V = 2^22. Weights that err by e of themselves move a
+// border by no more than e / 2 of the mass (the sum before it against its part p of all: 2 p (1 - p) e),
+// so with fraction's e a border is within 2^-38 of where exact weights put it, 2^-36 for V = 2^24.
 __device__ __forceinline__ int unit_of(float z) {
   int e;
   frexpf(fmaxf(z * 1.01f, 1.f), &e);   // z < 2^e, e >= 1
@@ -703,8 +707,7 @@ __device__ void decide_values(SampleSmem &s, float m) {
 }
 
 // ------------------------------------------------------------- by a list
-// Counts (and with `masses` the masses) of the intervals of the list's tokens with keys from
-// `from` on, scanned; 4 intervals per thread.
+// The L equal intervals of the distance below m, `scale` of them per unit of it.
 // inside: the one that these intervals divide again, -1 for the first division.
 template <int L>
 struct Intervals {
@@ -743,6 +746,8 @@ __device__ void scan_level(SampleSmem &s, bool masses) {
   }
   block_scan(s, c, mass);
 }
+// Counts (and with `masses` the masses) of the intervals of the list's tokens with keys from
+// `from` on, scanned.
 __device__ void count_list(SampleSmem &s, int n, const Intervals<SA_LIST_LEVEL> &iv, unsigned long long from, bool masses, int S) {
   const int t = threadIdx.x;
   for (int i = t; i < SA_LIST_LEVEL; i += SA_THREADS) {

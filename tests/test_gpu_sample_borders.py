@@ -203,3 +203,24 @@ def test_lists_that_are_nearly_full(many, dtype):
     assert float(law["temperature"]) * math.log(float(law["min_p"])) > -9
     check_borders(inside, float(law["temperature"]), 0, float(law["top_p"]), float(u), int(tokens[0]), float(prob[0]),
                   int(kept[0]), None, 2.0 ** -37)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [2.0 ** 60, 2.0 ** 110, 3.4e38])
+def test_temperatures_that_level_a_row(T, dtype):
+    """Of ordinary logits every token is as likely as the next, of logits as large as T the law is the
+    one of logits of about 1."""
+    V, R = 9001, 5
+    rng = np.random.default_rng(V)
+    u = np.array([0.0, 0.25, 0.6, 0.9999, U24], np.float32)
+    for large in (False, True):
+        z = torch.tensor(rng.normal(size=V) * (min(T, 2.0 ** 105) if large else 1.0)).to(dtype).to(DEV)
+        zz = z.double().cpu().numpy()
+        for law in (dict(), dict(top_p=0.75), dict(top_k=500)):
+            t = {k: torch.full((R,), v, dtype=torch.int32 if k == "top_k" else F32, device=DEV) for k, v in law.items()}
+            tokens, prob, kept, _, ws = sv.spec_sample(z.expand(R, V).contiguous(), torch.tensor(u, device=DEV), want_kept=True,
+                                                       temperature=torch.full((R,), T, device=DEV), **t)
+            assert sv.spec_get_status(ws) == sv.SPEC_OK
+            for r in range(R):
+                check_borders(zz, float(np.float32(T)), law.get("top_k", 0), law.get("top_p", 1.0), float(u[r]),
+                              int(tokens[r]), float(prob[r]), int(kept[r]), None, 2.0 ** -37)
