@@ -12,8 +12,9 @@
 //
 // Squares are summed in f32 over 16 bytes x 4 of a thread, these sums in two f32 words. Where
 // such a sum is not over 1e-24, or takes the thread's to 3e38 (values that square to nothing, to
-// infinity or to more than f32 adds up), its values are squared again in 64 bits, unless they are all
-// zero: FP64 is too slow here for all of them (two multiply-adds per SM and cycle).
+// infinity or to more than f32 adds up), its values are squared again times a power of two and summed in
+// words of their own, so that gradients of any size take as long (480M bf16 of about 1e-14 or 1e18 between
+// flushes of L2: 158 us as of 1; squared in 64 bits, of which an SM has two a cycle, 1784 and 1662).
 #include "adamw.cuh"
 
 #include <algorithm>
@@ -65,18 +66,31 @@ __device__ __forceinline__ void runs(const AdHeader *table, long long i0, long l
   }
 }
 
-struct Acc {
-  float hi, lo;       // sum of squares in two words
-  double wide;        // what left the range of f32
-  uint32_t most;      // largest magnitude, as bits (NaN is over infinity)
+struct Words {      // a sum in two words
+  float hi, lo;
 };
-
-__device__ __noinline__ double wide_squares(const float *x, int n) {
-  double s = 0.0;
-  for (int i = 0; i < n; ++i) s += (double)x[i] * (double)x[i];
-  return s;
+__device__ __forceinline__ void add(Words &a, float x) {
+  const float t = a.hi + x, b = t - a.hi;
+  a.lo += (a.hi - (t - b)) + (x - b);
+  a.hi = t;
 }
 
+struct Acc {
+  Words sum;          // of squares
+  Words small, large; // of squares times SMALL^2 and LARGE^2, of what leaves the range of f32
+  uint32_t most;      // largest magnitude, as bits (NaN is over infinity); of a sum 1: infinite, 2: NaN
+};
+// Powers of two. The smallest f32 times SMALL has a square that is a normal number, and 10^9 sums of up to
+// 1e-24 stay in f32 (a thread has some millions); the largest one times LARGE leaves room for 2^46 sums.
+constexpr float SMALL = 0x1p88f, LARGE = 0x1p-90f;
+
+template <int N>
+__device__ __forceinline__ float squares(const float (&x)[N], float scale) {
+  float s[4] = {};
+#pragma unroll
+  for (int i = 0; i < N; ++i) s[i % 4] = fmaf(x[i] * scale, x[i] * scale, s[i % 4]);
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
 template <int N>
 __device__ __forceinline__ void add_values(Acc &a, const float (&x)[N], bool inf) {
   if (inf) {
@@ -84,26 +98,16 @@ __device__ __forceinline__ void add_values(Acc &a, const float (&x)[N], bool inf
     for (int i = 0; i < N; ++i) a.most = max(a.most, __float_as_uint(x[i]) & 0x7fffffffu);
     return;
   }
-  float s[4] = {};
-#pragma unroll
-  for (int i = 0; i < N; ++i) s[i % 4] = fmaf(x[i], x[i], s[i % 4]);
-  const float sum = (s[0] + s[1]) + (s[2] + s[3]);
-  const float t = a.hi + sum;
-  if (sum > 1e-24f && t < 3e38f) {
-    const float b = t - a.hi;
-    a.lo += (a.hi - (t - b)) + (sum - b);
-    a.hi = t;
-  } else {
-    uint32_t any = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) any |= __float_as_uint(x[i]) << 1;
-    if (any != 0) {
-      float y[N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) y[i] = x[i];
-      a.wide += wide_squares(y, N);
-    }
+  const float sum = squares(x, 1.f);
+  if (sum > 1e-24f && a.sum.hi + sum < 3e38f) {
+    add(a.sum, sum);
+    return;
   }
+  const bool small = sum <= 1e-24f;
+  const float q = squares(x, small ? SMALL : LARGE);
+  if (small) add(a.small, q);
+  else if (q < 3e38f) add(a.large, q);
+  else a.most = max(a.most, q != q ? 2u : 1u);   // infinity, NaN
 }
 
 template <bool BF>
@@ -136,19 +140,17 @@ __device__ __forceinline__ void norm_run(Acc &acc, const void *p, long long e0, 
   const int t = threadIdx.x;
   const long long v0 = first_vector<BF>(p, e0, e1), nv = (e1 - v0) / PER;
   const uint4 *v = reinterpret_cast<const uint4 *>(static_cast<const char *>(p) + v0 * (BF ? 2 : 4));
-  long long i = t;
-  for (; i + (GN_AHEAD - 1) * GN_THREADS < nv; i += GN_AHEAD * GN_THREADS) {
+  for (long long i = t; i < nv; i += GN_AHEAD * GN_THREADS) {   // zeros behind the end
     uint4 w[GN_AHEAD];
 #pragma unroll
-    for (int k = 0; k < GN_AHEAD; ++k) w[k] = KEEP ? v[i + k * GN_THREADS] : __ldcs(v + i + k * GN_THREADS);
+    for (int k = 0; k < GN_AHEAD; ++k) {
+      const long long at = i + k * GN_THREADS;
+      w[k] = make_uint4(0, 0, 0, 0);
+      if (at < nv) w[k] = KEEP ? v[at] : __ldcs(v + at);
+    }
     float x[GN_AHEAD * PER];
 #pragma unroll
     for (int k = 0; k < GN_AHEAD; ++k) unpack16<BF>(w[k], x + k * PER);
-    add_values(acc, x, inf);
-  }
-  for (; i < nv; i += GN_THREADS) {
-    float x[PER];
-    unpack16<BF>(v[i], x);
     add_values(acc, x, inf);
   }
   // fewer than PER elements on either side
@@ -157,6 +159,19 @@ __device__ __forceinline__ void norm_run(Acc &acc, const void *p, long long e0, 
     const float x[1] = {value_at<BF>(p, t < head ? e0 + t : v0 + nv * PER + (t - head))};
     add_values(acc, x, inf);
   }
+}
+
+// What is there seldom, out of line (150 x 30000 bf16 clipped: 18.4 us, in line 19.3).
+__device__ __noinline__ double other_sums(Words small, Words large, uint32_t most) {
+  constexpr double s = 1.0 / SMALL, l = 1.0 / LARGE;
+  if (most != 0) return most == 1 ? (double)INFINITY : (double)NAN;
+  return ((double)small.hi + (double)small.lo) * (s * s) + ((double)large.hi + (double)large.lo) * (l * l);
+}
+__device__ __forceinline__ double total(const Acc &a) {
+  double x = (double)a.sum.hi + (double)a.sum.lo;
+  if (a.small.hi != 0.f || a.large.hi != 0.f || a.most != 0)
+    x += other_sums(a.small, a.large, a.most);
+  return x;
 }
 
 // The sum (or the largest) over a block, in a fixed order; the result in thread 0.
@@ -185,7 +200,7 @@ __global__ void __launch_bounds__(GN_THREADS, ctas_per_sm(KEEP)) k_grad_norm(con
     if (x.bf16) norm_run<true, KEEP>(acc, x.grad, e0, e1, a.inf);
     else norm_run<false, KEEP>(acc, x.grad, e0, e1, a.inf);
   });
-  const double mine = a.inf ? (double)__uint_as_float(acc.most) : (double)acc.hi + (double)acc.lo + acc.wide;
+  const double mine = a.inf ? (double)__uint_as_float(acc.most) : total(acc);
   const double sum = block_join(mine, a.inf);
   if (threadIdx.x == 0) a.part[blockIdx.x] = sum;
 }

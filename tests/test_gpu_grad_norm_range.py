@@ -110,3 +110,52 @@ def test_scales_that_are_no_ordinary_numbers():
             assert sv.spec_get_status(ws) == sv.SPEC_OK
             got = float(out[0])
             assert (math.isnan(got) and math.isnan(want)) or got == want or abs(got - want) <= TOL * want, (s, inf, got)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("scale", [1e-12, 2e-13, 1e-14, 1e-20, 1e-30, 1e-37, 3e-40])
+def test_many_small_gradients(scale, dtype):
+    """Squares that are no normal numbers of f32, a few hundred thousand of a CTA's threads and more."""
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    g = (torch.empty(6_000_001, device=DEV).normal_(generator=gen) * scale).to(dtype)
+    norm = norm_of([g])
+    out, ws = sv.spec_grad_norm(table_of([g]))
+    assert sv.spec_get_status(ws) == sv.SPEC_OK and float(out[1]) == 1.0
+    assert abs(float(out[0]) - norm) <= TOL * norm + 2.0 ** -149
+    # next to ones of every size
+    rest = [torch.full((33,), v, dtype=dtype, device=DEV) for v in (0.0, 1e-38, 1e-25, norm, -norm)]
+    norm = norm_of([g] + rest)
+    out, _ = sv.spec_grad_norm(table_of(rest + [g]))
+    assert abs(float(out[0]) - norm) <= TOL * norm + 2.0 ** -149
+
+
+def test_gradients_of_every_magnitude():
+    """Threads that take sums of all three kinds in turn."""
+    gen = torch.Generator(device=DEV).manual_seed(6)
+    for top in (-60, -20, 0, 40, 62, 70, 126):
+        power = torch.randint(-148, top, (4_000_000,), generator=gen, device=DEV)
+        power = power.view(-1, 16)[:, :1].expand(-1, 16).reshape(-1)       # alike in a thread's vectors
+        g = torch.ldexp(torch.rand(power.numel(), generator=gen, device=DEV, dtype=torch.float64) + 1, power).float()
+        if norm_of([g]) < 3e38:
+            check_norm_and_clip([g]) if top > 0 else None
+            out, _ = sv.spec_grad_norm(table_of([g]))
+            assert abs(float(out[0]) - norm_of([g])) <= TOL * norm_of([g])
+        else:
+            s = torch.tensor([2.0 ** -20], device=DEV)
+            out, _ = sv.spec_grad_norm(table_of([g]), grad_scale=s)
+            assert abs(float(out[0]) - 2.0 ** -20 * norm_of([g])) <= TOL * 2.0 ** -20 * norm_of([g])
+
+
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+def test_an_infinity_among_large_and_small_ones(value):
+    for base in (1e-20, 1.0, 1.5e19):
+        g = torch.full((3_000_000,), base, device=DEV)
+        g[1_234_567] = value
+        out, ws = sv.spec_grad_norm(table_of([g]), max_norm=1.0)
+        assert sv.spec_get_status(ws) == sv.SPEC_OK
+        if math.isnan(value):
+            assert math.isnan(float(out[0])) and math.isnan(float(out[1]))
+        else:
+            assert math.isinf(float(out[0])) and float(out[1]) == 0
+        g[17] = math.nan
+        assert math.isnan(float(sv.spec_grad_norm(table_of([g]))[0][0]))
