@@ -8,7 +8,7 @@
 // read twice: the second kernel's CTAs take their runs backwards, so that what was read
 // last, and may still be in L2, is read first, and the first pass's loads then leave their lines
 // there (25M f32 in 59 us, forwards 61, with lines marked for early eviction 65; 200M f32
-// 381 us, 6.3 TB/s). A norm alone marks them: 160 against 168 us between flushes of L2.
+// 378 us, 6.3 TB/s). A norm alone marks them: 160 against 168 us between flushes of L2.
 //
 // Squares are summed in f32 over 16 bytes x 4 of a thread, these sums in two f32 words. Where
 // such a sum is not over 1e-24, or takes the thread's to 3e38 (values that square to nothing, to

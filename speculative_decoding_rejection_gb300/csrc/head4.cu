@@ -33,7 +33,7 @@
 //
 // Measured, 4096 columns to 128256 (263 to 279 MB of weights): 1 row 64 us, 5 rows 68 (groups of 64,
 // 4.1 TB/s, 0.62 of the copy rate), 8 rows 72; issue slots bound them, the ring alone would take
-// 62. 16, 32, 64 rows 120, 150, 245 us: latency with four or five warps per scheduler, the tensor
+// 62. 16, 32, 64 rows 124, 151, 255 us: latency with four or five warps per scheduler, the tensor
 // instructions alone would take 113 us for 64. 4096 to 32000, 1 row: 22.5 us.
 #include "draft.cuh"
 

@@ -30,11 +30,11 @@
 //   Which of the equal values it is goes by id there: the matches are counted per chunk
 //   of the row, in the chunks whose largest logit reaches the value.
 //
-// Measured, 1024 rows of 201088 bf16 logits (the copy rate would take 61.5 us): min-p 126 us,
-// top-k 154, top-p alone 244, mixed 178. Lists come at 0.74 of the copy rate; then a row's
+// Measured, 1024 rows of 201088 bf16 logits (the copy rate would take 61.5 us): min-p 128 us,
+// top-k 151, top-p alone 241, mixed 178. Lists come at 0.74 of the copy rate; then a row's
 // decision is a chain of barriers, 10 to 25 thousand clocks, which the other CTA of the SM covers in
 // part. A histogram costs an atomic per logit (3.7 clocks for 32). f32 by intervals: a weight and three
-// atomics per logit, 250 rows of 128256 in 235 us. Few rows are latency: 4 x 1024 f32 14 us,
+// atomics per logit, 250 rows of 128256 in 227 us. Few rows are latency: 4 x 1024 f32 15 us,
 // most of it code that runs once and is fetched for it, so loops stay rolled up.
 #include "draft.cuh"
 
