@@ -224,3 +224,20 @@ def test_temperatures_that_level_a_row(T, dtype):
             for r in range(R):
                 check_borders(zz, float(np.float32(T)), law.get("top_k", 0), law.get("top_p", 1.0), float(u[r]),
                               int(tokens[r]), float(prob[r]), int(kept[r]), None, 2.0 ** -37)
+
+
+@pytest.fixture
+def checked():
+    sv.use_checked_library(True)
+    yield
+    sv.use_checked_library(False)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_no_access_leaves_the_call(dtype, checked):
+    """Rows off the histogram and rows whose list is full, of odd lengths and in clusters."""
+    for kind in ("tiny", "spread"):
+        test_borders_in_the_tail_of_a_peaked_row(7, 50257, kind, dtype)
+    for many in (2560, 4000):
+        test_lists_that_are_nearly_full(many, dtype)
+    test_results_do_not_go_by_the_way_a_row_is_decided(*NEAR[0], "min_p", dtype)
